@@ -3,7 +3,8 @@
  *
  * The path: Lightning Indexer scores -> per-query top-k -> sparse multi-query
  * attention (MLA weight-absorbed) over the selected kv rows, its backward, and
- * the indexer KL loss with its gradients.
+ * the indexer KL loss with its gradients.  For serving: a paged cache of kv
+ * rows, its bookkeeping on the device.
  *
  * Sources (pages):
  *  [DSA-32K] "CANN&TorchTitan: DeepSeek-V3.2 32k long-sequence pretraining on
@@ -60,7 +61,9 @@ enum {
   DSA_ERR_WORKSPACE = -3,   /* workspace missing or smaller than required      */
   DSA_ERR_CUDA = -4,        /* a CUDA launch or runtime call failed            */
   DSA_ERR_TIMEOUT = -5,     /* (device) a bounded wait ran out of time         */
-  DSA_ERR_INDEX = -6        /* (device) a top-k index outside [-1, S_k)        */
+  DSA_ERR_INDEX = -6,       /* (device) a top-k index outside [-1, S_k); a page,
+                               length, parent or row index out of range (cache) */
+  DSA_ERR_PAGES = -7        /* (device) the cache has too few free pages       */
 };
 
 enum { DSA_BSND = 0, DSA_TND = 1 };
@@ -321,10 +324,107 @@ int dsa_forward_static_ws(const dsa_params *p, const void *q_I, const void *k_I,
                           const void *q, const void *kv, int32_t *idx_out, void *out,
                           float *softmax_max, float *softmax_sum, dsa_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged cache.  This library's own addition: the pages describe training.
+ *
+ * A pool holds n_pages pages of page_rows rows (one row per cached token; any
+ * row: a bf16 latent of 1152 bytes, an E4M3 index key with its scale, ...).
+ * Sequence i holds pages table[i][0 .. ceil(lens[i] / page_rows)) and lens[i]
+ * rows, the last page partly filled; further table entries mean nothing.
+ * refs[page] counts the uses of a page: one per table entry that holds it,
+ * plus any that the caller adds for itself (to keep a prefix alive, say).  A
+ * page with refs 0 is free.  A new cache: lens and refs all zero.  Full pages
+ * may be shared; a partly filled last page belongs to one sequence.
+ *
+ * The bookkeeping runs on the device, so a captured graph can hold it.  Free
+ * pages are taken lowest id first, in the order of the sequences: the results
+ * are the same on every run.  A call is carried out whole or not at all: with
+ * a length, page, parent or count out of range (DSA_ERR_INDEX) or too few free
+ * pages (DSA_ERR_PAGES) it writes its inputs through unchanged, with no copies
+ * and all slots -1, and sets the status word.
+ *
+ * n_seqs <= 8192, n_pages * page_rows < 2^31, max_pages * page_rows < 2^31.
+ */
+typedef struct {
+  int64_t n_seqs, n_pages, page_rows, max_pages; /* table is [n_seqs][max_pages] int32 */
+} dsa_cache;
+
+/* Rows of a pool: byte address base + layer * layer_stride + page * page_stride
+ * + row * row_bytes; the rows of a page are contiguous.  Layers and pages may
+ * be interleaved either way, but must not run into each other. */
+typedef struct {
+  void *base;
+  int64_t n_layers, layer_stride, page_stride, row_bytes;
+} dsa_pool;
+
+/*
+ * Fork, reorder and free: sequence i becomes a copy of old sequence parent[i]
+ * (-1: it is emptied), all at once.  A beam-search step passes the chosen
+ * beams' parents; a new sample of a prompt passes the prompt's sequence; a
+ * finished request passes -1.  Pages that no sequence holds any more become
+ * free.  A parent's full pages are shared by its children; its partly filled
+ * last page goes to the first of them (lowest i), and each further child gets
+ * a free page for it and an entry of the copy list.
+ *   parent [n_seqs], table, lens, refs: the old state
+ *   table_out (unused entries -1), lens_out, refs_out: the new state, in other
+ *          buffers than the old one
+ *   copies [n_seqs][3] int32: source page, destination page, rows; n_copies:
+ *          one int32.  For dsa_cache_copy_pages, on every pool of this cache,
+ *          before the next rows are written.
+ */
+int dsa_cache_fork(const dsa_cache *p, const int32_t *parent, const int32_t *table, const int32_t *lens,
+                   const int32_t *refs, int32_t *table_out, int32_t *lens_out, int32_t *refs_out,
+                   int32_t *copies, int32_t *n_copies, dsa_stream_t stream);
+
+/*
+ * Room for n_new[i] >= 0 more rows of each sequence: takes the pages that are
+ * needed, and writes where each new row goes.  Entries are added to table in
+ * place; lens_out may be lens and refs_out may be refs.
+ *   slots [n_slots] int32: page * page_rows + row of the new rows, those of
+ *          sequence 0 first; -1 behind the last.  The new rows together must
+ *          not be more than n_slots (<= 2^20).
+ */
+int dsa_cache_extend(const dsa_cache *p, const int32_t *n_new, int32_t *table, const int32_t *lens,
+                     const int32_t *refs, int32_t *lens_out, int32_t *refs_out, int32_t *slots, int64_t n_slots,
+                     dsa_stream_t stream);
+
+/*
+ * Compaction: the pages in use move to ids 0 .. n_live-1, so that the rest of
+ * the pool is free in one piece.  The pages at n_live and above move, in
+ * ascending order, into the free ids below, in ascending order; others stay.
+ *   table_out (unused entries -1), refs_out: other buffers than table, refs;
+ *   page_map [n_pages]: each used page's new id, -1 for a free page;
+ *   copies [n_pages / 2 + 1][3], n_copies as in dsa_cache_fork.
+ */
+int dsa_cache_compact(const dsa_cache *p, const int32_t *table, const int32_t *lens, const int32_t *refs,
+                      int32_t *table_out, int32_t *refs_out, int32_t *page_map, int32_t *copies,
+                      int32_t *n_copies, dsa_stream_t stream);
+
+/*
+ * Carries out a copy list on a pool: for k < min(*n_copies, max_copies), the
+ * first `rows` rows of the source page go to the destination page, in every
+ * layer; the destination's other rows stay as they were.  Entries out of range
+ * are skipped and flag DSA_ERR_INDEX.
+ */
+int dsa_cache_copy_pages(const dsa_cache *p, const dsa_pool *pool, const int32_t *copies, const int32_t *n_copies,
+                         int64_t max_copies, dsa_stream_t stream);
+
+/*
+ * Writes new rows: row i of each layer goes to slots[i] (of dsa_cache_extend;
+ * -1: skipped).  With row_index the row written is rows[row_index[i]], which
+ * picks the accepted ones out of the drafted rows.
+ *   rows [n_layers][n_src][row_bytes], layers rows_layer_stride bytes apart;
+ *   slots, row_index (or NULL) [n_rows] int32.  Values out of range are
+ *   skipped and flag DSA_ERR_INDEX; a slot must not occur twice.
+ */
+int dsa_cache_write(const dsa_cache *p, const dsa_pool *pool, const void *rows, int64_t n_src,
+                    int64_t rows_layer_stride, const int32_t *slots, const int32_t *row_index, int64_t n_rows,
+                    dsa_stream_t stream);
+
 /*
  * Device status.  Synchronises `stream`, then writes the device status word
- * of the current device to *device_status (DSA_OK, DSA_ERR_TIMEOUT or
- * DSA_ERR_INDEX) and clears it.  Returns DSA_ERR_CUDA if the stream reported
+ * of the current device to *device_status (DSA_OK, DSA_ERR_TIMEOUT,
+ * DSA_ERR_INDEX or DSA_ERR_PAGES) and clears it.  Returns DSA_ERR_CUDA if the stream reported
  * a CUDA error, else DSA_OK.
  * There is ONE status word per device, shared by every stream and host thread
  * that uses the library on it: the first device error since the last read

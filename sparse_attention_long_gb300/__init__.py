@@ -16,7 +16,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdsa_gb300.so")
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_WORKSPACE = 0, -1, -2, -3
-DSA_ERR_CUDA, DSA_ERR_TIMEOUT, DSA_ERR_INDEX = -4, -5, -6
+DSA_ERR_CUDA, DSA_ERR_TIMEOUT, DSA_ERR_INDEX, DSA_ERR_PAGES = -4, -5, -6, -7
 DSA_BSND, DSA_TND = 0, 1
 DSA_BF16, DSA_FP32 = 0, 1
 DSA_CP_COLOSSAL, DSA_CP_ULYSSES = 0, 1
@@ -25,7 +25,8 @@ DSA_CALL_INDEXER_TOPK = 5
 DSA_FLAG_CAUSAL_ONLY, DSA_FLAG_FP8_INDEXER, DSA_FLAG_FUSED_TOPK = 1, 2, 4
 
 _ERRNAMES = {0: "DSA_OK", -1: "DSA_ERR_INVALID_ARG", -2: "DSA_ERR_UNSUPPORTED",
-             -3: "DSA_ERR_WORKSPACE", -4: "DSA_ERR_CUDA", -5: "DSA_ERR_TIMEOUT", -6: "DSA_ERR_INDEX"}
+             -3: "DSA_ERR_WORKSPACE", -4: "DSA_ERR_CUDA", -5: "DSA_ERR_TIMEOUT", -6: "DSA_ERR_INDEX",
+             -7: "DSA_ERR_PAGES"}
 
 
 class DSAError(RuntimeError):
@@ -45,6 +46,16 @@ class dsa_params(ctypes.Structure):
                 ("wave_rows", ctypes.c_int64)]
 
 
+class dsa_cache(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int64), ("n_pages", ctypes.c_int64), ("page_rows", ctypes.c_int64),
+                ("max_pages", ctypes.c_int64)]
+
+
+class dsa_pool(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("n_layers", ctypes.c_int64), ("layer_stride", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("row_bytes", ctypes.c_int64)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
                       "(nvcc, sm_103a); there is no fallback implementation")
@@ -52,6 +63,7 @@ lib = ctypes.CDLL(LIB_PATH)
 
 _vp, _i64, _i32p = ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p
 _P = ctypes.POINTER(dsa_params)
+_C, _L = ctypes.POINTER(dsa_cache), ctypes.POINTER(dsa_pool)
 _sigs = {
     "dsa_version": ([], ctypes.c_int),
     "dsa_workspace_size": ([_P, ctypes.c_int], ctypes.c_size_t),
@@ -66,6 +78,11 @@ _sigs = {
     "dsa_backward": ([_P] + [_vp] * 18, ctypes.c_int),
     "dsa_forward": ([_P] + [_vp] * 11, ctypes.c_int),
     "dsa_forward_static_ws": ([_P] + [_vp] * 10, ctypes.c_int),
+    "dsa_cache_fork": ([_C] + [_vp] * 10, ctypes.c_int),
+    "dsa_cache_extend": ([_C] + [_vp] * 7 + [_i64, _vp], ctypes.c_int),
+    "dsa_cache_compact": ([_C] + [_vp] * 9, ctypes.c_int),
+    "dsa_cache_copy_pages": ([_C, _L, _vp, _vp, _i64, _vp], ctypes.c_int),
+    "dsa_cache_write": ([_C, _L, _vp, _i64, _i64, _vp, _vp, _i64, _vp], ctypes.c_int),
     "dsa_get_status": ([_vp, ctypes.POINTER(ctypes.c_int)], ctypes.c_int),
     "dsa_set_wait_budget_ns": ([ctypes.c_uint64], ctypes.c_int),
     "dsa_selftest_wait_timeout": ([ctypes.c_uint64, _vp], ctypes.c_int),
@@ -202,6 +219,126 @@ def forward_static_ws(p, q_I, k_I, w, q, kv, idx_out, out, softmax_max, softmax_
     _chk(lib.dsa_forward_static_ws(ctypes.byref(p), _ptr(q_I), _ptr(k_I), _ptr(w), _ptr(q),
                                    _ptr(kv), _ptr(idx_out), _ptr(out), _ptr(softmax_max),
                                    _ptr(softmax_sum), _stream(stream)), "dsa_forward_static_ws")
+
+
+# ------------------------------- paged cache -------------------------------
+class _Args:
+    """Checks the tensors of one call (type, size, one CUDA device) and makes
+    that device current while the call enqueues its work."""
+
+    def __init__(self, where):
+        self.where, self.device, self.guard = where, None, None
+
+    def _on(self, t, name):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{self.where}: {name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{self.where}: {name} is not a CUDA tensor")
+        if self.device is None:
+            self.device = t.device
+        elif t.device != self.device:
+            raise ValueError(f"{self.where}: {name} is on {t.device}, other tensors on {self.device}")
+
+    def ptr(self, t, name, dtypes, numel, optional=False, at_least=False):
+        if t is None and optional:
+            return None
+        self._on(t, name)
+        if t.dtype not in (dtypes if isinstance(dtypes, tuple) else (dtypes,)):
+            raise TypeError(f"{self.where}: {name} is {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{self.where}: {name} must be contiguous")
+        if t.numel() != numel and not (at_least and t.numel() >= numel):
+            raise ValueError(f"{self.where}: {name} has {t.numel()} elements, needs {numel}")
+        return t.data_ptr()
+
+    def pool(self, cache, t):
+        """dsa_pool of a tensor [n_pages, page_rows, D] or [layers, n_pages, page_rows, D] whose
+        rows are contiguous within a page (layers and pages may have any stride)."""
+        self._on(t, "pool")
+        if t.dim() == 3:
+            t = t.unsqueeze(0)
+        if t.dim() != 4 or t.shape[1] != cache.n_pages or t.shape[2] != cache.page_rows:
+            raise ValueError(f"{self.where}: pool must be [(layers,) n_pages, page_rows, D]")
+        e, D = t.element_size(), t.shape[3]
+        if (D > 1 and t.stride(3) != 1) or (t.shape[2] > 1 and t.stride(2) != D):
+            raise ValueError(f"{self.where}: the rows of a pool's page must be contiguous")
+        page = cache.page_rows * D * e
+        return dsa_pool(t.data_ptr(), t.shape[0], t.stride(0) * e if t.shape[0] > 1 else page,
+                        t.stride(1) * e if t.shape[1] > 1 else page, D * e), t
+
+    def call(self, fn, *args, stream=None):
+        if self.device.index == torch.cuda.current_device():
+            _chk(fn(*args, _stream(stream)), self.where)
+        else:
+            with torch.cuda.device(self.device):
+                _chk(fn(*args, _stream(stream)), self.where)
+
+
+def make_cache(*, n_seqs, n_pages, page_rows, max_pages) -> dsa_cache:
+    """Sizes of a paged cache: table [n_seqs, max_pages], lens [n_seqs] and refs [n_pages]
+    are int32 tensors of the caller; a new cache has lens and refs all zero."""
+    return dsa_cache(n_seqs, n_pages, page_rows, max_pages)
+
+
+def cache_fork(c, parent, table, lens, refs, table_out, lens_out, refs_out, copies, n_copies, stream=None):
+    """Sequence i becomes a copy of old sequence parent[i] (-1: emptied); full pages are shared.
+    Follow with cache_copy_pages(copies, n_copies) on every pool."""
+    a, i32, n = _Args("dsa_cache_fork"), torch.int32, c.n_seqs
+    args = (a.ptr(parent, "parent", i32, n), a.ptr(table, "table", i32, n * c.max_pages), a.ptr(lens, "lens", i32, n),
+            a.ptr(refs, "refs", i32, c.n_pages), a.ptr(table_out, "table_out", i32, n * c.max_pages),
+            a.ptr(lens_out, "lens_out", i32, n), a.ptr(refs_out, "refs_out", i32, c.n_pages),
+            a.ptr(copies, "copies", i32, 3 * n, at_least=True), a.ptr(n_copies, "n_copies", i32, 1))
+    a.call(lib.dsa_cache_fork, ctypes.byref(c), *args, stream=stream)
+
+
+def cache_extend(c, n_new, table, lens, refs, lens_out, refs_out, slots, stream=None):
+    """Takes pages for n_new[i] further rows of each sequence (table in place; lens_out and
+    refs_out may be lens and refs) and writes the slots of the new rows, -1 behind the last."""
+    a, i32, n = _Args("dsa_cache_extend"), torch.int32, c.n_seqs
+    args = (a.ptr(n_new, "n_new", i32, n), a.ptr(table, "table", i32, n * c.max_pages), a.ptr(lens, "lens", i32, n),
+            a.ptr(refs, "refs", i32, c.n_pages), a.ptr(lens_out, "lens_out", i32, n),
+            a.ptr(refs_out, "refs_out", i32, c.n_pages), a.ptr(slots, "slots", i32, slots.numel()), slots.numel())
+    a.call(lib.dsa_cache_extend, ctypes.byref(c), *args, stream=stream)
+
+
+def cache_compact(c, table, lens, refs, table_out, refs_out, page_map, copies, n_copies, stream=None):
+    """Moves the used pages to the lowest ids; page_map gives each its new id. Follow with
+    cache_copy_pages(copies, n_copies) on every pool (copies: [n_pages // 2 + 1, 3])."""
+    a, i32, n = _Args("dsa_cache_compact"), torch.int32, c.n_seqs
+    args = (a.ptr(table, "table", i32, n * c.max_pages), a.ptr(lens, "lens", i32, n),
+            a.ptr(refs, "refs", i32, c.n_pages), a.ptr(table_out, "table_out", i32, n * c.max_pages),
+            a.ptr(refs_out, "refs_out", i32, c.n_pages), a.ptr(page_map, "page_map", i32, c.n_pages),
+            a.ptr(copies, "copies", i32, 3 * (c.n_pages // 2 + 1), at_least=True), a.ptr(n_copies, "n_copies", i32, 1))
+    a.call(lib.dsa_cache_compact, ctypes.byref(c), *args, stream=stream)
+
+
+def cache_copy_pages(c, pool, copies, n_copies, stream=None):
+    """Carries out a copy list on a pool tensor [(layers,) n_pages, page_rows, D] of any type."""
+    a, i32 = _Args("dsa_cache_copy_pages"), torch.int32
+    pl, _ = a.pool(c, pool)
+    args = (a.ptr(copies, "copies", i32, copies.numel()), a.ptr(n_copies, "n_copies", i32, 1), copies.numel() // 3)
+    a.call(lib.dsa_cache_copy_pages, ctypes.byref(c), ctypes.byref(pl), *args, stream=stream)
+
+
+def cache_write(c, pool, rows, slots, row_index=None, stream=None):
+    """rows [(layers,) n, D] (of the pool's type) to slots [n] of cache_extend; with row_index
+    [len(slots)] the row written to slots[i] is rows[row_index[i]]."""
+    a, i32 = _Args("dsa_cache_write"), torch.int32
+    pl, pt = a.pool(c, pool)
+    a._on(rows, "rows")
+    if rows.dim() == 2:
+        rows = rows.unsqueeze(0)
+    if rows.dim() != 3 or rows.shape[0] != pt.shape[0] or rows.shape[2] != pt.shape[3] or rows.dtype != pool.dtype:
+        raise ValueError("dsa_cache_write: rows must be [(layers,) n, D] of the pool's type")
+    if (rows.shape[2] > 1 and rows.stride(2) != 1) or (rows.shape[1] > 1 and rows.stride(1) != rows.shape[2]):
+        raise ValueError("dsa_cache_write: the rows of a layer must be contiguous")
+    n = slots.numel()
+    if row_index is None and rows.shape[1] < n:
+        raise ValueError("dsa_cache_write: fewer rows than slots")
+    ls = rows.stride(0) * rows.element_size() if rows.shape[0] > 1 else 0
+    args = (rows.data_ptr(), rows.shape[1], ls, a.ptr(slots, "slots", i32, n),
+            a.ptr(row_index, "row_index", i32, n, optional=True), n)
+    a.call(lib.dsa_cache_write, ctypes.byref(c), ctypes.byref(pl), *args, stream=stream)
 
 
 def get_status(stream=None) -> int:

@@ -157,3 +157,53 @@ def test_fused_indexer_topk_workspace_and_rejections():
         dsa.DSA_ERR_WORKSPACE
     assert dsa.lib.dsa_forward_static_ws(ctypes.byref(mk(flags=dsa.DSA_FLAG_FUSED_TOPK)),
                                          *([16] * 9), None) == dsa.DSA_ERR_UNSUPPORTED
+
+
+def test_cache_host_validation_without_gpu():
+    dsa = _lib()
+    assert ctypes.sizeof(dsa.dsa_cache) == 4 * 8 and ctypes.sizeof(dsa.dsa_pool) == 5 * 8
+    mk = lambda **kw: dsa.make_cache(**dict(dict(n_seqs=2, n_pages=8, page_rows=4, max_pages=3), **kw))
+    ref = ctypes.byref
+    # distinct made-up addresses, far enough apart not to overlap
+    A = [0x10000 * (i + 1) for i in range(10)]
+    for bad, code in ((mk(n_seqs=0), dsa.DSA_ERR_INVALID_ARG), (mk(page_rows=0), dsa.DSA_ERR_INVALID_ARG),
+                      (mk(n_seqs=8193), dsa.DSA_ERR_UNSUPPORTED),
+                      (mk(n_pages=1 << 26, page_rows=64), dsa.DSA_ERR_UNSUPPORTED),
+                      (mk(max_pages=1 << 26, page_rows=64), dsa.DSA_ERR_UNSUPPORTED)):
+        assert dsa.lib.dsa_cache_fork(ref(bad), *A[:9], None) == code
+        assert dsa.lib.dsa_cache_extend(ref(bad), *A[:7], 5, None) == code
+        assert dsa.lib.dsa_cache_compact(ref(bad), *A[:8], None) == code
+    c = mk()
+    assert dsa.lib.dsa_cache_fork(None, *A[:9], None) == dsa.DSA_ERR_INVALID_ARG
+    for i in range(9):
+        assert dsa.lib.dsa_cache_fork(ref(c), *[None if j == i else A[j] for j in range(9)], None) == \
+            dsa.DSA_ERR_INVALID_ARG
+    # outputs over inputs: the whole table, and one entry of it
+    for shift in (0, 4, -4):
+        assert dsa.lib.dsa_cache_fork(ref(c), A[0], A[1], A[2], A[3], A[1] + shift, A[5], A[6], A[7], A[8], None) == \
+            dsa.DSA_ERR_INVALID_ARG
+        assert dsa.lib.dsa_cache_compact(ref(c), A[0], A[1], A[2], A[3], A[2] + shift, A[5], A[6], A[7], None) == \
+            dsa.DSA_ERR_INVALID_ARG
+    assert dsa.lib.dsa_cache_extend(ref(c), A[0], A[1], A[2], A[3], A[2] + 4, A[5], A[6], 5, None) == \
+        dsa.DSA_ERR_INVALID_ARG
+    assert dsa.lib.dsa_cache_extend(ref(c), *A[:7], 0, None) == dsa.DSA_ERR_INVALID_ARG
+    assert dsa.lib.dsa_cache_extend(ref(c), *A[:7], (1 << 20) + 1, None) == dsa.DSA_ERR_UNSUPPORTED
+    pool = lambda *a: ref(dsa.dsa_pool(*a))
+    copy = lambda pl, n=4: dsa.lib.dsa_cache_copy_pages(ref(c), pl, A[0], A[1], n, None)
+    assert copy(pool(None, 1, 0, 64, 16)) == dsa.DSA_ERR_INVALID_ARG
+    assert copy(pool(A[2], 0, 0, 64, 16)) == dsa.DSA_ERR_INVALID_ARG
+    assert copy(pool(A[2], 1, 0, 63, 16)) == dsa.DSA_ERR_INVALID_ARG      # pages closer than their rows
+    assert copy(pool(A[2], 2, 64, 64, 16)) == dsa.DSA_ERR_INVALID_ARG     # layers and pages on each other
+    assert copy(pool(A[2], 2, 511, 64, 16)) == dsa.DSA_ERR_INVALID_ARG
+    assert copy(pool(A[2], 2, 512, 64, 16), -1) == dsa.DSA_ERR_INVALID_ARG
+    assert copy(pool(A[2], 2, 512, 64, 16), 0) == dsa.DSA_OK              # nothing to do, nothing launched
+    assert copy(pool(A[2], 2, 64, 128, 16), 0) == dsa.DSA_OK
+    assert dsa.lib.dsa_cache_write(ref(c), pool(A[2], 1, 0, 64, 16), A[3], 0, 0, A[4], None, 3, None) == \
+        dsa.DSA_ERR_INVALID_ARG
+    assert dsa.lib.dsa_cache_write(ref(c), pool(A[2], 1, 0, 64, 16), None, 3, 0, A[4], None, 3, None) == \
+        dsa.DSA_ERR_INVALID_ARG
+    # the binding refuses tensors that are not on a GPU
+    import torch
+    with pytest.raises(ValueError):
+        dsa.cache_copy_pages(c, torch.zeros(8, 4, 16), torch.zeros(3, dtype=torch.int32),
+                             torch.zeros(1, dtype=torch.int32))
