@@ -4,7 +4,7 @@
  * The path: Lightning Indexer scores -> per-query top-k -> sparse multi-query
  * attention (MLA weight-absorbed) over the selected kv rows, its backward, and
  * the indexer KL loss with its gradients.  For serving: a paged cache of kv
- * rows, its bookkeeping on the device.
+ * rows, its bookkeeping on the device, and attention of drafted tokens over it.
  *
  * Sources (pages):
  *  [DSA-32K] "CANN&TorchTitan: DeepSeek-V3.2 32k long-sequence pretraining on
@@ -420,6 +420,50 @@ int dsa_cache_copy_pages(const dsa_cache *p, const dsa_pool *pool, const int32_t
 int dsa_cache_write(const dsa_cache *p, const dsa_pool *pool, const void *rows, int64_t n_src,
                     int64_t rows_layer_stride, const int32_t *slots, const int32_t *row_index, int64_t n_rows,
                     dsa_stream_t stream);
+
+/*
+ * Attention of drafted tokens over a paged cache (this library's own addition;
+ * the sparse attention's formula over every key, [DSA-32K]: while a sequence
+ * has at most topk keys the selection keeps them all and the two agree).
+ * Sequence b has lens[b] cached rows and T_b = tok_start[b+1] - tok_start[b]
+ * drafted tokens, whose own kv rows are not in the cache yet.  Token t of it
+ * sees every cached row and the drafted rows that its mask names:
+ *   x_s = scale * q[t,h] . k_s,  m = max x_s,  l = sum exp(x_s - m),
+ *   out[t,h] = sum exp(x_s - m) k_s[:d_v] / l.
+ * A tree of drafts has each token see its ancestors and itself; T_b = 1 is one
+ * step of plain decoding; without a mask token t sees drafted tokens 0 .. t (a
+ * chain of drafts, or a chunk of a prompt).  A token that sees nothing gives
+ * out = 0, m = -inf, l = 0.
+ *   q [n_tok, H, d_qk]   kv_new [n_tok, d_qk]
+ *   pool: one layer, rows of d_qk values;  table, lens: as dsa_cache
+ *   tok_start [n_seqs+1] int32, not descending, from 0 up to n_tok; rows of
+ *          tokens at and behind tok_start[n_seqs] are left as they were
+ *   mask [n_tok][mask_words] uint64: bit j of token t (bit j % 64 of word
+ *          j / 64): it sees drafted token j of its sequence.  NULL iff
+ *          mask_words is 0.  T_b <= 64 * mask_words.
+ *   out [n_tok, H, d_v]   softmax_max / softmax_sum [n_tok, H] fp32
+ * A key that a token does not see has no effect on it, whatever it holds; a
+ * NaN in a key that it does see gives NaN, an infinity there unspecified values.  A sequence whose
+ * numbers are out of range (DSA_ERR_INDEX) is left out, its outputs as they
+ * were; a page out of range (DSA_ERR_INDEX) counts as unseen.
+ *   dtype DSA_BF16: d_qk 576, d_v 512, page_rows a multiple of 16, any
+ *          H <= 1024; q, kv_new, out, the pool's base and page stride 16-byte
+ *          aligned.  DSA_FP32: any H <= 1024, d_qk <= 1024, d_v <= d_qk.
+ *   workspace: dsa_tree_workspace_size(p, t) bytes, 16-byte aligned (0 for
+ *          fp32: NULL allowed); one call at a time.
+ */
+typedef struct {
+  int32_t dtype;              /* DSA_BF16 or DSA_FP32                        */
+  float scale;                /* softmax scale                               */
+  int64_t n_tok, H, d_qk, d_v; /* drafted tokens of all sequences; heads; widths */
+  int64_t mask_words;         /* 64-bit words of a token's mask, 0: no masks */
+} dsa_tree;
+
+size_t dsa_tree_workspace_size(const dsa_cache *p, const dsa_tree *t);
+int dsa_tree_attn_fwd(const dsa_cache *p, const dsa_tree *t, const void *q, const dsa_pool *pool,
+                      const int32_t *table, const int32_t *lens, const void *kv_new, const int32_t *tok_start,
+                      const uint64_t *mask, void *out, float *softmax_max, float *softmax_sum, void *workspace,
+                      dsa_stream_t stream);
 
 /*
  * Device status.  Synchronises `stream`, then writes the device status word

@@ -56,6 +56,12 @@ class dsa_pool(ctypes.Structure):
                 ("page_stride", ctypes.c_int64), ("row_bytes", ctypes.c_int64)]
 
 
+class dsa_tree(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("n_tok", ctypes.c_int64),
+                ("H", ctypes.c_int64), ("d_qk", ctypes.c_int64), ("d_v", ctypes.c_int64),
+                ("mask_words", ctypes.c_int64)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
                       "(nvcc, sm_103a); there is no fallback implementation")
@@ -63,7 +69,7 @@ lib = ctypes.CDLL(LIB_PATH)
 
 _vp, _i64, _i32p = ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p
 _P = ctypes.POINTER(dsa_params)
-_C, _L = ctypes.POINTER(dsa_cache), ctypes.POINTER(dsa_pool)
+_C, _L, _T = ctypes.POINTER(dsa_cache), ctypes.POINTER(dsa_pool), ctypes.POINTER(dsa_tree)
 _sigs = {
     "dsa_version": ([], ctypes.c_int),
     "dsa_workspace_size": ([_P, ctypes.c_int], ctypes.c_size_t),
@@ -83,6 +89,8 @@ _sigs = {
     "dsa_cache_compact": ([_C] + [_vp] * 9, ctypes.c_int),
     "dsa_cache_copy_pages": ([_C, _L, _vp, _vp, _i64, _vp], ctypes.c_int),
     "dsa_cache_write": ([_C, _L, _vp, _i64, _i64, _vp, _vp, _i64, _vp], ctypes.c_int),
+    "dsa_tree_workspace_size": ([_C, _T], ctypes.c_size_t),
+    "dsa_tree_attn_fwd": ([_C, _T, _vp, _L] + [_vp] * 10, ctypes.c_int),
     "dsa_get_status": ([_vp, ctypes.POINTER(ctypes.c_int)], ctypes.c_int),
     "dsa_set_wait_budget_ns": ([ctypes.c_uint64], ctypes.c_int),
     "dsa_selftest_wait_timeout": ([ctypes.c_uint64, _vp], ctypes.c_int),
@@ -339,6 +347,40 @@ def cache_write(c, pool, rows, slots, row_index=None, stream=None):
     args = (rows.data_ptr(), rows.shape[1], ls, a.ptr(slots, "slots", i32, n),
             a.ptr(row_index, "row_index", i32, n, optional=True), n)
     a.call(lib.dsa_cache_write, ctypes.byref(c), ctypes.byref(pl), *args, stream=stream)
+
+
+# ------------------- attention of drafted tokens over the cache -------------------
+def make_tree(*, n_tok, H, d_qk, d_v, scale, dtype="bf16", mask_words=0) -> dsa_tree:
+    """Sizes of tree_attn_fwd: n_tok drafted tokens of all sequences together."""
+    return dsa_tree({"bf16": DSA_BF16, "fp32": DSA_FP32}[dtype], float(scale), n_tok, H, d_qk, d_v, mask_words)
+
+
+def tree_workspace_size(c, t) -> int:
+    return lib.dsa_tree_workspace_size(ctypes.byref(c), ctypes.byref(t))
+
+
+def tree_attn_fwd(c, t, q, pool, table, lens, kv_new, tok_start, mask, out, softmax_max, softmax_sum, workspace=None,
+                  stream=None):
+    """Attention of each sequence's drafted tokens (rows tok_start[b] .. tok_start[b+1] of q and
+    kv_new) over its cached rows and the drafted ones that mask [n_tok, mask_words] (int64 bits)
+    names; mask None: token t sees drafted tokens 0 .. t."""
+    a = _Args("dsa_tree_attn_fwd")
+    dt = torch.bfloat16 if t.dtype == DSA_BF16 else torch.float32
+    pl, pt = a.pool(c, pool)
+    if pt.dtype != dt or pt.shape[0] != 1 or pt.shape[3] != t.d_qk:
+        raise ValueError("dsa_tree_attn_fwd: pool must be [n_pages, page_rows, d_qk] of the call's type")
+    rows = t.n_tok * t.H
+    need = tree_workspace_size(c, t)
+    if workspace is not None and workspace.numel() * workspace.element_size() < need:
+        raise DSAError(DSA_ERR_WORKSPACE, "dsa_tree_attn_fwd")
+    i32, f32 = torch.int32, torch.float32
+    args = (a.ptr(q, "q", dt, rows * t.d_qk), ctypes.byref(pl), a.ptr(table, "table", i32, c.n_seqs * c.max_pages),
+            a.ptr(lens, "lens", i32, c.n_seqs), a.ptr(kv_new, "kv_new", dt, t.n_tok * t.d_qk),
+            a.ptr(tok_start, "tok_start", i32, c.n_seqs + 1),
+            a.ptr(mask, "mask", torch.int64, t.n_tok * t.mask_words, optional=True), a.ptr(out, "out", dt, rows * t.d_v),
+            a.ptr(softmax_max, "softmax_max", f32, rows), a.ptr(softmax_sum, "softmax_sum", f32, rows),
+            a.ptr(workspace, "workspace", workspace.dtype, workspace.numel()) if workspace is not None else None)
+    a.call(lib.dsa_tree_attn_fwd, ctypes.byref(c), ctypes.byref(t), *args, stream=stream)
 
 
 def get_status(stream=None) -> int:

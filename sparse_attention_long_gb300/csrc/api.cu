@@ -146,6 +146,23 @@ bool make_tmap_2d_bf16(CUtensorMap* tm, const void* base, uint64_t rows, uint64_
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 pages [pages][rows][cols], `page_stride` bytes apart, with a
+// (box_cols x box_rows) box inside one page
+bool make_tmap_pages_bf16(CUtensorMap* tm, const void* base, uint64_t pages, uint64_t page_stride,
+                          uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows,
+                          int swizzle_bytes) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {cols, rows, pages};
+  cuuint64_t strides[2] = {cols * 2, page_stride};
+  cuuint32_t box[3] = {box_cols, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 2D uint8 tensor map [rows, cols] with a (box_cols x box_rows) box, 128-byte swizzle
 bool make_tmap_2d_u8(CUtensorMap* tm, const void* base, uint64_t rows, uint64_t cols, uint32_t box_cols,
                      uint32_t box_rows) {

@@ -1,0 +1,1090 @@
+// Attention of drafted tokens over a paged latent cache on tcgen05 (bf16 in,
+// fp32 accumulate): for token t of sequence b and head h, over the cached rows
+// and the drafted rows that t sees,
+//   x_s = scale q[t,h].k_s,  out = sum_s exp(x_s - m) k_s[:512] / l.
+// The heads of all drafted tokens of a sequence share the sequence's keys, so
+// its T * H query rows are cut into tiles of 128 and each tile runs over the
+// keys in blocks of 112 slots, cached blocks first, then drafted ones.
+//
+// Work split.  One CTA pair per two SMs; the (tile, block) pairs of the whole
+// batch form one list, cut into equal runs, one per CTA pair, whatever the
+// lengths are (the lengths live on the device: every pair finds its run by
+// itself).  A run covers whole tiles and, at its ends, parts of a tile, whose
+// unnormalised O, running maximum and sum go to the workspace and are joined
+// by tree_join_kernel.  The order of every sum follows from the lengths alone.
+//
+// MMA layout (two-CTA MMAs, M = 128 = 64 rows per CTA, issued by CTA 0).  B is
+// split by N between the CTAs' shared memories, and each CTA's accumulator
+// keeps its 64 rows twice over the 128 TMEM lanes: lanes 0..63 pair with CTA
+// 0's half of B, lanes 64..127 with CTA 1's.  CTA c holds columns D_c of every
+// key: value columns [128c, 128c+128) u [256+128c, 256+128c+128) and rope
+// columns [512+32c, 512+32c+32), so a key row crosses from L2 into shared
+// memory once per pair:
+//   logits: A in TMEM, lanes h / 64+h hold row h's columns D_0 / D_1; lane h
+//     ends with the partial logit over D_0, lane 64+h with the one over D_1;
+//     the softmax warps add the two through shared memory;
+//   O += P V: N = 256 value columns, CTA 0's half of B in lanes 0..63, CTA 1's
+//     in lanes 64..127; 2 MMAs per 16 slots cover the 512 columns in 256 TMEM
+//     columns.
+// TMEM: O 256 + logits 112 + query 144 columns.  Three key stages, two P
+// buffers; the logits of block j+1 run during the softmax of block j.
+//
+// Keys arrive by TMA in boxes of 16 rows (pages hold a multiple of 16 rows),
+// straight from the pages.  What a masked place holds never reaches the sums:
+// a slot past the last row, on an unusable page, or seen by no token of the
+// tile is zeroed in shared memory before the tensor cores read it; a drafted
+// row with an infinity or NaN that only some of the tile's tokens see is
+// zeroed too, and the tokens that see it get NaN.
+//
+// Roles per CTA: warp 0 = TMEM allocation, MMA issuer (CTA 0); warps 1..4 =
+// the tile's query columns into TMEM, and the passing on of each key stage
+// (with the zeroing above); warps 5..12 = softmax and epilogue; warp 13 =
+// schedule; warp 14 = TMA producer.
+#include <math.h>
+
+#include "tree_attn.cuh"
+
+namespace dsa {
+namespace tree {
+
+constexpr int kHC = 64, kTile = 128, kDQK = 576, kDV = 512;
+constexpr int kBlk = 112, kGroups = kBlk / 16;
+constexpr int kStages = 3;
+constexpr int kChunk = kBlk * 128;                 // 112 slots x 64 value columns (SW128 rows)
+constexpr int kRope = kBlk * 64;                   // 112 slots x 32 rope columns (SW64 rows)
+constexpr int kStageBytes = 4 * kChunk + kRope;
+constexpr int kGroupBytes = 16 * (4 * 128 + 64);   // one box row group of 16 slots, all columns of a CTA
+constexpr int kPBytes = 2 * kHC * 128;
+constexpr int kPvSteps = kBlk / 16;
+constexpr int kFixWarps = 4, kSoftWarps = 8;
+constexpr int kWarpFix0 = 1, kWarpSoft0 = kWarpFix0 + kFixWarps;
+constexpr int kWarpScan = kWarpSoft0 + kSoftWarps, kWarpLoad = kWarpScan + 1;
+constexpr int kThreads = 32 * (kWarpLoad + 1);
+constexpr int kSlotsPerFix = kBlk / kFixWarps;     // 28
+constexpr int kTmemCols = 512;
+constexpr uint32_t kColO = 0, kColS = 256, kColQ = kColS + kBlk;
+constexpr uint32_t kIdescS = idesc_bf16(128, 2 * kBlk, false, false);
+constexpr uint32_t kIdescPV = idesc_bf16(128, 256, false, true);
+constexpr float kRescaleThreshold = 8.0f;          // log2 units
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+static_assert(kColQ + 144 == kTmemCols, "TMEM columns");
+static_assert(kChunk % 1024 == 0 && kRope % 512 == 0 && kStageBytes % 1024 == 0, "operand alignment");
+
+// A pair's run is at least this many blocks: a shorter one costs more in its
+// own start and in the join than the blocks that another pair takes over.
+constexpr int kMinRun = 4;
+
+// one part of one tile, as the schedule hands it to the other roles
+struct Seg {
+  int b, tile, j0, j1, nc, len, t0, T;               // blocks [j0, j1) of the tile; nc = cached blocks
+  int part;                                        // workspace slot of a partial result, -1: whole tile
+  int end;                                         // no further segment
+};
+
+// workspace: partial O [slot][128 column quads][128 rows] float4, then
+// [slot][128 rows] float4 (running max, sum, true max), then the join list
+struct Join {
+  long long row0;                                  // first query row (token * H + head)
+  int nrows, nparts;                               // rows of the tile; 0 parts: nothing to join
+};
+constexpr size_t kPartBytes = (size_t)kTile * kDV * 4, kStatBytes = (size_t)kTile * 16;
+
+struct __align__(1024) Smem {
+  uint8_t stage[kStages][kStageBytes];             // [value chunk 0..3 | rope][slot][row]
+  uint8_t p[2][kPBytes];                           // P of even / odd blocks (and the exchange, and O)
+  Seg seg[2];
+  unsigned long long valid[kStages][2];            // slots that hold a row
+  uint32_t bad[kStages][kFixWarps];                // 28 slots each: zeroed for an infinity or NaN
+  float red[kSoftWarps][32];
+  uint32_t sink[kSoftWarps];                       // targets of CTA 1's signalling stores
+  uint32_t sink_f[kFixWarps];
+  uint64_t st_full[kStages], st_empty[kStages], fixed[kStages], ready[kStages];
+  uint64_t s_full, s_free, p_full[2];
+  uint64_t q_tm[2], q_free[2], mma_done[2], sc_full[2], sc_empty[2], fin;
+  uint32_t tmem_base;
+  int abort, no_abort;
+};
+static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory budget");
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ---- two-CTA tcgen05 forms ----
+__device__ __forceinline__ void tmem_alloc2(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void mma2_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma2_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// arrive once on the barrier at the same offset in both CTAs of the pair when
+// every tcgen05 operation issued so far by this thread has completed
+__device__ __forceinline__ void commit2(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// arrive on a barrier of CTA 0, releasing at cluster scope
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// true if any of the `n` threads of named barrier `id` passed true
+__device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, %2, %3, q;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+// 4-byte store into the peer CTA's shared memory that completes 4 bytes of the
+// transaction count of the peer's barrier; the issuing thread does not wait
+__device__ __forceinline__ void st_async_signal(uint32_t cluster_addr, uint32_t cluster_bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(cluster_addr),
+               "r"(0u), "r"(cluster_bar)
+               : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(tm), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// ---- schedule: tiles and blocks of a sequence ----
+struct Plan {
+  int tiles, nc, nd;                               // query tiles; cached / drafted blocks (all tokens)
+  int T, H;
+  bool chain;
+};
+__device__ __forceinline__ Plan make_plan(const TreeArgs& a, const TreeSeq& s) {
+  Plan p;
+  p.T = s.T;
+  p.H = a.H;
+  p.chain = a.mask == nullptr;
+  p.tiles = (int)(((long long)s.T * a.H + kTile - 1) / kTile);
+  p.nc = (s.len + kBlk - 1) / kBlk;
+  p.nd = (s.T + kBlk - 1) / kBlk;
+  return p;
+}
+// blocks of one tile: a chain's tokens see no drafted row behind themselves
+__device__ __forceinline__ int tile_blocks(const Plan& p, int tile) {
+  if (!p.chain) return p.nc + p.nd;
+  const long long last = (128ll * tile + 127) / p.H;
+  return p.nc + (int)(last < p.T - 1 ? last : p.T - 1) / kBlk + 1;
+}
+// blocks of the first r tiles.  Chain: tile r' runs over drafted block k iff
+// (128 r' + 127) / H >= 112 k, i.e. r' >= 112 k H / 128 (both rounded down).
+__device__ __forceinline__ long long chain_term(const Plan& p, long long r, int k) {
+  const long long from = 112ll * k * p.H / 128;
+  return r > from ? r - from : 0;
+}
+__device__ __forceinline__ long long tiles_cost(const Plan& p, long long r) {  // one thread
+  if (p.T == 0) return 0;
+  if (!p.chain) return r * (p.nc + p.nd);
+  long long c = r * (p.nc + 1);
+  for (int k = 1; k <= (p.T - 1) / kBlk; ++k) c += chain_term(p, r, k);
+  return c;
+}
+__device__ __forceinline__ long long tiles_cost_warp(const Plan& p, long long r) {  // chain, one warp
+  long long c = 0;
+  for (int k = 1 + (threadIdx.x & 31); k <= (p.T - 1) / kBlk; k += 32) c += chain_term(p, r, k);
+  return warp_sum(c) + r * (p.nc + 1);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    tree_attn_tc_kernel(TreeArgs a, const __nv_bfloat16* __restrict__ qg, const __nv_bfloat16* __restrict__ kvn,
+                        __nv_bfloat16* __restrict__ out, float* __restrict__ mx, float* __restrict__ sm_out,
+                        float4* __restrict__ parts, float4* __restrict__ stats, Join* __restrict__ joins,
+                        DevCtx c, const __grid_constant__ CUtensorMap tm_page_v,
+                        const __grid_constant__ CUtensorMap tm_page_r, const __grid_constant__ CUtensorMap tm_new_v,
+                        const __grid_constant__ CUtensorMap tm_new_r) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  volatile int* abort_flag = &sm.abort;
+
+  if (threadIdx.x == 32 * kWarpFix0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&sm.st_full[i]), 1);
+      mbar_init(smem_u32(&sm.st_empty[i]), 1);
+      mbar_init(smem_u32(&sm.fixed[i]), kFixWarps);
+      mbar_init(smem_u32(&sm.ready[i]), 2 * kFixWarps);  // CTA 0's: both CTAs' stages passed on
+    }
+    mbar_init(smem_u32(&sm.s_full), 1);
+    // s_free, p_full, q_tm (used in CTA 0): the local warps arrive, the first
+    // of them also expecting the 4 bytes that each of CTA 1's warps stores
+    mbar_init(smem_u32(&sm.s_free), kSoftWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sm.p_full[i]), kSoftWarps);
+      mbar_init(smem_u32(&sm.q_tm[i]), kFixWarps);
+      mbar_init(smem_u32(&sm.q_free[i]), 1);
+      mbar_init(smem_u32(&sm.mma_done[i]), 1);
+      mbar_init(smem_u32(&sm.sc_full[i]), 1);
+      // readers of a segment: fix, softmax and load warps, and CTA 0's issuer
+      mbar_init(smem_u32(&sm.sc_empty[i]), kFixWarps + kSoftWarps + 1 + (crank == 0 ? 1 : 0));
+    }
+    mbar_init(smem_u32(&sm.fin), 1);
+    sm.abort = 0;
+    sm.no_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc2(smem_u32(&sm.tmem_base), kTmemCols);
+    tmem_relinquish2();
+    tc_fence_before();
+  }
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers initialised before any remote arrive
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  if (warp == kWarpScan) {
+    // ------------------------------- schedule -------------------------------
+    bool wrong = false;
+    long long total = 0;
+    for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
+      if (b0 + lane < a.n_seqs) {
+        const Plan p = make_plan(a, tree_seq(a, b0 + lane, &wrong));
+        total += tiles_cost(p, p.tiles);
+      }
+    }
+    total = warp_sum(total);
+    if (__any_sync(0xffffffffu, wrong) && lane == 0) set_status(c, DSA_ERR_INDEX);
+    long long run = (total + npairs - 1) / npairs;
+    if (run < kMinRun) run = kMinRun;
+    long long x = run * pair;
+    const long long x1 = x + run < total ? x + run : total;
+    int i = 0;                                     // segments so far
+    bool ok = true;
+    Join join = {0, 0, 0};
+    if (x < x1) {
+      // the sequence, tile and block where this pair's run starts
+      int b = 0;
+      long long off = x;
+      for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
+        long long cost = 0;
+        if (b0 + lane < a.n_seqs) {
+          const Plan p = make_plan(a, tree_seq(a, b0 + lane, &wrong));
+          cost = tiles_cost(p, p.tiles);
+        }
+        long long incl = cost;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, incl > off);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          off -= __shfl_sync(0xffffffffu, incl - cost, l);
+          b = b0 + l;
+          break;
+        }
+        off -= __shfl_sync(0xffffffffu, incl, 31);
+      }
+      TreeSeq s = tree_seq(a, b, &wrong);
+      Plan p = make_plan(a, s);
+      int tile, j;
+      if (!p.chain) {
+        tile = (int)(off / (p.nc + p.nd));
+        j = (int)(off % (p.nc + p.nd));
+      } else {
+        int lo = 0, hi = p.tiles;                  // cost(lo) <= off < cost(hi)
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (tiles_cost_warp(p, mid) <= off) lo = mid;
+          else hi = mid;
+        }
+        tile = lo;
+        j = (int)(off - tiles_cost_warp(p, lo));
+      }
+      while (x < x1) {
+        const int nb = tile_blocks(p, tile);
+        const long long left = x1 - x;
+        const int j1 = nb - j < left ? nb : (int)(j + left);
+        if (!mbar_wait_warp(smem_u32(&sm.sc_empty[i & 1]), ((i >> 1) & 1) ^ 1, c, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const bool whole = j == 0 && j1 == nb;
+        if (lane == 0) {
+          Seg g;
+          g.b = b;
+          g.tile = tile;
+          g.j0 = j;
+          g.j1 = j1;
+          g.nc = p.nc;
+          g.len = s.len;
+          g.t0 = s.t0;
+          g.T = s.T;
+          g.part = whole ? -1 : 2 * pair + (j == 0 ? 1 : 0);
+          g.end = 0;
+          sm.seg[i & 1] = g;
+          mbar_arrive(smem_u32(&sm.sc_full[i & 1]));
+        }
+        __syncwarp();
+        if (!whole && j == 0) {                    // the tile starts here and goes on in the next runs
+          const long long rows = (long long)s.T * a.H - 128ll * tile;
+          join.row0 = (long long)s.t0 * a.H + 128ll * tile;
+          join.nrows = rows < kTile ? (int)rows : kTile;
+          join.nparts = (int)((x + nb - 1) / run) - pair + 1;
+        }
+        ++i;
+        x += j1 - j;
+        j = 0;
+        if (++tile == p.tiles && x < x1) {
+          do {
+            ++b;
+            s = tree_seq(a, b, &wrong);
+          } while (s.T == 0);
+          p = make_plan(a, s);
+          tile = 0;
+        }
+      }
+    }
+    if (crank == 0 && lane == 0) joins[pair] = join;
+    if (ok && mbar_wait_warp(smem_u32(&sm.sc_empty[i & 1]), ((i >> 1) & 1) ^ 1, c, abort_flag) && lane == 0) {
+      sm.seg[i & 1].end = 1;
+      mbar_arrive(smem_u32(&sm.sc_full[i & 1]));
+    }
+  } else if (warp == kWarpLoad) {
+    // ------------------------------- key loads -------------------------------
+    // 35 boxes per block: box = (16-slot group, 64 value columns or the rope)
+    int G = 0;                                     // blocks so far
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      if (!mbar_wait_warp(smem_u32(&sm.sc_full[i & 1]), (i >> 1) & 1, c, abort_flag)) break;
+      const Seg g = sm.seg[i & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[i & 1]));
+      if (g.end) break;
+      const int32_t* trow = a.table + (long long)g.b * a.max_pages;
+      for (int j = g.j0; j < g.j1; ++j, ++G) {
+        const int st = G % kStages;
+        const bool drafted = j >= g.nc;
+        // lane l < 7: group l
+        int cnt = 0, x = 0, page = 0;              // rows of the group, first row (in the page / drafted), page
+        if (lane < kGroups) {
+          const int pos = (drafted ? j - g.nc : j) * kBlk + 16 * lane;
+          const int left = (drafted ? g.T : g.len) - pos;
+          cnt = left <= 0 ? 0 : (left < 16 ? left : 16);
+          if (drafted) {
+            x = g.t0 + pos;
+          } else if (cnt > 0) {
+            page = trow[pos / a.R];
+            x = pos % a.R;
+            if (page < 0 || page >= a.n_pages) {
+              cnt = 0;
+              set_status(c, DSA_ERR_INDEX);
+            }
+          }
+        }
+        const uint32_t loaded = __ballot_sync(0xffffffffu, cnt > 0);
+        unsigned long long v0 = 0, v1 = 0;
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+          const unsigned long long bits = (1u << __shfl_sync(0xffffffffu, cnt, k)) - 1u;
+          if (k < 4) v0 |= bits << (16 * k);
+          else v1 |= bits << (16 * (k - 4));
+        }
+        if (!mbar_wait_warp(smem_u32(&sm.st_empty[st]), ((G / kStages) & 1) ^ 1, c, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = smem_u32(&sm.st_full[st]), base = smem_u32(sm.stage[st]);
+        if (lane == 0) {
+          sm.valid[st][0] = v0;
+          sm.valid[st][1] = v1;
+          mbar_arrive_expect_tx(bar, (uint32_t)__popc(loaded) * kGroupBytes);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int box = 32 * u + lane, k = box % kGroups, ch = box / kGroups;  // ch 4: rope
+          const int bx = __shfl_sync(0xffffffffu, x, k), bp = __shfl_sync(0xffffffffu, page, k);
+          if (box < 5 * kGroups && ((loaded >> k) & 1u)) {
+            const bool rope = ch == 4;
+            const int col = rope ? kDV + 32 * (int)crank : 256 * (ch >> 1) + 128 * (int)crank + 64 * (ch & 1);
+            const uint32_t dst = base + (rope ? 4 * kChunk + k * 1024 : ch * kChunk + k * 2048);
+            if (drafted) tma_load_2d(dst, rope ? &tm_new_r : &tm_new_v, col, bx, bar);
+            else tma_load_3d(dst, rope ? &tm_page_r : &tm_page_v, col, bx, bp, bar);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // no copy may still be in flight when the CTA exits (bounded, whatever the others do)
+    for (int k = G - kStages < 0 ? 0 : G - kStages; k < G; ++k)
+      mbar_wait_warp(smem_u32(&sm.st_full[k % kStages]), (k / kStages) & 1, c, &sm.no_abort);
+  } else if (warp >= kWarpFix0 && warp < kWarpSoft0) {
+    // ---------------------- query columns, key stages passed on ----------------------
+    const int fw = warp - kWarpFix0;
+    int G = 0;
+    bool ok = true;
+    // one arrive per warp on a barrier of CTA 0
+    for (int i = 0; ok; ++i) {
+      if (!mbar_wait_warp(smem_u32(&sm.sc_full[i & 1]), (i >> 1) & 1, c, abort_flag)) break;
+      const Seg g = sm.seg[i & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[i & 1]));
+      if (g.end) break;
+      const long long rows = (long long)g.T * a.H - 128ll * g.tile;   // of the tile (more than 128: 128)
+      {
+        // thread = TMEM lane l of this warp's quadrant: row l & 63, column half l >> 6
+        if (i > 0 && !mbar_wait_warp(smem_u32(&sm.q_free[(i - 1) & 1]), ((i - 1) >> 1) & 1, c, abort_flag)) break;
+        tc_fence_after();
+        const int l = (warp & 3) * 32 + lane, rr = kHC * (int)crank + (l & 63);
+        const bool live = rr < rows;
+        const __nv_bfloat16* qh =
+            qg + ((long long)g.t0 * a.H + 128ll * g.tile + (live ? rr : 0)) * (long long)kDQK;
+        const uint32_t lane_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint4* vsrc = reinterpret_cast<const uint4*>(qh + 128 * (l >> 6));
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+        for (int p = 0; p < 4; ++p) {              // 64 value columns at a time -> TMEM columns kColQ + 32p
+          uint32_t w[32];
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            const uint4 v = live ? __ldg(vsrc + 32 * (p >> 1) + 8 * (p & 1) + t) : zero;
+            w[4 * t] = v.x, w[4 * t + 1] = v.y, w[4 * t + 2] = v.z, w[4 * t + 3] = v.w;
+          }
+          tmem_st32(lane_tmem + kColQ + 32 * p, w);
+          tmem_st_wait();
+        }
+        {
+          const uint4* rsrc = reinterpret_cast<const uint4*>(qh + kDV + 32 * (l >> 6));
+          uint32_t w2[16];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint4 v = live ? __ldg(rsrc + t) : zero;
+            w2[4 * t] = v.x, w2[4 * t + 1] = v.y, w2[4 * t + 2] = v.z, w2[4 * t + 3] = v.w;
+          }
+          tmem_st16(lane_tmem + kColQ + 128, w2);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&sm.q_tm[i & 1]);
+          if (crank == 0) {
+            if (fw == 0) mbar_arrive_expect_tx(bar, 4 * kFixWarps);
+            else mbar_arrive(bar);
+          } else {
+            st_async_signal(mapa_shared(smem_u32(&sm.sink_f[fw]), 0), mapa_shared(bar, 0));
+          }
+        }
+      }
+      // the tokens of the tile
+      const int ta = (int)(128ll * g.tile / a.H);
+      const long long last = (128ll * g.tile + 127) / a.H;
+      const int tb = last < g.T - 1 ? (int)last : g.T - 1;
+      for (int j = g.j0; j < g.j1; ++j, ++G) {
+        const int st = G % kStages;
+        if (!mbar_wait_warp(smem_u32(&sm.st_full[st]), (G / kStages) & 1, c, abort_flag)) {
+          ok = false;
+          break;
+        }
+        // this warp's 28 slots: those that hold a row, those that any / every token of the tile sees
+        constexpr uint32_t kAll = (1u << kSlotsPerFix) - 1u;
+        const int s0 = kSlotsPerFix * fw;
+        uint32_t valid;
+        {
+          const unsigned long long v0 = sm.valid[st][0], v1 = sm.valid[st][1];
+          const unsigned long long w = s0 >= 64 ? v1 >> (s0 - 64) : (s0 ? (v0 >> s0) | (v1 << (64 - s0)) : v0);
+          valid = (uint32_t)w & kAll;
+        }
+        uint32_t any = kAll, every = kAll;
+        if (j >= g.nc) {
+          const int first = (j - g.nc) * kBlk + s0;
+          if (a.mask == nullptr) {
+            const int na = ta - first + 1, nb = tb - first + 1;  // slots that the first / last token sees
+            every = na <= 0 ? 0u : na >= kSlotsPerFix ? kAll : (1u << na) - 1u;
+            any = nb <= 0 ? 0u : nb >= kSlotsPerFix ? kAll : (1u << nb) - 1u;
+          } else {
+            const int w = first >> 6, sh = first & 63;
+            uint32_t o = 0u, n = kAll;
+            for (int t = ta + lane; t <= tb; t += 32) {
+              const unsigned long long* mrow = a.mask + (long long)(g.t0 + t) * a.mask_words;
+              unsigned long long m = w < a.mask_words ? mrow[w] >> sh : 0ull;
+              if (sh && w + 1 < a.mask_words) m |= mrow[w + 1] << (64 - sh);
+              o |= (uint32_t)m & kAll;
+              n &= (uint32_t)m;
+            }
+            any = __reduce_or_sync(0xffffffffu, o);
+            every = __reduce_and_sync(0xffffffffu, n);
+          }
+        }
+        uint32_t clear = kAll & ~(valid & any), bad = 0;
+        for (uint32_t mixed = valid & any & ~every; mixed; mixed &= mixed - 1) {
+          const int k = __ffs(mixed) - 1;
+          const uint4* src =
+              reinterpret_cast<const uint4*>(kvn + (long long)(g.t0 + (j - g.nc) * kBlk + s0 + k) * kDQK);
+          bool inf = false;
+#pragma unroll
+          for (int u = 0; u < 3; ++u) {
+            const int e = 32 * u + lane;
+            if (e < kDQK / 8) {
+              const uint4 v = __ldg(src + e);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                inf |= (w[q] & 0x7F80u) == 0x7F80u || (w[q] & 0x7F800000u) == 0x7F800000u;
+            }
+          }
+          if (__any_sync(0xffffffffu, inf)) bad |= 1u << k;
+        }
+        clear |= bad;
+        if (lane == 0) sm.bad[st][fw] = bad;
+        if (clear) {
+          for (uint32_t m = clear; m; m &= m - 1) {
+            const int r = s0 + __ffs(m) - 1;
+            uint8_t* base = sm.stage[st];
+            *reinterpret_cast<uint4*>(base + (lane >> 3) * kChunk + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+            if (lane < 4) *reinterpret_cast<uint4*>(base + 4 * kChunk + r * 64 + lane * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();                // these writes -> the tensor cores' reads
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sm.fixed[st]));
+          mbar_arrive_cluster(mapa_shared(smem_u32(&sm.ready[st]), 0));
+        }
+      }
+    }
+  } else if (warp == 0) {
+    if (crank == 0 && lane == 0) {
+      // ------------------------------- MMA issuer -------------------------------
+      // Whichever is ready, the logits of the next block first; no progress
+      // for the wait budget is a timeout.
+      int Gs = 0, Gp = 0;                          // blocks so far: logits issued / PVs issued
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        const int bi = i & 1;
+        if (!mbar_wait(smem_u32(&sm.sc_full[bi]), (i >> 1) & 1, c, abort_flag)) break;
+        const int nblk = sm.seg[bi].j1 - sm.seg[bi].j0, end = sm.seg[bi].end;
+        mbar_arrive(smem_u32(&sm.sc_empty[bi]));
+        if (end) break;
+        if (!mbar_wait<true>(smem_u32(&sm.q_tm[bi]), (i >> 1) & 1, c, abort_flag)) break;
+        tc_fence_after();
+        int js = 0, jp = 0;
+        uint64_t t_idle = 0;
+        uint32_t spins = 0;
+        while (ok && jp < nblk) {
+          bool progressed = false;
+          if (js < nblk && js <= jp + 2 && (Gs == 0 || mbar_poll(smem_u32(&sm.s_free), (Gs - 1) & 1)) &&
+              mbar_poll(smem_u32(&sm.ready[Gs % kStages]), (Gs / kStages) & 1)) {
+            tc_fence_after();
+            const uint32_t sb = smem_u32(sm.stage[Gs % kStages]);
+#pragma unroll
+            for (int kk = 0; kk < 16; ++kk)
+              mma2_ts(tmem + kColS, tmem + kColQ + kk * 8,
+                      sdesc(sb + (kk >> 2) * kChunk + (kk & 3) * 32, 16, 1024, kSw128), kIdescS, kk > 0 ? 1u : 0u);
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              mma2_ts(tmem + kColS, tmem + kColQ + 128 + r * 8, sdesc(sb + 4 * kChunk + r * 32, 16, 512, kSw64),
+                      kIdescS, 1u);
+            commit2(smem_u32(&sm.s_full));
+            ++js;
+            ++Gs;
+            if (js == nblk) commit2(smem_u32(&sm.q_free[bi]));
+            progressed = true;
+          } else if (jp < js && mbar_poll(smem_u32(&sm.p_full[Gp & 1]), (Gp >> 1) & 1)) {
+            tc_fence_after();
+            const uint32_t sb = smem_u32(sm.stage[Gp % kStages]), pa = smem_u32(sm.p[Gp & 1]);
+#pragma unroll
+            for (int kk = 0; kk < kPvSteps; ++kk) {
+              const uint64_t ad = sdesc(pa + (kk >> 2) * (kHC * 128) + (kk & 3) * 32, 16, 1024, kSw128);
+#pragma unroll
+              for (int m = 0; m < 2; ++m)
+                mma2_ss(tmem + kColO + 128 * m, ad, sdesc(sb + 2 * m * kChunk + kk * 2048, kChunk, 1024, kSw128),
+                        kIdescPV, (jp > 0 || kk > 0) ? 1u : 0u);
+            }
+            commit2(smem_u32(&sm.st_empty[Gp % kStages]));
+            ++jp;
+            ++Gp;
+            progressed = true;
+          }
+          if (progressed) {
+            spins = 0;
+          } else if ((++spins & 63u) == 0) {
+            const uint64_t now = globaltimer();
+            if (spins == 64) t_idle = now;
+            if (*abort_flag) ok = false;
+            else if (now - t_idle > c.budget) {
+              set_status(c, DSA_ERR_TIMEOUT);
+              *abort_flag = 1;
+              ok = false;
+            }
+          }
+        }
+        commit2(smem_u32(&sm.mma_done[bi]));       // this segment's O complete
+      }
+      commit2(smem_u32(&sm.fin));
+      mbar_wait(smem_u32(&sm.fin), 0, c, &sm.no_abort);
+    }
+  } else {
+    // --------------------------- softmax / epilogue ---------------------------
+    const int quad = warp & 3, ch = (warp - kWarpSoft0) >> 2;
+    const int ws = 4 * ch + quad;                  // slot in red[]
+    const int l = quad * 32 + lane;                // TMEM lane
+    const int hl = l & 63, half = l >> 6;          // row in the CTA; lane half
+    const int rr = kHC * (int)crank + hl;          // row in the tile
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const float sl2e = a.scale * kLog2e;
+    // thread (lane l, column half ch) keeps slots [56ch, 56ch+32) of row hl in
+    // lane half 0, [56ch+32, 56ch+56) in lane half 1
+    const int kept = half ? 24 : 32;
+    const int s0 = 56 * ch + (half ? 32 : 0);
+    auto signal = [&](uint64_t* bar) {
+      if (lane == 0) {
+        if (crank == 0) {
+          if (warp == kWarpSoft0) mbar_arrive_expect_tx(smem_u32(bar), 4 * kSoftWarps);
+          else mbar_arrive(smem_u32(bar));
+        } else {
+          st_async_signal(mapa_shared(smem_u32(&sm.sink[ws]), 0), mapa_shared(smem_u32(bar), 0));
+        }
+      }
+    };
+    // bits [s0, s0 + 32) of 112 slot bits
+    auto cut = [&](unsigned long long v0, unsigned long long v1) -> uint32_t {
+      return (uint32_t)(s0 >= 64 ? v1 >> (s0 - 64) : (s0 ? (v0 >> s0) | (v1 << (64 - s0)) : v0));
+    };
+    // Every warp executes the same sequence of named barriers whatever happens
+    // (after a failed wait it goes on through the segment without work, and
+    // the vote at the next one makes all of them stop).
+    bool ok = true;
+    int G = 0;
+    for (int i = 0;; ++i) {
+      const int bi = i & 1;
+      if (ok) ok = mbar_wait_warp(smem_u32(&sm.sc_full[bi]), (i >> 1) & 1, c, abort_flag);
+      if (named_bar_or(2, kSoftWarps * 32, !ok)) break;
+      const Seg g = sm.seg[bi];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[bi]));
+      if (g.end) break;
+      const long long rows = (long long)g.T * a.H - 128ll * g.tile;
+      const bool live = rr < rows;
+      const int tok = live ? (int)((128ll * g.tile + rr) / a.H) : g.T - 1;
+      float m_run = -INFINITY, m_true = -INFINITY, l_run = 0.f;
+      bool poison = false;
+      for (int j = g.j0; j < g.j1; ++j, ++G) {
+        const int pb = G & 1, st = G % kStages;
+        if (ok) ok = mbar_wait_warp(smem_u32(&sm.fixed[st]), (G / kStages) & 1, c, abort_flag);
+        // visible slots of the kept range
+        uint32_t vmask = 0;
+        if (ok) {
+          vmask = cut(sm.valid[st][0], sm.valid[st][1]);
+          if (j >= g.nc) {
+            const int first = (j - g.nc) * kBlk + s0;
+            if (a.mask == nullptr) {
+              const int n = tok - first + 1;
+              vmask &= n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+            } else {
+              const unsigned long long* mrow = a.mask + (long long)(g.t0 + tok) * a.mask_words;
+              const int w = first >> 6, sh = first & 63;
+              unsigned long long m = w < a.mask_words ? __ldg(mrow + w) >> sh : 0ull;
+              if (sh && w + 1 < a.mask_words) m |= __ldg(mrow + w + 1) << (64 - sh);
+              vmask &= (uint32_t)m;
+            }
+            const unsigned long long b0 = sm.bad[st][0], b1 = sm.bad[st][1], b2 = sm.bad[st][2], b3 = sm.bad[st][3];
+            const uint32_t bad = cut(b0 | (b1 << 28) | (b2 << 56), (b2 >> 8) | (b3 << 20));
+            if (vmask & bad & (half ? 0x00ffffffu : 0xffffffffu)) poison = true;
+          }
+          if (half) vmask &= 0x00ffffffu;
+        }
+        if (ok) ok = mbar_wait_warp(smem_u32(&sm.s_full), G & 1, c, abort_flag);
+        // partial logits of row hl over this lane half's columns
+        uint32_t v0[32], v1[16], v2[8];
+        if (ok) {
+          tc_fence_after();
+          const uint32_t sbuf = tmem + lane_off + kColS + 56 * ch;
+          tmem_ld32(sbuf, v0);
+          tmem_ld16(sbuf + 32, v1);
+          tmem_ld8(sbuf + 48, v2);
+          tmem_ld_wait(v0);
+          tmem_ld_also16(v1);
+          tmem_ld_also8(v2);
+          tc_fence_before();
+          __syncwarp();
+          signal(&sm.s_free);                      // the logit buffer is free
+          // the exchange below reuses P buffer pb, last read by PV(G - 2)
+          if (G >= 2)
+            ok = mbar_wait_warp(smem_u32(&sm.st_empty[(G - 2) % kStages]), ((G - 2) / kStages) & 1, c, abort_flag);
+        } else {
+#pragma unroll
+          for (int t = 0; t < 32; ++t) v0[t] = 0u;
+#pragma unroll
+          for (int t = 0; t < 16; ++t) v1[t] = 0u;
+#pragma unroll
+          for (int t = 0; t < 8; ++t) v2[t] = 0u;
+        }
+        // Exchange with the lane-pair partner (lane l ^ 64, same ch) through P
+        // buffer pb, in two rounds of up to 4 float4 per thread: half 0 sends
+        // slots 32..55, half 1 slots 0..31 of the column half.
+        float4* xb = reinterpret_cast<float4*>(sm.p[pb]);
+        auto xslot = [&](int t, int dest) { return xb + ((t * 2 + ch) * 2 + dest) * kHC + hl; };
+        float x[32];
+        if (half == 0) {
+#pragma unroll
+          for (int t = 0; t < 32; ++t) x[t] = __uint_as_float(v0[t]);
+        } else {
+#pragma unroll
+          for (int t = 0; t < 16; ++t) x[t] = __uint_as_float(v1[t]);
+#pragma unroll
+          for (int t = 0; t < 8; ++t) x[16 + t] = __uint_as_float(v2[t]);
+#pragma unroll
+          for (int t = 24; t < 32; ++t) x[t] = 0.f;
+        }
+#pragma unroll
+        for (int rnd = 0; rnd < 2; ++rnd) {
+          if (half == 0) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const int q = 4 * rnd + t;
+              if (q < 4)
+                *xslot(t, 1) = make_float4(__uint_as_float(v1[4 * q]), __uint_as_float(v1[4 * q + 1]),
+                                           __uint_as_float(v1[4 * q + 2]), __uint_as_float(v1[4 * q + 3]));
+              else if (q < 6)
+                *xslot(t, 1) =
+                    make_float4(__uint_as_float(v2[4 * (q - 4)]), __uint_as_float(v2[4 * (q - 4) + 1]),
+                                __uint_as_float(v2[4 * (q - 4) + 2]), __uint_as_float(v2[4 * (q - 4) + 3]));
+            }
+          } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const int q = 4 * rnd + t;
+              *xslot(t, 0) = make_float4(__uint_as_float(v0[4 * q]), __uint_as_float(v0[4 * q + 1]),
+                                         __uint_as_float(v0[4 * q + 2]), __uint_as_float(v0[4 * q + 3]));
+            }
+          }
+          named_bar_sync(1, kSoftWarps * 32);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const int q = 4 * rnd + t;
+            if (4 * q < kept) {
+              const float4 pr = *xslot(t, half);
+              x[4 * q] += pr.x;
+              x[4 * q + 1] += pr.y;
+              x[4 * q + 2] += pr.z;
+              x[4 * q + 3] += pr.w;
+            }
+          }
+          named_bar_sync(1, kSoftWarps * 32);      // the region is rewritten next
+        }
+        float bm = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 32; ++t) {
+          if (((vmask >> t) & 1u) == 0) x[t] = -INFINITY;
+          bm = fmaxf(bm, x[t]);
+        }
+        // the row's block max over its four threads (lane pair x column halves)
+        sm.red[ws][lane] = bm;
+        named_bar_sync(1, kSoftWarps * 32);
+        bm = fmaxf(fmaxf(sm.red[quad][lane], sm.red[quad + 4][lane]),
+                   fmaxf(sm.red[quad ^ 2][lane], sm.red[(quad ^ 2) + 4][lane]));
+        // (red is rewritten only behind the next block's first barrier)
+        if (!ok) continue;
+        bm *= sl2e;                                // log2 units (sl2e > 0)
+        m_true = fmaxf(m_true, bm);
+        // The maximum that P is taken against moves only when a block's exceeds
+        // it by more than 2^8: rescaling O in TMEM is rare, and P stays below
+        // 2^8 (bf16 and fp32 lose nothing by a power of two).
+        const bool need = bm > m_run + kRescaleThreshold;
+        if (__any_sync(0xffffffffu, need)) {
+          const float m_new = need ? bm : m_run;
+          const float alpha = (m_run == -INFINITY || !need) ? (need ? 0.f : 1.f) : ex2(m_run - m_new);
+          if (j > g.j0 && __any_sync(0xffffffffu, need && m_run != -INFINITY)) {
+            // O must hold PV(G-1) before it is rescaled
+            ok = mbar_wait_warp(smem_u32(&sm.st_empty[(G - 1) % kStages]), ((G - 1) / kStages) & 1, c, abort_flag);
+            if (!ok) continue;
+            tc_fence_after();
+#pragma unroll 1
+            for (int m = 0; m < 2; ++m)
+#pragma unroll 1
+              for (int cc = 0; cc < 64; cc += 32) {
+                const uint32_t oa = tmem + lane_off + kColO + 128 * m + 64 * ch + cc;
+                uint32_t o[32];
+                tmem_ld32(oa, o);
+                tmem_ld_wait(o);
+#pragma unroll
+                for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * alpha);
+                tmem_st32(oa, o);
+                tmem_st_wait();
+              }
+            tc_fence_before();
+          }
+          l_run *= alpha;
+          m_run = m_new;
+        }
+        const float mu = (m_run == -INFINITY) ? 0.f : m_run;
+        uint32_t pk[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+          const float pa = ex2(fmaf(x[2 * t], sl2e, -mu));
+          const float pc = ex2(fmaf(x[2 * t + 1], sl2e, -mu));
+          l_run += pa + pc;                        // the sum takes P before its rounding
+          pk[t] = pack_bf16x2(pa, pc);             // bf16: the operand type of the PV product
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (8 * q < kept) {
+            const int sl = s0 + 8 * q;
+            uint8_t* prow = sm.p[pb] + (sl >> 6) * (kHC * 128) + hl * 128;
+            *reinterpret_cast<uint4*>(prow + ((((sl & 63) >> 3) ^ (hl & 7)) << 4)) =
+                make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        signal(&sm.p_full[pb]);
+      }
+      // ------------------------------- epilogue -------------------------------
+      if (ok) ok = mbar_wait_warp(smem_u32(&sm.mma_done[bi]), (i >> 1) & 1, c, abort_flag);
+      tc_fence_after();
+      if (poison) l_run = NAN;
+      named_bar_sync(1, kSoftWarps * 32);
+      sm.red[ws][lane] = l_run;
+      named_bar_sync(1, kSoftWarps * 32);
+      const float lsum = (sm.red[quad][lane] + sm.red[quad + 4][lane]) +
+                         (sm.red[quad ^ 2][lane] + sm.red[(quad ^ 2) + 4][lane]);
+      const bool all_ok = named_bar_or(2, kSoftWarps * 32, !ok) == false;
+      if (!all_ok) {
+        ok = false;
+        continue;
+      }
+      if (g.part >= 0) {
+        // part of a tile: O as it stands, [column quad][row] so that a warp's
+        // 32 rows make whole lines
+        float4* po = parts + (size_t)g.part * (kTile * kDV / 4) + rr;
+#pragma unroll 1
+        for (int m = 0; m < 2; ++m)
+#pragma unroll 1
+          for (int cc = 0; cc < 64; cc += 32) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lane_off + kColO + 128 * m + 64 * ch + cc, o);
+            tmem_ld_wait(o);
+            const int quad0 = (256 * m + 128 * half + 64 * ch + cc) / 4;
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+              po[(size_t)(quad0 + t) * kTile] =
+                  make_float4(__uint_as_float(o[4 * t]), __uint_as_float(o[4 * t + 1]),
+                              __uint_as_float(o[4 * t + 2]), __uint_as_float(o[4 * t + 3]));
+          }
+        if (half == 0 && ch == 0) stats[(size_t)g.part * kTile + rr] = make_float4(m_run, lsum, m_true, 0.f);
+      } else {
+        const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // no visible key: 0
+        const long long row0 = (long long)g.t0 * a.H + 128ll * g.tile + kHC * (int)crank;  // first row of this CTA
+        const int nrow = rows - kHC * (int)crank < kHC ? (int)(rows - kHC * (int)crank) : kHC;
+        // bf16 rows through shared memory, in two rounds of 256 value columns
+        // (both P buffers, as four 64-column tiles with the 128-byte swizzle)
+        uint8_t* const ostage = &sm.p[0][0];
+        uint8_t* const trow = ostage + (2 * half + ch) * (kHC * 128) + hl * 128;
+        const int th = threadIdx.x - 32 * kWarpSoft0;
+#pragma unroll 1
+        for (int m = 0; m < 2; ++m) {
+          if (m == 1) named_bar_sync(1, kSoftWarps * 32);  // round 0 read before it is overwritten
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            uint32_t o[16];
+            tmem_ld16(tmem + lane_off + kColO + 128 * m + 64 * ch + 16 * q4, o);
+            tmem_ld_wait16(o);
+            uint32_t pw[8];
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+              pw[t] = pack_bf16x2(__uint_as_float(o[2 * t]) * inv, __uint_as_float(o[2 * t + 1]) * inv);
+            *reinterpret_cast<uint4*>(trow + (((2 * q4) ^ (hl & 7)) << 4)) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+            *reinterpret_cast<uint4*>(trow + (((2 * q4 + 1) ^ (hl & 7)) << 4)) = make_uint4(pw[4], pw[5], pw[6], pw[7]);
+          }
+          named_bar_sync(1, kSoftWarps * 32);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int r = 8 * e + (th >> 5), c16 = th & 31;  // row, 16-byte piece of the 256 columns
+            if (r < nrow)
+              *reinterpret_cast<uint4*>(out + (row0 + r) * kDV + 256 * m + 8 * c16) = *reinterpret_cast<const uint4*>(
+                  ostage + (c16 >> 3) * (kHC * 128) + r * 128 + (((c16 & 7) ^ (r & 7)) << 4));
+          }
+        }
+        if (half == 0 && ch == 0 && live) {
+          const bool any = m_true != -INFINITY;
+          mx[row0 + hl] = any ? m_true * kLn2 : -INFINITY;
+          sm_out[row0 + hl] = lsum == 0.f ? 0.f : lsum * ex2(m_run - m_true);
+        }
+      }
+      tc_fence_before();                           // O is overwritten by the next segment's first PV
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the peer may still read our shared memory / arrive until here
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc2(tmem, kTmemCols);
+  }
+}
+
+// Joins the parts of the tiles that several pairs worked on:
+//   M = max m_k, w_k = 2^(m_k - M), l = sum w_k l_k, out = sum w_k O_k / l,
+// the parts in ascending key order.  grid (pairs, 16): 32 of the 512 columns.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads)
+    tree_join_kernel(const float4* __restrict__ parts, const float4* __restrict__ stats,
+                     const Join* __restrict__ joins, __nv_bfloat16* __restrict__ out, float* __restrict__ mx,
+                     float* __restrict__ sm_out) {
+  const int pair = blockIdx.x;
+  const Join jn = joins[pair];
+  if (jn.nparts == 0) return;
+  const int row = threadIdx.x & 127, q0 = 8 * blockIdx.y + 4 * (threadIdx.x >> 7);
+  if (row >= jn.nrows) return;
+  auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * pair + 1 : 2 * (pair + k)); };
+  float M = -INFINITY, true_max = -INFINITY;
+  for (int k = 0; k < jn.nparts; ++k) {
+    const float4 s = stats[slot(k) * kTile + row];
+    M = fmaxf(M, s.x);
+    true_max = fmaxf(true_max, s.z);
+  }
+  const float mu = M == -INFINITY ? 0.f : M;
+  float l = 0.f;
+  float4 o[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) o[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < jn.nparts; ++k) {
+    const float4 s = stats[slot(k) * kTile + row];
+    const float w = ex2(s.x - mu);                 // a part with no visible key: 2^-inf = 0
+    l += w * s.y;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const float4 v = parts[slot(k) * (kTile * kDV / 4) + (size_t)(q0 + t) * kTile + row];
+      o[t].x = fmaf(w, v.x, o[t].x);
+      o[t].y = fmaf(w, v.y, o[t].y);
+      o[t].z = fmaf(w, v.z, o[t].z);
+      o[t].w = fmaf(w, v.w, o[t].w);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const long long r = jn.row0 + row;
+  uint32_t pw[8];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    pw[2 * t] = pack_bf16x2(o[t].x * inv, o[t].y * inv);
+    pw[2 * t + 1] = pack_bf16x2(o[t].z * inv, o[t].w * inv);
+  }
+  uint4* dst = reinterpret_cast<uint4*>(out + r * kDV + 4 * q0);
+  dst[0] = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+  dst[1] = make_uint4(pw[4], pw[5], pw[6], pw[7]);
+  if (q0 == 0) {
+    mx[r] = true_max == -INFINITY ? -INFINITY : true_max * kLn2;
+    sm_out[r] = l == 0.f ? 0.f : l * ex2(mu - true_max);
+  }
+}
+
+}  // namespace tree
+
+bool make_tmap_2d_bf16(CUtensorMap* tm, const void* base, uint64_t rows, uint64_t cols, uint32_t box_cols,
+                       uint32_t box_rows, int swizzle_bytes);
+bool make_tmap_pages_bf16(CUtensorMap* tm, const void* base, uint64_t pages, uint64_t page_stride, uint64_t rows,
+                          uint64_t cols, uint32_t box_cols, uint32_t box_rows, int swizzle_bytes);
+
+// CTA pairs of the kernel at most: one CTA per SM (152 SMs when there is no device to ask)
+static int tree_pairs_bound() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 2) {
+    cudaGetLastError();
+    sms = 152;
+  }
+  return sms / 2;
+}
+static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+size_t tree_tc_workspace() {
+  const size_t n = (size_t)tree_pairs_bound();
+  return up256(2 * n * tree::kPartBytes) + up256(2 * n * tree::kStatBytes) + up256(n * sizeof(tree::Join));
+}
+
+int launch_tree_attn_tc(const TreeArgs& a, const void* q, const void* pool, long long page_stride, const void* kv_new,
+                        void* out, float* mx, float* sm, void* ws, DevCtx c, cudaStream_t st) {
+  using namespace tree;
+  const size_t smem = sizeof(Smem) + 1024;
+  if (cudaFuncSetAttribute(tree_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  static int pairs_by_device[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
+  int pairs = dev < 64 ? pairs_by_device[dev] : 0;
+  if (pairs <= 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    if (cudaOccupancyMaxActiveClusters(&pairs, tree_attn_tc_kernel, &cfg) != cudaSuccess || pairs <= 0) {
+      cudaGetLastError();
+      pairs = tree_pairs_bound();
+    }
+    if (dev < 64) pairs_by_device[dev] = pairs;
+  }
+  const int bound = tree_pairs_bound();
+  if (pairs > bound) pairs = bound;
+  const size_t n = (size_t)bound;
+  float4* parts = (float4*)ws;
+  float4* stats = (float4*)((uint8_t*)ws + up256(2 * n * kPartBytes));
+  Join* joins = (Join*)((uint8_t*)ws + up256(2 * n * kPartBytes) + up256(2 * n * kStatBytes));
+  CUtensorMap pv, pr, nv, nr;
+  if (!make_tmap_pages_bf16(&pv, pool, a.n_pages, page_stride, a.R, kDQK, 64, 16, 128) ||
+      !make_tmap_pages_bf16(&pr, pool, a.n_pages, page_stride, a.R, kDQK, 32, 16, 64) ||
+      !make_tmap_2d_bf16(&nv, kv_new, a.n_tok, kDQK, 64, 16, 128) ||
+      !make_tmap_2d_bf16(&nr, kv_new, a.n_tok, kDQK, 32, 16, 64))
+    return DSA_ERR_CUDA;
+  tree_attn_tc_kernel<<<2 * pairs, kThreads, smem, st>>>(a, (const __nv_bfloat16*)q, (const __nv_bfloat16*)kv_new,
+                                                         (__nv_bfloat16*)out, mx, sm, parts, stats, joins, c, pv, pr,
+                                                         nv, nr);
+  if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
+  tree_join_kernel<<<dim3(pairs, 16), kJoinThreads, 0, st>>>(parts, stats, joins, (__nv_bfloat16*)out, mx, sm);
+  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+}  // namespace dsa

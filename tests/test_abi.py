@@ -207,3 +207,34 @@ def test_cache_host_validation_without_gpu():
     with pytest.raises(ValueError):
         dsa.cache_copy_pages(c, torch.zeros(8, 4, 16), torch.zeros(3, dtype=torch.int32),
                              torch.zeros(1, dtype=torch.int32))
+
+
+def test_tree_attention_host_validation_without_gpu():
+    dsa = _lib()
+    assert ctypes.sizeof(dsa.dsa_tree) == 8 + 5 * 8
+    A = [0x10000 * (i + 1) for i in range(12)]
+    cache = lambda **kw: dsa.make_cache(**dict(dict(n_seqs=2, n_pages=8, page_rows=64, max_pages=3), **kw))
+    tree = lambda **kw: dsa.make_tree(**dict(dict(n_tok=5, H=16, d_qk=576, d_v=512, scale=0.1), **kw))
+
+    def call(c, t, pool=None, mask=None, q=A[0], ws=A[11]):
+        pool = pool or dsa.dsa_pool(A[1], 1, 0, 64 * 1152, 1152)
+        return dsa.lib.dsa_tree_attn_fwd(ctypes.byref(c), ctypes.byref(t), q, ctypes.byref(pool), A[2], A[3], A[4],
+                                         A[5], mask, A[6], A[7], A[8], ws, None)
+
+    I, U = dsa.DSA_ERR_INVALID_ARG, dsa.DSA_ERR_UNSUPPORTED
+    for c, t, code in ((cache(n_seqs=0), tree(), I), (cache(page_rows=24), tree(), U), (cache(), tree(n_tok=0), I),
+                       (cache(), tree(H=0), I), (cache(), tree(H=1025), U), (cache(), tree(d_qk=512), U),
+                       (cache(), tree(d_v=576), U), (cache(), tree(d_v=600), I), (cache(), tree(scale=-1.0), I),
+                       (cache(), tree(scale=float("nan")), I), (cache(), tree(n_tok=1 << 30), U),
+                       (cache(), tree(mask_words=-1), I), (cache(), tree(dtype="fp32", d_qk=1025), U)):
+        assert call(c, t) == code
+        assert dsa.tree_workspace_size(c, t) == 0
+    assert call(cache(), tree(mask_words=1)) == I and call(cache(), tree(), mask=A[9]) == I
+    assert call(cache(), tree(), q=None) == I and call(cache(), tree(), q=A[0] + 8) == I
+    for pool in (dsa.dsa_pool(None, 1, 0, 64 * 1152, 1152), dsa.dsa_pool(A[1], 2, 1 << 20, 64 * 1152, 1152),
+                 dsa.dsa_pool(A[1], 1, 0, 64 * 1152, 1024), dsa.dsa_pool(A[1], 1, 0, 64 * 1152 - 16, 1152),
+                 dsa.dsa_pool(A[1], 1, 0, 64 * 1152 + 8, 1152)):
+        assert call(cache(), tree(), pool=pool) == I
+    assert call(cache(), tree(), ws=None) == dsa.DSA_ERR_WORKSPACE
+    assert dsa.tree_workspace_size(cache(), tree()) > 0
+    assert dsa.tree_workspace_size(cache(page_rows=5), tree(dtype="fp32", d_qk=80, d_v=64)) == 0
