@@ -17,9 +17,8 @@
 // split by N between the CTAs' shared memories, and each CTA's accumulator
 // keeps its 64 rows twice over the 128 TMEM lanes: lanes 0..63 pair with CTA
 // 0's half of B, lanes 64..127 with CTA 1's.  CTA c holds columns D_c of every
-// key: value columns [128c, 128c+128) u [256+128c, 256+128c+128) and rope
-// columns [512+32c, 512+32c+32), so a key row crosses from L2 into shared
-// memory once per pair:
+// key: value columns [256c, 256c+256) and rope columns [512+32c, 512+32c+32),
+// so a key row crosses from L2 into shared memory once per pair:
 //   logits: A in TMEM, lanes h / 64+h hold row h's columns D_0 / D_1; lane h
 //     ends with the partial logit over D_0, lane 64+h with the one over D_1;
 //     the softmax warps add the two through shared memory;
@@ -29,8 +28,14 @@
 // TMEM: O 256 + logits 112 + query 144 columns.  Three key stages, two P
 // buffers; the logits of block j+1 run during the softmax of block j.
 //
-// Keys arrive by TMA in boxes of 16 rows (pages hold a multiple of 16 rows),
-// straight from the pages.  What a masked place holds never reaches the sums:
+// Keys arrive by TMA straight from the pages (which hold a multiple of 16
+// rows): one copy brings 16 or 32 rows x 256 value columns, already as the
+// tensor cores read them, [8-row group][64 columns][8 rows], one more their
+// rope columns.  Few large copies matter: issuing one holds the issuing thread
+// for about 180 cycles whatever its size (measured without any other work: 32
+// rows from one thread 55 bytes per cycle and SM, with the rope columns from a
+// second warp 69; 16 rows 34; 16 x 64 pieces 21, which bounded the whole loop).
+// What a masked place holds never reaches the sums:
 // a slot past the last row, on an unusable page, or seen by no token of the
 // tile is zeroed in shared memory before the tensor cores read it; a drafted
 // row with an infinity or NaN that only some of the tile's tokens see is
@@ -39,7 +44,7 @@
 // Roles per CTA: warp 0 = TMEM allocation, MMA issuer (CTA 0); warps 1..4 =
 // the tile's query columns into TMEM, and the passing on of each key stage
 // (with the zeroing above); warps 5..12 = softmax and epilogue; warp 13 =
-// schedule; warp 14 = TMA producer.
+// schedule; warps 14, 15 = key loads (value columns, rope columns).
 #include <math.h>
 
 #include "tree_attn.cuh"
@@ -50,16 +55,18 @@ namespace tree {
 constexpr int kHC = 64, kTile = 128, kDQK = 576, kDV = 512;
 constexpr int kBlk = 112, kGroups = kBlk / 16;
 constexpr int kStages = 3;
-constexpr int kChunk = kBlk * 128;                 // 112 slots x 64 value columns (SW128 rows)
+constexpr int kAtom = 8 * 128;                     // 8 slots x 64 value columns (SW128 rows)
+constexpr int kOct = 4 * kAtom;                    // 8 slots x the CTA's 256 value columns
+constexpr int kValue = kBlk / 8 * kOct;            // value part of a stage: [8-slot group][64 columns][8 slots]
 constexpr int kRope = kBlk * 64;                   // 112 slots x 32 rope columns (SW64 rows)
-constexpr int kStageBytes = 4 * kChunk + kRope;
-constexpr int kGroupBytes = 16 * (4 * 128 + 64);   // one box row group of 16 slots, all columns of a CTA
+constexpr int kStageBytes = kValue + kRope;
 constexpr int kPBytes = 2 * kHC * 128;
 constexpr int kPvSteps = kBlk / 16;
-constexpr int kFixWarps = 4, kSoftWarps = 8;
+constexpr int kUnit = 2 * kHC * 16;                // one float4 of every (column half, row): exchange unit
+constexpr int kFixWarps = 4, kSoftWarps = 8, kLoadWarps = 2, kSoftThreads = 32 * kSoftWarps;
 constexpr int kWarpFix0 = 1, kWarpSoft0 = kWarpFix0 + kFixWarps;
 constexpr int kWarpScan = kWarpSoft0 + kSoftWarps, kWarpLoad = kWarpScan + 1;
-constexpr int kThreads = 32 * (kWarpLoad + 1);
+constexpr int kThreads = 32 * (kWarpLoad + kLoadWarps);
 constexpr int kSlotsPerFix = kBlk / kFixWarps;     // 28
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = kColS + kBlk;
@@ -69,7 +76,7 @@ constexpr float kRescaleThreshold = 8.0f;          // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 static_assert(kColQ + 144 == kTmemCols, "TMEM columns");
-static_assert(kChunk % 1024 == 0 && kRope % 512 == 0 && kStageBytes % 1024 == 0, "operand alignment");
+static_assert(kValue % 1024 == 0 && kRope % 512 == 0 && kStageBytes % 1024 == 0, "operand alignment");
 
 // A pair's run is at least this many blocks: a shorter one costs more in its
 // own start and in the join than the blocks that another pair takes over.
@@ -91,21 +98,22 @@ struct Join {
 constexpr size_t kPartBytes = (size_t)kTile * kDV * 4, kStatBytes = (size_t)kTile * 16;
 
 struct __align__(1024) Smem {
-  uint8_t stage[kStages][kStageBytes];             // [value chunk 0..3 | rope][slot][row]
+  uint8_t stage[kStages][kStageBytes];             // value columns | rope columns
   uint8_t p[2][kPBytes];                           // P of even / odd blocks (and the exchange, and O)
   Seg seg[2];
   unsigned long long valid[kStages][2];            // slots that hold a row
   uint32_t bad[kStages][kFixWarps];                // 28 slots each: zeroed for an infinity or NaN
+  uint8_t spare[2 * kUnit];                        // of the logit exchange
   float red[kSoftWarps][32];
   uint32_t sink[kSoftWarps];                       // targets of CTA 1's signalling stores
-  uint32_t sink_f[kFixWarps];
+  uint32_t sink_f[2][kFixWarps];
   uint64_t st_full[kStages], st_empty[kStages], fixed[kStages], ready[kStages];
   uint64_t s_full, s_free, p_full[2];
   uint64_t q_tm[2], q_free[2], mma_done[2], sc_full[2], sc_empty[2], fin;
   uint32_t tmem_base;
   int abort, no_abort;
 };
-static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory budget");
+static_assert(sizeof(Smem) <= 232448, "shared memory budget");
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -147,10 +155,6 @@ __device__ __forceinline__ void commit2(uint32_t bar) {
       "h"((uint16_t)3)
       : "memory");
 }
-// arrive on a barrier of CTA 0, releasing at cluster scope
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
 __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -185,6 +189,18 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm,
           dst),
       "l"(tm), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* tm, int x0, int x1, int x2, int x3, int x4,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(tm), "r"(x0), "r"(x1), "r"(x2), "r"(x3), "r"(x4), "r"(bar)
+      : "memory");
+}
+// hint: bring `bytes` (a multiple of 16) from global memory into L2
+__device__ __forceinline__ void prefetch_l2_bulk(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ long long warp_sum(long long v) {
@@ -238,25 +254,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tree_attn_tc_kernel(TreeArgs a, const __nv_bfloat16* __restrict__ qg, const __nv_bfloat16* __restrict__ kvn,
                         __nv_bfloat16* __restrict__ out, float* __restrict__ mx, float* __restrict__ sm_out,
                         float4* __restrict__ parts, float4* __restrict__ stats, Join* __restrict__ joins,
-                        DevCtx c, const __grid_constant__ CUtensorMap tm_page_v,
-                        const __grid_constant__ CUtensorMap tm_page_r, const __grid_constant__ CUtensorMap tm_new_v,
-                        const __grid_constant__ CUtensorMap tm_new_r) {
-  extern __shared__ uint8_t smem_raw[];
-  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+                        DevCtx c, int wide, const __grid_constant__ CUtensorMap tm_page_v,
+                        const __grid_constant__ CUtensorMap tm_page_v2, const __grid_constant__ CUtensorMap tm_page_r,
+                        const __grid_constant__ CUtensorMap tm_page_r2, const __grid_constant__ CUtensorMap tm_new_v,
+                        const __grid_constant__ CUtensorMap tm_new_r, const __grid_constant__ CUtensorMap tm_out) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);   // the operands' swizzles need the 1024-byte alignment
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   volatile int* abort_flag = &sm.abort;
+  if ((smem_u32(smem_raw) & 1023u) != 0) {         // (dynamic shared memory starts at 1 KB: never)
+    set_status(c, DSA_ERR_CUDA);
+    return;
+  }
 
   if (threadIdx.x == 32 * kWarpFix0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&sm.st_full[i]), 1);
+      mbar_init(smem_u32(&sm.st_full[i]), kLoadWarps);
       mbar_init(smem_u32(&sm.st_empty[i]), 1);
       mbar_init(smem_u32(&sm.fixed[i]), kFixWarps);
-      mbar_init(smem_u32(&sm.ready[i]), 2 * kFixWarps);  // CTA 0's: both CTAs' stages passed on
+      mbar_init(smem_u32(&sm.ready[i]), kFixWarps);
     }
     mbar_init(smem_u32(&sm.s_full), 1);
-    // s_free, p_full, q_tm (used in CTA 0): the local warps arrive, the first
+    // ready, s_free, p_full, q_tm (used in CTA 0): the local warps arrive, the first
     // of them also expecting the 4 bytes that each of CTA 1's warps stores
     mbar_init(smem_u32(&sm.s_free), kSoftWarps);
     for (int i = 0; i < 2; ++i) {
@@ -266,7 +287,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sm.mma_done[i]), 1);
       mbar_init(smem_u32(&sm.sc_full[i]), 1);
       // readers of a segment: fix, softmax and load warps, and CTA 0's issuer
-      mbar_init(smem_u32(&sm.sc_empty[i]), kFixWarps + kSoftWarps + 1 + (crank == 0 ? 1 : 0));
+      mbar_init(smem_u32(&sm.sc_empty[i]), kFixWarps + kSoftWarps + kLoadWarps + (crank == 0 ? 1 : 0));
     }
     mbar_init(smem_u32(&sm.fin), 1);
     sm.abort = 0;
@@ -368,9 +389,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           mbar_arrive(smem_u32(&sm.sc_full[i & 1]));
         }
         __syncwarp();
+        const long long rows = (long long)s.T * a.H - 128ll * tile;
+        const long long row0 = (long long)s.t0 * a.H + 128ll * tile;
+        {                                          // this CTA's 64 query rows, into L2 ahead of their load
+          const long long mine = rows - kHC * (int)crank < kHC ? rows - kHC * (int)crank : kHC;
+          if (lane == 0 && mine > 0)
+            prefetch_l2_bulk(qg + (row0 + kHC * (int)crank) * kDQK, (uint32_t)mine * kDQK * 2);
+        }
         if (!whole && j == 0) {                    // the tile starts here and goes on in the next runs
-          const long long rows = (long long)s.T * a.H - 128ll * tile;
-          join.row0 = (long long)s.t0 * a.H + 128ll * tile;
+          join.row0 = row0;
           join.nrows = rows < kTile ? (int)rows : kTile;
           join.nparts = (int)((x + nb - 1) / run) - pair + 1;
         }
@@ -392,9 +419,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       sm.seg[i & 1].end = 1;
       mbar_arrive(smem_u32(&sm.sc_full[i & 1]));
     }
-  } else if (warp == kWarpLoad) {
+  } else if (warp >= kWarpLoad) {
     // ------------------------------- key loads -------------------------------
-    // 35 boxes per block: box = (16-slot group, 64 value columns or the rope)
+    // Groups of 16 slots; one copy takes two of them where they lie in one page
+    // (`wide`: pages of a multiple of 32 rows).  A drafted group starts at any
+    // row: value copies of 8 rows.
+    const bool rope = warp != kWarpLoad;
     int G = 0;                                     // blocks so far
     bool ok = true;
     for (int i = 0; ok; ++i) {
@@ -437,22 +467,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
         }
         const uint32_t bar = smem_u32(&sm.st_full[st]), base = smem_u32(sm.stage[st]);
+        // the second group of a pair goes with the first
+        uint32_t first = loaded, pairs = 0;
+        if (wide && !drafted) {
+          const uint32_t even = (j & 1) ? 0x2Au : 0x15u;  // groups at a multiple of 32 rows: 7 j + k even
+          pairs = loaded & even & 0x3Fu;                  // (group 6 has no second one in this block)
+          first = loaded & ~(pairs << 1);
+        }
         if (lane == 0) {
-          sm.valid[st][0] = v0;
-          sm.valid[st][1] = v1;
-          mbar_arrive_expect_tx(bar, (uint32_t)__popc(loaded) * kGroupBytes);
+          if (!rope) {
+            sm.valid[st][0] = v0;
+            sm.valid[st][1] = v1;
+          }
+          // a pair brings both its groups, the second past the last row or not
+          const int left = g.T - (j - g.nc) * kBlk, n8 = ((left < kBlk ? left : kBlk) + 7) / 8;
+          const int groups = __popc(first) + __popc(pairs);
+          mbar_arrive_expect_tx(bar, rope ? groups * 1024u : drafted ? n8 * (uint32_t)kOct : groups * 2u * kOct);
         }
         __syncwarp();
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int box = 32 * u + lane, k = box % kGroups, ch = box / kGroups;  // ch 4: rope
-          const int bx = __shfl_sync(0xffffffffu, x, k), bp = __shfl_sync(0xffffffffu, page, k);
-          if (box < 5 * kGroups && ((loaded >> k) & 1u)) {
-            const bool rope = ch == 4;
-            const int col = rope ? kDV + 32 * (int)crank : 256 * (ch >> 1) + 128 * (int)crank + 64 * (ch & 1);
-            const uint32_t dst = base + (rope ? 4 * kChunk + k * 1024 : ch * kChunk + k * 2048);
-            if (drafted) tma_load_2d(dst, rope ? &tm_new_r : &tm_new_v, col, bx, bar);
-            else tma_load_3d(dst, rope ? &tm_page_r : &tm_page_v, col, bx, bp, bar);
+#pragma unroll 1
+        for (uint32_t m = first; m; m &= m - 1) {
+          const int k = __ffs(m) - 1;
+          const int gx = __shfl_sync(0xffffffffu, x, k), gp = __shfl_sync(0xffffffffu, page, k);
+          const int gn = __shfl_sync(0xffffffffu, cnt, k);
+          const bool two = (pairs >> k) & 1u;
+          if (lane == 0) {
+            if (rope) {
+              const uint32_t dr = base + kValue + k * 1024;
+              const int col = kDV + 32 * (int)crank;
+              if (drafted) tma_load_2d(dr, &tm_new_r, col, gx, bar);
+              else tma_load_3d(dr, two ? &tm_page_r2 : &tm_page_r, col, gx, gp, bar);
+            } else {
+              const uint32_t dv = base + 2 * k * kOct;
+              if (drafted) {
+                tma_load_3d(dv, &tm_new_v, 0, gx, 4 * (int)crank, bar);
+                if (gn > 8) tma_load_3d(dv + kOct, &tm_new_v, 0, gx + 8, 4 * (int)crank, bar);
+              } else {
+                tma_load_5d(dv, two ? &tm_page_v2 : &tm_page_v, 0, 0, 4 * (int)crank, gx >> 3, gp, bar);
+              }
+            }
           }
         }
         __syncwarp();
@@ -466,7 +519,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int fw = warp - kWarpFix0;
     int G = 0;
     bool ok = true;
-    // one arrive per warp on a barrier of CTA 0
     for (int i = 0; ok; ++i) {
       if (!mbar_wait_warp(smem_u32(&sm.sc_full[i & 1]), (i >> 1) & 1, c, abort_flag)) break;
       const Seg g = sm.seg[i & 1];
@@ -475,38 +527,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (g.end) break;
       const long long rows = (long long)g.T * a.H - 128ll * g.tile;   // of the tile (more than 128: 128)
       {
-        // thread = TMEM lane l of this warp's quadrant: row l & 63, column half l >> 6
-        if (i > 0 && !mbar_wait_warp(smem_u32(&sm.q_free[(i - 1) & 1]), ((i - 1) >> 1) & 1, c, abort_flag)) break;
-        tc_fence_after();
+        // thread = TMEM lane l of this warp's quadrant: row l & 63, column half l >> 6.
+        // The first 192 value columns are loaded before the wait for the old query.
         const int l = (warp & 3) * 32 + lane, rr = kHC * (int)crank + (l & 63);
         const bool live = rr < rows;
         const __nv_bfloat16* qh =
             qg + ((long long)g.t0 * a.H + 128ll * g.tile + (live ? rr : 0)) * (long long)kDQK;
         const uint32_t lane_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint4* vsrc = reinterpret_cast<const uint4*>(qh + 128 * (l >> 6));
+        const uint4* vsrc = reinterpret_cast<const uint4*>(qh + 256 * (l >> 6));
+        const uint4* rsrc = reinterpret_cast<const uint4*>(qh + kDV + 32 * (l >> 6));
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 1
-        for (int p = 0; p < 4; ++p) {              // 64 value columns at a time -> TMEM columns kColQ + 32p
-          uint32_t w[32];
+        uint32_t w0[32], w1[32], w2[32];
+        auto fetch = [&](const uint4* src, uint32_t* w, int n) {
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            const uint4 v = live ? __ldg(vsrc + 32 * (p >> 1) + 8 * (p & 1) + t) : zero;
+          for (int t = 0; t < n; ++t) {
+            const uint4 v = live ? __ldg(src + t) : zero;
             w[4 * t] = v.x, w[4 * t + 1] = v.y, w[4 * t + 2] = v.z, w[4 * t + 3] = v.w;
           }
-          tmem_st32(lane_tmem + kColQ + 32 * p, w);
-          tmem_st_wait();
-        }
-        {
-          const uint4* rsrc = reinterpret_cast<const uint4*>(qh + kDV + 32 * (l >> 6));
-          uint32_t w2[16];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const uint4 v = live ? __ldg(rsrc + t) : zero;
-            w2[4 * t] = v.x, w2[4 * t + 1] = v.y, w2[4 * t + 2] = v.z, w2[4 * t + 3] = v.w;
-          }
-          tmem_st16(lane_tmem + kColQ + 128, w2);
-          tmem_st_wait();
-        }
+        };
+        fetch(vsrc, w0, 8);
+        fetch(vsrc + 8, w1, 8);
+        fetch(vsrc + 16, w2, 8);
+        if (i > 0 && !mbar_wait_warp(smem_u32(&sm.q_free[(i - 1) & 1]), ((i - 1) >> 1) & 1, c, abort_flag)) break;
+        tc_fence_after();
+        tmem_st32(lane_tmem + kColQ, w0);
+        tmem_st32(lane_tmem + kColQ + 32, w1);
+        tmem_st32(lane_tmem + kColQ + 64, w2);
+        tmem_st_wait();
+        uint32_t w3[16];
+        fetch(vsrc + 24, w0, 8);
+        fetch(rsrc, w3, 4);
+        tmem_st32(lane_tmem + kColQ + 96, w0);
+        tmem_st16(lane_tmem + kColQ + 128, w3);
+        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -515,7 +568,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (fw == 0) mbar_arrive_expect_tx(bar, 4 * kFixWarps);
             else mbar_arrive(bar);
           } else {
-            st_async_signal(mapa_shared(smem_u32(&sm.sink_f[fw]), 0), mapa_shared(bar, 0));
+            st_async_signal(mapa_shared(smem_u32(&sm.sink_f[0][fw]), 0), mapa_shared(bar, 0));
           }
         }
       }
@@ -525,19 +578,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int tb = last < g.T - 1 ? (int)last : g.T - 1;
       for (int j = g.j0; j < g.j1; ++j, ++G) {
         const int st = G % kStages;
-        if (!mbar_wait_warp(smem_u32(&sm.st_full[st]), (G / kStages) & 1, c, abort_flag)) {
-          ok = false;
-          break;
-        }
         // this warp's 28 slots: those that hold a row, those that any / every token of the tile sees
         constexpr uint32_t kAll = (1u << kSlotsPerFix) - 1u;
         const int s0 = kSlotsPerFix * fw;
-        uint32_t valid;
-        {
-          const unsigned long long v0 = sm.valid[st][0], v1 = sm.valid[st][1];
-          const unsigned long long w = s0 >= 64 ? v1 >> (s0 - 64) : (s0 ? (v0 >> s0) | (v1 << (64 - s0)) : v0);
-          valid = (uint32_t)w & kAll;
-        }
         uint32_t any = kAll, every = kAll;
         if (j >= g.nc) {
           const int first = (j - g.nc) * kBlk + s0;
@@ -558,6 +601,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             any = __reduce_or_sync(0xffffffffu, o);
             every = __reduce_and_sync(0xffffffffu, n);
           }
+        }
+        if (!mbar_wait_warp(smem_u32(&sm.st_full[st]), (G / kStages) & 1, c, abort_flag)) {
+          ok = false;
+          break;
+        }
+        uint32_t valid;
+        {
+          const unsigned long long v0 = sm.valid[st][0], v1 = sm.valid[st][1];
+          const unsigned long long w = s0 >= 64 ? v1 >> (s0 - 64) : (s0 ? (v0 >> s0) | (v1 << (64 - s0)) : v0);
+          valid = (uint32_t)w & kAll;
         }
         uint32_t clear = kAll & ~(valid & any), bad = 0;
         for (uint32_t mixed = valid & any & ~every; mixed; mixed &= mixed - 1) {
@@ -584,23 +637,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (uint32_t m = clear; m; m &= m - 1) {
             const int r = s0 + __ffs(m) - 1;
             uint8_t* base = sm.stage[st];
-            *reinterpret_cast<uint4*>(base + (lane >> 3) * kChunk + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-            if (lane < 4) *reinterpret_cast<uint4*>(base + 4 * kChunk + r * 64 + lane * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(base + (r >> 3) * kOct + (lane >> 3) * kAtom + (r & 7) * 128 + (lane & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+            if (lane < 4) *reinterpret_cast<uint4*>(base + kValue + r * 64 + lane * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();                // these writes -> the tensor cores' reads
         }
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_u32(&sm.fixed[st]));
-          mbar_arrive_cluster(mapa_shared(smem_u32(&sm.ready[st]), 0));
+          const uint32_t bar = smem_u32(&sm.ready[st]);
+          if (crank == 0) {
+            if (fw == 0) mbar_arrive_expect_tx(bar, 4 * kFixWarps);
+            else mbar_arrive(bar);
+          } else {
+            st_async_signal(mapa_shared(smem_u32(&sm.sink_f[1][fw]), 0), mapa_shared(bar, 0));
+          }
         }
       }
     }
   } else if (warp == 0) {
     if (crank == 0 && lane == 0) {
       // ------------------------------- MMA issuer -------------------------------
-      // Whichever is ready, the logits of the next block first; no progress
-      // for the wait budget is a timeout.
+      // Whichever is ready, the logits S(G) of the next block first once PV(G-2)
+      // is issued (the softmax of block G exchanges logits through that P
+      // buffer); no progress for the wait budget is a timeout.
       int Gs = 0, Gp = 0;                          // blocks so far: logits issued / PVs issued
       bool ok = true;
       for (int i = 0; ok; ++i) {
@@ -616,17 +677,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t spins = 0;
         while (ok && jp < nblk) {
           bool progressed = false;
-          if (js < nblk && js <= jp + 2 && (Gs == 0 || mbar_poll(smem_u32(&sm.s_free), (Gs - 1) & 1)) &&
+          if (js < nblk && js <= jp + 1 && (Gs == 0 || mbar_poll(smem_u32(&sm.s_free), (Gs - 1) & 1)) &&
               mbar_poll(smem_u32(&sm.ready[Gs % kStages]), (Gs / kStages) & 1)) {
             tc_fence_after();
             const uint32_t sb = smem_u32(sm.stage[Gs % kStages]);
 #pragma unroll
             for (int kk = 0; kk < 16; ++kk)
               mma2_ts(tmem + kColS, tmem + kColQ + kk * 8,
-                      sdesc(sb + (kk >> 2) * kChunk + (kk & 3) * 32, 16, 1024, kSw128), kIdescS, kk > 0 ? 1u : 0u);
+                      sdesc(sb + (kk >> 2) * kAtom + (kk & 3) * 32, 16, kOct, kSw128), kIdescS, kk > 0 ? 1u : 0u);
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-              mma2_ts(tmem + kColS, tmem + kColQ + 128 + r * 8, sdesc(sb + 4 * kChunk + r * 32, 16, 512, kSw64),
+              mma2_ts(tmem + kColS, tmem + kColQ + 128 + r * 8, sdesc(sb + kValue + r * 32, 16, 512, kSw64),
                       kIdescS, 1u);
             commit2(smem_u32(&sm.s_full));
             ++js;
@@ -641,7 +702,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               const uint64_t ad = sdesc(pa + (kk >> 2) * (kHC * 128) + (kk & 3) * 32, 16, 1024, kSw128);
 #pragma unroll
               for (int m = 0; m < 2; ++m)
-                mma2_ss(tmem + kColO + 128 * m, ad, sdesc(sb + 2 * m * kChunk + kk * 2048, kChunk, 1024, kSw128),
+                mma2_ss(tmem + kColO + 128 * m, ad, sdesc(sb + 2 * m * kAtom + kk * 2 * kOct, kAtom, kOct, kSw128),
                         kIdescPV, (jp > 0 || kk > 0) ? 1u : 0u);
             }
             commit2(smem_u32(&sm.st_empty[Gp % kStages]));
@@ -698,11 +759,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // (after a failed wait it goes on through the segment without work, and
     // the vote at the next one makes all of them stop).
     bool ok = true;
+    const bool o_storer = warp == kWarpSoft0 && lane == 0;
     int G = 0;
     for (int i = 0;; ++i) {
       const int bi = i & 1;
+      if (o_storer) bulk_wait_read_all();          // the last tile's O has left the P buffers
       if (ok) ok = mbar_wait_warp(smem_u32(&sm.sc_full[bi]), (i >> 1) & 1, c, abort_flag);
-      if (named_bar_or(2, kSoftWarps * 32, !ok)) break;
+      if (named_bar_or(2, kSoftThreads, !ok)) break;
       const Seg g = sm.seg[bi];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[bi]));
@@ -710,7 +773,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const long long rows = (long long)g.T * a.H - 128ll * g.tile;
       const bool live = rr < rows;
       const int tok = live ? (int)((128ll * g.tile + rr) / a.H) : g.T - 1;
-      float m_run = -INFINITY, m_true = -INFINITY, l_run = 0.f;
+      float m_run = -INFINITY, m_own = -INFINITY, l_run = 0.f;  // m_own: over this thread's slots
       bool poison = false;
       for (int j = g.j0; j < g.j1; ++j, ++G) {
         const int pb = G & 1, st = G % kStages;
@@ -737,6 +800,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (half) vmask &= 0x00ffffffu;
         }
+        // the exchange below uses P buffer pb, last read by PV(G - 2), which is issued ahead of the logits of G
+        if (ok && G >= 2)
+          ok = mbar_wait_warp(smem_u32(&sm.st_empty[(G - 2) % kStages]), ((G - 2) / kStages) & 1, c, abort_flag);
         if (ok) ok = mbar_wait_warp(smem_u32(&sm.s_full), G & 1, c, abort_flag);
         // partial logits of row hl over this lane half's columns
         uint32_t v0[32], v1[16], v2[8];
@@ -752,9 +818,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc_fence_before();
           __syncwarp();
           signal(&sm.s_free);                      // the logit buffer is free
-          // the exchange below reuses P buffer pb, last read by PV(G - 2)
-          if (G >= 2)
-            ok = mbar_wait_warp(smem_u32(&sm.st_empty[(G - 2) % kStages]), ((G - 2) / kStages) & 1, c, abort_flag);
         } else {
 #pragma unroll
           for (int t = 0; t < 32; ++t) v0[t] = 0u;
@@ -763,11 +826,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int t = 0; t < 8; ++t) v2[t] = 0u;
         }
-        // Exchange with the lane-pair partner (lane l ^ 64, same ch) through P
-        // buffer pb, in two rounds of up to 4 float4 per thread: half 0 sends
-        // slots 32..55, half 1 slots 0..31 of the column half.
-        float4* xb = reinterpret_cast<float4*>(sm.p[pb]);
-        auto xslot = [&](int t, int dest) { return xb + ((t * 2 + ch) * 2 + dest) * kHC + hl; };
+        // Exchange with the lane-pair partner (lane l ^ 64, same ch): half 1
+        // sends slots 0..31 of the column half (8 float4), half 0 slots 32..55
+        // (6 float4).  One float4 of all 128 (ch, row) is a unit of 2 KB; the 14
+        // units take what is free now: P buffer pb (8), the rope part of this
+        // block's stage (3; its last reader, the logits, is done), the spare (2)
+        // and the slots 112..127 that the other P buffer's rows do not use (1).
+        auto unit = [&](int u) -> float4* {
+          uint8_t* base;
+          if (u < 8) base = sm.p[pb] + u * kUnit;
+          else if (u < 11) base = sm.stage[st] + kValue + (u - 8) * kUnit;
+          else if (u < 13) base = sm.spare + (u - 11) * kUnit;
+          else return reinterpret_cast<float4*>(sm.p[pb ^ 1] + kHC * 128 + hl * 128 + (((6 + ch) ^ (hl & 7)) << 4));
+          return reinterpret_cast<float4*>(base + (ch * kHC + hl) * 16);
+        };
         float x[32];
         if (half == 0) {
 #pragma unroll
@@ -780,41 +852,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int t = 24; t < 32; ++t) x[t] = 0.f;
         }
+        if (half == 0) {
 #pragma unroll
-        for (int rnd = 0; rnd < 2; ++rnd) {
-          if (half == 0) {
+          for (int q = 0; q < 6; ++q)
+            *unit(8 + q) = q < 4 ? make_float4(__uint_as_float(v1[4 * (q & 3)]), __uint_as_float(v1[4 * (q & 3) + 1]),
+                                               __uint_as_float(v1[4 * (q & 3) + 2]), __uint_as_float(v1[4 * (q & 3) + 3]))
+                                 : make_float4(__uint_as_float(v2[4 * (q & 1)]), __uint_as_float(v2[4 * (q & 1) + 1]),
+                                               __uint_as_float(v2[4 * (q & 1) + 2]), __uint_as_float(v2[4 * (q & 1) + 3]));
+        } else {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              const int q = 4 * rnd + t;
-              if (q < 4)
-                *xslot(t, 1) = make_float4(__uint_as_float(v1[4 * q]), __uint_as_float(v1[4 * q + 1]),
-                                           __uint_as_float(v1[4 * q + 2]), __uint_as_float(v1[4 * q + 3]));
-              else if (q < 6)
-                *xslot(t, 1) =
-                    make_float4(__uint_as_float(v2[4 * (q - 4)]), __uint_as_float(v2[4 * (q - 4) + 1]),
-                                __uint_as_float(v2[4 * (q - 4) + 2]), __uint_as_float(v2[4 * (q - 4) + 3]));
-            }
-          } else {
+          for (int q = 0; q < 8; ++q)
+            *unit(q) = make_float4(__uint_as_float(v0[4 * q]), __uint_as_float(v0[4 * q + 1]),
+                                   __uint_as_float(v0[4 * q + 2]), __uint_as_float(v0[4 * q + 3]));
+        }
+        named_bar_sync(1, kSoftThreads);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              const int q = 4 * rnd + t;
-              *xslot(t, 0) = make_float4(__uint_as_float(v0[4 * q]), __uint_as_float(v0[4 * q + 1]),
-                                         __uint_as_float(v0[4 * q + 2]), __uint_as_float(v0[4 * q + 3]));
-            }
+        for (int q = 0; q < 8; ++q) {
+          if (4 * q < kept) {
+            const float4 pr = half == 0 ? *unit(q) : *unit(8 + (q < 6 ? q : 0));
+            x[4 * q] += pr.x;
+            x[4 * q + 1] += pr.y;
+            x[4 * q + 2] += pr.z;
+            x[4 * q + 3] += pr.w;
           }
-          named_bar_sync(1, kSoftWarps * 32);
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int q = 4 * rnd + t;
-            if (4 * q < kept) {
-              const float4 pr = *xslot(t, half);
-              x[4 * q] += pr.x;
-              x[4 * q + 1] += pr.y;
-              x[4 * q + 2] += pr.z;
-              x[4 * q + 3] += pr.w;
-            }
-          }
-          named_bar_sync(1, kSoftWarps * 32);      // the region is rewritten next
         }
         float bm = -INFINITY;
 #pragma unroll
@@ -822,54 +882,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (((vmask >> t) & 1u) == 0) x[t] = -INFINITY;
           bm = fmaxf(bm, x[t]);
         }
-        // the row's block max over its four threads (lane pair x column halves)
-        sm.red[ws][lane] = bm;
-        named_bar_sync(1, kSoftWarps * 32);
-        bm = fmaxf(fmaxf(sm.red[quad][lane], sm.red[quad + 4][lane]),
-                   fmaxf(sm.red[quad ^ 2][lane], sm.red[(quad ^ 2) + 4][lane]));
-        // (red is rewritten only behind the next block's first barrier)
-        if (!ok) continue;
         bm *= sl2e;                                // log2 units (sl2e > 0)
-        m_true = fmaxf(m_true, bm);
-        // The maximum that P is taken against moves only when a block's exceeds
-        // it by more than 2^8: rescaling O in TMEM is rare, and P stays below
-        // 2^8 (bf16 and fp32 lose nothing by a power of two).
-        const bool need = bm > m_run + kRescaleThreshold;
-        if (__any_sync(0xffffffffu, need)) {
-          const float m_new = need ? bm : m_run;
-          const float alpha = (m_run == -INFINITY || !need) ? (need ? 0.f : 1.f) : ex2(m_run - m_new);
-          if (j > g.j0 && __any_sync(0xffffffffu, need && m_run != -INFINITY)) {
-            // O must hold PV(G-1) before it is rescaled
-            ok = mbar_wait_warp(smem_u32(&sm.st_empty[(G - 1) % kStages]), ((G - 1) / kStages) & 1, c, abort_flag);
-            if (!ok) continue;
-            tc_fence_after();
-#pragma unroll 1
-            for (int m = 0; m < 2; ++m)
-#pragma unroll 1
-              for (int cc = 0; cc < 64; cc += 32) {
-                const uint32_t oa = tmem + lane_off + kColO + 128 * m + 64 * ch + cc;
-                uint32_t o[32];
-                tmem_ld32(oa, o);
-                tmem_ld_wait(o);
+        m_own = fmaxf(m_own, bm);
+        // The maximum that P is taken against moves only when a logit exceeds it
+        // by more than 2^8: rescaling O in TMEM is rare, and P stays below 2^8
+        // (bf16 and fp32 lose nothing by a power of two).  So P is computed
+        // before it is known whether another thread of the row has such a logit.
+        float lsum_blk;
+        uint32_t pk[16];
+        auto weights = [&]() {
+          const float mu = (m_run == -INFINITY) ? 0.f : m_run;
+          lsum_blk = 0.f;
 #pragma unroll
-                for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * alpha);
-                tmem_st32(oa, o);
+          for (int t = 0; t < 16; ++t) {
+            const float pa = ex2(fmaf(x[2 * t], sl2e, -mu));
+            const float pc = ex2(fmaf(x[2 * t + 1], sl2e, -mu));
+            lsum_blk += pa + pc;                   // the sum takes P before its rounding
+            pk[t] = pack_bf16x2(pa, pc);           // bf16: the operand type of the PV product
+          }
+        };
+        weights();
+        // (this barrier also ends the reads of the exchange units)
+        if (named_bar_or(3, kSoftThreads, bm > m_run + kRescaleThreshold)) {
+          // the row's block max over its four threads (lane pair x column halves)
+          sm.red[ws][lane] = bm;
+          named_bar_sync(1, kSoftThreads);
+          bm = fmaxf(fmaxf(sm.red[quad][lane], sm.red[quad + 4][lane]),
+                     fmaxf(sm.red[quad ^ 2][lane], sm.red[(quad ^ 2) + 4][lane]));
+          // (red is rewritten only behind the next block's first barrier)
+          const bool need = bm > m_run + kRescaleThreshold;
+          if (ok && __any_sync(0xffffffffu, need)) {
+            const float m_new = need ? bm : m_run;
+            const float alpha = (m_run == -INFINITY || !need) ? (need ? 0.f : 1.f) : ex2(m_run - m_new);
+            if (j > g.j0 && __any_sync(0xffffffffu, need && m_run != -INFINITY)) {
+              // O must hold PV(G-1) before it is rescaled
+              ok = mbar_wait_warp(smem_u32(&sm.st_empty[(G - 1) % kStages]), ((G - 1) / kStages) & 1, c, abort_flag);
+              if (!ok) continue;
+              tc_fence_after();
+#pragma unroll 1
+              for (int cc = 0; cc < 128; cc += 16) {
+                const uint32_t oa = tmem + lane_off + kColO + 128 * (cc >> 6) + 64 * ch + (cc & 63);
+                uint32_t o[16];
+                tmem_ld16(oa, o);
+                tmem_ld_wait16(o);
+#pragma unroll
+                for (int t = 0; t < 16; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * alpha);
+                tmem_st16(oa, o);
                 tmem_st_wait();
               }
-            tc_fence_before();
+              tc_fence_before();
+            }
+            l_run *= alpha;
+            m_run = m_new;
+            weights();
           }
-          l_run *= alpha;
-          m_run = m_new;
         }
-        const float mu = (m_run == -INFINITY) ? 0.f : m_run;
-        uint32_t pk[16];
-#pragma unroll
-        for (int t = 0; t < 16; ++t) {
-          const float pa = ex2(fmaf(x[2 * t], sl2e, -mu));
-          const float pc = ex2(fmaf(x[2 * t + 1], sl2e, -mu));
-          l_run += pa + pc;                        // the sum takes P before its rounding
-          pk[t] = pack_bf16x2(pa, pc);             // bf16: the operand type of the PV product
-        }
+        if (!ok) continue;
+        l_run += lsum_blk;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if (8 * q < kept) {
@@ -887,12 +956,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (ok) ok = mbar_wait_warp(smem_u32(&sm.mma_done[bi]), (i >> 1) & 1, c, abort_flag);
       tc_fence_after();
       if (poison) l_run = NAN;
-      named_bar_sync(1, kSoftWarps * 32);
+      named_bar_sync(1, kSoftThreads);
       sm.red[ws][lane] = l_run;
-      named_bar_sync(1, kSoftWarps * 32);
+      named_bar_sync(1, kSoftThreads);
       const float lsum = (sm.red[quad][lane] + sm.red[quad + 4][lane]) +
                          (sm.red[quad ^ 2][lane] + sm.red[(quad ^ 2) + 4][lane]);
-      const bool all_ok = named_bar_or(2, kSoftWarps * 32, !ok) == false;
+      named_bar_sync(1, kSoftThreads);
+      sm.red[ws][lane] = m_own;
+      const bool all_ok = named_bar_or(2, kSoftThreads, !ok) == false;
+      const float m_true = fmaxf(fmaxf(sm.red[quad][lane], sm.red[quad + 4][lane]),
+                                 fmaxf(sm.red[quad ^ 2][lane], sm.red[(quad ^ 2) + 4][lane]));
       if (!all_ok) {
         ok = false;
         continue;
@@ -908,7 +981,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t o[32];
             tmem_ld32(tmem + lane_off + kColO + 128 * m + 64 * ch + cc, o);
             tmem_ld_wait(o);
-            const int quad0 = (256 * m + 128 * half + 64 * ch + cc) / 4;
+            const int quad0 = (256 * half + 128 * m + 64 * ch + cc) / 4;
 #pragma unroll
             for (int t = 0; t < 8; ++t)
               po[(size_t)(quad0 + t) * kTile] =
@@ -920,14 +993,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // no visible key: 0
         const long long row0 = (long long)g.t0 * a.H + 128ll * g.tile + kHC * (int)crank;  // first row of this CTA
         const int nrow = rows - kHC * (int)crank < kHC ? (int)(rows - kHC * (int)crank) : kHC;
-        // bf16 rows through shared memory, in two rounds of 256 value columns
-        // (both P buffers, as four 64-column tiles with the 128-byte swizzle)
+        // bf16 rows out through shared memory, in two rounds of 256 value columns
+        // (both P buffers, as four 64-column tiles with the 128-byte swizzle;
+        // tile 2 half + ch: columns 256 half + 128 m + 64 ch)
         uint8_t* const ostage = &sm.p[0][0];
         uint8_t* const trow = ostage + (2 * half + ch) * (kHC * 128) + hl * 128;
         const int th = threadIdx.x - 32 * kWarpSoft0;
 #pragma unroll 1
         for (int m = 0; m < 2; ++m) {
-          if (m == 1) named_bar_sync(1, kSoftWarps * 32);  // round 0 read before it is overwritten
+          if (m == 1) {                            // round 0 read before it is overwritten
+            if (o_storer) bulk_wait_read_all();
+            named_bar_sync(1, kSoftThreads);
+          }
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {
             uint32_t o[16];
@@ -940,13 +1017,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(trow + (((2 * q4) ^ (hl & 7)) << 4)) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
             *reinterpret_cast<uint4*>(trow + (((2 * q4 + 1) ^ (hl & 7)) << 4)) = make_uint4(pw[4], pw[5], pw[6], pw[7]);
           }
-          named_bar_sync(1, kSoftWarps * 32);
+          fence_proxy_async_smem();
+          named_bar_sync(1, kSoftThreads);
+          if (nrow == kHC) {                       // all 64 rows: TMA stores, not waited for here
+            if (o_storer) {
+#pragma unroll 1
+              for (int tt = 0; tt < 4; ++tt)
+                tma_store_2d(&tm_out, smem_u32(ostage + tt * (kHC * 128)), 256 * (tt >> 1) + 128 * m + 64 * (tt & 1),
+                             (int)row0);
+              bulk_commit_group();
+            }
+          } else {                                 // the sequence's last rows: nothing behind them is touched
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int r = 8 * e + (th >> 5), c16 = th & 31;  // row, 16-byte piece of the 256 columns
-            if (r < nrow)
-              *reinterpret_cast<uint4*>(out + (row0 + r) * kDV + 256 * m + 8 * c16) = *reinterpret_cast<const uint4*>(
-                  ostage + (c16 >> 3) * (kHC * 128) + r * 128 + (((c16 & 7) ^ (r & 7)) << 4));
+            for (int e = 0; e < 8; ++e) {
+              const int r = 8 * e + (th >> 5), tt = (th >> 3) & 3, pc = th & 7;  // row, tile, 16-byte piece
+              if (r < nrow)
+                *reinterpret_cast<uint4*>(out + (row0 + r) * kDV + 256 * (tt >> 1) + 128 * m + 64 * (tt & 1) + 8 * pc) =
+                    *reinterpret_cast<const uint4*>(ostage + tt * (kHC * 128) + r * 128 + ((pc ^ (r & 7)) << 4));
+            }
           }
         }
         if (half == 0 && ch == 0 && live) {
@@ -957,6 +1045,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();                           // O is overwritten by the next segment's first PV
     }
+    if (o_storer) bulk_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -1025,10 +1114,8 @@ __global__ void __launch_bounds__(kJoinThreads)
 
 }  // namespace tree
 
-bool make_tmap_2d_bf16(CUtensorMap* tm, const void* base, uint64_t rows, uint64_t cols, uint32_t box_cols,
-                       uint32_t box_rows, int swizzle_bytes);
-bool make_tmap_pages_bf16(CUtensorMap* tm, const void* base, uint64_t pages, uint64_t page_stride, uint64_t rows,
-                          uint64_t cols, uint32_t box_cols, uint32_t box_rows, int swizzle_bytes);
+bool make_tmap_bf16(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                    const uint32_t* box, int swizzle_bytes);
 
 // CTA pairs of the kernel at most: one CTA per SM (152 SMs when there is no device to ask)
 static int tree_pairs_bound() {
@@ -1049,7 +1136,7 @@ size_t tree_tc_workspace() {
 int launch_tree_attn_tc(const TreeArgs& a, const void* q, const void* pool, long long page_stride, const void* kv_new,
                         void* out, float* mx, float* sm, void* ws, DevCtx c, cudaStream_t st) {
   using namespace tree;
-  const size_t smem = sizeof(Smem) + 1024;
+  const size_t smem = sizeof(Smem);
   if (cudaFuncSetAttribute(tree_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return DSA_ERR_CUDA;
   static int pairs_by_device[64] = {0};
@@ -1073,15 +1160,29 @@ int launch_tree_attn_tc(const TreeArgs& a, const void* q, const void* pool, long
   float4* parts = (float4*)ws;
   float4* stats = (float4*)((uint8_t*)ws + up256(2 * n * kPartBytes));
   Join* joins = (Join*)((uint8_t*)ws + up256(2 * n * kPartBytes) + up256(2 * n * kStatBytes));
-  CUtensorMap pv, pr, nv, nr;
-  if (!make_tmap_pages_bf16(&pv, pool, a.n_pages, page_stride, a.R, kDQK, 64, 16, 128) ||
-      !make_tmap_pages_bf16(&pr, pool, a.n_pages, page_stride, a.R, kDQK, 32, 16, 64) ||
-      !make_tmap_2d_bf16(&nv, kv_new, a.n_tok, kDQK, 64, 16, 128) ||
-      !make_tmap_2d_bf16(&nr, kv_new, a.n_tok, kDQK, 32, 16, 64))
+  CUtensorMap pv, pv2, pr, pr2, nv, nr, po;
+  // cached value columns: 64 columns, 8 rows, 64-column blocks, 8-row groups, pages; drafted ones: any first row
+  const uint64_t row = kDQK * 2, R = (uint64_t)a.R, P = (uint64_t)a.n_pages, N = (uint64_t)a.n_tok;
+  const uint64_t pv_dim[5] = {64, 8, 8, R / 8, P}, pv_str[4] = {row, 128, 8 * row, (uint64_t)page_stride};
+  const uint64_t pr_dim[3] = {kDQK, R, P}, pr_str[2] = {row, (uint64_t)page_stride};
+  const uint64_t nv_dim[3] = {64, N, 8}, nv_str[2] = {row, 128};
+  const uint64_t nr_dim[2] = {kDQK, N}, nr_str[1] = {row};
+  const uint32_t pv_box[5] = {64, 8, 4, 2, 1}, pr_box[3] = {32, 16, 1}, nv_box[3] = {64, 8, 4}, nr_box[2] = {32, 16};
+  const uint64_t po_dim[2] = {kDV, N * (uint64_t)a.H}, po_str[1] = {kDV * 2};
+  const uint32_t po_box[2] = {64, kHC};
+  const int wide = a.R % 32 == 0;                  // two groups of 16 rows per copy
+  const uint32_t pv2_box[5] = {64, 8, 4, wide ? 4u : 2u, 1}, pr2_box[3] = {32, wide ? 32u : 16u, 1};
+  if (!make_tmap_bf16(&pv, pool, 5, pv_dim, pv_str, pv_box, 128) ||
+      !make_tmap_bf16(&pv2, pool, 5, pv_dim, pv_str, pv2_box, 128) ||
+      !make_tmap_bf16(&pr, pool, 3, pr_dim, pr_str, pr_box, 64) ||
+      !make_tmap_bf16(&pr2, pool, 3, pr_dim, pr_str, pr2_box, 64) ||
+      !make_tmap_bf16(&nv, kv_new, 3, nv_dim, nv_str, nv_box, 128) ||
+      !make_tmap_bf16(&nr, kv_new, 2, nr_dim, nr_str, nr_box, 64) ||
+      !make_tmap_bf16(&po, out, 2, po_dim, po_str, po_box, 128))
     return DSA_ERR_CUDA;
   tree_attn_tc_kernel<<<2 * pairs, kThreads, smem, st>>>(a, (const __nv_bfloat16*)q, (const __nv_bfloat16*)kv_new,
-                                                         (__nv_bfloat16*)out, mx, sm, parts, stats, joins, c, pv, pr,
-                                                         nv, nr);
+                                                         (__nv_bfloat16*)out, mx, sm, parts, stats, joins, c,
+                                                         wide, pv, pv2, pr, pr2, nv, nr, po);
   if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
   tree_join_kernel<<<dim3(pairs, 16), kJoinThreads, 0, st>>>(parts, stats, joins, (__nv_bfloat16*)out, mx, sm);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
