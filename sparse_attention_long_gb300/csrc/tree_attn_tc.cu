@@ -198,6 +198,15 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* tm,
       "l"(tm), "r"(x0), "r"(x1), "r"(x2), "r"(x3), "r"(x4), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void st_zero16(uint32_t addr) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+}
+// 32 bytes (32-byte aligned) of global memory that is only read here
+__device__ __forceinline__ void ld_global32(const void* p, uint32_t* w) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
 // hint: bring `bytes` (a multiple of 16) from global memory into L2
 __device__ __forceinline__ void prefetch_l2_bulk(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
@@ -517,6 +526,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp >= kWarpFix0 && warp < kWarpSoft0) {
     // ---------------------- query columns, key stages passed on ----------------------
     const int fw = warp - kWarpFix0;
+    const bool wide_q = (reinterpret_cast<uintptr_t>(qg) & 31u) == 0;  // 32-byte loads (rows are 1152 bytes)
     int G = 0;
     bool ok = true;
     for (int i = 0; ok; ++i) {
@@ -534,20 +544,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const __nv_bfloat16* qh =
             qg + ((long long)g.t0 * a.H + 128ll * g.tile + (live ? rr : 0)) * (long long)kDQK;
         const uint32_t lane_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint4* vsrc = reinterpret_cast<const uint4*>(qh + 256 * (l >> 6));
-        const uint4* rsrc = reinterpret_cast<const uint4*>(qh + kDV + 32 * (l >> 6));
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        const __nv_bfloat16 *vsrc = qh + 256 * (l >> 6), *rsrc = qh + kDV + 32 * (l >> 6);
         uint32_t w0[32], w1[32], w2[32];
-        auto fetch = [&](const uint4* src, uint32_t* w, int n) {
+        // A warp's load touches 32 rows, so 32 lines: the widest loads take the
+        // fewest turns of the load pipe, which the softmax's exchange shares.
+        auto fetch = [&](const __nv_bfloat16* src, uint32_t* w, int n) {
 #pragma unroll
           for (int t = 0; t < n; ++t) {
-            const uint4 v = live ? __ldg(src + t) : zero;
-            w[4 * t] = v.x, w[4 * t + 1] = v.y, w[4 * t + 2] = v.z, w[4 * t + 3] = v.w;
+            if (!live) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[8 * t + e] = 0u;
+            } else if (wide_q) {
+              ld_global32(src + 16 * t, w + 8 * t);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + 16 * t) + e);
+                w[8 * t + 4 * e] = v.x, w[8 * t + 4 * e + 1] = v.y, w[8 * t + 4 * e + 2] = v.z, w[8 * t + 4 * e + 3] = v.w;
+              }
+            }
           }
         };
-        fetch(vsrc, w0, 8);
-        fetch(vsrc + 8, w1, 8);
-        fetch(vsrc + 16, w2, 8);
+        fetch(vsrc, w0, 4);
+        fetch(vsrc + 64, w1, 4);
+        fetch(vsrc + 128, w2, 4);
         if (i > 0 && !mbar_wait_warp(smem_u32(&sm.q_free[(i - 1) & 1]), ((i - 1) >> 1) & 1, c, abort_flag)) break;
         tc_fence_after();
         tmem_st32(lane_tmem + kColQ, w0);
@@ -555,8 +575,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_st32(lane_tmem + kColQ + 64, w2);
         tmem_st_wait();
         uint32_t w3[16];
-        fetch(vsrc + 24, w0, 8);
-        fetch(rsrc, w3, 4);
+        fetch(vsrc + 192, w0, 4);
+        fetch(rsrc, w3, 2);
         tmem_st32(lane_tmem + kColQ + 96, w0);
         tmem_st16(lane_tmem + kColQ + 128, w3);
         tmem_st_wait();
@@ -634,12 +654,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         clear |= bad;
         if (lane == 0) sm.bad[st][fw] = bad;
         if (clear) {
-          for (uint32_t m = clear; m; m &= m - 1) {
-            const int r = s0 + __ffs(m) - 1;
-            uint8_t* base = sm.stage[st];
-            *reinterpret_cast<uint4*>(base + (r >> 3) * kOct + (lane >> 3) * kAtom + (r & 7) * 128 + (lane & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-            if (lane < 4) *reinterpret_cast<uint4*>(base + kValue + r * 64 + lane * 16) = make_uint4(0, 0, 0, 0);
+          const uint32_t base = smem_u32(sm.stage[st]);
+          const uint32_t pv = base + (lane >> 3) * kAtom + (lane & 7) * 16, pr = base + kValue + (lane & 3) * 16;
+#pragma unroll
+          for (int k = 0; k < kSlotsPerFix; ++k) {
+            const int r = s0 + k;
+            if ((clear >> k) & 1u) {
+              st_zero16(pv + (r >> 3) * kOct + (r & 7) * 128);
+              if (lane < 4) st_zero16(pr + r * 64);
+            }
           }
           fence_proxy_async_smem();                // these writes -> the tensor cores' reads
         }
@@ -1001,22 +1024,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int th = threadIdx.x - 32 * kWarpSoft0;
 #pragma unroll 1
         for (int m = 0; m < 2; ++m) {
+          uint32_t pw[32];
+#pragma unroll
+          for (int cc = 0; cc < 64; cc += 32) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lane_off + kColO + 128 * m + 64 * ch + cc, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int t = 0; t < 16; ++t)
+              pw[cc / 2 + t] = pack_bf16x2(__uint_as_float(o[2 * t]) * inv, __uint_as_float(o[2 * t + 1]) * inv);
+          }
           if (m == 1) {                            // round 0 read before it is overwritten
             if (o_storer) bulk_wait_read_all();
             named_bar_sync(1, kSoftThreads);
           }
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            uint32_t o[16];
-            tmem_ld16(tmem + lane_off + kColO + 128 * m + 64 * ch + 16 * q4, o);
-            tmem_ld_wait16(o);
-            uint32_t pw[8];
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-              pw[t] = pack_bf16x2(__uint_as_float(o[2 * t]) * inv, __uint_as_float(o[2 * t + 1]) * inv);
-            *reinterpret_cast<uint4*>(trow + (((2 * q4) ^ (hl & 7)) << 4)) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
-            *reinterpret_cast<uint4*>(trow + (((2 * q4 + 1) ^ (hl & 7)) << 4)) = make_uint4(pw[4], pw[5], pw[6], pw[7]);
-          }
+          for (int t = 0; t < 8; ++t)
+            *reinterpret_cast<uint4*>(trow + ((t ^ (hl & 7)) << 4)) =
+                make_uint4(pw[4 * t], pw[4 * t + 1], pw[4 * t + 2], pw[4 * t + 3]);
           fence_proxy_async_smem();
           named_bar_sync(1, kSoftThreads);
           if (nrow == kHC) {                       // all 64 rows: TMA stores, not waited for here
