@@ -43,8 +43,8 @@
 //
 // Roles per CTA: warp 0 = TMEM allocation, MMA issuer (CTA 0); warps 1..4 =
 // the tile's query columns into TMEM, and the passing on of each key stage
-// (with the zeroing above); warps 5..12 = softmax and epilogue; warp 13 =
-// schedule; warps 14, 15 = key loads (value columns, rope columns).
+// (with the zeroing above); warps 5..20 = softmax and epilogue; warp 21 =
+// schedule; warps 22, 23 = key loads (value columns, rope columns).
 #include <math.h>
 
 #include "tree_attn.cuh"
@@ -62,8 +62,8 @@ constexpr int kRope = kBlk * 64;                   // 112 slots x 32 rope column
 constexpr int kStageBytes = kValue + kRope;
 constexpr int kPBytes = 2 * kHC * 128;
 constexpr int kPvSteps = kBlk / 16;
-constexpr int kUnit = 2 * kHC * 16;                // one float4 of every (column half, row): exchange unit
-constexpr int kFixWarps = 4, kSoftWarps = 8, kLoadWarps = 2, kSoftThreads = 32 * kSoftWarps;
+constexpr int kUnit = 4 * kHC * 16;                // one float4 of every (column part, row): exchange unit
+constexpr int kFixWarps = 4, kSoftWarps = 16, kLoadWarps = 2, kSoftThreads = 32 * kSoftWarps;
 constexpr int kWarpFix0 = 1, kWarpSoft0 = kWarpFix0 + kFixWarps;
 constexpr int kWarpScan = kWarpSoft0 + kSoftWarps, kWarpLoad = kWarpScan + 1;
 constexpr int kThreads = 32 * (kWarpLoad + kLoadWarps);
@@ -103,8 +103,7 @@ struct __align__(1024) Smem {
   Seg seg[2];
   unsigned long long valid[kStages][2];            // slots that hold a row
   uint32_t bad[kStages][kFixWarps];                // 28 slots each: zeroed for an infinity or NaN
-  uint8_t spare[2 * kUnit];                        // of the logit exchange
-  float red[kSoftWarps][32];
+  uint8_t spare[kUnit];                            // of the logit exchange; row maxima and sums between exchanges
   uint32_t sink[kSoftWarps];                       // targets of CTA 1's signalling stores
   uint32_t sink_f[2][kFixWarps];
   uint64_t st_full[kStages], st_empty[kStages], fixed[kStages], ready[kStages];
@@ -132,18 +131,27 @@ __device__ __forceinline__ void tmem_relinquish2() {
 __device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-__device__ __forceinline__ void mma2_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The issuing thread shares its scheduler with the softmax warps, so each
+// instruction of it takes several cycles: an operand descriptor is one low word
+// that moves by a constant from MMA to MMA, and a constant high word (18 MMAs
+// with whole descriptors computed for each took 1,350 cycles to issue, against
+// the 1,010 that they run).
+constexpr uint32_t desc_hi(uint32_t sbo, uint32_t layout) { return (sbo >> 4) | (1u << 14) | (layout << 29); }
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+__device__ __forceinline__ void mma2_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                        uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void mma2_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma2_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                        uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 // arrive once on the barrier at the same offset in both CTAs of the pair when
@@ -464,6 +472,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         const uint32_t loaded = __ballot_sync(0xffffffffu, cnt > 0);
+        const uint32_t bar = smem_u32(&sm.st_full[st]), base = smem_u32(sm.stage[st]);
+        const uint32_t even = (j & 1) ? 0x2Au : 0x15u;  // groups at a multiple of 32 rows: 7 j + k even
+        if (wide && !drafted && loaded == 0x7Fu) {
+          // The usual block: three copies of 32 rows and one of 16, the 16 first (j
+          // odd) or last, from coordinates that are ready before the wait.
+          const int k0 = j & 1;
+          int gx[4], gp[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {            // t < 3: groups k0 + 2t and the next; t = 3: the single one
+            const int k = t < 3 ? k0 + 2 * t : (k0 ? 0 : 6);
+            gx[t] = __shfl_sync(0xffffffffu, x, k);
+            gp[t] = __shfl_sync(0xffffffffu, page, k);
+          }
+          const int last = __shfl_sync(0xffffffffu, cnt, kGroups - 1);
+          const uint32_t d0 = base + (rope ? kValue + k0 * 1024 : k0 * 2 * kOct);
+          const uint32_t d3 = base + (rope ? kValue + (k0 ? 0 : 6 * 1024) : (k0 ? 0 : 12 * kOct));
+          if (!mbar_wait_warp(smem_u32(&sm.st_empty[st]), ((G / kStages) & 1) ^ 1, c, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            if (rope) {
+              mbar_arrive_expect_tx(bar, kRope);
+              const int col = kDV + 32 * (int)crank;
+#pragma unroll
+              for (int t = 0; t < 3; ++t) tma_load_3d(d0 + t * 2048, &tm_page_r2, col, gx[t], gp[t], bar);
+              tma_load_3d(d3, &tm_page_r, col, gx[3], gp[3], bar);
+            } else {
+              sm.valid[st][0] = ~0ull;
+              sm.valid[st][1] = 0xFFFFFFFFull | ((unsigned long long)((1u << last) - 1u) << 32);
+              mbar_arrive_expect_tx(bar, kValue);
+#pragma unroll
+              for (int t = 0; t < 3; ++t)
+                tma_load_5d(d0 + t * 4 * kOct, &tm_page_v2, 0, 0, 4 * (int)crank, gx[t] >> 3, gp[t], bar);
+              tma_load_5d(d3, &tm_page_v, 0, 0, 4 * (int)crank, gx[3] >> 3, gp[3], bar);
+            }
+          }
+          __syncwarp();
+          continue;
+        }
         unsigned long long v0 = 0, v1 = 0;
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) {
@@ -475,12 +523,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        const uint32_t bar = smem_u32(&sm.st_full[st]), base = smem_u32(sm.stage[st]);
         // the second group of a pair goes with the first
         uint32_t first = loaded, pairs = 0;
         if (wide && !drafted) {
-          const uint32_t even = (j & 1) ? 0x2Au : 0x15u;  // groups at a multiple of 32 rows: 7 j + k even
-          pairs = loaded & even & 0x3Fu;                  // (group 6 has no second one in this block)
+          pairs = loaded & even & 0x3Fu;           // (group 6 has no second one in this block)
           first = loaded & ~(pairs << 1);
         }
         if (lane == 0) {
@@ -538,14 +584,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const long long rows = (long long)g.T * a.H - 128ll * g.tile;   // of the tile (more than 128: 128)
       {
         // thread = TMEM lane l of this warp's quadrant: row l & 63, column half l >> 6.
-        // The first 192 value columns are loaded before the wait for the old query.
+        // The first 64 value columns are loaded before the wait for the old query.
         const int l = (warp & 3) * 32 + lane, rr = kHC * (int)crank + (l & 63);
         const bool live = rr < rows;
         const __nv_bfloat16* qh =
             qg + ((long long)g.t0 * a.H + 128ll * g.tile + (live ? rr : 0)) * (long long)kDQK;
         const uint32_t lane_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const __nv_bfloat16 *vsrc = qh + 256 * (l >> 6), *rsrc = qh + kDV + 32 * (l >> 6);
-        uint32_t w0[32], w1[32], w2[32];
+        uint32_t w0[32];
         // A warp's load touches 32 rows, so 32 lines: the widest loads take the
         // fewest turns of the load pipe, which the softmax's exchange shares.
         auto fetch = [&](const __nv_bfloat16* src, uint32_t* w, int n) {
@@ -566,18 +612,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         };
         fetch(vsrc, w0, 4);
-        fetch(vsrc + 64, w1, 4);
-        fetch(vsrc + 128, w2, 4);
         if (i > 0 && !mbar_wait_warp(smem_u32(&sm.q_free[(i - 1) & 1]), ((i - 1) >> 1) & 1, c, abort_flag)) break;
         tc_fence_after();
-        tmem_st32(lane_tmem + kColQ, w0);
-        tmem_st32(lane_tmem + kColQ + 32, w1);
-        tmem_st32(lane_tmem + kColQ + 64, w2);
-        tmem_st_wait();
+#pragma unroll 1
+        for (int p = 0; p < 4; ++p) {              // 64 value columns -> TMEM columns kColQ + 32p
+          tmem_st32(lane_tmem + kColQ + 32 * p, w0);
+          tmem_st_wait();
+          if (p < 3) fetch(vsrc + 64 * (p + 1), w0, 4);
+        }
         uint32_t w3[16];
-        fetch(vsrc + 192, w0, 4);
         fetch(rsrc, w3, 2);
-        tmem_st32(lane_tmem + kColQ + 96, w0);
         tmem_st16(lane_tmem + kColQ + 128, w3);
         tmem_st_wait();
         tc_fence_before();
@@ -626,9 +670,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
+        const unsigned long long v0 = sm.valid[st][0], v1 = sm.valid[st][1];
         uint32_t valid;
         {
-          const unsigned long long v0 = sm.valid[st][0], v1 = sm.valid[st][1];
           const unsigned long long w = s0 >= 64 ? v1 >> (s0 - 64) : (s0 ? (v0 >> s0) | (v1 << (64 - s0)) : v0);
           valid = (uint32_t)w & kAll;
         }
@@ -686,6 +730,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // is issued (the softmax of block G exchanges logits through that P
       // buffer); no progress for the wait budget is a timeout.
       int Gs = 0, Gp = 0;                          // blocks so far: logits issued / PVs issued
+      uint32_t ss = 0, ss_par = 0, sp = 0;         // their stages (and the parity of the first's phase)
       bool ok = true;
       for (int i = 0; ok; ++i) {
         const int bi = i & 1;
@@ -701,34 +746,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         while (ok && jp < nblk) {
           bool progressed = false;
           if (js < nblk && js <= jp + 1 && (Gs == 0 || mbar_poll(smem_u32(&sm.s_free), (Gs - 1) & 1)) &&
-              mbar_poll(smem_u32(&sm.ready[Gs % kStages]), (Gs / kStages) & 1)) {
+              mbar_poll(smem_u32(&sm.ready[0]) + 8 * ss, ss_par)) {
             tc_fence_after();
-            const uint32_t sb = smem_u32(sm.stage[Gs % kStages]);
+            const uint32_t sb = smem_u32(sm.stage[0]) + ss * kStageBytes;
+            const uint32_t v = desc_lo(sb, 16), r = desc_lo(sb + kValue, 16);
 #pragma unroll
             for (int kk = 0; kk < 16; ++kk)
-              mma2_ts(tmem + kColS, tmem + kColQ + kk * 8,
-                      sdesc(sb + (kk >> 2) * kAtom + (kk & 3) * 32, 16, kOct, kSw128), kIdescS, kk > 0 ? 1u : 0u);
+              mma2_ts(tmem + kColS, tmem + kColQ + kk * 8, v + ((kk >> 2) * kAtom + (kk & 3) * 32) / 16,
+                      desc_hi(kOct, kSw128), kIdescS, kk > 0 ? 1u : 0u);
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-              mma2_ts(tmem + kColS, tmem + kColQ + 128 + r * 8, sdesc(sb + kValue + r * 32, 16, 512, kSw64),
-                      kIdescS, 1u);
+            for (int k = 0; k < 2; ++k)
+              mma2_ts(tmem + kColS, tmem + kColQ + 128 + k * 8, r + 2 * k, desc_hi(512, kSw64), kIdescS, 1u);
             commit2(smem_u32(&sm.s_full));
             ++js;
             ++Gs;
+            if (++ss == kStages) ss = 0, ss_par ^= 1;
             if (js == nblk) commit2(smem_u32(&sm.q_free[bi]));
             progressed = true;
           } else if (jp < js && mbar_poll(smem_u32(&sm.p_full[Gp & 1]), (Gp >> 1) & 1)) {
             tc_fence_after();
-            const uint32_t sb = smem_u32(sm.stage[Gp % kStages]), pa = smem_u32(sm.p[Gp & 1]);
+            const uint32_t sb = smem_u32(sm.stage[0]) + sp * kStageBytes;
+            const uint32_t v = desc_lo(sb, kAtom), p = desc_lo(smem_u32(sm.p[0]) + (Gp & 1) * kPBytes, 16);
 #pragma unroll
             for (int kk = 0; kk < kPvSteps; ++kk) {
-              const uint64_t ad = sdesc(pa + (kk >> 2) * (kHC * 128) + (kk & 3) * 32, 16, 1024, kSw128);
 #pragma unroll
               for (int m = 0; m < 2; ++m)
-                mma2_ss(tmem + kColO + 128 * m, ad, sdesc(sb + 2 * m * kAtom + kk * 2 * kOct, kAtom, kOct, kSw128),
-                        kIdescPV, (jp > 0 || kk > 0) ? 1u : 0u);
+                mma2_ss(tmem + kColO + 128 * m, p + ((kk >> 2) * (kHC * 128) + (kk & 3) * 32) / 16,
+                        desc_hi(1024, kSw128), v + (2 * m * kAtom + kk * 2 * kOct) / 16, desc_hi(kOct, kSw128),
+                        kIdescPV, kk > 0 ? 1u : (uint32_t)(jp > 0));
             }
-            commit2(smem_u32(&sm.st_empty[Gp % kStages]));
+            commit2(smem_u32(&sm.st_empty[0]) + 8 * sp);
+            if (++sp == kStages) sp = 0;
             ++jp;
             ++Gp;
             progressed = true;
@@ -760,10 +808,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int rr = kHC * (int)crank + hl;          // row in the tile
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const float sl2e = a.scale * kLog2e;
-    // thread (lane l, column half ch) keeps slots [56ch, 56ch+32) of row hl in
-    // lane half 0, [56ch+32, 56ch+56) in lane half 1
-    const int kept = half ? 24 : 32;
-    const int s0 = 56 * ch + (half ? 32 : 0);
+    // Column part ch = slots [c0, c0 + 32) (ch even) or [c0, c0 + 24) (ch odd) of
+    // the block; thread (lane l, part ch) keeps the first 16 of row hl in lane
+    // half 0, the rest in lane half 1 (runs of 8: whole 16-byte pieces of P).
+    const int c0 = 56 * (ch >> 1) + 32 * (ch & 1);
+    const int kept = half && (ch & 1) ? 8 : 16;
+    const int s0 = c0 + 16 * half;
+    const uint32_t keep_bits = (1u << kept) - 1u;
     auto signal = [&](uint64_t* bar) {
       if (lane == 0) {
         if (crank == 0) {
@@ -774,7 +825,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     };
-    // bits [s0, s0 + 32) of 112 slot bits
+    float (*red)[32] = reinterpret_cast<float(*)[32]>(sm.spare);  // [kSoftWarps][32]
+    // of a row's eight values in red[], the same order in each of its threads
+    auto row_max = [&]() {
+      float m = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        m = fmaxf(m, fmaxf(red[4 * t + (quad & 1)][lane], red[4 * t + 2 + (quad & 1)][lane]));
+      return m;
+    };
+    // bits from s0 on of 112 slot bits
     auto cut = [&](unsigned long long v0, unsigned long long v1) -> uint32_t {
       return (uint32_t)(s0 >= 64 ? v1 >> (s0 - 64) : (s0 ? (v0 >> s0) | (v1 << (64 - s0)) : v0));
     };
@@ -809,7 +869,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int first = (j - g.nc) * kBlk + s0;
             if (a.mask == nullptr) {
               const int n = tok - first + 1;
-              vmask &= n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+              vmask &= n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1u;
             } else {
               const unsigned long long* mrow = a.mask + (long long)(g.t0 + tok) * a.mask_words;
               const int w = first >> 6, sh = first & 63;
@@ -819,80 +879,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             const unsigned long long b0 = sm.bad[st][0], b1 = sm.bad[st][1], b2 = sm.bad[st][2], b3 = sm.bad[st][3];
             const uint32_t bad = cut(b0 | (b1 << 28) | (b2 << 56), (b2 >> 8) | (b3 << 20));
-            if (vmask & bad & (half ? 0x00ffffffu : 0xffffffffu)) poison = true;
+            if (vmask & bad & keep_bits) poison = true;
           }
-          if (half) vmask &= 0x00ffffffu;
+          vmask &= keep_bits;
         }
         // the exchange below uses P buffer pb, last read by PV(G - 2), which is issued ahead of the logits of G
         if (ok && G >= 2)
           ok = mbar_wait_warp(smem_u32(&sm.st_empty[(G - 2) % kStages]), ((G - 2) / kStages) & 1, c, abort_flag);
         if (ok) ok = mbar_wait_warp(smem_u32(&sm.s_full), G & 1, c, abort_flag);
         // partial logits of row hl over this lane half's columns
-        uint32_t v0[32], v1[16], v2[8];
+        uint32_t lo[16], hi[16];                   // the part's slots 0..15 and 16..31 (ch odd: 16..23)
+#pragma unroll
+        for (int t = 0; t < 16; ++t) hi[t] = 0u;
         if (ok) {
           tc_fence_after();
-          const uint32_t sbuf = tmem + lane_off + kColS + 56 * ch;
-          tmem_ld32(sbuf, v0);
-          tmem_ld16(sbuf + 32, v1);
-          tmem_ld8(sbuf + 48, v2);
-          tmem_ld_wait(v0);
-          tmem_ld_also16(v1);
-          tmem_ld_also8(v2);
+          const uint32_t sbuf = tmem + lane_off + kColS + c0;
+          tmem_ld16(sbuf, lo);
+          tmem_ld16(sbuf + 16, hi);                // (ch odd: 8 columns of the next part or the query, unused)
+          tmem_ld_wait16(lo);
+          tmem_ld_also16(hi);
           tc_fence_before();
           __syncwarp();
           signal(&sm.s_free);                      // the logit buffer is free
         } else {
 #pragma unroll
-          for (int t = 0; t < 32; ++t) v0[t] = 0u;
-#pragma unroll
-          for (int t = 0; t < 16; ++t) v1[t] = 0u;
-#pragma unroll
-          for (int t = 0; t < 8; ++t) v2[t] = 0u;
+          for (int t = 0; t < 16; ++t) lo[t] = 0u;
         }
         // Exchange with the lane-pair partner (lane l ^ 64, same ch): half 1
-        // sends slots 0..31 of the column half (8 float4), half 0 slots 32..55
-        // (6 float4).  One float4 of all 128 (ch, row) is a unit of 2 KB; the 14
-        // units take what is free now: P buffer pb (8), the rope part of this
-        // block's stage (3; its last reader, the logits, is done), the spare (2)
-        // and the slots 112..127 that the other P buffer's rows do not use (1).
-        auto unit = [&](int u) -> float4* {
+        // sends the part's slots 0..15 (4 float4), half 0 the others (4, or 2 for
+        // ch odd).  One float4 of all 256 (ch, row) takes 4 KB; the 28 KB take what
+        // is free now: P buffer pb (half 1's), the rope part of this block's stage
+        // (its last reader, the logits, is done; half 0's first and third), the
+        // spare (second), and the slots 112..127 that the other P buffer's rows do
+        // not use (fourth).
+        auto unit = [&](int q, int from_half) -> float4* {
           uint8_t* base;
-          if (u < 8) base = sm.p[pb] + u * kUnit;
-          else if (u < 11) base = sm.stage[st] + kValue + (u - 8) * kUnit;
-          else if (u < 13) base = sm.spare + (u - 11) * kUnit;
-          else return reinterpret_cast<float4*>(sm.p[pb ^ 1] + kHC * 128 + hl * 128 + (((6 + ch) ^ (hl & 7)) << 4));
-          return reinterpret_cast<float4*>(base + (ch * kHC + hl) * 16);
+          if (from_half) base = sm.p[pb] + q * kUnit + (ch * kHC + hl) * 16;
+          else if (q == 0) base = sm.stage[st] + kValue + (ch * kHC + hl) * 16;
+          else if (q == 1) base = sm.spare + (ch * kHC + hl) * 16;
+          else if (q == 2) base = sm.stage[st] + kValue + kUnit + ((ch >> 1) * kHC + hl) * 16;
+          else base = sm.p[pb ^ 1] + kHC * 128 + hl * 128 + (((6 + (ch >> 1)) ^ (hl & 7)) << 4);
+          return reinterpret_cast<float4*>(base);
         };
-        float x[32];
+        float x[16];
         if (half == 0) {
 #pragma unroll
-          for (int t = 0; t < 32; ++t) x[t] = __uint_as_float(v0[t]);
+          for (int q = 0; q < 4; ++q)
+            if (q < 2 || (ch & 1) == 0)
+              *unit(q, 0) = make_float4(__uint_as_float(hi[4 * q]), __uint_as_float(hi[4 * q + 1]),
+                                        __uint_as_float(hi[4 * q + 2]), __uint_as_float(hi[4 * q + 3]));
+#pragma unroll
+          for (int t = 0; t < 16; ++t) x[t] = __uint_as_float(lo[t]);
         } else {
 #pragma unroll
-          for (int t = 0; t < 16; ++t) x[t] = __uint_as_float(v1[t]);
+          for (int q = 0; q < 4; ++q)
+            *unit(q, 1) = make_float4(__uint_as_float(lo[4 * q]), __uint_as_float(lo[4 * q + 1]),
+                                      __uint_as_float(lo[4 * q + 2]), __uint_as_float(lo[4 * q + 3]));
 #pragma unroll
-          for (int t = 0; t < 8; ++t) x[16 + t] = __uint_as_float(v2[t]);
-#pragma unroll
-          for (int t = 24; t < 32; ++t) x[t] = 0.f;
-        }
-        if (half == 0) {
-#pragma unroll
-          for (int q = 0; q < 6; ++q)
-            *unit(8 + q) = q < 4 ? make_float4(__uint_as_float(v1[4 * (q & 3)]), __uint_as_float(v1[4 * (q & 3) + 1]),
-                                               __uint_as_float(v1[4 * (q & 3) + 2]), __uint_as_float(v1[4 * (q & 3) + 3]))
-                                 : make_float4(__uint_as_float(v2[4 * (q & 1)]), __uint_as_float(v2[4 * (q & 1) + 1]),
-                                               __uint_as_float(v2[4 * (q & 1) + 2]), __uint_as_float(v2[4 * (q & 1) + 3]));
-        } else {
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            *unit(q) = make_float4(__uint_as_float(v0[4 * q]), __uint_as_float(v0[4 * q + 1]),
-                                   __uint_as_float(v0[4 * q + 2]), __uint_as_float(v0[4 * q + 3]));
+          for (int t = 0; t < 16; ++t) x[t] = __uint_as_float(hi[t]);
         }
         named_bar_sync(1, kSoftThreads);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
+        for (int q = 0; q < 4; ++q) {
           if (4 * q < kept) {
-            const float4 pr = half == 0 ? *unit(q) : *unit(8 + (q < 6 ? q : 0));
+            const float4 pr = half == 0 ? *unit(q, 1) : *unit(q, 0);
             x[4 * q] += pr.x;
             x[4 * q + 1] += pr.y;
             x[4 * q + 2] += pr.z;
@@ -901,7 +951,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         float bm = -INFINITY;
 #pragma unroll
-        for (int t = 0; t < 32; ++t) {
+        for (int t = 0; t < 16; ++t) {
           if (((vmask >> t) & 1u) == 0) x[t] = -INFINITY;
           bm = fmaxf(bm, x[t]);
         }
@@ -912,12 +962,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // (bf16 and fp32 lose nothing by a power of two).  So P is computed
         // before it is known whether another thread of the row has such a logit.
         float lsum_blk;
-        uint32_t pk[16];
+        uint32_t pk[8];
         auto weights = [&]() {
           const float mu = (m_run == -INFINITY) ? 0.f : m_run;
           lsum_blk = 0.f;
 #pragma unroll
-          for (int t = 0; t < 16; ++t) {
+          for (int t = 0; t < 8; ++t) {
             const float pa = ex2(fmaf(x[2 * t], sl2e, -mu));
             const float pc = ex2(fmaf(x[2 * t + 1], sl2e, -mu));
             lsum_blk += pa + pc;                   // the sum takes P before its rounding
@@ -927,12 +977,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         weights();
         // (this barrier also ends the reads of the exchange units)
         if (named_bar_or(3, kSoftThreads, bm > m_run + kRescaleThreshold)) {
-          // the row's block max over its four threads (lane pair x column halves)
-          sm.red[ws][lane] = bm;
+          // the row's block max over its eight threads (lane pair x column parts)
+          red[ws][lane] = bm;
           named_bar_sync(1, kSoftThreads);
-          bm = fmaxf(fmaxf(sm.red[quad][lane], sm.red[quad + 4][lane]),
-                     fmaxf(sm.red[quad ^ 2][lane], sm.red[(quad ^ 2) + 4][lane]));
-          // (red is rewritten only behind the next block's first barrier)
+          bm = row_max();
+          named_bar_sync(1, kSoftThreads);         // red makes room for the next exchange
           const bool need = bm > m_run + kRescaleThreshold;
           if (ok && __any_sync(0xffffffffu, need)) {
             const float m_new = need ? bm : m_run;
@@ -943,8 +992,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (!ok) continue;
               tc_fence_after();
 #pragma unroll 1
-              for (int cc = 0; cc < 128; cc += 16) {
-                const uint32_t oa = tmem + lane_off + kColO + 128 * (cc >> 6) + 64 * ch + (cc & 63);
+              for (int cc = 0; cc < 64; cc += 16) {
+                const uint32_t oa = tmem + lane_off + kColO + 128 * (cc >> 5) + 32 * ch + (cc & 31);
                 uint32_t o[16];
                 tmem_ld16(oa, o);
                 tmem_ld_wait16(o);
@@ -963,7 +1012,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok) continue;
         l_run += lsum_blk;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
           if (8 * q < kept) {
             const int sl = s0 + 8 * q;
             uint8_t* prow = sm.p[pb] + (sl >> 6) * (kHC * 128) + hl * 128;
@@ -980,15 +1029,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_after();
       if (poison) l_run = NAN;
       named_bar_sync(1, kSoftThreads);
-      sm.red[ws][lane] = l_run;
+      red[ws][lane] = l_run;
       named_bar_sync(1, kSoftThreads);
-      const float lsum = (sm.red[quad][lane] + sm.red[quad + 4][lane]) +
-                         (sm.red[quad ^ 2][lane] + sm.red[(quad ^ 2) + 4][lane]);
+      float lsum = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) lsum += red[4 * t + (quad & 1)][lane] + red[4 * t + 2 + (quad & 1)][lane];
       named_bar_sync(1, kSoftThreads);
-      sm.red[ws][lane] = m_own;
+      red[ws][lane] = m_own;
       const bool all_ok = named_bar_or(2, kSoftThreads, !ok) == false;
-      const float m_true = fmaxf(fmaxf(sm.red[quad][lane], sm.red[quad + 4][lane]),
-                                 fmaxf(sm.red[quad ^ 2][lane], sm.red[(quad ^ 2) + 4][lane]));
+      const float m_true = row_max();
       if (!all_ok) {
         ok = false;
         continue;
@@ -998,19 +1047,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // 32 rows make whole lines
         float4* po = parts + (size_t)g.part * (kTile * kDV / 4) + rr;
 #pragma unroll 1
-        for (int m = 0; m < 2; ++m)
-#pragma unroll 1
-          for (int cc = 0; cc < 64; cc += 32) {
-            uint32_t o[32];
-            tmem_ld32(tmem + lane_off + kColO + 128 * m + 64 * ch + cc, o);
-            tmem_ld_wait(o);
-            const int quad0 = (256 * half + 128 * m + 64 * ch + cc) / 4;
+        for (int m = 0; m < 2; ++m) {
+          uint32_t o[32];
+          tmem_ld32(tmem + lane_off + kColO + 128 * m + 32 * ch, o);
+          tmem_ld_wait(o);
+          const int quad0 = (256 * half + 128 * m + 32 * ch) / 4;
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
-              po[(size_t)(quad0 + t) * kTile] =
-                  make_float4(__uint_as_float(o[4 * t]), __uint_as_float(o[4 * t + 1]),
-                              __uint_as_float(o[4 * t + 2]), __uint_as_float(o[4 * t + 3]));
-          }
+          for (int t = 0; t < 8; ++t)
+            po[(size_t)(quad0 + t) * kTile] =
+                make_float4(__uint_as_float(o[4 * t]), __uint_as_float(o[4 * t + 1]), __uint_as_float(o[4 * t + 2]),
+                            __uint_as_float(o[4 * t + 3]));
+        }
         if (half == 0 && ch == 0) stats[(size_t)g.part * kTile + rr] = make_float4(m_run, lsum, m_true, 0.f);
       } else {
         const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // no visible key: 0
@@ -1018,29 +1065,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int nrow = rows - kHC * (int)crank < kHC ? (int)(rows - kHC * (int)crank) : kHC;
         // bf16 rows out through shared memory, in two rounds of 256 value columns
         // (both P buffers, as four 64-column tiles with the 128-byte swizzle;
-        // tile 2 half + ch: columns 256 half + 128 m + 64 ch)
+        // tile 2 half + ch / 2: columns 256 half + 128 m + 64 (ch / 2))
         uint8_t* const ostage = &sm.p[0][0];
-        uint8_t* const trow = ostage + (2 * half + ch) * (kHC * 128) + hl * 128;
+        uint8_t* const trow = ostage + (2 * half + (ch >> 1)) * (kHC * 128) + hl * 128;
         const int th = threadIdx.x - 32 * kWarpSoft0;
 #pragma unroll 1
         for (int m = 0; m < 2; ++m) {
-          uint32_t pw[32];
-#pragma unroll
-          for (int cc = 0; cc < 64; cc += 32) {
+          uint32_t pw[16];
+          {
             uint32_t o[32];
-            tmem_ld32(tmem + lane_off + kColO + 128 * m + 64 * ch + cc, o);
+            tmem_ld32(tmem + lane_off + kColO + 128 * m + 32 * ch, o);
             tmem_ld_wait(o);
 #pragma unroll
             for (int t = 0; t < 16; ++t)
-              pw[cc / 2 + t] = pack_bf16x2(__uint_as_float(o[2 * t]) * inv, __uint_as_float(o[2 * t + 1]) * inv);
+              pw[t] = pack_bf16x2(__uint_as_float(o[2 * t]) * inv, __uint_as_float(o[2 * t + 1]) * inv);
           }
           if (m == 1) {                            // round 0 read before it is overwritten
             if (o_storer) bulk_wait_read_all();
             named_bar_sync(1, kSoftThreads);
           }
 #pragma unroll
-          for (int t = 0; t < 8; ++t)
-            *reinterpret_cast<uint4*>(trow + ((t ^ (hl & 7)) << 4)) =
+          for (int t = 0; t < 4; ++t)
+            *reinterpret_cast<uint4*>(trow + (((4 * (ch & 1) + t) ^ (hl & 7)) << 4)) =
                 make_uint4(pw[4 * t], pw[4 * t + 1], pw[4 * t + 2], pw[4 * t + 3]);
           fence_proxy_async_smem();
           named_bar_sync(1, kSoftThreads);
@@ -1054,8 +1100,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           } else {                                 // the sequence's last rows: nothing behind them is touched
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int r = 8 * e + (th >> 5), tt = (th >> 3) & 3, pc = th & 7;  // row, tile, 16-byte piece
+            for (int e = 0; e < 4; ++e) {
+              const int r = 16 * e + (th >> 5), tt = (th >> 3) & 3, pc = th & 7;  // row, tile, 16-byte piece
               if (r < nrow)
                 *reinterpret_cast<uint4*>(out + (row0 + r) * kDV + 256 * (tt >> 1) + 128 * m + 64 * (tt & 1) + 8 * pc) =
                     *reinterpret_cast<const uint4*>(ostage + tt * (kHC * 128) + r * 128 + ((pc ^ (r & 7)) << 4));
