@@ -35,17 +35,19 @@
 // for about 180 cycles whatever its size (measured without any other work: 32
 // rows from one thread 55 bytes per cycle and SM, with the rope columns from a
 // second warp 69; 16 rows 34; 16 x 64 pieces 21, which bounded the whole loop).
-// What a masked place holds never reaches the sums:
-// a slot past the last row, on an unusable page, or seen by no token of the
-// tile is zeroed in shared memory before the tensor cores read it; a drafted
-// row with an infinity or NaN that only some of the tile's tokens see is
-// zeroed too, and the tokens that see it get NaN.
+// What a masked place holds never reaches the sums.  Its logit is masked; and
+// where a 16-slot step of P V has a slot past the last row, on an unusable
+// page, or seen by no token of the tile, the slot's value columns are zeroed in
+// shared memory before the tensor cores read them (steps without any seen slot
+// are not run).  A drafted row with an infinity or NaN that only some of the
+// tile's tokens see is zeroed too, and the tokens that see it get NaN.
 //
 // Roles per CTA: warp 0 = TMEM allocation, MMA issuer (CTA 0); warps 1..4 =
-// the tile's query columns into TMEM, and the passing on of each key stage
-// (with the zeroing above); warps 5..20 = softmax and epilogue; warp 21 =
-// schedule; warps 22, 23 = key loads (value columns, rope columns).
+// passing on of each key stage (with the zeroing above); warps 5..20 = softmax,
+// epilogue, and the next tile's query columns into TMEM; warp 21 = schedule;
+// warps 22, 23 = key loads (value columns, rope columns).
 #include <math.h>
+#include <stddef.h>
 
 #include "tree_attn.cuh"
 
@@ -67,7 +69,7 @@ constexpr int kFixWarps = 4, kSoftWarps = 16, kLoadWarps = 2, kSoftThreads = 32 
 constexpr int kWarpFix0 = 1, kWarpSoft0 = kWarpFix0 + kFixWarps;
 constexpr int kWarpScan = kWarpSoft0 + kSoftWarps, kWarpLoad = kWarpScan + 1;
 constexpr int kThreads = 32 * (kWarpLoad + kLoadWarps);
-constexpr int kSlotsPerFix = kBlk / kFixWarps;     // 28
+static_assert(kBlk <= 32 * kFixWarps && kBlk % 16 == 0, "a fix warp takes two 16-slot steps");
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = kColS + kBlk;
 constexpr uint32_t kIdescS = idesc_bf16(128, 2 * kBlk, false, false);
@@ -102,16 +104,20 @@ struct __align__(1024) Smem {
   uint8_t p[2][kPBytes];                           // P of even / odd blocks (and the exchange, and O)
   Seg seg[2];
   unsigned long long valid[kStages][2];            // slots that hold a row
-  uint32_t bad[kStages][kFixWarps];                // 28 slots each: zeroed for an infinity or NaN
-  uint8_t spare[kUnit];                            // of the logit exchange; row maxima and sums between exchanges
+  uint32_t bad[kStages][kFixWarps];                // 32 slots each: zeroed for an infinity or NaN
+  alignas(4) uint8_t live[kStages][kFixWarps];                // 2 steps of 16 slots each: some token sees some slot
+  alignas(16) uint8_t spare[kUnit];                // of the logit exchange; row maxima and sums between exchanges
   uint32_t sink[kSoftWarps];                       // targets of CTA 1's signalling stores
-  uint32_t sink_f[2][kFixWarps];
+  uint32_t sink_f[kFixWarps];
   uint64_t st_full[kStages], st_empty[kStages], fixed[kStages], ready[kStages];
   uint64_t s_full, s_free, p_full[2];
   uint64_t q_tm[2], q_free[2], mma_done[2], sc_full[2], sc_empty[2], fin;
   uint32_t tmem_base;
   int abort, no_abort;
 };
+static_assert(offsetof(Smem, p) % 1024 == 0 && offsetof(Smem, spare) % 16 == 0 && offsetof(Smem, live) % 4 == 0 &&
+                  offsetof(Smem, valid) % 8 == 0 && offsetof(Smem, st_full) % 8 == 0 && kPBytes % 1024 == 0,
+              "vector accesses and operands");
 static_assert(sizeof(Smem) <= 232448, "shared memory budget");
 
 __device__ __forceinline__ float ex2(float x) {
@@ -215,6 +221,12 @@ __device__ __forceinline__ void ld_global32(const void* p, uint32_t* w) {
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                : "l"(p));
 }
+// lane = thread's TMEM lane, 4 consecutive 32-bit columns
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint4& v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
 // hint: bring `bytes` (a multiple of 16) from global memory into L2
 __device__ __forceinline__ void prefetch_l2_bulk(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
@@ -299,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&sm.s_free), kSoftWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm.p_full[i]), kSoftWarps);
-      mbar_init(smem_u32(&sm.q_tm[i]), kFixWarps);
+      mbar_init(smem_u32(&sm.q_tm[i]), kSoftWarps);
       mbar_init(smem_u32(&sm.q_free[i]), 1);
       mbar_init(smem_u32(&sm.mma_done[i]), 1);
       mbar_init(smem_u32(&sm.sc_full[i]), 1);
@@ -570,9 +582,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int k = G - kStages < 0 ? 0 : G - kStages; k < G; ++k)
       mbar_wait_warp(smem_u32(&sm.st_full[k % kStages]), (k / kStages) & 1, c, &sm.no_abort);
   } else if (warp >= kWarpFix0 && warp < kWarpSoft0) {
-    // ---------------------- query columns, key stages passed on ----------------------
+    // ------------------------- key stages passed on -------------------------
     const int fw = warp - kWarpFix0;
-    const bool wide_q = (reinterpret_cast<uintptr_t>(qg) & 31u) == 0;  // 32-byte loads (rows are 1152 bytes)
+    const int s0 = 32 * fw;                        // this warp's slots: [s0, s0 + 32) of the block
+    const uint32_t kAll = kBlk - s0 >= 32 ? 0xffffffffu : (1u << ((kBlk - s0) & 31)) - 1u;
     int G = 0;
     bool ok = true;
     for (int i = 0; ok; ++i) {
@@ -581,77 +594,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[i & 1]));
       if (g.end) break;
-      const long long rows = (long long)g.T * a.H - 128ll * g.tile;   // of the tile (more than 128: 128)
-      {
-        // thread = TMEM lane l of this warp's quadrant: row l & 63, column half l >> 6.
-        // The first 64 value columns are loaded before the wait for the old query.
-        const int l = (warp & 3) * 32 + lane, rr = kHC * (int)crank + (l & 63);
-        const bool live = rr < rows;
-        const __nv_bfloat16* qh =
-            qg + ((long long)g.t0 * a.H + 128ll * g.tile + (live ? rr : 0)) * (long long)kDQK;
-        const uint32_t lane_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const __nv_bfloat16 *vsrc = qh + 256 * (l >> 6), *rsrc = qh + kDV + 32 * (l >> 6);
-        uint32_t w0[32];
-        // A warp's load touches 32 rows, so 32 lines: the widest loads take the
-        // fewest turns of the load pipe, which the softmax's exchange shares.
-        auto fetch = [&](const __nv_bfloat16* src, uint32_t* w, int n) {
-#pragma unroll
-          for (int t = 0; t < n; ++t) {
-            if (!live) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) w[8 * t + e] = 0u;
-            } else if (wide_q) {
-              ld_global32(src + 16 * t, w + 8 * t);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + 16 * t) + e);
-                w[8 * t + 4 * e] = v.x, w[8 * t + 4 * e + 1] = v.y, w[8 * t + 4 * e + 2] = v.z, w[8 * t + 4 * e + 3] = v.w;
-              }
-            }
-          }
-        };
-        fetch(vsrc, w0, 4);
-        if (i > 0 && !mbar_wait_warp(smem_u32(&sm.q_free[(i - 1) & 1]), ((i - 1) >> 1) & 1, c, abort_flag)) break;
-        tc_fence_after();
-#pragma unroll 1
-        for (int p = 0; p < 4; ++p) {              // 64 value columns -> TMEM columns kColQ + 32p
-          tmem_st32(lane_tmem + kColQ + 32 * p, w0);
-          tmem_st_wait();
-          if (p < 3) fetch(vsrc + 64 * (p + 1), w0, 4);
-        }
-        uint32_t w3[16];
-        fetch(rsrc, w3, 2);
-        tmem_st16(lane_tmem + kColQ + 128, w3);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(&sm.q_tm[i & 1]);
-          if (crank == 0) {
-            if (fw == 0) mbar_arrive_expect_tx(bar, 4 * kFixWarps);
-            else mbar_arrive(bar);
-          } else {
-            st_async_signal(mapa_shared(smem_u32(&sm.sink_f[0][fw]), 0), mapa_shared(bar, 0));
-          }
-        }
-      }
       // the tokens of the tile
       const int ta = (int)(128ll * g.tile / a.H);
       const long long last = (128ll * g.tile + 127) / a.H;
       const int tb = last < g.T - 1 ? (int)last : g.T - 1;
       for (int j = g.j0; j < g.j1; ++j, ++G) {
         const int st = G % kStages;
-        // this warp's 28 slots: those that hold a row, those that any / every token of the tile sees
-        constexpr uint32_t kAll = (1u << kSlotsPerFix) - 1u;
-        const int s0 = kSlotsPerFix * fw;
+        // slots that any / every token of the tile sees
         uint32_t any = kAll, every = kAll;
         if (j >= g.nc) {
           const int first = (j - g.nc) * kBlk + s0;
           if (a.mask == nullptr) {
             const int na = ta - first + 1, nb = tb - first + 1;  // slots that the first / last token sees
-            every = na <= 0 ? 0u : na >= kSlotsPerFix ? kAll : (1u << na) - 1u;
-            any = nb <= 0 ? 0u : nb >= kSlotsPerFix ? kAll : (1u << nb) - 1u;
+            every = na <= 0 ? 0u : na >= 32 ? kAll : (1u << na) - 1u;
+            any = nb <= 0 ? 0u : nb >= 32 ? kAll : (1u << nb) - 1u;
           } else {
             const int w = first >> 6, sh = first & 63;
             uint32_t o = 0u, n = kAll;
@@ -670,14 +626,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        const unsigned long long v0 = sm.valid[st][0], v1 = sm.valid[st][1];
-        uint32_t valid;
-        {
-          const unsigned long long w = s0 >= 64 ? v1 >> (s0 - 64) : (s0 ? (v0 >> s0) | (v1 << (64 - s0)) : v0);
-          valid = (uint32_t)w & kAll;
-        }
-        uint32_t clear = kAll & ~(valid & any), bad = 0;
-        for (uint32_t mixed = valid & any & ~every; mixed; mixed &= mixed - 1) {
+        const uint32_t valid = (uint32_t)(sm.valid[st][fw >> 1] >> (32 * (fw & 1))) & kAll;
+        const uint32_t seen = valid & any;
+        uint32_t bad = 0;
+        for (uint32_t mixed = seen & ~every; mixed; mixed &= mixed - 1) {
           const int k = __ffs(mixed) - 1;
           const uint4* src =
               reinterpret_cast<const uint4*>(kvn + (long long)(g.t0 + (j - g.nc) * kBlk + s0 + k) * kDQK);
@@ -695,18 +647,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (__any_sync(0xffffffffu, inf)) bad |= 1u << k;
         }
-        clear |= bad;
-        if (lane == 0) sm.bad[st][fw] = bad;
+        const uint32_t live = ((seen & 0xffffu) ? 1u : 0u) | ((seen >> 16) ? 2u : 0u);
+        if (lane == 0) {
+          sm.bad[st][fw] = bad;
+          sm.live[st][fw] = (uint8_t)live;
+        }
+        // zero rows of the steps that run (step 0 always counts: a block without a
+        // seen slot may have to start O)
+        const uint32_t runs = ((live & 1u) || fw == 0 ? 0xffffu : 0u) | ((live & 2u) ? 0xffff0000u : 0u);
+        const uint32_t clear = (~seen | bad) & runs & kAll;
         if (clear) {
-          const uint32_t base = smem_u32(sm.stage[st]);
-          const uint32_t pv = base + (lane >> 3) * kAtom + (lane & 7) * 16, pr = base + kValue + (lane & 3) * 16;
+          const uint32_t pv = smem_u32(sm.stage[st]) + fw * 4 * kOct + (lane >> 3) * kAtom + (lane & 7) * 16;
 #pragma unroll
-          for (int k = 0; k < kSlotsPerFix; ++k) {
-            const int r = s0 + k;
-            if ((clear >> k) & 1u) {
-              st_zero16(pv + (r >> 3) * kOct + (r & 7) * 128);
-              if (lane < 4) st_zero16(pr + r * 64);
-            }
+          for (int o = 0; o < 4; ++o) {            // 8 rows x 512 bytes each
+            if (((clear >> (8 * o)) & 0xffu) == 0) continue;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if ((clear >> (8 * o + k)) & 1u) st_zero16(pv + o * kOct + k * 128);
           }
           fence_proxy_async_smem();                // these writes -> the tensor cores' reads
         }
@@ -718,7 +675,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (fw == 0) mbar_arrive_expect_tx(bar, 4 * kFixWarps);
             else mbar_arrive(bar);
           } else {
-            st_async_signal(mapa_shared(smem_u32(&sm.sink_f[1][fw]), 0), mapa_shared(bar, 0));
+            st_async_signal(mapa_shared(smem_u32(&sm.sink_f[fw]), 0), mapa_shared(bar, 0));
           }
         }
       }
@@ -767,13 +724,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t sb = smem_u32(sm.stage[0]) + sp * kStageBytes;
             const uint32_t v = desc_lo(sb, kAtom), p = desc_lo(smem_u32(sm.p[0]) + (Gp & 1) * kPBytes, 16);
+            // the 16-slot steps that some token sees (2 bits per byte); one at least
+            const uint32_t lv = *reinterpret_cast<const uint32_t*>(sm.live[sp]);
+            uint32_t steps = (lv & 3u) | ((lv >> 6) & 12u) | ((lv >> 12) & 48u) | ((lv >> 18) & 192u);
+            uint32_t acc = jp > 0;
+            if (steps == 0x7fu) {
 #pragma unroll
-            for (int kk = 0; kk < kPvSteps; ++kk) {
+              for (int kk = 0; kk < kPvSteps; ++kk) {
 #pragma unroll
-              for (int m = 0; m < 2; ++m)
-                mma2_ss(tmem + kColO + 128 * m, p + ((kk >> 2) * (kHC * 128) + (kk & 3) * 32) / 16,
-                        desc_hi(1024, kSw128), v + (2 * m * kAtom + kk * 2 * kOct) / 16, desc_hi(kOct, kSw128),
-                        kIdescPV, kk > 0 ? 1u : (uint32_t)(jp > 0));
+                for (int m = 0; m < 2; ++m)
+                  mma2_ss(tmem + kColO + 128 * m, p + ((kk >> 2) * (kHC * 128) + (kk & 3) * 32) / 16,
+                          desc_hi(1024, kSw128), v + (2 * m * kAtom + kk * 2 * kOct) / 16, desc_hi(kOct, kSw128),
+                          kIdescPV, kk > 0 ? 1u : acc);
+              }
+            } else {
+              if (steps == 0) steps = 1;
+#pragma unroll 1
+              for (; steps; steps &= steps - 1, acc = 1) {
+                const int kk = __ffs(steps) - 1;
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+                  mma2_ss(tmem + kColO + 128 * m, p + ((kk >> 2) * (kHC * 128) + (kk & 3) * 32) / 16,
+                          desc_hi(1024, kSw128), v + (2 * m * kAtom + kk * 2 * kOct) / 16, desc_hi(kOct, kSw128),
+                          kIdescPV, acc);
+              }
             }
             commit2(smem_u32(&sm.st_empty[0]) + 8 * sp);
             if (++sp == kStages) sp = 0;
@@ -838,16 +812,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto cut = [&](unsigned long long v0, unsigned long long v1) -> uint32_t {
       return (uint32_t)(s0 >= 64 ? v1 >> (s0 - 64) : (s0 ? (v0 >> s0) | (v1 << (64 - s0)) : v0));
     };
+    // A tile's query into TMEM: part ch of this lane's row and column half, 64
+    // value columns and 8 rope columns, before the epilogue of the tile ahead of
+    // it.  A warp's load touches 32 rows, so 32 lines: the widest loads take the
+    // fewest turns of the load pipe.
+    const bool wide_q = (reinterpret_cast<uintptr_t>(qg) & 31u) == 0;  // 32-byte loads (rows are 1152 bytes)
+    auto load_query = [&](int i) -> bool {
+      const Seg& n = sm.seg[i & 1];
+      const long long left = (long long)n.T * a.H - 128ll * n.tile;
+      const bool live = rr < left;
+      const __nv_bfloat16* qh =
+          qg + ((long long)n.t0 * a.H + 128ll * n.tile + (live ? rr : 0)) * (long long)kDQK;
+      const __nv_bfloat16* vsrc = qh + 256 * half + 64 * ch;
+      uint32_t w[32];
+      uint4 rope = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if (!live) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[8 * t + e] = 0u;
+        } else if (wide_q) {
+          ld_global32(vsrc + 16 * t, w + 8 * t);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(vsrc + 16 * t) + e);
+            w[8 * t + 4 * e] = v.x, w[8 * t + 4 * e + 1] = v.y, w[8 * t + 4 * e + 2] = v.z, w[8 * t + 4 * e + 3] = v.w;
+          }
+        }
+      }
+      if (live) rope = __ldg(reinterpret_cast<const uint4*>(qh + kDV + 32 * half + 8 * ch));
+      // the last logits of the tile ahead have read the old query
+      if (i > 0 && !mbar_wait_warp(smem_u32(&sm.q_free[(i - 1) & 1]), ((i - 1) >> 1) & 1, c, abort_flag)) return false;
+      tc_fence_after();
+      tmem_st32(tmem + lane_off + kColQ + 32 * ch, w);
+      tmem_st4(tmem + lane_off + kColQ + 128 + 4 * ch, rope);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      signal(&sm.q_tm[i & 1]);
+      return true;
+    };
     // Every warp executes the same sequence of named barriers whatever happens
     // (after a failed wait it goes on through the segment without work, and
     // the vote at the next one makes all of them stop).
     bool ok = true;
     const bool o_storer = warp == kWarpSoft0 && lane == 0;
     int G = 0;
+    ok = mbar_wait_warp(smem_u32(&sm.sc_full[0]), 0, c, abort_flag);
+    if (ok && !sm.seg[0].end) ok = load_query(0);
     for (int i = 0;; ++i) {
       const int bi = i & 1;
       if (o_storer) bulk_wait_read_all();          // the last tile's O has left the P buffers
-      if (ok) ok = mbar_wait_warp(smem_u32(&sm.sc_full[bi]), (i >> 1) & 1, c, abort_flag);
       if (named_bar_or(2, kSoftThreads, !ok)) break;
       const Seg g = sm.seg[bi];
       __syncwarp();
@@ -878,7 +894,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               vmask &= (uint32_t)m;
             }
             const unsigned long long b0 = sm.bad[st][0], b1 = sm.bad[st][1], b2 = sm.bad[st][2], b3 = sm.bad[st][3];
-            const uint32_t bad = cut(b0 | (b1 << 28) | (b2 << 56), (b2 >> 8) | (b3 << 20));
+            const uint32_t bad = cut(b0 | (b1 << 32), b2 | (b3 << 32));
             if (vmask & bad & keep_bits) poison = true;
           }
           vmask &= keep_bits;
@@ -1025,6 +1041,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         signal(&sm.p_full[pb]);
       }
       // ------------------------------- epilogue -------------------------------
+      if (ok) ok = mbar_wait_warp(smem_u32(&sm.sc_full[bi ^ 1]), ((i + 1) >> 1) & 1, c, abort_flag);
+      if (ok && !sm.seg[bi ^ 1].end) ok = load_query(i + 1);
       if (ok) ok = mbar_wait_warp(smem_u32(&sm.mma_done[bi]), (i >> 1) & 1, c, abort_flag);
       tc_fence_after();
       if (poison) l_run = NAN;
