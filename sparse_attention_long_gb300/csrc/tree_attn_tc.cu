@@ -103,20 +103,20 @@ struct __align__(1024) Smem {
   uint8_t stage[kStages][kStageBytes];             // value columns | rope columns
   uint8_t p[2][kPBytes];                           // P of even / odd blocks (and the exchange, and O)
   Seg seg[2];
-  unsigned long long valid[kStages][2];            // slots that hold a row
+  alignas(16) unsigned long long valid[kStages][2];            // slots that hold a row
   uint32_t bad[kStages][kFixWarps];                // 32 slots each: zeroed for an infinity or NaN
   alignas(4) uint8_t live[kStages][kFixWarps];                // 2 steps of 16 slots each: some token sees some slot
   alignas(16) uint8_t spare[kUnit];                // of the logit exchange; row maxima and sums between exchanges
   uint32_t sink[kSoftWarps];                       // targets of CTA 1's signalling stores
   uint32_t sink_f[kFixWarps];
-  uint64_t st_full[kStages], st_empty[kStages], fixed[kStages], ready[kStages];
+  uint64_t st_full[kStages], st_empty[kStages], ready[kStages];
   uint64_t s_full, s_free, p_full[2];
   uint64_t q_tm[2], q_free[2], mma_done[2], sc_full[2], sc_empty[2], fin;
   uint32_t tmem_base;
   int abort, no_abort;
 };
 static_assert(offsetof(Smem, p) % 1024 == 0 && offsetof(Smem, spare) % 16 == 0 && offsetof(Smem, live) % 4 == 0 &&
-                  offsetof(Smem, valid) % 8 == 0 && offsetof(Smem, st_full) % 8 == 0 && kPBytes % 1024 == 0,
+                  offsetof(Smem, valid) % 16 == 0 && offsetof(Smem, st_full) % 8 == 0 && kPBytes % 1024 == 0,
               "vector accesses and operands");
 static_assert(sizeof(Smem) <= 232448, "shared memory budget");
 
@@ -302,7 +302,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&sm.st_full[i]), kLoadWarps);
       mbar_init(smem_u32(&sm.st_empty[i]), 1);
-      mbar_init(smem_u32(&sm.fixed[i]), kFixWarps);
       mbar_init(smem_u32(&sm.ready[i]), kFixWarps);
     }
     mbar_init(smem_u32(&sm.s_full), 1);
@@ -669,7 +668,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(&sm.fixed[st]));
           const uint32_t bar = smem_u32(&sm.ready[st]);
           if (crank == 0) {
             if (fw == 0) mbar_arrive_expect_tx(bar, 4 * kFixWarps);
@@ -876,35 +874,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool poison = false;
       for (int j = g.j0; j < g.j1; ++j, ++G) {
         const int pb = G & 1, st = G % kStages;
-        if (ok) ok = mbar_wait_warp(smem_u32(&sm.fixed[st]), (G / kStages) & 1, c, abort_flag);
-        // visible slots of the kept range
-        uint32_t vmask = 0;
-        if (ok) {
-          vmask = cut(sm.valid[st][0], sm.valid[st][1]);
-          if (j >= g.nc) {
-            const int first = (j - g.nc) * kBlk + s0;
-            if (a.mask == nullptr) {
-              const int n = tok - first + 1;
-              vmask &= n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1u;
-            } else {
-              const unsigned long long* mrow = a.mask + (long long)(g.t0 + tok) * a.mask_words;
-              const int w = first >> 6, sh = first & 63;
-              unsigned long long m = w < a.mask_words ? __ldg(mrow + w) >> sh : 0ull;
-              if (sh && w + 1 < a.mask_words) m |= __ldg(mrow + w + 1) << (64 - sh);
-              vmask &= (uint32_t)m;
-            }
-            const unsigned long long b0 = sm.bad[st][0], b1 = sm.bad[st][1], b2 = sm.bad[st][2], b3 = sm.bad[st][3];
-            const uint32_t bad = cut(b0 | (b1 << 32), b2 | (b3 << 32));
-            if (vmask & bad & keep_bits) poison = true;
-          }
-          vmask &= keep_bits;
-        }
-        // the exchange below uses P buffer pb, last read by PV(G - 2), which is issued ahead of the logits of G
-        if (ok && G >= 2)
-          ok = mbar_wait_warp(smem_u32(&sm.st_empty[(G - 2) % kStages]), ((G - 2) / kStages) & 1, c, abort_flag);
+        // One wait: the logits' commit completes after every MMA issued before it,
+        // PV(G-2) among them, so P buffer pb is free as well; and the issuer took
+        // this block after the load and fix warps had passed it on, so valid and
+        // bad are there, too.
         if (ok) ok = mbar_wait_warp(smem_u32(&sm.s_full), G & 1, c, abort_flag);
-        // partial logits of row hl over this lane half's columns
         uint32_t lo[16], hi[16];                   // the part's slots 0..15 and 16..31 (ch odd: 16..23)
+        ulonglong2 vv = make_ulonglong2(0ull, 0ull);  // slots of the block that hold a row
 #pragma unroll
         for (int t = 0; t < 16; ++t) hi[t] = 0u;
         if (ok) {
@@ -912,6 +888,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t sbuf = tmem + lane_off + kColS + c0;
           tmem_ld16(sbuf, lo);
           tmem_ld16(sbuf + 16, hi);                // (ch odd: 8 columns of the next part or the query, unused)
+          vv = *reinterpret_cast<const ulonglong2*>(sm.valid[st]);
           tmem_ld_wait16(lo);
           tmem_ld_also16(hi);
           tc_fence_before();
@@ -954,6 +931,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int t = 0; t < 16; ++t) x[t] = __uint_as_float(hi[t]);
         }
+        // visible slots of the kept range
+        uint32_t vmask = cut(vv.x, vv.y) & keep_bits;
+        if (j >= g.nc) {
+          const int first = (j - g.nc) * kBlk + s0;
+          if (a.mask == nullptr) {
+            const int n = tok - first + 1;
+            vmask &= n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1u;
+          } else {
+            const unsigned long long* mrow = a.mask + (long long)(g.t0 + tok) * a.mask_words;
+            const int w = first >> 6, sh = first & 63;
+            unsigned long long m = w < a.mask_words ? __ldg(mrow + w) >> sh : 0ull;
+            if (sh && w + 1 < a.mask_words) m |= __ldg(mrow + w + 1) << (64 - sh);
+            vmask &= (uint32_t)m;
+          }
+          const unsigned long long b0 = sm.bad[st][0], b1 = sm.bad[st][1], b2 = sm.bad[st][2], b3 = sm.bad[st][3];
+          if (vmask & cut(b0 | (b1 << 32), b2 | (b3 << 32))) poison = true;
+        }
         named_bar_sync(1, kSoftThreads);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -965,12 +959,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             x[4 * q + 3] += pr.w;
           }
         }
-        float bm = -INFINITY;
+        if (vmask != keep_bits || kept != 16) {
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
-          if (((vmask >> t) & 1u) == 0) x[t] = -INFINITY;
-          bm = fmaxf(bm, x[t]);
+          for (int t = 0; t < 16; ++t)
+            if (((vmask >> t) & 1u) == 0) x[t] = -INFINITY;
         }
+        float bm = x[0], bn = x[1];
+#pragma unroll
+        for (int t = 2; t < 16; t += 2) {
+          bm = fmaxf(bm, x[t]);
+          bn = fmaxf(bn, x[t + 1]);
+        }
+        bm = fmaxf(bm, bn);
         bm *= sl2e;                                // log2 units (sl2e > 0)
         m_own = fmaxf(m_own, bm);
         // The maximum that P is taken against moves only when a logit exceeds it
@@ -982,13 +982,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         auto weights = [&]() {
           const float mu = (m_run == -INFINITY) ? 0.f : m_run;
           lsum_blk = 0.f;
+          float other = 0.f;
 #pragma unroll
           for (int t = 0; t < 8; ++t) {
             const float pa = ex2(fmaf(x[2 * t], sl2e, -mu));
             const float pc = ex2(fmaf(x[2 * t + 1], sl2e, -mu));
-            lsum_blk += pa + pc;                   // the sum takes P before its rounding
+            lsum_blk += pa;                        // the sum takes P before its rounding
+            other += pc;
             pk[t] = pack_bf16x2(pa, pc);           // bf16: the operand type of the PV product
           }
+          lsum_blk += other;
         };
         weights();
         // (this barrier also ends the reads of the exchange units)
