@@ -4,7 +4,8 @@
  * The path: Lightning Indexer scores -> per-query top-k -> sparse multi-query
  * attention (MLA weight-absorbed) over the selected kv rows, its backward, and
  * the indexer KL loss with its gradients.  For serving: a paged cache of kv
- * rows, its bookkeeping on the device, and attention of drafted tokens over it.
+ * rows, its bookkeeping on the device, attention of drafted tokens over it,
+ * and beam selection.
  *
  * Sources (pages):
  *  [DSA-32K] "CANN&TorchTitan: DeepSeek-V3.2 32k long-sequence pretraining on
@@ -464,6 +465,42 @@ int dsa_tree_attn_fwd(const dsa_cache *p, const dsa_tree *t, const void *q, cons
                       const int32_t *table, const int32_t *lens, const void *kv_new, const int32_t *tok_start,
                       const uint64_t *mask, void *out, float *softmax_max, float *softmax_sum, void *workspace,
                       dsa_stream_t stream);
+
+/*
+ * Beam selection (this library's own addition).  Per request, from the logits
+ * x of its beams' next tokens and the beams' scores, the beams_out best of
+ *   cand(w, v) = scores[w] + x[w, v] - log sum_u exp(x[w, u]),
+ * best first, ties to the lower w * vocab + v.  A finished beam has one
+ * candidate only: token eos at its unchanged score.  The parents reorder the
+ * beams' states through dsa_cache_fork.
+ *   logits [n_batch, beams_in, ld], vocab of each ld used; dtype
+ *   scores [n_batch, beams_in] fp32; -inf: the beam has no candidates (all but
+ *          the first beam of a request at its first step)
+ *   finished [n_batch, beams_in] uint8, or NULL: none is
+ *   parent, token [n_batch, beams_out] int32: the beam as row of the input
+ *          (request * beams_in + beam), the token; -1 where there are too few
+ *          candidates (score -inf)
+ *   scores_out [n_batch, beams_out] fp32; finished_out [n_batch, beams_out]
+ *          uint8 or NULL: parent finished, or token eos
+ * A logit of -inf, +inf or NaN is never chosen and counts nothing in the sum.
+ * Sums and scores are fp64 (terms fp32): the order of candidates is that of
+ * their scores as far as fp64 sums of fp32 exponentials tell them apart.
+ * beams_in, beams_out <= 32, vocab <= 2^24, eos in [-1, vocab) (-1: no such
+ * token; finished must be NULL then).  Outputs must not
+ * overlap inputs.
+ *   workspace: dsa_beam_workspace_size(p) bytes, 16-byte aligned; one call at
+ *   a time.
+ */
+typedef struct {
+  int32_t dtype; /* DSA_BF16 or DSA_FP32 */
+  int32_t reserved0;
+  int64_t n_batch, beams_in, beams_out, vocab, ld, eos;
+} dsa_beam;
+
+size_t dsa_beam_workspace_size(const dsa_beam *p);
+int dsa_beam_select(const dsa_beam *p, const void *logits, const float *scores, const uint8_t *finished,
+                    int32_t *parent, int32_t *token, float *scores_out, uint8_t *finished_out, void *workspace,
+                    dsa_stream_t stream);
 
 /*
  * Device status.  Synchronises `stream`, then writes the device status word

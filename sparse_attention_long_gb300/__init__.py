@@ -62,6 +62,12 @@ class dsa_tree(ctypes.Structure):
                 ("mask_words", ctypes.c_int64)]
 
 
+class dsa_beam(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("reserved0", ctypes.c_int32), ("n_batch", ctypes.c_int64),
+                ("beams_in", ctypes.c_int64), ("beams_out", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("eos", ctypes.c_int64)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
                       "(nvcc, sm_103a); there is no fallback implementation")
@@ -70,6 +76,7 @@ lib = ctypes.CDLL(LIB_PATH)
 _vp, _i64, _i32p = ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p
 _P = ctypes.POINTER(dsa_params)
 _C, _L, _T = ctypes.POINTER(dsa_cache), ctypes.POINTER(dsa_pool), ctypes.POINTER(dsa_tree)
+_B = ctypes.POINTER(dsa_beam)
 _sigs = {
     "dsa_version": ([], ctypes.c_int),
     "dsa_workspace_size": ([_P, ctypes.c_int], ctypes.c_size_t),
@@ -91,6 +98,8 @@ _sigs = {
     "dsa_cache_write": ([_C, _L, _vp, _i64, _i64, _vp, _vp, _i64, _vp], ctypes.c_int),
     "dsa_tree_workspace_size": ([_C, _T], ctypes.c_size_t),
     "dsa_tree_attn_fwd": ([_C, _T, _vp, _L] + [_vp] * 10, ctypes.c_int),
+    "dsa_beam_workspace_size": ([_B], ctypes.c_size_t),
+    "dsa_beam_select": ([_B] + [_vp] * 9, ctypes.c_int),
     "dsa_get_status": ([_vp, ctypes.POINTER(ctypes.c_int)], ctypes.c_int),
     "dsa_set_wait_budget_ns": ([ctypes.c_uint64], ctypes.c_int),
     "dsa_selftest_wait_timeout": ([ctypes.c_uint64, _vp], ctypes.c_int),
@@ -371,7 +380,7 @@ def tree_attn_fwd(c, t, q, pool, table, lens, kv_new, tok_start, mask, out, soft
         raise ValueError("dsa_tree_attn_fwd: pool must be [n_pages, page_rows, d_qk] of the call's type")
     rows = t.n_tok * t.H
     need = tree_workspace_size(c, t)
-    if workspace is not None and workspace.numel() * workspace.element_size() < need:
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         raise DSAError(DSA_ERR_WORKSPACE, "dsa_tree_attn_fwd")
     i32, f32 = torch.int32, torch.float32
     args = (a.ptr(q, "q", dt, rows * t.d_qk), ctypes.byref(pl), a.ptr(table, "table", i32, c.n_seqs * c.max_pages),
@@ -381,6 +390,33 @@ def tree_attn_fwd(c, t, q, pool, table, lens, kv_new, tok_start, mask, out, soft
             a.ptr(softmax_max, "softmax_max", f32, rows), a.ptr(softmax_sum, "softmax_sum", f32, rows),
             a.ptr(workspace, "workspace", workspace.dtype, workspace.numel()) if workspace is not None else None)
     a.call(lib.dsa_tree_attn_fwd, ctypes.byref(c), ctypes.byref(t), *args, stream=stream)
+
+
+# ------------------------------ beam selection ------------------------------
+def make_beam(*, n_batch, beams_in, beams_out, vocab, ld=None, dtype="bf16", eos=-1) -> dsa_beam:
+    """Sizes of beam_select; logits rows are ld >= vocab elements apart (vocab if None)."""
+    return dsa_beam({"bf16": DSA_BF16, "fp32": DSA_FP32}[dtype], 0, n_batch, beams_in, beams_out, vocab,
+                    vocab if ld is None else ld, eos)
+
+
+def beam_workspace_size(b) -> int:
+    return lib.dsa_beam_workspace_size(ctypes.byref(b))
+
+
+def beam_select(b, logits, scores, finished, parent, token, scores_out, finished_out, workspace, stream=None):
+    """The beams_out best continuations of each request: parent (row of the input, for
+    cache_fork), token, score, finished; finished / finished_out (uint8) may be None."""
+    a, i32, u8 = _Args("dsa_beam_select"), torch.int32, torch.uint8
+    rows, outs = b.n_batch * b.beams_in, b.n_batch * b.beams_out
+    args = (a.ptr(logits, "logits", torch.bfloat16 if b.dtype == DSA_BF16 else torch.float32, rows * b.ld),
+            a.ptr(scores, "scores", torch.float32, rows), a.ptr(finished, "finished", u8, rows, optional=True),
+            a.ptr(parent, "parent", i32, outs), a.ptr(token, "token", i32, outs),
+            a.ptr(scores_out, "scores_out", torch.float32, outs),
+            a.ptr(finished_out, "finished_out", u8, outs, optional=True),
+            a.ptr(workspace, "workspace", u8, workspace.numel()))
+    if workspace.numel() < beam_workspace_size(b):
+        raise DSAError(DSA_ERR_WORKSPACE, "dsa_beam_select")
+    a.call(lib.dsa_beam_select, ctypes.byref(b), *args, stream=stream)
 
 
 def get_status(stream=None) -> int:

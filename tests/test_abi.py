@@ -238,3 +238,19 @@ def test_tree_attention_host_validation_without_gpu():
     assert call(cache(), tree(), ws=None) == dsa.DSA_ERR_WORKSPACE
     assert dsa.tree_workspace_size(cache(), tree()) > 0
     assert dsa.tree_workspace_size(cache(page_rows=5), tree(dtype="fp32", d_qk=80, d_v=64)) == 0
+
+
+def test_beam_host_validation_without_gpu():
+    dsa = _lib()
+    assert ctypes.sizeof(dsa.dsa_beam) == 8 + 6 * 8
+    mk = lambda **kw: dsa.make_beam(**dict(dict(n_batch=1, beams_in=2, beams_out=2, vocab=8, dtype="fp32"), **kw))
+    A = [0x10000 * (i + 1) for i in range(8)]
+    call = lambda b, fin=None, logits=A[0], ws=A[7]: dsa.lib.dsa_beam_select(
+        ctypes.byref(b), logits, A[1], fin, A[3], A[4], A[5], A[6], ws, None)
+    I, U = dsa.DSA_ERR_INVALID_ARG, dsa.DSA_ERR_UNSUPPORTED
+    for b, code in ((mk(n_batch=0), I), (mk(beams_in=0), I), (mk(beams_out=0), I), (mk(vocab=0), I), (mk(ld=7), I),
+                    (mk(eos=8), I), (mk(eos=-2), I), (mk(beams_in=33), U), (mk(beams_out=33), U),
+                    (mk(vocab=(1 << 24) + 1), U), (mk(n_batch=1 << 31), U)):
+        assert call(b) == code and dsa.beam_workspace_size(b) == 0
+    assert call(mk(), fin=A[2]) == I and call(mk(), logits=None) == I and call(mk(), logits=A[0] + 2) == I
+    assert call(mk(), ws=None) == dsa.DSA_ERR_WORKSPACE and call(mk(), ws=A[7] + 8) == dsa.DSA_ERR_WORKSPACE
