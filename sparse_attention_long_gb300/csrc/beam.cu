@@ -5,11 +5,15 @@
 // Two kernels.  beam_part_kernel reads the logits once: one CTA per (beam row,
 // chunk of the vocabulary), the chunk in registers.  Within a beam the order of
 // the candidates is the order of the logits, so a chunk only has to give its
-// best beams_out logits, its maximum m and its sum of exp(x - m).  The k-th
-// largest of the threads' own maxima bounds the chunk's k-th largest logit from
-// below (each of those k threads has a logit at least that large), so few
-// logits pass it; those are ranked by counting.  Keys are (order-preserving
-// bits of the logit, inverted index): unique, so ties need no care.
+// best beams_out logits, its maximum m and its sum of exp(x - m).  With c =
+// ceil(beams_out / 8), the smallest of the 8 warps' c-th largest thread maxima
+// bounds the chunk's beams_out-th largest logit from below (8 c threads have a
+// logit at least that large); some 20 logits of 8192 pass it for 8 beams.
+// Those are ranked by counting, as keys (order-preserving bits of the logit,
+// inverted index), which are unique.  Should too many pass (equal logits), the
+// bound is taken again over keys, which lets at most 32 beams_out pass.
+// An infinity or NaN shows in the maximum or the sum; only then are the logits
+// looked at one by one.
 // beam_join_kernel (one CTA per request) adds the chunks' sums in 64 bits and
 // ranks the candidates by their 64-bit scores.
 //
@@ -29,7 +33,7 @@ bool ext_dev_ctx(DevCtx* c);
 
 namespace beam {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kVec = 8;                            // consecutive elements per thread and step
 constexpr int kSteps = 4;
 constexpr int kChunk = kThreads * kVec * kSteps;   // 8192 logits per CTA
@@ -51,127 +55,221 @@ struct Stat {
 __device__ __forceinline__ unsigned long long make_key(float x, uint32_t idx) {
   return ((unsigned long long)ordered_key(x) << 32) | (0xFFFFFFFFu - idx);
 }
-__device__ __forceinline__ float key_value(unsigned long long k) {
-  const uint32_t u = (uint32_t)(k >> 32);
+__device__ __forceinline__ float ordered_value(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
+}
+__device__ __forceinline__ float key_value(unsigned long long k) {
+  return ordered_value((uint32_t)(k >> 32));
 }
 __device__ __forceinline__ uint32_t key_index(unsigned long long k) { return 0xFFFFFFFFu - (uint32_t)k; }
 
-// logits that may not be chosen count as -inf: -inf itself, +inf and NaN
-__device__ __forceinline__ float clean(float x) { return x < INFINITY ? x : -INFINITY; }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// two floats in one register pair
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 
+// a thread's 32 logits in registers, four runs of eight
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool vec, int n, float* x);
+struct Logits;
 template <>
-__device__ __forceinline__ void load8<float>(const float* p, bool vec, int n, float* x) {
-  if (vec && n >= 8) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
+struct Logits<float> {
+  float x[kSteps][kVec];
+  __device__ __forceinline__ void load(int s, const float* p, bool vec, int n) {
+    if (vec && n >= kVec) {
+      const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+      x[s][0] = a.x, x[s][1] = a.y, x[s][2] = a.z, x[s][3] = a.w;
+      x[s][4] = b.x, x[s][5] = b.y, x[s][6] = b.z, x[s][7] = b.w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = i < n ? __ldcs(p + i) : -INFINITY;
-  }
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, bool vec, int n, float* x) {
-  if (vec && n >= 8) {
-    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      for (int i = 0; i < kVec; ++i) x[s][i] = i < n ? __ldcs(p + i) : -INFINITY;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x[i] = i < n ? __uint_as_float((uint32_t)__ldcs(reinterpret_cast<const unsigned short*>(p) + i) << 16) : -INFINITY;
   }
-}
+  __device__ __forceinline__ float get(int s, int e) const { return x[s][e]; }
+  __device__ __forceinline__ float max() const {
+    float m[4] = {x[0][0], x[1][0], x[2][0], x[3][0]};
+#pragma unroll
+    for (int e = 1; e < kVec; ++e)
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) m[s] = fmaxf(m[s], x[s][e]);
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+  }
+  // logits that may not be chosen count as -inf
+  __device__ __forceinline__ void clean() {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) x[s][e] = x[s][e] < INFINITY ? x[s][e] : -INFINITY;
+  }
+};
+template <>
+struct Logits<__nv_bfloat16> {
+  uint32_t w[kSteps][kVec / 2];                    // two each, the first in the low half
+  __device__ __forceinline__ void load(int s, const __nv_bfloat16* p, bool vec, int n) {
+    if (vec && n >= kVec) {
+      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+      w[s][0] = a.x, w[s][1] = a.y, w[s][2] = a.z, w[s][3] = a.w;
+    } else {
+      const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+#pragma unroll
+      for (int i = 0; i < kVec / 2; ++i) {
+        const uint32_t lo = 2 * i < n ? __ldcs(q + 2 * i) : 0xFF80u, hi = 2 * i + 1 < n ? __ldcs(q + 2 * i + 1) : 0xFF80u;
+        w[s][i] = lo | (hi << 16);
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int s, int e) const {
+    return __uint_as_float((e & 1) ? w[s][e >> 1] & 0xFFFF0000u : w[s][e >> 1] << 16);
+  }
+  __device__ __forceinline__ float max() const {
+    uint32_t m[2] = {w[0][0], w[0][1]};
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int i = 0; i < kVec / 2; ++i)
+        if (s > 0 || i > 1) asm("max.bf16x2 %0, %0, %1;" : "+r"(m[i & 1]) : "r"(w[s][i]));
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(m[0]) : "r"(m[1]));
+    return fmaxf(__uint_as_float(m[0] << 16), __uint_as_float(m[0] & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ void clean() {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int i = 0; i < kVec / 2; ++i) {
+        const float lo = __uint_as_float(w[s][i] << 16), hi = __uint_as_float(w[s][i] & 0xFFFF0000u);
+        w[s][i] = (lo < INFINITY ? w[s][i] & 0xFFFFu : 0xFF80u) | (hi < INFINITY ? w[s][i] & 0xFFFF0000u : 0xFF800000u);
+      }
+  }
+};
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     beam_part_kernel(Args a, const T* __restrict__ logits, const float* __restrict__ scores,
                      const uint8_t* __restrict__ finished, Stat* __restrict__ stats,
                      unsigned long long* __restrict__ keys, int vec) {
-  __shared__ unsigned long long tmax[kThreads], cand[kMaxCand], kth;
-  __shared__ float wmax[kThreads / 32];
-  __shared__ double wsum[kThreads / 32];
+  __shared__ unsigned long long cand[kMaxCand], tmax[kThreads], kth;
+  __shared__ uint32_t wleast[kWarps];
+  __shared__ float wmax[kWarps];
+  __shared__ double wsum[kWarps];
   __shared__ int n_cand;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.wout;
   const long long row = blockIdx.x / a.chunks;
   const int chunk = blockIdx.x % a.chunks;
   // a finished beam has no logits, a beam of score -inf no candidates
   if ((finished && finished[row]) || !(scores[row] > -INFINITY)) return;
   const T* base = logits + row * a.ld;
-  float x[kSteps][kVec];
-  float m = -INFINITY;
-  unsigned long long best = 0;
+  Logits<T> x;
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     const int i0 = chunk * kChunk + (s * kThreads + tid) * kVec;
-    load8<T>(base + i0, vec != 0, a.vocab - i0, x[s]);
+    x.load(s, base + i0, vec != 0, a.vocab - i0);
   }
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      x[s][e] = clean(x[s][e]);
-      m = fmaxf(m, x[s][e]);
-    }
-  // the thread's best key: its first element equal to its maximum
-  if (m > -INFINITY) {
-#pragma unroll
-    for (int s = kSteps - 1; s >= 0; --s)
-#pragma unroll
-      for (int e = kVec - 1; e >= 0; --e)
-        if (x[s][e] == m) best = make_key(m, chunk * kChunk + (s * kThreads + tid) * kVec + e);
-  }
-  tmax[tid] = best;
   if (tid == 0) n_cand = 0;
-  float wm = m;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-  if (lane == 0) wmax[warp] = wm;
-  __syncthreads();
-  float cm = wmax[0];
-#pragma unroll
-  for (int w = 1; w < kThreads / 32; ++w) cm = fmaxf(cm, wmax[w]);
-  // rank of this thread's best key among all threads'
-  const int k = a.wout;
-  int rank = 0;
-#pragma unroll 8
-  for (int t = 0; t < kThreads; ++t) rank += tmax[t] > best;
-  if (rank == k - 1 && best != 0) kth = best;
-  if (tid == 0 && cm == -INFINITY) kth = 0;
-  // sum of exp(x - max) over the chunk
-  double sum = 0.0;
-  if (cm > -INFINITY) {
+  float m, wm;
+  for (int pass = 0; pass < 2; ++pass) {
+    m = x.max();
+    // sum of exp(x - m) over the thread, four chains
     float part = 0.f;
+    if (m != -INFINITY) {
+      // x - m first: it is nearly exact where it counts, however large m is
+      const uint64_t minus = pack2(-m, -m), l2e = pack2(kLog2e, kLog2e);
+      uint64_t p[2] = {0ull, 0ull};
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int e = 0; e < kVec; e += 2) {
+          float lo, hi;
+          unpack2(mul2(add2(pack2(x.get(s, e), x.get(s, e + 1)), minus), l2e), lo, hi);
+          p[(e >> 1) & 1] = add2(p[(e >> 1) & 1], pack2(ex2(lo), ex2(hi)));
+        }
+      float lo, hi;
+      unpack2(add2(p[0], p[1]), lo, hi);
+      part = lo + hi;
+    }
+    // the warp's c-th largest thread maximum
+    uint32_t v = ordered_key(m), top = 0, first = 0;
+    for (int r = (k + kWarps - 1) / kWarps; r > 0; --r) {
+      top = __reduce_max_sync(0xffffffffu, v);
+      if (first == 0) first = top;
+      if (__ffs(__ballot_sync(0xffffffffu, v == top)) - 1 == lane) v = 0;
+    }
+    wm = ordered_value(first);
+    double sum = m == -INFINITY ? 0.0 : (double)(part * ex2((m - wm) * kLog2e));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      wleast[warp] = top;
+      wmax[warp] = wm;
+      wsum[warp] = sum;
+    }
+    // an infinity or NaN among the logits: once more without them
+    if (!__syncthreads_or(part != part || m == INFINITY || m != m) || pass == 1) break;
+    x.clean();
+  }
+  uint32_t least = wleast[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) least = least < wleast[w] ? least : wleast[w];
+  if (ordered_key(m) >= least && m != -INFINITY) {
+    const float bound = least == 0 ? -INFINITY : ordered_value(least);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) part += __expf(x[s][e] - cm);
-    sum = part;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) wsum[warp] = sum;
-  const int have = __syncthreads_count(best != 0);  // threads with a logit
-  const unsigned long long least = have < k ? 1ull : kth;
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      const unsigned long long key = make_key(x[s][e], chunk * kChunk + (s * kThreads + tid) * kVec + e);
-      if (x[s][e] > -INFINITY && key >= least) {
-        const int at = atomicAdd(&n_cand, 1);
-        if (at < kMaxCand) cand[at] = key;
+      for (int e = 0; e < kVec; ++e) {
+        const float y = x.get(s, e);
+        if (y >= bound && y != -INFINITY) {
+          const int at = atomicAdd(&n_cand, 1);
+          if (at < kMaxCand) cand[at] = make_key(y, chunk * kChunk + (s * kThreads + tid) * kVec + e);
+        }
       }
-    }
+  }
   __syncthreads();
+  int n = n_cand;
+  if (n > kMaxCand) {                              // many equal logits: bound by unique keys
+    unsigned long long best = 0;
+    if (m != -INFINITY) {
+#pragma unroll
+      for (int s = kSteps - 1; s >= 0; --s)
+#pragma unroll
+        for (int e = kVec - 1; e >= 0; --e)
+          if (x.get(s, e) == m) best = make_key(m, chunk * kChunk + (s * kThreads + tid) * kVec + e);
+    }
+    tmax[tid] = best;
+    const int have = __syncthreads_count(best != 0);  // threads with a logit
+    int rank = 0;
+    for (int t = 0; t < kThreads; ++t) rank += tmax[t] > best;
+    if (rank == k - 1 && best != 0) kth = best;
+    if (tid == 0) n_cand = 0;
+    __syncthreads();
+    const unsigned long long from = have < k ? 1ull : kth;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        const float y = x.get(s, e);
+        const unsigned long long key = make_key(y, chunk * kChunk + (s * kThreads + tid) * kVec + e);
+        if (y != -INFINITY && key >= from) cand[atomicAdd(&n_cand, 1)] = key;  // at most 32 k
+      }
+    __syncthreads();
+    n = n_cand;
+  }
   const long long out = row * a.chunks + chunk;
-  const int n = n_cand;                            // only k threads have a key >= kth: at most 32 k
   for (int i = tid; i < n; i += kThreads) {
     const unsigned long long mine = cand[i];
     int r = 0;
@@ -180,9 +278,13 @@ __global__ void __launch_bounds__(kThreads)
   }
   for (int i = n + tid; i < k; i += kThreads) keys[out * k + i] = 0;
   if (tid == 0) {
+    float cm = wmax[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) cm = fmaxf(cm, wmax[w]);
     double t = 0.0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) t += wsum[w];
+    for (int w = 0; w < kWarps; ++w)
+      if (wmax[w] != -INFINITY) t += wsum[w] * (double)ex2((wmax[w] - cm) * kLog2e);
     stats[out].sum = t;
     stats[out].max = cm;
   }
@@ -194,43 +296,22 @@ __device__ __forceinline__ unsigned long long ordered64(double x) {
   return (unsigned long long)u ^ ((unsigned long long)(u >> 63) | 0x8000000000000000ull);
 }
 
-// candidates of a request, sorted by repeated choice of the best: beams_out
-// rounds over a list in shared memory (64-bit score, flattened index)
+// One CTA per request, one warp per beam: its log-sum-exp, then the best
+// beams_out of its chunks' sorted lists (lane = chunk, the largest head of the
+// lanes taken each time), then the request's candidates ranked by counting.
 constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads)
     beam_join_kernel(Args a, const float* __restrict__ scores, const uint8_t* __restrict__ finished,
                      const Stat* __restrict__ stats, const unsigned long long* __restrict__ keys,
                      int32_t* __restrict__ parent, int32_t* __restrict__ token, float* __restrict__ scores_out,
                      uint8_t* __restrict__ finished_out) {
-  __shared__ double lse[kMaxBeams];
   __shared__ unsigned long long key_s[kMaxBeams * kMaxBeams];
   __shared__ uint32_t key_i[kMaxBeams * kMaxBeams];
   __shared__ int n_list;
-  const int b = blockIdx.x, tid = threadIdx.x, k = a.wout;
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, k = a.wout;
   if (tid == 0) n_list = 0;
-  for (int i = tid; i < k; i += kJoinThreads) {
-    parent[(long long)b * k + i] = -1;
-    token[(long long)b * k + i] = -1;
-    scores_out[(long long)b * k + i] = -INFINITY;
-    if (finished_out) finished_out[(long long)b * k + i] = 0;
-  }
-  // log-sum-exp of each beam, the chunks in order
-  for (int w = tid; w < a.win; w += kJoinThreads) {
-    const long long row = (long long)b * a.win + w;
-    const bool done = finished && finished[row];
-    if (done || !(scores[row] > -INFINITY)) continue;
-    const Stat* s = stats + row * a.chunks;
-    float m = -INFINITY;
-    for (int c = 0; c < a.chunks; ++c) m = fmaxf(m, s[c].max);
-    double t = 0.0;
-    for (int c = 0; c < a.chunks; ++c)
-      if (s[c].max > -INFINITY) t += s[c].sum * exp((double)s[c].max - (double)m);
-    lse[w] = m > -INFINITY ? (double)m + log(t) : 0.0;
-  }
   __syncthreads();
-  // one warp per beam: the best k of its chunks' sorted lists
   for (int w = tid >> 5; w < a.win; w += kJoinThreads / 32) {
-    const int lane = tid & 31;
     const long long row = (long long)b * a.win + w;
     const float sc = scores[row];
     if (finished && finished[row]) {
@@ -242,27 +323,57 @@ __global__ void __launch_bounds__(kJoinThreads)
       continue;
     }
     if (!(sc > -INFINITY)) continue;
+    const Stat* s = stats + row * a.chunks;
     const unsigned long long* kr = keys + row * a.chunks * k;
-    const int n = a.chunks * k;
-    unsigned long long last = ~0ull;
-    for (int r = 0; r < k; ++r) {                  // the largest key below the last one taken
-      unsigned long long best = 0;
-      for (int i = lane; i < n; i += 32) {
-        const unsigned long long v = kr[i];
-        if (v < last && v > best) best = v;
-      }
+    // heads of this lane's lists (chunk lane, lane + 32, ...): one list up to 32 chunks
+    const bool few = a.chunks <= 32;
+    int pos = 0;
+    unsigned long long head = 0, next = 0;
+    if (few && lane < a.chunks) {
+      head = kr[lane * k];
+      next = k > 1 ? kr[lane * k + 1] : 0;
+    }
+    float m = -INFINITY;
+    for (int c = lane; c < a.chunks; c += 32) m = fmaxf(m, s[c].max);
 #pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const unsigned long long v = __shfl_xor_sync(0xffffffffu, best, o);
-        best = v > best ? v : best;
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m == -INFINITY) continue;                  // no logit
+    double t = 0.0;
+    for (int c = lane; c < a.chunks; c += 32)
+      if (s[c].max != -INFINITY) t += s[c].sum * exp((double)s[c].max - (double)m);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    const double lse = (double)m + log(t);
+    // round r's winner is kept by lane r
+    unsigned long long mine = 0, last = ~0ull;
+    int got = 0;
+    for (; got < k; ++got) {
+      unsigned long long best = head;
+      if (!few) {                                  // the largest key below the last one taken
+        best = 0;
+        for (int i = lane; i < a.chunks * k; i += 32) {
+          const unsigned long long v = kr[i];
+          if (v < last && v > best) best = v;
+        }
       }
-      if (best == 0) break;
-      last = best;
-      if (lane == 0) {
-        const int at = atomicAdd(&n_list, 1);
-        key_s[at] = ordered64((double)sc + ((double)key_value(best) - lse[w]));
-        key_i[at] = (uint32_t)w * (uint32_t)a.vocab + key_index(best);
+      const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
+      const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+      const unsigned long long win = ((unsigned long long)hi << 32) | lo;
+      if (win == 0) break;
+      if (few && best == win) {                    // keys are unique: one lane
+        head = next;
+        ++pos;
+        next = pos + 1 < k ? kr[lane * k + pos + 1] : 0;
       }
+      last = win;
+      if (lane == got) mine = win;
+    }
+    int at = 0;
+    if (lane == 0) at = atomicAdd(&n_list, got);
+    at = __shfl_sync(0xffffffffu, at, 0);
+    if (lane < got) {
+      key_s[at + lane] = ordered64((double)sc + ((double)key_value(mine) - lse));
+      key_i[at + lane] = (uint32_t)w * (uint32_t)a.vocab + key_index(mine);
     }
   }
   __syncthreads();
@@ -280,6 +391,12 @@ __global__ void __launch_bounds__(kJoinThreads)
     token[o] = v;
     scores_out[o] = (float)__longlong_as_double((long long)u);
     if (finished_out) finished_out[o] = (finished && finished[row]) || v == a.eos;
+  }
+  for (int i = n + tid; i < k; i += kJoinThreads) {  // too few candidates
+    const long long o = (long long)b * k + i;
+    parent[o] = token[o] = -1;
+    scores_out[o] = -INFINITY;
+    if (finished_out) finished_out[o] = 0;
   }
 }
 
