@@ -8,18 +8,19 @@
 // best beams_out logits, its maximum m and its sum of exp(x - m).  With c =
 // ceil(beams_out / 8), the smallest of the 8 warps' c-th largest thread maxima
 // bounds the chunk's beams_out-th largest logit from below (8 c threads have a
-// logit at least that large); some 20 logits of 8192 pass it for 8 beams.
+// logit at least that large); some 20 logits of a chunk pass it for 8 beams.
 // Those are ranked by counting, as keys (order-preserving bits of the logit,
 // inverted index), which are unique.  Should too many pass (equal logits), the
-// bound is taken again over keys, which lets at most 32 beams_out pass.
+// bound is taken again over keys, which lets the logits of at most beams_out threads pass.
 // An infinity or NaN shows in the maximum or the sum; only then are the logits
 // looked at one by one.
 // beam_join_kernel (one CTA per request) adds the chunks' sums in 64 bits and
 // ranks the candidates by their 64-bit scores.
 //
 // Candidates of different beams can lie close together, and their order is an
-// output: the sums are fp32 only inside a thread and a chunk's total and
-// everything after it is fp64.  A row gives the same bits wherever it lies:
+// output: the sums are fp32 only inside a thread, a warp adds them as integers
+// (2^-40 of its largest term: the order does not matter), everything after that
+// is fp64.  A row gives the same bits wherever it lies:
 // which element a thread takes depends on its index alone, not on alignment.
 //
 // Bound: reading the logits (HBM) for a batch; the two launches for one request.
@@ -35,21 +36,24 @@ namespace beam {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kVec = 8;                            // consecutive elements per thread and step
-constexpr int kSteps = 4;
-constexpr int kChunk = kThreads * kVec * kSteps;   // 8192 logits per CTA
+// elements per thread and CTA: 16,384 (bf16) or 8,192 (fp32) logits, 32 registers
+constexpr int kStepsBf16 = 8, kStepsFp32 = 4;
+constexpr int kMaxPerThread = kStepsBf16 * kVec;
+constexpr int chunk_of(int dtype) { return kThreads * kVec * (dtype == DSA_BF16 ? kStepsBf16 : kStepsFp32); }
 constexpr int kMaxBeams = 32;                      // in and out
-constexpr int kMaxCand = 32 * kMaxBeams;           // candidates of a chunk at most, see beam_part_kernel
+constexpr int kMaxCand = kMaxPerThread * kMaxBeams;  // candidates of a chunk at most, see beam_part_kernel
 
 struct Args {
   int n_batch, win, wout, vocab, chunks;
   long long ld;
   int eos;
 };
-// per (row, chunk): maximum and sum, then wout keys
+// per (row, chunk, warp): maximum, and sum of exp(x - max) in units of 2^-40
 struct Stat {
-  double sum;
+  unsigned long long sum;
   float max, pad;
 };
+constexpr float kUnit = 1099511627776.f;           // 2^40
 
 // larger logit first, then lower index; 0: no logit
 __device__ __forceinline__ unsigned long long make_key(float x, uint32_t idx) {
@@ -79,37 +83,36 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 constexpr float kLog2e = 1.4426950408889634f;
 
-// a thread's 32 logits in registers, four runs of eight
+// a thread's logits in registers, in runs of eight
 template <typename T>
 struct Logits;
 template <>
 struct Logits<float> {
+  static constexpr int kSteps = kStepsFp32;
   float x[kSteps][kVec];
-  __device__ __forceinline__ void load(int s, const float* p, bool vec, int n) {
-    if (vec && n >= kVec) {
-      const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-      x[s][0] = a.x, x[s][1] = a.y, x[s][2] = a.z, x[s][3] = a.w;
-      x[s][4] = b.x, x[s][5] = b.y, x[s][6] = b.z, x[s][7] = b.w;
-    } else {
+  __device__ __forceinline__ void load16(int s, const float* p) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    x[s][0] = a.x, x[s][1] = a.y, x[s][2] = a.z, x[s][3] = a.w;
+    x[s][4] = b.x, x[s][5] = b.y, x[s][6] = b.z, x[s][7] = b.w;
+  }
+  __device__ __forceinline__ void load1(int s, const float* p, int n) {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) x[s][i] = i < n ? __ldcs(p + i) : -INFINITY;
-    }
+    for (int i = 0; i < kVec; ++i) x[s][i] = i < n ? __ldcs(p + i) : -INFINITY;
   }
   __device__ __forceinline__ float get(int s, int e) const { return x[s][e]; }
+  __device__ __forceinline__ float run_max(int s) const {
+    float m = x[s][0];
+#pragma unroll
+    for (int e = 1; e < kVec; ++e) m = fmaxf(m, x[s][e]);
+    return m;
+  }
   __device__ __forceinline__ float max() const {
-    float m[4] = {x[0][0], x[1][0], x[2][0], x[3][0]};
+    float m = run_max(0);
 #pragma unroll
-    for (int e = 1; e < kVec; ++e)
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) m[s] = fmaxf(m[s], x[s][e]);
-    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    for (int s = 1; s < kSteps; ++s) m = fmaxf(m, run_max(s));
+    return m;
   }
   // logits that may not be chosen count as -inf
   __device__ __forceinline__ void clean() {
@@ -121,32 +124,38 @@ struct Logits<float> {
 };
 template <>
 struct Logits<__nv_bfloat16> {
+  static constexpr int kSteps = kStepsBf16;
   uint32_t w[kSteps][kVec / 2];                    // two each, the first in the low half
-  __device__ __forceinline__ void load(int s, const __nv_bfloat16* p, bool vec, int n) {
-    if (vec && n >= kVec) {
-      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
-      w[s][0] = a.x, w[s][1] = a.y, w[s][2] = a.z, w[s][3] = a.w;
-    } else {
-      const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+  __device__ __forceinline__ void load16(int s, const __nv_bfloat16* p) {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+    w[s][0] = a.x, w[s][1] = a.y, w[s][2] = a.z, w[s][3] = a.w;
+  }
+  __device__ __forceinline__ void load1(int s, const __nv_bfloat16* p, int n) {
+    const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
 #pragma unroll
-      for (int i = 0; i < kVec / 2; ++i) {
-        const uint32_t lo = 2 * i < n ? __ldcs(q + 2 * i) : 0xFF80u, hi = 2 * i + 1 < n ? __ldcs(q + 2 * i + 1) : 0xFF80u;
-        w[s][i] = lo | (hi << 16);
-      }
+    for (int i = 0; i < kVec / 2; ++i) {
+      const uint32_t lo = 2 * i < n ? __ldcs(q + 2 * i) : 0xFF80u, hi = 2 * i + 1 < n ? __ldcs(q + 2 * i + 1) : 0xFF80u;
+      w[s][i] = lo | (hi << 16);
     }
   }
   __device__ __forceinline__ float get(int s, int e) const {
     return __uint_as_float((e & 1) ? w[s][e >> 1] & 0xFFFF0000u : w[s][e >> 1] << 16);
   }
+  __device__ __forceinline__ uint32_t run_max2(int s) const {
+    uint32_t t = w[s][0];
+#pragma unroll
+    for (int i = 1; i < kVec / 2; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(t) : "r"(w[s][i]));
+    return t;
+  }
+  static __device__ __forceinline__ float larger(uint32_t t) {
+    return fmaxf(__uint_as_float(t << 16), __uint_as_float(t & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ float run_max(int s) const { return larger(run_max2(s)); }
   __device__ __forceinline__ float max() const {
-    uint32_t m[2] = {w[0][0], w[0][1]};
+    uint32_t t = run_max2(0);
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-      for (int i = 0; i < kVec / 2; ++i)
-        if (s > 0 || i > 1) asm("max.bf16x2 %0, %0, %1;" : "+r"(m[i & 1]) : "r"(w[s][i]));
-    asm("max.bf16x2 %0, %0, %1;" : "+r"(m[0]) : "r"(m[1]));
-    return fmaxf(__uint_as_float(m[0] << 16), __uint_as_float(m[0] & 0xFFFF0000u));
+    for (int s = 1; s < kSteps; ++s) asm("max.bf16x2 %0, %0, %1;" : "+r"(t) : "r"(run_max2(s)));
+    return larger(t);
   }
   __device__ __forceinline__ void clean() {
 #pragma unroll
@@ -164,60 +173,76 @@ __global__ void __launch_bounds__(kThreads)
     beam_part_kernel(Args a, const T* __restrict__ logits, const float* __restrict__ scores,
                      const uint8_t* __restrict__ finished, Stat* __restrict__ stats,
                      unsigned long long* __restrict__ keys, int vec) {
+  constexpr int kSteps = Logits<T>::kSteps, kChunk = kThreads * kVec * kSteps;
   __shared__ unsigned long long cand[kMaxCand], tmax[kThreads], kth;
   __shared__ uint32_t wleast[kWarps];
-  __shared__ float wmax[kWarps];
-  __shared__ double wsum[kWarps];
   __shared__ int n_cand;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.wout;
-  const long long row = blockIdx.x / a.chunks;
-  const int chunk = blockIdx.x % a.chunks;
+  const uint32_t item = blockIdx.x, row = item / (uint32_t)a.chunks;
+  const int first = (int)(item - row * (uint32_t)a.chunks) * kChunk + tid * kVec;  // this thread's first logit
   // a finished beam has no logits, a beam of score -inf no candidates
   if ((finished && finished[row]) || !(scores[row] > -INFINITY)) return;
-  const T* base = logits + row * a.ld;
-  Logits<T> x;
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const int i0 = chunk * kChunk + (s * kThreads + tid) * kVec;
-    x.load(s, base + i0, vec != 0, a.vocab - i0);
-  }
   if (tid == 0) n_cand = 0;
-  float m, wm;
+  Logits<T> x;
+  {
+    const T* base = logits + (long long)row * a.ld + first;
+    if (vec && first + (kSteps - 1) * kThreads * kVec + kVec <= a.vocab) {
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) x.load16(s, base + s * kThreads * kVec);
+    } else {
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int left = a.vocab - first - s * kThreads * kVec;
+        if (vec && left >= kVec) x.load16(s, base + s * kThreads * kVec);
+        else x.load1(s, base + s * kThreads * kVec, left);
+      }
+    }
+  }
+  float m;
   for (int pass = 0; pass < 2; ++pass) {
     m = x.max();
-    // sum of exp(x - m) over the thread, four chains
+    // sum of exp(x - m) over the thread
     float part = 0.f;
-    if (m != -INFINITY) {
-      // x - m first: it is nearly exact where it counts, however large m is
-      const uint64_t minus = pack2(-m, -m), l2e = pack2(kLog2e, kLog2e);
+    if (fabsf(m) < 1e37f) {
+      // 2^(x log2e - mu) with mu = m log2e as rounded; its rounding error, which a
+      // fused product gives exactly, is taken out of the sum at the end
+      const float mu = m * kLog2e;
+      const uint64_t minus = pack2(-mu, -mu);
       uint64_t p[2] = {0ull, 0ull};
 #pragma unroll
       for (int s = 0; s < kSteps; ++s)
 #pragma unroll
         for (int e = 0; e < kVec; e += 2) {
           float lo, hi;
-          unpack2(mul2(add2(pack2(x.get(s, e), x.get(s, e + 1)), minus), l2e), lo, hi);
+          unpack2(ffma2(kLog2e, kLog2e, x.get(s, e), x.get(s, e + 1), minus), lo, hi);
           p[(e >> 1) & 1] = add2(p[(e >> 1) & 1], pack2(ex2(lo), ex2(hi)));
         }
       float lo, hi;
       unpack2(add2(p[0], p[1]), lo, hi);
-      part = lo + hi;
+      part = (lo + hi) * ex2(-fmaf(m, kLog2e, -mu));
+    } else if (m != -INFINITY) {                   // so large that the product overflows (or NaN)
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) part += ex2((x.get(s, e) - m) * kLog2e);
     }
     // the warp's c-th largest thread maximum
-    uint32_t v = ordered_key(m), top = 0, first = 0;
+    uint32_t v = ordered_key(m), top = 0, largest = 0;
     for (int r = (k + kWarps - 1) / kWarps; r > 0; --r) {
       top = __reduce_max_sync(0xffffffffu, v);
-      if (first == 0) first = top;
+      if (largest == 0) largest = top;
       if (__ffs(__ballot_sync(0xffffffffu, v == top)) - 1 == lane) v = 0;
     }
-    wm = ordered_value(first);
-    double sum = m == -INFINITY ? 0.0 : (double)(part * ex2((m - wm) * kLog2e));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float wm = ordered_value(largest);
+    // at most 64 terms of at most 1 per thread: below 2^50, two halves of 25 bits
+    const unsigned long long fix = m == -INFINITY ? 0ull : __float2ull_rn(part * ex2((m - wm) * kLog2e) * kUnit);
+    const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)fix & 0x1FFFFFFu);
+    const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(fix >> 25));
     if (lane == 0) {
       wleast[warp] = top;
-      wmax[warp] = wm;
-      wsum[warp] = sum;
+      Stat& o = stats[(size_t)item * kWarps + warp];
+      o.sum = ((unsigned long long)hi << 25) + lo;
+      o.max = wm;
     }
     // an infinity or NaN among the logits: once more without them
     if (!__syncthreads_or(part != part || m == INFINITY || m != m) || pass == 1) break;
@@ -226,17 +251,22 @@ __global__ void __launch_bounds__(kThreads)
   uint32_t least = wleast[0];
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) least = least < wleast[w] ? least : wleast[w];
-  if (ordered_key(m) >= least && m != -INFINITY) {
-    const float bound = least == 0 ? -INFINITY : ordered_value(least);
+  // (too few logits for a bound: every one passes)
+  const float from = least == 0 ? -3.402823466e38f : fmaxf(ordered_value(least), -3.402823466e38f);
+  if (m >= from) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
+      if (x.run_max(s) >= from) {
+        uint32_t hit = 0;
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        const float y = x.get(s, e);
-        if (y >= bound && y != -INFINITY) {
-          const int at = atomicAdd(&n_cand, 1);
-          if (at < kMaxCand) cand[at] = make_key(y, chunk * kChunk + (s * kThreads + tid) * kVec + e);
-        }
+        for (int e = 0; e < kVec; ++e) hit |= x.get(s, e) >= from ? 1u << e : 0u;
+        int at = atomicAdd(&n_cand, __popc(hit));
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+          if ((hit >> e) & 1u) {
+            if (at < kMaxCand) cand[at] = make_key(x.get(s, e), first + s * kThreads * kVec + e);
+            ++at;
+          }
       }
   }
   __syncthreads();
@@ -248,7 +278,7 @@ __global__ void __launch_bounds__(kThreads)
       for (int s = kSteps - 1; s >= 0; --s)
 #pragma unroll
         for (int e = kVec - 1; e >= 0; --e)
-          if (x.get(s, e) == m) best = make_key(m, chunk * kChunk + (s * kThreads + tid) * kVec + e);
+          if (x.get(s, e) == m) best = make_key(m, first + s * kThreads * kVec + e);
     }
     tmax[tid] = best;
     const int have = __syncthreads_count(best != 0);  // threads with a logit
@@ -257,43 +287,57 @@ __global__ void __launch_bounds__(kThreads)
     if (rank == k - 1 && best != 0) kth = best;
     if (tid == 0) n_cand = 0;
     __syncthreads();
-    const unsigned long long from = have < k ? 1ull : kth;
+    const unsigned long long lowest = have < k ? 1ull : kth;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
         const float y = x.get(s, e);
-        const unsigned long long key = make_key(y, chunk * kChunk + (s * kThreads + tid) * kVec + e);
-        if (y != -INFINITY && key >= from) cand[atomicAdd(&n_cand, 1)] = key;  // at most 32 k
+        const unsigned long long key = make_key(y, first + s * kThreads * kVec + e);
+        if (y != -INFINITY && key >= lowest) cand[atomicAdd(&n_cand, 1)] = key;  // only k threads have such keys
       }
     __syncthreads();
     n = n_cand;
   }
-  const long long out = row * a.chunks + chunk;
+  unsigned long long* out = keys + (size_t)item * k;
   for (int i = tid; i < n; i += kThreads) {
     const unsigned long long mine = cand[i];
     int r = 0;
     for (int j = 0; j < n && r < k; ++j) r += cand[j] > mine;
-    if (r < k) keys[out * k + r] = mine;
+    if (r < k) out[r] = mine;
   }
-  for (int i = n + tid; i < k; i += kThreads) keys[out * k + i] = 0;
-  if (tid == 0) {
-    float cm = wmax[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) cm = fmaxf(cm, wmax[w]);
-    double t = 0.0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      if (wmax[w] != -INFINITY) t += wsum[w] * (double)ex2((wmax[w] - cm) * kLog2e);
-    stats[out].sum = t;
-    stats[out].max = cm;
-  }
+  for (int i = n + tid; i < k; i += kThreads) out[i] = 0;
 }
 
 // order-preserving map of a double (no NaN)
 __device__ __forceinline__ unsigned long long ordered64(double x) {
   const long long u = __double_as_longlong(x + 0.0);
   return (unsigned long long)u ^ ((unsigned long long)(u >> 63) | 0x8000000000000000ull);
+}
+
+// ln(t 2^-unit) for t >= 2^(unit-1).  fp64 instructions are slow here (some 15
+// cycles of the SM each), so few of them: t = f 2^e with f in [0.707, 1.414],
+// ln f = 2 artanh s, s = (f - 1) / (f + 1), |s| < 0.172, by its power series up
+// to s^17 (the next term is below 2^-50 of the first).
+__device__ __forceinline__ double log_of(unsigned long long t, int unit) {
+  int e = 63 - __clzll((long long)t);
+  const unsigned long long frac = e > 52 ? t >> (e - 52) : t << (52 - e);  // 53 bits, the first one 1
+  double f = __longlong_as_double((long long)((frac & 0xFFFFFFFFFFFFFull) | 0x3FF0000000000000ull));
+  if (f > 1.4142135623730951) {
+    f *= 0.5;
+    ++e;
+  }
+  const double s = (f - 1.0) / (f + 1.0), z = s * s;
+  double p = 1.0 / 17.0;
+  p = fma(p, z, 1.0 / 15.0);
+  p = fma(p, z, 1.0 / 13.0);
+  p = fma(p, z, 1.0 / 11.0);
+  p = fma(p, z, 1.0 / 9.0);
+  p = fma(p, z, 1.0 / 7.0);
+  p = fma(p, z, 1.0 / 5.0);
+  p = fma(p, z, 1.0 / 3.0);
+  p = fma(p, z, 1.0);
+  return fma((double)(e - unit), 0.6931471805599453, 2.0 * s * p);
 }
 
 // One CTA per request, one warp per beam: its log-sum-exp, then the best
@@ -323,7 +367,8 @@ __global__ void __launch_bounds__(kJoinThreads)
       continue;
     }
     if (!(sc > -INFINITY)) continue;
-    const Stat* s = stats + row * a.chunks;
+    const Stat* s = stats + row * a.chunks * kWarps;
+    const int ns = a.chunks * kWarps;
     const unsigned long long* kr = keys + row * a.chunks * k;
     // heads of this lane's lists (chunk lane, lane + 32, ...): one list up to 32 chunks
     const bool few = a.chunks <= 32;
@@ -334,16 +379,17 @@ __global__ void __launch_bounds__(kJoinThreads)
       next = k > 1 ? kr[lane * k + 1] : 0;
     }
     float m = -INFINITY;
-    for (int c = lane; c < a.chunks; c += 32) m = fmaxf(m, s[c].max);
+    for (int c = lane; c < ns; c += 32) m = fmaxf(m, s[c].max);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (m == -INFINITY) continue;                  // no logit
-    double t = 0.0;
-    for (int c = lane; c < a.chunks; c += 32)
-      if (s[c].max != -INFINITY) t += s[c].sum * exp((double)s[c].max - (double)m);
+    // in units of 2^-38 of the row's largest term: below 2^62
+    unsigned long long t = 0;
+    for (int c = lane; c < ns; c += 32)
+      t += __float2ull_rn((float)s[c].sum * ex2((s[c].max - m) * kLog2e) * 0.25f);  // (a warp without a logit: 0 * 0)
 #pragma unroll
     for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    const double lse = (double)m + log(t);
+    const double lse = (double)m + log_of(t, 38);
     // round r's winner is kept by lane r
     unsigned long long mine = 0, last = ~0ull;
     int got = 0;
@@ -407,18 +453,18 @@ static int check(const dsa_beam* p, Args* a) {
       p->eos >= p->vocab)
     return DSA_ERR_INVALID_ARG;
   if (p->beams_in > kMaxBeams || p->beams_out > kMaxBeams || p->vocab > (1 << 24) || p->ld > (1ll << 40) ||
-      p->n_batch * p->beams_in * ((p->vocab + kChunk - 1) / kChunk) >= (1ll << 31))
+      p->n_batch * p->beams_in * ((p->vocab + chunk_of(p->dtype) - 1) / chunk_of(p->dtype)) >= (1ll << 31))
     return DSA_ERR_UNSUPPORTED;
   a->n_batch = (int)p->n_batch;
   a->win = (int)p->beams_in;
   a->wout = (int)p->beams_out;
   a->vocab = (int)p->vocab;
-  a->chunks = (int)((p->vocab + kChunk - 1) / kChunk);
+  a->chunks = (int)((p->vocab + chunk_of(p->dtype) - 1) / chunk_of(p->dtype));
   a->ld = p->ld;
   a->eos = (int)p->eos;
   return DSA_OK;
 }
-static size_t stat_bytes(const Args& a) { return (size_t)a.n_batch * a.win * a.chunks * sizeof(Stat); }
+static size_t stat_bytes(const Args& a) { return (size_t)a.n_batch * a.win * a.chunks * kWarps * sizeof(Stat); }
 
 }  // namespace beam
 }  // namespace dsa
@@ -451,7 +497,8 @@ int dsa_beam_select(const dsa_beam* p, const void* logits, const float* scores, 
   unsigned long long* keys = (unsigned long long*)((uint8_t*)workspace + stat_bytes(a));
   cudaStream_t st = (cudaStream_t)stream;
   const int vec = (((uintptr_t)logits | (uintptr_t)(p->ld * esz)) & 15u) == 0;
-  const unsigned grid = (unsigned)(a.n_batch * a.win) * (unsigned)a.chunks;
+  const long long items = (long long)a.n_batch * a.win * a.chunks;
+  const unsigned grid = (unsigned)items;
   if (p->dtype == DSA_BF16)
     beam_part_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a, (const __nv_bfloat16*)logits, scores, finished, stats,
                                                                keys, vec);
