@@ -340,109 +340,125 @@ __device__ __forceinline__ double log_of(unsigned long long t, int unit) {
   return fma((double)(e - unit), 0.6931471805599453, 2.0 * s * p);
 }
 
-// One CTA per request, one warp per beam: its log-sum-exp, then the best
-// beams_out of its chunks' sorted lists (lane = chunk, the largest head of the
-// lanes taken each time), then the request's candidates ranked by counting.
+// One CTA per request.  One warp per beam adds its chunks' sums and merges their
+// sorted lists (lane = chunk, the largest head of the lanes taken each time);
+// then one warp merges the beams (lane = beam), whose lists are sorted by score,
+// too.  The fp64 part is one lane's per beam.
 constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads)
     beam_join_kernel(Args a, const float* __restrict__ scores, const uint8_t* __restrict__ finished,
                      const Stat* __restrict__ stats, const unsigned long long* __restrict__ keys,
                      int32_t* __restrict__ parent, int32_t* __restrict__ token, float* __restrict__ scores_out,
                      uint8_t* __restrict__ finished_out) {
-  __shared__ unsigned long long key_s[kMaxBeams * kMaxBeams];
-  __shared__ uint32_t key_i[kMaxBeams * kMaxBeams];
-  __shared__ int n_list;
+  __shared__ unsigned long long list[kMaxBeams][kMaxBeams + 1], total[kMaxBeams];  // best first; 0: no more
+  __shared__ float top[kMaxBeams];
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, k = a.wout;
-  if (tid == 0) n_list = 0;
-  __syncthreads();
   for (int w = tid >> 5; w < a.win; w += kJoinThreads / 32) {
     const long long row = (long long)b * a.win + w;
     const float sc = scores[row];
-    if (finished && finished[row]) {
-      if (lane == 0 && sc > -INFINITY) {
-        const int at = atomicAdd(&n_list, 1);
-        key_s[at] = ordered64((double)sc);
-        key_i[at] = (uint32_t)w * (uint32_t)a.vocab + (uint32_t)a.eos;
-      }
-      continue;
-    }
-    if (!(sc > -INFINITY)) continue;
-    const Stat* s = stats + row * a.chunks * kWarps;
-    const int ns = a.chunks * kWarps;
-    const unsigned long long* kr = keys + row * a.chunks * k;
-    // heads of this lane's lists (chunk lane, lane + 32, ...): one list up to 32 chunks
-    const bool few = a.chunks <= 32;
-    int pos = 0;
-    unsigned long long head = 0, next = 0;
-    if (few && lane < a.chunks) {
-      head = kr[lane * k];
-      next = k > 1 ? kr[lane * k + 1] : 0;
-    }
-    float m = -INFINITY;
-    for (int c = lane; c < ns; c += 32) m = fmaxf(m, s[c].max);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (m == -INFINITY) continue;                  // no logit
-    // in units of 2^-38 of the row's largest term: below 2^62
-    unsigned long long t = 0;
-    for (int c = lane; c < ns; c += 32)
-      t += __float2ull_rn((float)s[c].sum * ex2((s[c].max - m) * kLog2e) * 0.25f);  // (a warp without a logit: 0 * 0)
-#pragma unroll
-    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    const double lse = (double)m + log_of(t, 38);
-    // round r's winner is kept by lane r
-    unsigned long long mine = 0, last = ~0ull;
+    const bool done = finished && finished[row];
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what follows reads the first kernel's results
     int got = 0;
-    for (; got < k; ++got) {
-      unsigned long long best = head;
-      if (!few) {                                  // the largest key below the last one taken
-        best = 0;
-        for (int i = lane; i < a.chunks * k; i += 32) {
-          const unsigned long long v = kr[i];
-          if (v < last && v > best) best = v;
+    if (!done && sc > -INFINITY) {
+      const Stat* s = stats + row * a.chunks * kWarps;
+      const int ns = a.chunks * kWarps;
+      const unsigned long long* kr = keys + row * a.chunks * k;
+      // heads of this lane's lists (chunk lane, lane + 32, ...): one list up to 32 chunks
+      const bool few = a.chunks <= 32;
+      int pos = 0;
+      unsigned long long head = 0, next = 0;
+      if (few && lane < a.chunks) {
+        head = kr[lane * k];
+        next = k > 1 ? kr[lane * k + 1] : 0;
+      }
+      float m = -INFINITY;
+      for (int c = lane; c < ns; c += 32) m = fmaxf(m, s[c].max);
+      const uint32_t most = __reduce_max_sync(0xffffffffu, ordered_key(m));
+      m = ordered_value(most);
+      if (m != -INFINITY) {
+        // in units of 2^-38 of the row's largest term: below 2^62
+        unsigned long long t = 0;
+        for (int c = lane; c < ns; c += 32)
+          t += __float2ull_rn((float)s[c].sum * ex2((s[c].max - m) * kLog2e) * 0.25f);  // (no logit in a warp: 0 * 0)
+#pragma unroll
+        for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        if (lane == 0) {
+          total[w] = t;
+          top[w] = m;
+        }
+        unsigned long long last = ~0ull;
+        for (; got < k; ++got) {
+          unsigned long long best = head;
+          if (!few) {                              // the largest key below the last one taken
+            best = 0;
+            for (int i = lane; i < a.chunks * k; i += 32) {
+              const unsigned long long v = kr[i];
+              if (v < last && v > best) best = v;
+            }
+          }
+          const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
+          const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+          const unsigned long long win = ((unsigned long long)hi << 32) | lo;
+          if (win == 0) break;
+          if (few && best == win) {                // keys are unique: one lane
+            head = next;
+            ++pos;
+            next = pos + 1 < k ? kr[lane * k + pos + 1] : 0;
+          }
+          last = win;
+          if (lane == 0) list[w][got] = win;
         }
       }
-      const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
-      const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
-      const unsigned long long win = ((unsigned long long)hi << 32) | lo;
-      if (win == 0) break;
-      if (few && best == win) {                    // keys are unique: one lane
-        head = next;
-        ++pos;
-        next = pos + 1 < k ? kr[lane * k + pos + 1] : 0;
-      }
-      last = win;
-      if (lane == got) mine = win;
+    } else if (done && sc > -INFINITY) {
+      if (lane == 0) list[w][0] = ~0ull;           // the end token at the beam's score
+      got = 1;
     }
-    int at = 0;
-    if (lane == 0) at = atomicAdd(&n_list, got);
-    at = __shfl_sync(0xffffffffu, at, 0);
-    if (lane < got) {
-      key_s[at + lane] = ordered64((double)sc + ((double)key_value(mine) - lse));
-      key_i[at + lane] = (uint32_t)w * (uint32_t)a.vocab + key_index(mine);
-    }
+    if (lane == 0) list[w][got] = 0;
   }
   __syncthreads();
-  const int n = n_list;
-  for (int i = tid; i < n; i += kJoinThreads) {
-    const unsigned long long s = key_s[i];
-    const uint32_t id = key_i[i];
-    int r = 0;
-    for (int j = 0; j < n && r < k; ++j) r += key_s[j] > s || (key_s[j] == s && key_i[j] < id);
-    if (r >= k) continue;
-    const int w = (int)(id / (uint32_t)a.vocab), v = (int)(id % (uint32_t)a.vocab);
-    const long long o = (long long)b * k + r, row = (long long)b * a.win + w;
-    const unsigned long long u = (s & 0x8000000000000000ull) ? s ^ 0x8000000000000000ull : ~s;
-    parent[o] = (int32_t)row;
-    token[o] = v;
-    scores_out[o] = (float)__longlong_as_double((long long)u);
-    if (finished_out) finished_out[o] = (finished && finished[row]) || v == a.eos;
-  }
-  for (int i = n + tid; i < k; i += kJoinThreads) {  // too few candidates
-    const long long o = (long long)b * k + i;
-    parent[o] = token[o] = -1;
-    scores_out[o] = -INFINITY;
-    if (finished_out) finished_out[o] = 0;
+  if (tid >= 32) return;
+  // lane = beam: its next candidate's score and flattened index
+  const long long row = (long long)b * a.win + lane;
+  const bool mine = lane < a.win;
+  const double sc = mine ? (double)scores[row] : 0.0;
+  const bool done = mine && finished && finished[row];
+  double lse = 0.0;
+  if (mine && !done && list[lane][0] != 0) lse = (double)top[lane] + log_of(total[lane], 38);
+  int pos = 0;
+  unsigned long long cs = 0;
+  uint32_t ci = 0xFFFFFFFFu;
+  auto take = [&]() {
+    const unsigned long long key = mine ? list[lane][pos] : 0;
+    cs = 0;
+    ci = 0xFFFFFFFFu;
+    if (key != 0) {
+      cs = ordered64(done ? sc : sc + ((double)key_value(key) - lse));
+      ci = (uint32_t)lane * (uint32_t)a.vocab + (done ? (uint32_t)a.eos : key_index(key));
+    }
+  };
+  take();
+  for (int r = 0; r < k; ++r) {
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(cs >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(cs >> 32) == hi ? (uint32_t)cs : 0u);
+    const unsigned long long best = ((unsigned long long)hi << 32) | lo;
+    const uint32_t id = __reduce_min_sync(0xffffffffu, cs == best ? ci : 0xFFFFFFFFu);
+    const long long o = (long long)b * k + r;
+    if (id == 0xFFFFFFFFu) {                       // too few candidates
+      if (lane == 0) {
+        parent[o] = token[o] = -1;
+        scores_out[o] = -INFINITY;
+        if (finished_out) finished_out[o] = 0;
+      }
+    } else if (ci == id) {
+      const int v = (int)(id - (uint32_t)lane * (uint32_t)a.vocab);
+      const unsigned long long u = (cs & 0x8000000000000000ull) ? cs ^ 0x8000000000000000ull : ~cs;
+      parent[o] = (int32_t)row;
+      token[o] = v;
+      scores_out[o] = (float)__longlong_as_double((long long)u);
+      if (finished_out) finished_out[o] = done || v == a.eos;
+      ++pos;
+      take();
+    }
   }
 }
 
@@ -505,9 +521,20 @@ int dsa_beam_select(const dsa_beam* p, const void* logits, const float* scores, 
   else
     beam_part_kernel<float><<<grid, kThreads, 0, st>>>(a, (const float*)logits, scores, finished, stats, keys, vec);
   if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
-  beam_join_kernel<<<a.n_batch, kJoinThreads, 0, st>>>(a, scores, finished, stats, keys, parent, token, scores_out,
-                                                       finished_out);
-  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  // the join may be set up while the first kernel ends
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.n_batch, 1, 1);
+  cfg.blockDim = dim3(kJoinThreads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, beam_join_kernel, a, scores, finished, (const Stat*)stats,
+                            (const unsigned long long*)keys, parent, token, scores_out, finished_out) == cudaSuccess
+             ? DSA_OK
+             : DSA_ERR_CUDA;
 }
 
 }  // extern "C"
