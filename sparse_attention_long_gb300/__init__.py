@@ -239,56 +239,85 @@ def forward_static_ws(p, q_I, k_I, w, q, kv, idx_out, out, softmax_max, softmax_
 
 
 # ------------------------------- paged cache -------------------------------
-class _Args:
-    """Checks the tensors of one call (type, size, one CUDA device) and makes
-    that device current while the call enqueues its work."""
+# These calls are made once or several times per generated token, so their
+# checks are kept to a few attribute reads per tensor; _refuse says what is wrong.
+def _refuse(where, name, t, dtype, numel, device, at_least=False):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{where}: {name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{where}: {name} is not a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{where}: {name} is on {t.device}, other tensors on cuda:{device}")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{where}: {name} is {t.dtype}, needs {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous")
+    if not (t.numel() >= numel if at_least else t.numel() == numel):
+        raise ValueError(f"{where}: {name} has {t.numel()} elements, needs {numel}")
 
-    def __init__(self, where):
-        self.where, self.device, self.guard = where, None, None
 
-    def _on(self, t, name):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{self.where}: {name} must be a torch.Tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{self.where}: {name} is not a CUDA tensor")
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            raise ValueError(f"{self.where}: {name} is on {t.device}, other tensors on {self.device}")
+def _device(t, where, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _refuse(where, name, t, None, 0, -1)
+    return t.get_device()
 
-    def ptr(self, t, name, dtypes, numel, optional=False, at_least=False):
-        if t is None and optional:
-            return None
-        self._on(t, name)
-        if t.dtype not in (dtypes if isinstance(dtypes, tuple) else (dtypes,)):
-            raise TypeError(f"{self.where}: {name} is {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{self.where}: {name} must be contiguous")
-        if t.numel() != numel and not (at_least and t.numel() >= numel):
-            raise ValueError(f"{self.where}: {name} has {t.numel()} elements, needs {numel}")
+
+def _arg(t, name, dtype, numel, device, where):
+    """Address of a contiguous CUDA tensor of this type and size on this device."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == numel and t.get_device() == device \
+            and t.is_contiguous():
         return t.data_ptr()
+    _refuse(where, name, t, dtype, numel, device)
 
-    def pool(self, cache, t):
-        """dsa_pool of a tensor [n_pages, page_rows, D] or [layers, n_pages, page_rows, D] whose
-        rows are contiguous within a page (layers and pages may have any stride)."""
-        self._on(t, "pool")
-        if t.dim() == 3:
-            t = t.unsqueeze(0)
-        if t.dim() != 4 or t.shape[1] != cache.n_pages or t.shape[2] != cache.page_rows:
-            raise ValueError(f"{self.where}: pool must be [(layers,) n_pages, page_rows, D]")
-        e, D = t.element_size(), t.shape[3]
-        if (D > 1 and t.stride(3) != 1) or (t.shape[2] > 1 and t.stride(2) != D):
-            raise ValueError(f"{self.where}: the rows of a pool's page must be contiguous")
-        page = cache.page_rows * D * e
-        return dsa_pool(t.data_ptr(), t.shape[0], t.stride(0) * e if t.shape[0] > 1 else page,
-                        t.stride(1) * e if t.shape[1] > 1 else page, D * e), t
 
-    def call(self, fn, *args, stream=None):
-        if self.device.index == torch.cuda.current_device():
-            _chk(fn(*args, _stream(stream)), self.where)
-        else:
-            with torch.cuda.device(self.device):
-                _chk(fn(*args, _stream(stream)), self.where)
+def _list(t, name, numel, device, where):
+    """The same for an int32 list that may be longer."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.numel() < numel or \
+            t.get_device() != device or not t.is_contiguous():
+        _refuse(where, name, t, torch.int32, numel, device, at_least=True)
+    return t.data_ptr()
+
+
+def _pool(c, t, where):
+    """(dsa_pool, layers, D) of a tensor [n_pages, page_rows, D] or [layers, n_pages, page_rows, D] whose
+    rows are contiguous within a page (layers and pages may have any stride)."""
+    sh, st = t.shape, t.stride()
+    if len(sh) == 3:
+        sh, st = (1, *sh), (0, *st)
+    if len(sh) != 4 or sh[1] != c.n_pages or sh[2] != c.page_rows:
+        raise ValueError(f"{where}: pool must be [(layers,) n_pages, page_rows, D]")
+    D = sh[3]
+    if (D > 1 and st[3] != 1) or (sh[2] > 1 and st[2] != D):
+        raise ValueError(f"{where}: the rows of a pool's page must be contiguous")
+    e = t.element_size()
+    page = sh[2] * D * e
+    return dsa_pool(t.data_ptr(), sh[0], st[0] * e if sh[0] > 1 else page, st[1] * e if sh[1] > 1 else page,
+                    D * e), sh[0], D
+
+
+def _workspace(t, need, device, where):
+    """Address of a workspace tensor of any type with at least `need` bytes (None if 0)."""
+    if t is None and need == 0:
+        return None
+    if t is None or t.numel() * t.element_size() < need:
+        raise DSAError(DSA_ERR_WORKSPACE, where)
+    if t.get_device() != device or not t.is_contiguous():
+        _refuse(where, "workspace", t, t.dtype, t.numel(), device)
+    return t.data_ptr()
+
+
+def _call(fn, where, device, stream, *args):
+    """fn(*args, stream) with `device` current."""
+    if device == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream(stream))
+    if rc != DSA_OK:
+        raise DSAError(rc, where)
+
+
+_I32 = torch.int32
 
 
 def make_cache(*, n_seqs, n_pages, page_rows, max_pages) -> dsa_cache:
@@ -300,62 +329,69 @@ def make_cache(*, n_seqs, n_pages, page_rows, max_pages) -> dsa_cache:
 def cache_fork(c, parent, table, lens, refs, table_out, lens_out, refs_out, copies, n_copies, stream=None):
     """Sequence i becomes a copy of old sequence parent[i] (-1: emptied); full pages are shared.
     Follow with cache_copy_pages(copies, n_copies) on every pool."""
-    a, i32, n = _Args("dsa_cache_fork"), torch.int32, c.n_seqs
-    args = (a.ptr(parent, "parent", i32, n), a.ptr(table, "table", i32, n * c.max_pages), a.ptr(lens, "lens", i32, n),
-            a.ptr(refs, "refs", i32, c.n_pages), a.ptr(table_out, "table_out", i32, n * c.max_pages),
-            a.ptr(lens_out, "lens_out", i32, n), a.ptr(refs_out, "refs_out", i32, c.n_pages),
-            a.ptr(copies, "copies", i32, 3 * n, at_least=True), a.ptr(n_copies, "n_copies", i32, 1))
-    a.call(lib.dsa_cache_fork, ctypes.byref(c), *args, stream=stream)
+    w = "dsa_cache_fork"
+    d, n, t, p = _device(parent, w, "parent"), c.n_seqs, c.n_seqs * c.max_pages, c.n_pages
+    _call(lib.dsa_cache_fork, w, d, stream, ctypes.byref(c), _arg(parent, "parent", _I32, n, d, w),
+          _arg(table, "table", _I32, t, d, w), _arg(lens, "lens", _I32, n, d, w), _arg(refs, "refs", _I32, p, d, w),
+          _arg(table_out, "table_out", _I32, t, d, w), _arg(lens_out, "lens_out", _I32, n, d, w),
+          _arg(refs_out, "refs_out", _I32, p, d, w), _list(copies, "copies", 3 * n, d, w),
+          _arg(n_copies, "n_copies", _I32, 1, d, w))
 
 
 def cache_extend(c, n_new, table, lens, refs, lens_out, refs_out, slots, stream=None):
     """Takes pages for n_new[i] further rows of each sequence (table in place; lens_out and
     refs_out may be lens and refs) and writes the slots of the new rows, -1 behind the last."""
-    a, i32, n = _Args("dsa_cache_extend"), torch.int32, c.n_seqs
-    args = (a.ptr(n_new, "n_new", i32, n), a.ptr(table, "table", i32, n * c.max_pages), a.ptr(lens, "lens", i32, n),
-            a.ptr(refs, "refs", i32, c.n_pages), a.ptr(lens_out, "lens_out", i32, n),
-            a.ptr(refs_out, "refs_out", i32, c.n_pages), a.ptr(slots, "slots", i32, slots.numel()), slots.numel())
-    a.call(lib.dsa_cache_extend, ctypes.byref(c), *args, stream=stream)
+    w = "dsa_cache_extend"
+    d, n, p = _device(n_new, w, "n_new"), c.n_seqs, c.n_pages
+    _call(lib.dsa_cache_extend, w, d, stream, ctypes.byref(c), _arg(n_new, "n_new", _I32, n, d, w),
+          _arg(table, "table", _I32, n * c.max_pages, d, w), _arg(lens, "lens", _I32, n, d, w),
+          _arg(refs, "refs", _I32, p, d, w), _arg(lens_out, "lens_out", _I32, n, d, w),
+          _arg(refs_out, "refs_out", _I32, p, d, w), _list(slots, "slots", 1, d, w), slots.numel())
 
 
 def cache_compact(c, table, lens, refs, table_out, refs_out, page_map, copies, n_copies, stream=None):
     """Moves the used pages to the lowest ids; page_map gives each its new id. Follow with
     cache_copy_pages(copies, n_copies) on every pool (copies: [n_pages // 2 + 1, 3])."""
-    a, i32, n = _Args("dsa_cache_compact"), torch.int32, c.n_seqs
-    args = (a.ptr(table, "table", i32, n * c.max_pages), a.ptr(lens, "lens", i32, n),
-            a.ptr(refs, "refs", i32, c.n_pages), a.ptr(table_out, "table_out", i32, n * c.max_pages),
-            a.ptr(refs_out, "refs_out", i32, c.n_pages), a.ptr(page_map, "page_map", i32, c.n_pages),
-            a.ptr(copies, "copies", i32, 3 * (c.n_pages // 2 + 1), at_least=True), a.ptr(n_copies, "n_copies", i32, 1))
-    a.call(lib.dsa_cache_compact, ctypes.byref(c), *args, stream=stream)
+    w = "dsa_cache_compact"
+    d, n, t, p = _device(table, w, "table"), c.n_seqs, c.n_seqs * c.max_pages, c.n_pages
+    _call(lib.dsa_cache_compact, w, d, stream, ctypes.byref(c), _arg(table, "table", _I32, t, d, w),
+          _arg(lens, "lens", _I32, n, d, w), _arg(refs, "refs", _I32, p, d, w),
+          _arg(table_out, "table_out", _I32, t, d, w), _arg(refs_out, "refs_out", _I32, p, d, w),
+          _arg(page_map, "page_map", _I32, p, d, w), _list(copies, "copies", 3 * (p // 2 + 1), d, w),
+          _arg(n_copies, "n_copies", _I32, 1, d, w))
 
 
 def cache_copy_pages(c, pool, copies, n_copies, stream=None):
     """Carries out a copy list on a pool tensor [(layers,) n_pages, page_rows, D] of any type."""
-    a, i32 = _Args("dsa_cache_copy_pages"), torch.int32
-    pl, _ = a.pool(c, pool)
-    args = (a.ptr(copies, "copies", i32, copies.numel()), a.ptr(n_copies, "n_copies", i32, 1), copies.numel() // 3)
-    a.call(lib.dsa_cache_copy_pages, ctypes.byref(c), ctypes.byref(pl), *args, stream=stream)
+    w = "dsa_cache_copy_pages"
+    d = _device(pool, w, "pool")
+    pl, _, _ = _pool(c, pool, w)
+    _call(lib.dsa_cache_copy_pages, w, d, stream, ctypes.byref(c), ctypes.byref(pl), _list(copies, "copies", 3, d, w),
+          _arg(n_copies, "n_copies", _I32, 1, d, w), copies.numel() // 3)
 
 
 def cache_write(c, pool, rows, slots, row_index=None, stream=None):
     """rows [(layers,) n, D] (of the pool's type) to slots [n] of cache_extend; with row_index
     [len(slots)] the row written to slots[i] is rows[row_index[i]]."""
-    a, i32 = _Args("dsa_cache_write"), torch.int32
-    pl, pt = a.pool(c, pool)
-    a._on(rows, "rows")
-    if rows.dim() == 2:
-        rows = rows.unsqueeze(0)
-    if rows.dim() != 3 or rows.shape[0] != pt.shape[0] or rows.shape[2] != pt.shape[3] or rows.dtype != pool.dtype:
-        raise ValueError("dsa_cache_write: rows must be [(layers,) n, D] of the pool's type")
-    if (rows.shape[2] > 1 and rows.stride(2) != 1) or (rows.shape[1] > 1 and rows.stride(1) != rows.shape[2]):
-        raise ValueError("dsa_cache_write: the rows of a layer must be contiguous")
+    w = "dsa_cache_write"
+    d = _device(pool, w, "pool")
+    pl, layers, D = _pool(c, pool, w)
+    if _device(rows, w, "rows") != d:
+        raise ValueError(f"{w}: rows is on {rows.device}, other tensors on cuda:{d}")
+    sh, st = rows.shape, rows.stride()
+    if len(sh) == 2:
+        sh, st = (1, *sh), (0, *st)
+    if len(sh) != 3 or sh[0] != layers or sh[2] != D or rows.dtype is not pool.dtype:
+        raise ValueError(f"{w}: rows must be [(layers,) n, D] of the pool's type")
+    if (D > 1 and st[2] != 1) or (sh[1] > 1 and st[1] != D):
+        raise ValueError(f"{w}: the rows of a layer must be contiguous")
+    sp = _list(slots, "slots", 1, d, w)
     n = slots.numel()
-    if row_index is None and rows.shape[1] < n:
-        raise ValueError("dsa_cache_write: fewer rows than slots")
-    ls = rows.stride(0) * rows.element_size() if rows.shape[0] > 1 else 0
-    args = (rows.data_ptr(), rows.shape[1], ls, a.ptr(slots, "slots", i32, n),
-            a.ptr(row_index, "row_index", i32, n, optional=True), n)
-    a.call(lib.dsa_cache_write, ctypes.byref(c), ctypes.byref(pl), *args, stream=stream)
+    if row_index is None and sh[1] < n:
+        raise ValueError(f"{w}: fewer rows than slots")
+    _call(lib.dsa_cache_write, w, d, stream, ctypes.byref(c), ctypes.byref(pl), rows.data_ptr(), sh[1],
+          st[0] * rows.element_size() if layers > 1 else 0, sp,
+          None if row_index is None else _arg(row_index, "row_index", _I32, n, d, w), n)
 
 
 # ------------------- attention of drafted tokens over the cache -------------------
@@ -373,23 +409,23 @@ def tree_attn_fwd(c, t, q, pool, table, lens, kv_new, tok_start, mask, out, soft
     """Attention of each sequence's drafted tokens (rows tok_start[b] .. tok_start[b+1] of q and
     kv_new) over its cached rows and the drafted ones that mask [n_tok, mask_words] (int64 bits)
     names; mask None: token t sees drafted tokens 0 .. t."""
-    a = _Args("dsa_tree_attn_fwd")
-    dt = torch.bfloat16 if t.dtype == DSA_BF16 else torch.float32
-    pl, pt = a.pool(c, pool)
-    if pt.dtype != dt or pt.shape[0] != 1 or pt.shape[3] != t.d_qk:
-        raise ValueError("dsa_tree_attn_fwd: pool must be [n_pages, page_rows, d_qk] of the call's type")
-    rows = t.n_tok * t.H
-    need = tree_workspace_size(c, t)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        raise DSAError(DSA_ERR_WORKSPACE, "dsa_tree_attn_fwd")
-    i32, f32 = torch.int32, torch.float32
-    args = (a.ptr(q, "q", dt, rows * t.d_qk), ctypes.byref(pl), a.ptr(table, "table", i32, c.n_seqs * c.max_pages),
-            a.ptr(lens, "lens", i32, c.n_seqs), a.ptr(kv_new, "kv_new", dt, t.n_tok * t.d_qk),
-            a.ptr(tok_start, "tok_start", i32, c.n_seqs + 1),
-            a.ptr(mask, "mask", torch.int64, t.n_tok * t.mask_words, optional=True), a.ptr(out, "out", dt, rows * t.d_v),
-            a.ptr(softmax_max, "softmax_max", f32, rows), a.ptr(softmax_sum, "softmax_sum", f32, rows),
-            a.ptr(workspace, "workspace", workspace.dtype, workspace.numel()) if workspace is not None else None)
-    a.call(lib.dsa_tree_attn_fwd, ctypes.byref(c), ctypes.byref(t), *args, stream=stream)
+    w = "dsa_tree_attn_fwd"
+    dt, f32 = torch.bfloat16 if t.dtype == DSA_BF16 else torch.float32, torch.float32
+    d = _device(q, w, "q")
+    if _device(pool, w, "pool") != d:
+        raise ValueError(f"{w}: pool is on {pool.device}, other tensors on cuda:{d}")
+    pl, layers, D = _pool(c, pool, w)
+    if pool.dtype is not dt or layers != 1 or D != t.d_qk:
+        raise ValueError(f"{w}: pool must be [n_pages, page_rows, d_qk] of the call's type")
+    n, rows, n_tok = c.n_seqs, t.n_tok * t.H, t.n_tok
+    _call(lib.dsa_tree_attn_fwd, w, d, stream, ctypes.byref(c), ctypes.byref(t),
+          _arg(q, "q", dt, rows * D, d, w), ctypes.byref(pl), _arg(table, "table", _I32, n * c.max_pages, d, w),
+          _arg(lens, "lens", _I32, n, d, w), _arg(kv_new, "kv_new", dt, n_tok * D, d, w),
+          _arg(tok_start, "tok_start", _I32, n + 1, d, w),
+          None if mask is None else _arg(mask, "mask", torch.int64, n_tok * t.mask_words, d, w),
+          _arg(out, "out", dt, rows * t.d_v, d, w), _arg(softmax_max, "softmax_max", f32, rows, d, w),
+          _arg(softmax_sum, "softmax_sum", f32, rows, d, w),
+          _workspace(workspace, tree_workspace_size(c, t), d, w))
 
 
 # ------------------------------ beam selection ------------------------------
@@ -406,17 +442,16 @@ def beam_workspace_size(b) -> int:
 def beam_select(b, logits, scores, finished, parent, token, scores_out, finished_out, workspace, stream=None):
     """The beams_out best continuations of each request: parent (row of the input, for
     cache_fork), token, score, finished; finished / finished_out (uint8) may be None."""
-    a, i32, u8 = _Args("dsa_beam_select"), torch.int32, torch.uint8
-    rows, outs = b.n_batch * b.beams_in, b.n_batch * b.beams_out
-    args = (a.ptr(logits, "logits", torch.bfloat16 if b.dtype == DSA_BF16 else torch.float32, rows * b.ld),
-            a.ptr(scores, "scores", torch.float32, rows), a.ptr(finished, "finished", u8, rows, optional=True),
-            a.ptr(parent, "parent", i32, outs), a.ptr(token, "token", i32, outs),
-            a.ptr(scores_out, "scores_out", torch.float32, outs),
-            a.ptr(finished_out, "finished_out", u8, outs, optional=True),
-            a.ptr(workspace, "workspace", u8, workspace.numel()))
-    if workspace.numel() < beam_workspace_size(b):
-        raise DSAError(DSA_ERR_WORKSPACE, "dsa_beam_select")
-    a.call(lib.dsa_beam_select, ctypes.byref(b), *args, stream=stream)
+    w, u8, f32 = "dsa_beam_select", torch.uint8, torch.float32
+    d, rows, outs = _device(logits, w, "logits"), b.n_batch * b.beams_in, b.n_batch * b.beams_out
+    _call(lib.dsa_beam_select, w, d, stream, ctypes.byref(b),
+          _arg(logits, "logits", torch.bfloat16 if b.dtype == DSA_BF16 else f32, rows * b.ld, d, w),
+          _arg(scores, "scores", f32, rows, d, w),
+          None if finished is None else _arg(finished, "finished", u8, rows, d, w),
+          _arg(parent, "parent", _I32, outs, d, w), _arg(token, "token", _I32, outs, d, w),
+          _arg(scores_out, "scores_out", f32, outs, d, w),
+          None if finished_out is None else _arg(finished_out, "finished_out", u8, outs, d, w),
+          _workspace(workspace, beam_workspace_size(b), d, w))
 
 
 def get_status(stream=None) -> int:

@@ -90,7 +90,7 @@ template <typename T>
 struct Logits;
 template <>
 struct Logits<float> {
-  static constexpr int kSteps = kStepsFp32;
+  static constexpr int kSteps = kStepsFp32, kResident = 4;
   float x[kSteps][kVec];
   __device__ __forceinline__ void load16(int s, const float* p) {
     const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
@@ -124,7 +124,7 @@ struct Logits<float> {
 };
 template <>
 struct Logits<__nv_bfloat16> {
-  static constexpr int kSteps = kStepsBf16;
+  static constexpr int kSteps = kStepsBf16, kResident = 5;
   uint32_t w[kSteps][kVec / 2];                    // two each, the first in the low half
   __device__ __forceinline__ void load16(int s, const __nv_bfloat16* p) {
     const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
@@ -168,8 +168,23 @@ struct Logits<__nv_bfloat16> {
   }
 };
 
+// f(logit, index) for a thread's logits, read again (from L2): for the rare
+// paths, whose unrolled code would crowd the instruction cache
+template <typename T, typename F>
+__device__ __forceinline__ void reread(const T* row, int first, int vocab, F f) {
+#pragma unroll 1
+  for (int s = 0; s < Logits<T>::kSteps; ++s)
+#pragma unroll 1
+    for (int e = 0; e < kVec; ++e) {
+      const int i = first + s * kThreads * kVec + e;
+      if (i >= vocab) continue;
+      const float y = to_f32<T>(row[i]);
+      f(y < INFINITY ? y : -INFINITY, i);
+    }
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, Logits<T>::kResident)
     beam_part_kernel(Args a, const T* __restrict__ logits, const float* __restrict__ scores,
                      const uint8_t* __restrict__ finished, Stat* __restrict__ stats,
                      unsigned long long* __restrict__ keys, int vec) {
@@ -184,8 +199,9 @@ __global__ void __launch_bounds__(kThreads)
   if ((finished && finished[row]) || !(scores[row] > -INFINITY)) return;
   if (tid == 0) n_cand = 0;
   Logits<T> x;
+  const T* xrow = logits + (long long)row * a.ld;
   {
-    const T* base = logits + (long long)row * a.ld + first;
+    const T* base = xrow + first;
     if (vec && first + (kSteps - 1) * kThreads * kVec + kVec <= a.vocab) {
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) x.load16(s, base + s * kThreads * kVec);
@@ -208,23 +224,22 @@ __global__ void __launch_bounds__(kThreads)
       // fused product gives exactly, is taken out of the sum at the end
       const float mu = m * kLog2e;
       const uint64_t minus = pack2(-mu, -mu);
-      uint64_t p[2] = {0ull, 0ull};
+      uint64_t p[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
       for (int s = 0; s < kSteps; ++s)
 #pragma unroll
         for (int e = 0; e < kVec; e += 2) {
           float lo, hi;
           unpack2(ffma2(kLog2e, kLog2e, x.get(s, e), x.get(s, e + 1), minus), lo, hi);
-          p[(e >> 1) & 1] = add2(p[(e >> 1) & 1], pack2(ex2(lo), ex2(hi)));
+          p[e >> 1] = add2(p[e >> 1], pack2(ex2(lo), ex2(hi)));
         }
       float lo, hi;
-      unpack2(add2(p[0], p[1]), lo, hi);
+      unpack2(add2(add2(p[0], p[1]), add2(p[2], p[3])), lo, hi);
       part = (lo + hi) * ex2(-fmaf(m, kLog2e, -mu));
-    } else if (m != -INFINITY) {                   // so large that the product overflows (or NaN)
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) part += ex2((x.get(s, e) - m) * kLog2e);
+    } else if (m == INFINITY || m != m) {
+      part = m;                                    // the vote below sees it
+    } else if (m != -INFINITY) {                   // so large that the product overflows
+      reread(xrow, first, a.vocab, [&](float y, int) { part += ex2((y - m) * kLog2e); });
     }
     // the warp's c-th largest thread maximum
     uint32_t v = ordered_key(m), top = 0, largest = 0;
@@ -273,13 +288,9 @@ __global__ void __launch_bounds__(kThreads)
   int n = n_cand;
   if (n > kMaxCand) {                              // many equal logits: bound by unique keys
     unsigned long long best = 0;
-    if (m != -INFINITY) {
-#pragma unroll
-      for (int s = kSteps - 1; s >= 0; --s)
-#pragma unroll
-        for (int e = kVec - 1; e >= 0; --e)
-          if (x.get(s, e) == m) best = make_key(m, first + s * kThreads * kVec + e);
-    }
+    reread(xrow, first, a.vocab, [&](float y, int i) {
+      if (y == m && m != -INFINITY) best = best > make_key(y, i) ? best : make_key(y, i);
+    });
     tmax[tid] = best;
     const int have = __syncthreads_count(best != 0);  // threads with a logit
     int rank = 0;
@@ -288,14 +299,10 @@ __global__ void __launch_bounds__(kThreads)
     if (tid == 0) n_cand = 0;
     __syncthreads();
     const unsigned long long lowest = have < k ? 1ull : kth;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        const float y = x.get(s, e);
-        const unsigned long long key = make_key(y, first + s * kThreads * kVec + e);
-        if (y != -INFINITY && key >= lowest) cand[atomicAdd(&n_cand, 1)] = key;  // only k threads have such keys
-      }
+    reread(xrow, first, a.vocab, [&](float y, int i) {
+      const unsigned long long key = make_key(y, i);
+      if (y != -INFINITY && key >= lowest) cand[atomicAdd(&n_cand, 1)] = key;  // only k threads have such keys
+    });
     __syncthreads();
     n = n_cand;
   }
