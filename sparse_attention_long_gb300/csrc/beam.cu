@@ -195,6 +195,8 @@ __global__ void __launch_bounds__(kThreads, Logits<T>::kResident)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.wout;
   const uint32_t item = blockIdx.x, row = item / (uint32_t)a.chunks;
   const int first = (int)(item - row * (uint32_t)a.chunks) * kChunk + tid * kVec;  // this thread's first logit
+  let_next_launch();
+  wait_for_earlier();
   // a finished beam has no logits, a beam of score -inf no candidates
   if ((finished && finished[row]) || !(scores[row] > -INFINITY)) return;
   if (tid == 0) n_cand = 0;
@@ -360,11 +362,12 @@ __global__ void __launch_bounds__(kJoinThreads)
   __shared__ unsigned long long list[kMaxBeams][kMaxBeams + 1], total[kMaxBeams];  // best first; 0: no more
   __shared__ float top[kMaxBeams];
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, k = a.wout;
+  let_next_launch();
+  wait_for_earlier();
   for (int w = tid >> 5; w < a.win; w += kJoinThreads / 32) {
     const long long row = (long long)b * a.win + w;
     const float sc = scores[row];
     const bool done = finished && finished[row];
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // what follows reads the first kernel's results
     int got = 0;
     if (!done && sc > -INFINITY) {
       const Stat* s = stats + row * a.chunks * kWarps;
@@ -522,24 +525,16 @@ int dsa_beam_select(const dsa_beam* p, const void* logits, const float* scores, 
   const int vec = (((uintptr_t)logits | (uintptr_t)(p->ld * esz)) & 15u) == 0;
   const long long items = (long long)a.n_batch * a.win * a.chunks;
   const unsigned grid = (unsigned)items;
-  if (p->dtype == DSA_BF16)
-    beam_part_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a, (const __nv_bfloat16*)logits, scores, finished, stats,
-                                                               keys, vec);
-  else
-    beam_part_kernel<float><<<grid, kThreads, 0, st>>>(a, (const float*)logits, scores, finished, stats, keys, vec);
-  if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
-  // the join may be set up while the first kernel ends
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.n_batch, 1, 1);
-  cfg.blockDim = dim3(kJoinThreads, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, beam_join_kernel, a, scores, finished, (const Stat*)stats,
-                            (const unsigned long long*)keys, parent, token, scores_out, finished_out) == cudaSuccess
+  const bool ok =
+      p->dtype == DSA_BF16
+          ? launch_programmatic(beam_part_kernel<__nv_bfloat16>, dim3(grid), dim3(kThreads), 0, st, 1, a,
+                                (const __nv_bfloat16*)logits, scores, finished, stats, keys, vec)
+          : launch_programmatic(beam_part_kernel<float>, dim3(grid), dim3(kThreads), 0, st, 1, a, (const float*)logits,
+                                scores, finished, stats, keys, vec);
+  if (!ok) return DSA_ERR_CUDA;
+  return launch_programmatic(beam_join_kernel, dim3(a.n_batch), dim3(kJoinThreads), 0, st, 1, a, scores, finished,
+                             (const Stat*)stats, (const unsigned long long*)keys, parent, token, scores_out,
+                             finished_out)
              ? DSA_OK
              : DSA_ERR_CUDA;
 }

@@ -35,7 +35,6 @@ struct Dims {
 struct Shared {                       // what the other CTAs of the cluster read
   int count, bad;
   int warp[kWarps];                   // block scans
-  int total;
 };
 
 __device__ __forceinline__ uint32_t cluster_nctarank() {
@@ -61,21 +60,33 @@ __device__ __forceinline__ int block_scan(int v, Shared& s, int* total) {
   }
   if (lane == 31) s.warp[w] = x;
   __syncthreads();
-  if (w == 0) {
-    int t = s.warp[lane];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, t, d);
-      if (lane >= d) t += y;
-    }
-    s.warp[lane] = t;
-    if (lane == 31) s.total = t;
-  }
+  const int t = s.warp[lane];                      // every warp: the sums of all warps (kWarps = 32)
+  const int below = __reduce_add_sync(0xffffffffu, lane < w ? t : 0);
+  *total = __reduce_add_sync(0xffffffffu, t);
   __syncthreads();
-  const int r = x - v + (w ? s.warp[w - 1] : 0);
-  *total = s.total;
+  return x - v + below;
+}
+// the same for a flag
+__device__ __forceinline__ int block_rank(bool yes, Shared& s, int* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const uint32_t bits = __ballot_sync(0xffffffffu, yes);
+  if (lane == 0) s.warp[w] = __popc(bits);
   __syncthreads();
-  return r;
+  const int t = s.warp[lane];
+  const int below = __reduce_add_sync(0xffffffffu, lane < w ? t : 0);
+  *total = __reduce_add_sync(0xffffffffu, t);
+  __syncthreads();
+  return below + __popc(bits & ((1u << lane) - 1u));
+}
+// total of a thread's counts over the block
+__device__ __forceinline__ int block_sum(int v, Shared& s) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int x = __reduce_add_sync(0xffffffffu, v);
+  if (lane == 0) s.warp[w] = x;
+  __syncthreads();
+  const int t = __reduce_add_sync(0xffffffffu, s.warp[lane]);
+  __syncthreads();
+  return t;
 }
 
 // sums of this CTA's `count` over the lower ranks and over all; any CTA's `bad`
@@ -83,14 +94,19 @@ struct Totals {
   int before, all, bad;
 };
 __device__ __forceinline__ Totals gather_totals(const Shared& s, uint32_t rank, uint32_t n) {
-  Totals t = {0, 0, 0};
-  for (uint32_t r = 0; r < n; ++r) {
-    const int c = ld_peer(&s.count, r);
-    if (r < rank) t.before += c;
-    t.all += c;
-    t.bad |= ld_peer(&s.bad, r);
-  }
+  if (n == 1) return {0, s.count, s.bad};
+  const uint32_t lane = threadIdx.x & 31;
+  const int c = lane < n ? ld_peer(&s.count, lane) : 0, b = lane < n ? ld_peer(&s.bad, lane) : 0;
+  Totals t;
+  t.before = __reduce_add_sync(0xffffffffu, lane < rank ? c : 0);
+  t.all = __reduce_add_sync(0xffffffffu, c);
+  t.bad = __reduce_or_sync(0xffffffffu, (uint32_t)b);
   return t;
+}
+// all CTAs of the cluster, or the one
+__device__ __forceinline__ void sync_all(uint32_t n) {
+  if (n == 1) __syncthreads();
+  else cluster_sync_all();
 }
 
 // pages [lo, hi) of this CTA's slice
@@ -109,7 +125,7 @@ __device__ __forceinline__ void in_order(int lo, int hi, int first, int limit, S
     const int p = base + threadIdx.x;
     const bool yes = p < hi && pick(p);
     int n;
-    const int at = first + block_scan(yes ? 1 : 0, s, &n);
+    const int at = first + block_rank(yes, s, &n);
     if (yes && at < limit) f(at, p);
     first += n;
   }
@@ -118,9 +134,7 @@ template <typename P>
 __device__ __forceinline__ int count_if(int lo, int hi, Shared& s, P pick) {
   int n = 0;
   for (int p = lo + threadIdx.x; p < hi; p += kThreads) n += pick(p) ? 1 : 0;
-  int total;
-  block_scan(n, s, &total);
-  return total;
+  return block_sum(n, s);
 }
 
 // ---------------------------------- fork ----------------------------------
@@ -136,6 +150,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ int dyn[];
   int* first = dyn;                   // [n_seqs] lowest child of each parent
   int* needy = dyn + d.n_seqs;        // [n_seqs] sequences that need a page, ascending
+  int* par = dyn + 2 * d.n_seqs;      // [n_seqs] parent, lens
+  int* len = dyn + 3 * d.n_seqs;
+  let_next_launch();
+  wait_for_earlier();
   const uint32_t rank = cluster_ctarank(), nc = cluster_nctarank();
   const int n = d.n_seqs, R = d.R, tid = threadIdx.x;
   int lo, hi;
@@ -145,16 +163,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int p = lo + tid; p < hi; p += kThreads) refs_out[p] = refs[p];
   __syncthreads();
   for (int i = tid; i < n; i += kThreads) {
-    const int p = parent[i], len = lens[i];
-    if (p < -1 || p >= n || len < 0 || len > (long long)d.max_pages * R) s.bad = 1;
+    const int p = parent[i], l = lens[i];
+    par[i] = p;
+    len[i] = l;
+    if (p < -1 || p >= n || l < 0 || l > (long long)d.max_pages * R) s.bad = 1;
     else if (p >= 0) atomicMin(&first[p], i);
   }
   __syncthreads();
   const bool bad_rows = s.bad != 0;   // the same in every CTA
-  cluster_sync_all();                 // refs_out initialised
+  sync_all(nc);                 // refs_out initialised
   auto need_page = [&](int i) {
-    const int p = parent[i];
-    return p >= 0 && first[p] != i && lens[p] % R != 0;
+    const int p = par[i];
+    return p >= 0 && first[p] != i && len[p] % R != 0;
   };
   if (!bad_rows) {
     // 256 table entries per warp step; uses that do not change are not counted
@@ -162,8 +182,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long items = (long long)n * nch;
     for (long long it = (long long)rank * kWarps + (tid >> 5); it < items; it += (long long)nc * kWarps) {
       const int i = (int)(it / nch), j0 = (int)(it % nch) * 256;
-      const int p = parent[i];
-      const int po = pages_of(lens[i], R), pn = p >= 0 ? pages_of(lens[p], R) : 0;
+      const int p = par[i];
+      const int po = pages_of(len[i], R), pn = p >= 0 ? pages_of(len[p], R) : 0;
       const int hole = need_page(i) ? pn - 1 : -1;
       int a[8], v[8];
 #pragma unroll
@@ -187,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (v[u] >= 0) atomicAdd(refs_out + v[u], 1);
         }
       }
-      if (j0 == 0 && lane == 0) lens_out[i] = p >= 0 ? lens[p] : 0;
+      if (j0 == 0 && lane == 0) lens_out[i] = p >= 0 ? len[p] : 0;
     }
   }
   // the sequences that need a page, in order
@@ -196,11 +216,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = base + tid;
     const bool yes = !bad_rows && i < n && need_page(i);
     int t;
-    const int at = block_scan(yes ? 1 : 0, s, &t);
+    const int at = block_rank(yes, s, &t);
     if (yes) needy[n_need + at] = i;
     n_need += t;
   }
-  cluster_sync_all();                 // every use counted
+  sync_all(nc);                 // every use counted
   {
     bool neg = false;
     const int free_pages = count_if(lo, hi, s, [&](int p) {
@@ -211,19 +231,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (neg) s.bad = 1;
     if (tid == 0) s.count = free_pages;
   }
-  cluster_sync_all();
+  sync_all(nc);
   const Totals t = gather_totals(s, rank, nc);
   const bool bad = t.bad != 0, fail = bad || n_need > t.all;
   if (!fail) {
     in_order(
         lo, hi, t.before, n_need, s, [&](int p) { return __ldcg(refs_out + p) == 0; },
         [&](int k, int page) {
-          const int i = needy[k], p = parent[i], last = pages_of(lens[p], R) - 1;
+          const int i = needy[k], p = par[i], last = pages_of(len[p], R) - 1;
           table_out[(long long)i * d.max_pages + last] = page;
           refs_out[page] = 1;
           copies[3 * k] = table[(long long)p * d.max_pages + last];
           copies[3 * k + 1] = page;
-          copies[3 * k + 2] = lens[p] % R;
+          copies[3 * k + 2] = len[p] % R;
         });
     if (rank == 0 && tid == 0) *n_copies = n_need;
   } else {
@@ -231,14 +251,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long e = (long long)n * d.max_pages;
     for (long long i = (long long)rank * kThreads + tid; i < e; i += (long long)nc * kThreads) table_out[i] = table[i];
     if (rank == 0) {
-      for (int i = tid; i < n; i += kThreads) lens_out[i] = lens[i];
+      for (int i = tid; i < n; i += kThreads) lens_out[i] = len[i];
       if (tid == 0) {
         *n_copies = 0;
         set_status(c, bad ? DSA_ERR_INDEX : DSA_ERR_PAGES);
       }
     }
   }
-  cluster_sync_all();                 // the others may still read this CTA's counts
+  sync_all(nc);                 // the others may still read this CTA's counts
 }
 
 // --------------------------------- extend ---------------------------------
@@ -250,6 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* len = dyn;                     // [n_seqs] rows before the call
   int* prow = dyn + d.n_seqs;         // [n_seqs + 1] exclusive prefix of the new rows
   int* ppage = prow + d.n_seqs + 1;   // [n_seqs + 1] exclusive prefix of the new pages
+  let_next_launch();
+  wait_for_earlier();
   const uint32_t rank = cluster_ctarank(), nc = cluster_nctarank();
   const int n = d.n_seqs, R = d.R, tid = threadIdx.x;
   int lo, hi;
@@ -305,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (neg) s.bad = 1;
     if (tid == 0) s.count = free_pages;
   }
-  cluster_sync_all();
+  sync_all(nc);
   const Totals t = gather_totals(s, rank, nc);
   const bool bad = t.bad != 0, fail = bad || pages > t.all;
   if (refs_out != refs) {
@@ -331,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           refs_out[page] = 1;
         });
   }
-  cluster_sync_all();                 // the table is complete; every CTA has its lens
+  sync_all(nc);                 // the table is complete; every CTA has its lens
   const int total = fail ? 0 : rows;
   for (int k = (int)rank * kThreads + tid; k < n_slots; k += (int)nc * kThreads) {
     int slot = -1;
@@ -356,6 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                    int32_t* __restrict__ page_map, int32_t* __restrict__ copies, int32_t* __restrict__ n_copies,
                    DevCtx c) {
   __shared__ Shared s;
+  let_next_launch();
+  wait_for_earlier();
   const uint32_t rank = cluster_ctarank(), nc = cluster_nctarank();
   const int n = d.n_seqs, R = d.R, tid = threadIdx.x, lane = tid & 31;
   int lo, hi;
@@ -392,21 +416,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (neg) s.bad = 1;
     if (tid == 0) s.count = live;
   }
-  cluster_sync_all();
+  sync_all(nc);
   Totals t = gather_totals(s, rank, nc);
   const int n_live = t.all;
   const bool bad = t.bad != 0;
-  cluster_sync_all();                 // counts read before they are replaced
+  sync_all(nc);                 // counts read before they are replaced
   // free ids below n_live: their number, and how many lie in lower slices
   const int mid = n_live < lo ? lo : (n_live > hi ? hi : n_live);  // slice = [lo, mid) low, [mid, hi) high
   const int holes_here = count_if(lo, mid, s, [&](int p) { return refs[p] == 0; });
   const int high_here = count_if(mid, hi, s, [&](int p) { return refs[p] > 0; });
   if (tid == 0) s.count = holes_here;
-  cluster_sync_all();
+  sync_all(nc);
   const Totals th = gather_totals(s, rank, nc);
-  cluster_sync_all();
+  sync_all(nc);
   if (tid == 0) s.count = high_here;
-  cluster_sync_all();
+  sync_all(nc);
   const Totals tm = gather_totals(s, rank, nc);
   const int H = bad ? 0 : th.all;
   if (!bad) {
@@ -418,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                copies[3 * k + 2] = R;
              });
   }
-  cluster_sync_all();                 // the list is complete
+  sync_all(nc);                 // the list is complete
   for (int p = lo + tid; p < hi; p += kThreads) {
     const int r = refs[p];
     // ids that move are filled in by their copy below
@@ -440,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *n_copies = H;
     if (bad) set_status(c, DSA_ERR_INDEX);
   }
-  cluster_sync_all();                 // the map is complete
+  sync_all(nc);                 // the map is complete
   entries([&](long long e, bool held) {
     table_out[e] = bad ? table[e] : (held ? __ldcg(page_map + table[e]) : -1);
   });
@@ -477,6 +501,8 @@ template <typename V>
 __global__ void __launch_bounds__(kCopyThreads)
     copy_pages_kernel(Dims d, Pool pool, const int32_t* __restrict__ copies, const int32_t* __restrict__ n_copies,
                       int max_copies, int pieces, long long piece_bytes, DevCtx c) {
+  let_next_launch();
+  wait_for_earlier();
   int n = *n_copies;
   if (n > max_copies) n = max_copies;
   const long long per = (long long)pool.n_layers * pieces, items = (long long)n * per;
@@ -500,6 +526,8 @@ template <typename V>
 __global__ void __launch_bounds__(kCopyThreads)
     write_rows_kernel(Dims d, Pool pool, const uint8_t* __restrict__ rows, long long rows_layer_stride, int n_src,
                       const int32_t* __restrict__ slots, const int32_t* __restrict__ row_index, int n_rows, DevCtx c) {
+  let_next_launch();
+  wait_for_earlier();
   const long long items = (long long)n_rows * pool.n_layers;
   const int lane = threadIdx.x & 31;
   for (long long it = blockIdx.x * (long long)(kCopyThreads / 32) + (threadIdx.x >> 5); it < items;
@@ -547,18 +575,7 @@ static int launch_cluster(void (*kernel)(A...), int ctas, size_t smem, cudaStrea
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return DSA_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ctas;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, A(args)...) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  return launch_programmatic(kernel, dim3(ctas), dim3(kThreads), smem, st, ctas, args...) ? DSA_OK : DSA_ERR_CUDA;
 }
 
 static int check_pool(const dsa_cache* p, const dsa_pool* pool, Pool* o) {
@@ -616,7 +633,7 @@ int dsa_cache_fork(const dsa_cache* p, const int32_t* parent, const int32_t* tab
     return DSA_ERR_INVALID_ARG;
   DevCtx c;
   if (!ext_dev_ctx(&c)) return DSA_ERR_CUDA;
-  return launch_cluster(fork_kernel, cluster_size(d), 2 * ns, (cudaStream_t)stream, d, parent, table, lens, refs,
+  return launch_cluster(fork_kernel, cluster_size(d), 4 * ns, (cudaStream_t)stream, d, parent, table, lens, refs,
                         table_out, lens_out, refs_out, copies, n_copies, c);
 }
 
@@ -678,8 +695,10 @@ int dsa_cache_copy_pages(const dsa_cache* p, const dsa_pool* pool, const int32_t
   const long long most = max_copies * pieces * o.n_layers;
   const int grid = (int)(most < 8ll * sms ? most : 8ll * sms);
   auto kernel = vb == 16 ? copy_pages_kernel<uint4> : vb == 4 ? copy_pages_kernel<uint32_t> : copy_pages_kernel<uint8_t>;
-  kernel<<<grid, kCopyThreads, 0, (cudaStream_t)stream>>>(d, o, copies, n_copies, (int)max_copies, (int)pieces, piece, c);
-  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  return launch_programmatic(kernel, dim3(grid), dim3(kCopyThreads), 0, (cudaStream_t)stream, 1, d, o, copies, n_copies,
+                             (int)max_copies, (int)pieces, piece, c)
+             ? DSA_OK
+             : DSA_ERR_CUDA;
 }
 
 int dsa_cache_write(const dsa_cache* p, const dsa_pool* pool, const void* rows, int64_t n_src,
@@ -703,9 +722,10 @@ int dsa_cache_write(const dsa_cache* p, const dsa_pool* pool, const void* rows, 
   const long long most = (n_rows * o.n_layers + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
   const int grid = (int)(most < 8ll * sms ? most : 8ll * sms);
   auto kernel = vb == 16 ? write_rows_kernel<uint4> : vb == 4 ? write_rows_kernel<uint32_t> : write_rows_kernel<uint8_t>;
-  kernel<<<grid, kCopyThreads, 0, (cudaStream_t)stream>>>(d, o, (const uint8_t*)rows, rows_layer_stride, (int)n_src,
-                                                          slots, row_index, (int)n_rows, c);
-  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  return launch_programmatic(kernel, dim3(grid), dim3(kCopyThreads), 0, (cudaStream_t)stream, 1, d, o,
+                             (const uint8_t*)rows, rows_layer_stride, (int)n_src, slots, row_index, (int)n_rows, c)
+             ? DSA_OK
+             : DSA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -331,6 +331,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync_all();  // both CTAs' barriers initialised before any remote arrive
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
+  let_next_launch();
+  wait_for_earlier();
 
   if (warp == kWarpScan) {
     // ------------------------------- schedule -------------------------------
@@ -1151,12 +1153,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // Joins the parts of the tiles that several pairs worked on:
 //   M = max m_k, w_k = 2^(m_k - M), l = sum w_k l_k, out = sum w_k O_k / l,
 // the parts in ascending key order.  grid (pairs, 16): 32 of the 512 columns.
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kJoinSplit = 16;
 __global__ void __launch_bounds__(kJoinThreads)
     tree_join_kernel(const float4* __restrict__ parts, const float4* __restrict__ stats,
                      const Join* __restrict__ joins, __nv_bfloat16* __restrict__ out, float* __restrict__ mx,
                      float* __restrict__ sm_out) {
   const int pair = blockIdx.x;
+  let_next_launch();
+  wait_for_earlier();
   const Join jn = joins[pair];
   if (jn.nparts == 0) return;
   const int row = threadIdx.x & 127, q0 = 8 * blockIdx.y + 4 * (threadIdx.x >> 7);
@@ -1272,12 +1276,15 @@ int launch_tree_attn_tc(const TreeArgs& a, const void* q, const void* pool, long
       !make_tmap_bf16(&nr, kv_new, 2, nr_dim, nr_str, nr_box, 64) ||
       !make_tmap_bf16(&po, out, 2, po_dim, po_str, po_box, 128))
     return DSA_ERR_CUDA;
-  tree_attn_tc_kernel<<<2 * pairs, kThreads, smem, st>>>(a, (const __nv_bfloat16*)q, (const __nv_bfloat16*)kv_new,
-                                                         (__nv_bfloat16*)out, mx, sm, parts, stats, joins, c,
-                                                         wide, pv, pv2, pr, pr2, nv, nr, po);
-  if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
-  tree_join_kernel<<<dim3(pairs, 16), kJoinThreads, 0, st>>>(parts, stats, joins, (__nv_bfloat16*)out, mx, sm);
-  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  if (!launch_programmatic(tree_attn_tc_kernel, dim3(2 * pairs), dim3(kThreads), smem, st, 1, a, (const __nv_bfloat16*)q,
+                           (const __nv_bfloat16*)kv_new, (__nv_bfloat16*)out, mx, sm, parts, stats, joins, c, wide, pv,
+                           pv2, pr, pr2, nv, nr, po))
+    return DSA_ERR_CUDA;
+  return launch_programmatic(tree_join_kernel, dim3(pairs, kJoinSplit), dim3(kJoinThreads), 0, st, 1,
+                             (const float4*)parts, (const float4*)stats, (const Join*)joins, (__nv_bfloat16*)out, mx,
+                             sm)
+             ? DSA_OK
+             : DSA_ERR_CUDA;
 }
 
 }  // namespace dsa
