@@ -33,7 +33,7 @@ struct Dims {
 };
 
 struct Shared {                       // what the other CTAs of the cluster read
-  int count, bad;
+  int count, more, bad;
   int warp[kWarps];                   // block scans
 };
 
@@ -386,26 +386,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   slice(d.n_pages, rank, nc, &lo, &hi);
   if (tid == 0) s.bad = 0;
   __syncthreads();
-  // f(sequence, entry, held) over the table, 256 entries per warp step
+  // f(table offset of entry j0 of a sequence, j0, entries held) for every 256
+  // entries of the table, one warp each; lane l takes entries j0 + l + 32 u
   const int nch = (d.max_pages + 255) / 256;
   auto entries = [&](auto f) {
-    const long long items = (long long)n * nch;
-    for (long long it = (long long)rank * kWarps + (tid >> 5); it < items; it += (long long)nc * kWarps) {
-      const int i = (int)(it / nch), j0 = (int)(it % nch) * 256, len = lens[i];
+    const int items = n * nch;        // < 2^31 / 256 + n
+    for (int it = (int)rank * kWarps + (tid >> 5); it < items; it += (int)nc * kWarps) {
+      const int i = it / nch, j0 = (it - i * nch) * 256, len = lens[i];
       const bool ok = len >= 0 && len <= (long long)d.max_pages * R;
-      const int po = ok ? pages_of(len, R) : 0;
       if (!ok) s.bad = 1;
-#pragma unroll 8
-      for (int u = 0; u < 8; ++u) {
-        const int j = j0 + 32 * u + lane;
-        if (j < d.max_pages) f((long long)i * d.max_pages + j, j < po);
-      }
+      f((long long)i * d.max_pages + j0, j0, ok ? pages_of(len, R) : 0);
     }
   };
-  entries([&](long long e, bool held) {
-    if (!held) return;
-    const int p = table[e];
-    if (p < 0 || p >= d.n_pages || refs[p] <= 0) s.bad = 1;
+  entries([&](long long e, int j0, int held) {
+    int p[8], r[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) p[u] = j0 + 32 * u + lane < held ? table[e + 32 * u + lane] : -2;
+    bool wrong = false;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const bool in = p[u] >= 0 && p[u] < d.n_pages;
+      r[u] = in ? refs[p[u]] : (p[u] == -2 && j0 + 32 * u + lane >= held ? 1 : 0);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) wrong |= r[u] <= 0;
+    if (wrong) s.bad = 1;
   });
   {
     bool neg = false;
@@ -417,30 +422,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) s.count = live;
   }
   sync_all(nc);
-  Totals t = gather_totals(s, rank, nc);
-  const int n_live = t.all;
+  const Totals t = gather_totals(s, rank, nc);
+  const int n_live = t.all, live_here = s.count;
   const bool bad = t.bad != 0;
-  sync_all(nc);                 // counts read before they are replaced
-  // free ids below n_live: their number, and how many lie in lower slices
+  sync_all(nc);                       // counts read before they are replaced
+  // free ids below n_live and used ones above: here, in the lower slices, in all
   const int mid = n_live < lo ? lo : (n_live > hi ? hi : n_live);  // slice = [lo, mid) low, [mid, hi) high
-  const int holes_here = count_if(lo, mid, s, [&](int p) { return refs[p] == 0; });
-  const int high_here = count_if(mid, hi, s, [&](int p) { return refs[p] > 0; });
-  if (tid == 0) s.count = holes_here;
+  const int live_low = count_if(lo, mid, s, [&](int p) { return refs[p] > 0; });
+  if (tid == 0) {
+    s.count = (mid - lo) - live_low;
+    s.more = live_here - live_low;
+  }
   sync_all(nc);
-  const Totals th = gather_totals(s, rank, nc);
-  sync_all(nc);
-  if (tid == 0) s.count = high_here;
-  sync_all(nc);
-  const Totals tm = gather_totals(s, rank, nc);
-  const int H = bad ? 0 : th.all;
-  if (!bad) {
-    in_order(lo, mid, th.before, H, s, [&](int p) { return refs[p] == 0; },
-             [&](int k, int p) { copies[3 * k + 1] = p; });
-    in_order(mid, hi, tm.before, H, s, [&](int p) { return refs[p] > 0; },
-             [&](int k, int p) {
-               copies[3 * k] = p;
-               copies[3 * k + 2] = R;
-             });
+  int hole = 0, mover = 0, H = 0;     // ranks of this slice's first hole and mover; holes in all
+  if (nc == 1) {
+    H = s.count;
+  } else {
+    const uint32_t l = lane;
+    const int a = l < nc ? ld_peer(&s.count, l) : 0, b = l < nc ? ld_peer(&s.more, l) : 0;
+    hole = __reduce_add_sync(0xffffffffu, l < rank ? a : 0);
+    mover = __reduce_add_sync(0xffffffffu, l < rank ? b : 0);
+    H = __reduce_add_sync(0xffffffffu, a);
+  }
+  if (bad) H = 0;
+  for (int base = lo; base < hi && H > 0; base += kThreads) {
+    const int p = base + tid;
+    const bool used = p < hi && refs[p] > 0;
+    const bool is_hole = p < mid && !used, is_mover = p >= mid && used;
+    int n;
+    const int kh = hole + block_rank(is_hole, s, &n);
+    hole += n;
+    const int km = mover + block_rank(is_mover, s, &n);
+    mover += n;
+    if (is_hole) copies[3 * kh + 1] = p;
+    if (is_mover) {
+      copies[3 * km] = p;
+      copies[3 * km + 2] = R;
+    }
   }
   sync_all(nc);                 // the list is complete
   for (int p = lo + tid; p < hi; p += kThreads) {
@@ -465,8 +483,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (bad) set_status(c, DSA_ERR_INDEX);
   }
   sync_all(nc);                 // the map is complete
-  entries([&](long long e, bool held) {
-    table_out[e] = bad ? table[e] : (held ? __ldcg(page_map + table[e]) : -1);
+  entries([&](long long e, int j0, int held) {
+    int p[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int j = j0 + 32 * u + lane;
+      p[u] = j < (bad ? d.max_pages : held) ? table[e + 32 * u + lane] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (!bad && p[u] >= 0) p[u] = __ldcg(page_map + p[u]);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (j0 + 32 * u + lane < d.max_pages) table_out[e + 32 * u + lane] = p[u];
   });
 }
 
@@ -477,6 +506,35 @@ struct Pool {
   int n_layers;
 };
 
+// streamed once: past L1
+struct alignas(32) Wide {
+  uint32_t w[8];
+};
+template <typename V>
+__device__ __forceinline__ V ld_once(const V* p) {
+  return __ldcs(p);
+}
+template <>
+__device__ __forceinline__ Wide ld_once<Wide>(const Wide* p) {
+  Wide v;
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]),
+                 "=r"(v.w[7])
+               : "l"(p)
+               : "memory");
+  return v;
+}
+template <typename V>
+__device__ __forceinline__ void st_once(V* p, const V& v) {
+  __stcs(p, v);
+}
+template <>
+__device__ __forceinline__ void st_once<Wide>(Wide* p, const Wide& v) {
+  asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v.w[0]), "r"(v.w[1]),
+               "r"(v.w[2]), "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]), "r"(v.w[7])
+               : "memory");
+}
+
 template <typename V>
 __device__ __forceinline__ void copy_span(uint8_t* dst, const uint8_t* src, long long bytes, int t, int nt) {
   const long long nv = bytes / (long long)sizeof(V);
@@ -486,10 +544,10 @@ __device__ __forceinline__ void copy_span(uint8_t* dst, const uint8_t* src, long
     V x[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      if (i + (long long)u * nt < nv) x[u] = a[i + (long long)u * nt];
+      if (i + (long long)u * nt < nv) x[u] = ld_once<V>(a + i + (long long)u * nt);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      if (i + (long long)u * nt < nv) b[i + (long long)u * nt] = x[u];
+      if (i + (long long)u * nt < nv) st_once<V>(b + i + (long long)u * nt, x[u]);
   }
   for (long long j = nv * (long long)sizeof(V) + t; j < bytes; j += nt) dst[j] = src[j];
 }
@@ -688,13 +746,17 @@ int dsa_cache_copy_pages(const dsa_cache* p, const dsa_pool* pool, const int32_t
   const int sms = sm_count();
   if (sms <= 0) return DSA_ERR_CUDA;
   const long long page = (long long)d.R * o.row_bytes;
-  const int vb = vector_bytes((uintptr_t)o.base | (uintptr_t)o.page_stride | (uintptr_t)o.layer_stride);
+  const uintptr_t bits = (uintptr_t)o.base | (uintptr_t)o.page_stride | (uintptr_t)o.layer_stride;
+  const int vb = (bits & 31) == 0 ? 32 : vector_bytes(bits);
   const long long piece = 16384ll;    // a multiple of every vector width
   const long long pieces = (page + piece - 1) / piece;
   if (pieces * o.n_layers > (1ll << 30)) return DSA_ERR_UNSUPPORTED;
   const long long most = max_copies * pieces * o.n_layers;
   const int grid = (int)(most < 8ll * sms ? most : 8ll * sms);
-  auto kernel = vb == 16 ? copy_pages_kernel<uint4> : vb == 4 ? copy_pages_kernel<uint32_t> : copy_pages_kernel<uint8_t>;
+  auto kernel = vb == 32   ? copy_pages_kernel<Wide>
+                : vb == 16 ? copy_pages_kernel<uint4>
+                : vb == 4  ? copy_pages_kernel<uint32_t>
+                           : copy_pages_kernel<uint8_t>;
   return launch_programmatic(kernel, dim3(grid), dim3(kCopyThreads), 0, (cudaStream_t)stream, 1, d, o, copies, n_copies,
                              (int)max_copies, (int)pieces, piece, c)
              ? DSA_OK
