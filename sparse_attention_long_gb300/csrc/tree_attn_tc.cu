@@ -80,10 +80,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 static_assert(kColQ + 144 == kTmemCols, "TMEM columns");
 static_assert(kValue % 1024 == 0 && kRope % 512 == 0 && kStageBytes % 1024 == 0, "operand alignment");
 
-// A pair's run is at least this many blocks: a shorter one costs more in its
-// own start and in the join than the blocks that another pair takes over.
-constexpr int kMinRun = 4;
-
 // one part of one tile, as the schedule hands it to the other roles
 struct Seg {
   int b, tile, j0, j1, nc, len, t0, T;               // blocks [j0, j1) of the tile; nc = cached blocks
@@ -124,6 +120,32 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Partial results lie in L2 from a run's first tile to the join, while the keys
+// stream past: they are written with the wish to stay (32 of 40 MB were gone and
+// the join read them from HBM), and read for the last time without it.
+__device__ __forceinline__ uint64_t policy_stay() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t policy_go() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void st_part(float4* p, float a, float b, float c, float d, uint64_t policy) {
+  asm volatile("st.global.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(d),
+               "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ float4 ld_part(const float4* p, uint64_t policy) {
+  float4 v;
+  asm volatile("ld.global.L2::cache_hint.v4.f32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p), "l"(policy));
+  return v;
 }
 
 // ---- two-CTA tcgen05 forms ----
@@ -346,8 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     total = warp_sum(total);
     if (__any_sync(0xffffffffu, wrong) && lane == 0) set_status(c, DSA_ERR_INDEX);
-    long long run = (total + npairs - 1) / npairs;
-    if (run < kMinRun) run = kMinRun;
+    const long long run = (total + npairs - 1) / npairs;
     long long x = run * pair;
     const long long x1 = x + run < total ? x + run : total;
     int i = 0;                                     // segments so far
@@ -1069,6 +1090,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // part of a tile: O as it stands, [column quad][row] so that a warp's
         // 32 rows make whole lines
         float4* po = parts + (size_t)g.part * (kTile * kDV / 4) + rr;
+        const uint64_t stay = policy_stay();
 #pragma unroll 1
         for (int m = 0; m < 2; ++m) {
           uint32_t o[32];
@@ -1077,9 +1099,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int quad0 = (256 * half + 128 * m + 32 * ch) / 4;
 #pragma unroll
           for (int t = 0; t < 8; ++t)
-            po[(size_t)(quad0 + t) * kTile] =
-                make_float4(__uint_as_float(o[4 * t]), __uint_as_float(o[4 * t + 1]), __uint_as_float(o[4 * t + 2]),
-                            __uint_as_float(o[4 * t + 3]));
+            st_part(po + (size_t)(quad0 + t) * kTile, __uint_as_float(o[4 * t]), __uint_as_float(o[4 * t + 1]),
+                    __uint_as_float(o[4 * t + 2]), __uint_as_float(o[4 * t + 3]), stay);
         }
         if (half == 0 && ch == 0) stats[(size_t)g.part * kTile + rr] = make_float4(m_run, lsum, m_true, 0.f);
       } else {
@@ -1152,59 +1173,158 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // Joins the parts of the tiles that several pairs worked on:
 //   M = max m_k, w_k = 2^(m_k - M), l = sum w_k l_k, out = sum w_k O_k / l,
-// the parts in ascending key order.  grid (pairs, 16): 32 of the 512 columns.
-constexpr int kJoinThreads = 256, kJoinSplit = 16;
+// in a fixed order.  A tile may have a part from every pair (one long sequence),
+// or the batch a two-part tile from every pair.  Up to 8 parts, one thread takes
+// all parts of one row's 16 columns; above, four threads share the parts of one
+// row's 8 columns.  What counts is that many loads are in flight (one thread for
+// 4 columns of all 74 parts of a 16K-row sequence: 25 us).
+constexpr int kJoinThreads = 256, kJoinGroups = 4, kJoinFew = 8;
+constexpr int kJoinPerPair = 6;                    // CTAs: what is resident at once (a CTA's start costs a piece's time)
+constexpr int kMaxPairs = 256;
+
+// parts k = g, g + step, ... of one row: running max, sum, true max, and O of NQ column quads
+template <int NQ>
+struct Joined {
+  float M, l, true_max;
+  float4 o[NQ];
+};
+// U parts at a time, all of their loads in flight together
+template <int NQ, int U>
+__device__ __forceinline__ Joined<NQ> join_parts(const float4* __restrict__ parts, const float4* __restrict__ stats,
+                                                 int pair, int nparts, int g, int step, int row, int q) {
+  auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * pair + 1 : 2 * (pair + k)); };
+  const uint64_t go = policy_go();
+  Joined<NQ> j;
+  j.M = j.true_max = -INFINITY;
+  j.l = 0.f;
+#pragma unroll
+  for (int t = 0; t < NQ; ++t) j.o[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int k0 = g; k0 < nparts; k0 += U * step) {
+    float4 s[U], v[U][NQ];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * step;
+      const bool in = k < nparts;
+      const size_t sl = slot(in ? k : k0);
+      s[u] = stats[sl * kTile + row];
+      const float4* p = parts + sl * (kTile * kDV / 4) + (size_t)q * kTile + row;
+#pragma unroll
+      for (int t = 0; t < NQ; ++t) v[u][t] = in ? ld_part(p + t * kTile, go) : make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!in) s[u] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    }
+    float M = j.M;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      M = fmaxf(M, s[u].x);
+      j.true_max = fmaxf(j.true_max, s[u].z);
+    }
+    const float mu = M == -INFINITY ? 0.f : M, w0 = ex2(j.M - mu);  // nothing so far: 2^-inf = 0
+    j.l *= w0;
+#pragma unroll
+    for (int t = 0; t < NQ; ++t) j.o[t] = make_float4(w0 * j.o[t].x, w0 * j.o[t].y, w0 * j.o[t].z, w0 * j.o[t].w);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float w = ex2(s[u].x - mu);            // a part with no visible key: 0
+      j.l = fmaf(w, s[u].y, j.l);
+#pragma unroll
+      for (int t = 0; t < NQ; ++t) {
+        j.o[t].x = fmaf(w, v[u][t].x, j.o[t].x);
+        j.o[t].y = fmaf(w, v[u][t].y, j.o[t].y);
+        j.o[t].z = fmaf(w, v[u][t].z, j.o[t].z);
+        j.o[t].w = fmaf(w, v[u][t].w, j.o[t].w);
+      }
+    }
+    j.M = M;
+  }
+  return j;
+}
+template <int NQ>
+__device__ __forceinline__ void join_store(const Joined<NQ>& j, long long r, int q, __nv_bfloat16* out, float* mx,
+                                           float* sm_out) {
+  const float inv = j.l == 0.f ? 0.f : 1.f / j.l;
+  uint2* dst = reinterpret_cast<uint2*>(out + r * kDV + 4 * q);
+#pragma unroll
+  for (int t = 0; t < NQ; ++t)
+    dst[t] = make_uint2(pack_bf16x2(j.o[t].x * inv, j.o[t].y * inv), pack_bf16x2(j.o[t].z * inv, j.o[t].w * inv));
+  if (q == 0) {
+    mx[r] = j.true_max == -INFINITY ? -INFINITY : j.true_max * kLn2;
+    sm_out[r] = j.l == 0.f ? 0.f : j.l * ex2((j.M == -INFINITY ? 0.f : j.M) - j.true_max);
+  }
+}
+
 __global__ void __launch_bounds__(kJoinThreads)
     tree_join_kernel(const float4* __restrict__ parts, const float4* __restrict__ stats,
-                     const Join* __restrict__ joins, __nv_bfloat16* __restrict__ out, float* __restrict__ mx,
-                     float* __restrict__ sm_out) {
-  const int pair = blockIdx.x;
+                     const Join* __restrict__ joins, int npairs, __nv_bfloat16* __restrict__ out,
+                     float* __restrict__ mx, float* __restrict__ sm_out) {
+  __shared__ Joined<2> shared[kJoinGroups - 1][64];
+  __shared__ Join list[kMaxPairs];
+  __shared__ uint16_t list_pair[kMaxPairs];
+  __shared__ int below[kMaxPairs / 32];
   let_next_launch();
   wait_for_earlier();
-  const Join jn = joins[pair];
-  if (jn.nparts == 0) return;
-  const int row = threadIdx.x & 127, q0 = 8 * blockIdx.y + 4 * (threadIdx.x >> 7);
-  if (row >= jn.nrows) return;
-  auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * pair + 1 : 2 * (pair + k)); };
-  float M = -INFINITY, true_max = -INFINITY;
-  for (int k = 0; k < jn.nparts; ++k) {
-    const float4 s = stats[slot(k) * kTile + row];
-    M = fmaxf(M, s.x);
-    true_max = fmaxf(true_max, s.z);
+  const int tid = threadIdx.x;
+  // the pairs whose tile is to be joined, in order
+  Join mine = {0, 0, 0};
+  if (tid < npairs) mine = joins[tid];
+  const uint32_t bits = __ballot_sync(0xffffffffu, mine.nparts > 0);
+  if ((tid & 31) == 0) below[tid >> 5] = __popc(bits);
+  __syncthreads();
+  int at = __popc(bits & ((1u << (tid & 31)) - 1u)), n = 0;
+#pragma unroll
+  for (int w = 0; w < kMaxPairs / 32; ++w) {
+    if (w < (tid >> 5)) at += below[w];
+    n += below[w];
   }
-  const float mu = M == -INFINITY ? 0.f : M;
-  float l = 0.f;
-  float4 o[4];
+  if (mine.nparts > 0) {
+    list[at] = mine;
+    list_pair[at] = (uint16_t)tid;
+  }
+  __syncthreads();
+  int piece = blockIdx.x;                          // this CTA's next piece, counted from the current tile's first
+  for (int i = 0; i < n; ++i) {
+    const Join jn = list[i];
+    const int pair = list_pair[i];
+    const bool few = jn.nparts <= kJoinFew;
+    const int pieces = few ? 16 : 128;
+    for (; piece < pieces; piece += gridDim.x) {
+      if (few) {                                   // 128 rows x 2 x 16 columns
+        const int row = tid & 127, q = 8 * piece + 4 * (tid >> 7);
+        const Joined<4> j = join_parts<4, 2>(parts, stats, pair, jn.nparts, 0, 1, row, q);
+        if (row < jn.nrows) join_store<4>(j, jn.row0 + row, q, out, mx, sm_out);
+        continue;
+      }
+      // 64 rows x 8 columns, four threads each
+      const int cell = tid & 63, row = (piece & 1) * 64 + cell, q = 2 * (piece >> 1), g = tid >> 6;
+      Joined<2> j = join_parts<2, 4>(parts, stats, pair, jn.nparts, g, kJoinGroups, row, q);
+      __syncthreads();                             // the last piece's sums are read
+      if (g > 0) shared[g - 1][cell] = j;
+      __syncthreads();
+      if (g > 0 || row >= jn.nrows) continue;
+      Joined<2> all = j;
 #pragma unroll
-  for (int t = 0; t < 4; ++t) o[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = 0; k < jn.nparts; ++k) {
-    const float4 s = stats[slot(k) * kTile + row];
-    const float w = ex2(s.x - mu);                 // a part with no visible key: 2^-inf = 0
-    l += w * s.y;
+      for (int t = 0; t < kJoinGroups - 1; ++t) {
+        all.M = fmaxf(all.M, shared[t][cell].M);
+        all.true_max = fmaxf(all.true_max, shared[t][cell].true_max);
+      }
+      const float mu = all.M == -INFINITY ? 0.f : all.M;
+      auto add = [&](const Joined<2>& p, bool first) {  // (no key in the group: weight 0)
+        const float w = ex2(p.M - mu);
+        all.l = fmaf(w, p.l, first ? 0.f : all.l);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const float4 v = parts[slot(k) * (kTile * kDV / 4) + (size_t)(q0 + t) * kTile + row];
-      o[t].x = fmaf(w, v.x, o[t].x);
-      o[t].y = fmaf(w, v.y, o[t].y);
-      o[t].z = fmaf(w, v.z, o[t].z);
-      o[t].w = fmaf(w, v.w, o[t].w);
+        for (int t = 0; t < 2; ++t) {
+          all.o[t].x = fmaf(w, p.o[t].x, first ? 0.f : all.o[t].x);
+          all.o[t].y = fmaf(w, p.o[t].y, first ? 0.f : all.o[t].y);
+          all.o[t].z = fmaf(w, p.o[t].z, first ? 0.f : all.o[t].z);
+          all.o[t].w = fmaf(w, p.o[t].w, first ? 0.f : all.o[t].w);
+        }
+      };
+      add(j, true);
+#pragma unroll
+      for (int t = 0; t < kJoinGroups - 1; ++t) add(shared[t][cell], false);
+      join_store<2>(all, jn.row0 + row, q, out, mx, sm_out);
     }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const long long r = jn.row0 + row;
-  uint32_t pw[8];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    pw[2 * t] = pack_bf16x2(o[t].x * inv, o[t].y * inv);
-    pw[2 * t + 1] = pack_bf16x2(o[t].z * inv, o[t].w * inv);
-  }
-  uint4* dst = reinterpret_cast<uint4*>(out + r * kDV + 4 * q0);
-  dst[0] = make_uint4(pw[0], pw[1], pw[2], pw[3]);
-  dst[1] = make_uint4(pw[4], pw[5], pw[6], pw[7]);
-  if (q0 == 0) {
-    mx[r] = true_max == -INFINITY ? -INFINITY : true_max * kLn2;
-    sm_out[r] = l == 0.f ? 0.f : l * ex2(mu - true_max);
+    piece -= pieces;
   }
 }
 
@@ -1252,6 +1372,7 @@ int launch_tree_attn_tc(const TreeArgs& a, const void* q, const void* pool, long
   }
   const int bound = tree_pairs_bound();
   if (pairs > bound) pairs = bound;
+  if (pairs > kMaxPairs) pairs = kMaxPairs;
   const size_t n = (size_t)bound;
   float4* parts = (float4*)ws;
   float4* stats = (float4*)((uint8_t*)ws + up256(2 * n * kPartBytes));
@@ -1280,9 +1401,9 @@ int launch_tree_attn_tc(const TreeArgs& a, const void* q, const void* pool, long
                            (const __nv_bfloat16*)kv_new, (__nv_bfloat16*)out, mx, sm, parts, stats, joins, c, wide, pv,
                            pv2, pr, pr2, nv, nr, po))
     return DSA_ERR_CUDA;
-  return launch_programmatic(tree_join_kernel, dim3(pairs, kJoinSplit), dim3(kJoinThreads), 0, st, 1,
-                             (const float4*)parts, (const float4*)stats, (const Join*)joins, (__nv_bfloat16*)out, mx,
-                             sm)
+  return launch_programmatic(tree_join_kernel, dim3(kJoinPerPair * pairs), dim3(kJoinThreads), 0, st, 1,
+                             (const float4*)parts, (const float4*)stats, (const Join*)joins, pairs,
+                             (__nv_bfloat16*)out, mx, sm)
              ? DSA_OK
              : DSA_ERR_CUDA;
 }
