@@ -42,10 +42,16 @@
 // are not run).  A drafted row with an infinity or NaN that only some of the
 // tile's tokens see is zeroed too, and the tokens that see it get NaN.
 //
+// A tile's query takes a slot of the key ring ahead of its keys: 448 of its value
+// columns come by TMA, and the fix warps move them into TMEM, with the other 64
+// and the rope columns from registers, once the last logits of the tile before
+// have read the old query (per-row loads of the softmax warps took 4,200 cycles
+// between two tiles).
+//
 // Roles per CTA: warp 0 = TMEM allocation, MMA issuer (CTA 0); warps 1..4 =
-// passing on of each key stage (with the zeroing above); warps 5..20 = softmax,
-// epilogue, and the next tile's query columns into TMEM; warp 21 = schedule;
-// warps 22, 23 = key loads (value columns, rope columns).
+// query into TMEM, passing on of each key stage (with the zeroing above); warps
+// 5..20 = softmax and epilogue; warp 21 = schedule; warps 22, 23 = key loads
+// (value columns and query; rope columns).
 #include <math.h>
 #include <stddef.h>
 
@@ -64,11 +70,13 @@ constexpr int kRope = kBlk * 64;                   // 112 slots x 32 rope column
 constexpr int kStageBytes = kValue + kRope;
 constexpr int kPBytes = 2 * kHC * 128;
 constexpr int kPvSteps = kBlk / 16;
+constexpr int kQTile = kHC * 128, kQTiles = 7;     // query through a stage: tiles of 64 rows x 64 columns (SW128 rows)
 constexpr int kUnit = 4 * kHC * 16;                // one float4 of every (column part, row): exchange unit
 constexpr int kFixWarps = 4, kSoftWarps = 16, kLoadWarps = 2, kSoftThreads = 32 * kSoftWarps;
 constexpr int kWarpFix0 = 1, kWarpSoft0 = kWarpFix0 + kFixWarps;
 constexpr int kWarpScan = kWarpSoft0 + kSoftWarps, kWarpLoad = kWarpScan + 1;
 constexpr int kThreads = 32 * (kWarpLoad + kLoadWarps);
+static_assert(kQTiles * kQTile <= kStageBytes, "the query's slot");
 static_assert(kBlk <= 32 * kFixWarps && kBlk % 16 == 0, "a fix warp takes two 16-slot steps");
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = kColS + kBlk;
@@ -97,14 +105,14 @@ constexpr size_t kPartBytes = (size_t)kTile * kDV * 4, kStatBytes = (size_t)kTil
 
 struct __align__(1024) Smem {
   uint8_t stage[kStages][kStageBytes];             // value columns | rope columns
-  uint8_t p[2][kPBytes];                           // P of even / odd blocks (and the exchange, and O)
+  uint8_t p[2][kPBytes];                           // P of even / odd blocks (and the exchange)
   Seg seg[2];
   alignas(16) unsigned long long valid[kStages][2];            // slots that hold a row
   uint32_t bad[kStages][kFixWarps];                // 32 slots each: zeroed for an infinity or NaN
   alignas(4) uint8_t live[kStages][kFixWarps];                // 2 steps of 16 slots each: some token sees some slot
   alignas(16) uint8_t spare[kUnit];                // of the logit exchange; row maxima and sums between exchanges
   uint32_t sink[kSoftWarps];                       // targets of CTA 1's signalling stores
-  uint32_t sink_f[kFixWarps];
+  uint32_t sink_f[2][kFixWarps];
   uint64_t st_full[kStages], st_empty[kStages], ready[kStages];
   uint64_t s_full, s_free, p_full[2];
   uint64_t q_tm[2], q_free[2], mma_done[2], sc_full[2], sc_empty[2], fin;
@@ -237,11 +245,11 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* tm,
 __device__ __forceinline__ void st_zero16(uint32_t addr) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
 }
-// 32 bytes (32-byte aligned) of global memory that is only read here
-__device__ __forceinline__ void ld_global32(const void* p, uint32_t* w) {
-  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-               : "l"(p));
+// 32 bytes to global memory (32-byte aligned)
+__device__ __forceinline__ void st_global32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 // lane = thread's TMEM lane, 4 consecutive 32-bit columns
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint4& v) {
@@ -308,7 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         DevCtx c, int wide, const __grid_constant__ CUtensorMap tm_page_v,
                         const __grid_constant__ CUtensorMap tm_page_v2, const __grid_constant__ CUtensorMap tm_page_r,
                         const __grid_constant__ CUtensorMap tm_page_r2, const __grid_constant__ CUtensorMap tm_new_v,
-                        const __grid_constant__ CUtensorMap tm_new_r, const __grid_constant__ CUtensorMap tm_out) {
+                        const __grid_constant__ CUtensorMap tm_new_r, const __grid_constant__ CUtensorMap tm_q) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);   // the operands' swizzles need the 1024-byte alignment
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -332,7 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&sm.s_free), kSoftWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm.p_full[i]), kSoftWarps);
-      mbar_init(smem_u32(&sm.q_tm[i]), kSoftWarps);
+      mbar_init(smem_u32(&sm.q_tm[i]), kFixWarps);
       mbar_init(smem_u32(&sm.q_free[i]), 1);
       mbar_init(smem_u32(&sm.mma_done[i]), 1);
       mbar_init(smem_u32(&sm.sc_full[i]), 1);
@@ -485,6 +493,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[i & 1]));
       if (g.end) break;
       const int32_t* trow = a.table + (long long)g.b * a.max_pages;
+      {
+        // the query's slot: 64 rows x 448 value columns (rows behind the tile's last
+        // come along; nothing of theirs is written)
+        const int st = G % kStages;
+        if (!mbar_wait_warp(smem_u32(&sm.st_empty[st]), ((G / kStages) & 1) ^ 1, c, abort_flag)) break;
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&sm.st_full[st]);
+          if (rope) {
+            mbar_arrive(bar);
+          } else {
+            mbar_arrive_expect_tx(bar, kQTiles * kQTile);
+            const int y = (int)((long long)g.t0 * a.H + 128ll * g.tile) + kHC * (int)crank;
+#pragma unroll 1
+            for (int k = 0; k < kQTiles; ++k) tma_load_2d(smem_u32(sm.stage[st]) + k * kQTile, &tm_q, 64 * k, y, bar);
+          }
+        }
+        __syncwarp();
+        ++G;
+      }
       for (int j = g.j0; j < g.j1; ++j, ++G) {
         const int st = G % kStages;
         const bool drafted = j >= g.nc;
@@ -616,6 +643,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[i & 1]));
       if (g.end) break;
+      {
+        // thread = TMEM lane l of this warp's quadrant: row l & 63, column half l >> 6
+        const int st = G % kStages, l = (warp & 3) * 32 + lane, rl = l & 63, half = l >> 6;
+        const long long qrow = (long long)g.t0 * a.H + 128ll * g.tile + kHC * (int)crank + rl;
+        const bool there = qrow < (long long)a.n_tok * a.H;
+        const __nv_bfloat16* qh = qg + (there ? qrow : 0) * kDQK;
+        uint4 r[4];                                // rope columns [32 half, +32)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          r[t] = there ? __ldg(reinterpret_cast<const uint4*>(qh + kDV + 32 * half) + t) : make_uint4(0, 0, 0, 0);
+        uint32_t x[32];                            // half 1: value columns 448..511
+        auto put = [&](int t, uint4 v) { x[4 * t] = v.x, x[4 * t + 1] = v.y, x[4 * t + 2] = v.z, x[4 * t + 3] = v.w; };
+        if (half == 1) {
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+            put(t, there ? __ldg(reinterpret_cast<const uint4*>(qh + 448) + t) : make_uint4(0, 0, 0, 0));
+        }
+        ok = mbar_wait_warp(smem_u32(&sm.st_full[st]), (G / kStages) & 1, c, abort_flag) &&
+             (i == 0 || mbar_wait_warp(smem_u32(&sm.q_free[(i - 1) & 1]), ((i - 1) >> 1) & 1, c, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t dst = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColQ;
+        const uint8_t* src = sm.stage[st] + rl * 128;
+#pragma unroll 1
+        for (int p = 3; p >= 0; --p) {             // 64 value columns -> 32 TMEM columns
+          if (p < 3 || half == 0) {
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+              put(t, *reinterpret_cast<const uint4*>(src + (4 * half + p) * kQTile + ((t ^ (rl & 7)) << 4)));
+          }
+          __syncwarp();
+          tmem_st32(dst + 32 * p, x);
+          tmem_st_wait();
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) tmem_st4(dst + 128 + 4 * t, r[t]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&sm.q_tm[i & 1]);
+          if (crank == 0) {
+            if (fw == 0) mbar_arrive_expect_tx(bar, 4 * kFixWarps);
+            else mbar_arrive(bar);
+          } else {
+            st_async_signal(mapa_shared(smem_u32(&sm.sink_f[0][fw]), 0), mapa_shared(bar, 0));
+          }
+        }
+        __syncwarp();
+        ++G;
+      }
       // the tokens of the tile
       const int ta = (int)(128ll * g.tile / a.H);
       const long long last = (128ll * g.tile + 127) / a.H;
@@ -696,7 +774,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (fw == 0) mbar_arrive_expect_tx(bar, 4 * kFixWarps);
             else mbar_arrive(bar);
           } else {
-            st_async_signal(mapa_shared(smem_u32(&sm.sink_f[fw]), 0), mapa_shared(bar, 0));
+            st_async_signal(mapa_shared(smem_u32(&sm.sink_f[1][fw]), 0), mapa_shared(bar, 0));
           }
         }
       }
@@ -708,7 +786,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // is issued (the softmax of block G exchanges logits through that P
       // buffer); no progress for the wait budget is a timeout.
       int Gs = 0, Gp = 0;                          // blocks so far: logits issued / PVs issued
-      uint32_t ss = 0, ss_par = 0, sp = 0;         // their stages (and the parity of the first's phase)
+      uint32_t ss = 0, sp = 0;                     // their stages
+      uint32_t ready_par = 0;                      // parity of each stage's next `ready` phase, a bit each
       bool ok = true;
       for (int i = 0; ok; ++i) {
         const int bi = i & 1;
@@ -719,12 +798,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!mbar_wait<true>(smem_u32(&sm.q_tm[bi]), (i >> 1) & 1, c, abort_flag)) break;
         tc_fence_after();
         int js = 0, jp = 0;
+        commit2(smem_u32(&sm.st_empty[0]) + 8 * ss);  // the query's slot is free
+        if (++ss == kStages) ss = 0;
+        if (++sp == kStages) sp = 0;
         uint64_t t_idle = 0;
         uint32_t spins = 0;
         while (ok && jp < nblk) {
           bool progressed = false;
           if (js < nblk && js <= jp + 1 && (Gs == 0 || mbar_poll(smem_u32(&sm.s_free), (Gs - 1) & 1)) &&
-              mbar_poll(smem_u32(&sm.ready[0]) + 8 * ss, ss_par)) {
+              mbar_poll(smem_u32(&sm.ready[0]) + 8 * ss, (ready_par >> ss) & 1u)) {
             tc_fence_after();
             const uint32_t sb = smem_u32(sm.stage[0]) + ss * kStageBytes;
             const uint32_t v = desc_lo(sb, 16), r = desc_lo(sb + kValue, 16);
@@ -738,7 +820,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             commit2(smem_u32(&sm.s_full));
             ++js;
             ++Gs;
-            if (++ss == kStages) ss = 0, ss_par ^= 1;
+            ready_par ^= 1u << ss;
+            if (++ss == kStages) ss = 0;
             if (js == nblk) commit2(smem_u32(&sm.q_free[bi]));
             progressed = true;
           } else if (jp < js && mbar_poll(smem_u32(&sm.p_full[Gp & 1]), (Gp >> 1) & 1)) {
@@ -833,58 +916,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto cut = [&](unsigned long long v0, unsigned long long v1) -> uint32_t {
       return (uint32_t)(s0 >= 64 ? v1 >> (s0 - 64) : (s0 ? (v0 >> s0) | (v1 << (64 - s0)) : v0));
     };
-    // A tile's query into TMEM: part ch of this lane's row and column half, 64
-    // value columns and 8 rope columns, before the epilogue of the tile ahead of
-    // it.  A warp's load touches 32 rows, so 32 lines: the widest loads take the
-    // fewest turns of the load pipe.
-    const bool wide_q = (reinterpret_cast<uintptr_t>(qg) & 31u) == 0;  // 32-byte loads (rows are 1152 bytes)
-    auto load_query = [&](int i) -> bool {
-      const Seg& n = sm.seg[i & 1];
-      const long long left = (long long)n.T * a.H - 128ll * n.tile;
-      const bool live = rr < left;
-      const __nv_bfloat16* qh =
-          qg + ((long long)n.t0 * a.H + 128ll * n.tile + (live ? rr : 0)) * (long long)kDQK;
-      const __nv_bfloat16* vsrc = qh + 256 * half + 64 * ch;
-      uint32_t w[32];
-      uint4 rope = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if (!live) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[8 * t + e] = 0u;
-        } else if (wide_q) {
-          ld_global32(vsrc + 16 * t, w + 8 * t);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(vsrc + 16 * t) + e);
-            w[8 * t + 4 * e] = v.x, w[8 * t + 4 * e + 1] = v.y, w[8 * t + 4 * e + 2] = v.z, w[8 * t + 4 * e + 3] = v.w;
-          }
-        }
-      }
-      if (live) rope = __ldg(reinterpret_cast<const uint4*>(qh + kDV + 32 * half + 8 * ch));
-      // the last logits of the tile ahead have read the old query
-      if (i > 0 && !mbar_wait_warp(smem_u32(&sm.q_free[(i - 1) & 1]), ((i - 1) >> 1) & 1, c, abort_flag)) return false;
-      tc_fence_after();
-      tmem_st32(tmem + lane_off + kColQ + 32 * ch, w);
-      tmem_st4(tmem + lane_off + kColQ + 128 + 4 * ch, rope);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      signal(&sm.q_tm[i & 1]);
-      return true;
-    };
     // Every warp executes the same sequence of named barriers whatever happens
     // (after a failed wait it goes on through the segment without work, and
     // the vote at the next one makes all of them stop).
     bool ok = true;
-    const bool o_storer = warp == kWarpSoft0 && lane == 0;
-    int G = 0;
-    ok = mbar_wait_warp(smem_u32(&sm.sc_full[0]), 0, c, abort_flag);
-    if (ok && !sm.seg[0].end) ok = load_query(0);
+    int G = 0, B = 0;                              // ring slots, blocks so far
     for (int i = 0;; ++i) {
       const int bi = i & 1;
-      if (o_storer) bulk_wait_read_all();          // the last tile's O has left the P buffers
+      if (ok) ok = mbar_wait_warp(smem_u32(&sm.sc_full[bi]), (i >> 1) & 1, c, abort_flag);
       if (named_bar_or(2, kSoftThreads, !ok)) break;
       const Seg g = sm.seg[bi];
       __syncwarp();
@@ -895,13 +934,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int tok = live ? (int)((128ll * g.tile + rr) / a.H) : g.T - 1;
       float m_run = -INFINITY, m_own = -INFINITY, l_run = 0.f;  // m_own: over this thread's slots
       bool poison = false;
-      for (int j = g.j0; j < g.j1; ++j, ++G) {
-        const int pb = G & 1, st = G % kStages;
+      ++G;                                         // the query's slot
+      for (int j = g.j0; j < g.j1; ++j, ++G, ++B) {
+        const int pb = B & 1, st = G % kStages;
         // One wait: the logits' commit completes after every MMA issued before it,
         // PV(G-2) among them, so P buffer pb is free as well; and the issuer took
         // this block after the load and fix warps had passed it on, so valid and
         // bad are there, too.
-        if (ok) ok = mbar_wait_warp(smem_u32(&sm.s_full), G & 1, c, abort_flag);
+        if (ok) ok = mbar_wait_warp(smem_u32(&sm.s_full), B & 1, c, abort_flag);
         uint32_t lo[16], hi[16];                   // the part's slots 0..15 and 16..31 (ch odd: 16..23)
         ulonglong2 vv = make_ulonglong2(0ull, 0ull);  // slots of the block that hold a row
 #pragma unroll
@@ -1067,8 +1107,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         signal(&sm.p_full[pb]);
       }
       // ------------------------------- epilogue -------------------------------
-      if (ok) ok = mbar_wait_warp(smem_u32(&sm.sc_full[bi ^ 1]), ((i + 1) >> 1) & 1, c, abort_flag);
-      if (ok && !sm.seg[bi ^ 1].end) ok = load_query(i + 1);
       if (ok) ok = mbar_wait_warp(smem_u32(&sm.mma_done[bi]), (i >> 1) & 1, c, abort_flag);
       tc_fence_after();
       if (poison) l_run = NAN;
@@ -1106,49 +1144,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else {
         const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // no visible key: 0
         const long long row0 = (long long)g.t0 * a.H + 128ll * g.tile + kHC * (int)crank;  // first row of this CTA
-        const int nrow = rows - kHC * (int)crank < kHC ? (int)(rows - kHC * (int)crank) : kHC;
-        // bf16 rows out through shared memory, in two rounds of 256 value columns
-        // (both P buffers, as four 64-column tiles with the 128-byte swizzle;
-        // tile 2 half + ch / 2: columns 256 half + 128 m + 64 (ch / 2))
-        uint8_t* const ostage = &sm.p[0][0];
-        uint8_t* const trow = ostage + (2 * half + (ch >> 1)) * (kHC * 128) + hl * 128;
-        const int th = threadIdx.x - 32 * kWarpSoft0;
+        // A thread holds 2 x 32 columns of its row: 64 consecutive bytes, whole
+        // sectors, straight to global memory, and nobody waits for the stores (a way
+        // through shared memory and TMA had two rounds of barriers: 4,800 cycles).
+        const bool wide_out = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
 #pragma unroll 1
         for (int m = 0; m < 2; ++m) {
+          uint32_t o[32];
+          tmem_ld32(tmem + lane_off + kColO + 128 * m + 32 * ch, o);
+          tmem_ld_wait(o);
           uint32_t pw[16];
-          {
-            uint32_t o[32];
-            tmem_ld32(tmem + lane_off + kColO + 128 * m + 32 * ch, o);
-            tmem_ld_wait(o);
 #pragma unroll
-            for (int t = 0; t < 16; ++t)
-              pw[t] = pack_bf16x2(__uint_as_float(o[2 * t]) * inv, __uint_as_float(o[2 * t + 1]) * inv);
-          }
-          if (m == 1) {                            // round 0 read before it is overwritten
-            if (o_storer) bulk_wait_read_all();
-            named_bar_sync(1, kSoftThreads);
-          }
+          for (int t = 0; t < 16; ++t)
+            pw[t] = pack_bf16x2(__uint_as_float(o[2 * t]) * inv, __uint_as_float(o[2 * t + 1]) * inv);
+          if (live) {
+            __nv_bfloat16* dst = out + (row0 + hl) * kDV + 256 * half + 128 * m + 32 * ch;
+            if (wide_out) {
+              st_global32(dst, pw);
+              st_global32(dst + 16, pw + 8);
+            } else {
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
-            *reinterpret_cast<uint4*>(trow + (((4 * (ch & 1) + t) ^ (hl & 7)) << 4)) =
-                make_uint4(pw[4 * t], pw[4 * t + 1], pw[4 * t + 2], pw[4 * t + 3]);
-          fence_proxy_async_smem();
-          named_bar_sync(1, kSoftThreads);
-          if (nrow == kHC) {                       // all 64 rows: TMA stores, not waited for here
-            if (o_storer) {
-#pragma unroll 1
-              for (int tt = 0; tt < 4; ++tt)
-                tma_store_2d(&tm_out, smem_u32(ostage + tt * (kHC * 128)), 256 * (tt >> 1) + 128 * m + 64 * (tt & 1),
-                             (int)row0);
-              bulk_commit_group();
-            }
-          } else {                                 // the sequence's last rows: nothing behind them is touched
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int r = 16 * e + (th >> 5), tt = (th >> 3) & 3, pc = th & 7;  // row, tile, 16-byte piece
-              if (r < nrow)
-                *reinterpret_cast<uint4*>(out + (row0 + r) * kDV + 256 * (tt >> 1) + 128 * m + 64 * (tt & 1) + 8 * pc) =
-                    *reinterpret_cast<const uint4*>(ostage + tt * (kHC * 128) + r * 128 + ((pc ^ (r & 7)) << 4));
+              for (int t = 0; t < 4; ++t)
+                reinterpret_cast<uint4*>(dst)[t] = make_uint4(pw[4 * t], pw[4 * t + 1], pw[4 * t + 2], pw[4 * t + 3]);
             }
           }
         }
@@ -1160,7 +1177,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();                           // O is overwritten by the next segment's first PV
     }
-    if (o_storer) bulk_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -1377,7 +1393,7 @@ int launch_tree_attn_tc(const TreeArgs& a, const void* q, const void* pool, long
   float4* parts = (float4*)ws;
   float4* stats = (float4*)((uint8_t*)ws + up256(2 * n * kPartBytes));
   Join* joins = (Join*)((uint8_t*)ws + up256(2 * n * kPartBytes) + up256(2 * n * kStatBytes));
-  CUtensorMap pv, pv2, pr, pr2, nv, nr, po;
+  CUtensorMap pv, pv2, pr, pr2, nv, nr, pq;
   // cached value columns: 64 columns, 8 rows, 64-column blocks, 8-row groups, pages; drafted ones: any first row
   const uint64_t row = kDQK * 2, R = (uint64_t)a.R, P = (uint64_t)a.n_pages, N = (uint64_t)a.n_tok;
   const uint64_t pv_dim[5] = {64, 8, 8, R / 8, P}, pv_str[4] = {row, 128, 8 * row, (uint64_t)page_stride};
@@ -1385,8 +1401,8 @@ int launch_tree_attn_tc(const TreeArgs& a, const void* q, const void* pool, long
   const uint64_t nv_dim[3] = {64, N, 8}, nv_str[2] = {row, 128};
   const uint64_t nr_dim[2] = {kDQK, N}, nr_str[1] = {row};
   const uint32_t pv_box[5] = {64, 8, 4, 2, 1}, pr_box[3] = {32, 16, 1}, nv_box[3] = {64, 8, 4}, nr_box[2] = {32, 16};
-  const uint64_t po_dim[2] = {kDV, N * (uint64_t)a.H}, po_str[1] = {kDV * 2};
-  const uint32_t po_box[2] = {64, kHC};
+  const uint64_t pq_dim[2] = {kDQK, N * (uint64_t)a.H}, pq_str[1] = {row};
+  const uint32_t pq_box[2] = {64, kHC};
   const int wide = a.R % 32 == 0;                  // two groups of 16 rows per copy
   const uint32_t pv2_box[5] = {64, 8, 4, wide ? 4u : 2u, 1}, pr2_box[3] = {32, wide ? 32u : 16u, 1};
   if (!make_tmap_bf16(&pv, pool, 5, pv_dim, pv_str, pv_box, 128) ||
@@ -1395,11 +1411,11 @@ int launch_tree_attn_tc(const TreeArgs& a, const void* q, const void* pool, long
       !make_tmap_bf16(&pr2, pool, 3, pr_dim, pr_str, pr2_box, 64) ||
       !make_tmap_bf16(&nv, kv_new, 3, nv_dim, nv_str, nv_box, 128) ||
       !make_tmap_bf16(&nr, kv_new, 2, nr_dim, nr_str, nr_box, 64) ||
-      !make_tmap_bf16(&po, out, 2, po_dim, po_str, po_box, 128))
+      !make_tmap_bf16(&pq, q, 2, pq_dim, pq_str, pq_box, 128))
     return DSA_ERR_CUDA;
   if (!launch_programmatic(tree_attn_tc_kernel, dim3(2 * pairs), dim3(kThreads), smem, st, 1, a, (const __nv_bfloat16*)q,
                            (const __nv_bfloat16*)kv_new, (__nv_bfloat16*)out, mx, sm, parts, stats, joins, c, wide, pv,
-                           pv2, pr, pr2, nv, nr, po))
+                           pv2, pr, pr2, nv, nr, pq))
     return DSA_ERR_CUDA;
   return launch_programmatic(tree_join_kernel, dim3(kJoinPerPair * pairs), dim3(kJoinThreads), 0, st, 1,
                              (const float4*)parts, (const float4*)stats, (const Join*)joins, pairs,
