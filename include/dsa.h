@@ -344,7 +344,9 @@ int dsa_forward_static_ws(const dsa_params *p, const void *q_I, const void *k_I,
  * pages (DSA_ERR_PAGES) it writes its inputs through unchanged, with no copies
  * and all slots -1, and sets the status word.
  *
- * n_seqs <= 8192, n_pages * page_rows < 2^31, max_pages * page_rows < 2^31.
+ * Arrays of these calls and of the two below are aligned to their elements.
+ * n_seqs <= 8192; n_pages * page_rows, max_pages * page_rows and n_seqs *
+ * max_pages < 2^31.
  */
 typedef struct {
   int64_t n_seqs, n_pages, page_rows, max_pages; /* table is [n_seqs][max_pages] int32 */

@@ -479,6 +479,7 @@ static int check(const dsa_beam* p, Args* a) {
       p->eos >= p->vocab)
     return DSA_ERR_INVALID_ARG;
   if (p->beams_in > kMaxBeams || p->beams_out > kMaxBeams || p->vocab > (1 << 24) || p->ld > (1ll << 40) ||
+      p->n_batch >= (1ll << 31) ||
       p->n_batch * p->beams_in * ((p->vocab + chunk_of(p->dtype) - 1) / chunk_of(p->dtype)) >= (1ll << 31))
     return DSA_ERR_UNSUPPORTED;
   a->n_batch = (int)p->n_batch;
@@ -489,6 +490,10 @@ static int check(const dsa_beam* p, Args* a) {
   a->ld = p->ld;
   a->eos = (int)p->eos;
   return DSA_OK;
+}
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + nb && y < x + na;
 }
 static size_t stat_bytes(const Args& a) { return (size_t)a.n_batch * a.win * a.chunks * kWarps * sizeof(Stat); }
 
@@ -515,7 +520,13 @@ int dsa_beam_select(const dsa_beam* p, const void* logits, const float* scores, 
   if (!logits || !scores || !parent || !token || !scores_out) return DSA_ERR_INVALID_ARG;
   if (finished && p->eos < 0) return DSA_ERR_INVALID_ARG;
   const uintptr_t esz = p->dtype == DSA_BF16 ? 2 : 4;
-  if (((uintptr_t)logits & (esz - 1)) != 0) return DSA_ERR_INVALID_ARG;
+  if (((uintptr_t)logits & (esz - 1)) != 0 ||
+      (((uintptr_t)scores | (uintptr_t)parent | (uintptr_t)token | (uintptr_t)scores_out) & 3u) != 0)
+    return DSA_ERR_INVALID_ARG;
+  // one request's results over another's beams
+  const size_t in = (size_t)a.n_batch * a.win, out = (size_t)a.n_batch * a.wout;
+  if (overlap(scores, 4 * in, scores_out, 4 * out) || (finished && finished_out && overlap(finished, in, finished_out, out)))
+    return DSA_ERR_INVALID_ARG;
   if (!workspace || ((uintptr_t)workspace & 15u) != 0) return DSA_ERR_WORKSPACE;
   DevCtx c;
   if (!ext_dev_ctx(&c)) return DSA_ERR_CUDA;

@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // entries of the table, one warp each; lane l takes entries j0 + l + 32 u
   const int nch = (d.max_pages + 255) / 256;
   auto entries = [&](auto f) {
-    const int items = n * nch;        // < 2^31 / 256 + n
+    const int items = n * nch;        // n * max_pages < 2^31
     for (int it = (int)rank * kWarps + (tid >> 5); it < items; it += (int)nc * kWarps) {
       const int i = it / nch, j0 = (it - i * nch) * 256, len = lens[i];
       const bool ok = len >= 0 && len <= (long long)d.max_pages * R;
@@ -608,7 +608,8 @@ static int check(const dsa_cache* p, Dims* d) {
   if (!p) return DSA_ERR_INVALID_ARG;
   if (p->n_seqs < 1 || p->n_pages < 1 || p->page_rows < 1 || p->max_pages < 1) return DSA_ERR_INVALID_ARG;
   if (p->n_seqs > kMaxSeqs || p->n_pages > (1ll << 30) || p->page_rows > (1ll << 30) || p->max_pages > (1ll << 30) ||
-      p->n_pages * p->page_rows >= (1ll << 31) || p->max_pages * p->page_rows >= (1ll << 31))
+      p->n_pages * p->page_rows >= (1ll << 31) || p->max_pages * p->page_rows >= (1ll << 31) ||
+      p->n_seqs * p->max_pages >= (1ll << 31))
     return DSA_ERR_UNSUPPORTED;
   d->n_seqs = (int)p->n_seqs;
   d->n_pages = (int)p->n_pages;
@@ -620,7 +621,11 @@ static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
   return x < y + nb && y < x + na;
 }
-static bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+// int32 arrays: all there, 4-byte aligned
+template <typename... P>
+static bool ints(const P*... p) {
+  return ((p != nullptr && ((uintptr_t)p & 3u) == 0) && ...);
+}
 
 // one CTA while the work is small (a cluster barrier costs more than the
 // second CTA saves), else a cluster of eight
@@ -683,8 +688,7 @@ int dsa_cache_fork(const dsa_cache* p, const int32_t* parent, const int32_t* tab
   Dims d;
   int rc = check(p, &d);
   if (rc) return rc;
-  if (!parent || !table || !lens || !refs || !table_out || !lens_out || !refs_out || !copies || !n_copies)
-    return DSA_ERR_INVALID_ARG;
+  if (!ints(parent, table, lens, refs, table_out, lens_out, refs_out, copies, n_copies)) return DSA_ERR_INVALID_ARG;
   const size_t nt = (size_t)d.n_seqs * d.max_pages * 4, ns = (size_t)d.n_seqs * 4, np = (size_t)d.n_pages * 4;
   if (overlap(table, nt, table_out, nt) || overlap(lens, ns, lens_out, ns) || overlap(refs, np, refs_out, np) ||
       overlap(parent, ns, lens_out, ns))
@@ -701,7 +705,7 @@ int dsa_cache_extend(const dsa_cache* p, const int32_t* n_new, int32_t* table, c
   Dims d;
   int rc = check(p, &d);
   if (rc) return rc;
-  if (!n_new || !table || !lens || !refs || !lens_out || !refs_out || !slots) return DSA_ERR_INVALID_ARG;
+  if (!ints(n_new, table, lens, refs, lens_out, refs_out, slots)) return DSA_ERR_INVALID_ARG;
   if (n_slots < 1) return DSA_ERR_INVALID_ARG;
   if (n_slots > (1ll << 20)) return DSA_ERR_UNSUPPORTED;
   const size_t ns = (size_t)d.n_seqs * 4, np = (size_t)d.n_pages * 4;
@@ -720,8 +724,7 @@ int dsa_cache_compact(const dsa_cache* p, const int32_t* table, const int32_t* l
   Dims d;
   int rc = check(p, &d);
   if (rc) return rc;
-  if (!table || !lens || !refs || !table_out || !refs_out || !page_map || !copies || !n_copies)
-    return DSA_ERR_INVALID_ARG;
+  if (!ints(table, lens, refs, table_out, refs_out, page_map, copies, n_copies)) return DSA_ERR_INVALID_ARG;
   const size_t nt = (size_t)d.n_seqs * d.max_pages * 4, np = (size_t)d.n_pages * 4;
   if (overlap(table, nt, table_out, nt) || overlap(refs, np, refs_out, np) || overlap(refs, np, page_map, np))
     return DSA_ERR_INVALID_ARG;
@@ -739,7 +742,7 @@ int dsa_cache_copy_pages(const dsa_cache* p, const dsa_pool* pool, const int32_t
   Pool o;
   rc = check_pool(p, pool, &o);
   if (rc) return rc;
-  if (!copies || !n_copies || max_copies < 0 || max_copies > (1ll << 30)) return DSA_ERR_INVALID_ARG;
+  if (!ints(copies, n_copies) || max_copies < 0 || max_copies > (1ll << 30)) return DSA_ERR_INVALID_ARG;
   if (max_copies == 0) return DSA_OK;
   DevCtx c;
   if (!ext_dev_ctx(&c)) return DSA_ERR_CUDA;
@@ -772,7 +775,8 @@ int dsa_cache_write(const dsa_cache* p, const dsa_pool* pool, const void* rows, 
   Pool o;
   rc = check_pool(p, pool, &o);
   if (rc) return rc;
-  if (!rows || !slots || n_src < 1 || n_rows < 0 || rows_layer_stride < 0) return DSA_ERR_INVALID_ARG;
+  if (!rows || !ints(slots) || (row_index && !ints(row_index)) || n_src < 1 || n_rows < 0 || rows_layer_stride < 0)
+    return DSA_ERR_INVALID_ARG;
   if (n_src > (1ll << 30) || n_rows > (1ll << 30)) return DSA_ERR_UNSUPPORTED;
   if (n_rows == 0) return DSA_OK;
   DevCtx c;

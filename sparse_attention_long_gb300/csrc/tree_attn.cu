@@ -270,7 +270,9 @@ int dsa_tree_attn_fwd(const dsa_cache* p, const dsa_tree* t, const void* q, cons
   if (pool->page_stride >= (1ll << 38)) return DSA_ERR_UNSUPPORTED;
   const uintptr_t bits = (uintptr_t)q | (uintptr_t)pool->base | (uintptr_t)kv_new | (uintptr_t)out |
                          (uintptr_t)pool->page_stride;
-  if ((bits & (bf16 ? 15u : 3u)) != 0) return DSA_ERR_INVALID_ARG;
+  const uintptr_t words = (uintptr_t)table | (uintptr_t)lens | (uintptr_t)tok_start | (uintptr_t)softmax_max |
+                          (uintptr_t)softmax_sum;
+  if ((bits & (bf16 ? 15u : 3u)) != 0 || (words & 3u) != 0 || ((uintptr_t)mask & 7u) != 0) return DSA_ERR_INVALID_ARG;
   if (bf16 && (!workspace || ((uintptr_t)workspace & 15u) != 0)) return DSA_ERR_WORKSPACE;
   DevCtx c;
   if (!ext_dev_ctx(&c)) return DSA_ERR_CUDA;

@@ -254,3 +254,49 @@ def test_beam_host_validation_without_gpu():
         assert call(b) == code and dsa.beam_workspace_size(b) == 0
     assert call(mk(), fin=A[2]) == I and call(mk(), logits=None) == I and call(mk(), logits=A[0] + 2) == I
     assert call(mk(), ws=None) == dsa.DSA_ERR_WORKSPACE and call(mk(), ws=A[7] + 8) == dsa.DSA_ERR_WORKSPACE
+
+
+def test_decoding_calls_refuse_misaligned_and_overlapping_arrays():
+    dsa = _lib()
+    I, U = dsa.DSA_ERR_INVALID_ARG, dsa.DSA_ERR_UNSUPPORTED
+    ref = ctypes.byref
+    A = [0x10000 * (i + 1) for i in range(13)]
+    off = lambda k, n, by=2: [a + by if i == k else a for i, a in enumerate(A[:n])]
+    c = dsa.make_cache(n_seqs=2, n_pages=8, page_rows=64, max_pages=3)
+    pool = dsa.dsa_pool(A[11], 1, 0, 64 * 1152, 1152)
+    for k in range(9):
+        assert dsa.lib.dsa_cache_fork(ref(c), *off(k, 9), None) == I
+    for k in range(7):
+        assert dsa.lib.dsa_cache_extend(ref(c), *off(k, 7), 5, None) == I
+    for k in range(8):
+        assert dsa.lib.dsa_cache_compact(ref(c), *off(k, 8), None) == I
+    for k in range(2):
+        assert dsa.lib.dsa_cache_copy_pages(ref(c), ref(pool), *off(k, 2), 4, None) == I
+    assert dsa.lib.dsa_cache_write(ref(c), ref(pool), A[0], 4, 0, A[1] + 1, None, 4, None) == I
+    assert dsa.lib.dsa_cache_write(ref(c), ref(pool), A[0], 4, 0, A[1], A[2] + 2, 4, None) == I
+    wide = dsa.make_cache(n_seqs=8192, n_pages=8, page_rows=1, max_pages=1 << 18)
+    assert dsa.lib.dsa_cache_fork(ref(wide), *A[:9], None) == U
+
+    def tree(t, a, mask):                 # q, table, lens, kv_new, tok_start, out, max, sum
+        return dsa.lib.dsa_tree_attn_fwd(ref(c), ref(t), a[0], ref(pool), a[1], a[2], a[3], a[4], mask, a[5], a[6],
+                                         a[7], A[12], None)
+
+    t = dsa.make_tree(n_tok=5, H=16, d_qk=576, d_v=512, scale=0.1, mask_words=1)
+    for k in range(8):
+        assert tree(t, off(k, 8), A[8]) == I
+    assert tree(t, A, A[8] + 4) == I
+
+    def beam(b, a, fin, fin_out):         # logits, scores, parent, token, scores_out
+        return dsa.lib.dsa_beam_select(ref(b), a[0], a[1], fin, a[2], a[3], a[4], fin_out, A[12], None)
+
+    b = dsa.make_beam(n_batch=2, beams_in=2, beams_out=3, vocab=8, dtype="fp32", eos=0)
+    for k in range(5):
+        assert beam(b, off(k, 5), A[8], A[9]) == I
+    a = list(A)
+    for shift in (0, 12, -20):            # scores: 16 bytes, scores_out: 24
+        a[4] = A[1] + shift
+        assert beam(b, a, A[8], A[9]) == I
+    for shift in (0, 3, -5):
+        assert beam(b, A, A[8], A[8] + shift) == I
+    for n in (1 << 31, 1 << 60):
+        assert beam(dsa.make_beam(n_batch=n, beams_in=32, beams_out=3, vocab=8), A, None, None) == U
