@@ -903,19 +903,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     };
-    float (*red)[32] = reinterpret_cast<float(*)[32]>(sm.spare);  // [kSoftWarps][32]
+    // Row groups: 256 threads each (rows 0..31, 32..63 of the CTA); nothing but the
+    // signals to the issuer passes between them inside a block.
+    const uint32_t group_bar = 4 + (quad & 1), pair_bar = 6 + 2 * ch + (quad & 1);
+    // [ch][half] -> 32 rows of the group, in the spare's 4 x (64 rows x 16 bytes)
+    auto red = [&](int c4, int h) -> float& {
+      return *reinterpret_cast<float*>(sm.spare + (c4 >> 1) * 1024 + (quad & 1) * 512 + ((c4 & 1) * 2 + h) * 128 + lane * 4);
+    };
     // of a row's eight values in red[], the same order in each of its threads
     auto row_max = [&]() {
       float m = -INFINITY;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        m = fmaxf(m, fmaxf(red[4 * t + (quad & 1)][lane], red[4 * t + 2 + (quad & 1)][lane]));
+        m = fmaxf(m, fmaxf(red(t, 0), red(t, 1)));
       return m;
     };
-    // bits from s0 on of 112 slot bits
-    auto cut = [&](unsigned long long v0, unsigned long long v1) -> uint32_t {
-      return (uint32_t)(s0 >= 64 ? v1 >> (s0 - 64) : (s0 ? (v0 >> s0) | (v1 << (64 - s0)) : v0));
+    // this thread's bits of 112 slot bits (s0 is a multiple of 8)
+    auto cut = [&](const void* bits) -> uint32_t {
+      const uint8_t* b = static_cast<const uint8_t*>(bits) + (s0 >> 3);
+      return (b[0] | (uint32_t)b[1] << 8) & keep_bits;
     };
+    // Exchange with the lane-pair partner (lane l ^ 64, same ch): half 1 sends the
+    // part's slots 0..15 (4 float4), half 0 the others (4, or 2 for ch odd).  The
+    // first two lie where their reader's own P goes afterwards (16-byte pieces of
+    // its row, swizzled), so that reading and overwriting them needs no barrier;
+    // the others in the rope part of this block's stage (its last reader, the
+    // logits, is done), in the spare, and in pieces 14 and 15 of a P row, which
+    // hold no slots.
+    auto piece = [&](int t) { return (uint32_t)((t >> 3) * (kHC * 128) + hl * 128 + (((t & 7) ^ (hl & 7)) << 4)); };
+    const int p0 = c0 / 8;
+    const uint32_t first0 = piece(p0), first1 = piece(p0 + 1);  // half 0's pieces of P
+    const uint32_t last0 = piece(p0 + 2), last1 = piece((ch & 1) ? 14 + (ch >> 1) : p0 + 3);  // half 1's
+    const uint32_t own0 = half ? last0 : first0, own1 = half ? last1 : first1;
+    const uint32_t his0 = half ? first0 : last0, his1 = half ? first1 : last1;
+    const uint32_t spare_at = (ch >> 1) * 2048 + hl * 16, rope_at = kValue + ch * 1024 + hl * 16, pad_at = piece(14);
     // Every warp executes the same sequence of named barriers whatever happens
     // (after a failed wait it goes on through the segment without work, and
     // the vote at the next one makes all of them stop).
@@ -943,7 +964,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // bad are there, too.
         if (ok) ok = mbar_wait_warp(smem_u32(&sm.s_full), B & 1, c, abort_flag);
         uint32_t lo[16], hi[16];                   // the part's slots 0..15 and 16..31 (ch odd: 16..23)
-        ulonglong2 vv = make_ulonglong2(0ull, 0ull);  // slots of the block that hold a row
+        uint32_t vmask = 0;                        // visible ones of the slots that this thread keeps
 #pragma unroll
         for (int t = 0; t < 16; ++t) hi[t] = 0u;
         if (ok) {
@@ -951,7 +972,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t sbuf = tmem + lane_off + kColS + c0;
           tmem_ld16(sbuf, lo);
           tmem_ld16(sbuf + 16, hi);                // (ch odd: 8 columns of the next part or the query, unused)
-          vv = *reinterpret_cast<const ulonglong2*>(sm.valid[st]);
+          vmask = cut(sm.valid[st]);
           tmem_ld_wait16(lo);
           tmem_ld_also16(hi);
           tc_fence_before();
@@ -961,41 +982,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int t = 0; t < 16; ++t) lo[t] = 0u;
         }
-        // Exchange with the lane-pair partner (lane l ^ 64, same ch): half 1
-        // sends the part's slots 0..15 (4 float4), half 0 the others (4, or 2 for
-        // ch odd).  One float4 of all 256 (ch, row) takes 4 KB; the 28 KB take what
-        // is free now: P buffer pb (half 1's), the rope part of this block's stage
-        // (its last reader, the logits, is done; half 0's first and third), the
-        // spare (second), and the slots 112..127 that the other P buffer's rows do
-        // not use (fourth).
-        auto unit = [&](int q, int from_half) -> float4* {
-          uint8_t* base;
-          if (from_half) base = sm.p[pb] + q * kUnit + (ch * kHC + hl) * 16;
-          else if (q == 0) base = sm.stage[st] + kValue + (ch * kHC + hl) * 16;
-          else if (q == 1) base = sm.spare + (ch * kHC + hl) * 16;
-          else if (q == 2) base = sm.stage[st] + kValue + kUnit + ((ch >> 1) * kHC + hl) * 16;
-          else base = sm.p[pb ^ 1] + kHC * 128 + hl * 128 + (((6 + (ch >> 1)) ^ (hl & 7)) << 4);
-          return reinterpret_cast<float4*>(base);
+        uint8_t *const pbuf = sm.p[pb], *const xs = sm.spare + spare_at, *const xr = sm.stage[st] + rope_at;
+        uint8_t* const xr1 = ch < 3 ? xr + kUnit : sm.p[pb ^ 1] + pad_at;
+        auto put = [&](uint8_t* dst, const uint32_t* v) {
+          *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
         };
         float x[16];
         if (half == 0) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (q < 2 || (ch & 1) == 0)
-              *unit(q, 0) = make_float4(__uint_as_float(hi[4 * q]), __uint_as_float(hi[4 * q + 1]),
-                                        __uint_as_float(hi[4 * q + 2]), __uint_as_float(hi[4 * q + 3]));
+          put(pbuf + his0, hi);
+          put(pbuf + his1, hi + 4);
+          if ((ch & 1) == 0) {
+            put(xs, hi + 8);
+            put(xs + 1024, hi + 12);
+          }
 #pragma unroll
           for (int t = 0; t < 16; ++t) x[t] = __uint_as_float(lo[t]);
         } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *unit(q, 1) = make_float4(__uint_as_float(lo[4 * q]), __uint_as_float(lo[4 * q + 1]),
-                                      __uint_as_float(lo[4 * q + 2]), __uint_as_float(lo[4 * q + 3]));
+          put(pbuf + his0, lo);
+          put(pbuf + his1, lo + 4);
+          put(xr, lo + 8);
+          put(xr1, lo + 12);
 #pragma unroll
           for (int t = 0; t < 16; ++t) x[t] = __uint_as_float(hi[t]);
         }
-        // visible slots of the kept range
-        uint32_t vmask = cut(vv.x, vv.y) & keep_bits;
         if (j >= g.nc) {
           const int first = (j - g.nc) * kBlk + s0;
           if (a.mask == nullptr) {
@@ -1008,19 +1017,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (sh && w + 1 < a.mask_words) m |= __ldg(mrow + w + 1) << (64 - sh);
             vmask &= (uint32_t)m;
           }
-          const unsigned long long b0 = sm.bad[st][0], b1 = sm.bad[st][1], b2 = sm.bad[st][2], b3 = sm.bad[st][3];
-          if (vmask & cut(b0 | (b1 << 32), b2 | (b3 << 32))) poison = true;
+          if (vmask & cut(sm.bad[st])) poison = true;
         }
-        named_bar_sync(1, kSoftThreads);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (4 * q < kept) {
-            const float4 pr = half == 0 ? *unit(q, 1) : *unit(q, 0);
-            x[4 * q] += pr.x;
-            x[4 * q + 1] += pr.y;
-            x[4 * q + 2] += pr.z;
-            x[4 * q + 3] += pr.w;
-          }
+        named_bar_sync(pair_bar, 64);
+        auto add = [&](int t, const uint8_t* src) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          x[t] += v.x;
+          x[t + 1] += v.y;
+          x[t + 2] += v.z;
+          x[t + 3] += v.w;
+        };
+        add(0, pbuf + own0);
+        add(4, pbuf + own1);
+        if (kept == 16) {
+          add(8, half ? xs : xr);
+          add(12, half ? xs + 1024 : xr1);
         }
         if (vmask != keep_bits || kept != 16) {
 #pragma unroll
@@ -1056,14 +1067,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           lsum_blk += other;
         };
+        auto store_p = [&]() {
+          put(pbuf + own0, pk);
+          if (kept == 16) put(pbuf + own1, pk + 4);
+          fence_proxy_async_smem();
+        };
         weights();
-        // (this barrier also ends the reads of the exchange units)
-        if (named_bar_or(3, kSoftThreads, bm > m_run + kRescaleThreshold)) {
+        store_p();
+        // (this barrier also ends the reads of the exchange, before the next block's)
+        if (named_bar_or(group_bar, kSoftThreads / 2, bm > m_run + kRescaleThreshold)) {
           // the row's block max over its eight threads (lane pair x column parts)
-          red[ws][lane] = bm;
-          named_bar_sync(1, kSoftThreads);
+          red(ch, half) = bm;
+          named_bar_sync(group_bar, kSoftThreads / 2);
           bm = row_max();
-          named_bar_sync(1, kSoftThreads);         // red makes room for the next exchange
+          named_bar_sync(group_bar, kSoftThreads / 2);  // red makes room for the next exchange
           const bool need = bm > m_run + kRescaleThreshold;
           if (ok && __any_sync(0xffffffffu, need)) {
             const float m_new = need ? bm : m_run;
@@ -1089,20 +1106,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             l_run *= alpha;
             m_run = m_new;
             weights();
+            store_p();
           }
         }
         if (!ok) continue;
         l_run += lsum_blk;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (8 * q < kept) {
-            const int sl = s0 + 8 * q;
-            uint8_t* prow = sm.p[pb] + (sl >> 6) * (kHC * 128) + hl * 128;
-            *reinterpret_cast<uint4*>(prow + ((((sl & 63) >> 3) ^ (hl & 7)) << 4)) =
-                make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
-          }
-        }
-        fence_proxy_async_smem();
         __syncwarp();
         signal(&sm.p_full[pb]);
       }
@@ -1111,13 +1119,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_after();
       if (poison) l_run = NAN;
       named_bar_sync(1, kSoftThreads);
-      red[ws][lane] = l_run;
+      red(ch, half) = l_run;
       named_bar_sync(1, kSoftThreads);
       float lsum = 0.f;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) lsum += red[4 * t + (quad & 1)][lane] + red[4 * t + 2 + (quad & 1)][lane];
+      for (int t = 0; t < 4; ++t) lsum += red(t, 0) + red(t, 1);
       named_bar_sync(1, kSoftThreads);
-      red[ws][lane] = m_own;
+      red(ch, half) = m_own;
       const bool all_ok = named_bar_or(2, kSoftThreads, !ok) == false;
       const float m_true = row_max();
       if (!all_ok) {
