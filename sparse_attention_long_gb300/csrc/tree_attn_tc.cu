@@ -109,7 +109,8 @@ struct __align__(1024) Smem {
   Seg seg[2];
   alignas(16) unsigned long long valid[kStages][2];            // slots that hold a row
   uint32_t bad[kStages][kFixWarps];                // 32 slots each: zeroed for an infinity or NaN
-  alignas(4) uint8_t live[kStages][kFixWarps];                // 2 steps of 16 slots each: some token sees some slot
+  uint8_t plain[kStages];                          // the block needs no fix
+  alignas(4) uint8_t live[kStages][kFixWarps];     // 2 steps of 16 slots each: some token sees some slot
   alignas(16) uint8_t spare[kUnit];                // of the logit exchange; row maxima and sums between exchanges
   uint32_t sink[kSoftWarps];                       // targets of CTA 1's signalling stores
   uint32_t sink_f[2][kFixWarps];
@@ -242,6 +243,25 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* tm,
       "l"(tm), "r"(x0), "r"(x1), "r"(x2), "r"(x3), "r"(x4), "r"(bar)
       : "memory");
 }
+// the same, into this CTA, completing on a barrier of either CTA of the pair (cluster address)
+__device__ __forceinline__ void tma_load2_3d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(tm), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load2_5d(uint32_t dst, const CUtensorMap* tm, int x0, int x1, int x2, int x3,
+                                             int x4, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(tm), "r"(x0), "r"(x1), "r"(x2), "r"(x3), "r"(x4), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
 __device__ __forceinline__ void st_zero16(uint32_t addr) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
 }
@@ -331,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 32 * kWarpFix0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&sm.st_full[i]), kLoadWarps);
-      mbar_init(smem_u32(&sm.st_empty[i]), 1);
+      mbar_init(smem_u32(&sm.st_empty[i]), 1 + kFixWarps);  // the last MMAs, and the fix warps
       mbar_init(smem_u32(&sm.ready[i]), kFixWarps);
     }
     mbar_init(smem_u32(&sm.s_full), 1);
@@ -484,7 +504,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // (`wide`: pages of a multiple of 32 rows).  A drafted group starts at any
     // row: value copies of 8 rows.
     const bool rope = warp != kWarpLoad;
-    int G = 0;                                     // blocks so far
+    int G = 0;                                     // ring slots so far
+    uint32_t ready_par = 0, direct = 0;            // a bit per stage: phase of its `ready`, last use plain
     bool ok = true;
     for (int i = 0; ok; ++i) {
       if (!mbar_wait_warp(smem_u32(&sm.sc_full[i & 1]), (i >> 1) & 1, c, abort_flag)) break;
@@ -510,6 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
+        direct &= ~(1u << st);
         ++G;
       }
       for (int j = g.j0; j < g.j1; ++j, ++G) {
@@ -553,23 +575,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
+          // A block without an empty slot is plain: its copies complete on the
+          // issuer's barrier, past the fix warps (450 cycles, and the signals from
+          // the other CTA another 500)
+          const bool plain = last == 16;
           if (lane == 0) {
+            const uint32_t full = plain ? mapa_shared(smem_u32(&sm.ready[st]), 0) : mapa_shared(bar, crank);
             if (rope) {
-              mbar_arrive_expect_tx(bar, kRope);
+              if (plain) mbar_arrive(bar);
+              else mbar_arrive_expect_tx(bar, kRope);
               const int col = kDV + 32 * (int)crank;
 #pragma unroll
-              for (int t = 0; t < 3; ++t) tma_load_3d(d0 + t * 2048, &tm_page_r2, col, gx[t], gp[t], bar);
-              tma_load_3d(d3, &tm_page_r, col, gx[3], gp[3], bar);
+              for (int t = 0; t < 3; ++t) tma_load2_3d(d0 + t * 2048, &tm_page_r2, col, gx[t], gp[t], full);
+              tma_load2_3d(d3, &tm_page_r, col, gx[3], gp[3], full);
             } else {
               sm.valid[st][0] = ~0ull;
               sm.valid[st][1] = 0xFFFFFFFFull | ((unsigned long long)((1u << last) - 1u) << 32);
-              mbar_arrive_expect_tx(bar, kValue);
+              sm.plain[st] = plain;
+              if (plain) {
+                *reinterpret_cast<uint32_t*>(sm.live[st]) = 0x01030303u;
+                mbar_arrive(bar);
+                if (crank == 0) {                  // in the fix warps' stead, for the copies of both CTAs
+                  const uint32_t rd = smem_u32(&sm.ready[st]);
+                  mbar_arrive_expect_tx(rd, 2 * kStageBytes);
+                  mbar_arrive_n(rd, kFixWarps - 1);
+                }
+              } else {
+                mbar_arrive_expect_tx(bar, kValue);
+              }
 #pragma unroll
               for (int t = 0; t < 3; ++t)
-                tma_load_5d(d0 + t * 4 * kOct, &tm_page_v2, 0, 0, 4 * (int)crank, gx[t] >> 3, gp[t], bar);
-              tma_load_5d(d3, &tm_page_v, 0, 0, 4 * (int)crank, gx[3] >> 3, gp[3], bar);
+                tma_load2_5d(d0 + t * 4 * kOct, &tm_page_v2, 0, 0, 4 * (int)crank, gx[t] >> 3, gp[t], full);
+              tma_load2_5d(d3, &tm_page_v, 0, 0, 4 * (int)crank, gx[3] >> 3, gp[3], full);
             }
           }
+          direct = plain ? direct | (1u << st) : direct & ~(1u << st);
+          ready_par ^= 1u << st;
           __syncwarp();
           continue;
         }
@@ -584,6 +625,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
+        direct &= ~(1u << st);
+        ready_par ^= 1u << st;
         // the second group of a pair goes with the first
         uint32_t first = loaded, pairs = 0;
         if (wide && !drafted) {
@@ -594,6 +637,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!rope) {
             sm.valid[st][0] = v0;
             sm.valid[st][1] = v1;
+            sm.plain[st] = 0;
           }
           // a pair brings both its groups, the second past the last row or not
           const int left = g.T - (j - g.nc) * kBlk, n8 = ((left < kBlk ? left : kBlk) + 7) / 8;
@@ -628,8 +672,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     // no copy may still be in flight when the CTA exits (bounded, whatever the others do)
-    for (int k = G - kStages < 0 ? 0 : G - kStages; k < G; ++k)
-      mbar_wait_warp(smem_u32(&sm.st_full[k % kStages]), (k / kStages) & 1, c, &sm.no_abort);
+    for (int k = G - kStages < 0 ? 0 : G - kStages; k < G; ++k) {
+      const int st = k % kStages;
+      mbar_wait_warp(smem_u32(&sm.st_full[st]), (k / kStages) & 1, c, &sm.no_abort);
+      // (CTA 1's plain copies, too: it does not exit before CTA 0)
+      if (crank == 0 && ((direct >> st) & 1u))
+        mbar_wait_warp(smem_u32(&sm.ready[st]), ((ready_par >> st) & 1u) ^ 1u, c, &sm.no_abort);
+    }
   } else if (warp >= kWarpFix0 && warp < kWarpSoft0) {
     // ------------------------- key stages passed on -------------------------
     const int fw = warp - kWarpFix0;
@@ -683,6 +732,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
+          mbar_arrive(smem_u32(&sm.st_empty[st]));
           const uint32_t bar = smem_u32(&sm.q_tm[i & 1]);
           if (crank == 0) {
             if (fw == 0) mbar_arrive_expect_tx(bar, 4 * kFixWarps);
@@ -725,6 +775,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!mbar_wait_warp(smem_u32(&sm.st_full[st]), (G / kStages) & 1, c, abort_flag)) {
           ok = false;
           break;
+        }
+        if (sm.plain[st]) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.st_empty[st]));
+          continue;
         }
         const uint32_t valid = (uint32_t)(sm.valid[st][fw >> 1] >> (32 * (fw & 1))) & kAll;
         const uint32_t seen = valid & any;
@@ -769,6 +824,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) {
+          mbar_arrive(smem_u32(&sm.st_empty[st]));
           const uint32_t bar = smem_u32(&sm.ready[st]);
           if (crank == 0) {
             if (fw == 0) mbar_arrive_expect_tx(bar, 4 * kFixWarps);
