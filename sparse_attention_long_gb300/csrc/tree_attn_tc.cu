@@ -48,10 +48,10 @@
 // have read the old query (per-row loads of the softmax warps took 4,200 cycles
 // between two tiles).
 //
-// Roles per CTA: warp 0 = TMEM allocation, MMA issuer (CTA 0); warps 1..4 =
-// query into TMEM, passing on of each key stage (with the zeroing above); warps
-// 5..20 = softmax and epilogue; warp 21 = schedule; warps 22, 23 = key loads
-// (value columns and query; rope columns).
+// Roles per CTA: warp 0 = TMEM allocation, MMA issuer of the logits (CTA 0);
+// warps 1..4 = query into TMEM, passing on of key stages (with the zeroing
+// above); warps 5..20 = softmax and epilogue; warp 21 = MMA issuer of P V (CTA
+// 0); warps 22, 23 = loads (value columns and query; rope columns and schedule).
 #include <math.h>
 #include <stddef.h>
 
@@ -74,7 +74,7 @@ constexpr int kQTile = kHC * 128, kQTiles = 7;     // query through a stage: til
 constexpr int kUnit = 4 * kHC * 16;                // one float4 of every (column part, row): exchange unit
 constexpr int kFixWarps = 4, kSoftWarps = 16, kLoadWarps = 2, kSoftThreads = 32 * kSoftWarps;
 constexpr int kWarpFix0 = 1, kWarpSoft0 = kWarpFix0 + kFixWarps;
-constexpr int kWarpScan = kWarpSoft0 + kSoftWarps, kWarpLoad = kWarpScan + 1;
+constexpr int kWarpPv = kWarpSoft0 + kSoftWarps, kWarpLoad = kWarpPv + 1;
 constexpr int kThreads = 32 * (kWarpLoad + kLoadWarps);
 static_assert(kQTiles * kQTile <= kStageBytes, "the query's slot");
 static_assert(kBlk <= 32 * kFixWarps && kBlk % 16 == 0, "a fix warp takes two 16-slot steps");
@@ -116,7 +116,7 @@ struct __align__(1024) Smem {
   uint32_t sink_f[2][kFixWarps];
   uint64_t st_full[kStages], st_empty[kStages], ready[kStages];
   uint64_t s_full, s_free, p_full[2];
-  uint64_t q_tm[2], q_free[2], mma_done[2], sc_full[2], sc_empty[2], fin;
+  uint64_t q_tm[2], q_free[2], mma_done[2], sc_full[2], sc_empty[2], fin[2];
   uint32_t tmem_base;
   int abort, no_abort;
 };
@@ -200,16 +200,6 @@ __device__ __forceinline__ void commit2(uint32_t bar) {
       "h"((uint16_t)3)
       : "memory");
 }
-__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // true if any of the `n` threads of named barrier `id` passed true
 __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t n, bool v) {
   uint32_t r;
@@ -277,11 +267,6 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint4& v) {
                "r"(v.z), "r"(v.w)
                : "memory");
 }
-// hint: bring `bytes` (a multiple of 16) from global memory into L2
-__device__ __forceinline__ void prefetch_l2_bulk(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
 __device__ __forceinline__ long long warp_sum(long long v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -329,6 +314,112 @@ __device__ __forceinline__ long long tiles_cost_warp(const Plan& p, long long r)
   return warp_sum(c) + r * (p.nc + 1);
 }
 
+// A pair's run of the list of all (tile, block): an even share, segment by segment
+// (one warp, the same state in every lane).
+struct Schedule {
+  long long x, x1, run;                            // list positions: next, end; length of every run
+  TreeSeq s;
+  Plan p;
+  int b, tile, j;
+  Join join;                                       // the tile that starts in this run and goes on in the next ones
+
+  __device__ __forceinline__ void start(const TreeArgs& a, int pair, int npairs, const DevCtx& c) {
+    const int lane = threadIdx.x & 31;
+    bool wrong = false;
+    long long total = 0;
+    for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
+      if (b0 + lane < a.n_seqs) {
+        const Plan q = make_plan(a, tree_seq(a, b0 + lane, &wrong));
+        total += tiles_cost(q, q.tiles);
+      }
+    }
+    total = warp_sum(total);
+    if (__any_sync(0xffffffffu, wrong) && lane == 0) set_status(c, DSA_ERR_INDEX);
+    run = (total + npairs - 1) / npairs;
+    x = run * pair;
+    x1 = x + run < total ? x + run : total;
+    join = {0, 0, 0};
+    if (x >= x1) return;
+    // the sequence, tile and block where this pair's run starts
+    b = 0;
+    long long off = x;
+    for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
+      long long cost = 0;
+      if (b0 + lane < a.n_seqs) {
+        const Plan q = make_plan(a, tree_seq(a, b0 + lane, &wrong));
+        cost = tiles_cost(q, q.tiles);
+      }
+      long long incl = cost;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, incl > off);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        off -= __shfl_sync(0xffffffffu, incl - cost, l);
+        b = b0 + l;
+        break;
+      }
+      off -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    s = tree_seq(a, b, &wrong);
+    p = make_plan(a, s);
+    if (!p.chain) {
+      tile = (int)(off / (p.nc + p.nd));
+      j = (int)(off % (p.nc + p.nd));
+    } else {
+      int lo = 0, hi = p.tiles;                    // cost(lo) <= off < cost(hi)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (tiles_cost_warp(p, mid) <= off) lo = mid;
+        else hi = mid;
+      }
+      tile = lo;
+      j = (int)(off - tiles_cost_warp(p, lo));
+    }
+  }
+
+  __device__ __forceinline__ Seg next(const TreeArgs& a, int pair) {
+    Seg g;
+    g.end = x >= x1;
+    if (g.end) return g;
+    if (tile == p.tiles) {                         // on to the next sequence with tokens (there is one: x < x1)
+      bool wrong = false;
+      do {
+        ++b;
+        s = tree_seq(a, b, &wrong);
+      } while (s.T == 0);
+      p = make_plan(a, s);
+      tile = 0;
+    }
+    const int nb = tile_blocks(p, tile);
+    const long long left = x1 - x;
+    const int j1 = nb - j < left ? nb : (int)(j + left);
+    const bool whole = j == 0 && j1 == nb;
+    g.b = b;
+    g.tile = tile;
+    g.j0 = j;
+    g.j1 = j1;
+    g.nc = p.nc;
+    g.len = s.len;
+    g.t0 = s.t0;
+    g.T = s.T;
+    g.part = whole ? -1 : 2 * pair + (j == 0 ? 1 : 0);
+    if (!whole && j == 0) {
+      const long long rows = (long long)s.T * a.H - 128ll * tile;
+      join.row0 = (long long)s.t0 * a.H + 128ll * tile;
+      join.nrows = rows < kTile ? (int)rows : kTile;
+      join.nparts = (int)((x + nb - 1) / run) - pair + 1;
+    }
+    x += j1 - j;
+    j = 0;
+    ++tile;
+    return g;
+  }
+};
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tree_attn_tc_kernel(TreeArgs a, const __nv_bfloat16* __restrict__ qg, const __nv_bfloat16* __restrict__ kvn,
                         __nv_bfloat16* __restrict__ out, float* __restrict__ mx, float* __restrict__ sm_out,
@@ -359,15 +450,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // of them also expecting the 4 bytes that each of CTA 1's warps stores
     mbar_init(smem_u32(&sm.s_free), kSoftWarps);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sm.p_full[i]), kSoftWarps);
+      mbar_init(smem_u32(&sm.p_full[i]), 2);       // (row groups)
       mbar_init(smem_u32(&sm.q_tm[i]), kFixWarps);
       mbar_init(smem_u32(&sm.q_free[i]), 1);
       mbar_init(smem_u32(&sm.mma_done[i]), 1);
       mbar_init(smem_u32(&sm.sc_full[i]), 1);
-      // readers of a segment: fix, softmax and load warps, and CTA 0's issuer
-      mbar_init(smem_u32(&sm.sc_empty[i]), kFixWarps + kSoftWarps + kLoadWarps + (crank == 0 ? 1 : 0));
+      // readers of a segment: fix and softmax warps, value loads, and CTA 0's issuers
+      mbar_init(smem_u32(&sm.sc_empty[i]), kFixWarps + kSoftWarps + 1 + (crank == 0 ? 2 : 0));
+      mbar_init(smem_u32(&sm.fin[i]), 1);
     }
-    mbar_init(smem_u32(&sm.fin), 1);
     sm.abort = 0;
     sm.no_abort = 0;
     fence_mbar_init();
@@ -384,121 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   let_next_launch();
   wait_for_earlier();
 
-  if (warp == kWarpScan) {
-    // ------------------------------- schedule -------------------------------
-    bool wrong = false;
-    long long total = 0;
-    for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
-      if (b0 + lane < a.n_seqs) {
-        const Plan p = make_plan(a, tree_seq(a, b0 + lane, &wrong));
-        total += tiles_cost(p, p.tiles);
-      }
-    }
-    total = warp_sum(total);
-    if (__any_sync(0xffffffffu, wrong) && lane == 0) set_status(c, DSA_ERR_INDEX);
-    const long long run = (total + npairs - 1) / npairs;
-    long long x = run * pair;
-    const long long x1 = x + run < total ? x + run : total;
-    int i = 0;                                     // segments so far
-    bool ok = true;
-    Join join = {0, 0, 0};
-    if (x < x1) {
-      // the sequence, tile and block where this pair's run starts
-      int b = 0;
-      long long off = x;
-      for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
-        long long cost = 0;
-        if (b0 + lane < a.n_seqs) {
-          const Plan p = make_plan(a, tree_seq(a, b0 + lane, &wrong));
-          cost = tiles_cost(p, p.tiles);
-        }
-        long long incl = cost;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const long long y = __shfl_up_sync(0xffffffffu, incl, d);
-          if (lane >= d) incl += y;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, incl > off);
-        if (past) {
-          const int l = __ffs(past) - 1;
-          off -= __shfl_sync(0xffffffffu, incl - cost, l);
-          b = b0 + l;
-          break;
-        }
-        off -= __shfl_sync(0xffffffffu, incl, 31);
-      }
-      TreeSeq s = tree_seq(a, b, &wrong);
-      Plan p = make_plan(a, s);
-      int tile, j;
-      if (!p.chain) {
-        tile = (int)(off / (p.nc + p.nd));
-        j = (int)(off % (p.nc + p.nd));
-      } else {
-        int lo = 0, hi = p.tiles;                  // cost(lo) <= off < cost(hi)
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (tiles_cost_warp(p, mid) <= off) lo = mid;
-          else hi = mid;
-        }
-        tile = lo;
-        j = (int)(off - tiles_cost_warp(p, lo));
-      }
-      while (x < x1) {
-        const int nb = tile_blocks(p, tile);
-        const long long left = x1 - x;
-        const int j1 = nb - j < left ? nb : (int)(j + left);
-        if (!mbar_wait_warp(smem_u32(&sm.sc_empty[i & 1]), ((i >> 1) & 1) ^ 1, c, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const bool whole = j == 0 && j1 == nb;
-        if (lane == 0) {
-          Seg g;
-          g.b = b;
-          g.tile = tile;
-          g.j0 = j;
-          g.j1 = j1;
-          g.nc = p.nc;
-          g.len = s.len;
-          g.t0 = s.t0;
-          g.T = s.T;
-          g.part = whole ? -1 : 2 * pair + (j == 0 ? 1 : 0);
-          g.end = 0;
-          sm.seg[i & 1] = g;
-          mbar_arrive(smem_u32(&sm.sc_full[i & 1]));
-        }
-        __syncwarp();
-        const long long rows = (long long)s.T * a.H - 128ll * tile;
-        const long long row0 = (long long)s.t0 * a.H + 128ll * tile;
-        {                                          // this CTA's 64 query rows, into L2 ahead of their load
-          const long long mine = rows - kHC * (int)crank < kHC ? rows - kHC * (int)crank : kHC;
-          if (lane == 0 && mine > 0)
-            prefetch_l2_bulk(qg + (row0 + kHC * (int)crank) * kDQK, (uint32_t)mine * kDQK * 2);
-        }
-        if (!whole && j == 0) {                    // the tile starts here and goes on in the next runs
-          join.row0 = row0;
-          join.nrows = rows < kTile ? (int)rows : kTile;
-          join.nparts = (int)((x + nb - 1) / run) - pair + 1;
-        }
-        ++i;
-        x += j1 - j;
-        j = 0;
-        if (++tile == p.tiles && x < x1) {
-          do {
-            ++b;
-            s = tree_seq(a, b, &wrong);
-          } while (s.T == 0);
-          p = make_plan(a, s);
-          tile = 0;
-        }
-      }
-    }
-    if (crank == 0 && lane == 0) joins[pair] = join;
-    if (ok && mbar_wait_warp(smem_u32(&sm.sc_empty[i & 1]), ((i >> 1) & 1) ^ 1, c, abort_flag) && lane == 0) {
-      sm.seg[i & 1].end = 1;
-      mbar_arrive(smem_u32(&sm.sc_full[i & 1]));
-    }
-  } else if (warp >= kWarpLoad) {
+  if (warp >= kWarpLoad) {
     // ------------------------------- key loads -------------------------------
     // Groups of 16 slots; one copy takes two of them where they lie in one page
     // (`wide`: pages of a multiple of 32 rows).  A drafted group starts at any
@@ -507,11 +484,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int G = 0;                                     // ring slots so far
     uint32_t ready_par = 0, direct = 0;            // a bit per stage: phase of its `ready`, last use plain
     bool ok = true;
+    Schedule sched;                                // the rope warp's
+    if (rope) sched.start(a, pair, npairs, c);
     for (int i = 0; ok; ++i) {
-      if (!mbar_wait_warp(smem_u32(&sm.sc_full[i & 1]), (i >> 1) & 1, c, abort_flag)) break;
-      const Seg g = sm.seg[i & 1];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[i & 1]));
+      Seg g;
+      if (rope) {
+        // makes the segment out for everyone, once the last but one is read
+        if (!mbar_wait_warp(smem_u32(&sm.sc_empty[i & 1]), ((i >> 1) & 1) ^ 1, c, abort_flag)) break;
+        g = sched.next(a, pair);
+        if (lane == 0) {
+          sm.seg[i & 1] = g;
+          mbar_arrive(smem_u32(&sm.sc_full[i & 1]));
+        }
+        __syncwarp();
+      } else {
+        if (!mbar_wait_warp(smem_u32(&sm.sc_full[i & 1]), (i >> 1) & 1, c, abort_flag)) break;
+        g = sm.seg[i & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[i & 1]));
+      }
       if (g.end) break;
       const int32_t* trow = a.table + (long long)g.b * a.max_pages;
       {
@@ -671,6 +662,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
+    if (rope && crank == 0 && lane == 0) joins[pair] = sched.join;
     // no copy may still be in flight when the CTA exits (bounded, whatever the others do)
     for (int k = G - kStages < 0 ? 0 : G - kStages; k < G; ++k) {
       const int st = k % kStages;
@@ -837,12 +829,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 0) {
     if (crank == 0 && lane == 0) {
-      // ------------------------------- MMA issuer -------------------------------
-      // Whichever is ready, the logits S(G) of the next block first once PV(G-2)
-      // is issued (the softmax of block G exchanges logits through that P
-      // buffer); no progress for the wait budget is a timeout.
-      int Gs = 0, Gp = 0;                          // blocks so far: logits issued / PVs issued
-      uint32_t ss = 0, sp = 0;                     // their stages
+      // -------------------------- MMA issuer: logits --------------------------
+      // Two issuers: a thread's barrier tests wait behind its own queued MMAs (some
+      // 430 cycles), so while the MMAs of one run, the other has its answers.
+      int G = 0;                                   // blocks so far
+      uint32_t st = 0, slot = 0;                   // stage, ring slot
       uint32_t ready_par = 0;                      // parity of each stage's next `ready` phase, a bit each
       bool ok = true;
       for (int i = 0; ok; ++i) {
@@ -853,85 +844,87 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (end) break;
         if (!mbar_wait<true>(smem_u32(&sm.q_tm[bi]), (i >> 1) & 1, c, abort_flag)) break;
         tc_fence_after();
-        int js = 0, jp = 0;
-        commit2(smem_u32(&sm.st_empty[0]) + 8 * ss);  // the query's slot is free
-        if (++ss == kStages) ss = 0;
-        if (++sp == kStages) sp = 0;
-        uint64_t t_idle = 0;
-        uint32_t spins = 0;
-        while (ok && jp < nblk) {
-          bool progressed = false;
-          if (js < nblk && js <= jp + 1 && (Gs == 0 || mbar_poll(smem_u32(&sm.s_free), (Gs - 1) & 1)) &&
-              mbar_poll(smem_u32(&sm.ready[0]) + 8 * ss, (ready_par >> ss) & 1u)) {
-            tc_fence_after();
-            const uint32_t sb = smem_u32(sm.stage[0]) + ss * kStageBytes;
-            const uint32_t v = desc_lo(sb, 16), r = desc_lo(sb + kValue, 16);
+        commit2(smem_u32(&sm.st_empty[0]) + 8 * st);  // the query's slot is free
+        if (++st == kStages) st = 0;
+        ++slot;
+        for (int j = 0; j < nblk; ++j, ++G, ++slot) {
+          // the keys; the last logits read; PV(G-2) done, whose P buffer the softmax
+          // of this block exchanges logits through (with the tile before: mma_done)
+          ok = mbar_wait(smem_u32(&sm.ready[0]) + 8 * st, (ready_par >> st) & 1u, c, abort_flag) &&
+               (G == 0 || mbar_wait(smem_u32(&sm.s_free), (G - 1) & 1, c, abort_flag)) &&
+               (j < 2 || mbar_wait(smem_u32(&sm.st_empty[0]) + 8 * ((slot - 2) % kStages), ((slot - 2) / kStages) & 1, c,
+                                   abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sb = smem_u32(sm.stage[0]) + st * kStageBytes;
+          const uint32_t v = desc_lo(sb, 16), r = desc_lo(sb + kValue, 16);
 #pragma unroll
-            for (int kk = 0; kk < 16; ++kk)
-              mma2_ts(tmem + kColS, tmem + kColQ + kk * 8, v + ((kk >> 2) * kAtom + (kk & 3) * 32) / 16,
-                      desc_hi(kOct, kSw128), kIdescS, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < 16; ++kk)
+            mma2_ts(tmem + kColS, tmem + kColQ + kk * 8, v + ((kk >> 2) * kAtom + (kk & 3) * 32) / 16,
+                    desc_hi(kOct, kSw128), kIdescS, kk > 0 ? 1u : 0u);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              mma2_ts(tmem + kColS, tmem + kColQ + 128 + k * 8, r + 2 * k, desc_hi(512, kSw64), kIdescS, 1u);
-            commit2(smem_u32(&sm.s_full));
-            ++js;
-            ++Gs;
-            ready_par ^= 1u << ss;
-            if (++ss == kStages) ss = 0;
-            if (js == nblk) commit2(smem_u32(&sm.q_free[bi]));
-            progressed = true;
-          } else if (jp < js && mbar_poll(smem_u32(&sm.p_full[Gp & 1]), (Gp >> 1) & 1)) {
-            tc_fence_after();
-            const uint32_t sb = smem_u32(sm.stage[0]) + sp * kStageBytes;
-            const uint32_t v = desc_lo(sb, kAtom), p = desc_lo(smem_u32(sm.p[0]) + (Gp & 1) * kPBytes, 16);
-            // the 16-slot steps that some token sees (2 bits per byte); one at least
-            const uint32_t lv = *reinterpret_cast<const uint32_t*>(sm.live[sp]);
-            uint32_t steps = (lv & 3u) | ((lv >> 6) & 12u) | ((lv >> 12) & 48u) | ((lv >> 18) & 192u);
-            uint32_t acc = jp > 0;
-            if (steps == 0x7fu) {
-#pragma unroll
-              for (int kk = 0; kk < kPvSteps; ++kk) {
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-                  mma2_ss(tmem + kColO + 128 * m, p + ((kk >> 2) * (kHC * 128) + (kk & 3) * 32) / 16,
-                          desc_hi(1024, kSw128), v + (2 * m * kAtom + kk * 2 * kOct) / 16, desc_hi(kOct, kSw128),
-                          kIdescPV, kk > 0 ? 1u : acc);
-              }
-            } else {
-              if (steps == 0) steps = 1;
-#pragma unroll 1
-              for (; steps; steps &= steps - 1, acc = 1) {
-                const int kk = __ffs(steps) - 1;
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-                  mma2_ss(tmem + kColO + 128 * m, p + ((kk >> 2) * (kHC * 128) + (kk & 3) * 32) / 16,
-                          desc_hi(1024, kSw128), v + (2 * m * kAtom + kk * 2 * kOct) / 16, desc_hi(kOct, kSw128),
-                          kIdescPV, acc);
-              }
-            }
-            commit2(smem_u32(&sm.st_empty[0]) + 8 * sp);
-            if (++sp == kStages) sp = 0;
-            ++jp;
-            ++Gp;
-            progressed = true;
-          }
-          if (progressed) {
-            spins = 0;
-          } else if ((++spins & 63u) == 0) {
-            const uint64_t now = globaltimer();
-            if (spins == 64) t_idle = now;
-            if (*abort_flag) ok = false;
-            else if (now - t_idle > c.budget) {
-              set_status(c, DSA_ERR_TIMEOUT);
-              *abort_flag = 1;
-              ok = false;
-            }
-          }
+          for (int k = 0; k < 2; ++k)
+            mma2_ts(tmem + kColS, tmem + kColQ + 128 + k * 8, r + 2 * k, desc_hi(512, kSw64), kIdescS, 1u);
+          commit2(smem_u32(&sm.s_full));
+          ready_par ^= 1u << st;
+          if (++st == kStages) st = 0;
         }
-        commit2(smem_u32(&sm.mma_done[bi]));       // this segment's O complete
+        if (ok) commit2(smem_u32(&sm.q_free[bi]));
       }
-      commit2(smem_u32(&sm.fin));
-      mbar_wait(smem_u32(&sm.fin), 0, c, &sm.no_abort);
+      commit2(smem_u32(&sm.fin[0]));
+      mbar_wait(smem_u32(&sm.fin[0]), 0, c, &sm.no_abort);
+    }
+  } else if (warp == kWarpPv) {
+    if (crank == 0 && lane == 0) {
+      // --------------------------- MMA issuer: O += P V ---------------------------
+      int G = 0;
+      uint32_t st = 0;
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        const int bi = i & 1;
+        if (!mbar_wait(smem_u32(&sm.sc_full[bi]), (i >> 1) & 1, c, abort_flag)) break;
+        const int nblk = sm.seg[bi].j1 - sm.seg[bi].j0, end = sm.seg[bi].end;
+        mbar_arrive(smem_u32(&sm.sc_empty[bi]));
+        if (end) break;
+        if (++st == kStages) st = 0;               // the query's slot
+        for (int j = 0; j < nblk; ++j, ++G) {
+          ok = mbar_wait(smem_u32(&sm.p_full[G & 1]), (G >> 1) & 1, c, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sb = smem_u32(sm.stage[0]) + st * kStageBytes;
+          const uint32_t v = desc_lo(sb, kAtom), p = desc_lo(smem_u32(sm.p[0]) + (G & 1) * kPBytes, 16);
+          // the 16-slot steps that some token sees (2 bits per byte); one at least
+          const uint32_t lv = *reinterpret_cast<const volatile uint32_t*>(sm.live[st]);
+          uint32_t steps = (lv & 3u) | ((lv >> 6) & 12u) | ((lv >> 12) & 48u) | ((lv >> 18) & 192u);
+          uint32_t acc = j > 0;
+          if (steps == 0x7fu) {
+#pragma unroll
+            for (int kk = 0; kk < kPvSteps; ++kk) {
+#pragma unroll
+              for (int m = 0; m < 2; ++m)
+                mma2_ss(tmem + kColO + 128 * m, p + ((kk >> 2) * (kHC * 128) + (kk & 3) * 32) / 16,
+                        desc_hi(1024, kSw128), v + (2 * m * kAtom + kk * 2 * kOct) / 16, desc_hi(kOct, kSw128),
+                        kIdescPV, kk > 0 ? 1u : acc);
+            }
+          } else {
+            if (steps == 0) steps = 1;
+#pragma unroll 1
+            for (; steps; steps &= steps - 1, acc = 1) {
+              const int kk = __ffs(steps) - 1;
+#pragma unroll
+              for (int m = 0; m < 2; ++m)
+                mma2_ss(tmem + kColO + 128 * m, p + ((kk >> 2) * (kHC * 128) + (kk & 3) * 32) / 16,
+                        desc_hi(1024, kSw128), v + (2 * m * kAtom + kk * 2 * kOct) / 16, desc_hi(kOct, kSw128),
+                        kIdescPV, acc);
+            }
+          }
+          commit2(smem_u32(&sm.st_empty[0]) + 8 * st);
+          if (++st == kStages) st = 0;
+        }
+        if (ok) commit2(smem_u32(&sm.mma_done[bi]));  // this segment's O complete
+      }
+      commit2(smem_u32(&sm.fin[1]));
+      mbar_wait(smem_u32(&sm.fin[1]), 0, c, &sm.no_abort);
     }
   } else {
     // --------------------------- softmax / epilogue ---------------------------
@@ -949,10 +942,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int kept = half && (ch & 1) ? 8 : 16;
     const int s0 = c0 + 16 * half;
     const uint32_t keep_bits = (1u << kept) - 1u;
-    auto signal = [&](uint64_t* bar) {
+    auto signal = [&](uint64_t* bar, bool first, int n) {  // n signals of each CTA, this one `first`
       if (lane == 0) {
         if (crank == 0) {
-          if (warp == kWarpSoft0) mbar_arrive_expect_tx(smem_u32(bar), 4 * kSoftWarps);
+          if (first) mbar_arrive_expect_tx(smem_u32(bar), 4 * n);
           else mbar_arrive(smem_u32(bar));
         } else {
           st_async_signal(mapa_shared(smem_u32(&sm.sink[ws]), 0), mapa_shared(smem_u32(bar), 0));
@@ -1014,10 +1007,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ++G;                                         // the query's slot
       for (int j = g.j0; j < g.j1; ++j, ++G, ++B) {
         const int pb = B & 1, st = G % kStages;
-        // One wait: the logits' commit completes after every MMA issued before it,
-        // PV(G-2) among them, so P buffer pb is free as well; and the issuer took
-        // this block after the load and fix warps had passed it on, so valid and
-        // bad are there, too.
+        // One wait: the issuer of the logits took this block after PV(G-2), so P
+        // buffer pb is free, and after the load and fix warps had passed it on, so
+        // valid and bad are there.
         if (ok) ok = mbar_wait_warp(smem_u32(&sm.s_full), B & 1, c, abort_flag);
         uint32_t lo[16], hi[16];                   // the part's slots 0..15 and 16..31 (ch odd: 16..23)
         uint32_t vmask = 0;                        // visible ones of the slots that this thread keeps
@@ -1033,7 +1025,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tmem_ld_also16(hi);
           tc_fence_before();
           __syncwarp();
-          signal(&sm.s_free);                      // the logit buffer is free
+          signal(&sm.s_free, warp == kWarpSoft0, kSoftWarps);  // the logit buffer is free
         } else {
 #pragma unroll
           for (int t = 0; t < 16; ++t) lo[t] = 0u;
@@ -1144,10 +1136,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (j > g.j0 && __any_sync(0xffffffffu, need && m_run != -INFINITY)) {
               // O must hold PV(G-1) before it is rescaled
               ok = mbar_wait_warp(smem_u32(&sm.st_empty[(G - 1) % kStages]), ((G - 1) / kStages) & 1, c, abort_flag);
-              if (!ok) continue;
               tc_fence_after();
 #pragma unroll 1
-              for (int cc = 0; cc < 64; cc += 16) {
+              for (int cc = 0; cc < 64 && ok; cc += 16) {
                 const uint32_t oa = tmem + lane_off + kColO + 128 * (cc >> 5) + 32 * ch + (cc & 31);
                 uint32_t o[16];
                 tmem_ld16(oa, o);
@@ -1164,11 +1155,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             weights();
             store_p();
           }
+          named_bar_sync(group_bar, kSoftThreads / 2);
         }
         if (!ok) continue;
         l_run += lsum_blk;
-        __syncwarp();
-        signal(&sm.p_full[pb]);
+        // after the barrier P of all the group's warps is there
+        if (ch == 0 && half == 0) signal(&sm.p_full[pb], quad == 0, 2);
       }
       // ------------------------------- epilogue -------------------------------
       if (ok) ok = mbar_wait_warp(smem_u32(&sm.mma_done[bi]), (i >> 1) & 1, c, abort_flag);
