@@ -1120,17 +1120,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (kept == 16) put(pbuf + own1, pk + 4);
           fence_proxy_async_smem();
         };
-        weights();
-        store_p();
+        const bool start = j == g.j0;              // nothing to compare with yet
+        if (!start) {
+          weights();
+          store_p();
+        }
         // (this barrier also ends the reads of the exchange, before the next block's)
-        if (named_bar_or(group_bar, kSoftThreads / 2, bm > m_run + kRescaleThreshold)) {
+        if (named_bar_or(group_bar, kSoftThreads / 2, start || bm > m_run + kRescaleThreshold)) {
           // the row's block max over its eight threads (lane pair x column parts)
           red(ch, half) = bm;
           named_bar_sync(group_bar, kSoftThreads / 2);
           bm = row_max();
           named_bar_sync(group_bar, kSoftThreads / 2);  // red makes room for the next exchange
           const bool need = bm > m_run + kRescaleThreshold;
-          if (ok && __any_sync(0xffffffffu, need)) {
+          if (ok && (start || __any_sync(0xffffffffu, need))) {
             const float m_new = need ? bm : m_run;
             const float alpha = (m_run == -INFINITY || !need) ? (need ? 0.f : 1.f) : ex2(m_run - m_new);
             if (j > g.j0 && __any_sync(0xffffffffu, need && m_run != -INFINITY)) {
@@ -1163,23 +1166,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (ch == 0 && half == 0) signal(&sm.p_full[pb], quad == 0, 2);
       }
       // ------------------------------- epilogue -------------------------------
-      if (ok) ok = mbar_wait_warp(smem_u32(&sm.mma_done[bi]), (i >> 1) & 1, c, abort_flag);
-      tc_fence_after();
+      // the row's sum and maximum over its eight threads, while the last P V runs
       if (poison) l_run = NAN;
-      named_bar_sync(1, kSoftThreads);
       red(ch, half) = l_run;
-      named_bar_sync(1, kSoftThreads);
+      named_bar_sync(group_bar, kSoftThreads / 2);
       float lsum = 0.f;
 #pragma unroll
       for (int t = 0; t < 4; ++t) lsum += red(t, 0) + red(t, 1);
-      named_bar_sync(1, kSoftThreads);
+      named_bar_sync(group_bar, kSoftThreads / 2);
       red(ch, half) = m_own;
-      const bool all_ok = named_bar_or(2, kSoftThreads, !ok) == false;
+      named_bar_sync(group_bar, kSoftThreads / 2);
       const float m_true = row_max();
-      if (!all_ok) {
-        ok = false;
-        continue;
-      }
+      if (ok) ok = mbar_wait_warp(smem_u32(&sm.mma_done[bi]), (i >> 1) & 1, c, abort_flag);
+      if (!ok) continue;
+      tc_fence_after();
       if (g.part >= 0) {
         // part of a tile: O as it stands, [column quad][row] so that a warp's
         // 32 rows make whole lines
