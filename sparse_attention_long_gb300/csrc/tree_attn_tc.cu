@@ -1200,29 +1200,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else {
         const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // no visible key: 0
         const long long row0 = (long long)g.t0 * a.H + 128ll * g.tile + kHC * (int)crank;  // first row of this CTA
-        // A thread holds 2 x 32 columns of its row: 64 consecutive bytes, whole
-        // sectors, straight to global memory, and nobody waits for the stores (a way
-        // through shared memory and TMA had two rounds of barriers: 4,800 cycles).
-        const bool wide_out = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
-#pragma unroll 1
+        // A thread holds 64 columns of its row, 4 pieces of 32 bytes.  Four lanes
+        // transpose theirs, so that a store of the warp fills 8 whole lines instead of
+        // touching 32, and nobody waits for the stores.
+        uint32_t w[4][8];
+#pragma unroll
         for (int m = 0; m < 2; ++m) {
           uint32_t o[32];
-          tmem_ld32(tmem + lane_off + kColO + 128 * m + 32 * ch, o);
+          tmem_ld32(tmem + lane_off + kColO + 64 * ch + 32 * m, o);
           tmem_ld_wait(o);
-          uint32_t pw[16];
 #pragma unroll
           for (int t = 0; t < 16; ++t)
-            pw[t] = pack_bf16x2(__uint_as_float(o[2 * t]) * inv, __uint_as_float(o[2 * t + 1]) * inv);
-          if (live) {
-            __nv_bfloat16* dst = out + (row0 + hl) * kDV + 256 * half + 128 * m + 32 * ch;
-            if (wide_out) {
-              st_global32(dst, pw);
-              st_global32(dst + 16, pw + 8);
-            } else {
+            w[2 * m + (t >> 3)][t & 7] =
+                pack_bf16x2(__uint_as_float(o[2 * t]) * inv, __uint_as_float(o[2 * t + 1]) * inv);
+        }
 #pragma unroll
-              for (int t = 0; t < 4; ++t)
-                reinterpret_cast<uint4*>(dst)[t] = make_uint4(pw[4 * t], pw[4 * t + 1], pw[4 * t + 2], pw[4 * t + 3]);
+        for (int d = 1; d < 4; d <<= 1) {
+          const bool up = (lane & d) != 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k & d) continue;                   // pieces k and k + d of lanes l and l ^ d
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[k][t] : w[k + d][t], d);
+              if (up) w[k][t] = got;
+              else w[k + d][t] = got;
             }
+          }
+        }
+        const bool wide_out = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {              // row k of the four lanes, this lane's piece
+          const int r4 = (hl & ~3) + k;
+          __nv_bfloat16* dst = out + (row0 + r4) * kDV + 256 * half + 64 * ch + 16 * (lane & 3);
+          if (kHC * (int)crank + r4 >= rows) continue;
+          if (wide_out) {
+            st_global32(dst, w[k]);
+          } else {
+            reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+            reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[k][4], w[k][5], w[k][6], w[k][7]);
           }
         }
         if (half == 0 && ch == 0 && live) {
