@@ -737,9 +737,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++G;
       }
       // the tokens of the tile
-      const int ta = (int)(128ll * g.tile / a.H);
-      const long long last = (128ll * g.tile + 127) / a.H;
-      const int tb = last < g.T - 1 ? (int)last : g.T - 1;
+      const int ta = (int)(128u * (uint32_t)g.tile / (uint32_t)a.H);  // (rows of all tokens: below 2^31)
+      const int last = (int)((128u * (uint32_t)g.tile + 127u) / (uint32_t)a.H);
+      const int tb = last < g.T - 1 ? last : g.T - 1;
       for (int j = g.j0; j < g.j1; ++j, ++G) {
         const int st = G % kStages;
         // slots that any / every token of the tile sees
@@ -1001,7 +1001,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (g.end) break;
       const long long rows = (long long)g.T * a.H - 128ll * g.tile;
       const bool live = rr < rows;
-      const int tok = live ? (int)((128ll * g.tile + rr) / a.H) : g.T - 1;
+      const int tok = live ? (int)((128u * (uint32_t)g.tile + rr) / (uint32_t)a.H) : g.T - 1;
       float m_run = -INFINITY, m_own = -INFINITY, l_run = 0.f;  // m_own: over this thread's slots
       bool poison = false;
       ++G;                                         // the query's slot
