@@ -1263,26 +1263,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 //   M = max m_k, w_k = 2^(m_k - M), l = sum w_k l_k, out = sum w_k O_k / l,
 // in a fixed order.  A tile may have a part from every pair (one long sequence),
 // or the batch a two-part tile from every pair.  Up to 8 parts, one thread takes
-// all parts of one row's 16 columns; above, four threads share the parts of one
-// row's 8 columns.  What counts is that many loads are in flight (one thread for
-// 4 columns of all 74 parts of a 16K-row sequence: 25 us).
+// all parts of one row's 8 columns; above, four threads share them.  What counts
+// is that many loads are in flight (one thread for 4 columns of all 74 parts of a
+// 16K-row sequence: 25 us).  64 sequences, 39 MB of parts: 12 us.
 constexpr int kJoinThreads = 256, kJoinGroups = 4, kJoinFew = 8;
 constexpr int kJoinPerPair = 6;                    // CTAs: what is resident at once (a CTA's start costs a piece's time)
 constexpr int kMaxPairs = 256;
 
-// parts k = g, g + step, ... of one row: running max, sum, true max, and O of NQ column quads
-template <int NQ>
+// parts k = g, g + step, ... of one row: running max, sum, true max, and O of two column quads
 struct Joined {
   float M, l, true_max;
-  float4 o[NQ];
+  float4 o[2];
 };
-// U parts at a time, all of their loads in flight together
-template <int NQ, int U>
-__device__ __forceinline__ Joined<NQ> join_parts(const float4* __restrict__ parts, const float4* __restrict__ stats,
-                                                 int pair, int nparts, int g, int step, int row, int q) {
+// four parts at a time, all of their loads in flight together
+__device__ __forceinline__ Joined join_parts(const float4* __restrict__ parts, const float4* __restrict__ stats,
+                                             int pair, int nparts, int g, int step, int row, int q) {
   auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * pair + 1 : 2 * (pair + k)); };
+  constexpr int NQ = 2, U = 4;
   const uint64_t go = policy_go();
-  Joined<NQ> j;
+  Joined j;
   j.M = j.true_max = -INFINITY;
   j.l = 0.f;
 #pragma unroll
@@ -1327,13 +1326,12 @@ __device__ __forceinline__ Joined<NQ> join_parts(const float4* __restrict__ part
   }
   return j;
 }
-template <int NQ>
-__device__ __forceinline__ void join_store(const Joined<NQ>& j, long long r, int q, __nv_bfloat16* out, float* mx,
+__device__ __forceinline__ void join_store(const Joined& j, long long r, int q, __nv_bfloat16* out, float* mx,
                                            float* sm_out) {
   const float inv = j.l == 0.f ? 0.f : 1.f / j.l;
   uint2* dst = reinterpret_cast<uint2*>(out + r * kDV + 4 * q);
 #pragma unroll
-  for (int t = 0; t < NQ; ++t)
+  for (int t = 0; t < 2; ++t)
     dst[t] = make_uint2(pack_bf16x2(j.o[t].x * inv, j.o[t].y * inv), pack_bf16x2(j.o[t].z * inv, j.o[t].w * inv));
   if (q == 0) {
     mx[r] = j.true_max == -INFINITY ? -INFINITY : j.true_max * kLn2;
@@ -1345,7 +1343,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     tree_join_kernel(const float4* __restrict__ parts, const float4* __restrict__ stats,
                      const Join* __restrict__ joins, int npairs, __nv_bfloat16* __restrict__ out,
                      float* __restrict__ mx, float* __restrict__ sm_out) {
-  __shared__ Joined<2> shared[kJoinGroups - 1][64];
+  __shared__ Joined shared[kJoinGroups - 1][64];
   __shared__ Join list[kMaxPairs];
   __shared__ uint16_t list_pair[kMaxPairs];
   __shared__ int below[kMaxPairs / 32];
@@ -1369,50 +1367,51 @@ __global__ void __launch_bounds__(kJoinThreads)
     list_pair[at] = (uint16_t)tid;
   }
   __syncthreads();
-  int piece = blockIdx.x;                          // this CTA's next piece, counted from the current tile's first
-  for (int i = 0; i < n; ++i) {
-    const Join jn = list[i];
-    const int pair = list_pair[i];
-    const bool few = jn.nparts <= kJoinFew;
-    const int pieces = few ? 16 : 128;
-    for (; piece < pieces; piece += gridDim.x) {
-      if (few) {                                   // 128 rows x 2 x 16 columns
-        const int row = tid & 127, q = 8 * piece + 4 * (tid >> 7);
-        const Joined<4> j = join_parts<4, 2>(parts, stats, pair, jn.nparts, 0, 1, row, q);
-        if (row < jn.nrows) join_store<4>(j, jn.row0 + row, q, out, mx, sm_out);
-        continue;
-      }
-      // 64 rows x 8 columns, four threads each
-      const int cell = tid & 63, row = (piece & 1) * 64 + cell, q = 2 * (piece >> 1), g = tid >> 6;
-      Joined<2> j = join_parts<2, 4>(parts, stats, pair, jn.nparts, g, kJoinGroups, row, q);
-      __syncthreads();                             // the last piece's sums are read
-      if (g > 0) shared[g - 1][cell] = j;
-      __syncthreads();
-      if (g > 0 || row >= jn.nrows) continue;
-      Joined<2> all = j;
-#pragma unroll
-      for (int t = 0; t < kJoinGroups - 1; ++t) {
-        all.M = fmaxf(all.M, shared[t][cell].M);
-        all.true_max = fmaxf(all.true_max, shared[t][cell].true_max);
-      }
-      const float mu = all.M == -INFINITY ? 0.f : all.M;
-      auto add = [&](const Joined<2>& p, bool first) {  // (no key in the group: weight 0)
-        const float w = ex2(p.M - mu);
-        all.l = fmaf(w, p.l, first ? 0.f : all.l);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          all.o[t].x = fmaf(w, p.o[t].x, first ? 0.f : all.o[t].x);
-          all.o[t].y = fmaf(w, p.o[t].y, first ? 0.f : all.o[t].y);
-          all.o[t].z = fmaf(w, p.o[t].z, first ? 0.f : all.o[t].z);
-          all.o[t].w = fmaf(w, p.o[t].w, first ? 0.f : all.o[t].w);
-        }
-      };
-      add(j, true);
-#pragma unroll
-      for (int t = 0; t < kJoinGroups - 1; ++t) add(shared[t][cell], false);
-      join_store<2>(all, jn.row0 + row, q, out, mx, sm_out);
+  int i = 0, base = 0;                             // tile, its first piece
+  for (int piece = blockIdx.x;; piece += gridDim.x) {
+    int pieces = 0;
+    for (; i < n; ++i, base += pieces) {
+      pieces = list[i].nparts <= kJoinFew ? 32 : 128;
+      if (piece < base + pieces) break;
     }
-    piece -= pieces;
+    if (i == n) break;
+    const Join jn = list[i];
+    const int pair = list_pair[i], k = piece - base;
+    if (jn.nparts <= kJoinFew) {                   // 128 rows x 2 x 8 columns
+      const int row = tid & 127, q = 4 * k + 2 * (tid >> 7);
+      const Joined j = join_parts(parts, stats, pair, jn.nparts, 0, 1, row, q);
+      if (row < jn.nrows) join_store(j, jn.row0 + row, q, out, mx, sm_out);
+      continue;
+    }
+    // 64 rows x 8 columns, four threads each
+    const int cell = tid & 63, row = (k & 1) * 64 + cell, q = 2 * (k >> 1), g = tid >> 6;
+    Joined j = join_parts(parts, stats, pair, jn.nparts, g, kJoinGroups, row, q);
+    __syncthreads();                               // the last piece's sums are read
+    if (g > 0) shared[g - 1][cell] = j;
+    __syncthreads();
+    if (g > 0 || row >= jn.nrows) continue;
+    Joined all = j;
+#pragma unroll
+    for (int t = 0; t < kJoinGroups - 1; ++t) {
+      all.M = fmaxf(all.M, shared[t][cell].M);
+      all.true_max = fmaxf(all.true_max, shared[t][cell].true_max);
+    }
+    const float mu = all.M == -INFINITY ? 0.f : all.M;
+    auto add = [&](const Joined& p, bool first) {  // (no key in the group: weight 0)
+      const float w = ex2(p.M - mu);
+      all.l = fmaf(w, p.l, first ? 0.f : all.l);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        all.o[t].x = fmaf(w, p.o[t].x, first ? 0.f : all.o[t].x);
+        all.o[t].y = fmaf(w, p.o[t].y, first ? 0.f : all.o[t].y);
+        all.o[t].z = fmaf(w, p.o[t].z, first ? 0.f : all.o[t].z);
+        all.o[t].w = fmaf(w, p.o[t].w, first ? 0.f : all.o[t].w);
+      }
+    };
+    add(j, true);
+#pragma unroll
+    for (int t = 0; t < kJoinGroups - 1; ++t) add(shared[t][cell], false);
+    join_store(all, jn.row0 + row, q, out, mx, sm_out);
   }
 }
 
