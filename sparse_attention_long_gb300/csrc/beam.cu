@@ -6,8 +6,8 @@
 // chunk of the vocabulary), the chunk in registers.  Within a beam the order of
 // the candidates is the order of the logits, so a chunk only has to give its
 // best beams_out logits, its maximum m and its sum of exp(x - m).  With c =
-// ceil(beams_out / 8), the smallest of the 8 warps' c-th largest thread maxima
-// bounds the chunk's beams_out-th largest logit from below (8 c threads have a
+// ceil(beams_out / 4), the smallest of the 4 warps' c-th largest thread maxima
+// bounds the chunk's beams_out-th largest logit from below (4 c threads have a
 // logit at least that large); some 20 logits of a chunk pass it for 8 beams.
 // Those are ranked by counting, as keys (order-preserving bits of the logit,
 // inverted index), which are unique.  Should too many pass (equal logits), the
@@ -23,7 +23,11 @@
 // is fp64.  A row gives the same bits wherever it lies:
 // which element a thread takes depends on its index alone, not on alignment.
 //
-// Bound: reading the logits (HBM) for a batch; the two launches for one request.
+// Bound: for a batch, the logits' way from HBM and some 10 instructions per logit,
+// of which the CTAs of a wave do first the one and then the other: 64 x 8 beams x
+// 131071 bf16 take 42 us, 3.2 TB/s (2 instructions per cycle and SM, DRAM 41 %
+// busy).  Loading the next chunk ahead of the sums took more registers than it
+// gave.  One request of 4 x 32001: 9.3 us, the two launches and their latencies.
 #include <math.h>
 
 #include "dsa_common.cuh"
@@ -34,9 +38,11 @@ bool ext_dev_ctx(DevCtx* c);
 
 namespace beam {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kVec = 8;                            // consecutive elements per thread and step
-// elements per thread and CTA: 16,384 (bf16) or 8,192 (fp32) logits, 32 registers
+// elements per thread and CTA: 8,192 (bf16) or 4,096 (fp32) logits, 32 registers
+// (CTAs of 256 threads and twice the logits: 64 x 8 beams x 131071 bf16 41.4 us
+// against 42.0, but one request of 4 x 32001 10.4 us against 9.3)
 constexpr int kStepsBf16 = 8, kStepsFp32 = 4;
 constexpr int kMaxPerThread = kStepsBf16 * kVec;
 constexpr int chunk_of(int dtype) { return kThreads * kVec * (dtype == DSA_BF16 ? kStepsBf16 : kStepsFp32); }
@@ -90,7 +96,7 @@ template <typename T>
 struct Logits;
 template <>
 struct Logits<float> {
-  static constexpr int kSteps = kStepsFp32, kResident = 4;
+  static constexpr int kSteps = kStepsFp32, kResident = 8;
   float x[kSteps][kVec];
   __device__ __forceinline__ void load16(int s, const float* p) {
     const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
@@ -124,7 +130,7 @@ struct Logits<float> {
 };
 template <>
 struct Logits<__nv_bfloat16> {
-  static constexpr int kSteps = kStepsBf16, kResident = 5;
+  static constexpr int kSteps = kStepsBf16, kResident = 10;
   uint32_t w[kSteps][kVec / 2];                    // two each, the first in the low half
   __device__ __forceinline__ void load16(int s, const __nv_bfloat16* p) {
     const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
@@ -350,10 +356,11 @@ __device__ __forceinline__ double log_of(unsigned long long t, int unit) {
 }
 
 // One CTA per request.  One warp per beam adds its chunks' sums and merges their
-// sorted lists (lane = chunk, the largest head of the lanes taken each time);
+// sorted lists (lane = chunk and every 32nd after it, the largest head taken each time);
 // then one warp merges the beams (lane = beam), whose lists are sorted by score,
 // too.  The fp64 part is one lane's per beam.
 constexpr int kJoinThreads = 256;
+constexpr int kLists = 4;                           // per lane: 128 chunks, 1M (bf16) or 512K logits
 __global__ void __launch_bounds__(kJoinThreads)
     beam_join_kernel(Args a, const float* __restrict__ scores, const uint8_t* __restrict__ finished,
                      const Stat* __restrict__ stats, const unsigned long long* __restrict__ keys,
@@ -373,14 +380,16 @@ __global__ void __launch_bounds__(kJoinThreads)
       const Stat* s = stats + row * a.chunks * kWarps;
       const int ns = a.chunks * kWarps;
       const unsigned long long* kr = keys + row * a.chunks * k;
-      // heads of this lane's lists (chunk lane, lane + 32, ...): one list up to 32 chunks
-      const bool few = a.chunks <= 32;
-      int pos = 0;
-      unsigned long long head = 0, next = 0;
-      if (few && lane < a.chunks) {
-        head = kr[lane * k];
-        next = k > 1 ? kr[lane * k + 1] : 0;
+      // heads of this lane's lists (chunks lane, lane + 32, ...), and what follows the first list's
+      const bool few = a.chunks <= 32 * kLists;
+      int pos[kLists];
+      unsigned long long head[kLists], next = 0;
+#pragma unroll
+      for (int q = 0; q < kLists; ++q) {
+        pos[q] = 0;
+        head[q] = few && lane + 32 * q < a.chunks ? kr[(lane + 32 * q) * k] : 0;
       }
+      if (few && lane < a.chunks && k > 1) next = kr[lane * k + 1];
       float m = -INFINITY;
       for (int c = lane; c < ns; c += 32) m = fmaxf(m, s[c].max);
       const uint32_t most = __reduce_max_sync(0xffffffffu, ordered_key(m));
@@ -398,7 +407,9 @@ __global__ void __launch_bounds__(kJoinThreads)
         }
         unsigned long long last = ~0ull;
         for (; got < k; ++got) {
-          unsigned long long best = head;
+          unsigned long long best = head[0];
+#pragma unroll
+          for (int q = 1; q < kLists; ++q) best = head[q] > best ? head[q] : best;
           if (!few) {                              // the largest key below the last one taken
             best = 0;
             for (int i = lane; i < a.chunks * k; i += 32) {
@@ -410,10 +421,18 @@ __global__ void __launch_bounds__(kJoinThreads)
           const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
           const unsigned long long win = ((unsigned long long)hi << 32) | lo;
           if (win == 0) break;
-          if (few && best == win) {                // keys are unique: one lane
-            head = next;
-            ++pos;
-            next = pos + 1 < k ? kr[lane * k + pos + 1] : 0;
+          if (few && best == win) {                // keys are unique: one list of one lane
+            if (head[0] == win) {
+              head[0] = next;
+              ++pos[0];
+              next = pos[0] + 1 < k ? kr[lane * k + pos[0] + 1] : 0;
+            }
+#pragma unroll
+            for (int q = 1; q < kLists; ++q)
+              if (head[q] == win) {
+                ++pos[q];
+                head[q] = pos[q] < k ? kr[(lane + 32 * q) * k + pos[q]] : 0;
+              }
           }
           last = win;
           if (lane == 0) list[w][got] = win;

@@ -26,7 +26,8 @@
 //     in lanes 64..127; 2 MMAs per 16 slots cover the 512 columns in 256 TMEM
 //     columns.
 // TMEM: O 256 + logits 112 + query 144 columns.  Three key stages, two P
-// buffers; the logits of block j+1 run during the softmax of block j.
+// buffers; the logits of block j+1 run during the softmax of block j.  112 slots:
+// what 512 TMEM columns leave for the logits, and N = 2 x 112 runs at full rate.
 //
 // Keys arrive by TMA straight from the pages (which hold a multiple of 16
 // rows): one copy brings 16 or 32 rows x 256 value columns, already as the
@@ -47,6 +48,16 @@
 // and the rope columns from registers, once the last logits of the tile before
 // have read the old query (per-row loads of the softmax warps took 4,200 cycles
 // between two tiles).
+//
+// Bound.  A block's MMAs take 1,956 cycles back to back (logits 1,008, P V 896);
+// the loop takes about 2,750 per block (keys from L2) to 3,000 (from HBM), a tile
+// change some 5,500 more.  The loop is the softmax warps' chain of waits: logits
+// out of TMEM, the exchange through shared memory (whose bandwidth the operands'
+// reads, the copies and the exchange use to two thirds), P back, and the signals
+// between the CTAs.  Measured: 16 trees of 48 tokens over 2K-6K rows, 128 heads,
+// 660 us = 1,330 TFLOP/s; 64 single tokens over 1K-16K rows 144 us = 4.5 TB/s and
+// 1,060 TFLOP/s (12 us of it the join; tensor pipes 53 % and DRAM 62 % busy); one
+// token over 1K rows 14 us (the two launches, one tile, the join).
 //
 // Roles per CTA: warp 0 = TMEM allocation, MMA issuer of the logits (CTA 0);
 // warps 1..4 = query into TMEM, passing on of key stages (with the zeroing

@@ -176,3 +176,14 @@ def test_refused_calls():
         dsa.beam_select(mk(), x[..., :7], s, None, *o, ws)
     with pytest.raises(TypeError):
         dsa.beam_select(mk(dtype="bf16"), x, s, None, *o, ws)
+
+
+@pytest.mark.parametrize("W,V,keep,dtype", [
+    (1, 140001, 32, torch.float32), (2, 300000, 5, torch.float32), (1, 530001, 9, torch.float32),
+    (1, 270001, 32, torch.bfloat16)])
+def test_long_vocabularies(W, V, keep, dtype):
+    """Rows of more chunks than a warp has lanes, and of more than its lanes have lists."""
+    dsa = lib()
+    x = rand(1, W, V, seed=V)
+    x[0, 0, V - 40:] += 12.0                     # many of the best in the last chunk, some in others
+    check(dsa, x, [[-1.5] * W], None, keep, -1, dtype=dtype)
