@@ -47,6 +47,7 @@ constexpr int kStepsBf16 = 8, kStepsFp32 = 4;
 constexpr int kMaxPerThread = kStepsBf16 * kVec;
 constexpr int chunk_of(int dtype) { return kThreads * kVec * (dtype == DSA_BF16 ? kStepsBf16 : kStepsFp32); }
 constexpr int kMaxBeams = 32;                      // in and out
+constexpr int kMaxRuns = 128;                      // runs of eight logits that hold some
 constexpr int kMaxCand = kMaxPerThread * kMaxBeams;  // candidates of a chunk at most, see beam_part_kernel
 
 struct Args {
@@ -108,6 +109,10 @@ struct Logits<float> {
     for (int i = 0; i < kVec; ++i) x[s][i] = i < n ? __ldcs(p + i) : -INFINITY;
   }
   __device__ __forceinline__ float get(int s, int e) const { return x[s][e]; }
+  __device__ __forceinline__ void put_run(int s, float* p) const {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[s][0], x[s][1], x[s][2], x[s][3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[s][4], x[s][5], x[s][6], x[s][7]);
+  }
   __device__ __forceinline__ float run_max(int s) const {
     float m = x[s][0];
 #pragma unroll
@@ -146,6 +151,9 @@ struct Logits<__nv_bfloat16> {
   }
   __device__ __forceinline__ float get(int s, int e) const {
     return __uint_as_float((e & 1) ? w[s][e >> 1] & 0xFFFF0000u : w[s][e >> 1] << 16);
+  }
+  __device__ __forceinline__ void put_run(int s, __nv_bfloat16* p) const {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[s][0], w[s][1], w[s][2], w[s][3]);
   }
   __device__ __forceinline__ uint32_t run_max2(int s) const {
     uint32_t t = w[s][0];
@@ -196,8 +204,10 @@ __global__ void __launch_bounds__(kThreads, Logits<T>::kResident)
                      unsigned long long* __restrict__ keys, int vec) {
   constexpr int kSteps = Logits<T>::kSteps, kChunk = kThreads * kVec * kSteps;
   __shared__ unsigned long long cand[kMaxCand], tmax[kThreads], kth;
+  __shared__ __align__(16) T runs[kMaxRuns][kVec];
+  __shared__ int run_at[kMaxRuns];
   __shared__ uint32_t wleast[kWarps];
-  __shared__ int n_cand;
+  __shared__ int n_cand, n_runs;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.wout;
   const uint32_t item = blockIdx.x, row = item / (uint32_t)a.chunks;
   const int first = (int)(item - row * (uint32_t)a.chunks) * kChunk + tid * kVec;  // this thread's first logit
@@ -205,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, Logits<T>::kResident)
   wait_for_earlier();
   // a finished beam has no logits, a beam of score -inf no candidates
   if ((finished && finished[row]) || !(scores[row] > -INFINITY)) return;
-  if (tid == 0) n_cand = 0;
+  if (tid == 0) n_cand = n_runs = 0;
   Logits<T> x;
   const T* xrow = logits + (long long)row * a.ld;
   {
@@ -276,25 +286,27 @@ __global__ void __launch_bounds__(kThreads, Logits<T>::kResident)
   for (int w = 1; w < kWarps; ++w) least = least < wleast[w] ? least : wleast[w];
   // (too few logits for a bound: every one passes)
   const float from = least == 0 ? -3.402823466e38f : fmaxf(ordered_value(least), -3.402823466e38f);
+  // the runs with such a logit go to shared memory as they are (to pick their
+  // logits out here, every lane of the warp would wait for each of them)
   if (m >= from) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
       if (x.run_max(s) >= from) {
-        uint32_t hit = 0;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) hit |= x.get(s, e) >= from ? 1u << e : 0u;
-        int at = atomicAdd(&n_cand, __popc(hit));
-#pragma unroll
-        for (int e = 0; e < kVec; ++e)
-          if ((hit >> e) & 1u) {
-            if (at < kMaxCand) cand[at] = make_key(x.get(s, e), first + s * kThreads * kVec + e);
-            ++at;
-          }
+        const int at = atomicAdd(&n_runs, 1);
+        if (at < kMaxRuns) {
+          x.put_run(s, runs[at]);
+          run_at[at] = first + s * kThreads * kVec;
+        }
       }
   }
   __syncthreads();
-  int n = n_cand;
-  if (n > kMaxCand) {                              // many equal logits: bound by unique keys
+  const int nr = n_runs;
+  if (nr <= kMaxRuns) {
+    for (int i = tid; i < nr * kVec; i += kThreads) {
+      const float y = to_f32<T>(runs[i / kVec][i % kVec]);
+      if (y >= from) cand[atomicAdd(&n_cand, 1)] = make_key(y, run_at[i / kVec] + i % kVec);
+    }
+  } else {                                         // many equal logits: bound by unique keys
     unsigned long long best = 0;
     reread(xrow, first, a.vocab, [&](float y, int i) {
       if (y == m && m != -INFINITY) best = best > make_key(y, i) ? best : make_key(y, i);
@@ -304,16 +316,15 @@ __global__ void __launch_bounds__(kThreads, Logits<T>::kResident)
     int rank = 0;
     for (int t = 0; t < kThreads; ++t) rank += tmax[t] > best;
     if (rank == k - 1 && best != 0) kth = best;
-    if (tid == 0) n_cand = 0;
     __syncthreads();
     const unsigned long long lowest = have < k ? 1ull : kth;
     reread(xrow, first, a.vocab, [&](float y, int i) {
       const unsigned long long key = make_key(y, i);
       if (y != -INFINITY && key >= lowest) cand[atomicAdd(&n_cand, 1)] = key;  // only k threads have such keys
     });
-    __syncthreads();
-    n = n_cand;
   }
+  __syncthreads();
+  const int n = n_cand;
   unsigned long long* out = keys + (size_t)item * k;
   for (int i = tid; i < n; i += kThreads) {
     const unsigned long long mine = cand[i];
