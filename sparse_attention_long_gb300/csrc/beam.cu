@@ -135,7 +135,7 @@ struct Logits<float> {
 };
 template <>
 struct Logits<__nv_bfloat16> {
-  static constexpr int kSteps = kStepsBf16, kResident = 10;
+  static constexpr int kSteps = kStepsBf16, kResident = 8;
   uint32_t w[kSteps][kVec / 2];                    // two each, the first in the low half
   __device__ __forceinline__ void load16(int s, const __nv_bfloat16* p) {
     const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
@@ -289,14 +289,18 @@ __global__ void __launch_bounds__(kThreads, Logits<T>::kResident)
   // the runs with such a logit go to shared memory as they are (to pick their
   // logits out here, every lane of the warp would wait for each of them)
   if (m >= from) {
+    uint32_t hit = 0;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) hit |= x.run_max(s) >= from ? 1u << s : 0u;
+    int at = atomicAdd(&n_runs, __popc(hit));
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
-      if (x.run_max(s) >= from) {
-        const int at = atomicAdd(&n_runs, 1);
+      if ((hit >> s) & 1u) {
         if (at < kMaxRuns) {
           x.put_run(s, runs[at]);
           run_at[at] = first + s * kThreads * kVec;
         }
+        ++at;
       }
   }
   __syncthreads();
@@ -329,7 +333,8 @@ __global__ void __launch_bounds__(kThreads, Logits<T>::kResident)
   for (int i = tid; i < n; i += kThreads) {
     const unsigned long long mine = cand[i];
     int r = 0;
-    for (int j = 0; j < n && r < k; ++j) r += cand[j] > mine;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) r += cand[j] > mine;
     if (r < k) out[r] = mine;
   }
   for (int i = n + tid; i < k; i += kThreads) out[i] = 0;
