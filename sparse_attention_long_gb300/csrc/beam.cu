@@ -25,9 +25,9 @@
 //
 // Bound: for a batch, the logits' way from HBM and some 10 instructions per logit,
 // of which the CTAs of a wave do first the one and then the other: 64 x 8 beams x
-// 131071 bf16 take 42 us, 3.2 TB/s (2 instructions per cycle and SM, DRAM 41 %
-// busy).  Loading the next chunk ahead of the sums took more registers than it
-// gave.  One request of 4 x 32001: 9.3 us, the two launches and their latencies.
+// 131071 bf16 take 34 us, 3.9 TB/s; the first kernel alone 27 us, 5.0 TB/s.
+// Loading the next chunk ahead of the sums took more registers than it gave.  One
+// request of 4 x 32001: 7.3 us, the two launches and their latencies.
 #include <math.h>
 
 #include "dsa_common.cuh"
@@ -41,8 +41,8 @@ namespace beam {
 constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kVec = 8;                            // consecutive elements per thread and step
 // elements per thread and CTA: 8,192 (bf16) or 4,096 (fp32) logits, 32 registers
-// (CTAs of 256 threads and twice the logits: 64 x 8 beams x 131071 bf16 41.4 us
-// against 42.0, but one request of 4 x 32001 10.4 us against 9.3)
+// (CTAs of 256 threads and twice the logits took 0.6 us less for 64 x 8 beams x
+// 131071 bf16, but 1.1 us more for one request of 4 x 32001)
 constexpr int kStepsBf16 = 8, kStepsFp32 = 4;
 constexpr int kMaxPerThread = kStepsBf16 * kVec;
 constexpr int chunk_of(int dtype) { return kThreads * kVec * (dtype == DSA_BF16 ? kStepsBf16 : kStepsFp32); }
@@ -371,117 +371,127 @@ __device__ __forceinline__ double log_of(unsigned long long t, int unit) {
   return fma((double)(e - unit), 0.6931471805599453, 2.0 * s * p);
 }
 
-// One CTA per request.  One warp per beam adds its chunks' sums and merges their
-// sorted lists (lane = chunk and every 32nd after it, the largest head taken each time);
-// then one warp merges the beams (lane = beam), whose lists are sorted by score,
-// too.  The fp64 part is one lane's per beam.
-constexpr int kJoinThreads = 256;
+// One CTA per request.  Per beam, one warp merges its chunks' sorted lists (lane =
+// chunk and every 32nd after it, the largest head taken each time) while another
+// adds the chunks' sums and takes the logarithm; then all threads compute the
+// candidates' scores, and one warp merges the beams (lane = beam), whose lists are
+// sorted by score, too.  Bound: latency, of the fp64 logarithm and of 2 beams_out
+// rounds of warp reductions; the lists are read from global memory once, all loads
+// in flight, where they fit (with a load per round, sum and merge in one warp, one
+// request took 8.6 us in all, 7.3 now).
+constexpr int kJoinWarps = 8, kJoinThreads = 2 * 32 * kJoinWarps;
 constexpr int kLists = 4;                           // per lane: 128 chunks, 1M (bf16) or 512K logits
+constexpr int kKeyRoom = 512;                       // keys per warp
 __global__ void __launch_bounds__(kJoinThreads)
     beam_join_kernel(Args a, const float* __restrict__ scores, const uint8_t* __restrict__ finished,
                      const Stat* __restrict__ stats, const unsigned long long* __restrict__ keys,
                      int32_t* __restrict__ parent, int32_t* __restrict__ token, float* __restrict__ scores_out,
                      uint8_t* __restrict__ finished_out) {
-  __shared__ unsigned long long list[kMaxBeams][kMaxBeams + 1], total[kMaxBeams];  // best first; 0: no more
-  __shared__ float top[kMaxBeams];
+  __shared__ unsigned long long room[kJoinWarps][kKeyRoom];
+  __shared__ unsigned long long list[kMaxBeams][kMaxBeams + 1];  // best first: keys, then ordered scores; 0: none
+  __shared__ uint32_t index[kMaxBeams][kMaxBeams + 1];
+  __shared__ double lse[kMaxBeams];
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, k = a.wout;
+  const int wj = (tid >> 5) % kJoinWarps;
+  const bool merges = tid < 32 * kJoinWarps;
   let_next_launch();
   wait_for_earlier();
-  for (int w = tid >> 5; w < a.win; w += kJoinThreads / 32) {
+  for (int w = wj; w < a.win; w += kJoinWarps) {
     const long long row = (long long)b * a.win + w;
     const float sc = scores[row];
     const bool done = finished && finished[row];
-    int got = 0;
-    if (!done && sc > -INFINITY) {
-      const Stat* s = stats + row * a.chunks * kWarps;
-      const int ns = a.chunks * kWarps;
-      const unsigned long long* kr = keys + row * a.chunks * k;
-      // heads of this lane's lists (chunks lane, lane + 32, ...), and what follows the first list's
+    const bool open = !done && sc > -INFINITY;      // (what other beams' lists and sums hold is unspecified)
+    if (merges) {
+      const int have = a.chunks * k;
+      const unsigned long long* kr = keys + row * have;
+      if (have <= kKeyRoom) {
+#pragma unroll 4
+        for (int i = lane; i < have; i += 32) room[wj][i] = kr[i];
+        __syncwarp();
+        kr = room[wj];
+      }
       const bool few = a.chunks <= 32 * kLists;
       int pos[kLists];
-      unsigned long long head[kLists], next = 0;
+      unsigned long long head[kLists];             // of this lane's lists
 #pragma unroll
       for (int q = 0; q < kLists; ++q) {
         pos[q] = 0;
-        head[q] = few && lane + 32 * q < a.chunks ? kr[(lane + 32 * q) * k] : 0;
+        head[q] = open && few && lane + 32 * q < a.chunks ? kr[(lane + 32 * q) * k] : 0;
       }
-      if (few && lane < a.chunks && k > 1) next = kr[lane * k + 1];
+      unsigned long long last = ~0ull;
+      int got = 0;
+      for (; got < k && open; ++got) {
+        unsigned long long best = head[0];
+#pragma unroll
+        for (int q = 1; q < kLists; ++q) best = head[q] > best ? head[q] : best;
+        if (!few) {                                // the largest key below the last one taken
+          best = 0;
+          for (int i = lane; i < have; i += 32) {
+            const unsigned long long v = kr[i];
+            if (v < last && v > best) best = v;
+          }
+        }
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
+        const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+        const unsigned long long win = ((unsigned long long)hi << 32) | lo;
+        if (win == 0) break;
+        if (few && best == win) {                  // keys are unique: one list of one lane
+#pragma unroll
+          for (int q = 0; q < kLists; ++q)
+            if (head[q] == win) {
+              ++pos[q];
+              head[q] = pos[q] < k ? kr[(lane + 32 * q) * k + pos[q]] : 0;
+            }
+        }
+        last = win;
+        if (lane == 0) list[w][got] = win;
+      }
+      if (done && sc > -INFINITY) {
+        if (lane == 0) list[w][0] = ~0ull;         // the end token at the beam's score
+        got = 1;
+      }
+      for (int r = got + lane; r < k; r += 32) list[w][r] = 0;
+      __syncwarp();                                // room is read
+    } else if (open) {
+      const Stat* s = stats + row * a.chunks * kWarps;
+      const int ns = a.chunks * kWarps;
       float m = -INFINITY;
+#pragma unroll 4
       for (int c = lane; c < ns; c += 32) m = fmaxf(m, s[c].max);
-      const uint32_t most = __reduce_max_sync(0xffffffffu, ordered_key(m));
-      m = ordered_value(most);
+      m = ordered_value(__reduce_max_sync(0xffffffffu, ordered_key(m)));
       if (m != -INFINITY) {
         // in units of 2^-38 of the row's largest term: below 2^62
         unsigned long long t = 0;
+#pragma unroll 4
         for (int c = lane; c < ns; c += 32)
           t += __float2ull_rn((float)s[c].sum * ex2((s[c].max - m) * kLog2e) * 0.25f);  // (no logit in a warp: 0 * 0)
 #pragma unroll
         for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        if (lane == 0) {
-          total[w] = t;
-          top[w] = m;
-        }
-        unsigned long long last = ~0ull;
-        for (; got < k; ++got) {
-          unsigned long long best = head[0];
-#pragma unroll
-          for (int q = 1; q < kLists; ++q) best = head[q] > best ? head[q] : best;
-          if (!few) {                              // the largest key below the last one taken
-            best = 0;
-            for (int i = lane; i < a.chunks * k; i += 32) {
-              const unsigned long long v = kr[i];
-              if (v < last && v > best) best = v;
-            }
-          }
-          const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
-          const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
-          const unsigned long long win = ((unsigned long long)hi << 32) | lo;
-          if (win == 0) break;
-          if (few && best == win) {                // keys are unique: one list of one lane
-            if (head[0] == win) {
-              head[0] = next;
-              ++pos[0];
-              next = pos[0] + 1 < k ? kr[lane * k + pos[0] + 1] : 0;
-            }
-#pragma unroll
-            for (int q = 1; q < kLists; ++q)
-              if (head[q] == win) {
-                ++pos[q];
-                head[q] = pos[q] < k ? kr[(lane + 32 * q) * k + pos[q]] : 0;
-              }
-          }
-          last = win;
-          if (lane == 0) list[w][got] = win;
-        }
+        const double v = (double)m + log_of(t, 38);
+        if (lane == 0) lse[w] = v;
       }
-    } else if (done && sc > -INFINITY) {
-      if (lane == 0) list[w][0] = ~0ull;           // the end token at the beam's score
-      got = 1;
     }
-    if (lane == 0) list[w][got] = 0;
+  }
+  __syncthreads();
+  for (int i = tid; i < a.win * k; i += kJoinThreads) {
+    const int w = i / k, r = i - w * k;
+    const unsigned long long key = list[w][r];
+    if (key == 0) continue;
+    const long long row = (long long)b * a.win + w;
+    const double sc = (double)scores[row];
+    const bool done = finished && finished[row];
+    list[w][r] = ordered64(done ? sc : sc + ((double)key_value(key) - lse[w]));
+    index[w][r] = (uint32_t)w * (uint32_t)a.vocab + (done ? (uint32_t)a.eos : key_index(key));
   }
   __syncthreads();
   if (tid >= 32) return;
   // lane = beam: its next candidate's score and flattened index
-  const long long row = (long long)b * a.win + lane;
   const bool mine = lane < a.win;
-  const double sc = mine ? (double)scores[row] : 0.0;
+  const long long row = (long long)b * a.win + lane;
   const bool done = mine && finished && finished[row];
-  double lse = 0.0;
-  if (mine && !done && list[lane][0] != 0) lse = (double)top[lane] + log_of(total[lane], 38);
   int pos = 0;
-  unsigned long long cs = 0;
-  uint32_t ci = 0xFFFFFFFFu;
-  auto take = [&]() {
-    const unsigned long long key = mine ? list[lane][pos] : 0;
-    cs = 0;
-    ci = 0xFFFFFFFFu;
-    if (key != 0) {
-      cs = ordered64(done ? sc : sc + ((double)key_value(key) - lse));
-      ci = (uint32_t)lane * (uint32_t)a.vocab + (done ? (uint32_t)a.eos : key_index(key));
-    }
-  };
-  take();
+  unsigned long long cs = mine ? list[lane][0] : 0;
+  uint32_t ci = cs != 0 ? index[lane][0] : 0xFFFFFFFFu;
   for (int r = 0; r < k; ++r) {
     const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(cs >> 32));
     const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(cs >> 32) == hi ? (uint32_t)cs : 0u);
@@ -502,7 +512,8 @@ __global__ void __launch_bounds__(kJoinThreads)
       scores_out[o] = (float)__longlong_as_double((long long)u);
       if (finished_out) finished_out[o] = done || v == a.eos;
       ++pos;
-      take();
+      cs = pos < k ? list[lane][pos] : 0;
+      ci = cs != 0 ? index[lane][pos] : 0xFFFFFFFFu;
     }
   }
 }

@@ -15,6 +15,7 @@ namespace tree_exact {
 constexpr int kHeads = 4, kPerHead = 128;          // heads per CTA, threads of each
 constexpr int kThreads = kHeads * kPerHead, kWarps = kThreads / 32;
 constexpr int kMaxCols = 1024 / kThreads;
+constexpr int kMaxCluster = 4;                      // CTAs that share a token's keys
 constexpr int kMaxKeys = 128;                      // keys per tile at most
 constexpr int kStageFloats = 12 * 1024;            // 48 KB of keys
 __host__ __device__ inline int row_pitch(int d_qk) { return (d_qk + 3) / 4 * 4 + 4; }  // 16-byte rows, spread over the banks
@@ -39,38 +40,50 @@ __device__ __forceinline__ float head_reduce(float v, bool take_max, float (*red
                   : (red[head][0] + red[head][1]) + (red[head][2] + red[head][3]);
 }
 
+__device__ __forceinline__ float4 ld_peer4(const float4* local, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(mapa_shared(smem_u32(local), rank))
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// One CTA per (token, four heads).  Keys in tiles of `kt` rows (a power of two
+// One CTA per (token, four heads), or a cluster of them that takes the tiles in turn
+// and joins in rank order through distributed shared memory.  Keys in tiles of `kt` rows (a power of two
 // that fits the shared memory), staged row by row, a warp reading a row's
 // consecutive values, all of its rows in flight.  128 threads per head: one or
 // more per key for the logits; for the weighted sum a thread takes a value
 // column of the four heads and every G-th key, and the G groups are added at the
 // end.  A key that the token does not see is not read.  Small shapes: the time is
 // the latency of a few tiles, and issuing their instructions (one head per CTA,
-// staging the keys for itself, took 39 us for the case that takes 25.7 now: five
-// sequences of up to 700 rows, eight heads of 80 / 64 columns).
+// staging the keys for itself, took 39 us for the case that takes 18 now: five
+// sequences of up to 700 rows, seven tokens, eight heads of 80 / 64 columns).
 template <bool VEC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     tree_exact_kernel(TreeArgs a, const float* __restrict__ qg, const uint8_t* __restrict__ pool, long long page_stride,
                       const float* __restrict__ kvn, float* __restrict__ out, float* __restrict__ mx,
-                      float* __restrict__ sm_out, int kt, DevCtx c) {
+                      float* __restrict__ sm_out, int kt, int nc, DevCtx c) {
   extern __shared__ __align__(16) float sh[];
   const int pitch = row_pitch(a.d_qk);
   float* qs = sh;                                  // [kHeads][pitch]
   float* ks = sh + kHeads * pitch;                 // [kt][pitch]
   __shared__ __align__(16) float p[kMaxKeys][kHeads];
   __shared__ float4 sums[kThreads];
-  __shared__ float red[kHeads][4], alpha_s[kHeads], l_s[kHeads];
+  __shared__ float red[kHeads][4], alpha_s[kHeads];
+  __shared__ __align__(16) float l_s[kHeads], m_s[kHeads];
   __shared__ const float* rows[kMaxKeys];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   let_next_launch();
   wait_for_earlier();
   const int hgroups = (a.H + kHeads - 1) / kHeads;
-  const long long t = blockIdx.x / hgroups;
-  const int h0 = (blockIdx.x % hgroups) * kHeads, nh = a.H - h0 < kHeads ? a.H - h0 : kHeads;
+  const uint32_t rank = cluster_ctarank();
+  const unsigned item = blockIdx.x / nc;
+  const long long t = item / hgroups;
+  const int h0 = (item % hgroups) * kHeads, nh = a.H - h0 < kHeads ? a.H - h0 : kHeads;
   if (blockIdx.x == 0) {
     bool wrong = false;
     for (int b = tid; b < a.n_seqs; b += kThreads) tree_seq(a, b, &wrong);
@@ -114,8 +127,9 @@ __global__ void __launch_bounds__(kThreads)
   float4 o[kMaxCols];
 #pragma unroll
   for (int u = 0; u < kMaxCols; ++u) o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float* mine = tid < kt ? key_row(tid) : nullptr;
-  for (long long k0 = 0; k0 < keys; k0 += kt) {
+  const long long step = (long long)nc * kt;
+  const float* mine = tid < kt ? key_row((long long)rank * kt + tid) : nullptr;
+  for (long long k0 = (long long)rank * kt; k0 < keys; k0 += step) {
     const int n = keys - k0 < kt ? (int)(keys - k0) : kt;
     __syncthreads();                               // the last tile is read
     if (tid < kt) rows[tid] = mine;
@@ -135,7 +149,7 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
     }
-    if (tid < kt) mine = key_row(k0 + kt + tid);   // of the next tile, while this one is worked on
+    if (tid < kt) mine = key_row(k0 + step + tid);   // of the next tile, while this one is worked on
     cp_async_wait_all();
     __syncthreads();
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -193,6 +207,64 @@ __global__ void __launch_bounds__(kThreads)
       o[0].z += v.z;
       o[0].w += v.w;
     }
+  }
+  if (nc > 1) {
+    // every CTA's sums (columns of the four heads), maxima and denominators
+    float4* part = reinterpret_cast<float4*>(ks);  // [d_v]
+    if (group == 0)
+      for (int u = 0; u < kMaxCols && col + u * kThreads < a.d_v; ++u) part[col + u * kThreads] = o[u];
+    if (th == 0) m_s[head] = m_run;
+    cluster_sync_all();
+    if (rank == 0) {
+      float M[kHeads], l[kHeads], w[kMaxCluster][kHeads];
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h) M[h] = -INFINITY, l[h] = 0.f;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        if (r >= nc) break;
+        const float4 m = ld_peer4(reinterpret_cast<const float4*>(m_s), r);
+        w[r][0] = m.x, w[r][1] = m.y, w[r][2] = m.z, w[r][3] = m.w;
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) M[h] = fmaxf(M[h], w[r][h]);
+      }
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        if (r >= nc) break;
+        const float4 p4 = ld_peer4(reinterpret_cast<const float4*>(l_s), r);
+        const float lr[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) {
+          w[r][h] = expf(w[r][h] - (M[h] == -INFINITY ? 0.f : M[h]));  // no key: exp(-inf) = 0
+          l[h] = fmaf(w[r][h], lr[h], l[h]);
+        }
+      }
+      if (group == 0) {
+#pragma unroll
+        for (int u = 0; u < kMaxCols; ++u) {
+          const int d = col + u * kThreads;
+          if (d >= a.d_v) break;
+          float v[kHeads] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r) {
+            if (r >= nc) break;
+            const float4 p4 = ld_peer4(part + d, r);
+            v[0] = fmaf(w[r][0], p4.x, v[0]);
+            v[1] = fmaf(w[r][1], p4.y, v[1]);
+            v[2] = fmaf(w[r][2], p4.z, v[2]);
+            v[3] = fmaf(w[r][3], p4.w, v[3]);
+          }
+#pragma unroll
+          for (int h = 0; h < kHeads; ++h)
+            if (h < nh) out[(row + h) * a.d_v + d] = l[h] == 0.f ? 0.f : v[h] / l[h];
+        }
+      }
+      if (tid < nh) {
+        mx[row + tid] = tid == 0 ? M[0] : tid == 1 ? M[1] : tid == 2 ? M[2] : M[3];
+        sm_out[row + tid] = tid == 0 ? l[0] : tid == 1 ? l[1] : tid == 2 ? l[2] : l[3];
+      }
+    }
+    cluster_sync_all();                            // rank 0 has read the others' memory
+    return;
   }
   if (group == 0) {
 #pragma unroll
@@ -290,12 +362,24 @@ int dsa_tree_attn_fwd(const dsa_cache* p, const dsa_tree* t, const void* q, cons
   auto kernel = vec ? tree_exact_kernel<true> : tree_exact_kernel<false>;
   const int kt = tile_keys((int)t->d_qk);
   const size_t smem = (size_t)(kt + kHeads) * row_pitch((int)t->d_qk) * sizeof(float);
-  const unsigned grid = (unsigned)(t->n_tok * ((t->H + kHeads - 1) / kHeads));
+  const long long items = t->n_tok * ((t->H + kHeads - 1) / kHeads);
+  // CTAs per item: as many as are resident at once, two per SM, if the cache can hold
+  // more than a tile.  One CTA against several, d_qk 80: 2 items x 4000 rows 133 us
+  // against 38 (4 CTAs), 72 x 700 rows 31 against 19 (4), 128 x 700 rows 37 against
+  // 24 (2); one tile each 72 items 8.8 against 12 (4); with more CTAs than are
+  // resident 160 x 700 rows 38 against 45 (4).
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  int nc = p->max_pages * p->page_rows > kt ? kMaxCluster : 1;
+  while (nc > 1 && items * nc > 2ll * sms) nc /= 2;
+  const unsigned grid = (unsigned)(items * nc);
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return DSA_ERR_CUDA;
-  return launch_programmatic(kernel, dim3(grid), dim3(kThreads), smem, st, 1, a,
+  return launch_programmatic(kernel, dim3(grid), dim3(kThreads), smem, st, nc, a,
                              (const float*)q, (const uint8_t*)pool->base, (long long)pool->page_stride,
-                             (const float*)kv_new, (float*)out, softmax_max, softmax_sum, kt, c)
+                             (const float*)kv_new, (float*)out, softmax_max, softmax_sum, kt, nc, c)
              ? DSA_OK
              : DSA_ERR_CUDA;
 }
