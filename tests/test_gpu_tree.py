@@ -340,3 +340,20 @@ def test_refused_calls():
         dsa.tree_attn_fwd(base[0], base[1], c.q[:1], *base[3:])
     with pytest.raises(TypeError):
         dsa.tree_attn_fwd(base[0], base[1], c.q.half(), *base[3:])
+
+
+@pytest.mark.parametrize("H,T", [(4, [3, 1, 2]), (4, [40, 21, 39]), (9, [30, 20, 34])])
+def test_fp32_with_keys_shared_by_four_two_and_one_cta(H, T):
+    dsa = lib()
+    Case([701, 0, 130], T, H, R=16, kind="any", d_qk=80, d_v=64, dtype=torch.float32, seed=H).run(dsa).check()
+    Case([1500, 40, 129], T, H, R=1, d_qk=33, d_v=7, dtype=torch.float32, seed=H + 1).run(dsa).check()
+
+
+@pytest.mark.parametrize("H,T,R,kind", [(128, 1, 64, "chain"), (16, 9, 32, "tree"), (128, 3, 96, "any")])
+def test_bad_pages_between_full_blocks(H, T, R, kind):
+    dsa = lib()
+    c = Case([2000, 5000, 111], T, H, R=R, kind=kind, seed=R)
+    for i, js in ((0, (0, 7)), (1, (3, 20, 21, 4999 // R))):
+        for j in js:
+            c.table[i][j] = (-3, c.pool.shape[0])[j % 2]
+    c.run(dsa, status=dsa.DSA_ERR_INDEX).check()
