@@ -53,12 +53,12 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 }
 
 // One CTA per (token, four heads), or a cluster of them that takes the tiles in turn
-// and joins in rank order through distributed shared memory.  Keys in tiles of `kt` rows (a power of two
-// that fits the shared memory), staged row by row, a warp reading a row's
-// consecutive values, all of its rows in flight.  128 threads per head: one or
-// more per key for the logits; for the weighted sum a thread takes a value
-// column of the four heads and every G-th key, and the G groups are added at the
-// end.  A key that the token does not see is not read.  Small shapes: the time is
+// and joins in rank order through distributed shared memory.  Keys in tiles of `kt`
+// rows (a power of two that fits the shared memory), staged row by row, a warp
+// reading a row's consecutive values, all of its rows in flight.  128 threads per
+// head: one or more per key for the logits; for the weighted sum a thread takes a
+// value column of the four heads and every G-th key, and the G groups are added at
+// the end.  A key that the token does not see is not read.  Small shapes: the time is
 // the latency of a few tiles, and issuing their instructions (one head per CTA,
 // staging the keys for itself, took 39 us for the case that takes 18 now: five
 // sequences of up to 700 rows, seven tokens, eight heads of 80 / 64 columns).

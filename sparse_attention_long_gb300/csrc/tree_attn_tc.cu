@@ -284,6 +284,11 @@ __device__ __forceinline__ long long warp_sum(long long v) {
   return v;
 }
 
+// a / b for a >= 0, b > 0 (a 64-bit division takes one thread some 600 cycles)
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // ---- schedule: tiles and blocks of a sequence ----
 struct Plan {
   int tiles, nc, nd;                               // query tiles; cached / drafted blocks (all tokens)
@@ -303,8 +308,8 @@ __device__ __forceinline__ Plan make_plan(const TreeArgs& a, const TreeSeq& s) {
 // blocks of one tile: a chain's tokens see no drafted row behind themselves
 __device__ __forceinline__ int tile_blocks(const Plan& p, int tile) {
   if (!p.chain) return p.nc + p.nd;
-  const long long last = (128ll * tile + 127) / p.H;
-  return p.nc + (int)(last < p.T - 1 ? last : p.T - 1) / kBlk + 1;
+  const int last = (int)((128u * (uint32_t)tile + 127u) / (uint32_t)p.H);
+  return p.nc + (last < p.T - 1 ? last : p.T - 1) / kBlk + 1;
 }
 // blocks of the first r tiles.  Chain: tile r' runs over drafted block k iff
 // (128 r' + 127) / H >= 112 k, i.e. r' >= 112 k H / 128 (both rounded down).
@@ -337,16 +342,18 @@ struct Schedule {
   __device__ __forceinline__ void start(const TreeArgs& a, int pair, int npairs, const DevCtx& c) {
     const int lane = threadIdx.x & 31;
     bool wrong = false;
-    long long total = 0;
+    long long total = 0, cost = 0;                 // cost: of the last 32 sequences
     for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
+      cost = 0;
       if (b0 + lane < a.n_seqs) {
         const Plan q = make_plan(a, tree_seq(a, b0 + lane, &wrong));
-        total += tiles_cost(q, q.tiles);
+        cost = tiles_cost(q, q.tiles);
       }
+      total += cost;
     }
     total = warp_sum(total);
     if (__any_sync(0xffffffffu, wrong) && lane == 0) set_status(c, DSA_ERR_INDEX);
-    run = (total + npairs - 1) / npairs;
+    run = div_pos(total + npairs - 1, npairs);
     x = run * pair;
     x1 = x + run < total ? x + run : total;
     join = {0, 0, 0};
@@ -355,10 +362,12 @@ struct Schedule {
     b = 0;
     long long off = x;
     for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
-      long long cost = 0;
-      if (b0 + lane < a.n_seqs) {
-        const Plan q = make_plan(a, tree_seq(a, b0 + lane, &wrong));
-        cost = tiles_cost(q, q.tiles);
+      if (a.n_seqs > 32) {
+        cost = 0;
+        if (b0 + lane < a.n_seqs) {
+          const Plan q = make_plan(a, tree_seq(a, b0 + lane, &wrong));
+          cost = tiles_cost(q, q.tiles);
+        }
       }
       long long incl = cost;
 #pragma unroll
@@ -378,8 +387,8 @@ struct Schedule {
     s = tree_seq(a, b, &wrong);
     p = make_plan(a, s);
     if (!p.chain) {
-      tile = (int)(off / (p.nc + p.nd));
-      j = (int)(off % (p.nc + p.nd));
+      tile = (int)div_pos(off, p.nc + p.nd);
+      j = (int)(off - (long long)tile * (p.nc + p.nd));
     } else {
       int lo = 0, hi = p.tiles;                    // cost(lo) <= off < cost(hi)
       while (hi - lo > 1) {
@@ -422,7 +431,7 @@ struct Schedule {
       const long long rows = (long long)s.T * a.H - 128ll * tile;
       join.row0 = (long long)s.t0 * a.H + 128ll * tile;
       join.nrows = rows < kTile ? (int)rows : kTile;
-      join.nparts = (int)((x + nb - 1) / run) - pair + 1;
+      join.nparts = (int)div_pos(x + nb - 1, run) - pair + 1;
     }
     x += j1 - j;
     j = 0;
