@@ -20,14 +20,15 @@
 // Candidates of different beams can lie close together, and their order is an
 // output: the sums are fp32 only inside a thread, a warp adds them as integers
 // (2^-40 of its largest term: the order does not matter), everything after that
-// is fp64.  A row gives the same bits wherever it lies:
-// which element a thread takes depends on its index alone, not on alignment.
+// is fp64 but for the logarithm of a number near 1.  A row gives the same bits
+// wherever it lies: which element a thread takes depends on its index alone, not
+// on alignment.
 //
 // Bound: for a batch, the logits' way from HBM and some 10 instructions per logit,
 // of which the CTAs of a wave do first the one and then the other: 64 x 8 beams x
-// 131071 bf16 take 32 us, 4.2 TB/s; the first kernel alone 25 us, 5.4 TB/s.
+// 131071 bf16 take 31 us, 4.4 TB/s; the first kernel alone 25 us, 5.4 TB/s.
 // Loading the next chunk ahead of the sums took more registers than it gave.  One
-// request of 4 x 32001: 7.3 us, the two launches and their latencies.
+// request of 4 x 32001: 6.3 us, the two launches and their latencies.
 #include <math.h>
 
 #include "dsa_common.cuh"
@@ -348,39 +349,79 @@ __device__ __forceinline__ unsigned long long ordered64(double x) {
   return (unsigned long long)u ^ ((unsigned long long)(u >> 63) | 0x8000000000000000ull);
 }
 
-// ln(t 2^-unit) for t >= 2^(unit-1).  fp64 instructions are slow here (some 15
-// cycles of the SM each), so few of them: t = f 2^e with f in [0.707, 1.414],
-// ln f = 2 artanh s, s = (f - 1) / (f + 1), |s| < 0.172, by its power series up
-// to s^17 (the next term is below 2^-50 of the first).
+// ln(t 2^-unit) for t >= 2^(unit-1): t = f 2^e with f in [0.707, 1.414], whose
+// logarithm is below 0.35, so that fp32 gives it to 2^-24, a fourth of the terms'
+// own error; the rest is fp64 (all of it in fp64, instructions of some 50 cycles one
+// after another, took half a microsecond more).
 __device__ __forceinline__ double log_of(unsigned long long t, int unit) {
   int e = 63 - __clzll((long long)t);
-  const unsigned long long frac = e > 52 ? t >> (e - 52) : t << (52 - e);  // 53 bits, the first one 1
-  double f = __longlong_as_double((long long)((frac & 0xFFFFFFFFFFFFFull) | 0x3FF0000000000000ull));
-  if (f > 1.4142135623730951) {
-    f *= 0.5;
+  const unsigned long long frac = e > 23 ? t >> (e - 23) : t << (23 - e);  // 24 bits, the first one 1
+  float f = __uint_as_float(((uint32_t)frac & 0x7FFFFFu) | 0x3F800000u);
+  if (f > 1.41421356f) {
+    f *= 0.5f;
     ++e;
   }
-  const double s = (f - 1.0) / (f + 1.0), z = s * s;
-  double p = 1.0 / 17.0;
-  p = fma(p, z, 1.0 / 15.0);
-  p = fma(p, z, 1.0 / 13.0);
-  p = fma(p, z, 1.0 / 11.0);
-  p = fma(p, z, 1.0 / 9.0);
-  p = fma(p, z, 1.0 / 7.0);
-  p = fma(p, z, 1.0 / 5.0);
-  p = fma(p, z, 1.0 / 3.0);
-  p = fma(p, z, 1.0);
-  return fma((double)(e - unit), 0.6931471805599453, 2.0 * s * p);
+  return fma((double)(e - unit), 0.6931471805599453, (double)logf(f));
+}
+
+// A beam's `k` best keys out of its chunks' sorted lists kr[chunk][k] (one warp, a
+// lane has NL lists); how many there are.
+template <int NL>
+__device__ __forceinline__ int merge_lists(const unsigned long long* kr, int chunks, int k, unsigned long long* list) {
+  const int lane = threadIdx.x & 31;
+  int pos[NL];
+  unsigned long long head[NL];
+#pragma unroll
+  for (int q = 0; q < NL; ++q) {
+    pos[q] = 0;
+    head[q] = lane + 32 * q < chunks ? kr[(lane + 32 * q) * k] : 0;
+  }
+  int got = 0;
+  for (; got < k; ++got) {
+    unsigned long long best = head[0];
+#pragma unroll
+    for (int q = 1; q < NL; ++q) best = head[q] > best ? head[q] : best;
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+    const unsigned long long win = ((unsigned long long)hi << 32) | lo;
+    if (win == 0) break;
+    if (best == win) {                             // keys are unique: one list of one lane
+      list[got] = win;
+#pragma unroll
+      for (int q = 0; q < NL; ++q)
+        if (head[q] == win) head[q] = ++pos[q] < k ? kr[(lane + 32 * q) * k + pos[q]] : 0;
+    }
+  }
+  return got;
+}
+// the same for any number of chunks: each time the largest key below the last one
+__device__ __forceinline__ int merge_any(const unsigned long long* kr, int chunks, int k, unsigned long long* list) {
+  const int lane = threadIdx.x & 31;
+  unsigned long long last = ~0ull;
+  int got = 0;
+  for (; got < k; ++got) {
+    unsigned long long best = 0;
+    for (int i = lane; i < chunks * k; i += 32) {
+      const unsigned long long v = kr[i];
+      if (v < last && v > best) best = v;
+    }
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+    last = ((unsigned long long)hi << 32) | lo;
+    if (last == 0) break;
+    if (lane == 0) list[got] = last;
+  }
+  return got;
 }
 
 // One CTA per request.  Per beam, one warp merges its chunks' sorted lists (lane =
 // chunk and every 32nd after it, the largest head taken each time) while another
-// adds the chunks' sums and takes the logarithm; then all threads compute the
-// candidates' scores, and one warp merges the beams (lane = beam), whose lists are
-// sorted by score, too.  Bound: latency, of the fp64 logarithm and of 2 beams_out
-// rounds of warp reductions; the lists are read from global memory once, all loads
-// in flight, where they fit (with a load per round, sum and merge in one warp, one
-// request took 8.6 us in all, 7.3 now).
+// adds the chunks' sums and takes the logarithm; then every candidate has a thread,
+// which computes its score and, by a binary search in each beam's list, its place.
+// Bound: latency, of which beams_out rounds of warp reductions are the most; the
+// lists are read from global memory once, all loads in flight, where they fit (with a
+// load per round, sum and merge in one warp, and the beams merged by a warp, one
+// request took 8.6 us in all, 6.3 now).
 constexpr int kJoinWarps = 8, kJoinThreads = 2 * 32 * kJoinWarps;
 constexpr int kLists = 4;                           // per lane: 128 chunks, 1M (bf16) or 512K logits
 constexpr int kKeyRoom = 512;                       // keys per warp
@@ -391,7 +432,7 @@ __global__ void __launch_bounds__(kJoinThreads)
                      uint8_t* __restrict__ finished_out) {
   __shared__ unsigned long long room[kJoinWarps][kKeyRoom];
   __shared__ unsigned long long list[kMaxBeams][kMaxBeams + 1];  // best first: keys, then ordered scores; 0: none
-  __shared__ uint32_t index[kMaxBeams][kMaxBeams + 1];
+  __shared__ int32_t index[kMaxBeams][kMaxBeams];  // their tokens
   __shared__ double lse[kMaxBeams];
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, k = a.wout;
   const int wj = (tid >> 5) % kJoinWarps;
@@ -412,41 +453,11 @@ __global__ void __launch_bounds__(kJoinThreads)
         __syncwarp();
         kr = room[wj];
       }
-      const bool few = a.chunks <= 32 * kLists;
-      int pos[kLists];
-      unsigned long long head[kLists];             // of this lane's lists
-#pragma unroll
-      for (int q = 0; q < kLists; ++q) {
-        pos[q] = 0;
-        head[q] = open && few && lane + 32 * q < a.chunks ? kr[(lane + 32 * q) * k] : 0;
-      }
-      unsigned long long last = ~0ull;
       int got = 0;
-      for (; got < k && open; ++got) {
-        unsigned long long best = head[0];
-#pragma unroll
-        for (int q = 1; q < kLists; ++q) best = head[q] > best ? head[q] : best;
-        if (!few) {                                // the largest key below the last one taken
-          best = 0;
-          for (int i = lane; i < have; i += 32) {
-            const unsigned long long v = kr[i];
-            if (v < last && v > best) best = v;
-          }
-        }
-        const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
-        const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
-        const unsigned long long win = ((unsigned long long)hi << 32) | lo;
-        if (win == 0) break;
-        if (few && best == win) {                  // keys are unique: one list of one lane
-#pragma unroll
-          for (int q = 0; q < kLists; ++q)
-            if (head[q] == win) {
-              ++pos[q];
-              head[q] = pos[q] < k ? kr[(lane + 32 * q) * k + pos[q]] : 0;
-            }
-        }
-        last = win;
-        if (lane == 0) list[w][got] = win;
+      if (open) {
+        got = a.chunks <= 32            ? merge_lists<1>(kr, a.chunks, k, list[w])
+              : a.chunks <= 32 * kLists ? merge_lists<kLists>(kr, a.chunks, k, list[w])
+                                        : merge_any(kr, a.chunks, k, list[w]);
       }
       if (done && sc > -INFINITY) {
         if (lane == 0) list[w][0] = ~0ull;         // the end token at the beam's score
@@ -483,40 +494,45 @@ __global__ void __launch_bounds__(kJoinThreads)
     const double sc = (double)scores[row];
     const bool done = finished && finished[row];
     list[w][r] = ordered64(done ? sc : sc + ((double)key_value(key) - lse[w]));
-    index[w][r] = (uint32_t)w * (uint32_t)a.vocab + (done ? (uint32_t)a.eos : key_index(key));
+    index[w][r] = done ? a.eos : (int)key_index(key);
   }
   __syncthreads();
-  if (tid >= 32) return;
-  // lane = beam: its next candidate's score and flattened index
-  const bool mine = lane < a.win;
-  const long long row = (long long)b * a.win + lane;
-  const bool done = mine && finished && finished[row];
-  int pos = 0;
-  unsigned long long cs = mine ? list[lane][0] : 0;
-  uint32_t ci = cs != 0 ? index[lane][0] : 0xFFFFFFFFu;
-  for (int r = 0; r < k; ++r) {
-    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(cs >> 32));
-    const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(cs >> 32) == hi ? (uint32_t)cs : 0u);
-    const unsigned long long best = ((unsigned long long)hi << 32) | lo;
-    const uint32_t id = __reduce_min_sync(0xffffffffu, cs == best ? ci : 0xFFFFFFFFu);
-    const long long o = (long long)b * k + r;
-    if (id == 0xFFFFFFFFu) {                       // too few candidates
-      if (lane == 0) {
-        parent[o] = token[o] = -1;
-        scores_out[o] = -INFINITY;
-        if (finished_out) finished_out[o] = 0;
+  // a candidate's place: how many of every beam's (sorted) list are better.  Equal
+  // scores: the lower beam, within a beam the list's order.
+  const int items = a.win * k;
+  int n = 0;
+  for (int i0 = 0; i0 < items; i0 += kJoinThreads) {
+    const int i = i0 + tid, w = i / k, r = i - w * k;
+    const unsigned long long cs = i < items ? list[w][r] : 0;
+    n += __syncthreads_count(cs != 0);
+    if (cs == 0) continue;
+    int place = r;
+#pragma unroll 4
+    for (int v = 0; v < a.win; ++v) {
+      if (v == w) continue;
+      const unsigned long long least = v < w ? cs : cs + 1;  // scores from here on are better
+      int lo = 0, hi = k;                          // entries below lo are better, from hi on they are not
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (list[v][mid] >= least) lo = mid + 1;
+        else hi = mid;
       }
-    } else if (ci == id) {
-      const int v = (int)(id - (uint32_t)lane * (uint32_t)a.vocab);
-      const unsigned long long u = (cs & 0x8000000000000000ull) ? cs ^ 0x8000000000000000ull : ~cs;
-      parent[o] = (int32_t)row;
-      token[o] = v;
-      scores_out[o] = (float)__longlong_as_double((long long)u);
-      if (finished_out) finished_out[o] = done || v == a.eos;
-      ++pos;
-      cs = pos < k ? list[lane][pos] : 0;
-      ci = cs != 0 ? index[lane][pos] : 0xFFFFFFFFu;
+      place += lo;
     }
+    if (place >= k) continue;
+    const long long o = (long long)b * k + place, row = (long long)b * a.win + w;
+    const int v = index[w][r];
+    const unsigned long long u = (cs & 0x8000000000000000ull) ? cs ^ 0x8000000000000000ull : ~cs;
+    parent[o] = (int32_t)row;
+    token[o] = v;
+    scores_out[o] = (float)__longlong_as_double((long long)u);
+    if (finished_out) finished_out[o] = (finished && finished[row]) || v == a.eos;
+  }
+  for (int r = n + tid; r < k; r += kJoinThreads) {  // too few candidates
+    const long long o = (long long)b * k + r;
+    parent[o] = token[o] = -1;
+    scores_out[o] = -INFINITY;
+    if (finished_out) finished_out[o] = 0;
   }
 }
 

@@ -5,8 +5,8 @@ them equal exactly).  Scores: a term exp(-d), d = max - x, has a relative error
 of at most d 2^-23 (the roundings of d and of d log2 e) + 2^-22 (the
 exponential's own 2 units), so the sum is off by the mean of that over the
 softmax's weights.  The mean of d is below 5 for every input here (some 4.5
-for the normal logits of deviation 2.5), which gives
-less than 2^-20 for the logarithm; then the score is rounded to fp32.
+for the normal logits of deviation 2.5), which gives less than 2^-20 for the
+logarithm, its own error of 2^-24 included; then the score is rounded to fp32.
 """
 import math
 import random
@@ -187,3 +187,15 @@ def test_long_vocabularies(W, V, keep, dtype):
     x = rand(1, W, V, seed=V)
     x[0, 0, V - 40:] += 12.0                     # many of the best in the last chunk, some in others
     check(dsa, x, [[-1.5] * W], None, keep, -1, dtype=dtype)
+
+
+def test_scores_too_large_to_tell_logits_apart():
+    """fp64 rounds every candidate of a beam to the beam's score: within the beam the logits'
+    order holds, equal beams go by number, and every place is filled."""
+    dsa = lib()
+    x = rand(2, 3, 5000, seed=3)
+    got = run(dsa, x, [[-1e30, -1e30, -2e30], [-2e30, -1e30, -1e30]], None, 7, -1)
+    for b, w in ((0, 0), (1, 1)):
+        best = x[b, w].float().topk(7).indices.tolist()
+        assert [(p, t) for p, t, _, _ in got[b]] == [(3 * b + w, t) for t in best]
+        assert all(s == float(torch.tensor(-1e30)) for _, _, s, _ in got[b])
