@@ -1202,7 +1202,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_after();
       if (g.part >= 0) {
         // part of a tile: O as it stands, [column quad][row] so that a warp's
-        // 32 rows make whole lines
+        // 32 rows make whole lines.  128 KB for 64 rows at the 32 bytes per cycle that
+        // an SM writes (by any kind of store): 4,100 cycles.
         float4* po = parts + (size_t)g.part * (kTile * kDV / 4) + rr;
         const uint64_t stay = policy_stay();
 #pragma unroll 1
@@ -1211,12 +1212,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tmem_ld32(tmem + lane_off + kColO + 128 * m + 32 * ch, o);
           tmem_ld_wait(o);
           const int quad0 = (256 * half + 128 * m + 32 * ch) / 4;
+          if (!live) continue;
 #pragma unroll
           for (int t = 0; t < 8; ++t)
             st_part(po + (size_t)(quad0 + t) * kTile, __uint_as_float(o[4 * t]), __uint_as_float(o[4 * t + 1]),
                     __uint_as_float(o[4 * t + 2]), __uint_as_float(o[4 * t + 3]), stay);
         }
-        if (half == 0 && ch == 0) stats[(size_t)g.part * kTile + rr] = make_float4(m_run, lsum, m_true, 0.f);
+        if (half == 0 && ch == 0 && live) stats[(size_t)g.part * kTile + rr] = make_float4(m_run, lsum, m_true, 0.f);
       } else {
         const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // no visible key: 0
         const long long row0 = (long long)g.t0 * a.H + 128ll * g.tile + kHC * (int)crank;  // first row of this CTA
@@ -1359,7 +1361,8 @@ __device__ __forceinline__ void join_store(const Joined& j, long long r, int q, 
   }
 }
 
-__global__ void __launch_bounds__(kJoinThreads)
+// (three CTAs per SM: 93 registers and two took 3 us more for 64 tokens)
+__global__ void __launch_bounds__(kJoinThreads, 3)
     tree_join_kernel(const float4* __restrict__ parts, const float4* __restrict__ stats,
                      const Join* __restrict__ joins, int npairs, __nv_bfloat16* __restrict__ out,
                      float* __restrict__ mx, float* __restrict__ sm_out) {
@@ -1399,13 +1402,14 @@ __global__ void __launch_bounds__(kJoinThreads)
     const int pair = list_pair[i], k = piece - base;
     if (jn.nparts <= kJoinFew) {                   // 128 rows x 2 x 8 columns
       const int row = tid & 127, q = 4 * k + 2 * (tid >> 7);
-      const Joined j = join_parts(parts, stats, pair, jn.nparts, 0, 1, row, q);
-      if (row < jn.nrows) join_store(j, jn.row0 + row, q, out, mx, sm_out);
+      if (row < jn.nrows)
+        join_store(join_parts(parts, stats, pair, jn.nparts, 0, 1, row, q), jn.row0 + row, q, out, mx, sm_out);
       continue;
     }
     // 64 rows x 8 columns, four threads each
     const int cell = tid & 63, row = (k & 1) * 64 + cell, q = 2 * (k >> 1), g = tid >> 6;
-    Joined j = join_parts(parts, stats, pair, jn.nparts, g, kJoinGroups, row, q);
+    Joined j;
+    if (row < jn.nrows) j = join_parts(parts, stats, pair, jn.nparts, g, kJoinGroups, row, q);
     __syncthreads();                               // the last piece's sums are read
     if (g > 0) shared[g - 1][cell] = j;
     __syncthreads();
