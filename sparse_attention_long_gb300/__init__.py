@@ -239,8 +239,35 @@ def forward_static_ws(p, q_I, k_I, w, q, kv, idx_out, out, softmax_max, softmax_
 
 
 # ------------------------------- paged cache -------------------------------
-# These calls are made once or several times per generated token, so their
-# checks are kept to a few attribute reads per tensor; _refuse says what is wrong.
+# These calls are made once or several times per generated token.  _native makes
+# them in a few hundred nanoseconds on top of the launch; it answers 1, having
+# done nothing, when an argument is not exactly what the call needs or a stream
+# is given.  The Python code below it then makes the call or says what is wrong.
+class _Absent:
+    def __getattr__(self, name):
+        return lambda *args: 1
+
+
+def _load_native():
+    try:
+        from . import _binding
+    except ImportError:                            # built without PyTorch's or Python's headers
+        return _Absent()
+    names = ("dsa_cache_fork", "dsa_cache_extend", "dsa_cache_compact", "dsa_cache_copy_pages", "dsa_cache_write",
+             "dsa_tree_attn_fwd", "dsa_tree_workspace_size", "dsa_beam_select", "dsa_beam_workspace_size")
+    _binding.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names), dsa_cache, dsa_tree, dsa_beam)
+    return _binding
+
+
+_native = _load_native()
+
+
+def _made(rc, where):
+    if rc < 0:
+        raise DSAError(rc, where)
+    return rc == 0
+
+
 def _refuse(where, name, t, dtype, numel, device, at_least=False):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{where}: {name} must be a torch.Tensor")
@@ -330,6 +357,9 @@ def cache_fork(c, parent, table, lens, refs, table_out, lens_out, refs_out, copi
     """Sequence i becomes a copy of old sequence parent[i] (-1: emptied); full pages are shared.
     Follow with cache_copy_pages(copies, n_copies) on every pool."""
     w = "dsa_cache_fork"
+    if stream is None and _made(_native.cache_fork(c, parent, table, lens, refs, table_out, lens_out, refs_out, copies,
+                                                   n_copies), w):
+        return
     d, n, t, p = _device(parent, w, "parent"), c.n_seqs, c.n_seqs * c.max_pages, c.n_pages
     _call(lib.dsa_cache_fork, w, d, stream, ctypes.byref(c), _arg(parent, "parent", _I32, n, d, w),
           _arg(table, "table", _I32, t, d, w), _arg(lens, "lens", _I32, n, d, w), _arg(refs, "refs", _I32, p, d, w),
@@ -342,6 +372,8 @@ def cache_extend(c, n_new, table, lens, refs, lens_out, refs_out, slots, stream=
     """Takes pages for n_new[i] further rows of each sequence (table in place; lens_out and
     refs_out may be lens and refs) and writes the slots of the new rows, -1 behind the last."""
     w = "dsa_cache_extend"
+    if stream is None and _made(_native.cache_extend(c, n_new, table, lens, refs, lens_out, refs_out, slots), w):
+        return
     d, n, p = _device(n_new, w, "n_new"), c.n_seqs, c.n_pages
     _call(lib.dsa_cache_extend, w, d, stream, ctypes.byref(c), _arg(n_new, "n_new", _I32, n, d, w),
           _arg(table, "table", _I32, n * c.max_pages, d, w), _arg(lens, "lens", _I32, n, d, w),
@@ -353,6 +385,9 @@ def cache_compact(c, table, lens, refs, table_out, refs_out, page_map, copies, n
     """Moves the used pages to the lowest ids; page_map gives each its new id. Follow with
     cache_copy_pages(copies, n_copies) on every pool (copies: [n_pages // 2 + 1, 3])."""
     w = "dsa_cache_compact"
+    if stream is None and _made(_native.cache_compact(c, table, lens, refs, table_out, refs_out, page_map, copies,
+                                                      n_copies), w):
+        return
     d, n, t, p = _device(table, w, "table"), c.n_seqs, c.n_seqs * c.max_pages, c.n_pages
     _call(lib.dsa_cache_compact, w, d, stream, ctypes.byref(c), _arg(table, "table", _I32, t, d, w),
           _arg(lens, "lens", _I32, n, d, w), _arg(refs, "refs", _I32, p, d, w),
@@ -364,6 +399,8 @@ def cache_compact(c, table, lens, refs, table_out, refs_out, page_map, copies, n
 def cache_copy_pages(c, pool, copies, n_copies, stream=None):
     """Carries out a copy list on a pool tensor [(layers,) n_pages, page_rows, D] of any type."""
     w = "dsa_cache_copy_pages"
+    if stream is None and _made(_native.cache_copy_pages(c, pool, copies, n_copies), w):
+        return
     d = _device(pool, w, "pool")
     pl, _, _ = _pool(c, pool, w)
     _call(lib.dsa_cache_copy_pages, w, d, stream, ctypes.byref(c), ctypes.byref(pl), _list(copies, "copies", 3, d, w),
@@ -374,6 +411,8 @@ def cache_write(c, pool, rows, slots, row_index=None, stream=None):
     """rows [(layers,) n, D] (of the pool's type) to slots [n] of cache_extend; with row_index
     [len(slots)] the row written to slots[i] is rows[row_index[i]]."""
     w = "dsa_cache_write"
+    if stream is None and _made(_native.cache_write(c, pool, rows, slots, row_index), w):
+        return
     d = _device(pool, w, "pool")
     pl, layers, D = _pool(c, pool, w)
     if _device(rows, w, "rows") != d:
@@ -410,6 +449,9 @@ def tree_attn_fwd(c, t, q, pool, table, lens, kv_new, tok_start, mask, out, soft
     kv_new) over its cached rows and the drafted ones that mask [n_tok, mask_words] (int64 bits)
     names; mask None: token t sees drafted tokens 0 .. t."""
     w = "dsa_tree_attn_fwd"
+    if stream is None and _made(_native.tree_attn_fwd(c, t, q, pool, table, lens, kv_new, tok_start, mask, out,
+                                                      softmax_max, softmax_sum, workspace), w):
+        return
     dt, f32 = torch.bfloat16 if t.dtype == DSA_BF16 else torch.float32, torch.float32
     d = _device(q, w, "q")
     if _device(pool, w, "pool") != d:
@@ -443,6 +485,9 @@ def beam_select(b, logits, scores, finished, parent, token, scores_out, finished
     """The beams_out best continuations of each request: parent (row of the input, for
     cache_fork), token, score, finished; finished / finished_out (uint8) may be None."""
     w, u8, f32 = "dsa_beam_select", torch.uint8, torch.float32
+    if stream is None and _made(_native.beam_select(b, logits, scores, finished, parent, token, scores_out,
+                                                    finished_out, workspace), w):
+        return
     d, rows, outs = _device(logits, w, "logits"), b.n_batch * b.beams_in, b.n_batch * b.beams_out
     _call(lib.dsa_beam_select, w, d, stream, ctypes.byref(b),
           _arg(logits, "logits", torch.bfloat16 if b.dtype == DSA_BF16 else f32, rows * b.ld, d, w),

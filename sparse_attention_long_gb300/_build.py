@@ -1,17 +1,23 @@
 """Builds libdsa_gb300.so in-tree with nvcc for sm_103a (one translation unit
-per .cu file, compiled in parallel, then linked).  No cmake, no torch."""
+per .cu file, compiled in parallel, then linked; no cmake, no torch), and the
+module that marshals the serving calls' tensors (_binding.so, g++ against
+PyTorch's and Python's headers; without those the Python code does its work)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdsa_gb300.so")
+BINDING, BINDING_SRC = os.path.join(PKG, "_binding.so"), os.path.join(CSRC, "binding.cpp")
 SOURCES = ["api.cu", "topk.cu", "simt.cu", "indexer_tc.cu", "attn_fwd_tc.cu", "static_ws.cu",
            "bwd_tc.cu", "kl_tc.cu", "indexer_fp8.cu", "cache.cu", "tree_attn.cu", "tree_attn_tc.cu",
            "beam.cu"]
@@ -35,6 +41,34 @@ def _stale(obj: str, src: str) -> bool:
     return any(os.path.getmtime(d) > os.path.getmtime(obj) for d in deps)
 
 
+def _binding_job(nvcc: str, force: bool):
+    """The command that builds _binding.so, or None: up to date, or no headers."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    torch, python = os.path.dirname(spec.origin), sysconfig.get_paths()["include"]
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"), python,
+           cuda, os.path.join(ROOT, "include")]
+    deps = [BINDING_SRC, os.path.join(ROOT, "include", "dsa.h"), os.path.join(torch, "version.py"), __file__]
+    if not shutil.which("g++") or not os.path.exists(os.path.join(python, "Python.h")):
+        return None
+    if not force and os.path.exists(BINDING) and \
+            all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
+        return None
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", *(f"-I{p}" for p in inc), BINDING_SRC, "-o",
+            BINDING + ".tmp", "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda"]
+
+
+def _build_binding(cmd) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode == 0:
+        os.replace(BINDING + ".tmp", BINDING)
+    else:
+        print("_binding.so not built, Python marshals the serving calls:\n" + r.stderr[-2000:], file=sys.stderr)
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -53,8 +87,12 @@ def build(verbose: bool = False, force: bool = False) -> str:
             print(" ".join(cmd))
         return cmd
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        cmd = _binding_job(nvcc, force)
+        binding = ex.submit(_build_binding, cmd) if cmd else None
         list(ex.map(run, jobs))
+        if binding:
+            binding.result()
     objs = [os.path.join(BUILD, s.replace(".cu", ".o")) for s in SOURCES]
     if force or jobs or not os.path.exists(LIB):
         tmp = LIB + ".tmp"

@@ -226,3 +226,60 @@ def test_draft_and_accept(n, T, H, R, graph):
         cache.check(hist, kv, keys)
         held = sum(r > 0 for r in cache.refs.tolist())
         assert all(r > 0 for r in cache.refs.tolist()[:held])
+
+
+def test_native_marshalling_is_there_and_python_agrees(monkeypatch):
+    """The calls go through the compiled module; without it the same functions give the same steps."""
+    dsa = lib()
+    assert hasattr(dsa._native, "bind")
+    answers = []
+
+    class Spy:
+        def __getattr__(self, name):
+            def call(*args):
+                answers.append((name, getattr(native, name)(*args)))
+                return answers[-1][1]
+            return call
+
+    native = dsa._native
+    monkeypatch.setattr(dsa, "_native", Spy())
+    test_beam_search(1, 2, 20, 3, 16, 18, False)
+    test_draft_and_accept(2, 5, 4, 16, False)
+    assert {n for n, _ in answers} == {"cache_fork", "cache_extend", "cache_compact", "cache_copy_pages", "cache_write",
+                                       "tree_attn_fwd", "beam_select"}
+    assert all(a == 0 for _, a in answers)
+    monkeypatch.setattr(dsa, "_native", dsa._Absent())
+    test_beam_search(1, 2, 20, 3, 16, 18, False)
+    test_draft_and_accept(2, 5, 4, 16, False)
+
+
+def test_native_marshalling_refuses_what_the_python_code_refuses():
+    dsa = lib()
+    n, P, R, M = 2, 6, 16, 3
+    c = dsa.make_cache(n_seqs=n, n_pages=P, page_rows=R, max_pages=M)
+    good = dict(parent=ints(n), table=ints(n, M, fill=-1), lens=ints(n), refs=ints(P), table_out=ints(n, M),
+                lens_out=ints(n), refs_out=ints(P), copies=ints(n, 3), n_copies=ints(1))
+    fork = lambda c=c, **kw: dsa._native.cache_fork(c, *{**good, **kw}.values())
+    assert fork() == 0
+    bad = [dict(table=good["table"].cpu()), dict(lens=ints(n).long()), dict(refs=ints(P + 1)), dict(copies=ints(n, 2)),
+           dict(table=ints(M, n).t()), dict(n_copies=None), dict(parent=[0, 0]), dict(lens_out=ints(2 * n)[::2])]
+    for kw in bad:
+        assert fork(**kw) == 1
+        with pytest.raises((TypeError, ValueError)):
+            dsa.cache_fork(c, *{**good, **kw}.values())
+    assert fork(c=b"x" * 32) == 1 and fork(c=dsa.make_beam(n_batch=1, beams_in=1, beams_out=1, vocab=1)) == 1
+    assert dsa._native.cache_fork(c) == 1
+    wide = dsa.make_cache(n_seqs=2 ** 62, n_pages=P, page_rows=R, max_pages=2 ** 62)
+    assert fork(c=wide) == 1
+    # what the library itself refuses comes back as its error
+    assert fork(table_out=good["table"]) == dsa.DSA_ERR_INVALID_ARG
+    with pytest.raises(dsa.DSAError):
+        dsa.cache_fork(c, *{**good, "table_out": good["table"]}.values())
+    # another stream than the current one, given or current
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    dsa.cache_fork(c, *good.values(), stream=s)
+    with torch.cuda.stream(s):
+        assert fork() == 0
+    torch.cuda.synchronize()
+    assert dsa.get_status() == 0
