@@ -632,14 +632,17 @@ static bool ints(const P*... p) {
 }
 
 // One CTA while the work is small (a cluster barrier costs more than the other
-// CTAs save), else a cluster of eight.  One CTA against eight, us:
-//   entries   768: fork 5.1 / 7.4, extend 4.6 / 6.2, compact 4.8 / 9.4
-//           10240:      8.0 / 9.2,        5.7 / 6.8,         11.0 / 11.8
-//           20480:     10.9 / 10.0,       6.3 / 7.5,         17.8 / 13.5
-//           40960:     15.2 / 11.9,       7.6 / 8.0,         29.9 / 16.4
-constexpr long long kAloneFork = 16384, kAloneExtend = 40960, kAloneCompact = 12288;
-static int cluster_size(const Dims& d, long long alone) {
-  return (long long)d.n_pages + (long long)d.n_seqs * d.max_pages <= alone ? 1 : kMaxCluster;
+// CTAs save), else a cluster of eight.  What counts is how often a warp of the one
+// CTA goes round: over the steps of 256 table entries (fork, compact) and over the
+// pages, in blocks of 1024.  One CTA against eight, us, by steps and pages:
+//    16 /  2048: fork  5.9 /  7.8, extend 5.2 / 6.5, compact  6.4 / 10.2
+//    32 /  6144:       8.1 /  9.2,        5.7 / 6.8,         11.0 / 11.7
+//    64 / 12288:      11.0 / 10.0,        6.4 / 7.5,         17.9 / 13.5
+//   256 /  2691:      20.5 /  8.7,        7.0 / 7.6,         21.1 / 10.9
+//   128 / 16268:      22.7 / 11.7,       11.9 / 9.1,         29.7 / 14.7
+static int cluster_size(const Dims& d, int alone_steps, int alone_pages) {
+  const long long steps = (long long)d.n_seqs * ((d.max_pages + 255) / 256);
+  return steps <= alone_steps && d.n_pages <= alone_pages ? 1 : kMaxCluster;
 }
 template <typename... A, typename... B>
 static int launch_cluster(void (*kernel)(A...), int ctas, size_t smem, cudaStream_t st, B... args) {
@@ -703,7 +706,7 @@ int dsa_cache_fork(const dsa_cache* p, const int32_t* parent, const int32_t* tab
     return DSA_ERR_INVALID_ARG;
   DevCtx c;
   if (!ext_dev_ctx(&c)) return DSA_ERR_CUDA;
-  return launch_cluster(fork_kernel, cluster_size(d, kAloneFork), 4 * ns, (cudaStream_t)stream, d, parent, table, lens, refs,
+  return launch_cluster(fork_kernel, cluster_size(d, 48, 12288), 4 * ns, (cudaStream_t)stream, d, parent, table, lens, refs,
                         table_out, lens_out, refs_out, copies, n_copies, c);
 }
 
@@ -722,7 +725,7 @@ int dsa_cache_extend(const dsa_cache* p, const int32_t* n_new, int32_t* table, c
     return DSA_ERR_INVALID_ARG;
   DevCtx c;
   if (!ext_dev_ctx(&c)) return DSA_ERR_CUDA;
-  return launch_cluster(extend_kernel, cluster_size(d, kAloneExtend), 3 * ns + 8, (cudaStream_t)stream, d, n_new, table, lens, refs,
+  return launch_cluster(extend_kernel, cluster_size(d, INT_MAX, 12288), 3 * ns + 8, (cudaStream_t)stream, d, n_new, table, lens, refs,
                         lens_out, refs_out, slots, (int)n_slots, c);
 }
 
@@ -738,7 +741,7 @@ int dsa_cache_compact(const dsa_cache* p, const int32_t* table, const int32_t* l
     return DSA_ERR_INVALID_ARG;
   DevCtx c;
   if (!ext_dev_ctx(&c)) return DSA_ERR_CUDA;
-  return launch_cluster(compact_kernel, cluster_size(d, kAloneCompact), 0, (cudaStream_t)stream, d, table, lens, refs, table_out,
+  return launch_cluster(compact_kernel, cluster_size(d, 32, 8192), 0, (cudaStream_t)stream, d, table, lens, refs, table_out,
                         refs_out, page_map, copies, n_copies, c);
 }
 
