@@ -13,8 +13,8 @@
 // sets the status word.
 //
 // Bound: a few cluster barriers and dependent L2 reads.  Fork, extend and compact
-// of 16 sequences and 2048 pages take 5.9, 5.1 and 6.3 us, of 256 sequences and
-// 98304 pages 12.9, 10.2 and 26 us; the tables and refs are read at L2 rate.
+// of 16 sequences and 2048 pages take 5.0, 4.4 and 6.3 us, of 256 sequences and
+// 98304 pages 13.0, 10.1 and 26 us; the tables and refs are read at L2 rate.
 #include <limits.h>
 
 #include "dsa_common.cuh"
@@ -25,7 +25,8 @@ bool ext_dev_ctx(DevCtx* c);
 
 namespace cache {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
+// The plan kernels take kThreads (256, 512 or 1024) as a template argument.
+constexpr int kMaxThreads = 1024;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSeqs = 8192;
 
@@ -35,7 +36,7 @@ struct Dims {
 
 struct Shared {                       // what the other CTAs of the cluster read
   int count, more, bad;
-  int warp[kWarps];                   // block scans
+  int warp[kMaxThreads / 32];         // block scans
 };
 
 __device__ __forceinline__ uint32_t cluster_nctarank() {
@@ -51,6 +52,7 @@ __device__ __forceinline__ int ld_peer(const int* local, uint32_t rank) {
 __device__ __forceinline__ int pages_of(int len, int R) { return (int)(((long long)len + R - 1) / R); }
 
 // exclusive prefix of v over the block and its total (all threads call it)
+template <int kThreads>
 __device__ __forceinline__ int block_scan(int v, Shared& s, int* total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int x = v;
@@ -61,31 +63,33 @@ __device__ __forceinline__ int block_scan(int v, Shared& s, int* total) {
   }
   if (lane == 31) s.warp[w] = x;
   __syncthreads();
-  const int t = s.warp[lane];                      // every warp: the sums of all warps (kWarps = 32)
+  const int t = lane < kThreads / 32 ? s.warp[lane] : 0;  // every warp: the sums of all warps
   const int below = __reduce_add_sync(0xffffffffu, lane < w ? t : 0);
   *total = __reduce_add_sync(0xffffffffu, t);
   __syncthreads();
   return x - v + below;
 }
 // the same for a flag
+template <int kThreads>
 __device__ __forceinline__ int block_rank(bool yes, Shared& s, int* total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const uint32_t bits = __ballot_sync(0xffffffffu, yes);
   if (lane == 0) s.warp[w] = __popc(bits);
   __syncthreads();
-  const int t = s.warp[lane];
+  const int t = lane < kThreads / 32 ? s.warp[lane] : 0;
   const int below = __reduce_add_sync(0xffffffffu, lane < w ? t : 0);
   *total = __reduce_add_sync(0xffffffffu, t);
   __syncthreads();
   return below + __popc(bits & ((1u << lane) - 1u));
 }
 // total of a thread's counts over the block
+template <int kThreads>
 __device__ __forceinline__ int block_sum(int v, Shared& s) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int x = __reduce_add_sync(0xffffffffu, v);
   if (lane == 0) s.warp[w] = x;
   __syncthreads();
-  const int t = __reduce_add_sync(0xffffffffu, s.warp[lane]);
+  const int t = __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? s.warp[lane] : 0);
   __syncthreads();
   return t;
 }
@@ -120,28 +124,29 @@ __device__ __forceinline__ void slice(int n_pages, uint32_t rank, uint32_t n, in
 
 // f(rank, page) for the pages of [lo, hi) that satisfy `pick`, in ascending
 // order, ranks from `first`; stops once the rank reaches `limit`
-template <typename P, typename F>
+template <int kThreads, typename P, typename F>
 __device__ __forceinline__ void in_order(int lo, int hi, int first, int limit, Shared& s, P pick, F f) {
   for (int base = lo; base < hi && first < limit; base += kThreads) {
     const int p = base + threadIdx.x;
     const bool yes = p < hi && pick(p);
     int n;
-    const int at = first + block_rank(yes, s, &n);
+    const int at = first + block_rank<kThreads>(yes, s, &n);
     if (yes && at < limit) f(at, p);
     first += n;
   }
 }
-template <typename P>
+template <int kThreads, typename P>
 __device__ __forceinline__ int count_if(int lo, int hi, Shared& s, P pick) {
   int n = 0;
   for (int p = lo + threadIdx.x; p < hi; p += kThreads) n += pick(p) ? 1 : 0;
-  return block_sum(n, s);
+  return block_sum<kThreads>(n, s);
 }
 
 // ---------------------------------- fork ----------------------------------
 // table row i <- old row parent[i].  The first child (lowest i) of a parent
 // keeps the parent's partial last page, the other children need a page of
 // their own for it.
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1)
     fork_kernel(Dims d, const int32_t* __restrict__ parent, const int32_t* __restrict__ table,
                 const int32_t* __restrict__ lens, const int32_t* __restrict__ refs,
@@ -181,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 256 table entries per warp step; uses that do not change are not counted
     const int nch = (d.max_pages + 255) / 256, lane = tid & 31;
     const long long items = (long long)n * nch;
-    for (long long it = (long long)rank * kWarps + (tid >> 5); it < items; it += (long long)nc * kWarps) {
+    for (long long it = (long long)rank * (kThreads / 32) + (tid >> 5); it < items; it += (long long)nc * (kThreads / 32)) {
       const int i = (int)(it / nch), j0 = (int)(it % nch) * 256;
       const int p = par[i];
       const int po = pages_of(len[i], R), pn = p >= 0 ? pages_of(len[p], R) : 0;
@@ -217,14 +222,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = base + tid;
     const bool yes = !bad_rows && i < n && need_page(i);
     int t;
-    const int at = block_rank(yes, s, &t);
+    const int at = block_rank<kThreads>(yes, s, &t);
     if (yes) needy[n_need + at] = i;
     n_need += t;
   }
   sync_all(nc);                 // every use counted
   {
     bool neg = false;
-    const int free_pages = count_if(lo, hi, s, [&](int p) {
+    const int free_pages = count_if<kThreads>(lo, hi, s, [&](int p) {
       const int r = __ldcg(refs_out + p);
       neg |= r < 0;
       return r == 0;
@@ -236,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Totals t = gather_totals(s, rank, nc);
   const bool bad = t.bad != 0, fail = bad || n_need > t.all;
   if (!fail) {
-    in_order(
+    in_order<kThreads>(
         lo, hi, t.before, n_need, s, [&](int p) { return __ldcg(refs_out + p) == 0; },
         [&](int k, int page) {
           const int i = needy[k], p = par[i], last = pages_of(len[p], R) - 1;
@@ -263,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // --------------------------------- extend ---------------------------------
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1)
     extend_kernel(Dims d, const int32_t* __restrict__ n_new, int32_t* table, const int32_t* lens, const int32_t* refs,
                   int32_t* lens_out, int32_t* refs_out, int32_t* __restrict__ slots, int n_slots, DevCtx c) {
@@ -299,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     int ta, tb;
-    const int ea = block_scan(a, s, &ta), eb = block_scan(b, s, &tb);
+    const int ea = block_scan<kThreads>(a, s, &ta), eb = block_scan<kThreads>(b, s, &tb);
     if (i < n) {
       prow[i] = rows + ea;
       ppage[i] = pages + eb;
@@ -321,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   {
     bool neg = false;
-    const int free_pages = count_if(lo, hi, s, [&](int p) {
+    const int free_pages = count_if<kThreads>(lo, hi, s, [&](int p) {
       neg |= refs[p] < 0;
       return refs[p] == 0;
     });
@@ -346,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return a;
   };
   if (!fail) {
-    in_order(
+    in_order<kThreads>(
         lo, hi, t.before, pages, s, [&](int p) { return refs_out[p] == 0; },
         [&](int k, int page) {
           const int i = find(ppage, k);
@@ -373,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // --------------------------------- compact ---------------------------------
 // n_live pages are in use: those at n_live and above move, in ascending order,
 // into the free ids below n_live, in ascending order.
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1)
     compact_kernel(Dims d, const int32_t* __restrict__ table, const int32_t* __restrict__ lens,
                    const int32_t* __restrict__ refs, int32_t* __restrict__ table_out, int32_t* __restrict__ refs_out,
@@ -392,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nch = (d.max_pages + 255) / 256;
   auto entries = [&](auto f) {
     const int items = n * nch;        // n * max_pages < 2^31
-    for (int it = (int)rank * kWarps + (tid >> 5); it < items; it += (int)nc * kWarps) {
+    for (int it = (int)rank * (kThreads / 32) + (tid >> 5); it < items; it += (int)nc * (kThreads / 32)) {
       const int i = it / nch, j0 = (it - i * nch) * 256, len = lens[i];
       const bool ok = len >= 0 && len <= (long long)d.max_pages * R;
       if (!ok) s.bad = 1;
@@ -415,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   });
   {
     bool neg = false;
-    const int live = count_if(lo, hi, s, [&](int p) {
+    const int live = count_if<kThreads>(lo, hi, s, [&](int p) {
       neg |= refs[p] < 0;
       return refs[p] > 0;
     });
@@ -429,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   sync_all(nc);                       // counts read before they are replaced
   // free ids below n_live and used ones above: here, in the lower slices, in all
   const int mid = n_live < lo ? lo : (n_live > hi ? hi : n_live);  // slice = [lo, mid) low, [mid, hi) high
-  const int live_low = count_if(lo, mid, s, [&](int p) { return refs[p] > 0; });
+  const int live_low = count_if<kThreads>(lo, mid, s, [&](int p) { return refs[p] > 0; });
   if (tid == 0) {
     s.count = (mid - lo) - live_low;
     s.more = live_here - live_low;
@@ -451,9 +458,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool used = p < hi && refs[p] > 0;
     const bool is_hole = p < mid && !used, is_mover = p >= mid && used;
     int n;
-    const int kh = hole + block_rank(is_hole, s, &n);
+    const int kh = hole + block_rank<kThreads>(is_hole, s, &n);
     hole += n;
-    const int km = mover + block_rank(is_mover, s, &n);
+    const int km = mover + block_rank<kThreads>(is_mover, s, &n);
     mover += n;
     if (is_hole) copies[3 * kh + 1] = p;
     if (is_mover) {
@@ -640,16 +647,34 @@ static bool ints(const P*... p) {
 //    64 / 12288:      11.0 / 10.0,        6.4 / 7.5,         17.9 / 13.5
 //   256 /  2691:      20.5 /  8.7,        7.0 / 7.6,         21.1 / 10.9
 //   128 / 16268:      22.7 / 11.7,       11.9 / 9.1,         29.7 / 14.7
-static int cluster_size(const Dims& d, int alone_steps, int alone_pages) {
+struct Shape {
+  int ctas, threads;
+};
+static int pow2_from(long long x, int lo, int hi) {
+  int p = lo;
+  while (p < x && p < hi) p *= 2;
+  return p;
+}
+static Shape shape(const Dims& d, int alone_steps, int alone_pages) {
   const long long steps = (long long)d.n_seqs * ((d.max_pages + 255) / 256);
-  return steps <= alone_steps && d.n_pages <= alone_pages ? 1 : kMaxCluster;
+  if (steps > alone_steps || d.n_pages > alone_pages) return {kMaxCluster, kMaxThreads};
+  // a warp for each step, but a barrier of few warps is faster: 256, 512, 1024 threads
+  // take, us, by steps and pages (extend: by pages; 256 sequences whose free pages are
+  // the last of 2691 8.4 with 512, 7.0 with 1024)
+  //   4 /   38: fork 4.5, 4.8, 5.0                        extend 3.2, 3.4, 3.7
+  //  16 /  512:                     compact 6.1, 4.6, 5.0
+  //  16 / 2048: fork 6.5, 5.4, 5.9, compact 8.8, 6.6, 6.4, extend 4.4, 4.6, 5.2
+  //  32 / 6144: fork 11.2, 8.6, 8.1                       extend 5.5, 5.4, 5.7
+  return {1, 32 * pow2_from(alone_steps == INT_MAX ? d.n_pages / 128 : steps, 8, 32)};
 }
 template <typename... A, typename... B>
-static int launch_cluster(void (*kernel)(A...), int ctas, size_t smem, cudaStream_t st, B... args) {
+static int launch_plan(void (*k256)(A...), void (*k512)(A...), void (*k1024)(A...), Shape sh, size_t smem, cudaStream_t st,
+                       B... args) {
+  auto kernel = sh.threads == 256 ? k256 : sh.threads == 512 ? k512 : k1024;
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return DSA_ERR_CUDA;
-  return launch_programmatic(kernel, dim3(ctas), dim3(kThreads), smem, st, ctas, args...) ? DSA_OK : DSA_ERR_CUDA;
+  return launch_programmatic(kernel, dim3(sh.ctas), dim3(sh.threads), smem, st, sh.ctas, args...) ? DSA_OK : DSA_ERR_CUDA;
 }
 
 static int check_pool(const dsa_cache* p, const dsa_pool* pool, Pool* o) {
@@ -706,7 +731,7 @@ int dsa_cache_fork(const dsa_cache* p, const int32_t* parent, const int32_t* tab
     return DSA_ERR_INVALID_ARG;
   DevCtx c;
   if (!ext_dev_ctx(&c)) return DSA_ERR_CUDA;
-  return launch_cluster(fork_kernel, cluster_size(d, 48, 12288), 4 * ns, (cudaStream_t)stream, d, parent, table, lens, refs,
+  return launch_plan(fork_kernel<256>, fork_kernel<512>, fork_kernel<1024>, shape(d, 48, 12288), 4 * ns, (cudaStream_t)stream, d, parent, table, lens, refs,
                         table_out, lens_out, refs_out, copies, n_copies, c);
 }
 
@@ -725,7 +750,7 @@ int dsa_cache_extend(const dsa_cache* p, const int32_t* n_new, int32_t* table, c
     return DSA_ERR_INVALID_ARG;
   DevCtx c;
   if (!ext_dev_ctx(&c)) return DSA_ERR_CUDA;
-  return launch_cluster(extend_kernel, cluster_size(d, INT_MAX, 12288), 3 * ns + 8, (cudaStream_t)stream, d, n_new, table, lens, refs,
+  return launch_plan(extend_kernel<256>, extend_kernel<512>, extend_kernel<1024>, shape(d, INT_MAX, 12288), 3 * ns + 8, (cudaStream_t)stream, d, n_new, table, lens, refs,
                         lens_out, refs_out, slots, (int)n_slots, c);
 }
 
@@ -741,7 +766,7 @@ int dsa_cache_compact(const dsa_cache* p, const int32_t* table, const int32_t* l
     return DSA_ERR_INVALID_ARG;
   DevCtx c;
   if (!ext_dev_ctx(&c)) return DSA_ERR_CUDA;
-  return launch_cluster(compact_kernel, cluster_size(d, 32, 8192), 0, (cudaStream_t)stream, d, table, lens, refs, table_out,
+  return launch_plan(compact_kernel<256>, compact_kernel<512>, compact_kernel<1024>, shape(d, 32, 8192), 0, (cudaStream_t)stream, d, table, lens, refs, table_out,
                         refs_out, page_map, copies, n_copies, c);
 }
 
