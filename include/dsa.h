@@ -446,9 +446,10 @@ int dsa_cache_write(const dsa_cache *p, const dsa_pool *pool, const void *rows, 
  *          mask_words is 0.  T_b <= 64 * mask_words.
  *   out [n_tok, H, d_v]   softmax_max / softmax_sum [n_tok, H] fp32
  * A key that a token does not see has no effect on it, whatever it holds; a
- * NaN in a key that it does see gives NaN, an infinity there unspecified values.  A sequence whose
- * numbers are out of range (DSA_ERR_INDEX) is left out, its outputs as they
- * were; a page out of range (DSA_ERR_INDEX) counts as unseen.
+ * NaN in a key that it does see gives NaN, an infinity there unspecified
+ * values.  A sequence whose numbers are out of range (DSA_ERR_INDEX) is left
+ * out, its outputs as they were; a page out of range (DSA_ERR_INDEX) counts as
+ * unseen.
  *   dtype DSA_BF16: d_qk 576, d_v 512, page_rows a multiple of 16, any
  *          H <= 1024; q, kv_new, out, the pool's base and page stride 16-byte
  *          aligned.  DSA_FP32: any H <= 1024, d_qk <= 1024, d_v <= d_qk.
@@ -489,8 +490,7 @@ int dsa_tree_attn_fwd(const dsa_cache *p, const dsa_tree *t, const void *q, cons
  * different beams is that of their scores as far as those tell them apart (to
  * some 2^-20), within a beam that of the logits.
  * beams_in, beams_out <= 32, vocab <= 2^24, eos in [-1, vocab) (-1: no such
- * token; finished must be NULL then).  Outputs must not
- * overlap inputs.
+ * token; finished must be NULL then).  Outputs must not overlap inputs.
  *   workspace: dsa_beam_workspace_size(p) bytes, 16-byte aligned; one call at
  *   a time.
  */

@@ -589,7 +589,8 @@ int dsa_beam_select(const dsa_beam* p, const void* logits, const float* scores, 
     return DSA_ERR_INVALID_ARG;
   // one request's results over another's beams
   const size_t in = (size_t)a.n_batch * a.win, out = (size_t)a.n_batch * a.wout;
-  if (overlap(scores, 4 * in, scores_out, 4 * out) || (finished && finished_out && overlap(finished, in, finished_out, out)))
+  if (overlap(scores, 4 * in, scores_out, 4 * out) ||
+      (finished && finished_out && overlap(finished, in, finished_out, out)))
     return DSA_ERR_INVALID_ARG;
   if (!workspace || ((uintptr_t)workspace & 15u) != 0) return DSA_ERR_WORKSPACE;
   DevCtx c;

@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 256 table entries per warp step; uses that do not change are not counted
     const int nch = (d.max_pages + 255) / 256, lane = tid & 31;
     const long long items = (long long)n * nch;
-    for (long long it = (long long)rank * (kThreads / 32) + (tid >> 5); it < items; it += (long long)nc * (kThreads / 32)) {
+    for (long long it = (long long)rank * (kThreads / 32) + (tid >> 5); it < items;
+         it += (long long)nc * (kThreads / 32)) {
       const int i = (int)(it / nch), j0 = (int)(it % nch) * 256;
       const int p = par[i];
       const int po = pages_of(len[i], R), pn = p >= 0 ? pages_of(len[p], R) : 0;
@@ -668,13 +669,14 @@ static Shape shape(const Dims& d, int alone_steps, int alone_pages) {
   return {1, 32 * pow2_from(alone_steps == INT_MAX ? d.n_pages / 128 : steps, 8, 32)};
 }
 template <typename... A, typename... B>
-static int launch_plan(void (*k256)(A...), void (*k512)(A...), void (*k1024)(A...), Shape sh, size_t smem, cudaStream_t st,
-                       B... args) {
+static int launch_plan(void (*k256)(A...), void (*k512)(A...), void (*k1024)(A...), Shape sh, size_t smem,
+                       cudaStream_t st, B... args) {
   auto kernel = sh.threads == 256 ? k256 : sh.threads == 512 ? k512 : k1024;
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return DSA_ERR_CUDA;
-  return launch_programmatic(kernel, dim3(sh.ctas), dim3(sh.threads), smem, st, sh.ctas, args...) ? DSA_OK : DSA_ERR_CUDA;
+  return launch_programmatic(kernel, dim3(sh.ctas), dim3(sh.threads), smem, st, sh.ctas, args...) ? DSA_OK
+                                                                                                  : DSA_ERR_CUDA;
 }
 
 static int check_pool(const dsa_cache* p, const dsa_pool* pool, Pool* o) {
@@ -731,8 +733,9 @@ int dsa_cache_fork(const dsa_cache* p, const int32_t* parent, const int32_t* tab
     return DSA_ERR_INVALID_ARG;
   DevCtx c;
   if (!ext_dev_ctx(&c)) return DSA_ERR_CUDA;
-  return launch_plan(fork_kernel<256>, fork_kernel<512>, fork_kernel<1024>, shape(d, 48, 12288), 4 * ns, (cudaStream_t)stream, d, parent, table, lens, refs,
-                        table_out, lens_out, refs_out, copies, n_copies, c);
+  return launch_plan(fork_kernel<256>, fork_kernel<512>, fork_kernel<1024>, shape(d, 48, 12288), 4 * ns,
+                     (cudaStream_t)stream, d, parent, table, lens, refs, table_out, lens_out, refs_out, copies,
+                     n_copies, c);
 }
 
 int dsa_cache_extend(const dsa_cache* p, const int32_t* n_new, int32_t* table, const int32_t* lens,
@@ -750,8 +753,8 @@ int dsa_cache_extend(const dsa_cache* p, const int32_t* n_new, int32_t* table, c
     return DSA_ERR_INVALID_ARG;
   DevCtx c;
   if (!ext_dev_ctx(&c)) return DSA_ERR_CUDA;
-  return launch_plan(extend_kernel<256>, extend_kernel<512>, extend_kernel<1024>, shape(d, INT_MAX, 12288), 3 * ns + 8, (cudaStream_t)stream, d, n_new, table, lens, refs,
-                        lens_out, refs_out, slots, (int)n_slots, c);
+  return launch_plan(extend_kernel<256>, extend_kernel<512>, extend_kernel<1024>, shape(d, INT_MAX, 12288), 3 * ns + 8,
+                     (cudaStream_t)stream, d, n_new, table, lens, refs, lens_out, refs_out, slots, (int)n_slots, c);
 }
 
 int dsa_cache_compact(const dsa_cache* p, const int32_t* table, const int32_t* lens, const int32_t* refs,
@@ -766,8 +769,8 @@ int dsa_cache_compact(const dsa_cache* p, const int32_t* table, const int32_t* l
     return DSA_ERR_INVALID_ARG;
   DevCtx c;
   if (!ext_dev_ctx(&c)) return DSA_ERR_CUDA;
-  return launch_plan(compact_kernel<256>, compact_kernel<512>, compact_kernel<1024>, shape(d, 32, 8192), 0, (cudaStream_t)stream, d, table, lens, refs, table_out,
-                        refs_out, page_map, copies, n_copies, c);
+  return launch_plan(compact_kernel<256>, compact_kernel<512>, compact_kernel<1024>, shape(d, 32, 8192), 0,
+                     (cudaStream_t)stream, d, table, lens, refs, table_out, refs_out, page_map, copies, n_copies, c);
 }
 
 int dsa_cache_copy_pages(const dsa_cache* p, const dsa_pool* pool, const int32_t* copies, const int32_t* n_copies,
