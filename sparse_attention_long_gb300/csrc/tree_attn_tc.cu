@@ -864,7 +864,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (end) break;
         if (!mbar_wait<true>(smem_u32(&sm.q_tm[bi]), (i >> 1) & 1, c, abort_flag)) break;
         tc_fence_after();
-        commit2(smem_u32(&sm.st_empty[0]) + 8 * st);  // the query's slot is free
+        const uint32_t query = smem_u32(&sm.st_empty[0]) + 8 * st;
         if (++st == kStages) st = 0;
         ++slot;
         for (int j = 0; j < nblk; ++j, ++G, ++slot) {
@@ -876,6 +876,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                    abort_flag));
           if (!ok) break;
           tc_fence_after();
+          // The query's slot is free only now, although q_tm said that it is read: s_free
+          // says that every softmax warp is past the last block but one of the tile
+          // before, whose wait for its P V (to rescale O) is on this slot's st_empty.
+          // Released at once, that barrier could complete two phases ahead of a late warp.
+          if (j == 0) commit2(query);
           const uint32_t sb = smem_u32(sm.stage[0]) + st * kStageBytes;
           const uint32_t v = desc_lo(sb, 16), r = desc_lo(sb + kValue, 16);
 #pragma unroll
@@ -1157,7 +1162,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float m_new = need ? bm : m_run;
             const float alpha = (m_run == -INFINITY || !need) ? (need ? 0.f : 1.f) : ex2(m_run - m_new);
             if (j > g.j0 && __any_sync(0xffffffffu, need && m_run != -INFINITY)) {
-              // O must hold PV(G-1) before it is rescaled
+              // O must hold PV(G-1) before it is rescaled.  (The stage's next use needs
+              // this block's P or, as a query's slot, s_free of the block after this one:
+              // its st_empty cannot complete twice ahead of this wait.)
               ok = mbar_wait_warp(smem_u32(&sm.st_empty[(G - 1) % kStages]), ((G - 1) / kStages) & 1, c, abort_flag);
               tc_fence_after();
 #pragma unroll 1
