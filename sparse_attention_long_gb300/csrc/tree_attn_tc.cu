@@ -123,9 +123,7 @@ struct __align__(1024) Smem {
   uint8_t plain[kStages];                          // the block needs no fix
   alignas(4) uint8_t live[kStages][kFixWarps];     // 2 steps of 16 slots each: some token sees some slot
   alignas(16) uint8_t spare[kUnit];                // of the logit exchange; row maxima and sums between exchanges
-  uint32_t sink[kSoftWarps];                       // targets of CTA 1's signalling stores
-  uint32_t sink_f[2][kFixWarps];
-  uint64_t st_full[kStages], st_empty[kStages], ready[kStages];
+  uint64_t st_full[kStages], st_empty[kStages], ready[kStages], fixed[kStages];
   uint64_t s_full, s_free, p_full[2];
   uint64_t q_tm[2], q_free[2], mma_done[2], sc_full[2], sc_empty[2], fin[2];
   uint32_t tmem_base;
@@ -222,12 +220,20 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t n, bool v) {
       : "memory");
   return r != 0;
 }
-// 4-byte store into the peer CTA's shared memory that completes 4 bytes of the
-// transaction count of the peer's barrier; the issuing thread does not wait
-__device__ __forceinline__ void st_async_signal(uint32_t cluster_addr, uint32_t cluster_bar) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(cluster_addr),
-               "r"(0u), "r"(cluster_bar)
-               : "memory");
+// Signals to the issuers: an arrive on a barrier of CTA 0 from either CTA of the pair,
+// for a thread that waits at cluster scope.  arrive_leader orders accesses to tensor
+// memory only (by the tcgen05 fences on both sides).  arrive_leader_shared also hands
+// over what this thread wrote to its CTA's shared memory or knows of through a barrier of
+// its CTA.  Its fence is restricted to shared memory: 64 cycles with the arrive, where
+// the release of all memory at cluster scope takes 350 (trees of 48 tokens: 19 % more
+// time).
+__device__ __forceinline__ void arrive_leader(uint64_t* bar, uint32_t crank) {
+  if (crank == 0) mbar_arrive(smem_u32(bar));
+  else mbar_arrive_remote_relaxed(mapa_shared(smem_u32(bar), 0));
+}
+__device__ __forceinline__ void arrive_leader_shared(uint64_t* bar, uint32_t crank) {
+  if (crank != 0) asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  arrive_leader(bar, crank);
 }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
   asm volatile(
@@ -463,15 +469,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&sm.st_full[i]), kLoadWarps);
       mbar_init(smem_u32(&sm.st_empty[i]), 1 + kFixWarps);  // the last MMAs, and the fix warps
-      mbar_init(smem_u32(&sm.ready[i]), kFixWarps);
+      mbar_init(smem_u32(&sm.ready[i]), 2 * kFixWarps);
+      mbar_init(smem_u32(&sm.fixed[i]), kFixWarps);
     }
     mbar_init(smem_u32(&sm.s_full), 1);
-    // ready, s_free, p_full, q_tm (used in CTA 0): the local warps arrive, the first
-    // of them also expecting the 4 bytes that each of CTA 1's warps stores
-    mbar_init(smem_u32(&sm.s_free), kSoftWarps);
+    // ready, s_free, p_full, q_tm (used in CTA 0): the warps of both CTAs arrive
+    mbar_init(smem_u32(&sm.s_free), 2 * kSoftWarps);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sm.p_full[i]), 2);       // (row groups)
-      mbar_init(smem_u32(&sm.q_tm[i]), kFixWarps);
+      mbar_init(smem_u32(&sm.p_full[i]), 2 * 2);   // (row groups)
+      mbar_init(smem_u32(&sm.q_tm[i]), 2 * kFixWarps);
       mbar_init(smem_u32(&sm.q_free[i]), 1);
       mbar_init(smem_u32(&sm.mma_done[i]), 1);
       mbar_init(smem_u32(&sm.sc_full[i]), 1);
@@ -609,7 +615,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (crank == 0) {                  // in the fix warps' stead, for the copies of both CTAs
                   const uint32_t rd = smem_u32(&sm.ready[st]);
                   mbar_arrive_expect_tx(rd, 2 * kStageBytes);
-                  mbar_arrive_n(rd, kFixWarps - 1);
+                  mbar_arrive_n(rd, 2 * kFixWarps - 1);
                 }
               } else {
                 mbar_arrive_expect_tx(bar, kValue);
@@ -745,13 +751,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_u32(&sm.st_empty[st]));
-          const uint32_t bar = smem_u32(&sm.q_tm[i & 1]);
-          if (crank == 0) {
-            if (fw == 0) mbar_arrive_expect_tx(bar, 4 * kFixWarps);
-            else mbar_arrive(bar);
-          } else {
-            st_async_signal(mapa_shared(smem_u32(&sm.sink_f[0][fw]), 0), mapa_shared(bar, 0));
-          }
+          mbar_arrive(smem_u32(&sm.fixed[st]));    // (its phases are those of the slots)
+          arrive_leader(&sm.q_tm[i & 1], crank);
         }
         __syncwarp();
         ++G;
@@ -790,7 +791,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (sm.plain[st]) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sm.st_empty[st]));
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&sm.st_empty[st]));
+            mbar_arrive(smem_u32(&sm.fixed[st]));
+          }
           continue;
         }
         const uint32_t valid = (uint32_t)(sm.valid[st][fw >> 1] >> (32 * (fw & 1))) & kAll;
@@ -837,13 +841,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_u32(&sm.st_empty[st]));
-          const uint32_t bar = smem_u32(&sm.ready[st]);
-          if (crank == 0) {
-            if (fw == 0) mbar_arrive_expect_tx(bar, 4 * kFixWarps);
-            else mbar_arrive(bar);
-          } else {
-            st_async_signal(mapa_shared(smem_u32(&sm.sink_f[1][fw]), 0), mapa_shared(bar, 0));
-          }
+          mbar_arrive(smem_u32(&sm.fixed[st]));
+          arrive_leader_shared(&sm.ready[st], crank);
         }
       }
     }
@@ -870,8 +869,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int j = 0; j < nblk; ++j, ++G, ++slot) {
           // the keys; the last logits read; PV(G-2) done, whose P buffer the softmax
           // of this block exchanges logits through (with the tile before: mma_done)
-          ok = mbar_wait(smem_u32(&sm.ready[0]) + 8 * st, (ready_par >> st) & 1u, c, abort_flag) &&
-               (G == 0 || mbar_wait(smem_u32(&sm.s_free), (G - 1) & 1, c, abort_flag)) &&
+          ok = mbar_wait<true>(smem_u32(&sm.ready[0]) + 8 * st, (ready_par >> st) & 1u, c, abort_flag) &&
+               (G == 0 || mbar_wait<true>(smem_u32(&sm.s_free), (G - 1) & 1, c, abort_flag)) &&
                (j < 2 || mbar_wait(smem_u32(&sm.st_empty[0]) + 8 * ((slot - 2) % kStages), ((slot - 2) / kStages) & 1, c,
                                    abort_flag));
           if (!ok) break;
@@ -913,7 +912,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (end) break;
         if (++st == kStages) st = 0;               // the query's slot
         for (int j = 0; j < nblk; ++j, ++G) {
-          ok = mbar_wait(smem_u32(&sm.p_full[G & 1]), (G >> 1) & 1, c, abort_flag);
+          ok = mbar_wait<true>(smem_u32(&sm.p_full[G & 1]), (G >> 1) & 1, c, abort_flag);
           if (!ok) break;
           tc_fence_after();
           const uint32_t sb = smem_u32(sm.stage[0]) + st * kStageBytes;
@@ -954,7 +953,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     // --------------------------- softmax / epilogue ---------------------------
     const int quad = warp & 3, ch = (warp - kWarpSoft0) >> 2;
-    const int ws = 4 * ch + quad;                  // slot in red[]
     const int l = quad * 32 + lane;                // TMEM lane
     const int hl = l & 63, half = l >> 6;          // row in the CTA; lane half
     const int rr = kHC * (int)crank + hl;          // row in the tile
@@ -967,16 +965,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int kept = half && (ch & 1) ? 8 : 16;
     const int s0 = c0 + 16 * half;
     const uint32_t keep_bits = (1u << kept) - 1u;
-    auto signal = [&](uint64_t* bar, bool first, int n) {  // n signals of each CTA, this one `first`
-      if (lane == 0) {
-        if (crank == 0) {
-          if (first) mbar_arrive_expect_tx(smem_u32(bar), 4 * n);
-          else mbar_arrive(smem_u32(bar));
-        } else {
-          st_async_signal(mapa_shared(smem_u32(&sm.sink[ws]), 0), mapa_shared(smem_u32(bar), 0));
-        }
-      }
-    };
     // Row groups: 256 threads each (rows 0..31, 32..63 of the CTA); nothing but the
     // signals to the issuer passes between them inside a block.
     const uint32_t group_bar = 4 + (quad & 1), pair_bar = 6 + 2 * ch + (quad & 1);
@@ -1032,10 +1020,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ++G;                                         // the query's slot
       for (int j = g.j0; j < g.j1; ++j, ++G, ++B) {
         const int pb = B & 1, st = G % kStages;
-        // One wait: the issuer of the logits took this block after PV(G-2), so P
-        // buffer pb is free, and after the load and fix warps had passed it on, so
-        // valid and bad are there.
-        if (ok) ok = mbar_wait_warp(smem_u32(&sm.s_full), B & 1, c, abort_flag);
+        // fixed: valid and bad of this CTA's load and fix warps are there (long before
+        // the logits, and not done again before this block's P V).  s_full: the issuer of
+        // the logits took this block after PV(G-2), so P buffer pb is free.
+        if (ok) {
+          const uint32_t fixed = smem_u32(&sm.fixed[st]), full = smem_u32(&sm.s_full), f = (G / kStages) & 1;
+          const bool there = mbar_test(full, B & 1) & mbar_test(fixed, f);  // (both in flight)
+          if (!__all_sync(0xffffffffu, there))
+            ok = mbar_wait_warp(fixed, f, c, abort_flag) && mbar_wait_warp(full, B & 1, c, abort_flag);
+        }
         uint32_t lo[16], hi[16];                   // the part's slots 0..15 and 16..31 (ch odd: 16..23)
         uint32_t vmask = 0;                        // visible ones of the slots that this thread keeps
 #pragma unroll
@@ -1050,7 +1043,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tmem_ld_also16(hi);
           tc_fence_before();
           __syncwarp();
-          signal(&sm.s_free, warp == kWarpSoft0, kSoftWarps);  // the logit buffer is free
+          if (lane == 0) arrive_leader(&sm.s_free, crank);  // the logit buffer is free
         } else {
 #pragma unroll
           for (int t = 0; t < 16; ++t) lo[t] = 0u;
@@ -1190,7 +1183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok) continue;
         l_run += lsum_blk;
         // after the barrier P of all the group's warps is there
-        if (ch == 0 && half == 0) signal(&sm.p_full[pb], quad == 0, 2);
+        if (ch == 0 && half == 0 && lane == 0) arrive_leader_shared(&sm.p_full[pb], crank);
       }
       // ------------------------------- epilogue -------------------------------
       // the row's sum and maximum over its eight threads, while the last P V runs

@@ -357,3 +357,26 @@ def test_bad_pages_between_full_blocks(H, T, R, kind):
         for j in js:
             c.table[i][j] = (-3, c.pool.shape[0])[j % 2]
     c.run(dsa, status=dsa.DSA_ERR_INDEX).check()
+
+
+@pytest.mark.parametrize("lens,T,H,kind", [
+    ([336, 448, 560], 40, 128, "tree"), ([224] * 30, 9, 128, "chain"), ([230] * 40, 5, 128, "any"),
+    ([3360], 100, 128, "chain")])
+def test_every_block_of_every_tile_moves_the_maximum(lens, T, H, kind):
+    # logits rise by 9 from one block of 112 keys to the next (more than O may lag behind, 8 ln 2): short
+    # tiles one after the other, O rescaled in each of their cached blocks
+    dsa = lib()
+    c = Case(lens, T, H, 64, kind)
+    u = torch.randn(c.d_qk, device=DEV, generator=torch.Generator(device=DEV).manual_seed(5))
+    u *= SCALE ** -0.5 / u.norm()
+    c.q = (c.q.float() * 0.25 + u).to(c.dtype)
+    for b, n in enumerate(lens):
+        pos = torch.arange(n, device=DEV)
+        pg = torch.tensor(c.table[b], device=DEV)[pos // c.R]
+        c.pool[pg, pos % c.R] = (c.pool[pg, pos % c.R].float() * 0.25 + (pos // 112)[:, None] * 9.0 * u).to(c.dtype)
+    c.run(dsa).check()
+    first = [x.clone() for x in (c.out, c.m, c.l)]
+    for _ in range(20):
+        c.out.fill_(7)
+        c.run(dsa)
+        assert all(torch.equal(a, b) for a, b in zip(first, (c.out, c.m, c.l)))
