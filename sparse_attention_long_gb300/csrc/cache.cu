@@ -672,7 +672,10 @@ template <typename... A, typename... B>
 static int launch_plan(void (*k256)(A...), void (*k512)(A...), void (*k1024)(A...), Shape sh, size_t smem,
                        cudaStream_t st, B... args) {
   auto kernel = sh.threads == 256 ? k256 : sh.threads == 512 ? k512 : k1024;
-  if (smem > 48 * 1024 &&
+  // (what a kernel may have without asking for more includes its static part)
+  constexpr size_t kStatic = 1024;
+  static_assert(sizeof(Shared) <= kStatic, "static shared memory of the plan kernels");
+  if (smem + kStatic > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return DSA_ERR_CUDA;
   return launch_programmatic(kernel, dim3(sh.ctas), dim3(sh.threads), smem, st, sh.ctas, args...) ? DSA_OK

@@ -297,3 +297,22 @@ def test_refused_calls():
     bad = dsa.dsa_pool(pool.data_ptr(), 2, 64, 256, 64)  # layers run into pages
     assert dsa.lib.dsa_cache_copy_pages(ctypes.byref(c), ctypes.byref(bad), cp.data_ptr(), k.data_ptr(), 1,
                                         None) == dsa.DSA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("n", [3063, 3064, 3068, 3071, 4083, 4084, 4095, 4096, 8192])
+def test_any_number_of_sequences(n):
+    # the plans keep some numbers of each sequence in shared memory: below, around and above the 48 KB that
+    # a kernel has without asking for more (fork 16, extend 12 bytes per sequence, each with some 150 fixed)
+    rng = random.Random(n)
+    R, P, M = 2, 2 * n, 2
+    d = Device(lib(), n, R, P, M)
+    table, lens, refs = random_state(rng, n, R, n, M)
+    refs += [0] * (P - len(refs))
+    n_new = [rng.randint(0, min(2, M * R - x)) for x in lens]
+    got, st = d.extend(n_new, table, lens, refs, sum(n_new) + 5)
+    assert st == 0 and got == list(oc.extend(n_new, table, lens, refs, R, M, sum(n_new) + 5))
+    parent = [i if rng.random() < 0.9 else rng.randrange(n) for i in range(n)]
+    got, st = d.fork(parent, table, lens, refs)
+    assert st == 0 and got == list(oc.fork(parent, table, lens, refs, R, M))
+    got, st = d.compact(table, lens, refs)
+    assert st == 0 and got == list(oc.compact(table, lens, refs, R, M))
