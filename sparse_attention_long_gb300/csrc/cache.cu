@@ -676,7 +676,7 @@ static int launch_plan(void (*k256)(A...), void (*k512)(A...), void (*k1024)(A..
   constexpr size_t kStatic = 1024;
   static_assert(sizeof(Shared) <= kStatic, "static shared memory of the plan kernels");
   if (smem + kStatic > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      !cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
     return DSA_ERR_CUDA;
   return launch_programmatic(kernel, dim3(sh.ctas), dim3(sh.threads), smem, st, sh.ctas, args...) ? DSA_OK
                                                                                                   : DSA_ERR_CUDA;
@@ -709,8 +709,7 @@ static int check_pool(const dsa_cache* p, const dsa_pool* pool, Pool* o) {
 static int vector_bytes(uintptr_t bits) { return (bits & 15) == 0 ? 16 : (bits & 3) == 0 ? 4 : 1; }
 static int sm_count() {
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+  if (!cuda_ok(cudaGetDevice(&dev)) || !cuda_ok(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)))
     return 0;
   return sms;
 }

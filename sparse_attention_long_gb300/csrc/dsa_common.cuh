@@ -453,6 +453,14 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major,
          ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// Whether a runtime call succeeded.  A failure is reported by the call that met it: the
+// runtime's last error, which the next launch's check would read, is cleared.
+inline bool cuda_ok(cudaError_t e) {
+  if (e == cudaSuccess) return true;
+  (void)cudaGetLastError();
+  return false;
+}
+
 // kernel<<<grid, block, smem, st>>>(args...) as a programmatic launch, as a
 // cluster of `cluster` CTAs if that is above 1: for kernels that begin with
 // wait_for_earlier()
@@ -472,7 +480,7 @@ inline bool launch_programmatic(void (*kernel)(A...), dim3 grid, dim3 block, siz
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, A(args)...) == cudaSuccess;
+  return cuda_ok(cudaLaunchKernelEx(&cfg, kernel, A(args)...));
 }
 
 // order-preserving map of fp32 bits to uint32 (-0.0 first folded onto +0.0)

@@ -369,13 +369,12 @@ int dsa_tree_attn_fwd(const dsa_cache* p, const dsa_tree* t, const void* q, cons
   // 24 (2); one tile each 72 items 8.8 against 12 (4); with more CTAs than are
   // resident 160 x 700 rows 38 against 45 (4).
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+  if (!cuda_ok(cudaGetDevice(&dev)) || !cuda_ok(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)))
     return DSA_ERR_CUDA;
   int nc = p->max_pages * p->page_rows > kt ? kMaxCluster : 1;
   while (nc > 1 && items * nc > 2ll * sms) nc /= 2;
   const unsigned grid = (unsigned)(items * nc);
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  if (!cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
     return DSA_ERR_CUDA;
   return launch_programmatic(kernel, dim3(grid), dim3(kThreads), smem, st, nc, a,
                              (const float*)q, (const uint8_t*)pool->base, (long long)pool->page_stride,

@@ -1447,11 +1447,9 @@ bool make_tmap_bf16(CUtensorMap* tm, const void* base, int rank, const uint64_t*
 // CTA pairs of the kernel at most: one CTA per SM (152 SMs when there is no device to ask)
 static int tree_pairs_bound() {
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 2) {
-    cudaGetLastError();
+  if (!cuda_ok(cudaGetDevice(&dev)) || !cuda_ok(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) ||
+      sms < 2)
     sms = 152;
-  }
   return sms / 2;
 }
 static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -1464,21 +1462,19 @@ int launch_tree_attn_tc(const TreeArgs& a, const void* q, const void* pool, long
                         void* out, float* mx, float* sm, void* ws, DevCtx c, cudaStream_t st) {
   using namespace tree;
   const size_t smem = sizeof(Smem);
-  if (cudaFuncSetAttribute(tree_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  if (!cuda_ok(cudaFuncSetAttribute(tree_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
     return DSA_ERR_CUDA;
   static int pairs_by_device[64] = {0};
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
+  if (!cuda_ok(cudaGetDevice(&dev))) return DSA_ERR_CUDA;
   int pairs = dev < 64 ? pairs_by_device[dev] : 0;
   if (pairs <= 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
-    if (cudaOccupancyMaxActiveClusters(&pairs, tree_attn_tc_kernel, &cfg) != cudaSuccess || pairs <= 0) {
-      cudaGetLastError();
+    if (!cuda_ok(cudaOccupancyMaxActiveClusters(&pairs, tree_attn_tc_kernel, &cfg)) || pairs <= 0)
       pairs = tree_pairs_bound();
-    }
     if (dev < 64) pairs_by_device[dev] = pairs;
   }
   const int bound = tree_pairs_bound();

@@ -316,3 +316,37 @@ def test_any_number_of_sequences(n):
     assert st == 0 and got == list(oc.fork(parent, table, lens, refs, R, M))
     got, st = d.compact(table, lens, refs)
     assert st == 0 and got == list(oc.compact(table, lens, refs, R, M))
+
+
+def test_a_launch_that_fails_leaves_nothing_behind():
+    # a call on the legacy stream while another stream is captured is refused by the runtime; the
+    # library's next call, of any kind, is not taken for the one that failed
+    dsa = lib()
+    rt = ctypes.CDLL("libcudart.so.13")
+    d = Device(dsa, 2, 4, 8, 3)
+    t, ln, rf = ints([[1, -1, -1], [2, -1, -1]]), ints([3, 4]), ints([0, 1, 1, 0, 0, 0, 0, 0])
+    o = [torch.empty_like(t), torch.empty_like(ln), torch.empty_like(rf), ints([[0] * 3] * 2), ints([0])]
+    S = 40000                                      # (longer rows than the selection sets attributes for)
+    par, x = ints([0, 1]), torch.randn(4, S, device=DEV)
+    idx = torch.empty(4, 8, dtype=torch.int32, device=DEV)
+    p = dsa.make_params(B=1, S_q=4, S_k=S, H=1, d_qk=8, d_v=8, H_I=1, d_I=8, topk=8, scale=1.0, dtype="fp32",
+                        q_row_offset=S - 4)
+    dsa.cache_fork(d.c, par, t, ln, rf, *o)
+    dsa.topk(p, x, 0, 4, idx)
+    torch.cuda.synchronize()
+    side, legacy, graph = ctypes.c_void_p(), torch.cuda.default_stream(), ctypes.c_void_p()
+    assert legacy.cuda_stream == 0 and rt.cudaStreamCreate(ctypes.byref(side)) == 0
+    assert rt.cudaStreamBeginCapture(side, 0) == 0
+    try:
+        with pytest.raises(dsa.DSAError) as e:
+            dsa.cache_fork(d.c, par, t, ln, rf, *o, stream=legacy)
+    finally:
+        rt.cudaStreamEndCapture(side, ctypes.byref(graph))
+        rt.cudaStreamDestroy(side)
+        rt.cudaGetLastError()
+    assert e.value.code == dsa.DSA_ERR_CUDA
+    dsa.topk(p, x, 0, 4, idx)
+    dsa.cache_fork(d.c, par, t, ln, rf, *o)
+    torch.cuda.synchronize()
+    assert dsa.get_status() == 0
+    assert torch.equal(idx[3].sort().values, x[3].topk(8).indices.int().sort().values)
