@@ -21,8 +21,9 @@ def beam_select(logits, scores, finished, keep, eos):
             if not ok:
                 continue
             top = max(x[v] for v in ok)
-            lse = top + math.log(math.fsum(math.exp(x[v] - top) for v in ok))
-            cand += [(-(s + (x[v] - lse)), w * len(x) + v, w, v, s + (x[v] - lse)) for v in ok]
+            # (x - top first: added to a large maximum the logarithm would be lost)
+            ln = math.log(math.fsum(math.exp(x[v] - top) for v in ok))
+            cand += [(-(s + ((x[v] - top) - ln)), w * len(x) + v, w, v, s + ((x[v] - top) - ln)) for v in ok]
         cand.sort()
         rows = [(b * len(beams) + w, v, s, bool((finished is not None and finished[b][w]) or v == eos))
                 for _, _, w, v, s in cand[:keep]]

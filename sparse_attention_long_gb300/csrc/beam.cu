@@ -26,7 +26,7 @@
 //
 // Bound: for a batch, the logits' way from HBM and some 10 instructions per logit,
 // of which the CTAs of a wave do first the one and then the other: 64 x 8 beams x
-// 131071 bf16 take 31 us, 4.4 TB/s; the first kernel alone 25 us, 5.4 TB/s.
+// 131071 bf16 take 32 us, 4.2 TB/s; the first kernel alone 25 us, 5.4 TB/s.
 // Loading the next chunk ahead of the sums took more registers than it gave.  One
 // request of 4 x 32001: 6.3 us, the two launches and their latencies.
 #include <math.h>
@@ -92,6 +92,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 constexpr float kLog2e = 1.4426950408889634f;
+// Below this size of the maximum m, x log2e - m log2e is one fused product.  From here on
+// the difference comes first: m log2e's rounding error, 2^-25 of it, would be more than a
+// few terms' own errors, and from 2^31 on its power of two overflows.  (64 x 8 beams x
+// 131071 bf16 of which 99 % are masked by -1e9: 37 us; read again one by one 93.)
+constexpr float kFused = 1048576.f;
 
 // a thread's logits in registers, in runs of eight.  kResident: CTAs per SM; bf16
 // 64 x 8 beams x 131071 35.5 / 33.6 / 32.2 / 36.2 us with 7 / 8 / 9 / 10 (registers
@@ -240,9 +245,9 @@ __global__ void __launch_bounds__(kThreads, Logits<T>::kResident)
     m = x.max();
     // sum of exp(x - m) over the thread
     float part = 0.f;
-    if (fabsf(m) < 1e37f) {
-      // 2^(x log2e - mu) with mu = m log2e as rounded; its rounding error, which a
-      // fused product gives exactly, is taken out of the sum at the end
+    if (fabsf(m) < kFused) {
+      // 2^(x log2e - mu) with mu = m log2e as rounded; its rounding error, below 2^-4,
+      // which a fused product gives exactly, is taken out of the sum at the end
       const float mu = m * kLog2e;
       const uint64_t minus = pack2(-mu, -mu);
       uint64_t p[4] = {0ull, 0ull, 0ull, 0ull};
@@ -259,8 +264,20 @@ __global__ void __launch_bounds__(kThreads, Logits<T>::kResident)
       part = (lo + hi) * ex2(-fmaf(m, kLog2e, -mu));
     } else if (m == INFINITY || m != m) {
       part = m;                                    // the vote below sees it
-    } else if (m != -INFINITY) {                   // so large that the product overflows
-      reread(xrow, first, a.vocab, [&](float y, int) { part += ex2((y - m) * kLog2e); });
+    } else if (m != -INFINITY) {                   // (a finite mask, say)
+      const uint64_t minus = pack2(-m, -m);
+      uint64_t p[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int e = 0; e < kVec; e += 2) {
+          float lo, hi;
+          unpack2(add2(pack2(x.get(s, e), x.get(s, e + 1)), minus), lo, hi);
+          p[e >> 1] = add2(p[e >> 1], pack2(ex2(lo * kLog2e), ex2(hi * kLog2e)));
+        }
+      float lo, hi;
+      unpack2(add2(add2(p[0], p[1]), add2(p[2], p[3])), lo, hi);
+      part = lo + hi;
     }
     // the warp's c-th largest thread maximum
     uint32_t v = ordered_key(m), top = 0, largest = 0;
@@ -433,7 +450,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   __shared__ unsigned long long room[kJoinWarps][kKeyRoom];
   __shared__ unsigned long long list[kMaxBeams][kMaxBeams + 1];  // best first: keys, then ordered scores; 0: none
   __shared__ int32_t index[kMaxBeams][kMaxBeams];  // their tokens
-  __shared__ double lse[kMaxBeams];
+  __shared__ float top[kMaxBeams];                 // a beam's largest logit, and the logarithm of
+  __shared__ double ln[kMaxBeams];                 // its sum of exp(x - top): added, a large top would take its bits
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, k = a.wout;
   const int wj = (tid >> 5) % kJoinWarps;
   const bool merges = tid < 32 * kJoinWarps;
@@ -480,8 +498,11 @@ __global__ void __launch_bounds__(kJoinThreads)
           t += __float2ull_rn((float)s[c].sum * ex2((s[c].max - m) * kLog2e) * 0.25f);  // (no logit in a warp: 0 * 0)
 #pragma unroll
         for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        const double v = (double)m + log_of(t, 38);
-        if (lane == 0) lse[w] = v;
+        const double v = log_of(t, 38);
+        if (lane == 0) {
+          top[w] = m;
+          ln[w] = v;
+        }
       }
     }
   }
@@ -493,7 +514,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     const long long row = (long long)b * a.win + w;
     const double sc = (double)scores[row];
     const bool done = finished && finished[row];
-    list[w][r] = ordered64(done ? sc : sc + ((double)key_value(key) - lse[w]));
+    list[w][r] = ordered64(done ? sc : sc + (((double)key_value(key) - (double)top[w]) - ln[w]));
     index[w][r] = done ? a.eos : (int)key_index(key);
   }
   __syncthreads();

@@ -199,3 +199,32 @@ def test_scores_too_large_to_tell_logits_apart():
         best = x[b, w].float().topk(7).indices.tolist()
         assert [(p, t) for p, t, _, _ in got[b]] == [(3 * b + w, t) for t in best]
         assert all(s == float(torch.tensor(-1e30)) for _, _, s, _ in got[b])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("fill", [-1e4, -1e6, -1e9, -3e9, -1e10, -1e20, -1e30, -1e37, -3e38, 5e9, 1e30])
+def test_finite_logits_of_any_size(fill, dtype):
+    """Masks of a finite fill: a row that holds nothing else is uniform, one that holds other logits
+    (if the fill is low) is as if they alone were there."""
+    dsa = lib()
+    V = 9000
+    x = rand(2, 3, V, seed=7)
+    x[0, 1] = fill
+    x[0, 2, :8500] = fill                    # whole chunks, and part of one
+    x[1, 0, ::3] = fill                      # some of each thread's
+    x[1, 1, 100:] = fill
+    x[1, 2, torch.arange(V) // 64 % 2 == 0] = fill  # all of some threads', none of others'
+    check(dsa, x, [[-9.0, 0.0, -9.5], [-1.0, -2.0, -3.0]], None, 32, -1, dtype=dtype)
+    check(dsa, x[:1, 1:2].contiguous(), [[-1.5]], None, 8, -1, dtype=dtype)
+
+
+@pytest.mark.parametrize("size", [1e5, 3e6, 1e9, 2e9, 1e10, 1e20])
+@pytest.mark.parametrize("sign", [-1, 1])
+def test_large_logits_close_together(size, sign):
+    # neighbours among the numbers of that size: whole steps of their last place apart
+    dsa = lib()
+    top = torch.tensor(sign * size, dtype=torch.float32)
+    step = float((torch.nextafter(top, torch.tensor(math.inf)) - top).double())
+    g = torch.Generator().manual_seed(3)
+    x = float(top) - step * torch.randint(0, 400, (1, 2, 5000), generator=g).double() * max(1.0, round(0.01 / step))
+    check(dsa, x, [[-3.0, -3.5]], None, 32, -1)
