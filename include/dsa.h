@@ -486,9 +486,11 @@ int dsa_tree_attn_fwd(const dsa_cache *p, const dsa_tree *t, const void *q, cons
  *   scores_out [n_batch, beams_out] fp32; finished_out [n_batch, beams_out]
  *          uint8 or NULL: parent finished, or token eos
  * A logit of -inf, +inf or NaN is never chosen and counts nothing in the sum.
- * Scores are fp64, from sums of fp32 exponentials: the order of candidates of
- * different beams is that of their scores as far as those tell them apart (to
- * some 2^-20), within a beam that of the logits.
+ * Finite ones count whatever their size.  Scores are fp64, from sums of fp32
+ * exponentials: the order of candidates of different beams is that of their
+ * scores as far as those exponentials tell them apart (each is off by some
+ * 2^-21 of itself; equal logits give scores to 1e-10), within a beam that of
+ * the logits.
  * beams_in, beams_out <= 32, vocab <= 2^24, eos in [-1, vocab) (-1: no such
  * token; finished must be NULL then).  Outputs must not overlap inputs.
  *   workspace: dsa_beam_workspace_size(p) bytes, 16-byte aligned; one call at

@@ -20,15 +20,14 @@
 // Candidates of different beams can lie close together, and their order is an
 // output: the sums are fp32 only inside a thread, a warp adds them as integers
 // (2^-40 of its largest term: the order does not matter), everything after that
-// is fp64 but for the logarithm of a number near 1.  A row gives the same bits
-// wherever it lies: which element a thread takes depends on its index alone, not
-// on alignment.
+// is fp64 or as exact.  A row gives the same bits wherever it lies: which element a
+// thread takes depends on its index alone, not on alignment.
 //
 // Bound: for a batch, the logits' way from HBM and some 10 instructions per logit,
 // of which the CTAs of a wave do first the one and then the other: 64 x 8 beams x
 // 131071 bf16 take 32 us, 4.2 TB/s; the first kernel alone 25 us, 5.4 TB/s.
 // Loading the next chunk ahead of the sums took more registers than it gave.  One
-// request of 4 x 32001: 6.3 us, the two launches and their latencies.
+// request of 4 x 32001: 7.8 us, the two launches and their latencies.
 #include <math.h>
 
 #include "dsa_common.cuh"
@@ -366,19 +365,38 @@ __device__ __forceinline__ unsigned long long ordered64(double x) {
   return (unsigned long long)u ^ ((unsigned long long)(u >> 63) | 0x8000000000000000ull);
 }
 
-// ln(t 2^-unit) for t >= 2^(unit-1): t = f 2^e with f in [0.707, 1.414], whose
-// logarithm is below 0.35, so that fp32 gives it to 2^-24, a fourth of the terms'
-// own error; the rest is fp64 (all of it in fp64, instructions of some 50 cycles one
-// after another, took half a microsecond more).
+// ln(t 2^-unit) for t >= 2^(unit-1), to 2e-11: t = f 2^e with f in [0.707, 1.414],
+// ln f = 2 artanh s, s = (f - 1) / (f + 1), |s| < 0.172, by its power series.  fp64
+// instructions are slow here (some 15 cycles of the SM each), so the quotient is an fp32
+// one and its remainder, and the series is fp32 from s^5 on (at most 2e-4 of the whole;
+// up to s^13, the next term is below 1e-12).  One request took 7.3 us with the logarithm
+// all in fp32, but candidates of different beams that lie closer than 2^-25 changed
+// places; 7.8 like this, 8.0 all in fp64.
 __device__ __forceinline__ double log_of(unsigned long long t, int unit) {
   int e = 63 - __clzll((long long)t);
-  const unsigned long long frac = e > 23 ? t >> (e - 23) : t << (23 - e);  // 24 bits, the first one 1
-  float f = __uint_as_float(((uint32_t)frac & 0x7FFFFFu) | 0x3F800000u);
-  if (f > 1.41421356f) {
-    f *= 0.5f;
+  const unsigned long long frac = e > 52 ? t >> (e - 52) : t << (52 - e);  // 53 bits, the first one 1
+  double f = __longlong_as_double((long long)((frac & 0xFFFFFFFFFFFFFull) | 0x3FF0000000000000ull));
+  if (f > 1.4142135623730951) {
+    f *= 0.5;
     ++e;
   }
-  return fma((double)(e - unit), 0.6931471805599453, (double)logf(f));
+  // the quotient: fp32, corrected by its remainder
+  const double a = f - 1.0, b = f + 1.0;
+  const float bf = __frcp_rn((float)b), s0 = (float)a * bf;
+  const double s = (double)s0 + (double)((float)fma(-(double)s0, b, a) * bf), z = s * s;
+  const float y = s0 * s0;
+  float p = 1.f / 13.f;
+  p = fmaf(p, y, 1.f / 11.f);
+  p = fmaf(p, y, 1.f / 9.f);
+  p = fmaf(p, y, 1.f / 7.f);
+  p = fmaf(p, y, 1.f / 5.f);
+  const double c = 2.0 * s, r = z * (1.0 / 3.0 + (double)(p * y));
+  return fma((double)(e - unit), 0.6931471805599453, fma(c, r, c));
+}
+
+// sum w / 4, w <= 1 taken to 2^-32: the product of integers keeps the sum's bits
+__device__ __forceinline__ unsigned long long scaled(unsigned long long sum, float w) {
+  return __umul64hi(sum, (unsigned long long)__float2uint_rn(w * 2147483648.f) << 31);
 }
 
 // A beam's `k` best keys out of its chunks' sorted lists kr[chunk][k] (one warp, a
@@ -435,10 +453,11 @@ __device__ __forceinline__ int merge_any(const unsigned long long* kr, int chunk
 // chunk and every 32nd after it, the largest head taken each time) while another
 // adds the chunks' sums and takes the logarithm; then every candidate has a thread,
 // which computes its score and, by a binary search in each beam's list, its place.
-// Bound: latency, of which beams_out rounds of warp reductions are the most; the
-// lists are read from global memory once, all loads in flight, where they fit (with a
-// load per round, sum and merge in one warp, and the beams merged by a warp, one
-// request took 8.6 us in all, 6.3 now).
+// One warp takes the logarithms of all beams (lane = beam), in the time of the merges.
+// Bound: latency, of which beams_out rounds of warp reductions and the logarithm are the
+// most; the lists are read from global memory once, all loads in flight, where they fit
+// (with a load per round, sum and merge in one warp, and the beams merged by a warp,
+// 2 us more for one request).
 constexpr int kJoinWarps = 8, kJoinThreads = 2 * 32 * kJoinWarps;
 constexpr int kLists = 4;                           // per lane: 128 chunks, 1M (bf16) or 512K logits
 constexpr int kKeyRoom = 512;                       // keys per warp
@@ -452,6 +471,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   __shared__ int32_t index[kMaxBeams][kMaxBeams];  // their tokens
   __shared__ float top[kMaxBeams];                 // a beam's largest logit, and the logarithm of
   __shared__ double ln[kMaxBeams];                 // its sum of exp(x - top): added, a large top would take its bits
+  __shared__ unsigned long long sum[kMaxBeams];    // that sum, in units of 2^-38; 0: no logit
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, k = a.wout;
   const int wj = (tid >> 5) % kJoinWarps;
   const bool merges = tid < 32 * kJoinWarps;
@@ -490,21 +510,25 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll 4
       for (int c = lane; c < ns; c += 32) m = fmaxf(m, s[c].max);
       m = ordered_value(__reduce_max_sync(0xffffffffu, ordered_key(m)));
+      unsigned long long t = 0;
       if (m != -INFINITY) {
-        // in units of 2^-38 of the row's largest term: below 2^62
-        unsigned long long t = 0;
 #pragma unroll 4
         for (int c = lane; c < ns; c += 32)
-          t += __float2ull_rn((float)s[c].sum * ex2((s[c].max - m) * kLog2e) * 0.25f);  // (no logit in a warp: 0 * 0)
+          t += scaled(s[c].sum, expf(s[c].max - m));  // (no logit in a warp: 0 * 0)
 #pragma unroll
         for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        const double v = log_of(t, 38);
-        if (lane == 0) {
-          top[w] = m;
-          ln[w] = v;
-        }
       }
+      if (lane == 0) {
+        top[w] = m;
+        sum[w] = t;
+      }
+    } else if (lane == 0) {
+      sum[w] = 0;
     }
+  }
+  if (!merges) {                                   // the logarithms, lane = beam, while the lists are merged
+    named_bar_sync(1, 32 * kJoinWarps);
+    if (wj == 0 && lane < a.win && sum[lane] != 0) ln[lane] = log_of(sum[lane], 38);
   }
   __syncthreads();
   for (int i = tid; i < a.win * k; i += kJoinThreads) {

@@ -228,3 +228,25 @@ def test_large_logits_close_together(size, sign):
     g = torch.Generator().manual_seed(3)
     x = float(top) - step * torch.randint(0, 400, (1, 2, 5000), generator=g).double() * max(1.0, round(0.01 / step))
     check(dsa, x, [[-3.0, -3.5]], None, 32, -1)
+
+
+def test_scores_a_few_billionths_apart():
+    """n equal logits: every term and sum is exact, a candidate's score is score - ln n.  Pairs of beams
+    whose candidates differ by 1e-10 to 4e-9 are told apart (a logarithm is off by 2e-11 at most; an fp32
+    one would be off by up to 3e-8)."""
+    dsa = lib()
+    rng = random.Random(1)
+    cases = []
+    while len(cases) < 200:
+        a, b = rng.randrange(1, 4000), rng.randrange(1, 4000)
+        sb = torch.tensor(rng.uniform(-2.0, -1.0)).item()
+        sa = torch.tensor(sb + math.log(a) - math.log(b)).item()   # rounded to fp32
+        if 1e-10 < abs((sa - sb) - (math.log(a) - math.log(b))) < 4e-9:
+            cases.append((a, b, sa, sb))
+    x = torch.full((len(cases), 2, 4000), -INF, dtype=torch.float64)
+    for i, (a, b, _, _) in enumerate(cases):
+        x[i, 0, :a] = x[i, 1, :b] = 0.0
+    got = run(dsa, x, [[sa, sb] for _, _, sa, sb in cases], None, 1, -1)
+    want = [int((sa - sb) < math.log(a) - math.log(b)) for a, b, sa, sb in cases]
+    assert 50 < sum(want) < 150
+    assert [g[0][0] - 2 * i for i, g in enumerate(got)] == want
