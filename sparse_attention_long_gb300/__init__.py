@@ -8,6 +8,7 @@ or ``__graft_entry__.build()``); importing this module without it raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -248,10 +249,21 @@ class _Absent:
         return lambda *args: 1
 
 
+def _present_stamp():
+    # (by its path: `python -m` runs the same file as a module of this package)
+    spec = importlib.util.spec_from_file_location("_dsa_build", os.path.join(_HERE, "_build.py"))
+    build = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(build)
+    return build.binding_stamp(torch.__version__)
+
+
 def _load_native():
     try:
         from . import _binding
-    except ImportError:                            # built without PyTorch's or Python's headers
+        present = _present_stamp()
+    except (ImportError, OSError):                 # built without PyTorch's or Python's headers; no sources here
+        return _Absent()
+    if getattr(_binding, "stamp", None) != present:  # made of another dsa.h, PyTorch or Python
         return _Absent()
     names = ("dsa_cache_fork", "dsa_cache_extend", "dsa_cache_compact", "dsa_cache_copy_pages", "dsa_cache_write",
              "dsa_tree_attn_fwd", "dsa_tree_workspace_size", "dsa_beam_select", "dsa_beam_workspace_size")

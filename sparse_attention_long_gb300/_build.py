@@ -5,8 +5,10 @@ PyTorch's and Python's headers; without those the Python code does its work)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import hashlib
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -41,24 +43,44 @@ def _stale(obj: str, src: str) -> bool:
     return any(os.path.getmtime(d) > os.path.getmtime(obj) for d in deps)
 
 
+def binding_stamp(torch_version: str) -> str:
+    """What _binding.so is made of: the package loads only one that carries the present stamp."""
+    h = hashlib.sha256(f"{torch_version} {sys.version}".encode())
+    for path in (BINDING_SRC, os.path.join(ROOT, "include", "dsa.h")):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()[:16]
+
+
+def _drop_binding() -> None:
+    """An old module must not outlive the sources it was made of."""
+    for path in (BINDING, BINDING + ".tmp"):
+        if os.path.exists(path):
+            os.remove(path)
+
+
 def _binding_job(nvcc: str, force: bool):
-    """The command that builds _binding.so, or None: up to date, or no headers."""
+    """The command that builds _binding.so, or None: up to date, or it cannot be built (then there is none)."""
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.origin:
+        _drop_binding()
         return None
     torch, python = os.path.dirname(spec.origin), sysconfig.get_paths()["include"]
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
     inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"), python,
            cuda, os.path.join(ROOT, "include")]
     deps = [BINDING_SRC, os.path.join(ROOT, "include", "dsa.h"), os.path.join(torch, "version.py"), __file__]
-    if not shutil.which("g++") or not os.path.exists(os.path.join(python, "Python.h")):
-        return None
     if not force and os.path.exists(BINDING) and \
             all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
         return None
-    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", *(f"-I{p}" for p in inc), BINDING_SRC, "-o",
-            BINDING + ".tmp", "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
-            "-lc10_cuda"]
+    if not shutil.which("g++") or not os.path.exists(os.path.join(python, "Python.h")):
+        _drop_binding()
+        return None
+    with open(os.path.join(torch, "version.py")) as f:
+        version = re.search(r"__version__ = '([^']+)'", f.read())
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+            f'-DDSA_STAMP="{binding_stamp(version.group(1) if version else "")}"', *(f"-I{p}" for p in inc), BINDING_SRC, "-o", BINDING + ".tmp", "-L" + os.path.join(torch, "lib"),
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def _build_binding(cmd) -> None:
@@ -66,6 +88,7 @@ def _build_binding(cmd) -> None:
     if r.returncode == 0:
         os.replace(BINDING + ".tmp", BINDING)
     else:
+        _drop_binding()
         print("_binding.so not built, Python marshals the serving calls:\n" + r.stderr[-2000:], file=sys.stderr)
 
 
