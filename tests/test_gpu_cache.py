@@ -350,3 +350,73 @@ def test_a_launch_that_fails_leaves_nothing_behind():
     torch.cuda.synchronize()
     assert dsa.get_status() == 0
     assert torch.equal(idx[3].sort().values, x[3].topk(8).indices.int().sort().values)
+
+
+# more steps than one CTA takes on, more pages than one CTA takes on, both
+@pytest.mark.parametrize("n,R,P,M", [(64, 4, 4000, 300), (9, 16, 20011, 40), (70, 3, 24000, 290)])
+def test_a_cluster_that_cannot_carry_a_call_out_changes_nothing(n, R, P, M):
+    rng = random.Random(P)
+    d = Device(lib(), n, R, P, M)
+    ids = rng.sample(range(P), P // 2)
+    table, lens, refs = [], [], [0] * P
+    for i in range(n):
+        most = min(M, P // 2 // n)
+        lens.append(rng.randint(most // 2, most - 2) * R + 1)  # a partial last page each
+        row = [ids.pop() for _ in range(oc.pages_of(lens[i], R))]
+        for p in row:
+            refs[p] += 1
+        table.append(row + [-1] * (M - len(row)))
+    E, few = d.dsa.DSA_ERR_INDEX, d.dsa.DSA_ERR_PAGES
+    same, grow = list(range(n)), [1] * n
+    f = lambda parent=same, t=table, ln=lens, rf=refs: (d.fork(parent, t, ln, rf), ([t, ln, rf, []]))
+    e = lambda n_new=grow, t=table, ln=lens, rf=refs: (d.extend(n_new, t, ln, rf, n + 3), [t, ln, rf, [-1] * (n + 3)])
+    c = lambda t=table, ln=lens, rf=refs: (d.compact(t, ln, rf), [t, rf, [p if r > 0 else -1 for p, r in enumerate(rf)], []])
+
+    def put(x, i, v):
+        x = list(x)
+        x[i] = v
+        return x
+
+    def check(result, code):
+        (got, st), want = result
+        assert st == code and got == want
+
+    for i in (0, n // 2, n - 1):
+        last = oc.pages_of(lens[i], R) - 1
+        for page in (-1, P, 2 ** 31 - 1, -2 ** 31):
+            for j in (0, last):
+                bad = put(table, i, put(table[i], j, page))
+                check(f(t=bad), E)
+                check(c(t=bad), E)
+            check(e(t=bad), E)                     # (the last page, into which the row goes)
+        for ln in (-1, M * R + 1, 2 ** 31 - 1, -2 ** 31):
+            check(f(ln=put(lens, i, ln)), E)
+            check(e(ln=put(lens, i, ln)), E)
+            check(c(ln=put(lens, i, ln)), E)
+        for parent in (-2, n, 2 ** 31 - 1):
+            check(f(parent=put(same, i, parent)), E)
+        for a in (-1, M * R, n + 4):
+            check(e(n_new=put(grow, i, a)), E)
+        check(f(parent=put(same, i, -1), rf=put(refs, table[i][last], 0)), E)  # a count below the uses given up
+        check(c(rf=put(refs, table[i][0], 0)), E)
+        check(e(rf=put(refs, table[i][last], 2)), E)           # rows into a shared page
+    for p in (0, P // 2, P - 1):
+        if refs[p] == 0:
+            for call in (f, e, c):
+                check(call(rf=put(refs, p, -1)), E)
+    # too few free pages: k of them, and one more needed (first of each request's children keeps its own)
+    for k in (0, 3):
+        free = [p for p, r in enumerate(refs) if r == 0]
+        held = list(refs)
+        for p in free[k:]:
+            held[p] = 1
+        n_new = [R if i <= k else 0 for i in same]             # a page each
+        assert oc.extend(n_new, table, lens, held, R, M, n * R) is None
+        got, st = d.extend(n_new, table, lens, held, n * R)
+        assert st == few and got == [table, lens, held, [-1] * (n * R)]
+        need = [0] * (k + 2) + same[k + 2:]        # k + 1 further children of sequence 0
+        for i in range(1, k + 2):                  # their old pages would fall free: someone holds them
+            for p in table[i][:oc.pages_of(lens[i], R)]:
+                held[p] += 1
+        assert oc.fork(need, table, lens, held, R, M) is None
+        check(f(parent=need, rf=held), few)

@@ -380,3 +380,37 @@ def test_every_block_of_every_tile_moves_the_maximum(lens, T, H, kind):
         c.out.fill_(7)
         c.run(dsa)
         assert all(torch.equal(a, b) for a, b in zip(first, (c.out, c.m, c.l)))
+
+
+@pytest.mark.parametrize("lens,T,H,kind,dtype", [
+    ([700], 1500, 16, "chain", torch.bfloat16), ([0, 130, 2001], [900, 0, 513], 24, "chain", torch.bfloat16),
+    ([300], 700, 128, "chain", torch.bfloat16), ([50, 513], [1000, 300], 8, "tree", torch.bfloat16),
+    ([0, 90], [700, 129], 5, "chain", torch.float32), ([200], 400, 6, "any", torch.float32)])
+def test_chunk_of_a_prompt(lens, T, H, kind, dtype):
+    # more drafted rows than cached ones, over many blocks and words of mask bits
+    kw = dict(d_qk=576, d_v=512) if dtype == torch.bfloat16 else dict(d_qk=80, d_v=64)
+    Case(lens, T, H, 64, kind, dtype=dtype, extra_tok=2, **kw).run(lib()).check()
+
+
+def test_calls_on_two_streams_at_once():
+    # each with a workspace of its own
+    dsa = lib()
+    cases = [Case([900, 3000, 40], [3, 2, 40], 64, 64, "tree", seed=1), Case([5000], 9, 128, 64, "chain", seed=2)]
+    args = [c.args(dsa) for c in cases]
+    want = []
+    for c, a in zip(cases, args):
+        dsa.tree_attn_fwd(*a)
+        torch.cuda.synchronize()
+        c.check()
+        want.append([x.clone() for x in (c.out, c.m, c.l)])
+        for x in (c.out, c.m, c.l):
+            x.fill_(7)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(20):
+        for a, s in zip(args, streams):
+            dsa.tree_attn_fwd(*a, stream=s)
+    torch.cuda.synchronize()
+    assert dsa.get_status() == 0
+    for c, w in zip(cases, want):
+        assert all(torch.equal(x, y) for x, y in zip((c.out, c.m, c.l), w))
