@@ -186,8 +186,8 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t n, bool v) {
   return r != 0;
 }
 // 4-byte store into the peer CTA's shared memory that completes 4 bytes of the
-// transaction count of the peer's barrier `cluster_bar` (release at cluster
-// scope); the issuing thread does not wait for it
+// transaction count of the peer's barrier `cluster_bar`; the issuing thread does
+// not wait for it, and none of its earlier stores is released by it
 __device__ __forceinline__ void st_async_signal(uint32_t cluster_addr, uint32_t cluster_bar) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(cluster_addr),
                "r"(0u), "r"(cluster_bar)
@@ -268,11 +268,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sm.st_empty[i]), 1);
     }
     mbar_init(smem_u32(&sm.s_full), 1);
-    // s_free, p_full, q_tm (used in CTA 0): the 8 local softmax warps arrive,
-    // the first of them also expecting the 8 x 4 bytes CTA 1's warps store
+    // s_free, q_tm (used in CTA 0, tensor memory only): the 8 local softmax warps
+    // arrive, the first of them also expecting the 8 x 4 bytes CTA 1's warps store;
+    // p_full, which hands over P in shared memory: the softmax warps of both CTAs arrive
     mbar_init(smem_u32(&sm.s_free), kSoftWarps);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sm.p_full[i]), kSoftWarps);  // blocks of parity i
+      mbar_init(smem_u32(&sm.p_full[i]), 2 * kSoftWarps);  // blocks of parity i
       // tokens of parity i: the local gather warps store the query, the first
       // also expecting CTA 1's gather warps' 4 x 4 bytes (used in CTA 0)
       mbar_init(smem_u32(&sm.q_tm[i]), kGatherWarps);
@@ -792,7 +793,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        signal(&sm.p_full[pb]);
+        if (lane == 0) arrive_leader_shared(&sm.p_full[pb], crank);
       }
       // this token's masks are no longer read
       __syncwarp();

@@ -220,21 +220,6 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t n, bool v) {
       : "memory");
   return r != 0;
 }
-// Signals to the issuers: an arrive on a barrier of CTA 0 from either CTA of the pair,
-// for a thread that waits at cluster scope.  arrive_leader orders accesses to tensor
-// memory only (by the tcgen05 fences on both sides).  arrive_leader_shared also hands
-// over what this thread wrote to its CTA's shared memory or knows of through a barrier of
-// its CTA.  Its fence is restricted to shared memory: 64 cycles with the arrive, where
-// the release of all memory at cluster scope takes 350 (trees of 48 tokens: 19 % more
-// time).
-__device__ __forceinline__ void arrive_leader(uint64_t* bar, uint32_t crank) {
-  if (crank == 0) mbar_arrive(smem_u32(bar));
-  else mbar_arrive_remote_relaxed(mapa_shared(smem_u32(bar), 0));
-}
-__device__ __forceinline__ void arrive_leader_shared(uint64_t* bar, uint32_t crank) {
-  if (crank != 0) asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
-  arrive_leader(bar, crank);
-}
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
