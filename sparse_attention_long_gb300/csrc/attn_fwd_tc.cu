@@ -47,10 +47,11 @@
 // ready PV, so the logits of block j+1 run during the softmax of block j.
 //
 // CTA 0 must know when CTA 1's operands are ready and its logits read.  CTA
-// 1's softmax warps signal CTA 0's barriers with 4-byte st.async stores that
-// complete on them (a cluster-scope arrive costs the arriving thread ~300
-// cycles, the store ~6); CTA 0's first softmax warp expects those bytes when
-// it arrives.  CTA 1's gathered blocks reach CTA 0's stage barriers through
+// 1's softmax warps signal what concerns tensor memory (logits read, query there)
+// with 4-byte st.async stores that complete on CTA 0's barriers; CTA 0's first
+// warp expects those bytes when it arrives.  P, in shared memory, they hand over
+// by an arrive behind a release fence restricted to shared memory (64 cycles; the
+// release of all memory takes ~340).  CTA 1's gathered blocks reach CTA 0's stage barriers through
 // the relay thread (a proxy fence, then a cluster-scope arrive).
 //
 // Roles per CTA: warp 0 = TMEM allocation, the MMA issuer in CTA 0 and the

@@ -25,7 +25,7 @@
 //
 // Bound: for a batch, the logits' way from HBM and some 10 instructions per logit,
 // of which the CTAs of a wave do first the one and then the other: 64 x 8 beams x
-// 131071 bf16 take 32 us, 4.2 TB/s; the first kernel alone 25 us, 5.4 TB/s.
+// 131071 bf16 take 33 us, 4.1 TB/s; the first kernel alone 26 us, 5.1 TB/s.
 // Loading the next chunk ahead of the sums took more registers than it gave.  One
 // request of 4 x 32001: 7.8 us, the two launches and their latencies.
 #include <math.h>

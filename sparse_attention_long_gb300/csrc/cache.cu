@@ -13,8 +13,8 @@
 // sets the status word.
 //
 // Bound: a few cluster barriers and dependent L2 reads.  Fork, extend and compact
-// of 16 sequences and 2048 pages take 5.0, 4.4 and 6.3 us, of 256 sequences and
-// 98304 pages 13.0, 10.1 and 26 us; the tables and refs are read at L2 rate.
+// of 16 sequences and 2048 pages take 5.5, 4.3 and 6.6 us, of 256 sequences and
+// 98304 pages 15.6, 9.6 and 27 us; the tables and refs are read at L2 rate.
 #include <limits.h>
 
 #include "dsa_common.cuh"

@@ -50,14 +50,17 @@
 // between two tiles).
 //
 // Bound.  A block's MMAs take 1,956 cycles back to back (logits 1,008, P V 896);
-// the loop takes about 2,750 per block (keys from L2) to 3,000 (from HBM), a tile
+// the loop takes about 2,800 per block (keys from L2) to 3,050 (from HBM), a tile
 // change some 5,500 more.  The loop is the softmax warps' chain of waits: logits
 // out of TMEM, the exchange through shared memory (whose bandwidth the operands'
 // reads, the copies and the exchange use to two thirds), P back, and the signals
-// between the CTAs.  Measured: 16 trees of 48 tokens over 2K-6K rows, 128 heads,
-// 660 us = 1,330 TFLOP/s; 64 single tokens over 1K-16K rows 144 us = 4.5 TB/s and
-// 1,060 TFLOP/s (12 us of it the join; tensor pipes 53 % and DRAM 62 % busy); one
-// token over 1K rows 14 us (the two launches, one tile, the join).
+// between the CTAs.  Measured, each call on other inputs than the last: 16 trees of 48
+// tokens over 2K-6K rows, 128 heads, 714 us = 1,230 TFLOP/s (the same inputs again and
+// again: 673 us); 64 single tokens over 1K-16K rows 152 us = 4.3 TB/s and 1,010 TFLOP/s
+// (12 us of it the join; tensor pipes 53 % and DRAM 61 % busy); one token over 1K rows
+// 15 us (the two launches, one tile, the join); 1,024 tokens after 16K rows 3,220 us =
+// 1,500 TFLOP/s.  A prompt's first 2,048 tokens take 1,080 us, 540 TFLOP/s: their blocks
+// are drafted ones, whose copies are of 8 rows and pass the fix warps.
 //
 // Roles per CTA: warp 0 = TMEM allocation, MMA issuer of the logits (CTA 0);
 // warps 1..4 = query into TMEM, passing on of key stages (with the zeroing
