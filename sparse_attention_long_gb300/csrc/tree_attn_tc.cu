@@ -62,6 +62,10 @@
 // 1,500 TFLOP/s.  A prompt's first 2,048 tokens take 1,080 us, 540 TFLOP/s: their blocks
 // are drafted ones, whose copies are of 8 rows and pass the fix warps.
 //
+// A wait tests the parity of a barrier's phase: no barrier may complete two phases ahead
+// of a waiting thread.  tests/test_tree_ring.py models the roles' order of waits and
+// arrivals for that; a change of either belongs in both.
+//
 // Roles per CTA: warp 0 = TMEM allocation, MMA issuer of the logits (CTA 0);
 // warps 1..4 = query into TMEM, passing on of key stages (with the zeroing
 // above); warps 5..20 = softmax and epilogue; warp 21 = MMA issuer of P V (CTA
