@@ -5,7 +5,8 @@
  * attention (MLA weight-absorbed) over the selected kv rows, its backward, and
  * the indexer KL loss with its gradients.  For serving: a paged cache of kv
  * rows, its bookkeeping on the device, attention of drafted tokens over it,
- * and beam selection.
+ * and beam selection.  Around the attention: rotary positions of its inputs
+ * (and their gradients), sampling of tokens, acceptance of drafted ones.
  *
  * Sources (pages):
  *  [DSA-32K] "CANN&TorchTitan: DeepSeek-V3.2 32k long-sequence pretraining on
@@ -63,7 +64,8 @@ enum {
   DSA_ERR_CUDA = -4,        /* a CUDA launch or runtime call failed            */
   DSA_ERR_TIMEOUT = -5,     /* (device) a bounded wait ran out of time         */
   DSA_ERR_INDEX = -6,       /* (device) a top-k index outside [-1, S_k); a page,
-                               length, parent or row index out of range (cache) */
+                               length, parent or row index out of range (cache);
+                               a sampling setting out of range */
   DSA_ERR_PAGES = -7        /* (device) the cache has too few free pages       */
 };
 
@@ -506,6 +508,131 @@ size_t dsa_beam_workspace_size(const dsa_beam *p);
 int dsa_beam_select(const dsa_beam *p, const void *logits, const float *scores, const uint8_t *finished,
                     int32_t *parent, int32_t *token, float *scores_out, uint8_t *finished_out, void *workspace,
                     dsa_stream_t stream);
+
+/*
+ * Rotary positions (this library's own addition: the pages take the rope
+ * columns of query and key as already rotated).  Pair i of a head's rot_dim
+ * rotated columns turns by angle = pos[t] * f_i:
+ *   (a, b) -> mscale * (a cos - b sin, a sin + b cos);
+ * transposed, sin counts negative: that is the gradient's way back.  One call
+ * serves up to four tensors of a layer (q, kv, q_I, k_I), each with its own
+ * type and layout: DSA_ROPE_INTERLEAVED pairs columns 2i, 2i+1, DSA_ROPE_HALF
+ * columns i, i + rot_dim/2 of the rotated part, which begins at `offset`.
+ *
+ * step[i] is the angle per position in units of 2^-64 turns; an angle is
+ * pos * step modulo one turn, exact whatever the position (steps by dsa_rope_steps
+ * are rounded to 53 bits: at position 2^31 an angle is off by 2^-22 at most).
+ * Arithmetic is fp32, each result rounded once.
+ */
+enum { DSA_ROPE_INTERLEAVED = 0, DSA_ROPE_HALF = 1 };
+enum { DSA_ROPE_PLAIN = 0, DSA_ROPE_LINEAR = 1, DSA_ROPE_NTK = 2, DSA_ROPE_YARN = 3 };
+enum { DSA_ROPE_PARTS = 4, DSA_ROPE_MAX_DIM = 256 };
+typedef struct {
+  int32_t dtype, layout;      /* DSA_BF16 or DSA_FP32; DSA_ROPE_*              */
+  int64_t heads, dim, offset; /* a head's columns; the first rotated one       */
+} dsa_rope_part;
+typedef struct {
+  int32_t rot_dim, n_parts;   /* even, 2..256; 1..4                            */
+  float mscale;               /* factor of cos and sin, 1 as a rule            */
+  int32_t reserved0;
+  dsa_rope_part part[DSA_ROPE_PARTS];
+  uint64_t step[DSA_ROPE_MAX_DIM / 2];
+} dsa_rope;
+/* Element (t, h, d) of a tensor: base + t * tok_stride + h * head_stride + d elements. */
+typedef struct {
+  void *base;
+  int64_t tok_stride, head_stride;
+} dsa_rope_rows;
+
+/*
+ * Host only: fills p->step from p->rot_dim.  f_i = base^(-2i / rot_dim), for a
+ * context of `factor` times the trained length (`original` positions)
+ *   DSA_ROPE_LINEAR: f_i / factor
+ *   DSA_ROPE_NTK: base times factor^(rot_dim / (rot_dim - 2))
+ *   DSA_ROPE_YARN: pairs that turn more than beta_fast times in `original`
+ *          positions keep f_i, those that turn less than beta_slow times get
+ *          f_i / factor, between them the two are mixed linearly in i.
+ * factor, original, beta_fast, beta_slow are read by the schemes that use them.
+ */
+int dsa_rope_steps(dsa_rope *p, double base, int scaling, double factor, double original, double beta_fast,
+                   double beta_slow);
+
+/*
+ * Rotates n_tok tokens.
+ *   pos [n_tok] int32, any value
+ *   x, out [n_parts]: out is the same rows as x (in place: only the rotated
+ *          columns are touched), or a span of memory that does not meet x's
+ *          (the other columns are copied).  x may hold rows twice (stride 0),
+ *          out's rows must not overlap.  Aligned to their elements.  Two parts
+ *          must not write the same elements, nor one what another reads.
+ *   heads * n_tok < 2^31 for each part, dim <= 2^20.
+ */
+int dsa_rope_apply(const dsa_rope *p, int64_t n_tok, const int32_t *pos, const dsa_rope_rows *x,
+                   const dsa_rope_rows *out, int transposed, dsa_stream_t stream);
+
+/*
+ * Sampling (this library's own addition).  One token per row of logits x, from
+ * one given uniform number u in [0, 1) per row:
+ *   w_v = exp((x_v - max x) / temperature), larger logits first, ties to the
+ *   lower v; kept are the tokens with w_v >= min_p, of those the first top_k,
+ *   of those the shortest run whose mass reaches top_p of theirs, one at least;
+ *   token = the lowest kept v at which the mass of the kept tokens up to v
+ *   exceeds u times the mass of all kept; prob = w_token / that mass.
+ * Temperature 0: the largest logit (prob 1).  A logit of -inf, +inf or NaN is
+ * never chosen and counts nothing; a row without another gives token -1, prob
+ * 0.  Finite ones count whatever their size, masks of the type's lowest value
+ * too.
+ *   logits [rows, ld], vocab of each ld used; dtype
+ *   u [rows] fp32
+ *   temperature (NULL: 1), top_k (NULL or 0: all), top_p (NULL or 1: all),
+ *          min_p (NULL or 0: all) [requests] fp32, top_k int32: settings of a
+ *          request; row r has those of index[r] ([rows] int32), of r without
+ *          an index (requests == rows then)
+ *   token [rows] int32, prob [rows] fp32 or NULL
+ * A row whose numbers are out of range (u outside [0, 1), temperature or top_k
+ * below 0, top_p outside (0, 1], min_p outside [0, 1], a NaN, an index) gives
+ * token -1, prob 0 and DSA_ERR_INDEX; what its request does not use is not
+ * looked at (a NULL array, and with temperature 0 all but the temperature).
+ * Weights are good to 2^-30 of themselves, sums are integers in units of 2^-44
+ * of the largest weight or finer: a row gives the same bits wherever it lies,
+ * and a token lighter than a unit is never drawn.
+ * vocab <= 2^18.  Outputs must not overlap inputs.
+ */
+typedef struct {
+  int32_t dtype; /* DSA_BF16 or DSA_FP32 */
+  int32_t reserved0;
+  int64_t rows, vocab, ld, requests;
+} dsa_sampler;
+
+int dsa_sample(const dsa_sampler *p, const void *logits, const float *u, const float *temperature,
+               const int32_t *top_k, const float *top_p, const float *min_p, const int32_t *index, int32_t *token,
+               float *prob, dsa_stream_t stream);
+
+/*
+ * Acceptance of drafted tokens (this library's own addition): which of the
+ * tokens that dsa_tree_attn_fwd attended to a sequence keeps, and what follows
+ * them.  drafted[t] is token t itself, sampled[t] the one that the model's
+ * logits at t gave (of dsa_sample, say).  A sequence's drafted token 0 is the
+ * one that its last step ended with; it is kept.  The parent of token t is the
+ * last token before t that t sees.  From a kept token t the sequence goes on to
+ * its first child c with drafted[c] == sampled[t]; where there is none, or
+ * sampled[t] is eos or negative, it ends, and sampled[t] is what follows.  A tree of drafts
+ * is tested against one sampled path, so the result follows the model's
+ * distribution whatever was drafted.
+ *   p, t: n_seqs, n_tok and mask_words are read, tok_start and mask are those of
+ *          dsa_tree_attn_fwd (no mask: a chain)
+ *   drafted, sampled [n_tok] int32; eos -1: none
+ *   n_new [n_seqs]: kept tokens, for dsa_cache_extend (0 without drafted tokens)
+ *   row_index [n_tok]: their rows, sequence 0's first, for dsa_cache_write
+ *          beside the slots of dsa_cache_extend; -1 behind the last
+ *   tokens [n_tok]: sampled[row_index[i]], what the sequences gained; -1 likewise
+ *   next [n_seqs]: a sequence's last of those (-1 without drafted tokens)
+ * A sequence whose numbers are out of range keeps nothing (DSA_ERR_INDEX).
+ * Outputs must not overlap inputs.
+ */
+int dsa_tree_accept(const dsa_cache *p, const dsa_tree *t, const int32_t *tok_start, const uint64_t *mask,
+                    const int32_t *drafted, const int32_t *sampled, int64_t eos, int32_t *n_new, int32_t *row_index,
+                    int32_t *tokens, int32_t *next, dsa_stream_t stream);
 
 /*
  * Device status.  Synchronises `stream`, then writes the device status word

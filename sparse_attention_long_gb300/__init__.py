@@ -24,6 +24,9 @@ DSA_CP_COLOSSAL, DSA_CP_ULYSSES = 0, 1
 DSA_CALL_FORWARD, DSA_CALL_ATTN_FWD, DSA_CALL_ATTN_BWD, DSA_CALL_KL_BWD, DSA_CALL_BACKWARD = 0, 1, 2, 3, 4
 DSA_CALL_INDEXER_TOPK = 5
 DSA_FLAG_CAUSAL_ONLY, DSA_FLAG_FP8_INDEXER, DSA_FLAG_FUSED_TOPK = 1, 2, 4
+DSA_ROPE_INTERLEAVED, DSA_ROPE_HALF = 0, 1
+DSA_ROPE_PLAIN, DSA_ROPE_LINEAR, DSA_ROPE_NTK, DSA_ROPE_YARN = 0, 1, 2, 3
+DSA_ROPE_PARTS, DSA_ROPE_MAX_DIM = 4, 256
 
 _ERRNAMES = {0: "DSA_OK", -1: "DSA_ERR_INVALID_ARG", -2: "DSA_ERR_UNSUPPORTED",
              -3: "DSA_ERR_WORKSPACE", -4: "DSA_ERR_CUDA", -5: "DSA_ERR_TIMEOUT", -6: "DSA_ERR_INDEX",
@@ -69,6 +72,26 @@ class dsa_beam(ctypes.Structure):
                 ("ld", ctypes.c_int64), ("eos", ctypes.c_int64)]
 
 
+class dsa_rope_part(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("layout", ctypes.c_int32), ("heads", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("offset", ctypes.c_int64)]
+
+
+class dsa_rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("n_parts", ctypes.c_int32), ("mscale", ctypes.c_float),
+                ("reserved0", ctypes.c_int32), ("part", dsa_rope_part * DSA_ROPE_PARTS),
+                ("step", ctypes.c_uint64 * (DSA_ROPE_MAX_DIM // 2))]
+
+
+class dsa_rope_rows(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("tok_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class dsa_sampler(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("reserved0", ctypes.c_int32), ("rows", ctypes.c_int64),
+                ("vocab", ctypes.c_int64), ("ld", ctypes.c_int64), ("requests", ctypes.c_int64)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
                       "(nvcc, sm_103a); there is no fallback implementation")
@@ -78,6 +101,8 @@ _vp, _i64, _i32p = ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p
 _P = ctypes.POINTER(dsa_params)
 _C, _L, _T = ctypes.POINTER(dsa_cache), ctypes.POINTER(dsa_pool), ctypes.POINTER(dsa_tree)
 _B = ctypes.POINTER(dsa_beam)
+_R, _RR, _S = ctypes.POINTER(dsa_rope), ctypes.POINTER(dsa_rope_rows), ctypes.POINTER(dsa_sampler)
+_f64 = ctypes.c_double
 _sigs = {
     "dsa_version": ([], ctypes.c_int),
     "dsa_workspace_size": ([_P, ctypes.c_int], ctypes.c_size_t),
@@ -101,6 +126,10 @@ _sigs = {
     "dsa_tree_attn_fwd": ([_C, _T, _vp, _L] + [_vp] * 10, ctypes.c_int),
     "dsa_beam_workspace_size": ([_B], ctypes.c_size_t),
     "dsa_beam_select": ([_B] + [_vp] * 9, ctypes.c_int),
+    "dsa_rope_steps": ([_R, _f64, ctypes.c_int, _f64, _f64, _f64, _f64], ctypes.c_int),
+    "dsa_rope_apply": ([_R, _i64, _vp, _RR, _RR, ctypes.c_int, _vp], ctypes.c_int),
+    "dsa_sample": ([_S] + [_vp] * 10, ctypes.c_int),
+    "dsa_tree_accept": ([_C, _T] + [_vp] * 4 + [_i64] + [_vp] * 5, ctypes.c_int),
     "dsa_get_status": ([_vp, ctypes.POINTER(ctypes.c_int)], ctypes.c_int),
     "dsa_set_wait_budget_ns": ([ctypes.c_uint64], ctypes.c_int),
     "dsa_selftest_wait_timeout": ([ctypes.c_uint64, _vp], ctypes.c_int),
@@ -266,8 +295,10 @@ def _load_native():
     if getattr(_binding, "stamp", None) != present:  # made of another dsa.h, PyTorch or Python
         return _Absent()
     names = ("dsa_cache_fork", "dsa_cache_extend", "dsa_cache_compact", "dsa_cache_copy_pages", "dsa_cache_write",
-             "dsa_tree_attn_fwd", "dsa_tree_workspace_size", "dsa_beam_select", "dsa_beam_workspace_size")
-    _binding.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names), dsa_cache, dsa_tree, dsa_beam)
+             "dsa_tree_attn_fwd", "dsa_tree_workspace_size", "dsa_beam_select", "dsa_beam_workspace_size",
+             "dsa_rope_apply", "dsa_sample", "dsa_tree_accept")
+    _binding.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names), dsa_cache, dsa_tree, dsa_beam,
+                  dsa_rope, dsa_sampler)
     return _binding
 
 
@@ -509,6 +540,115 @@ def beam_select(b, logits, scores, finished, parent, token, scores_out, finished
           _arg(scores_out, "scores_out", f32, outs, d, w),
           None if finished_out is None else _arg(finished_out, "finished_out", u8, outs, d, w),
           _workspace(workspace, beam_workspace_size(b), d, w))
+
+
+# ------------------------------ rotary positions ------------------------------
+def rope_part(*, heads, dim, offset=0, layout="interleaved", dtype="bf16") -> dsa_rope_part:
+    """One tensor of rope_apply: rows of `heads` heads of `dim` columns, of which rot_dim from `offset` on are rotated;
+    layout "interleaved" pairs columns 2i and 2i + 1, "half" i and i + rot_dim / 2."""
+    return dsa_rope_part({"bf16": DSA_BF16, "fp32": DSA_FP32}[dtype],
+                         {"interleaved": DSA_ROPE_INTERLEAVED, "half": DSA_ROPE_HALF}[layout], heads, dim, offset)
+
+
+def make_rope(*, rot_dim, parts, base=10000.0, scaling=None, factor=1.0, original=0, beta_fast=32.0, beta_slow=1.0,
+              mscale=1.0) -> dsa_rope:
+    """Frequencies base^(-2i / rot_dim) and up to four tensors (rope_part) that rope_apply rotates.  scaling, for a
+    context `factor` times the trained one: None, "linear", "ntk" or "yarn" (`original`: the trained length)."""
+    parts = list(parts)
+    if not 1 <= len(parts) <= DSA_ROPE_PARTS:
+        raise ValueError(f"make_rope: 1 to {DSA_ROPE_PARTS} parts")
+    r = dsa_rope(rot_dim, len(parts), mscale, 0, tuple(parts))
+    kind = {None: DSA_ROPE_PLAIN, "linear": DSA_ROPE_LINEAR, "ntk": DSA_ROPE_NTK, "yarn": DSA_ROPE_YARN}[scaling]
+    _chk(lib.dsa_rope_steps(ctypes.byref(r), base, kind, factor, original, beta_fast, beta_slow), "dsa_rope_steps")
+    return r
+
+
+def _rope_rows(t, name, part, n_tok, device, where):
+    """dsa_rope_rows of a tensor [..., heads, dim] ([..., dim] with one head) whose leading dimensions are n_tok rows at
+    one stride."""
+    dt = torch.bfloat16 if part.dtype == DSA_BF16 else torch.float32
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != device or t.dtype is not dt:
+        _refuse(where, name, t, dt, 0, device, at_least=True)
+        raise TypeError(f"{where}: {name} is {t.dtype}, needs {dt}")
+    sh, st = list(t.shape), list(t.stride())
+    if not sh or sh[-1] != part.dim or (part.dim > 1 and st[-1] != 1):
+        raise ValueError(f"{where}: {name} must have {part.dim} contiguous columns")
+    sh, st, head = sh[:-1], st[:-1], 0
+    if part.heads > 1:
+        if not sh or sh[-1] != part.heads:
+            raise ValueError(f"{where}: {name} must be [..., {part.heads}, {part.dim}]")
+        head, sh, st = st[-1], sh[:-1], st[:-1]
+    n, tok = 1, 0
+    for size, stride in zip(reversed(sh), reversed(st)):
+        if size == 1:
+            continue
+        if n == 1:
+            tok = stride
+        elif stride != tok * n:
+            raise ValueError(f"{where}: the tokens of {name} must lie at one stride")
+        n *= size
+    if n != n_tok:
+        raise ValueError(f"{where}: {name} has {n} tokens, pos {n_tok}")
+    return dsa_rope_rows(t.data_ptr(), tok, head)
+
+
+def rope_apply(r, pos, x, out=None, transposed=False, stream=None):
+    """Rotates the tensors x (one per part of r, [..., heads, dim]) of the tokens at pos (int32) into out (None: in
+    place); transposed: gradients of the results into gradients of the inputs."""
+    w = "dsa_rope_apply"
+    out = x if out is None else out
+    if stream is None and _made(_native.rope_apply(r, pos, x, out, transposed), w):
+        return
+    d = _device(pos, w, "pos")
+    n = pos.numel()
+    if len(x) != r.n_parts or len(out) != r.n_parts:
+        raise ValueError(f"{w}: x and out must have {r.n_parts} tensors")
+    rows = [(dsa_rope_rows * r.n_parts)(*(_rope_rows(t, f"{name}[{i}]", r.part[i], n, d, w) for i, t in enumerate(ts)))
+            for name, ts in (("x", x), ("out", out))]
+    _call(lib.dsa_rope_apply, w, d, stream, ctypes.byref(r), n, _arg(pos, "pos", _I32, n, d, w), *rows,
+          int(bool(transposed)))
+
+
+# ---------------------------------- sampling ----------------------------------
+def make_sampler(*, rows, vocab, ld=None, dtype="bf16", requests=None) -> dsa_sampler:
+    """Sizes of sample; logits rows are ld >= vocab elements apart (vocab if None).  requests: how many settings there
+    are, if not one per row."""
+    return dsa_sampler({"bf16": DSA_BF16, "fp32": DSA_FP32}[dtype], 0, rows, vocab, vocab if ld is None else ld,
+                       rows if requests is None else requests)
+
+
+def sample(s, logits, u, temperature, top_k, top_p, min_p, index, token, prob=None, stream=None):
+    """A token per row of logits by the uniform numbers u, and its probability.  Settings [requests] fp32 (top_k int32)
+    or None; row r has those of index[r] (int32), of r without an index."""
+    w, f32 = "dsa_sample", torch.float32
+    if stream is None and _made(_native.sample(s, logits, u, temperature, top_k, top_p, min_p, index, token, prob), w):
+        return
+    d, n, m = _device(logits, w, "logits"), s.rows, s.requests
+    setting = lambda t, name, dt: None if t is None else _arg(t, name, dt, m, d, w)
+    _call(lib.dsa_sample, w, d, stream, ctypes.byref(s),
+          _arg(logits, "logits", torch.bfloat16 if s.dtype == DSA_BF16 else f32, n * s.ld, d, w),
+          _arg(u, "u", f32, n, d, w), setting(temperature, "temperature", f32), setting(top_k, "top_k", _I32),
+          setting(top_p, "top_p", f32), setting(min_p, "min_p", f32),
+          None if index is None else _arg(index, "index", _I32, n, d, w), _arg(token, "token", _I32, n, d, w),
+          None if prob is None else _arg(prob, "prob", f32, n, d, w))
+
+
+# ------------------------ acceptance of drafted tokens ------------------------
+def tree_accept(c, t, tok_start, mask, drafted, sampled, n_new, row_index, tokens, next_token, eos=-1, stream=None):
+    """Which drafted tokens of tree_attn_fwd each sequence keeps, given the tokens sampled at each: n_new (for
+    cache_extend), row_index [n_tok] (for cache_write, -1 behind the last), tokens [n_tok] (what was gained) and
+    next_token (each sequence's last)."""
+    w = "dsa_tree_accept"
+    if stream is None and _made(_native.tree_accept(c, t, tok_start, mask, drafted, sampled, n_new, row_index, tokens,
+                                                    next_token, eos), w):
+        return
+    d, n, n_tok = _device(tok_start, w, "tok_start"), c.n_seqs, t.n_tok
+    _call(lib.dsa_tree_accept, w, d, stream, ctypes.byref(c), ctypes.byref(t),
+          _arg(tok_start, "tok_start", _I32, n + 1, d, w),
+          None if mask is None else _arg(mask, "mask", torch.int64, n_tok * t.mask_words, d, w),
+          _arg(drafted, "drafted", _I32, n_tok, d, w), _arg(sampled, "sampled", _I32, n_tok, d, w), eos,
+          _arg(n_new, "n_new", _I32, n, d, w), _arg(row_index, "row_index", _I32, n_tok, d, w),
+          _arg(tokens, "tokens", _I32, n_tok, d, w), _arg(next_token, "next_token", _I32, n, d, w))
 
 
 def get_status(stream=None) -> int:

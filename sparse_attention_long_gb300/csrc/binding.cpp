@@ -28,8 +28,11 @@ struct Lib {
   decltype(&dsa_tree_workspace_size) tree_size;
   decltype(&dsa_beam_select) beam;
   decltype(&dsa_beam_workspace_size) beam_size;
+  decltype(&dsa_rope_apply) rope;
+  decltype(&dsa_sample) sample;
+  decltype(&dsa_tree_accept) accept;
 } lib;
-PyObject *cache_type, *tree_type, *beam_type;      // of the ctypes structures
+PyObject *cache_type, *tree_type, *beam_type, *rope_type, *sampler_type;      // of the ctypes structures
 
 // sizes multiply to a tensor's element count; -1 matches none
 int64_t times(int64_t a, int64_t b) {
@@ -95,6 +98,32 @@ class Args {
     const int64_t layers = k ? t.size(0) : 1;
     return dsa_pool{t.data_ptr(), layers, layers > 1 ? t.stride(0) * e : page,
                     c.n_pages > 1 ? t.stride(k) * e : page, D * e};
+  }
+  // n_tok rows of heads, leading dimensions at one stride
+  dsa_rope_rows rope_rows(PyObject* o, const dsa_rope_part& p, int64_t n_tok) {
+    const at::Tensor& t = tensor(o);
+    int64_t k = t.dim() - 1;
+    if (t.scalar_type() != (p.dtype == DSA_BF16 ? at::kBFloat16 : at::kFloat) || k < 0 || t.size(k) != p.dim ||
+        (p.dim > 1 && t.stride(k) != 1))
+      throw Refused();
+    dsa_rope_rows r{t.data_ptr(), 0, 0};
+    if (p.heads > 1) {
+      if (--k < 0 || t.size(k) != p.heads) throw Refused();
+      r.head_stride = t.stride(k);
+    }
+    int64_t n = 1;
+    while (--k >= 0) {
+      if (t.size(k) == 1) continue;
+      if (n == 1) r.tok_stride = t.stride(k);
+      else if (t.stride(k) != times(r.tok_stride, n)) throw Refused();
+      n *= t.size(k);
+    }
+    if (n != n_tok) throw Refused();
+    return r;
+  }
+  template <typename T>
+  T* exactly_or_none(PyObject* o, at::ScalarType type, int64_t n) {
+    return o == Py_None ? nullptr : static_cast<T*>(exactly(o, type, n));
   }
   void* workspace(PyObject* o, size_t need) {
     if (o == Py_None) {
@@ -257,11 +286,71 @@ PyObject* beam_select(PyObject*, PyObject* const* o, Py_ssize_t n) {
   });
 }
 
+PyObject* rope_apply(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  return answer(n, 5, [&] {
+    const dsa_rope r = structure<dsa_rope>(o[0], rope_type);
+    if (r.n_parts < 1 || r.n_parts > DSA_ROPE_PARTS || (o[4] != Py_True && o[4] != Py_False)) throw Refused();
+    Args a;
+    int64_t n_tok;
+    int32_t* pos = a.list(o[1], 1, &n_tok);
+    dsa_rope_rows rows[2][DSA_ROPE_PARTS];
+    for (int side = 0; side < 2; ++side) {
+      PyObject* s = o[2 + side];
+      if (!PyTuple_CheckExact(s) && !PyList_CheckExact(s)) throw Refused();
+      if (PySequence_Fast_GET_SIZE(s) != r.n_parts) throw Refused();
+      for (int i = 0; i < r.n_parts; ++i) rows[side][i] = a.rope_rows(PySequence_Fast_GET_ITEM(s, i), r.part[i], n_tok);
+    }
+    const int transposed = o[4] == Py_True;
+    dsa_stream_t st = a.stream();
+    return unlocked([&] { return lib.rope(&r, n_tok, pos, rows[0], rows[1], transposed, st); });
+  });
+}
+
+PyObject* sample(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  return answer(n, 10, [&] {
+    const dsa_sampler s = structure<dsa_sampler>(o[0], sampler_type);
+    Args a;
+    const void* x = a.exactly(o[1], s.dtype == DSA_BF16 ? at::kBFloat16 : at::kFloat, times(s.rows, s.ld));
+    float* u = static_cast<float*>(a.exactly(o[2], at::kFloat, s.rows));
+    float* temperature = a.exactly_or_none<float>(o[3], at::kFloat, s.requests);
+    int32_t* top_k = a.exactly_or_none<int32_t>(o[4], at::kInt, s.requests);
+    float* top_p = a.exactly_or_none<float>(o[5], at::kFloat, s.requests);
+    float* min_p = a.exactly_or_none<float>(o[6], at::kFloat, s.requests);
+    int32_t* index = a.exactly_or_none<int32_t>(o[7], at::kInt, s.rows);
+    int32_t* token = a.ints(o[8], s.rows);
+    float* prob = a.exactly_or_none<float>(o[9], at::kFloat, s.rows);
+    dsa_stream_t st = a.stream();
+    return unlocked([&] { return lib.sample(&s, x, u, temperature, top_k, top_p, min_p, index, token, prob, st); });
+  });
+}
+
+PyObject* tree_accept(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  return answer(n, 11, [&] {
+    const dsa_cache c = structure<dsa_cache>(o[0], cache_type);
+    const dsa_tree t = structure<dsa_tree>(o[1], tree_type);
+    Args a;
+    int32_t* start = a.ints(o[2], c.n_seqs + 1);
+    const uint64_t* mask = a.exactly_or_none<uint64_t>(o[3], at::kLong, times(t.n_tok, t.mask_words));
+    int32_t *drafted = a.ints(o[4], t.n_tok), *sampled = a.ints(o[5], t.n_tok), *n_new = a.ints(o[6], c.n_seqs);
+    int32_t *rows = a.ints(o[7], t.n_tok), *tokens = a.ints(o[8], t.n_tok), *next = a.ints(o[9], c.n_seqs);
+    if (!PyLong_CheckExact(o[10])) throw Refused();
+    const long long eos = PyLong_AsLongLong(o[10]);
+    if (eos == -1 && PyErr_Occurred()) {
+      PyErr_Clear();
+      throw Refused();
+    }
+    dsa_stream_t st = a.stream();
+    return unlocked([&] { return lib.accept(&c, &t, start, mask, drafted, sampled, eos, n_new, rows, tokens, next, st); });
+  });
+}
+
 // the library's functions (addresses, in Lib's order) and the ctypes structures
 PyObject* bind(PyObject*, PyObject* const* o, Py_ssize_t n) {
   void* f[sizeof(Lib) / sizeof(void*)];
   constexpr Py_ssize_t kFunctions = sizeof(f) / sizeof(f[0]);
-  if (n != kFunctions + 3) {
+  PyObject** types[] = {&cache_type, &tree_type, &beam_type, &rope_type, &sampler_type};
+  constexpr int kTypes = sizeof(types) / sizeof(types[0]);
+  if (n != kFunctions + kTypes) {
     PyErr_SetString(PyExc_TypeError, "bind: wrong number of arguments");
     return nullptr;
   }
@@ -273,8 +362,7 @@ PyObject* bind(PyObject*, PyObject* const* o, Py_ssize_t n) {
     }
   }
   memcpy(&lib, f, sizeof(lib));
-  PyObject** types[] = {&cache_type, &tree_type, &beam_type};
-  for (int i = 0; i < 3; ++i) Py_XSETREF(*types[i], Py_NewRef(o[kFunctions + i]));
+  for (int i = 0; i < kTypes; ++i) Py_XSETREF(*types[i], Py_NewRef(o[kFunctions + i]));
   Py_RETURN_NONE;
 }
 
@@ -282,7 +370,8 @@ PyObject* bind(PyObject*, PyObject* const* o, Py_ssize_t n) {
   { #name, (PyCFunction)(void*)name, METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {METHOD(bind),          METHOD(cache_fork),  METHOD(cache_extend),
                          METHOD(cache_compact), METHOD(cache_copy_pages), METHOD(cache_write),
-                         METHOD(tree_attn_fwd), METHOD(beam_select), {nullptr, nullptr, 0, nullptr}};
+                         METHOD(tree_attn_fwd), METHOD(beam_select),
+                         METHOD(rope_apply),    METHOD(sample),      METHOD(tree_accept), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

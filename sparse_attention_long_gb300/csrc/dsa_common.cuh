@@ -164,6 +164,8 @@ __device__ __forceinline__ void arrive_leader_shared(uint64_t* bar, uint32_t cra
   if (crank != 0) asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
   arrive_leader(bar, crank);
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
                    : "memory");

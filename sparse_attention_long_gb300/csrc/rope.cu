@@ -1,0 +1,311 @@
+// Rotary positions (dsa_rope_steps, dsa_rope_apply): the rotated columns of up to
+// four tensors of a layer in one launch, forwards and transposed.
+//
+// The angle of a pair is pos * f.  In fp32 that product has no bits of the turn's
+// fraction left at far positions, and a table of sines is one more thing to read.
+// Here f is a 64-bit fraction of a turn, and the product is taken modulo 2^64, that is
+// modulo a turn: exact at every position.  Its upper 32 bits (1.5e-9 radians) go through
+// sincospif.
+//
+// A thread holds the same pairs of several rows (a row: one head of one token), one
+// head after the other, and takes sine and cosine again only when the token changes.
+#include <math.h>
+
+#include "dsa_common.cuh"
+
+namespace dsa {
+namespace rope {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;                         // rows that a thread has in flight
+
+struct Part {
+  const uint8_t* x;
+  uint8_t* out;
+  long long x_tok, x_head, out_tok, out_head;      // strides in elements
+  int heads, offset, dim;
+  int rot_slots, slots;                            // threads of a row: rotating ones, and copying ones behind them
+  int kind;                                        // bit 0 fp32, bit 1 half layout, bit 2 sixteen bytes at a time
+  unsigned rows, rows_cta, first_cta;              // rows in all and of a CTA
+};
+struct Args {
+  Part part[DSA_ROPE_PARTS];
+  int n_parts, half;                               // pairs of a row
+  float mscale, sign;
+  uint64_t step[DSA_ROPE_MAX_DIM / 2];
+};
+
+__device__ __forceinline__ void turn(int pos, uint64_t step, float m, float sign, float& c, float& s) {
+  const uint64_t a = (uint64_t)(int64_t)pos * step;
+  sincospif((float)(int32_t)(uint32_t)(a >> 32) * 4.6566128730773926e-10f, &s, &c);  // 2^-31: half turns
+  c *= m;
+  s *= m * sign;
+}
+
+// P pairs of a row in 16-byte pieces (or one pair, element by element): a[], b[]
+template <typename T, bool HALF, int P>
+__device__ __forceinline__ void load_pairs(const T* p, int half, float (&a)[P], float (&b)[P]) {
+  if constexpr (P == 1) {
+    a[0] = to_f32(p[0]);
+    b[0] = to_f32(p[HALF ? half : 1]);
+  } else if constexpr (sizeof(T) == 4) {
+    const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + (HALF ? half : 4));
+    if constexpr (HALF) {
+      a[0] = u.x, a[1] = u.y, a[2] = u.z, a[3] = u.w, b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+    } else {
+      a[0] = u.x, b[0] = u.y, a[1] = u.z, b[1] = u.w, a[2] = v.x, b[2] = v.y, a[3] = v.z, b[3] = v.w;
+    }
+  } else {
+    const auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+    const auto hi = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
+    if constexpr (HALF) {
+      const uint2 u = *reinterpret_cast<const uint2*>(p), v = *reinterpret_cast<const uint2*>(p + half);
+      a[0] = lo(u.x), a[1] = hi(u.x), a[2] = lo(u.y), a[3] = hi(u.y);
+      b[0] = lo(v.x), b[1] = hi(v.x), b[2] = lo(v.y), b[3] = hi(v.y);
+    } else {
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      a[0] = lo(u.x), b[0] = hi(u.x), a[1] = lo(u.y), b[1] = hi(u.y);
+      a[2] = lo(u.z), b[2] = hi(u.z), a[3] = lo(u.w), b[3] = hi(u.w);
+    }
+  }
+}
+template <typename T, bool HALF, int P>
+__device__ __forceinline__ void store_pairs(T* p, int half, const float (&a)[P], const float (&b)[P]) {
+  if constexpr (P == 1) {
+    p[0] = from_f32<T>(a[0]);
+    p[HALF ? half : 1] = from_f32<T>(b[0]);
+  } else if constexpr (sizeof(T) == 4) {
+    float4* q = reinterpret_cast<float4*>(p);
+    if constexpr (HALF) {
+      q[0] = make_float4(a[0], a[1], a[2], a[3]);
+      *reinterpret_cast<float4*>(p + half) = make_float4(b[0], b[1], b[2], b[3]);
+    } else {
+      q[0] = make_float4(a[0], b[0], a[1], b[1]);
+      q[1] = make_float4(a[2], b[2], a[3], b[3]);
+    }
+  } else if constexpr (HALF) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+    *reinterpret_cast<uint2*>(p + half) = make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(a[0], b[0]), pack_bf16x2(a[1], b[1]),
+                                              pack_bf16x2(a[2], b[2]), pack_bf16x2(a[3], b[3]));
+  }
+}
+
+template <typename T, bool HALF, bool VEC>
+__device__ __forceinline__ void rotate_rows(const Args& g, const Part& p, const int32_t* __restrict__ pos, unsigned cta) {
+  constexpr int P = VEC ? 4 : 1, E = VEC ? 16 / (int)sizeof(T) : 1;  // pairs, or copied elements, per thread and row
+  using V = typename std::conditional<VEC, uint4, T>::type;
+  const int width = p.slots < kThreads ? p.slots : kThreads;         // threads of a row
+  const int rows_step = kThreads / width;
+  const int r0 = threadIdx.x / width, s0 = threadIdx.x - r0 * width;
+  if (r0 >= rows_step) return;
+  const unsigned begin = cta * p.rows_cta, end = min(begin + p.rows_cta, p.rows);
+  const T* x = (const T*)p.x;
+  T* out = (T*)p.out;
+  for (int slot = s0; slot < p.slots; slot += width) {
+    const bool rotates = slot < p.rot_slots;
+    uint64_t step[P];
+    int col;                                       // first column of this thread
+    if (rotates) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) step[i] = g.step[slot * P + i];
+      col = p.offset + slot * P * (HALF ? 1 : 2);
+    } else {
+      col = (slot - p.rot_slots) * E;
+      if (col >= p.offset) col += 2 * g.half;
+    }
+    int token = -1;
+    float c[P], s[P];
+    for (unsigned row = begin + r0; row < end; row += kUnroll * rows_step) {
+      unsigned t[kUnroll], h[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const unsigned r = row + k * rows_step;
+        t[k] = r / (unsigned)p.heads;
+        h[k] = r - t[k] * (unsigned)p.heads;
+      }
+      if (rotates) {
+        float a[kUnroll][P], b[kUnroll][P];
+        int at[kUnroll];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k)
+          if (row + k * rows_step < end) {
+            at[k] = pos[t[k]];
+            load_pairs<T, HALF, P>(x + t[k] * p.x_tok + h[k] * p.x_head + col, g.half, a[k], b[k]);
+          }
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k)
+          if (row + k * rows_step < end) {
+            if ((int)t[k] != token) {
+              token = (int)t[k];
+#pragma unroll
+              for (int i = 0; i < P; ++i) turn(at[k], step[i], g.mscale, g.sign, c[i], s[i]);
+            }
+            float u[P], v[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+              u[i] = a[k][i] * c[i] - b[k][i] * s[i];
+              v[i] = a[k][i] * s[i] + b[k][i] * c[i];
+            }
+            store_pairs<T, HALF, P>(out + t[k] * p.out_tok + h[k] * p.out_head + col, g.half, u, v);
+          }
+      } else {
+        V w[kUnroll];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k)
+          if (row + k * rows_step < end)
+            w[k] = *reinterpret_cast<const V*>(x + t[k] * p.x_tok + h[k] * p.x_head + col);
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k)
+          if (row + k * rows_step < end)
+            *reinterpret_cast<V*>(out + t[k] * p.out_tok + h[k] * p.out_head + col) = w[k];
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ Args g, const int32_t* __restrict__ pos) {
+  let_next_launch();
+  wait_for_earlier();
+  int i = 0;
+  while (i + 1 < g.n_parts && blockIdx.x >= g.part[i + 1].first_cta) ++i;
+  const Part& p = g.part[i];
+  const unsigned cta = blockIdx.x - p.first_cta;
+  switch (p.kind) {
+    case 0: return rotate_rows<__nv_bfloat16, false, false>(g, p, pos, cta);
+    case 1: return rotate_rows<float, false, false>(g, p, pos, cta);
+    case 2: return rotate_rows<__nv_bfloat16, true, false>(g, p, pos, cta);
+    case 3: return rotate_rows<float, true, false>(g, p, pos, cta);
+    case 4: return rotate_rows<__nv_bfloat16, false, true>(g, p, pos, cta);
+    case 5: return rotate_rows<float, false, true>(g, p, pos, cta);
+    case 6: return rotate_rows<__nv_bfloat16, true, true>(g, p, pos, cta);
+    default: return rotate_rows<float, true, true>(g, p, pos, cta);
+  }
+}
+
+// --------------------------------- host side ---------------------------------
+// Elements from the first to behind the last one of a tensor's rows; false: they run
+// into each other (apart: they must not) or out of 2^62.
+static bool span(const dsa_rope_rows& r, long long n_tok, long long heads, long long dim, bool apart, long long* n) {
+  const long long limit = 1ll << 40;
+  if (r.tok_stride < 0 || r.head_stride < 0 || r.tok_stride > limit || r.head_stride > limit) return false;
+  long long s0 = heads > 1 ? r.head_stride : 0, n0 = heads, s1 = n_tok > 1 ? r.tok_stride : 0, n1 = n_tok;
+  if (n0 == 1 || (n1 > 1 && s0 > s1)) {
+    const long long s = s0, k = n0;
+    s0 = s1, n0 = n1, s1 = s, n1 = k;
+  }
+  if (apart && n0 > 1 && s0 < dim) return false;
+  const __int128 inner = (__int128)(n0 - 1) * s0 + dim;
+  if (apart && n1 > 1 && s1 < inner) return false;
+  const __int128 all = inner + (__int128)(n1 - 1) * s1;
+  if (all > ((__int128)1 << 58)) return false;
+  *n = (long long)all;
+  return true;
+}
+
+static int check(const dsa_rope* p) {
+  if (!p) return DSA_ERR_INVALID_ARG;
+  if (p->rot_dim < 2 || (p->rot_dim & 1) || p->n_parts < 1 || p->n_parts > DSA_ROPE_PARTS || !isfinite(p->mscale))
+    return DSA_ERR_INVALID_ARG;
+  if (p->rot_dim > DSA_ROPE_MAX_DIM) return DSA_ERR_UNSUPPORTED;
+  for (int i = 0; i < p->n_parts; ++i) {
+    const dsa_rope_part& q = p->part[i];
+    if (q.dtype != DSA_BF16 && q.dtype != DSA_FP32) return DSA_ERR_UNSUPPORTED;
+    if (q.layout != DSA_ROPE_INTERLEAVED && q.layout != DSA_ROPE_HALF) return DSA_ERR_INVALID_ARG;
+    if (q.heads < 1 || q.dim < p->rot_dim || q.offset < 0 || q.offset > q.dim - p->rot_dim) return DSA_ERR_INVALID_ARG;
+    if (q.dim > (1 << 20)) return DSA_ERR_UNSUPPORTED;
+  }
+  return DSA_OK;
+}
+
+}  // namespace rope
+}  // namespace dsa
+
+using namespace dsa;
+using namespace dsa::rope;
+
+extern "C" {
+
+int dsa_rope_steps(dsa_rope* p, double base, int scaling, double factor, double original, double beta_fast,
+                   double beta_slow) {
+  if (!p || p->rot_dim < 2 || (p->rot_dim & 1)) return DSA_ERR_INVALID_ARG;
+  if (p->rot_dim > DSA_ROPE_MAX_DIM) return DSA_ERR_UNSUPPORTED;
+  if (scaling < DSA_ROPE_PLAIN || scaling > DSA_ROPE_YARN) return DSA_ERR_UNSUPPORTED;
+  if (!(base > 1.0) || !isfinite(base)) return DSA_ERR_INVALID_ARG;
+  if (scaling != DSA_ROPE_PLAIN && (!(factor >= 1.0) || !isfinite(factor))) return DSA_ERR_INVALID_ARG;
+  const double r = p->rot_dim, two_pi = 6.283185307179586;
+  double low = 0, high = 0;
+  if (scaling == DSA_ROPE_YARN) {
+    if (!(original > 0) || !isfinite(original) || !(beta_slow > 0) || !(beta_fast >= beta_slow) || !isfinite(beta_fast))
+      return DSA_ERR_INVALID_ARG;
+    // the pair that turns so many times in `original` positions
+    const auto pair = [&](double turns) { return r * log(original / (turns * two_pi)) / (2 * log(base)); };
+    low = fmax(floor(pair(beta_fast)), 0.0);
+    high = fmin(ceil(pair(beta_slow)), r - 1);
+  }
+  if (scaling == DSA_ROPE_NTK && p->rot_dim > 2) base *= pow(factor, r / (r - 2));
+  if (!isfinite(base)) return DSA_ERR_INVALID_ARG;
+  for (int i = 0; i < p->rot_dim / 2; ++i) {
+    double f = pow(base, -2.0 * i / r);
+    if (scaling == DSA_ROPE_LINEAR) f /= factor;
+    if (scaling == DSA_ROPE_YARN) {
+      const double g = fmin(fmax((i - low) / fmax(high - low, 0.001), 0.0), 1.0);
+      f = f * (1 - g) + f / factor * g;
+    }
+    p->step[i] = (uint64_t)(f / two_pi * 18446744073709551616.0);  // f <= 1: below 2^62
+  }
+  return DSA_OK;
+}
+
+int dsa_rope_apply(const dsa_rope* p, int64_t n_tok, const int32_t* pos, const dsa_rope_rows* x,
+                   const dsa_rope_rows* out, int transposed, dsa_stream_t stream) {
+  int rc = check(p);
+  if (rc) return rc;
+  if (n_tok < 1 || !pos || ((uintptr_t)pos & 3u) || !x || !out) return DSA_ERR_INVALID_ARG;
+  Args g = {};
+  g.n_parts = p->n_parts;
+  g.half = p->rot_dim / 2;
+  g.mscale = p->mscale;
+  g.sign = transposed ? -1.f : 1.f;
+  for (int i = 0; i < g.half; ++i) g.step[i] = p->step[i];
+  long long ctas = 0;
+  for (int i = 0; i < p->n_parts; ++i) {
+    const dsa_rope_part& q = p->part[i];
+    Part& t = g.part[i];
+    const uintptr_t esz = q.dtype == DSA_BF16 ? 2 : 4;
+    if (!x[i].base || !out[i].base || ((uintptr_t)x[i].base & (esz - 1)) || ((uintptr_t)out[i].base & (esz - 1)))
+      return DSA_ERR_INVALID_ARG;
+    if (q.heads >= (1ll << 31) || n_tok >= (1ll << 31) || q.heads * n_tok >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
+    long long nx, no;
+    if (!span(x[i], n_tok, q.heads, q.dim, false, &nx) || !span(out[i], n_tok, q.heads, q.dim, true, &no))
+      return DSA_ERR_INVALID_ARG;
+    const bool in_place = x[i].base == out[i].base && (n_tok == 1 || x[i].tok_stride == out[i].tok_stride) &&
+                          (q.heads == 1 || x[i].head_stride == out[i].head_stride);
+    const uintptr_t bx = (uintptr_t)x[i].base, bo = (uintptr_t)out[i].base;
+    if (!in_place && bx < bo + no * esz && bo < bx + nx * esz) return DSA_ERR_INVALID_ARG;
+    t.x = (const uint8_t*)x[i].base;
+    t.out = (uint8_t*)out[i].base;
+    t.x_tok = x[i].tok_stride, t.x_head = x[i].head_stride, t.out_tok = out[i].tok_stride, t.out_head = out[i].head_stride;
+    t.heads = (int)q.heads, t.offset = (int)q.offset, t.dim = (int)q.dim;
+    const int rest = in_place ? 0 : (int)q.dim - p->rot_dim, e = 16 / (int)esz;
+    // sixteen bytes at a time where rows, columns and the pairs of a thread allow it
+    const uintptr_t at = bx | bo | (uintptr_t)((n_tok > 1 ? x[i].tok_stride | out[i].tok_stride : 0) * esz) |
+                         (uintptr_t)((q.heads > 1 ? x[i].head_stride | out[i].head_stride : 0) * esz);
+    const bool vec = (at & 15) == 0 && p->rot_dim % 8 == 0 && q.offset % e == 0 && rest % e == 0;
+    t.kind = (q.dtype == DSA_FP32) | (q.layout == DSA_ROPE_HALF) << 1 | vec << 2;
+    t.rot_slots = vec ? g.half / 4 : g.half;
+    t.slots = t.rot_slots + (vec ? rest / e : rest);
+    const int width = t.slots < kThreads ? t.slots : kThreads, rows_step = kThreads / width;
+    t.rows = (unsigned)(q.heads * n_tok);
+    t.rows_cta = (unsigned)(rows_step * kUnroll);
+    t.first_cta = (unsigned)ctas;
+    ctas += (t.rows + t.rows_cta - 1) / t.rows_cta;
+  }
+  if (ctas >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
+  return launch_programmatic(rope_kernel, dim3((unsigned)ctas), dim3(kThreads), 0, (cudaStream_t)stream, 1, g, pos)
+             ? DSA_OK
+             : DSA_ERR_CUDA;
+}
+
+}  // extern "C"

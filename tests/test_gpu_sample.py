@@ -1,0 +1,288 @@
+"""Sampling on the GPU against the fp64 definition.
+
+Tokens must be equal.  A weight is off by 2^-30 of itself and one unit of 2^-44 of the
+largest, so a part of the mass is off by less than 2^-29 + vocab 2^-44 times the largest
+token's part of the mass; the inputs keep every draw and every border of top-p further than
+that from a sum of weights (checked), or make all of them whole numbers of units.  A probability is off by 2^-28 and its rounding, 2^-24, relative.
+"""
+import math
+import random
+
+import pytest
+import torch
+
+from gpu_util import DEV, lib
+from oracle.sample import kept_tokens, sample
+
+pytestmark = pytest.mark.gpu
+INF = math.inf
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def dev(x, dtype=F32):
+    return None if x is None else torch.tensor(x, dtype=dtype, device=DEV)
+
+
+def run(dsa, logits, u, temperature=None, top_k=None, top_p=None, min_p=None, index=None, ld=None, dtype=F32, offset=0,
+        stream=None):
+    """logits [rows, V] (any float tensor) -> tokens, probabilities."""
+    n, V = logits.shape
+    ld = ld or V
+    store = torch.full((n * ld + offset,), INF, dtype=dtype, device=DEV)    # what lies between the rows is not read
+    x = store[offset:].view(n, ld)
+    x[:, :V] = logits.to(dtype)
+    settings = [temperature, top_k, top_p, min_p]
+    m = next((len(t) for t in settings if t is not None), n)
+    s = dsa.make_sampler(rows=n, vocab=V, ld=ld, dtype="bf16" if dtype == BF16 else "fp32", requests=m)
+    token = torch.full((n,), 77, dtype=torch.int32, device=DEV)
+    prob = torch.full((n,), math.nan, device=DEV)
+    dsa.sample(s, x, dev(u), dev(temperature), dev(top_k, torch.int32), dev(top_p), dev(min_p), dev(index, torch.int32),
+               token, prob, stream=stream)
+    torch.cuda.synchronize()
+    return token.tolist(), prob.tolist()
+
+
+def check(dsa, logits, u, temperature=None, top_k=None, top_p=None, min_p=None, index=None, dtype=F32, exact=False, **kw):
+    tokens, probs = run(dsa, logits, u, temperature, top_k, top_p, min_p, index, dtype=dtype, **kw)
+    assert dsa.get_status() == 0
+    x = logits.to(dtype).double().numpy()
+    f32 = lambda t, i, default: default if t is None else float(torch.tensor(t[i], dtype=F32))
+    for r in range(x.shape[0]):
+        q = r if index is None else index[r]
+        cuts = f32(temperature, q, 1.0), 0 if top_k is None else top_k[q], f32(top_p, q, 1.0), f32(min_p, q, 0.0)
+        want, p, margin = sample(x[r], f32(u, r, 0), *cuts)
+        largest = 1 / max(1.0, float(kept_tokens(x[r], *cuts)[1].sum()))
+        assert exact or margin > 2.0 ** -29 + x.shape[1] * 2.0 ** -44 * largest
+        assert tokens[r] == want, (r, tokens[r], want, margin)
+        assert abs(probs[r] - p) <= p * 2.0 ** -23
+
+
+def rand(*shape, seed=0, scale=2.5):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed), dtype=torch.float64) * scale
+
+
+def uniform(n, seed=0):
+    return torch.rand(n, generator=torch.Generator().manual_seed(seed)).tolist()
+
+
+SETTINGS = [dict(), dict(temperature=[0.0]), dict(temperature=[0.7]), dict(temperature=[3.0], top_k=[1]),
+            dict(top_k=[7]), dict(top_k=[50], top_p=[0.9]), dict(top_k=[3000]), dict(top_p=[0.95]), dict(top_p=[0.3]),
+            dict(temperature=[1.3], min_p=[0.05]), dict(temperature=[0.9], top_k=[40], top_p=[0.8], min_p=[0.02]),
+            dict(top_p=[0.999], min_p=[1e-4])]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V,ld,offset", [(1, None, 0), (2, None, 0), (5, 7, 1), (100, None, 0), (1000, 1008, 0), (4099, None, 3),
+                                         (8192, None, 0), (32001, 32008, 0), (70001, None, 0), (131071, 131072, 0)])
+def test_settings_and_sizes(V, ld, offset, dtype):
+    dsa = lib()
+    rows = 4 if V < 50000 else 2
+    x = rand(rows, V, seed=V)
+    for i, s in enumerate(SETTINGS):
+        kw = {k: v * rows for k, v in s.items()}
+        check(dsa, x, uniform(rows, seed=1000 * i + V), ld=ld, dtype=dtype, offset=offset, **kw)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("spread", [0.01, 1.0, 8.0])
+def test_rows_of_many_requests(spread, dtype):
+    dsa = lib()
+    n, m, V = 120, 7, 5003
+    rng = random.Random(int(100 * spread))
+    check(dsa, rand(n, V, seed=3, scale=spread), uniform(n, seed=9), index=[rng.randrange(m) for _ in range(n)], dtype=dtype,
+          temperature=[0.0, 0.5, 0.8, 1.0, 1.2, 0.3, 2.0], top_k=[0, 0, 1, 30, 500, 5003, 6000],
+          top_p=[1.0, 0.9, 1.0, 0.5, 0.99, 0.7, 0.01], min_p=[0.0, 0.1, 0.0, 0.0, 0.001, 1.0, 0.0])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_ties(dtype):
+    """Equal logits: weights are whole, every border is exact; those kept are the lowest."""
+    dsa = lib()
+    V = 1 << 15
+    x = torch.zeros(6, V, dtype=torch.float64)
+    u = [0.0, 0.25, 0.5, 1 - 2.0 ** -15, 1 - 2.0 ** -24, 2.0 ** -15]
+    check(dsa, x, u, dtype=dtype, exact=True)
+    check(dsa, x, u, dtype=dtype, exact=True, top_k=[1, 3, 4, 1000, 20000, 32767])
+    check(dsa, x, u, dtype=dtype, exact=True, top_p=[2.0 ** -15, 0.25, 0.5, 2.0 ** -10, 0.75, 1.0])
+    check(dsa, x, u, dtype=dtype, exact=True, top_k=[4, 8, 16, 1024, 16384, 2], top_p=[0.5, 0.25, 0.75, 1.0, 0.5, 0.5])
+    check(dsa, x, u, dtype=dtype, exact=True, min_p=[1.0] * 6, temperature=[0.0, 1.0, 2.0, 3.0, 0.1, 1e-3])
+    check(dsa, (rand(8, 30000, seed=2).round() * 0.5), uniform(8, seed=5), dtype=dtype, top_k=[1, 2, 20, 300, 4000, 0, 0, 9],
+          top_p=[1.0, 1.0, 0.9, 0.8, 0.7, 0.6, 0.5, 0.4])          # many equal logits
+    signed = torch.zeros(1, 300, dtype=torch.float64)
+    signed[:, ::2] = -0.0                                          # -0 and +0 are one value
+    check(dsa, signed, [0.55], dtype=dtype, top_k=[256], exact=True)
+    check(dsa, torch.cat([signed, torch.tensor([[-1.0, -2.0]])], 1), [0.55], dtype=dtype, top_p=[0.5])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_masked_and_unusable_logits(dtype):
+    dsa = lib()
+    x = rand(6, 9000, seed=4)
+    x[0, 10:] = -INF                         # fewer logits than top_k
+    x[1] = -INF                              # none
+    x[2, 5], x[2, 6], x[2, 8999] = INF, math.nan, -INF
+    x[3] = torch.finfo(dtype).min            # the type's lowest value is a logit like any other
+    x[4, ::2] = math.nan
+    x[5, :8500] = INF
+    u = uniform(6, seed=2)
+    for kw in (dict(), dict(top_k=[50] * 6), dict(top_p=[0.9] * 6), dict(min_p=[0.1] * 6), dict(temperature=[0.0] * 6)):
+        check(dsa, x, u, dtype=dtype, **kw)
+    assert run(dsa, x[1:2], [0.5], dtype=dtype) == ([-1], [0.0])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("fill", [-1e4, -1e9, -1e30, -3e38, 5e9, 1e30])
+def test_finite_logits_of_any_size(fill, dtype):
+    dsa = lib()
+    V = 9000
+    x = rand(4, V, seed=7)
+    x[0] = fill
+    x[1, :8500] = fill
+    x[2, ::3] = fill
+    x[3, 100:] = fill
+    u = [0.50317, 0.30023, 0.70041, 0.12343]
+    for kw in (dict(), dict(top_k=[40] * 4, top_p=[0.91] * 4), dict(top_p=[0.81234] * 4), dict(temperature=[1e7, 0.5, 2.0, 1.0])):
+        check(dsa, x, u, dtype=dtype, **kw)
+
+
+@pytest.mark.parametrize("T", [1e-30, 1e-6, 0.01, 100.0, 1e6, 1e30])
+def test_extreme_temperatures(T):
+    dsa = lib()
+    x = rand(3, 5000, seed=11, scale=4.0)
+    check(dsa, x, [0.20031, 0.50071, 0.90013], temperature=[T] * 3)
+    check(dsa, x, [0.20031, 0.50071, 0.90013], temperature=[T] * 3, top_p=[0.9131] * 3, top_k=[101] * 3)
+
+
+def test_a_large_spread_of_small_differences():
+    """Logits of some 1e5 apart by a few units of their last place (2^-7): the difference comes first."""
+    dsa = lib()
+    g = torch.Generator().manual_seed(3)
+    x = 1e5 - 2.0 ** -7 * torch.randint(0, 400, (3, 5000), generator=g).double()
+    check(dsa, x, [0.1, 0.6, 0.95])
+    check(dsa, x, [0.1, 0.6, 0.95], top_p=[0.5] * 3, temperature=[0.7] * 3)
+
+
+def test_every_cdf_step_of_a_small_row():
+    """u in the middle of each token's part of the mass, and a hair below its end."""
+    dsa = lib()
+    V = 257
+    x = rand(1, V, seed=21)
+    w = torch.exp(x[0].float().double() - x.max())
+    c = torch.cumsum(w, 0) / w.sum()
+    mid = (c - 0.5 * w / w.sum()).float().tolist()
+    assert run(dsa, x.expand(V, V), mid)[0] == list(range(V))
+    end = (c - 2.0 ** -22).float().tolist()
+    assert run(dsa, x.expand(V, V), end)[0] == list(range(V))
+
+
+def test_frequencies_follow_the_distribution():
+    """4,096 evenly spaced draws: a token's count is its part of the mass, to one at either end."""
+    dsa = lib()
+    n, V = 4096, 40
+    x = rand(1, V, seed=22, scale=1.0)
+    u = [(i + 0.5) / n for i in range(n)]
+    tokens, _ = run(dsa, x.expand(n, V), u, temperature=[0.8] * n, top_p=[0.9] * n)
+    kept, w, _ = kept_tokens(x[0].float().double().numpy(), float(torch.tensor(0.8)), 0, float(torch.tensor(0.9)))
+    count = torch.bincount(torch.tensor(tokens), minlength=V)
+    assert int(count.sum()) == int(count[kept.tolist()].sum()) == n
+    for t, part in zip(kept.tolist(), w / w.sum()):
+        assert abs(int(count[t]) - n * part) <= 1 + n * 2.0 ** -23
+
+
+def test_settings_out_of_range():
+    dsa = lib()
+    x = rand(8, 100, seed=1)
+    u = [0.5] * 8
+    bad = [-1, 0.0]
+    good, _ = run(dsa, x, u)
+    for kw in (dict(temperature=[1, -0.5, math.nan, INF, 1, 1, 1, 1]), dict(top_k=[0, -1, -5, -2 ** 31, 0, 0, 0, 0]),
+               dict(top_p=[1, 0, 1.5, math.nan, 1, 1, 1, 1]), dict(min_p=[0, -0.1, 1.1, math.nan, 0, 0, 0, 0])):
+        t, p = run(dsa, x, u, **kw)
+        assert dsa.get_status() == dsa.DSA_ERR_INDEX
+        assert t == [good[0], -1, -1, -1] + good[4:] and p[1:4] == [0.0] * 3
+    t, _ = run(dsa, x, [0.5, 1.0, -0.1, math.nan] + u[4:])
+    assert dsa.get_status() == dsa.DSA_ERR_INDEX and t == [good[0], -1, -1, -1] + good[4:]
+    t, _ = run(dsa, x, u, temperature=[1.0] * 3, index=[0, 3, -1, 2 ** 31 - 1, 0, 1, 2, 0])
+    assert dsa.get_status() == dsa.DSA_ERR_INDEX and t == [good[0], -1, -1, -1] + good[4:]
+    # a greedy row uses neither u nor the other settings
+    t, p = run(dsa, x, [math.nan] * 8, temperature=[0.0] * 8, top_p=[-1.0] * 8, top_k=[-1] * 8, min_p=[2.0] * 8)
+    assert dsa.get_status() == 0 and t == x.float().argmax(1).tolist() and p == [1.0] * 8
+
+
+def test_a_row_gives_the_same_bits_wherever_it_lies():
+    dsa = lib()
+    x = rand(1, 7003, seed=5)
+    for dtype in (F32, BF16):
+        seen = set()
+        for ld, offset in ((None, 0), (7008, 0), (7004, 1), (7003, 5), (9001, 2)):
+            t, p = run(dsa, x.expand(3, 7003), [0.37] * 3, temperature=[0.9] * 3, top_p=[0.93] * 3, ld=ld, offset=offset,
+                       dtype=dtype)
+            seen |= set(zip(t, p))
+        assert len(seen) == 1
+
+
+def test_graph_replay_on_new_logits_and_other_stream():
+    dsa = lib()
+    n, V = 5, 9001
+    s = dsa.make_sampler(rows=n, vocab=V, dtype="fp32")
+    x, u, k = torch.zeros(n, V, device=DEV), torch.zeros(n, device=DEV), torch.zeros(n, dtype=torch.int32, device=DEV)
+    T, p, token = torch.ones(n, device=DEV), torch.ones(n, device=DEV), torch.zeros(n, dtype=torch.int32, device=DEV)
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=side):
+        dsa.sample(s, x, u, T, k, p, None, None, token)
+    for seed in range(3):
+        y, r = rand(n, V, seed=seed), uniform(n, seed)
+        ks, ps, ts = [0, 5, 100, 0, 2000], [0.9, 1.0, 0.8, 0.7, 0.95], [0.0, 1.0, 0.8, 1.2, 0.6]
+        for t, v in ((x, y), (u, torch.tensor(r)), (k, torch.tensor(ks)), (p, torch.tensor(ps)), (T, torch.tensor(ts))):
+            t.copy_(v)
+        g.replay()
+        torch.cuda.synchronize()
+        f = lambda v: float(torch.tensor(v, dtype=F32))
+        want = [sample(y[i].float().double().numpy(), f(r[i]), f(ts[i]), ks[i], f(ps[i]))[0] for i in range(n)]
+        assert token.tolist() == want
+    assert run(dsa, y, r, ts, ks, ps, stream=side)[0] == want
+
+
+def test_rows_past_four_gigabytes():
+    dsa = lib()
+    n, V, ld = 4, 1000, 800_000_000
+    x = torch.zeros(n * ld, dtype=BF16, device=DEV).view(n, ld)
+    y = rand(n, V, seed=1).to(BF16)
+    x[:, :V] = y.to(DEV)
+    token = torch.zeros(n, dtype=torch.int32, device=DEV)
+    dsa.sample(dsa.make_sampler(rows=n, vocab=V, ld=ld), x, dev([0.3] * n), None, None, None, None, None, token)
+    assert token.tolist() == [sample(y[i].double().numpy(), float(torch.tensor(0.3)))[0] for i in range(n)]
+
+
+def test_largest_vocabulary_and_many_rows():
+    dsa = lib()
+    x = rand(1, 1 << 18, seed=31)
+    for dtype in (F32, BF16):
+        for i, kw in enumerate((dict(), dict(top_k=[60]), dict(top_p=[0.9]), dict(top_k=[100000], top_p=[0.95]))):
+            check(dsa, x, [0.1 + 0.2 * i], dtype=dtype, **kw)
+    n = 20000
+    y = rand(1, 11, seed=32)
+    u = torch.arange(n, dtype=F32) / n
+    w = torch.exp(y[0].float().double() - y.float().max())
+    want = torch.searchsorted(torch.cumsum(w, 0) / w.sum(), u.double(), right=True)
+    assert run(dsa, y.expand(n, 11), u.tolist())[0] == want.tolist()
+
+
+def test_refused_tensors():
+    dsa = lib()
+    n, V = 2, 8
+    mk = lambda **kw: dsa.make_sampler(**dict(dict(rows=n, vocab=V, dtype="fp32"), **kw))
+    x, u, token = torch.zeros(n, V, device=DEV), torch.zeros(n, device=DEV), torch.zeros(n, dtype=torch.int32, device=DEV)
+    ok = dict(logits=x, u=u, temperature=None, top_k=None, top_p=None, min_p=None, index=None, token=token, prob=None)
+    dsa.sample(mk(), **ok)
+    for e, kw in ((TypeError, dict(logits=x.to(BF16))), (ValueError, dict(logits=x[:, :7])), (ValueError, dict(u=u[:1])),
+                  (TypeError, dict(u=u.double())), (TypeError, dict(top_k=u)), (ValueError, dict(top_p=torch.ones(3, device=DEV))),
+                  (ValueError, dict(min_p=u.cpu())), (TypeError, dict(index=u)), (TypeError, dict(token=token.long())),
+                  (TypeError, dict(prob=token)), (TypeError, dict(token=None))):
+        with pytest.raises(e):
+            dsa.sample(mk(), **dict(ok, **kw))
+    for s, kw in ((mk(requests=1), {}), (mk(), dict(prob=u)), (mk(), dict(index=token))):
+        with pytest.raises(dsa.DSAError) as e:
+            dsa.sample(s, **dict(ok, **kw))
+        assert e.value.code == dsa.DSA_ERR_INVALID_ARG
+    assert dsa.get_status() == 0
