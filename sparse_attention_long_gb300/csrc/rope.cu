@@ -7,8 +7,9 @@
 // modulo a turn: exact at every position.  Its upper 32 bits (1.5e-9 radians) go through
 // sincospif.
 //
-// A thread holds the same pairs of several rows (a row: one head of one token), one
-// head after the other, and takes sine and cosine again only when the token changes.
+// A CTA takes consecutive rows (a row: one head of one token), its threads the same pairs
+// of several of them; sines and cosines of its tokens are computed once, into shared
+// memory, while the first rows are on their way.
 #include <math.h>
 
 #include "dsa_common.cuh"
@@ -17,7 +18,7 @@ namespace dsa {
 namespace rope {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;                         // rows that a thread has in flight
+constexpr int kTable = 2048;                       // pairs whose sine and cosine a CTA holds at once
 
 struct Part {
   const uint8_t* x;
@@ -42,130 +43,179 @@ __device__ __forceinline__ void turn(int pos, uint64_t step, float m, float sign
   s *= m * sign;
 }
 
-// P pairs of a row in 16-byte pieces (or one pair, element by element): a[], b[]
-template <typename T, bool HALF, int P>
-__device__ __forceinline__ void load_pairs(const T* p, int half, float (&a)[P], float (&b)[P]) {
-  if constexpr (P == 1) {
-    a[0] = to_f32(p[0]);
-    b[0] = to_f32(p[HALF ? half : 1]);
-  } else if constexpr (sizeof(T) == 4) {
-    const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + (HALF ? half : 4));
+// What a thread holds of a row, as it lies in memory: P pairs (or, of the columns that are
+// copied, E elements).
+template <typename T, bool HALF, bool VEC>
+struct Piece;
+template <typename T, bool HALF>
+struct Piece<T, HALF, false> {
+  static constexpr int P = 1, E = 1;
+  T u, v;
+  __device__ __forceinline__ void load(const T* p, int half) { u = p[0], v = p[HALF ? half : 1]; }
+  __device__ __forceinline__ void store(T* p, int half) const { p[0] = u, p[HALF ? half : 1] = v; }
+  __device__ __forceinline__ void load_copy(const T* p) { u = *p; }
+  __device__ __forceinline__ void store_copy(T* p) const { *p = u; }
+  __device__ __forceinline__ void get(float (&a)[1], float (&b)[1]) const { a[0] = to_f32(u), b[0] = to_f32(v); }
+  __device__ __forceinline__ void set(const float (&a)[1], const float (&b)[1]) {
+    u = from_f32<T>(a[0]), v = from_f32<T>(b[0]);
+  }
+};
+template <bool HALF>
+struct Piece<float, HALF, true> {
+  static constexpr int P = 4, E = 4;
+  float4 u, v;
+  __device__ __forceinline__ void load(const float* p, int half) {
+    u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + (HALF ? half : 4));
+  }
+  __device__ __forceinline__ void store(float* p, int half) const {
+    *reinterpret_cast<float4*>(p) = u, *reinterpret_cast<float4*>(p + (HALF ? half : 4)) = v;
+  }
+  __device__ __forceinline__ void load_copy(const float* p) { u = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void store_copy(float* p) const { *reinterpret_cast<float4*>(p) = u; }
+  __device__ __forceinline__ void get(float (&a)[4], float (&b)[4]) const {
     if constexpr (HALF) {
       a[0] = u.x, a[1] = u.y, a[2] = u.z, a[3] = u.w, b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
     } else {
       a[0] = u.x, b[0] = u.y, a[1] = u.z, b[1] = u.w, a[2] = v.x, b[2] = v.y, a[3] = v.z, b[3] = v.w;
     }
-  } else {
-    const auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
-    const auto hi = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
+  }
+  __device__ __forceinline__ void set(const float (&a)[4], const float (&b)[4]) {
     if constexpr (HALF) {
-      const uint2 u = *reinterpret_cast<const uint2*>(p), v = *reinterpret_cast<const uint2*>(p + half);
+      u = make_float4(a[0], a[1], a[2], a[3]), v = make_float4(b[0], b[1], b[2], b[3]);
+    } else {
+      u = make_float4(a[0], b[0], a[1], b[1]), v = make_float4(a[2], b[2], a[3], b[3]);
+    }
+  }
+};
+template <bool HALF>
+struct Piece<__nv_bfloat16, HALF, true> {
+  static constexpr int P = 4, E = 8;
+  uint2 u, v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int half) {
+    if constexpr (HALF) u = *reinterpret_cast<const uint2*>(p), v = *reinterpret_cast<const uint2*>(p + half);
+    else load_copy(p);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p, int half) const {
+    if constexpr (HALF) *reinterpret_cast<uint2*>(p) = u, *reinterpret_cast<uint2*>(p + half) = v;
+    else store_copy(p);
+  }
+  __device__ __forceinline__ void load_copy(const __nv_bfloat16* p) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    u = make_uint2(w.x, w.y), v = make_uint2(w.z, w.w);
+  }
+  __device__ __forceinline__ void store_copy(__nv_bfloat16* p) const {
+    *reinterpret_cast<uint4*>(p) = make_uint4(u.x, u.y, v.x, v.y);
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+  static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+  __device__ __forceinline__ void get(float (&a)[4], float (&b)[4]) const {
+    if constexpr (HALF) {
       a[0] = lo(u.x), a[1] = hi(u.x), a[2] = lo(u.y), a[3] = hi(u.y);
       b[0] = lo(v.x), b[1] = hi(v.x), b[2] = lo(v.y), b[3] = hi(v.y);
     } else {
-      const uint4 u = *reinterpret_cast<const uint4*>(p);
       a[0] = lo(u.x), b[0] = hi(u.x), a[1] = lo(u.y), b[1] = hi(u.y);
-      a[2] = lo(u.z), b[2] = hi(u.z), a[3] = lo(u.w), b[3] = hi(u.w);
+      a[2] = lo(v.x), b[2] = hi(v.x), a[3] = lo(v.y), b[3] = hi(v.y);
     }
   }
-}
-template <typename T, bool HALF, int P>
-__device__ __forceinline__ void store_pairs(T* p, int half, const float (&a)[P], const float (&b)[P]) {
-  if constexpr (P == 1) {
-    p[0] = from_f32<T>(a[0]);
-    p[HALF ? half : 1] = from_f32<T>(b[0]);
-  } else if constexpr (sizeof(T) == 4) {
-    float4* q = reinterpret_cast<float4*>(p);
+  __device__ __forceinline__ void set(const float (&a)[4], const float (&b)[4]) {
     if constexpr (HALF) {
-      q[0] = make_float4(a[0], a[1], a[2], a[3]);
-      *reinterpret_cast<float4*>(p + half) = make_float4(b[0], b[1], b[2], b[3]);
+      u = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+      v = make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
     } else {
-      q[0] = make_float4(a[0], b[0], a[1], b[1]);
-      q[1] = make_float4(a[2], b[2], a[3], b[3]);
+      u = make_uint2(pack_bf16x2(a[0], b[0]), pack_bf16x2(a[1], b[1]));
+      v = make_uint2(pack_bf16x2(a[2], b[2]), pack_bf16x2(a[3], b[3]));
     }
-  } else if constexpr (HALF) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
-    *reinterpret_cast<uint2*>(p + half) = make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
-  } else {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(a[0], b[0]), pack_bf16x2(a[1], b[1]),
-                                              pack_bf16x2(a[2], b[2]), pack_bf16x2(a[3], b[3]));
   }
-}
+};
 
 template <typename T, bool HALF, bool VEC>
-__device__ __forceinline__ void rotate_rows(const Args& g, const Part& p, const int32_t* __restrict__ pos, unsigned cta) {
-  constexpr int P = VEC ? 4 : 1, E = VEC ? 16 / (int)sizeof(T) : 1;  // pairs, or copied elements, per thread and row
-  using V = typename std::conditional<VEC, uint4, T>::type;
-  const int width = p.slots < kThreads ? p.slots : kThreads;         // threads of a row
+__device__ __forceinline__ void rotate_rows(const Args& g, const Part& p, const int32_t* __restrict__ pos, unsigned cta,
+                                            float* __restrict__ cosines, float* __restrict__ sines) {
+  using Q = Piece<T, HALF, VEC>;
+  constexpr int P = Q::P, kUnroll = VEC && sizeof(T) == 4 ? 2 : 4;  // rows in flight: 64 bytes
+  const int width = min(p.slots, kThreads);        // threads of a row
   const int rows_step = kThreads / width;
   const int r0 = threadIdx.x / width, s0 = threadIdx.x - r0 * width;
-  if (r0 >= rows_step) return;
-  const unsigned begin = cta * p.rows_cta, end = min(begin + p.rows_cta, p.rows);
+  const unsigned heads = p.heads, begin = cta * p.rows_cta, end = min(begin + p.rows_cta, p.rows);
+  const unsigned token0 = begin / heads, tokens = (end - 1) / heads - token0 + 1;
+  const unsigned h_step = rows_step % heads, t_step = rows_step / heads;
   const T* x = (const T*)p.x;
   T* out = (T*)p.out;
-  for (int slot = s0; slot < p.slots; slot += width) {
-    const bool rotates = slot < p.rot_slots;
-    uint64_t step[P];
-    int col;                                       // first column of this thread
-    if (rotates) {
-#pragma unroll
-      for (int i = 0; i < P; ++i) step[i] = g.step[slot * P + i];
-      col = p.offset + slot * P * (HALF ? 1 : 2);
-    } else {
-      col = (slot - p.rot_slots) * E;
+  bool tabled = false;
+  for (int s = s0; s - s0 < p.slots; s += width) {
+    const bool here = r0 < rows_step && s < p.slots, rotates = here && s < p.rot_slots;
+    int col = p.offset + s * P * (HALF ? 1 : 2);   // first column of this thread
+    if (!rotates) {
+      col = (s - p.rot_slots) * Q::E;
       if (col >= p.offset) col += 2 * g.half;
     }
-    int token = -1;
-    float c[P], s[P];
-    for (unsigned row = begin + r0; row < end; row += kUnroll * rows_step) {
-      unsigned t[kUnroll], h[kUnroll];
+    unsigned row = here ? begin + r0 : end;
+    unsigned t = row / heads, h = row - t * heads;
+    const auto next = [&](unsigned& t, unsigned& h) {
+      t += t_step, h += h_step;
+      if (h >= heads) h -= heads, ++t;
+    };
+    Q q[kUnroll];
+    const auto load = [&](unsigned row, unsigned t, unsigned h) {
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k, next(t, h))
+        if (row + k * rows_step < end) {
+          const T* at = x + t * p.x_tok + h * p.x_head + col;
+          if (rotates) q[k].load(at, g.half);
+          else q[k].load_copy(at);
+        }
+    };
+    load(row, t, h);
+    if (!tabled) {                                 // the first rows are on their way: sines and cosines of the tokens
+      for (unsigned i = threadIdx.x; i < tokens * g.half; i += kThreads) {
+        const unsigned k = i / g.half;
+        turn(pos[token0 + k], g.step[i - k * g.half], g.mscale, g.sign, cosines[i], sines[i]);
+      }
+      __syncthreads();
+      tabled = true;
+    }
+    float c[P], d[P];
+    unsigned token = 0xFFFFFFFFu;
+    while (row < end) {
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
-        const unsigned r = row + k * rows_step;
-        t[k] = r / (unsigned)p.heads;
-        h[k] = r - t[k] * (unsigned)p.heads;
-      }
-      if (rotates) {
-        float a[kUnroll][P], b[kUnroll][P];
-        int at[kUnroll];
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
-          if (row + k * rows_step < end) {
-            at[k] = pos[t[k]];
-            load_pairs<T, HALF, P>(x + t[k] * p.x_tok + h[k] * p.x_head + col, g.half, a[k], b[k]);
-          }
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
-          if (row + k * rows_step < end) {
-            if ((int)t[k] != token) {
-              token = (int)t[k];
-#pragma unroll
-              for (int i = 0; i < P; ++i) turn(at[k], step[i], g.mscale, g.sign, c[i], s[i]);
+        if (row + k * rows_step < end) {
+          T* at = out + t * p.out_tok + h * p.out_head + col;
+          if (rotates) {
+            if (t != token) {
+              token = t;
+              const int i = (t - token0) * g.half + s * P;
+              if constexpr (P == 4) {
+                const float4 e = *reinterpret_cast<const float4*>(cosines + i), f = *reinterpret_cast<const float4*>(sines + i);
+                c[0] = e.x, c[1] = e.y, c[2] = e.z, c[3] = e.w, d[0] = f.x, d[1] = f.y, d[2] = f.z, d[3] = f.w;
+              } else {
+                c[0] = cosines[i], d[0] = sines[i];
+              }
             }
-            float u[P], v[P];
+            float a[P], b[P];
+            q[k].get(a, b);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-              u[i] = a[k][i] * c[i] - b[k][i] * s[i];
-              v[i] = a[k][i] * s[i] + b[k][i] * c[i];
+              const float u = a[i] * c[i] - b[i] * d[i];
+              b[i] = a[i] * d[i] + b[i] * c[i];
+              a[i] = u;
             }
-            store_pairs<T, HALF, P>(out + t[k] * p.out_tok + h[k] * p.out_head + col, g.half, u, v);
+            q[k].set(a, b);
+            q[k].store(at, g.half);
+          } else {
+            q[k].store_copy(at);
           }
-      } else {
-        V w[kUnroll];
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
-          if (row + k * rows_step < end)
-            w[k] = *reinterpret_cast<const V*>(x + t[k] * p.x_tok + h[k] * p.x_head + col);
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
-          if (row + k * rows_step < end)
-            *reinterpret_cast<V*>(out + t[k] * p.out_tok + h[k] * p.out_head + col) = w[k];
+        }
+        next(t, h);
       }
+      row += kUnroll * rows_step;
+      if (row < end) load(row, t, h);
     }
   }
 }
 
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ Args g, const int32_t* __restrict__ pos) {
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant__ Args g, const int32_t* __restrict__ pos) {
+  __shared__ __align__(16) float cosines[kTable], sines[kTable];
   let_next_launch();
   wait_for_earlier();
   int i = 0;
@@ -173,14 +223,14 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   const Part& p = g.part[i];
   const unsigned cta = blockIdx.x - p.first_cta;
   switch (p.kind) {
-    case 0: return rotate_rows<__nv_bfloat16, false, false>(g, p, pos, cta);
-    case 1: return rotate_rows<float, false, false>(g, p, pos, cta);
-    case 2: return rotate_rows<__nv_bfloat16, true, false>(g, p, pos, cta);
-    case 3: return rotate_rows<float, true, false>(g, p, pos, cta);
-    case 4: return rotate_rows<__nv_bfloat16, false, true>(g, p, pos, cta);
-    case 5: return rotate_rows<float, false, true>(g, p, pos, cta);
-    case 6: return rotate_rows<__nv_bfloat16, true, true>(g, p, pos, cta);
-    default: return rotate_rows<float, true, true>(g, p, pos, cta);
+    case 0: return rotate_rows<__nv_bfloat16, false, false>(g, p, pos, cta, cosines, sines);
+    case 1: return rotate_rows<float, false, false>(g, p, pos, cta, cosines, sines);
+    case 2: return rotate_rows<__nv_bfloat16, true, false>(g, p, pos, cta, cosines, sines);
+    case 3: return rotate_rows<float, true, false>(g, p, pos, cta, cosines, sines);
+    case 4: return rotate_rows<__nv_bfloat16, false, true>(g, p, pos, cta, cosines, sines);
+    case 5: return rotate_rows<float, false, true>(g, p, pos, cta, cosines, sines);
+    case 6: return rotate_rows<__nv_bfloat16, true, true>(g, p, pos, cta, cosines, sines);
+    default: return rotate_rows<float, true, true>(g, p, pos, cta, cosines, sines);
   }
 }
 
@@ -298,7 +348,10 @@ int dsa_rope_apply(const dsa_rope* p, int64_t n_tok, const int32_t* pos, const d
     t.slots = t.rot_slots + (vec ? rest / e : rest);
     const int width = t.slots < kThreads ? t.slots : kThreads, rows_step = kThreads / width;
     t.rows = (unsigned)(q.heads * n_tok);
-    t.rows_cta = (unsigned)(rows_step * kUnroll);
+    // four rows per thread, or eight where that leaves enough CTAs; the tokens' sines have to fit the table
+    long long steps = (long long)t.rows / rows_step >= 8 * 4096 ? 8 : 4;
+    while (steps > 1 && ((rows_step * steps + q.heads - 2) / q.heads + 1) * g.half > kTable) --steps;
+    t.rows_cta = (unsigned)(rows_step * steps);
     t.first_cta = (unsigned)ctas;
     ctas += (t.rows + t.rows_cta - 1) / t.rows_cta;
   }
