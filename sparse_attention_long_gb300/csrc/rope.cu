@@ -319,7 +319,7 @@ int dsa_rope_apply(const dsa_rope* p, int64_t n_tok, const int32_t* pos, const d
   g.mscale = p->mscale;
   g.sign = transposed ? -1.f : 1.f;
   for (int i = 0; i < g.half; ++i) g.step[i] = p->step[i];
-  long long ctas = 0;
+  long long work = 0, ctas = 0;                    // rows of all parts, in passes of a CTA's threads over them
   for (int i = 0; i < p->n_parts; ++i) {
     const dsa_rope_part& q = p->part[i];
     Part& t = g.part[i];
@@ -348,10 +348,19 @@ int dsa_rope_apply(const dsa_rope* p, int64_t n_tok, const int32_t* pos, const d
     t.slots = t.rot_slots + (vec ? rest / e : rest);
     const int width = t.slots < kThreads ? t.slots : kThreads, rows_step = kThreads / width;
     t.rows = (unsigned)(q.heads * n_tok);
-    // four rows per thread, or eight where that leaves enough CTAs; the tokens' sines have to fit the table
-    long long steps = (long long)t.rows / rows_step >= 8 * 4096 ? 8 : 4;
-    while (steps > 1 && ((rows_step * steps + q.heads - 2) / q.heads + 1) * g.half > kTable) --steps;
-    t.rows_cta = (unsigned)(rows_step * steps);
+    work += t.rows / rows_step + 1;
+  }
+  // Passes of a CTA: as many as leave 512 CTAs (3.4 per SM), 16 at most.  1 / 2 / 4 / 8 / 16
+  // passes: 16,384 tokens of the latent shapes 464 / 278 / 197 / 180 / 172 us, 768 tokens
+  // 24.5 / 16.6 / 14.3 / 13.0 / 13.7, 333 tokens x 10 heads of 80 fp32 5.0 / 3.4 / 3.8 / 5.1 / 7.1.
+  int passes = 1;
+  while (passes < 16 && work / (2 * passes) >= 512) passes *= 2;
+  for (int i = 0; i < p->n_parts; ++i) {
+    Part& t = g.part[i];
+    const int rows_step = kThreads / (t.slots < kThreads ? t.slots : kThreads);
+    int n = passes;                                // the sines of the CTA's tokens have to fit the table
+    while (n > 1 && (((long long)rows_step * n + t.heads - 2) / t.heads + 1) * g.half > kTable) --n;
+    t.rows_cta = (unsigned)(rows_step * n);
     t.first_cta = (unsigned)ctas;
     ctas += (t.rows + t.rows_cta - 1) / t.rows_cta;
   }
