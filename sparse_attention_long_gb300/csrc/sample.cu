@@ -25,10 +25,12 @@ bool ext_dev_ctx(DevCtx* c);
 namespace sample {
 
 constexpr int kMaxCluster = 8;
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kVec = 8;                            // consecutive logits of a thread
-constexpr int kChunk = 32768;                      // logits of a CTA at most
-constexpr int kMaxVocab = kMaxCluster * kChunk;
+constexpr int kMaxVocab = 1 << 18;
+constexpr int kList = 2048;                        // tokens that one CTA can order, 2^n
+constexpr int kCounted = 256;                      // up to so many by counting
+constexpr int kSmallK = 1024;                      // top_k up to which candidates are listed
 
 typedef unsigned long long u64;
 
@@ -135,7 +137,6 @@ struct Shared {
   uint32_t powers[256];
   u64 warp_sum[kWarps];
   uint32_t warp_count[kWarps];
-  float warp_max[kWarps];
   u64 sum[2][kMaxCluster], count[2][kMaxCluster];  // of every CTA of the cluster, two exchanges deep
 };
 
@@ -152,64 +153,212 @@ struct Team {
     }
     cluster_sync_all();
   }
-  // totals over the cluster
-  __device__ __forceinline__ void add(u64& sum, uint32_t& count) {
+  // this CTA's totals; the same of all threads that come between two barriers
+  __device__ __forceinline__ void add_cta(u64& sum, uint32_t& count) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     count = __reduce_add_sync(0xFFFFFFFFu, count);
-    // (the last exchange's barrier came after its reads of these)
     if (lane == 0) s.warp_sum[warp] = sum, s.warp_count[warp] = count;
     __syncthreads();
     sum = 0, count = 0;
     for (int w = 0; w < kWarps; ++w) sum += s.warp_sum[w], count += s.warp_count[w];
+  }
+  // totals over the cluster
+  __device__ __forceinline__ void add(u64& sum, uint32_t& count) {
+    add_cta(sum, count);                           // (read again before the exchange's barrier only)
     exchange(sum, count);
     sum = 0, count = 0;
     for (int r = 0; r < size; ++r) sum += s.sum[turn][r], count += (uint32_t)s.count[turn][r];
   }
-  __device__ __forceinline__ float largest(float x) {
+  // the sum of the threads before this one, and of all
+  __device__ __forceinline__ u64 before(u64 v, u64& all) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
-    if (lane == 0) s.warp_max[warp] = x;
+    u64 run = v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 r = __shfl_up_sync(0xFFFFFFFFu, run, o);
+      if (lane >= o) run += r;
+    }
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) x = fmaxf(x, s.warp_max[w]);
-    exchange(__float_as_uint(x), 0);
-    for (int r = 0; r < size; ++r) x = fmaxf(x, __uint_as_float((uint32_t)s.sum[turn][r]));
-    return x;
+    if (lane == 31) s.warp_sum[warp] = run;
+    __syncthreads();
+    u64 at = run - v;
+    all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) at += s.warp_sum[w];
+      all += s.warp_sum[w];
+    }
+    return at;
   }
 };
 
-// eight consecutive logits
-__device__ __forceinline__ void load8(const float* p, float (&v)[kVec]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[kVec]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// eight consecutive logits as they lie in memory
+template <typename T>
+struct Run;
+template <>
+struct Run<float> {
+  uint32_t w[8];
+  static constexpr uint32_t kNone = 0xFF800000u;   // -inf
+  __device__ __forceinline__ void load(const float* p) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 4);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(p + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+  __device__ __forceinline__ void load_some(const float* p, int n) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-}
+    for (int j = 0; j < 8; ++j) w[j] = j < n ? __float_as_uint(p[j]) : kNone;
+  }
+  __device__ __forceinline__ float get(int j) const { return __uint_as_float(w[j]); }
+  // infinities and NaN become -inf; returns the largest
+  __device__ __forceinline__ float clean() {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float v = fabsf(get(j)) <= FLT_MAX ? get(j) : -INFINITY;
+      w[j] = __float_as_uint(v);
+      m = fmaxf(m, v);
+    }
+    return m;
+  }
+  __device__ __forceinline__ bool any(float low) const {
+    float m = get(0);
+#pragma unroll
+    for (int j = 1; j < 8; ++j) m = fmaxf(m, get(j));
+    return m >= low;
+  }
+};
+template <>
+struct Run<__nv_bfloat16> {
+  uint32_t w[4];
+  static constexpr uint32_t kNone = 0xFF80u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void load_some(const __nv_bfloat16* p, int n) {
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = (2 * j < n ? q[2 * j] : kNone) | (2 * j + 1 < n ? q[2 * j + 1] : kNone) << 16;
+  }
+  __device__ __forceinline__ float get(int j) const {
+    return __uint_as_float((j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+  }
+  __device__ __forceinline__ float clean() {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool ok = fabsf(get(j)) <= FLT_MAX;
+      if (!ok) w[j >> 1] = (j & 1) ? (w[j >> 1] & 0xFFFFu) | kNone << 16 : (w[j >> 1] & 0xFFFF0000u) | kNone;
+      m = fmaxf(m, ok ? get(j) : -INFINITY);
+    }
+    return m;
+  }
+  __device__ __forceinline__ bool any(float low) const {
+    float m = get(0);
+#pragma unroll
+    for (int j = 1; j < 8; ++j) m = fmaxf(m, get(j));
+    return m >= low;
+  }
+};
 
-__device__ __forceinline__ void store8(float* p, const float (&v)[kVec]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+// larger logit first, then lower index
+__device__ __forceinline__ u64 make_key(float l, uint32_t idx) {
+  return ((u64)ordered_key(l) << 32) | (0xFFFFFFFFu - idx);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[kVec]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                            pack_bf16x2(v[6], v[7]));
+__device__ __forceinline__ float key_logit(u64 k) { return ordered_value((uint32_t)(k >> 32)); }
+
+// The end for n listed tokens, by one CTA: list[] in index order, sorted[] room for as
+// many (kList).  k: how many are kept at most; want(mass of these): as in top-p.
+__device__ __forceinline__ void finish(const Args& a, Team& team, const Weight& weight, const u64* __restrict__ list,
+                                       u64* __restrict__ sorted, int n, int k, float p, float u, int row) {
+  const Shared& s = team.s;
+  const int tid = threadIdx.x;
+  const int kk = min(n, k);
+  u64 least = 0;                                   // the last key that is kept
+  u64 total = 0;
+  if (kk < n || p < 1.f) {
+    if (n <= kCounted) {
+      // every key's place is the number of larger ones
+      if (tid < n) {
+        const u64 mine = list[tid];
+        int place = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) place += list[j] > mine;
+        sorted[place] = mine;
+      }
+      __syncthreads();
+    } else {
+      int m = kCounted;
+      while (m < n) m *= 2;
+      for (int i = tid; i < m; i += kThreads) sorted[i] = i < n ? list[i] : 0;
+      for (int size = 2; size <= m; size *= 2)
+        for (int step = size / 2; step; step /= 2) {
+          __syncthreads();
+          for (int i = tid; i < m / 2; i += kThreads) {
+            const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
+            const u64 x = sorted[lo], y = sorted[hi];
+            if ((x < y) == ((lo & size) == 0)) sorted[lo] = y, sorted[hi] = x;
+          }
+        }
+      __syncthreads();
+    }
+    // masses in that order, `each` places per thread
+    const int each = (n + kThreads - 1) / kThreads, first = tid * each, behind = min(first + each, kk);
+    int kept = kk;
+    if (p < 1.f) {
+      u64 mine = 0, all;
+      for (int i = first; i < behind; ++i) mine += weight(key_logit(sorted[i]), s.powers);
+      u64 at = team.before(mine, all);
+      const u64 want = scaled(p, all, true);       // the mass before a kept token is below this
+      int more = 0;
+      for (int i = first; i < behind; ++i) {
+        more += at < want;
+        at += weight(key_logit(sorted[i]), s.powers);
+      }
+      u64 none = 0;
+      uint32_t count = more;
+      __syncthreads();
+      team.add_cta(none, count);
+      kept = max(1, (int)count);
+    }
+    least = sorted[kept - 1];
+  }
+  const int each = (n + kThreads - 1) / kThreads, first = tid * each, behind = min(first + each, n);
+  u64 mine = 0;
+  for (int i = first; i < behind; ++i)
+    if (list[i] >= least) mine += weight(key_logit(list[i]), s.powers);
+  u64 at = team.before(mine, total);
+  const u64 target = scaled(u, total, false);
+  if (at > target || at + mine <= target) return;
+  for (int i = first; i < behind; ++i) {
+    const u64 w = list[i] >= least ? weight(key_logit(list[i]), s.powers) : 0;
+    if (at <= target && target < at + w) {
+      a.token[row] = (int32_t)(0xFFFFFFFFu - (uint32_t)list[i]);
+      if (a.prob) a.prob[row] = (float)((double)w / (double)total);
+    }
+    at += w;
+  }
 }
 
 // chunk: logits of a CTA; steps: runs of eight per thread, so that the chunk fits the CTA
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     sample_kernel(const __grid_constant__ Args a, const T* __restrict__ logits, int chunk, int steps, int vec, DevCtx c) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ Shared sh;
+  u64* list = (u64*)dyn;
+  T* mine = (T*)(dyn + kList * sizeof(u64));
   let_next_launch();
   cluster_arrive();                                // no CTA writes to one that has not begun
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int size = (int)cluster_nctarank(), rank = (int)cluster_ctarank(), row = blockIdx.x / size;
-  if (tid < 256) sh.powers[tid] = kPowers.at[tid];
+  for (int i = tid; i < 256; i += kThreads) sh.powers[i] = kPowers.at[i];
   wait_for_earlier();
   // the request's settings
   const int q = a.index ? a.index[row] : row;
@@ -219,44 +368,69 @@ __global__ void __launch_bounds__(kThreads)
   const bool greedy = temp == 0.f, draws = ok && !greedy;
   const float p = draws && a.top_p ? a.top_p[q] : 1.f, least = draws && a.min_p ? a.min_p[q] : 0.f;
   const float u = draws ? a.u[row] : 0.f;
-  const int k = draws && a.top_k ? a.top_k[q] : 0;
+  int k = draws && a.top_k ? a.top_k[q] : 0;
   ok = ok && k >= 0 && p > 0.f && p <= 1.f && least >= 0.f && least <= 1.f && u >= 0.f && u < 1.f;
+  if (k == 0 || k > a.vocab) k = a.vocab;
+  if (greedy) k = 1;
   // The row's logits of this CTA to shared memory: a warp's together in index order, a
   // thread's in runs of eight.
   const int first = (warp * steps * 32 + lane) * kVec;
   const int there = min(chunk, a.vocab - rank * chunk);
   const T* src = logits + row * a.ld + rank * chunk;
-  T* x = (T*)dyn + first;
+  T* x = mine + first;
   float m = -INFINITY;
 #pragma unroll 4
   for (int s = 0; s < steps; ++s) {
     const int i = first + s * 32 * kVec;
-    float v[kVec];
-    if (vec && i + kVec <= there) {
-      load8(src + i, v);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) v[j] = i + j < there ? to_f32(src[i + j]) : -INFINITY;
-    }
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      v[j] = fabsf(v[j]) <= FLT_MAX ? v[j] : -INFINITY;  // infinities and NaN are never chosen
-      m = fmaxf(m, v[j]);
-    }
-    store8(x + s * 32 * kVec, v);
+    Run<T> run;
+    if (vec && i + kVec <= there) run.load(src + i);
+    else run.load_some(src + i, there - i);
+    m = fmaxf(m, run.clean());
+    run.store(x + s * 32 * kVec);
   }
   // f(logit) over this thread's logits
   const auto each_logit = [&](auto f) {
     for (int s = 0; s < steps; ++s) {
-      float v[kVec];
-      load8(x + s * 32 * kVec, v);
+      Run<T> run;
+      run.load(x + s * 32 * kVec);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) f(v[j]);
+      for (int j = 0; j < kVec; ++j) f(run.get(j));
     }
   };
   Team team{sh, rank, size, 0};
+  // The CTA's largest logit; and with a small k a logit that at least k of the row reach:
+  // ceil(k / size) threads of each CTA have one.
+  const uint32_t best = ordered_key(m);
+  const uint32_t of_warp = __reduce_max_sync(0xFFFFFFFFu, best);
+  if (lane == 0) sh.warp_count[warp] = of_warp;
+  __syncthreads();
+  uint32_t top = 0;
+  for (int w = 0; w < kWarps; ++w) top = max(top, sh.warp_count[w]);
+  uint32_t bound = 0;
+  const bool small_k = k <= kSmallK && k < a.vocab;
+  if (small_k) {
+    const int need = (k + size - 1) / size;
+    bound = top;
+    if (need > 1) {
+      uint32_t lo = 0, hi = top + 1, step = 1u << 18;  // fewer than `need` threads reach hi, at least as many lo
+      while (hi - lo > 1) {
+        const uint32_t mid = lo == 0 && hi > step ? hi - step : lo + (hi - lo) / 2;
+        const int n = __syncthreads_count(best >= mid);
+        if (n >= need) lo = mid;
+        else hi = mid, step *= 2;
+        if (n >= need && n <= need + need / 4 + 1) break;
+        if (lo == 0 && step >= (1u << 30)) break;  // a CTA with few logits: all are candidates
+      }
+      bound = lo;
+    }
+  }
   cluster_wait();
-  m = team.largest(m);
+  team.exchange(top, bound);
+  for (int r = 0; r < size; ++r) {
+    top = max(top, (uint32_t)sh.sum[team.turn][r]);
+    bound = min(bound, (uint32_t)sh.count[team.turn][r]);
+  }
+  m = ordered_value(top);
   if (!ok || m == -INFINITY) {                     // the same for the whole cluster
     if (rank == 0 && tid == 0) {
       a.token[row] = -1;
@@ -277,76 +451,142 @@ __global__ void __launch_bounds__(kThreads)
     const double far = -log((double)least) * (double)temp;
     cut = fmaxf(__double2float_ru((double)m - far), -FLT_MAX);
   }
-  u64 mass = 0;
-  uint32_t count = 0, ties = 0x7FFFFFFFu;
-  const uint32_t top = Grid<T>::up(m) + 1;
-  uint32_t lo = Grid<T>::up(cut), hi = top;
-  if (greedy) {
-    ties = 1;
-  } else {
-    if (k > 0 && k < a.vocab) {
-      u64 none = 0;
-      count = 0;
-      each_logit([&](float l) { count += l >= cut; });
-      team.add(none, count);
-      if (count > (uint32_t)k) {
-        uint32_t above = 0;                        // logits at hi and above
-        while (hi - lo > 1) {
-          const uint32_t mid = lo + (hi - lo) / 2;
-          const float v = Grid<T>::value(mid);
-          none = count = 0;
-          each_logit([&](float l) { count += l >= v; });
-          team.add(none, count);
-          if (count >= (uint32_t)k) lo = mid;
-          else hi = mid, above = count;
-        }
-        ties = k - above;
-      }
+  if (small_k || least > 0.f) {
+    // Few tokens can be kept as a rule: CTA 0 gets them listed, in index order.
+    const float low = small_k ? fmaxf(cut, fmaxf(ordered_value(bound), -FLT_MAX)) : cut;
+    const int room = kList / size;
+    uint32_t n = 0;
+    for (int s = 0; s < steps; ++s) {
+      Run<T> run;
+      run.load(x + s * 32 * kVec);
+      if (run.any(low))
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) n += run.get(j) >= low;
     }
-    cut = Grid<T>::value(lo);
-    // the mass of what is kept so far
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    if (lane == 0) sh.warp_count[warp] = n;
+    __syncthreads();
+    uint32_t at = 0, in_cta = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) at += sh.warp_count[w];
+      in_cta += sh.warp_count[w];
+    }
+    if (in_cta <= (uint32_t)room && n)
+      for (int s = 0; s < steps; ++s) {
+        Run<T> run;
+        run.load(x + s * 32 * kVec);
+        uint32_t hits = 0;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) hits |= (uint32_t)(run.get(j) >= low) << j;
+        if (!__any_sync(0xFFFFFFFFu, hits)) continue;
+        const uint32_t have = __popc(hits);
+        uint32_t upto = have;
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t r = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+          if (lane >= o) upto += r;
+        }
+        uint32_t to = rank * room + at + upto - have;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+          if (hits >> j & 1)
+            store_remote(&list[to++], 0, make_key(run.get(j), (uint32_t)(rank * chunk + first + s * 32 * kVec + j)));
+        at += __shfl_sync(0xFFFFFFFFu, upto, 31);
+      }
+    team.exchange(0, in_cta);
+    bool all = true;
+    int total = 0;
+    for (int r = 0; r < size; ++r) {
+      all = all && sh.count[team.turn][r] <= (u64)room;
+      total += (int)sh.count[team.turn][r];
+    }
+    if (all) {
+      if (rank != 0) return;
+      // together; each CTA's part moves towards the front
+      if (size > 1) {
+        u64 keep[kList / kThreads];
+#pragma unroll
+        for (int i = 0; i < kList / kThreads; ++i) keep[i] = list[tid + i * kThreads];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kList / kThreads; ++i) {
+          const int from = tid + i * kThreads, r = from / room, o = from - r * room;
+          int to = o;
+          for (int b = 0; b < r; ++b) to += (int)sh.count[team.turn][b];
+          if (o < (int)sh.count[team.turn][r]) list[to] = keep[i];
+        }
+        __syncthreads();
+      }
+      finish(a, team, weight, list, (u64*)mine, total, k, p, u, row);
+      return;
+    }
+  }
+  // Any number of tokens: bisection over the logits' bits.
+  u64 mass = 0, sum = 0;
+  uint32_t count = 0, ties = greedy ? 1u : 0x7FFFFFFFu;
+  const uint32_t end = Grid<T>::up(m) + 1;
+  uint32_t lo = Grid<T>::up(cut), hi = end;
+  if (k < a.vocab && !greedy) {
+    u64 none = 0;
     count = 0;
+    each_logit([&](float l) { count += l >= cut; });
+    team.add(none, count);
+    if (count > (uint32_t)k) {
+      uint32_t above = 0;                          // logits at hi and above
+      while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        const float v = Grid<T>::value(mid);
+        none = count = 0;
+        each_logit([&](float l) { count += l >= v; });
+        team.add(none, count);
+        if (count >= (uint32_t)k) lo = mid;
+        else hi = mid, above = count;
+      }
+      ties = k - above;
+    }
+  }
+  if (!greedy) cut = Grid<T>::value(lo);
+  // this thread's part of what is kept so far
+  const auto kept_here = [&] {
+    sum = 0, count = 0;
     each_logit([&](float l) {
-      if (l > cut) mass += weight(l, sh.powers);
+      if (l > cut) sum += weight(l, sh.powers);
       count += l == cut;
     });
-    team.add(mass, count);
-    ties = min(ties, count);
+  };
+  kept_here();
+  if (p < 1.f) {
+    mass = sum;
+    uint32_t tied = count;
+    team.add(mass, tied);
+    ties = min(ties, tied);
     const u64 each = weight(cut, sh.powers);
-    if (p < 1.f) {
-      const u64 want = scaled(p, mass + ties * each, true);  // the mass before a kept token is below this
-      if (mass < want) {                           // tokens at the cut are among them
-        ties = (uint32_t)((want - mass + each - 1) / each);
-      } else {
-        u64 above = 0;                             // mass at hi and above
-        hi = top;
-        while (hi - lo > 1) {
-          const uint32_t mid = lo + (hi - lo) / 2;
-          const float v = Grid<T>::value(mid), w = hi == top ? INFINITY : Grid<T>::value(hi);
-          u64 some = 0;
-          count = 0;
-          each_logit([&](float l) {
-            if (l >= v && l < w) some += weight(l, sh.powers);
-          });
-          team.add(some, count);
-          some += above;
-          if (some >= want) lo = mid;
-          else hi = mid, above = some;
-        }
-        cut = Grid<T>::value(lo);
-        const u64 one = weight(cut, sh.powers);
-        ties = (uint32_t)((want - above + one - 1) / one);
+    const u64 want = scaled(p, mass + ties * each, true);  // the mass before a kept token is below this
+    if (mass < want) {                             // tokens at the cut are among them
+      ties = (uint32_t)((want - mass + each - 1) / each);
+    } else {
+      u64 above = 0;                               // mass at hi and above
+      hi = end;
+      while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        const float v = Grid<T>::value(mid), w = hi == end ? INFINITY : Grid<T>::value(hi);
+        u64 some = 0;
+        uint32_t none = 0;
+        each_logit([&](float l) {
+          if (l >= v && l < w) some += weight(l, sh.powers);
+        });
+        team.add(some, none);
+        some += above;
+        if (some >= want) lo = mid;
+        else hi = mid, above = some;
       }
+      cut = Grid<T>::value(lo);
+      const u64 one = weight(cut, sh.powers);
+      ties = (uint32_t)((want - above + one - 1) / one);
+      kept_here();
     }
   }
   // what each warp keeps, in the order of the tokens
   const u64 each = weight(cut, sh.powers);
-  u64 sum = 0;
-  count = 0;
-  each_logit([&](float l) {
-    if (l > cut) sum += weight(l, sh.powers);
-    count += l == cut;
-  });
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   count = __reduce_add_sync(0xFFFFFFFFu, count);
   if (lane == 0) sh.warp_sum[warp] = sum, sh.warp_count[warp] = count;
@@ -375,29 +615,30 @@ __global__ void __launch_bounds__(kThreads)
   if (before > target || before + sum + tie_mass(tied_before, count) <= target) return;
   // the one warp that holds the token, thread by thread
   for (int s = 0; s < steps; ++s) {
-    float v[kVec];
-    load8(x + s * 32 * kVec, v);
-    u64 mine = 0;
-    uint32_t t = 0;
+    Run<T> v;
+    v.load(x + s * 32 * kVec);
+    u64 run = 0;
+    uint32_t tie_run = 0;
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-      if (v[j] > cut) mine += weight(v[j], sh.powers);
-      t += v[j] == cut;
+      if (v.get(j) > cut) run += weight(v.get(j), sh.powers);
+      tie_run += v.get(j) == cut;
     }
-    u64 run = mine;
-    uint32_t tie_run = t;
+    const u64 own = run;
+    const uint32_t own_ties = tie_run;
     for (int o = 1; o < 32; o <<= 1) {
       const u64 r = __shfl_up_sync(0xFFFFFFFFu, run, o);
       const uint32_t n = __shfl_up_sync(0xFFFFFFFFu, tie_run, o);
       if (lane >= o) run += r, tie_run += n;
     }
-    uint32_t seen = tied_before + (tie_run - t);
-    u64 at = before + (run - mine) + tie_mass(tied_before, tie_run - t);
+    uint32_t seen = tied_before + (tie_run - own_ties);
+    u64 at = before + (run - own) + tie_mass(tied_before, tie_run - own_ties);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
+      const float l = v.get(j);
       u64 w = 0;
-      if (v[j] > cut) w = weight(v[j], sh.powers);
-      else if (v[j] == cut && seen++ < ties) w = each;
+      if (l > cut) w = weight(l, sh.powers);
+      else if (l == cut && seen++ < ties) w = each;
       if (at <= target && target < at + w) {
         a.token[row] = rank * chunk + first + s * 32 * kVec + j;
         if (a.prob) a.prob[row] = (float)((double)w / (double)total);
@@ -426,11 +667,16 @@ static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 
 template <typename T>
 static bool launch(const Args& a, const void* logits, DevCtx c, cudaStream_t st) {
-  int size = 1;
-  while (size < kMaxCluster && size * kChunk < a.vocab) size *= 2;
+  // 32 KB of logits per CTA, so that four fit an SM, and more CTAs for a few rows
+  int dev = 0, sms = 0, size = 1;
+  if (!cuda_ok(cudaGetDevice(&dev)) || !cuda_ok(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)))
+    return false;
+  while (size < kMaxCluster && (size * (32768ll / (int)sizeof(T)) < a.vocab ||
+                                ((long long)a.rows * size * 2 <= sms && size * 2048 < a.vocab)))
+    size *= 2;
   const int chunk = (a.vocab + size * kVec - 1) / (size * kVec) * kVec, step = kThreads * kVec;
   const int steps = (chunk + step - 1) / step;
-  const size_t smem = (size_t)steps * step * sizeof(T);
+  const size_t room = (size_t)steps * step * sizeof(T), smem = kList * 8 + (room > kList * 8 ? room : kList * 8);
   const int vec = (((uintptr_t)logits | (uintptr_t)(a.ld * sizeof(T))) & 15u) == 0;
   return cuda_ok(cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) &&
          launch_programmatic(sample_kernel<T>, dim3((unsigned)(a.rows * size)), dim3(kThreads), smem, st, size, a,
