@@ -135,6 +135,7 @@ __device__ __forceinline__ uint32_t cluster_nctarank() {
 
 struct Shared {
   uint32_t powers[256];
+  double far;                                      // how far below the largest logit min-p goes
   u64 warp_sum[kWarps];
   uint32_t warp_count[kWarps];
   u64 sum[2][kMaxCluster], count[2][kMaxCluster];  // of every CTA of the cluster, two exchanges deep
@@ -222,11 +223,11 @@ struct Run<float> {
     }
     return m;
   }
-  __device__ __forceinline__ bool any(float low) const {
+  __device__ __forceinline__ float largest() const {
     float m = get(0);
 #pragma unroll
     for (int j = 1; j < 8; ++j) m = fmaxf(m, get(j));
-    return m >= low;
+    return m;
   }
 };
 template <>
@@ -249,21 +250,26 @@ struct Run<__nv_bfloat16> {
   __device__ __forceinline__ float get(int j) const {
     return __uint_as_float((j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
   }
-  __device__ __forceinline__ float clean() {
-    float m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const bool ok = fabsf(get(j)) <= FLT_MAX;
-      if (!ok) w[j >> 1] = (j & 1) ? (w[j >> 1] & 0xFFFFu) | kNone << 16 : (w[j >> 1] & 0xFFFF0000u) | kNone;
-      m = fmaxf(m, ok ? get(j) : -INFINITY);
-    }
-    return m;
+  static __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
   }
-  __device__ __forceinline__ bool any(float low) const {
-    float m = get(0);
+  __device__ __forceinline__ float largest() const {
+    const uint32_t m = max2(max2(w[0], w[1]), max2(w[2], w[3]));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ float clean() {
+    uint32_t bad = 0;                              // an exponent of all ones carries into the sign
 #pragma unroll
-    for (int j = 1; j < 8; ++j) m = fmaxf(m, get(j));
-    return m >= low;
+    for (int j = 0; j < 4; ++j) bad |= (w[j] & 0x7F807F80u) + 0x00800080u;
+    if (bad & 0x80008000u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if ((w[j] & 0x7F80u) == 0x7F80u) w[j] = (w[j] & 0xFFFF0000u) | kNone;
+        if ((w[j] & 0x7F800000u) == 0x7F800000u) w[j] = (w[j] & 0xFFFFu) | kNone << 16;
+      }
+    return largest();
   }
 };
 
@@ -372,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   ok = ok && k >= 0 && p > 0.f && p <= 1.f && least >= 0.f && least <= 1.f && u >= 0.f && u < 1.f;
   if (k == 0 || k > a.vocab) k = a.vocab;
   if (greedy) k = 1;
+  if (tid == 0 && least > 0.f) sh.far = -log((double)least) * (double)temp;
   // The row's logits of this CTA to shared memory: a warp's together in index order, a
   // thread's in runs of eight.
   const int first = (warp * steps * 32 + lane) * kVec;
@@ -379,14 +386,22 @@ __global__ void __launch_bounds__(kThreads, 4)
   const T* src = logits + row * a.ld + rank * chunk;
   T* x = mine + first;
   float m = -INFINITY;
-#pragma unroll 4
-  for (int s = 0; s < steps; ++s) {
-    const int i = first + s * 32 * kVec;
-    Run<T> run;
-    if (vec && i + kVec <= there) run.load(src + i);
-    else run.load_some(src + i, there - i);
-    m = fmaxf(m, run.clean());
-    run.store(x + s * 32 * kVec);
+  constexpr int kAhead = sizeof(T) == 2 ? 8 : 4;   // runs in flight
+  for (int s0 = 0; s0 < steps; s0 += kAhead) {
+    Run<T> run[kAhead];
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+      const int i = first + (s0 + s) * 32 * kVec;
+      if (s0 + s >= steps) break;
+      if (vec && i + kVec <= there) run[s].load(src + i);
+      else run[s].load_some(src + i, there - i);
+    }
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+      if (s0 + s >= steps) break;
+      m = fmaxf(m, run[s].clean());
+      run[s].store(x + (s0 + s) * 32 * kVec);
+    }
   }
   // f(logit) over this thread's logits
   const auto each_logit = [&](auto f) {
@@ -442,27 +457,31 @@ __global__ void __launch_bounds__(kThreads, 4)
   // kept: logits above `cut`, and of those equal to it the first `ties`; first what min-p keeps
   Weight weight{m, 0.f, 0.f, a.unit};
   if (draws) {
-    const double f = fmin(1.4426950408889634 / (double)temp, 1e38);
-    weight.hi = (float)f;
-    weight.lo = (float)(f - (double)weight.hi);
+    // (no fp64: its units are few)
+    constexpr float kHi = 1.44269502162933349609375f, kLo = 1.9259629911e-8f;
+    weight.hi = __fdiv_rn(kHi, temp);
+    weight.lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-weight.hi, temp, kHi), kLo), temp);
+    if (!(weight.hi < 1e38f)) weight.hi = 1e38f, weight.lo = 0.f;
   }
   float cut = greedy ? m : -FLT_MAX;
   if (least > 0.f) {
-    const double far = -log((double)least) * (double)temp;
-    cut = fmaxf(__double2float_ru((double)m - far), -FLT_MAX);
+    cut = fmaxf(__double2float_ru((double)m - sh.far), -FLT_MAX);
   }
   if (small_k || least > 0.f) {
     // Few tokens can be kept as a rule: CTA 0 gets them listed, in index order.
     const float low = small_k ? fmaxf(cut, fmaxf(ordered_value(bound), -FLT_MAX)) : cut;
     const int room = kList / size;
-    uint32_t n = 0;
+    uint32_t n = 0, with = 0;                      // steps with some (steps <= 32)
     for (int s = 0; s < steps; ++s) {
       Run<T> run;
       run.load(x + s * 32 * kVec);
-      if (run.any(low))
+      if (run.largest() >= low) {
+        with |= 1u << s;
 #pragma unroll
         for (int j = 0; j < kVec; ++j) n += run.get(j) >= low;
+      }
     }
+    with = __reduce_or_sync(0xFFFFFFFFu, with);
     n = __reduce_add_sync(0xFFFFFFFFu, n);
     if (lane == 0) sh.warp_count[warp] = n;
     __syncthreads();
@@ -471,14 +490,14 @@ __global__ void __launch_bounds__(kThreads, 4)
       if (w < warp) at += sh.warp_count[w];
       in_cta += sh.warp_count[w];
     }
-    if (in_cta <= (uint32_t)room && n)
-      for (int s = 0; s < steps; ++s) {
+    if (in_cta <= (uint32_t)room)
+      for (; with; with &= with - 1) {
+        const int s = __ffs(with) - 1;
         Run<T> run;
         run.load(x + s * 32 * kVec);
         uint32_t hits = 0;
 #pragma unroll
         for (int j = 0; j < kVec; ++j) hits |= (uint32_t)(run.get(j) >= low) << j;
-        if (!__any_sync(0xFFFFFFFFu, hits)) continue;
         const uint32_t have = __popc(hits);
         uint32_t upto = have;
         for (int o = 1; o < 32; o <<= 1) {
