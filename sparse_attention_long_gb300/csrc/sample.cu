@@ -63,6 +63,9 @@ __device__ const Powers kPowers{};
 __device__ __forceinline__ void store_remote(u64* local, uint32_t rank, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_u32(local), rank)), "l"(v) : "memory");
 }
+__device__ __forceinline__ void store_remote(float* local, uint32_t rank, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(local), rank)), "f"(v) : "memory");
+}
 __device__ __forceinline__ float ordered_value(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
 }
@@ -139,6 +142,10 @@ struct Shared {
   u64 warp_sum[kWarps];
   uint32_t warp_count[kWarps];
   u64 sum[2][kMaxCluster], count[2][kMaxCluster];  // of every CTA of the cluster, two exchanges deep
+  u64 note[2];                                     // of CTA 0 to all
+  float warp_mass[kWarps], z;
+  int bin[3];
+  uint32_t rank_in;
 };
 
 // What a CTA sums, and what the cluster does.  An exchange's numbers stay readable until
@@ -272,6 +279,119 @@ struct Run<__nv_bfloat16> {
     return largest();
   }
 };
+
+__device__ __forceinline__ uint4 load_remote(const uint32_t* local, uint32_t rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(mapa_shared(smem_u32(local), rank))
+               : "memory");
+  return v;
+}
+
+// The largest grid value that `want` of what f counts (or weighs) reach: grid numbers lo
+// (reached) and hi (not); above: f at the grid number behind it.  f(v, w): of the logits
+// in [v, w), w infinite at first.
+template <typename T, typename S, typename F>
+__device__ __forceinline__ float bisect(uint32_t lo, uint32_t hi, S want, S& above, F f) {
+  float w = INFINITY;
+  while (hi - lo > 1) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    const float v = Grid<T>::value(mid);
+    const S some = above + f(v, w);
+    if (some >= want) lo = mid;
+    else hi = mid, w = v, above = some;
+  }
+  return Grid<T>::value(lo);
+}
+
+// A CTA's histogram: bin b holds logits whose distance to the largest is b / 128 powers of
+// two, to the nearest; the last one also what lies further down.
+constexpr int kBins = 4096;
+constexpr float kPerUnit = 128.f;
+struct Bins {
+  float max, scale;
+  __device__ __forceinline__ int operator()(float l) const {
+    const float v = fminf(__fmul_rn(__fsub_rn(max, l), scale), (float)(kBins - 1));
+    return (int)(__float_as_uint(__fadd_rn(v, 8388608.f)) - 0x4B000000u);
+  }
+};
+
+// CTA 0's choice of bins from the cluster's histograms (hist of each CTA).  bin[2]: where
+// the k-th logit lies (kBins: none does), `rank_in` of its bin's tokens are kept; bin[0]
+// to bin[1]: where top-p's border lies, by the counts and the weights of the bins' middles.
+// A middle is off by a part in 370 at most, a sum over many bins by much less: 2^-9 to
+// either side, and who has the exact sums looks whether the border lies between.
+__device__ __forceinline__ void choose_bins(Shared& s, const uint32_t* __restrict__ hist, int size, int k, bool cuts,
+                                            float p, uint32_t& rank_in) {
+  constexpr int kMine = kBins / kThreads;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t n[kMine] = {};
+  for (int r = 0; r < size; ++r)
+#pragma unroll
+    for (int i = 0; i < kMine; i += 4) {
+      const uint4 v = load_remote(hist + tid * kMine + i, r);
+      n[i] += v.x, n[i + 1] += v.y, n[i + 2] += v.z, n[i + 3] += v.w;
+    }
+  if (tid < 2) s.bin[tid] = kBins - 1;
+  if (tid == 0) s.bin[2] = kBins;
+  uint32_t count = 0;
+  float mass = 0;
+  const auto weight = [&](int i) { return n[i] * exp2f(-(float)(tid * kMine + i) / kPerUnit); };
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) count += n[i], mass += weight(i);
+  uint32_t c_run = count;
+  float m_run = mass;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t c = __shfl_up_sync(0xFFFFFFFFu, c_run, o);
+    const float a = __shfl_up_sync(0xFFFFFFFFu, m_run, o);
+    if (lane >= o) c_run += c, m_run += a;
+  }
+  if (lane == 31) s.warp_count[warp] = c_run, s.warp_mass[warp] = m_run;
+  __syncthreads();
+  // of the threads before this one (sums of positive numbers: nothing cancels)
+  c_run -= count, m_run = __shfl_up_sync(0xFFFFFFFFu, m_run, 1);
+  if (lane == 0) m_run = 0.f;
+  float z = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) c_run += s.warp_count[w], m_run += s.warp_mass[w];
+    z += s.warp_mass[w];
+  }
+  if (cuts && c_run < (uint32_t)k && (uint32_t)k <= c_run + count) {
+    uint32_t c = c_run;
+    float a = m_run;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      if (c < (uint32_t)k && (uint32_t)k <= c + n[i]) {
+        s.bin[2] = tid * kMine + i;
+        s.rank_in = k - c;
+        s.z = a + weight(i) / n[i] * (k - c);
+      }
+      c += n[i], a += weight(i);
+    }
+  }
+  __syncthreads();
+  rank_in = 0;
+  if (s.bin[2] < kBins) rank_in = s.rank_in, z = s.z;
+  if (p < 1.f) {
+    const float from = p * z * (1.f - 0x1p-9f), upto = p * z * (1.f + 0x1p-9f);
+    float a = m_run;
+    int b1 = kBins - 1, b2 = kBins - 1;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      a += weight(i);
+      if (a >= from) b1 = min(b1, tid * kMine + i);
+      if (a >= upto) b2 = min(b2, tid * kMine + i);
+    }
+    if (b1 < kBins - 1) atomicMin(&s.bin[0], b1);
+    if (b2 < kBins - 1) atomicMin(&s.bin[1], b2);
+    __syncthreads();
+    if (tid == 0) s.bin[0] = min(s.bin[0], s.bin[2]), s.bin[1] = max(s.bin[0], min(s.bin[1], s.bin[2]));
+  } else if (tid == 0) {
+    s.bin[0] = s.bin[1] = s.bin[2];
+  }
+  __syncthreads();
+}
 
 // larger logit first, then lower index
 __device__ __forceinline__ u64 make_key(float l, uint32_t idx) {
@@ -539,32 +659,9 @@ __global__ void __launch_bounds__(kThreads, 4)
       return;
     }
   }
-  // Any number of tokens: bisection over the logits' bits.
-  u64 mass = 0, sum = 0;
-  uint32_t count = 0, ties = greedy ? 1u : 0x7FFFFFFFu;
-  const uint32_t end = Grid<T>::up(m) + 1;
-  uint32_t lo = Grid<T>::up(cut), hi = end;
-  if (k < a.vocab && !greedy) {
-    u64 none = 0;
-    count = 0;
-    each_logit([&](float l) { count += l >= cut; });
-    team.add(none, count);
-    if (count > (uint32_t)k) {
-      uint32_t above = 0;                          // logits at hi and above
-      while (hi - lo > 1) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        const float v = Grid<T>::value(mid);
-        none = count = 0;
-        each_logit([&](float l) { count += l >= v; });
-        team.add(none, count);
-        if (count >= (uint32_t)k) lo = mid;
-        else hi = mid, above = count;
-      }
-      ties = k - above;
-    }
-  }
-  if (!greedy) cut = Grid<T>::value(lo);
-  // this thread's part of what is kept so far
+  // Any number of tokens.
+  u64 sum = 0;                                     // this thread's part of what is kept: logits above the cut,
+  uint32_t count = 0, ties = greedy ? 1u : 0x7FFFFFFFu;  // and those equal to it
   const auto kept_here = [&] {
     sum = 0, count = 0;
     each_logit([&](float l) {
@@ -572,36 +669,211 @@ __global__ void __launch_bounds__(kThreads, 4)
       count += l == cut;
     });
   };
-  kept_here();
-  if (p < 1.f) {
-    mass = sum;
-    uint32_t tied = count;
-    team.add(mass, tied);
-    ties = min(ties, tied);
-    const u64 each = weight(cut, sh.powers);
-    const u64 want = scaled(p, mass + ties * each, true);  // the mass before a kept token is below this
-    if (mass < want) {                             // tokens at the cut are among them
-      ties = (uint32_t)((want - mass + each - 1) / each);
-    } else {
-      u64 above = 0;                               // mass at hi and above
-      hi = end;
-      while (hi - lo > 1) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        const float v = Grid<T>::value(mid), w = hi == end ? INFINITY : Grid<T>::value(hi);
-        u64 some = 0;
-        uint32_t none = 0;
-        each_logit([&](float l) {
-          if (l >= v && l < w) some += weight(l, sh.powers);
-        });
-        team.add(some, none);
-        some += above;
-        if (some >= want) lo = mid;
-        else hi = mid, above = some;
+  const bool cuts = k < a.vocab && !greedy;
+  bool found = !cuts && p >= 1.f;
+  if (!greedy) cut = Grid<T>::value(Grid<T>::up(cut));
+  if (found) kept_here();
+  else if (!greedy) {
+    // A histogram tells near which logits the cuts lie; CTA 0 gets those listed.
+    uint32_t* hist = (uint32_t*)list;
+    static_assert(kBins * 4 <= kList * 8, "the histogram takes the list's place");
+    const Bins bin_of{m, fminf(weight.hi * kPerUnit, FLT_MAX)};
+    for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    each_logit([&](float l) {
+      if (l >= cut) atomicAdd(&hist[bin_of(l)], 1u);
+    });
+    cluster_sync_all();
+    uint32_t rank_in = 0;
+    if (rank == 0) {
+      choose_bins(sh, hist, size, k, cuts, p, rank_in);
+      if (tid < size)
+        store_remote(&sh.note[0], tid, (u64)sh.bin[0] | (u64)sh.bin[1] << 16 | (u64)sh.bin[2] << 32);
+    }
+    cluster_sync_all();
+    const int b1 = (int)(sh.note[0] & 0xFFFF), b2 = (int)(sh.note[0] >> 16 & 0xFFFF), bk = (int)(sh.note[0] >> 32);
+    // exact masses of what lies above and between the listed bins
+    u64 above = 0, between = 0;
+    uint32_t n = 0;
+    each_logit([&](float l) {
+      if (l < cut) return;
+      const int b = bin_of(l);
+      if (b > bk) return;
+      if ((b >= b1 && b <= b2) || b == bk) {
+        ++n;
+      } else {
+        const u64 w = weight(l, sh.powers);
+        if (b < b1) above += w;
+        else between += w;
       }
-      cut = Grid<T>::value(lo);
-      const u64 one = weight(cut, sh.powers);
-      ties = (uint32_t)((want - above + one - 1) / one);
-      kept_here();
+    });
+    const u64 above_here = above, between_here = between;
+    float* values = (float*)list;
+    const int room = 2 * kList / size;
+    uint32_t upto = n;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t r = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += r;
+    }
+    if (lane == 31) sh.warp_count[warp] = upto;
+    __syncthreads();
+    uint32_t at = upto - n, in_cta = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) at += sh.warp_count[w];
+      in_cta += sh.warp_count[w];
+    }
+    if (in_cta <= (uint32_t)room && n) {           // (in any order: equal logits are told apart later)
+      at += rank * room;
+      each_logit([&](float l) {
+        if (l < cut) return;
+        const int b = bin_of(l);
+        if ((b >= b1 && b <= b2) || b == bk) store_remote(&values[at++], 0, l);
+      });
+    }
+    __syncthreads();                               // warp_count is read
+    uint32_t none = 0;
+    team.add_cta(above, none);
+    __syncthreads();
+    team.add_cta(between, none);
+    team.exchange(above, in_cta);
+    bool all = true;
+    above = 0;
+    for (int r = 0; r < size; ++r) {
+      all = all && sh.count[team.turn][r] <= (u64)room;
+      above += sh.sum[team.turn][r];
+    }
+    const int last = team.turn;                    // how many each CTA listed
+    team.exchange(between, 0);
+    between = 0;
+    for (int r = 0; r < size; ++r) between += sh.sum[team.turn][r];
+    if (all) {
+      if (rank == 0) {
+        // f(logit) over the listed ones
+        const auto each_listed = [&](auto f) {
+          for (int r = 0; r < size; ++r)
+            for (int i = tid; i < (int)sh.count[last][r]; i += kThreads) f(values[r * room + i]);
+        };
+        uint32_t least_key = 0xFFFFFFFFu, most_key = 0, k_least = 0xFFFFFFFFu, k_most = 0;
+        each_listed([&](float l) {
+          const int b = bin_of(l);
+          const uint32_t g = Grid<T>::up(l);
+          if (b >= b1 && b <= b2) least_key = min(least_key, g), most_key = max(most_key, g);
+          if (b == bk) k_least = min(k_least, g), k_most = max(k_most, g);
+        });
+        const auto block_min = [&](uint32_t v) {
+          v = __reduce_min_sync(0xFFFFFFFFu, v);
+          __syncthreads();
+          if (lane == 0) sh.warp_count[warp] = v;
+          __syncthreads();
+          for (int w = 0; w < kWarps; ++w) v = min(v, sh.warp_count[w]);
+          return v;
+        };
+        least_key = block_min(least_key), most_key = ~block_min(~most_key);
+        k_least = block_min(k_least), k_most = ~block_min(~k_most);
+        float at_cut = Grid<T>::value(Grid<T>::up(cut) - 1);  // without a cut: below all of them
+        uint32_t tied = 0;
+        bool right = true;
+        if (bk < kBins) {                          // the rank_in-th of its bin
+          uint32_t over = 0;
+          at_cut = bisect<T>(k_least, k_most + 1, rank_in, over, [&](float v, float w) {
+            uint32_t n = 0;
+            u64 none = 0;
+            each_listed([&](float l) { n += l >= v && l < w && bin_of(l) == bk; });
+            __syncthreads();
+            team.add_cta(none, n);
+            return n;
+          });
+          tied = rank_in - over;
+        }
+        if (p < 1.f) {
+          u64 some = 0;
+          uint32_t none = 0;
+          each_listed([&](float l) {
+            if (bk == kBins || l > at_cut) some += weight(l, sh.powers);
+          });
+          __syncthreads();
+          team.add_cta(some, none);
+          some += above + between;                 // mass above the cut so far
+          const u64 each = weight(at_cut, sh.powers), want = scaled(p, some + tied * each, true);
+          if (some < want) {
+            tied = (uint32_t)((want - some + each - 1) / each);
+          } else {
+            u64 over = above;
+            const auto mass_of = [&](float v, float w) {
+              u64 some = 0;
+              uint32_t none = 0;
+              each_listed([&](float l) {
+                if (l >= v && l < w && bin_of(l) <= b2) some += weight(l, sh.powers);
+              });
+              __syncthreads();
+              team.add_cta(some, none);
+              return some;
+            };
+            right = above < want && above + mass_of(-FLT_MAX, INFINITY) >= want;
+            if (right) {
+              at_cut = bisect<T>(least_key, most_key + 1, want, over, mass_of);
+              const u64 one = weight(at_cut, sh.powers);
+              tied = (uint32_t)((want - over + one - 1) / one);
+            }
+          }
+        }
+        if (tid < size) store_remote(&sh.note[1], tid, right ? (u64)__float_as_uint(at_cut) << 32 | tied : ~0ull);
+      }
+      cluster_sync_all();
+      found = sh.note[1] != ~0ull;
+      if (found) {
+        cut = __uint_as_float((uint32_t)(sh.note[1] >> 32));
+        ties = (uint32_t)sh.note[1];
+        sum = above_here + (bin_of(cut) > b2 ? between_here : 0);
+        each_logit([&](float l) {
+          if (l < cut) return;
+          const int b = bin_of(l);
+          if (l > cut && ((b >= b1 && b <= b2) || b == bk)) sum += weight(l, sh.powers);
+          count += l == cut;
+        });
+      }
+    }
+  }
+  if (!found) {
+    // Too many near a cut (equal logits, say): bisection over all of them.
+    const auto count_of = [&](float v, float w) {
+      uint32_t n = 0;
+      u64 none = 0;
+      each_logit([&](float l) { n += l >= v && l < w; });
+      team.add(none, n);
+      return n;
+    };
+    const uint32_t end = Grid<T>::up(m) + 1;
+    if (cuts && count_of(cut, INFINITY) > (uint32_t)k) {
+      uint32_t over = 0;
+      cut = bisect<T>(Grid<T>::up(cut), end, (uint32_t)k, over, count_of);
+      ties = k - over;
+    }
+    kept_here();
+    if (p < 1.f) {
+      u64 mass = sum;
+      uint32_t tied = count;
+      team.add(mass, tied);
+      ties = min(ties, tied);
+      const u64 each = weight(cut, sh.powers);
+      const u64 want = scaled(p, mass + ties * each, true);  // the mass before a kept token is below this
+      if (mass < want) {                           // tokens at the cut are among them
+        ties = (uint32_t)((want - mass + each - 1) / each);
+      } else {
+        u64 over = 0;
+        cut = bisect<T>(Grid<T>::up(cut), end, want, over, [&](float v, float w) {
+          u64 some = 0;
+          uint32_t none = 0;
+          each_logit([&](float l) {
+            if (l >= v && l < w) some += weight(l, sh.powers);
+          });
+          team.add(some, none);
+          return some;
+        });
+        const u64 one = weight(cut, sh.powers);
+        ties = (uint32_t)((want - over + one - 1) / one);
+        kept_here();
+      }
     }
   }
   // what each warp keeps, in the order of the tokens
