@@ -589,11 +589,11 @@ int dsa_rope_apply(const dsa_rope *p, int64_t n_tok, const int32_t *pos, const d
  *          request; row r has those of index[r] ([rows] int32), of r without
  *          an index (requests == rows then)
  *   token [rows] int32, prob [rows] fp32 or NULL
- * A row whose numbers are out of range (u outside [0, 1), temperature or top_k
- * below 0, top_p outside (0, 1], min_p outside [0, 1], a NaN, an index) gives
+ * A row whose numbers are out of range (u outside [0, 1), temperature below 0 or
+ * above 2^100, top_k below 0, top_p outside (0, 1], min_p outside [0, 1], a NaN, an index) gives
  * token -1, prob 0 and DSA_ERR_INDEX; what its request does not use is not
  * looked at (a NULL array, and with temperature 0 all but the temperature).
- * Weights are good to 2^-30 of themselves, sums are integers in units of 2^-44
+ * Weights are good to 2^-29 of themselves, sums are integers in units of 2^-44
  * of the largest weight or finer: a row gives the same bits wherever it lies,
  * and a token lighter than a unit is never drawn.
  * vocab <= 2^18.  Outputs must not overlap inputs.

@@ -35,7 +35,7 @@ constexpr int kSmallK = 1024;                      // top_k up to which candidat
 typedef unsigned long long u64;
 
 struct Args {
-  int rows, vocab, requests, unit;                 // weights in units of 2^-unit
+  int rows, vocab, requests, bits;                 // vocab <= 2^bits
   long long ld;
   const float *u, *temperature, *top_p, *min_p;
   const int32_t *top_k, *index;
@@ -43,22 +43,22 @@ struct Args {
   float* prob;
 };
 
-// 2^31 * 2^(j / 256)
+// 2^30 * 2^(j / 1024)
 struct Powers {
-  uint32_t at[256];
+  uint32_t at[1024];
   constexpr Powers() : at() {
-    for (int j = 0; j < 256; ++j) {
-      const double x = j / 256.0 * 0.69314718055994530942;
+    for (int j = 0; j < 1024; ++j) {
+      const double x = j / 1024.0 * 0.69314718055994530942;
       double term = 1, sum = 1;
-      for (int k = 1; k < 24; ++k) {
+      for (int k = 1; k < 20; ++k) {
         term *= x / k;
         sum += term;
       }
-      at[j] = (uint32_t)(sum * 2147483648.0 + 0.5);
+      at[j] = (uint32_t)(sum * 1073741824.0 + 0.5);
     }
   }
 };
-__device__ const Powers kPowers{};
+__device__ __align__(16) const Powers kPowers{};
 
 __device__ __forceinline__ void store_remote(u64* local, uint32_t rank, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_u32(local), rank)), "l"(v) : "memory");
@@ -88,25 +88,65 @@ struct Grid<__nv_bfloat16> {
   }
 };
 
-// w = 2^-x in units of 2^-unit, x = (max - l) * log2(e) / temperature
+// two floats in one register pair
+__device__ __forceinline__ u64 pair(float lo, float hi) {
+  u64 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void halves(u64 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// w = 2^-x as a whole number of units, x = (max - l) * log2(e) / temperature.  Two logits
+// at once: max - l = d + e and d * scale = x + f without error, -x = q + r with q a
+// multiple of 2^-10, 2^q from the table and 2^r by a series.  Off by 2^-29 of itself
+// (the table by half a step of 2^-30, the product below by one) and the last unit.
 struct Weight {
   float max, hi, lo;                               // log2(e) / temperature in two floats
-  int unit;
+  int shift;                                       // the largest weight is 2^(62 - shift) units
+
+  __device__ __forceinline__ u64 of(float nx, float y, float z, const uint32_t* __restrict__ powers) const {
+    const uint32_t b = __float_as_uint(y);
+    // (what is further down, the exponent of 2 out of reach, weighs nothing)
+    const uint32_t p = nx > (float)shift - 62.5f ? powers[b & 1023u] : 0u;
+    const int s = (int)(__float_as_uint(z) - __float_as_uint(kZ) + 1u);
+    return ((u64)(p + (uint32_t)__mulhi((int)p, s)) << 32) >> (((shift << 10) + 1023 + __float_as_uint(kY) - b) >> 10 & 63u);
+  }
+  static constexpr float kY = 12288.f;             // 1.5 * 2^13: steps of 2^-10
+  static constexpr float kZ = 0.0029296875f;       // 1.5 * 2^-9: steps of 2^-32
+  static constexpr float kLn2 = 0.693147181f, kHalfLn2Sq = 0.240226507f;
+  __device__ __forceinline__ void two(float l0, float l1, u64& w0, u64& w1, const uint32_t* __restrict__ powers) const {
+    const u64 m = pair(max, max), nm = pair(-max, -max), h = pair(hi, hi), nh = pair(-hi, -hi), one = pair(-1.f, -1.f);
+    const u64 nl = pair(-l0, -l1);
+    const u64 d = add2(m, nl), t = add2(d, nm);
+    const u64 e = add2(fma2(fma2(t, one, d), one, m), fma2(t, one, nl));
+    const u64 nx = mul2(d, nh);
+    const u64 f = fma2(d, pair(lo, lo), fma2(e, h, fma2(d, h, nx)));
+    const u64 y = add2(nx, pair(kY, kY)), q = add2(y, pair(-kY, -kY));
+    const u64 r = fma2(f, one, fma2(q, one, nx));
+    const u64 z = fma2(r, fma2(r, pair(kHalfLn2Sq, kHalfLn2Sq), pair(kLn2, kLn2)), pair(kZ, kZ));
+    float n0, n1, y0, y1, z0, z1;
+    halves(nx, n0, n1), halves(y, y0, y1), halves(z, z0, z1);
+    w0 = of(n0, y0, z0, powers), w1 = of(n1, y1, z1, powers);
+  }
   __device__ __forceinline__ u64 operator()(float l, const uint32_t* __restrict__ powers) const {
-    const float d = __fsub_rn(max, l), t = __fsub_rn(d, max);
-    const float e = __fadd_rn(__fsub_rn(max, __fsub_rn(d, t)), -__fadd_rn(l, t));  // max - l = d + e
-    const float x = __fmul_rn(d, hi);
-    if (!(x < 62.f)) return 0;
-    const float y = __fmaf_rn(d, lo, __fmaf_rn(e, hi, __fmaf_rn(d, hi, -x)));
-    const float n = rintf(x);
-    const u64 z = -(((u64)(int64_t)n << 32) + (int64_t)__float2int_rn((x - n) * 4294967296.f) +
-                    (int64_t)__float2int_rn(y * 4294967296.f));               // -x, 32 bits behind the point
-    const int k = (int)((int64_t)z >> 32);
-    const uint32_t f = (uint32_t)z, p = powers[f >> 24];
-    const float r = (float)(f & 0xFFFFFFu) * (0.69314718056f / 4294967296.f);
-    const float s = r * __fmaf_rn(r, __fmaf_rn(r, 1.f / 6, 0.5f), 1.f);        // e^r - 1 < 2^-8
-    const u64 w = (u64)(p + __float2uint_rn((float)p * s)) << (unit - 31);
-    return k > 0 ? w : w >> -k;
+    u64 a, b;
+    two(l, l, a, b, powers);
+    return a;
   }
 };
 
@@ -136,8 +176,8 @@ __device__ __forceinline__ uint32_t cluster_nctarank() {
   return r;
 }
 
-struct Shared {
-  uint32_t powers[256];
+struct __align__(16) Shared {
+  uint32_t powers[1024];
   double far;                                      // how far below the largest logit min-p goes
   u64 warp_sum[kWarps];
   uint32_t warp_count[kWarps];
@@ -484,13 +524,14 @@ __global__ void __launch_bounds__(kThreads, 4)
   cluster_arrive();                                // no CTA writes to one that has not begun
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int size = (int)cluster_nctarank(), rank = (int)cluster_ctarank(), row = blockIdx.x / size;
-  for (int i = tid; i < 256; i += kThreads) sh.powers[i] = kPowers.at[i];
+  static_assert(kThreads == 256, "four powers per thread");
+  reinterpret_cast<uint4*>(sh.powers)[tid] = reinterpret_cast<const uint4*>(kPowers.at)[tid];
   wait_for_earlier();
   // the request's settings
   const int q = a.index ? a.index[row] : row;
   bool ok = q >= 0 && q < a.requests;
   const float temp = ok && a.temperature ? a.temperature[q] : 1.f;
-  ok = ok && temp >= 0.f && temp <= FLT_MAX;
+  ok = ok && temp >= 0.f && temp <= 0x1p100f;
   const bool greedy = temp == 0.f, draws = ok && !greedy;
   const float p = draws && a.top_p ? a.top_p[q] : 1.f, least = draws && a.min_p ? a.min_p[q] : 0.f;
   const float u = draws ? a.u[row] : 0.f;
@@ -575,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     return;
   }
   // kept: logits above `cut`, and of those equal to it the first `ties`; first what min-p keeps
-  Weight weight{m, 0.f, 0.f, a.unit};
+  Weight weight{m, 0.f, 0.f, a.bits};
   if (draws) {
     // (no fp64: its units are few)
     constexpr float kHi = 1.44269502162933349609375f, kLo = 1.9259629911e-8f;
@@ -664,10 +705,18 @@ __global__ void __launch_bounds__(kThreads, 4)
   uint32_t count = 0, ties = greedy ? 1u : 0x7FFFFFFFu;  // and those equal to it
   const auto kept_here = [&] {
     sum = 0, count = 0;
-    each_logit([&](float l) {
-      if (l > cut) sum += weight(l, sh.powers);
-      count += l == cut;
-    });
+    for (int s = 0; s < steps; ++s) {
+      Run<T> run;
+      run.load(x + s * 32 * kVec);
+#pragma unroll
+      for (int j = 0; j < kVec; j += 2) {
+        u64 w0, w1;
+        weight.two(run.get(j), run.get(j + 1), w0, w1, sh.powers);
+        sum += run.get(j) > cut ? w0 : 0;
+        sum += run.get(j + 1) > cut ? w1 : 0;
+        count += (run.get(j) == cut) + (run.get(j + 1) == cut);
+      }
+    }
   };
   const bool cuts = k < a.vocab && !greedy;
   bool found = !cuts && p >= 1.f;
@@ -1001,7 +1050,7 @@ extern "C" int dsa_sample(const dsa_sampler* p, const void* logits, const float*
   if (!ext_dev_ctx(&c)) return DSA_ERR_CUDA;
   int bits = 0;
   while ((1ll << bits) < p->vocab) ++bits;
-  const Args a{(int)p->rows, (int)p->vocab, (int)p->requests, 62 - bits, p->ld, u, temperature, top_p, min_p,
+  const Args a{(int)p->rows, (int)p->vocab, (int)p->requests, bits, p->ld, u, temperature, top_p, min_p,
                top_k, index, token, prob};
   const bool ok = p->dtype == DSA_BF16 ? launch<__nv_bfloat16>(a, logits, c, (cudaStream_t)stream)
                                        : launch<float>(a, logits, c, (cudaStream_t)stream);
