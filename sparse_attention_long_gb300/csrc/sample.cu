@@ -88,6 +88,13 @@ struct Grid<__nv_bfloat16> {
   }
 };
 
+// the largest value of the type below x (-0 has a number of its own, but is no other value than 0)
+template <typename T>
+__device__ __forceinline__ float next_below(float x) {
+  const uint32_t k = Grid<T>::up(x) - 1;
+  return Grid<T>::value(k == Grid<T>::up(0.f) - 1 ? k - 1 : k);
+}
+
 // two floats in one register pair
 __device__ __forceinline__ u64 pair(float lo, float hi) {
   u64 d;
@@ -119,19 +126,22 @@ struct Weight {
   float max, hi, lo;                               // log2(e) / temperature in two floats
   int shift;                                       // the largest weight is 2^(62 - shift) units
 
-  __device__ __forceinline__ u64 of(float nx, float y, float z, const uint32_t* __restrict__ powers) const {
-    const uint32_t b = __float_as_uint(y);
+  __device__ __forceinline__ u64 of(bool counts, float nx, uint32_t y, float z, const uint32_t* __restrict__ powers) const {
     // (what is further down, the exponent of 2 out of reach, weighs nothing)
-    const uint32_t p = nx > (float)shift - 62.5f ? powers[b & 1023u] : 0u;
+    const uint32_t p = counts && nx > (float)shift - 62.5f ? powers[y & 1023u] : 0u;
     const int s = (int)(__float_as_uint(z) - __float_as_uint(kZ) + 1u);
-    return ((u64)(p + (uint32_t)__mulhi((int)p, s)) << 32) >> (((shift << 10) + 1023 + __float_as_uint(kY) - b) >> 10 & 63u);
+    uint32_t w;
+    asm("mad.hi.s32 %0, %1, %2, %1;" : "=r"(w) : "r"(p), "r"(s));
+    return ((u64)w << 32) >> (((shift << 10) + 1023 + __float_as_uint(kY) - y) >> 10 & 63u);
   }
   static constexpr float kY = 12288.f;             // 1.5 * 2^13: steps of 2^-10
   static constexpr float kZ = 0.0029296875f;       // 1.5 * 2^-9: steps of 2^-32
   static constexpr float kLn2 = 0.693147181f, kHalfLn2Sq = 0.240226507f;
-  __device__ __forceinline__ void two(float l0, float l1, u64& w0, u64& w1, const uint32_t* __restrict__ powers) const {
+  // -l0, -l1 and whether they count; y0, y1: bits of the step numbers, see Bins
+  __device__ __forceinline__ void two(float l0, float l1, bool counts0, bool counts1, u64& w0, u64& w1, uint32_t& y0,
+                                      uint32_t& y1, const uint32_t* __restrict__ powers) const {
     const u64 m = pair(max, max), nm = pair(-max, -max), h = pair(hi, hi), nh = pair(-hi, -hi), one = pair(-1.f, -1.f);
-    const u64 nl = pair(-l0, -l1);
+    const u64 nl = pair(l0, l1);
     const u64 d = add2(m, nl), t = add2(d, nm);
     const u64 e = add2(fma2(fma2(t, one, d), one, m), fma2(t, one, nl));
     const u64 nx = mul2(d, nh);
@@ -139,13 +149,15 @@ struct Weight {
     const u64 y = add2(nx, pair(kY, kY)), q = add2(y, pair(-kY, -kY));
     const u64 r = fma2(f, one, fma2(q, one, nx));
     const u64 z = fma2(r, fma2(r, pair(kHalfLn2Sq, kHalfLn2Sq), pair(kLn2, kLn2)), pair(kZ, kZ));
-    float n0, n1, y0, y1, z0, z1;
-    halves(nx, n0, n1), halves(y, y0, y1), halves(z, z0, z1);
-    w0 = of(n0, y0, z0, powers), w1 = of(n1, y1, z1, powers);
+    float n0, n1, a0, a1, z0, z1;
+    halves(nx, n0, n1), halves(y, a0, a1), halves(z, z0, z1);
+    w0 = of(counts0, n0, __float_as_uint(a0), z0, powers), w1 = of(counts1, n1, __float_as_uint(a1), z1, powers);
+    y0 = __float_as_uint(a0), y1 = __float_as_uint(a1);
   }
   __device__ __forceinline__ u64 operator()(float l, const uint32_t* __restrict__ powers) const {
     u64 a, b;
-    two(l, l, a, b, powers);
+    uint32_t y;
+    two(-l, -l, true, false, a, b, y, y, powers);
     return a;
   }
 };
@@ -259,6 +271,7 @@ struct Run<float> {
     for (int j = 0; j < 8; ++j) w[j] = j < n ? __float_as_uint(p[j]) : kNone;
   }
   __device__ __forceinline__ float get(int j) const { return __uint_as_float(w[j]); }
+  __device__ __forceinline__ void get_negative(int j, float& a, float& b) const { a = -get(j), b = -get(j + 1); }
   // infinities and NaN become -inf; returns the largest
   __device__ __forceinline__ float clean() {
     float m = -INFINITY;
@@ -296,6 +309,10 @@ struct Run<__nv_bfloat16> {
   }
   __device__ __forceinline__ float get(int j) const {
     return __uint_as_float((j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+  }
+  __device__ __forceinline__ void get_negative(int j, float& a, float& b) const {
+    const uint32_t v = w[j >> 1] ^ 0x80008000u;
+    a = __uint_as_float(v << 16), b = __uint_as_float(v & 0xFFFF0000u);
   }
   static __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
     uint32_t r;
@@ -345,17 +362,13 @@ __device__ __forceinline__ float bisect(uint32_t lo, uint32_t hi, S want, S& abo
   return Grid<T>::value(lo);
 }
 
-// A CTA's histogram: bin b holds logits whose distance to the largest is b / 128 powers of
-// two, to the nearest; the last one also what lies further down.
+// A CTA's histogram: bin b holds logits whose distance to the largest is b / 128 to
+// (b + 1) / 128 powers of two; the last one also what lies further down.
 constexpr int kBins = 4096;
 constexpr float kPerUnit = 128.f;
-struct Bins {
-  float max, scale;
-  __device__ __forceinline__ int operator()(float l) const {
-    const float v = fminf(__fmul_rn(__fsub_rn(max, l), scale), (float)(kBins - 1));
-    return (int)(__float_as_uint(__fadd_rn(v, 8388608.f)) - 0x4B000000u);
-  }
-};
+__device__ __forceinline__ int bin_at(uint32_t y) {  // (y's bits fall with the distance, past a change of sign too)
+  return (int)min((__float_as_uint(Weight::kY) - y) >> 3, (uint32_t)(kBins - 1));
+}
 
 // CTA 0's choice of bins from the cluster's histograms (hist of each CTA).  bin[2]: where
 // the k-th logit lies (kBins: none does), `rank_in` of its bin's tokens are kept; bin[0]
@@ -377,7 +390,7 @@ __device__ __forceinline__ void choose_bins(Shared& s, const uint32_t* __restric
   if (tid == 0) s.bin[2] = kBins;
   uint32_t count = 0;
   float mass = 0;
-  const auto weight = [&](int i) { return n[i] * exp2f(-(float)(tid * kMine + i) / kPerUnit); };
+  const auto weight = [&](int i) { return n[i] * exp2f(-((float)(tid * kMine + i) + 0.5f) / kPerUnit); };
 #pragma unroll
   for (int i = 0; i < kMine; ++i) count += n[i], mass += weight(i);
   uint32_t c_run = count;
@@ -710,23 +723,28 @@ __global__ void __launch_bounds__(kThreads, 4)
       run.load(x + s * 32 * kVec);
 #pragma unroll
       for (int j = 0; j < kVec; j += 2) {
+        float l0, l1;
         u64 w0, w1;
-        weight.two(run.get(j), run.get(j + 1), w0, w1, sh.powers);
-        sum += run.get(j) > cut ? w0 : 0;
-        sum += run.get(j + 1) > cut ? w1 : 0;
-        count += (run.get(j) == cut) + (run.get(j + 1) == cut);
+        uint32_t y;
+        run.get_negative(j, l0, l1);
+        weight.two(l0, l1, l0 < -cut, l1 < -cut, w0, w1, y, y, sh.powers);
+        sum += w0 + w1;
       }
     }
+    if (ties)
+      each_logit([&](float l) { count += l == cut; });
   };
   const bool cuts = k < a.vocab && !greedy;
   bool found = !cuts && p >= 1.f;
   if (!greedy) cut = Grid<T>::value(Grid<T>::up(cut));
-  if (found) kept_here();
-  else if (!greedy) {
+  if (found) {                                     // nothing to cut, or the first of the largest
+    if (!greedy) cut = next_below<T>(cut), ties = 0;
+    kept_here();
+  } else {
     // A histogram tells near which logits the cuts lie; CTA 0 gets those listed.
     uint32_t* hist = (uint32_t*)list;
     static_assert(kBins * 4 <= kList * 8, "the histogram takes the list's place");
-    const Bins bin_of{m, fminf(weight.hi * kPerUnit, FLT_MAX)};
+    const auto bin_of = [&](float l) { return bin_at(__float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(m, l), -weight.hi), Weight::kY))); };
     for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     each_logit([&](float l) {
@@ -744,18 +762,28 @@ __global__ void __launch_bounds__(kThreads, 4)
     // exact masses of what lies above and between the listed bins
     u64 above = 0, between = 0;
     uint32_t n = 0;
-    each_logit([&](float l) {
-      if (l < cut) return;
-      const int b = bin_of(l);
-      if (b > bk) return;
-      if ((b >= b1 && b <= b2) || b == bk) {
-        ++n;
-      } else {
-        const u64 w = weight(l, sh.powers);
-        if (b < b1) above += w;
-        else between += w;
+    const uint32_t b_span = (uint32_t)(b2 - b1);
+    for (int s = 0; s < steps; ++s) {
+      Run<T> run;
+      run.load(x + s * 32 * kVec);
+#pragma unroll
+      for (int j = 0; j < kVec; j += 2) {
+        float l[2];
+        u64 w[2];
+        uint32_t y[2];
+        run.get_negative(j, l[0], l[1]);
+        const bool in[2] = {l[0] <= -cut, l[1] <= -cut};
+        weight.two(l[0], l[1], in[0], in[1], w[0], w[1], y[0], y[1], sh.powers);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int b = bin_at(y[i]);
+          const bool listed = (uint32_t)(b - b1) <= b_span || b == bk;
+          n += listed && in[i];
+          if (b < b1) above += w[i];
+          else if (!listed && b < bk) between += w[i];
+        }
       }
-    });
+    }
     const u64 above_here = above, between_here = between;
     float* values = (float*)list;
     const int room = 2 * kList / size;
@@ -819,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 4)
         };
         least_key = block_min(least_key), most_key = ~block_min(~most_key);
         k_least = block_min(k_least), k_most = ~block_min(~k_most);
-        float at_cut = Grid<T>::value(Grid<T>::up(cut) - 1);  // without a cut: below all of them
+        float at_cut = next_below<T>(cut);  // without a cut: below all of them
         uint32_t tied = 0;
         bool right = true;
         if (bk < kBins) {                          // the rank_in-th of its bin
