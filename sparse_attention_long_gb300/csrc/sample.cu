@@ -197,7 +197,7 @@ struct __align__(16) Shared {
   u64 note[2];                                     // of CTA 0 to all
   float warp_mass[kWarps], z;
   int bin[3];
-  uint32_t rank_in;
+  uint32_t rank_in, listed;
 };
 
 // What a CTA sums, and what the cluster does.  An exchange's numbers stay readable until
@@ -370,29 +370,51 @@ __device__ __forceinline__ int bin_at(uint32_t y) {  // (y's bits fall with the 
   return (int)min((__float_as_uint(Weight::kY) - y) >> 3, (uint32_t)(kBins - 1));
 }
 
-// CTA 0's choice of bins from the cluster's histograms (hist of each CTA).  bin[2]: where
-// the k-th logit lies (kBins: none does), `rank_in` of its bin's tokens are kept; bin[0]
-// to bin[1]: where top-p's border lies, by the counts and the weights of the bins' middles.
-// A middle is off by a part in 370 at most, a sum over many bins by much less: 2^-9 to
-// either side, and who has the exact sums looks whether the border lies between.
-__device__ __forceinline__ void choose_bins(Shared& s, const uint32_t* __restrict__ hist, int size, int k, bool cuts,
-                                            float p, uint32_t& rank_in) {
+// The cluster's histograms summed in CTA 0's: each CTA sums a part of the bins.  Between
+// two barriers of the cluster.
+__device__ __forceinline__ void sum_histograms(uint32_t* __restrict__ hist, int rank, int size) {
+  const int part = kBins / size, first = rank * part;
+  for (int i = first + 2 * (int)threadIdx.x; i < first + part; i += 2 * kThreads) {
+    uint32_t x[kMaxCluster] = {}, y[kMaxCluster] = {};
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      if (r >= size) break;
+      asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
+                   : "=r"(x[r]), "=r"(y[r])
+                   : "r"(mapa_shared(smem_u32(hist + i), r))
+                   : "memory");
+    }
+#pragma unroll
+    for (int r = 1; r < kMaxCluster; ++r) x[0] += x[r], y[0] += y[r];
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(mapa_shared(smem_u32(hist + i), 0)), "r"(x[0]), "r"(y[0])
+                 : "memory");
+  }
+}
+
+// CTA 0's choice of bins.  bin[2]: where the k-th logit lies (kBins: none does), rank_in of
+// its bin's tokens are kept; bin[0] to bin[1]: where top-p's border lies, by the counts and
+// the weights of the bins' middles, with a part `margin` of the mass to either side.  Who
+// has the exact sums looks whether the border lies there.
+__device__ __forceinline__ void choose_bins(Shared& s, const uint32_t* __restrict__ hist, int k, bool cuts, float p,
+                                            float margin, uint32_t& rank_in) {
   constexpr int kMine = kBins / kThreads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint32_t n[kMine] = {};
-  for (int r = 0; r < size; ++r)
+  uint32_t n[kMine];
+  float w[kMine];
 #pragma unroll
-    for (int i = 0; i < kMine; i += 4) {
-      const uint4 v = load_remote(hist + tid * kMine + i, r);
-      n[i] += v.x, n[i + 1] += v.y, n[i + 2] += v.z, n[i + 3] += v.w;
-    }
+  for (int i = 0; i < kMine; i += 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(hist + tid * kMine + i);
+    n[i] = v.x, n[i + 1] = v.y, n[i + 2] = v.z, n[i + 3] = v.w;
+  }
   if (tid < 2) s.bin[tid] = kBins - 1;
   if (tid == 0) s.bin[2] = kBins;
   uint32_t count = 0;
   float mass = 0;
-  const auto weight = [&](int i) { return n[i] * exp2f(-((float)(tid * kMine + i) + 0.5f) / kPerUnit); };
 #pragma unroll
-  for (int i = 0; i < kMine; ++i) count += n[i], mass += weight(i);
+  for (int i = 0; i < kMine; ++i) {
+    w[i] = n[i] * exp2f(-((float)(tid * kMine + i) + 0.5f) / kPerUnit);
+    count += n[i], mass += w[i];
+  }
   uint32_t c_run = count;
   float m_run = mass;
   for (int o = 1; o < 32; o <<= 1) {
@@ -406,9 +428,10 @@ __device__ __forceinline__ void choose_bins(Shared& s, const uint32_t* __restric
   c_run -= count, m_run = __shfl_up_sync(0xFFFFFFFFu, m_run, 1);
   if (lane == 0) m_run = 0.f;
   float z = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) c_run += s.warp_count[w], m_run += s.warp_mass[w];
-    z += s.warp_mass[w];
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < warp) c_run += s.warp_count[i], m_run += s.warp_mass[i];
+    z += s.warp_mass[i];
   }
   if (cuts && c_run < (uint32_t)k && (uint32_t)k <= c_run + count) {
     uint32_t c = c_run;
@@ -418,21 +441,21 @@ __device__ __forceinline__ void choose_bins(Shared& s, const uint32_t* __restric
       if (c < (uint32_t)k && (uint32_t)k <= c + n[i]) {
         s.bin[2] = tid * kMine + i;
         s.rank_in = k - c;
-        s.z = a + weight(i) / n[i] * (k - c);
+        s.z = a + w[i] / n[i] * (k - c);
       }
-      c += n[i], a += weight(i);
+      c += n[i], a += w[i];
     }
   }
   __syncthreads();
   rank_in = 0;
   if (s.bin[2] < kBins) rank_in = s.rank_in, z = s.z;
   if (p < 1.f) {
-    const float from = p * z * (1.f - 0x1p-9f), upto = p * z * (1.f + 0x1p-9f);
+    const float from = p * z * (1.f - margin), upto = p * z * (1.f + margin);
     float a = m_run;
     int b1 = kBins - 1, b2 = kBins - 1;
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-      a += weight(i);
+      a += w[i];
       if (a >= from) b1 = min(b1, tid * kMine + i);
       if (a >= upto) b2 = min(b2, tid * kMine + i);
     }
@@ -446,59 +469,103 @@ __device__ __forceinline__ void choose_bins(Shared& s, const uint32_t* __restric
   __syncthreads();
 }
 
+// The masses of a thread's logits from the cut on: of those in bins before b1 and of those
+// between b2 and bk; and the number of the others up to bk.
+struct Masses {
+  u64 above, between;
+  uint32_t listed;
+};
+template <typename T>
+__device__ __forceinline__ Masses mass_around(const T* x, int steps, float cut, const Weight& weight,
+                                              const uint32_t* __restrict__ powers, int b1, int b2, int bk) {
+  Masses a{0, 0, 0};
+  const uint32_t span = (uint32_t)(b2 - b1);
+  for (int s = 0; s < steps; ++s) {
+    Run<T> run;
+    run.load(x + s * 32 * kVec);
+#pragma unroll
+    for (int j = 0; j < kVec; j += 2) {
+      float l[2];
+      u64 w[2];
+      uint32_t y[2];
+      run.get_negative(j, l[0], l[1]);
+      const bool in[2] = {l[0] <= -cut, l[1] <= -cut};
+      weight.two(l[0], l[1], in[0], in[1], w[0], w[1], y[0], y[1], powers);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int b = bin_at(y[i]);
+        const bool listed = (uint32_t)(b - b1) <= span || b == bk;
+        a.listed += listed && in[i];
+        if (b < b1) a.above += w[i];
+        else if (!listed && b < bk) a.between += w[i];
+      }
+    }
+  }
+  return a;
+}
+
 // larger logit first, then lower index
 __device__ __forceinline__ u64 make_key(float l, uint32_t idx) {
   return ((u64)ordered_key(l) << 32) | (0xFFFFFFFFu - idx);
 }
 __device__ __forceinline__ float key_logit(u64 k) { return ordered_value((uint32_t)(k >> 32)); }
 
-// The end for n listed tokens, by one CTA: list[] in index order, sorted[] room for as
-// many (kList).  k: how many are kept at most; want(mass of these): as in top-p.
-__device__ __forceinline__ void finish(const Args& a, Team& team, const Weight& weight, const u64* __restrict__ list,
-                                       u64* __restrict__ sorted, int n, int k, float p, float u, int row) {
-  const Shared& s = team.s;
-  const int tid = threadIdx.x;
-  const int kk = min(n, k);
-  u64 least = 0;                                   // the last key that is kept
-  u64 total = 0;
-  if (kk < n || p < 1.f) {
-    if (n <= kCounted) {
-      // every key's place is the number of larger ones
-      if (tid < n) {
-        const u64 mine = list[tid];
-        int place = 0;
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) place += list[j] > mine;
-        sorted[place] = mine;
+// the m (2^n) keys at v in descending order of key & mask
+__device__ __forceinline__ void sort_down(u64* __restrict__ v, int m, u64 mask) {
+  for (int size = 2; size <= m; size *= 2)
+    for (int step = size / 2; step; step /= 2) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < m / 2; i += kThreads) {
+        const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
+        const u64 x = v[lo], y = v[hi];
+        if (((x & mask) < (y & mask)) == ((lo & size) == 0)) v[lo] = y, v[hi] = x;
       }
-      __syncthreads();
-    } else {
-      int m = kCounted;
-      while (m < n) m *= 2;
-      for (int i = tid; i < m; i += kThreads) sorted[i] = i < n ? list[i] : 0;
-      for (int size = 2; size <= m; size *= 2)
-        for (int step = size / 2; step; step /= 2) {
-          __syncthreads();
-          for (int i = tid; i < m / 2; i += kThreads) {
-            const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
-            const u64 x = sorted[lo], y = sorted[hi];
-            if ((x < y) == ((lo & size) == 0)) sorted[lo] = y, sorted[hi] = x;
-          }
-        }
-      __syncthreads();
     }
-    // masses in that order, `each` places per thread
-    const int each = (n + kThreads - 1) / kThreads, first = tid * each, behind = min(first + each, kk);
+  __syncthreads();
+}
+
+// The end for n listed tokens, by one CTA: list[] in any order, other[] room for as many
+// (kList).  The first k are kept at most, p as in top-p.
+__device__ __forceinline__ void finish(const Args& a, Team& team, const Weight& weight, u64* __restrict__ list,
+                                       u64* __restrict__ other, int n, int k, float p, float u, int row) {
+  const Shared& s = team.s;
+  const int tid = threadIdx.x, kk = min(n, k);
+  u64 *by_size = other, *by_index = list;
+  int m = kCounted;
+  while (m < n) m *= 2;
+  if (n <= kCounted) {
+    // a key's place is the number of larger ones, by logit and index and by index alone
+    u64 key = 0;
+    int place = 0, at = 0;
+    if (tid < n) {
+      key = list[tid];
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const u64 o = list[j];
+        place += o > key;
+        at += (uint32_t)o > (uint32_t)key;
+      }
+    }
+    __syncthreads();
+    if (tid < n) by_size[place] = key, by_index[at] = key;
+    __syncthreads();
+  } else if (kk < n || p < 1.f) {
+    for (int i = tid; i < m; i += kThreads) by_size[i] = i < n ? list[i] : 0;
+    sort_down(by_size, m, ~0ull);
+  }
+  const int each = (n + kThreads - 1) / kThreads, first = tid * each, behind = min(first + each, n);
+  u64 least = 0;                                   // the last key that is kept
+  if (kk < n || p < 1.f) {
     int kept = kk;
     if (p < 1.f) {
       u64 mine = 0, all;
-      for (int i = first; i < behind; ++i) mine += weight(key_logit(sorted[i]), s.powers);
+      for (int i = first; i < min(behind, kk); ++i) mine += weight(key_logit(by_size[i]), s.powers);
       u64 at = team.before(mine, all);
       const u64 want = scaled(p, all, true);       // the mass before a kept token is below this
       int more = 0;
-      for (int i = first; i < behind; ++i) {
+      for (int i = first; i < min(behind, kk); ++i) {
         more += at < want;
-        at += weight(key_logit(sorted[i]), s.powers);
+        if (each > 1) at += weight(key_logit(by_size[i]), s.powers);
       }
       u64 none = 0;
       uint32_t count = more;
@@ -506,19 +573,22 @@ __device__ __forceinline__ void finish(const Args& a, Team& team, const Weight& 
       team.add_cta(none, count);
       kept = max(1, (int)count);
     }
-    least = sorted[kept - 1];
+    least = by_size[kept - 1];
   }
-  const int each = (n + kThreads - 1) / kThreads, first = tid * each, behind = min(first + each, n);
-  u64 mine = 0;
+  if (n > kCounted) {                              // (low words are the indices' complements)
+    for (int i = n + tid; i < m; i += kThreads) list[i] = 0;
+    sort_down(list, m, 0xFFFFFFFFull);
+  }
+  u64 mine = 0, total;
   for (int i = first; i < behind; ++i)
-    if (list[i] >= least) mine += weight(key_logit(list[i]), s.powers);
+    if (by_index[i] >= least) mine += weight(key_logit(by_index[i]), s.powers);
   u64 at = team.before(mine, total);
   const u64 target = scaled(u, total, false);
   if (at > target || at + mine <= target) return;
   for (int i = first; i < behind; ++i) {
-    const u64 w = list[i] >= least ? weight(key_logit(list[i]), s.powers) : 0;
+    const u64 w = each == 1 ? mine : by_index[i] >= least ? weight(key_logit(by_index[i]), s.powers) : 0;
     if (at <= target && target < at + w) {
-      a.token[row] = (int32_t)(0xFFFFFFFFu - (uint32_t)list[i]);
+      a.token[row] = (int32_t)(0xFFFFFFFFu - (uint32_t)by_index[i]);
       if (a.prob) a.prob[row] = (float)((double)w / (double)total);
     }
     at += w;
@@ -539,20 +609,8 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int size = (int)cluster_nctarank(), rank = (int)cluster_ctarank(), row = blockIdx.x / size;
   static_assert(kThreads == 256, "four powers per thread");
   reinterpret_cast<uint4*>(sh.powers)[tid] = reinterpret_cast<const uint4*>(kPowers.at)[tid];
+  if (tid == 0) sh.listed = 0;
   wait_for_earlier();
-  // the request's settings
-  const int q = a.index ? a.index[row] : row;
-  bool ok = q >= 0 && q < a.requests;
-  const float temp = ok && a.temperature ? a.temperature[q] : 1.f;
-  ok = ok && temp >= 0.f && temp <= 0x1p100f;
-  const bool greedy = temp == 0.f, draws = ok && !greedy;
-  const float p = draws && a.top_p ? a.top_p[q] : 1.f, least = draws && a.min_p ? a.min_p[q] : 0.f;
-  const float u = draws ? a.u[row] : 0.f;
-  int k = draws && a.top_k ? a.top_k[q] : 0;
-  ok = ok && k >= 0 && p > 0.f && p <= 1.f && least >= 0.f && least <= 1.f && u >= 0.f && u < 1.f;
-  if (k == 0 || k > a.vocab) k = a.vocab;
-  if (greedy) k = 1;
-  if (tid == 0 && least > 0.f) sh.far = -log((double)least) * (double)temp;
   // The row's logits of this CTA to shared memory: a warp's together in index order, a
   // thread's in runs of eight.
   const int first = (warp * steps * 32 + lane) * kVec;
@@ -561,6 +619,10 @@ __global__ void __launch_bounds__(kThreads, 4)
   T* x = mine + first;
   float m = -INFINITY;
   constexpr int kAhead = sizeof(T) == 2 ? 8 : 4;   // runs in flight
+  int q = -1;
+  bool ok = false, greedy = false;
+  float temp = 1.f, p = 1.f, least = 0.f, u = 0.f;
+  int k = 0;
   for (int s0 = 0; s0 < steps; s0 += kAhead) {
     Run<T> run[kAhead];
 #pragma unroll
@@ -569,6 +631,20 @@ __global__ void __launch_bounds__(kThreads, 4)
       if (s0 + s >= steps) break;
       if (vec && i + kVec <= there) run[s].load(src + i);
       else run[s].load_some(src + i, there - i);
+    }
+    if (s0 == 0) {                                 // meanwhile the request's settings
+      q = a.index ? a.index[row] : row;
+      ok = q >= 0 && q < a.requests;
+      temp = ok && a.temperature ? a.temperature[q] : 1.f;
+      p = ok && a.top_p ? a.top_p[q] : 1.f, least = ok && a.min_p ? a.min_p[q] : 0.f;
+      u = a.u[row], k = ok && a.top_k ? a.top_k[q] : 0;
+      ok = ok && temp >= 0.f && temp <= 0x1p100f;
+      greedy = temp == 0.f;
+      if (!ok || greedy) p = 1.f, least = 0.f, u = 0.f, k = 0;
+      ok = ok && k >= 0 && p > 0.f && p <= 1.f && least >= 0.f && least <= 1.f && u >= 0.f && u < 1.f;
+      if (k == 0 || k > a.vocab) k = a.vocab;
+      if (greedy) k = 1;
+      if (tid == 0 && least > 0.f) sh.far = -log((double)least) * (double)temp;
     }
 #pragma unroll
     for (int s = 0; s < kAhead; ++s) {
@@ -594,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   if (lane == 0) sh.warp_count[warp] = of_warp;
   __syncthreads();
   uint32_t top = 0;
+#pragma unroll
   for (int w = 0; w < kWarps; ++w) top = max(top, sh.warp_count[w]);
   uint32_t bound = 0;
   const bool small_k = k <= kSmallK && k < a.vocab;
@@ -630,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   }
   // kept: logits above `cut`, and of those equal to it the first `ties`; first what min-p keeps
   Weight weight{m, 0.f, 0.f, a.bits};
-  if (draws) {
+  if (!greedy) {
     // (no fp64: its units are few)
     constexpr float kHi = 1.44269502162933349609375f, kLo = 1.9259629911e-8f;
     weight.hi = __fdiv_rn(kHi, temp);
@@ -638,58 +715,30 @@ __global__ void __launch_bounds__(kThreads, 4)
     if (!(weight.hi < 1e38f)) weight.hi = 1e38f, weight.lo = 0.f;
   }
   float cut = greedy ? m : -FLT_MAX;
-  if (least > 0.f) {
-    cut = fmaxf(__double2float_ru((double)m - sh.far), -FLT_MAX);
-  }
+  if (least > 0.f) cut = fmaxf(__double2float_ru((double)m - sh.far), -FLT_MAX);
   if (small_k || least > 0.f) {
-    // Few tokens can be kept as a rule: CTA 0 gets them listed, in index order.
+    // Few tokens can be kept as a rule: CTA 0 gets them listed.
     const float low = small_k ? fmaxf(cut, fmaxf(ordered_value(bound), -FLT_MAX)) : cut;
-    const int room = kList / size;
-    uint32_t n = 0, with = 0;                      // steps with some (steps <= 32)
+    const uint32_t room = kList / size;
     for (int s = 0; s < steps; ++s) {
       Run<T> run;
       run.load(x + s * 32 * kVec);
-      if (run.largest() >= low) {
-        with |= 1u << s;
+      if (run.largest() < low) continue;
+      uint32_t hits = 0;
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) n += run.get(j) >= low;
+      for (int j = 0; j < kVec; ++j) hits |= (uint32_t)(run.get(j) >= low) << j;
+      uint32_t to = atomicAdd(&sh.listed, __popc(hits));
+      for (; hits && to < room; hits &= hits - 1, ++to) {
+        const int i = s * 32 * kVec + __ffs(hits) - 1;
+        store_remote(&list[rank * room + to], 0, make_key(to_f32(x[i]), (uint32_t)(rank * chunk + first + i)));
       }
     }
-    with = __reduce_or_sync(0xFFFFFFFFu, with);
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    if (lane == 0) sh.warp_count[warp] = n;
     __syncthreads();
-    uint32_t at = 0, in_cta = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) at += sh.warp_count[w];
-      in_cta += sh.warp_count[w];
-    }
-    if (in_cta <= (uint32_t)room)
-      for (; with; with &= with - 1) {
-        const int s = __ffs(with) - 1;
-        Run<T> run;
-        run.load(x + s * 32 * kVec);
-        uint32_t hits = 0;
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) hits |= (uint32_t)(run.get(j) >= low) << j;
-        const uint32_t have = __popc(hits);
-        uint32_t upto = have;
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t r = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-          if (lane >= o) upto += r;
-        }
-        uint32_t to = rank * room + at + upto - have;
-#pragma unroll
-        for (int j = 0; j < kVec; ++j)
-          if (hits >> j & 1)
-            store_remote(&list[to++], 0, make_key(run.get(j), (uint32_t)(rank * chunk + first + s * 32 * kVec + j)));
-        at += __shfl_sync(0xFFFFFFFFu, upto, 31);
-      }
-    team.exchange(0, in_cta);
+    team.exchange(0, sh.listed);
     bool all = true;
     int total = 0;
     for (int r = 0; r < size; ++r) {
-      all = all && sh.count[team.turn][r] <= (u64)room;
+      all = all && sh.count[team.turn][r] <= room;
       total += (int)sh.count[team.turn][r];
     }
     if (all) {
@@ -702,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 4)
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kList / kThreads; ++i) {
-          const int from = tid + i * kThreads, r = from / room, o = from - r * room;
+          const int from = tid + i * kThreads, r = from / (int)room, o = from - r * (int)room;
           int to = o;
           for (int b = 0; b < r; ++b) to += (int)sh.count[team.turn][b];
           if (o < (int)sh.count[team.turn][r]) list[to] = keep[i];
@@ -740,175 +789,150 @@ __global__ void __launch_bounds__(kThreads, 4)
   if (found) {                                     // nothing to cut, or the first of the largest
     if (!greedy) cut = next_below<T>(cut), ties = 0;
     kept_here();
-  } else {
-    // A histogram tells near which logits the cuts lie; CTA 0 gets those listed.
+  }
+  // A histogram tells near which logits the cuts lie; CTA 0 gets those listed.  fp32 logits
+  // are many different ones as a rule, and few lie near a cut; if they do not (bf16 ones
+  // are few different ones), a second time with more room.
+  for (float margin = sizeof(T) == 4 ? 0x1p-13f : 0x1p-9f; !found && margin <= 0x1p-9f; margin *= 16.f) {
     uint32_t* hist = (uint32_t*)list;
     static_assert(kBins * 4 <= kList * 8, "the histogram takes the list's place");
     const auto bin_of = [&](float l) { return bin_at(__float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(m, l), -weight.hi), Weight::kY))); };
+    __syncthreads();
+    if (tid == 0) sh.listed = 0;
     for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     each_logit([&](float l) {
       if (l >= cut) atomicAdd(&hist[bin_of(l)], 1u);
     });
     cluster_sync_all();
+    sum_histograms(hist, rank, size);
+    cluster_sync_all();
     uint32_t rank_in = 0;
     if (rank == 0) {
-      choose_bins(sh, hist, size, k, cuts, p, rank_in);
+      choose_bins(sh, hist, k, cuts, p, margin, rank_in);
       if (tid < size)
         store_remote(&sh.note[0], tid, (u64)sh.bin[0] | (u64)sh.bin[1] << 16 | (u64)sh.bin[2] << 32);
     }
     cluster_sync_all();
     const int b1 = (int)(sh.note[0] & 0xFFFF), b2 = (int)(sh.note[0] >> 16 & 0xFFFF), bk = (int)(sh.note[0] >> 32);
+    const auto is_listed = [&](int b) { return (uint32_t)(b - b1) <= (uint32_t)(b2 - b1) || b == bk; };
     // exact masses of what lies above and between the listed bins
-    u64 above = 0, between = 0;
-    uint32_t n = 0;
-    const uint32_t b_span = (uint32_t)(b2 - b1);
-    for (int s = 0; s < steps; ++s) {
-      Run<T> run;
-      run.load(x + s * 32 * kVec);
-#pragma unroll
-      for (int j = 0; j < kVec; j += 2) {
-        float l[2];
-        u64 w[2];
-        uint32_t y[2];
-        run.get_negative(j, l[0], l[1]);
-        const bool in[2] = {l[0] <= -cut, l[1] <= -cut};
-        weight.two(l[0], l[1], in[0], in[1], w[0], w[1], y[0], y[1], sh.powers);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int b = bin_at(y[i]);
-          const bool listed = (uint32_t)(b - b1) <= b_span || b == bk;
-          n += listed && in[i];
-          if (b < b1) above += w[i];
-          else if (!listed && b < bk) between += w[i];
-        }
-      }
-    }
-    const u64 above_here = above, between_here = between;
+    const Masses masses = mass_around<T>(x, steps, cut, weight, sh.powers, b1, b2, bk);
     float* values = (float*)list;
-    const int room = 2 * kList / size;
-    uint32_t upto = n;
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t r = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-      if (lane >= o) upto += r;
-    }
-    if (lane == 31) sh.warp_count[warp] = upto;
-    __syncthreads();
-    uint32_t at = upto - n, in_cta = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) at += sh.warp_count[w];
-      in_cta += sh.warp_count[w];
-    }
-    if (in_cta <= (uint32_t)room && n) {           // (in any order: equal logits are told apart later)
-      at += rank * room;
+    const uint32_t room = 2 * kList / size;
+    if (masses.listed) {
+      uint32_t to = atomicAdd(&sh.listed, masses.listed);
       each_logit([&](float l) {
-        if (l < cut) return;
-        const int b = bin_of(l);
-        if ((b >= b1 && b <= b2) || b == bk) store_remote(&values[at++], 0, l);
+        if (l >= cut && is_listed(bin_of(l)) && to < room) store_remote(&values[rank * room + to++], 0, l);
       });
     }
-    __syncthreads();                               // warp_count is read
+    u64 above = masses.above, between = masses.between;
     uint32_t none = 0;
+    __syncthreads();
     team.add_cta(above, none);
     __syncthreads();
     team.add_cta(between, none);
-    team.exchange(above, in_cta);
+    team.exchange(above, sh.listed);
     bool all = true;
     above = 0;
     for (int r = 0; r < size; ++r) {
-      all = all && sh.count[team.turn][r] <= (u64)room;
+      all = all && sh.count[team.turn][r] <= room;
       above += sh.sum[team.turn][r];
     }
     const int last = team.turn;                    // how many each CTA listed
     team.exchange(between, 0);
     between = 0;
     for (int r = 0; r < size; ++r) between += sh.sum[team.turn][r];
-    if (all) {
-      if (rank == 0) {
-        // f(logit) over the listed ones
-        const auto each_listed = [&](auto f) {
-          for (int r = 0; r < size; ++r)
-            for (int i = tid; i < (int)sh.count[last][r]; i += kThreads) f(values[r * room + i]);
-        };
-        uint32_t least_key = 0xFFFFFFFFu, most_key = 0, k_least = 0xFFFFFFFFu, k_most = 0;
-        each_listed([&](float l) {
-          const int b = bin_of(l);
-          const uint32_t g = Grid<T>::up(l);
-          if (b >= b1 && b <= b2) least_key = min(least_key, g), most_key = max(most_key, g);
-          if (b == bk) k_least = min(k_least, g), k_most = max(k_most, g);
-        });
-        const auto block_min = [&](uint32_t v) {
-          v = __reduce_min_sync(0xFFFFFFFFu, v);
-          __syncthreads();
-          if (lane == 0) sh.warp_count[warp] = v;
-          __syncthreads();
-          for (int w = 0; w < kWarps; ++w) v = min(v, sh.warp_count[w]);
-          return v;
-        };
-        least_key = block_min(least_key), most_key = ~block_min(~most_key);
-        k_least = block_min(k_least), k_most = ~block_min(~k_most);
-        float at_cut = next_below<T>(cut);  // without a cut: below all of them
-        uint32_t tied = 0;
-        bool right = true;
-        if (bk < kBins) {                          // the rank_in-th of its bin
-          uint32_t over = 0;
-          at_cut = bisect<T>(k_least, k_most + 1, rank_in, over, [&](float v, float w) {
-            uint32_t n = 0;
-            u64 none = 0;
-            each_listed([&](float l) { n += l >= v && l < w && bin_of(l) == bk; });
-            __syncthreads();
-            team.add_cta(none, n);
-            return n;
-          });
-          tied = rank_in - over;
+    if (!all) break;
+    if (rank == 0) {
+      int total = 0;
+      for (int r = 0; r < size; ++r) total += (int)sh.count[last][r];
+      // f(logit) over this thread's part of the listed ones
+      const auto each_listed = [&](auto f) {
+        int r = 0, begin = 0;
+        for (int i = tid; i < total; i += kThreads) {
+          while (i - begin >= (int)sh.count[last][r]) begin += (int)sh.count[last][r++];
+          f(values[r * room + i - begin]);
         }
-        if (p < 1.f) {
-          u64 some = 0;
-          uint32_t none = 0;
-          each_listed([&](float l) {
-            if (bk == kBins || l > at_cut) some += weight(l, sh.powers);
-          });
+      };
+      uint32_t least_key = 0xFFFFFFFFu, most_key = 0, k_least = 0xFFFFFFFFu, k_most = 0;
+      each_listed([&](float l) {
+        const int b = bin_of(l);
+        const uint32_t g = Grid<T>::up(l);
+        if (b >= b1 && b <= b2) least_key = min(least_key, g), most_key = max(most_key, g);
+        if (b == bk) k_least = min(k_least, g), k_most = max(k_most, g);
+      });
+      const auto block_min = [&](uint32_t v) {
+        v = __reduce_min_sync(0xFFFFFFFFu, v);
+        __syncthreads();
+        if (lane == 0) sh.warp_count[warp] = v;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v = min(v, sh.warp_count[w]);
+        return v;
+      };
+      float at_cut = next_below<T>(cut);           // without a cut: below all of them
+      uint32_t tied = 0;
+      bool right = true;
+      if (bk < kBins) {                            // the rank_in-th of its bin
+        uint32_t over = 0;
+        k_least = block_min(k_least), k_most = ~block_min(~k_most);
+        at_cut = bisect<T>(k_least, k_most + 1, rank_in, over, [&](float v, float w) {
+          uint32_t n = 0;
+          u64 none = 0;
+          each_listed([&](float l) { n += l >= v && l < w && bin_of(l) == bk; });
           __syncthreads();
-          team.add_cta(some, none);
-          some += above + between;                 // mass above the cut so far
-          const u64 each = weight(at_cut, sh.powers), want = scaled(p, some + tied * each, true);
-          if (some < want) {
-            tied = (uint32_t)((want - some + each - 1) / each);
-          } else {
-            u64 over = above;
-            const auto mass_of = [&](float v, float w) {
-              u64 some = 0;
-              uint32_t none = 0;
-              each_listed([&](float l) {
-                if (l >= v && l < w && bin_of(l) <= b2) some += weight(l, sh.powers);
-              });
-              __syncthreads();
-              team.add_cta(some, none);
-              return some;
-            };
-            right = above < want && above + mass_of(-FLT_MAX, INFINITY) >= want;
-            if (right) {
-              at_cut = bisect<T>(least_key, most_key + 1, want, over, mass_of);
-              const u64 one = weight(at_cut, sh.powers);
-              tied = (uint32_t)((want - over + one - 1) / one);
-            }
+          team.add_cta(none, n);
+          return n;
+        });
+        tied = rank_in - over;
+      }
+      if (p < 1.f) {
+        u64 some = 0;
+        uint32_t none = 0;
+        each_listed([&](float l) {
+          if (bk == kBins || l > at_cut) some += weight(l, sh.powers);
+        });
+        __syncthreads();
+        team.add_cta(some, none);
+        some += above + between;                   // mass above the cut so far
+        const u64 each = weight(at_cut, sh.powers), want = scaled(p, some + tied * each, true);
+        if (some < want) {
+          tied = (uint32_t)((want - some + each - 1) / each);
+        } else {
+          u64 over = above;
+          const auto mass_of = [&](float v, float w) {
+            u64 some = 0;
+            uint32_t none = 0;
+            each_listed([&](float l) {
+              if (l >= v && l < w && bin_of(l) <= b2) some += weight(l, sh.powers);
+            });
+            __syncthreads();
+            team.add_cta(some, none);
+            return some;
+          };
+          right = above < want && above + mass_of(-FLT_MAX, INFINITY) >= want;
+          if (right) {
+            least_key = block_min(least_key), most_key = ~block_min(~most_key);
+            at_cut = bisect<T>(least_key, most_key + 1, want, over, mass_of);
+            const u64 one = weight(at_cut, sh.powers);
+            tied = (uint32_t)((want - over + one - 1) / one);
           }
         }
-        if (tid < size) store_remote(&sh.note[1], tid, right ? (u64)__float_as_uint(at_cut) << 32 | tied : ~0ull);
       }
-      cluster_sync_all();
-      found = sh.note[1] != ~0ull;
-      if (found) {
-        cut = __uint_as_float((uint32_t)(sh.note[1] >> 32));
-        ties = (uint32_t)sh.note[1];
-        sum = above_here + (bin_of(cut) > b2 ? between_here : 0);
+      if (tid < size) store_remote(&sh.note[1], tid, right ? (u64)__float_as_uint(at_cut) << 32 | tied : ~0ull);
+    }
+    cluster_sync_all();
+    found = sh.note[1] != ~0ull;
+    if (found) {
+      cut = __uint_as_float((uint32_t)(sh.note[1] >> 32));
+      ties = (uint32_t)sh.note[1];
+      sum = masses.above + (bin_of(cut) > b2 ? masses.between : 0);
+      if (masses.listed)
         each_logit([&](float l) {
-          if (l < cut) return;
-          const int b = bin_of(l);
-          if (l > cut && ((b >= b1 && b <= b2) || b == bk)) sum += weight(l, sh.powers);
+          if (l > cut && is_listed(bin_of(l))) sum += weight(l, sh.powers);
           count += l == cut;
         });
-      }
     }
   }
   if (!found) {
@@ -921,6 +945,7 @@ __global__ void __launch_bounds__(kThreads, 4)
       return n;
     };
     const uint32_t end = Grid<T>::up(m) + 1;
+    __syncthreads();
     if (cuts && count_of(cut, INFINITY) > (uint32_t)k) {
       uint32_t over = 0;
       cut = bisect<T>(Grid<T>::up(cut), end, (uint32_t)k, over, count_of);
@@ -961,62 +986,85 @@ __global__ void __launch_bounds__(kThreads, 4)
   __syncthreads();
   u64 cta_sum = 0;
   uint32_t cta_count = 0;
+#pragma unroll
   for (int w = 0; w < kWarps; ++w) cta_sum += sh.warp_sum[w], cta_count += sh.warp_count[w];
   team.exchange(cta_sum, cta_count);
-  u64 total = 0, before = 0;
-  uint32_t tied = 0, tied_before = 0;
+  u64 total = 0, before = 0, kept = 0;
+  uint32_t tied = 0, seen = 0;                     // of all CTAs, and before this one
   // mass of n tokens at the cut when `seen` of them came before
   const auto tie_mass = [&](uint32_t seen, uint32_t n) { return (u64)(min(ties, seen + n) - min(ties, seen)) * each; };
   for (int r = 0; r < size; ++r) {
     const uint32_t n = (uint32_t)sh.count[team.turn][r];
-    const u64 kept = sh.sum[team.turn][r] + tie_mass(tied, n);
-    if (r < rank) before += kept, tied_before += n;
-    total += kept;
+    const u64 some = sh.sum[team.turn][r] + (ties ? tie_mass(tied, n) : 0);
+    if (r < rank) before += some, seen += n;
+    if (r == rank) kept = some;
+    total += some;
     tied += n;
   }
   const u64 target = scaled(u, total, false);
-  for (int w = 0; w < warp; ++w) {
-    const uint32_t n = sh.warp_count[w];
-    before += sh.warp_sum[w] + tie_mass(tied_before, n);
-    tied_before += n;
+  if (before > target || before + kept <= target) return;
+  // The CTA that holds the token: the warp whose tokens reach it, one of its steps per warp,
+  // one of the step's lanes.
+  int who = 0;
+  for (;; ++who) {
+    const u64 some = sh.warp_sum[who] + tie_mass(seen, sh.warp_count[who]);
+    if (who == kWarps - 1 || target < before + some) break;
+    before += some;
+    seen += sh.warp_count[who];
   }
-  if (before > target || before + sum + tie_mass(tied_before, count) <= target) return;
-  // the one warp that holds the token, thread by thread
-  for (int s = 0; s < steps; ++s) {
+  __syncthreads();                                 // warp_sum is read
+  const T* at_x = mine + (who * steps * 32 + lane) * kVec;
+  for (int s0 = 0; s0 < steps; s0 += kWarps) {
+    const int s = s0 + warp;
     Run<T> v;
-    v.load(x + s * 32 * kVec);
-    u64 run = 0;
+    u64 run = 0, own[kVec];
     uint32_t tie_run = 0;
+    if (s < steps) {
+      v.load(at_x + s * 32 * kVec);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      if (v.get(j) > cut) run += weight(v.get(j), sh.powers);
-      tie_run += v.get(j) == cut;
+      for (int j = 0; j < kVec; j += 2) {
+        float l0, l1;
+        uint32_t y;
+        v.get_negative(j, l0, l1);
+        weight.two(l0, l1, l0 < -cut, l1 < -cut, own[j], own[j + 1], y, y, sh.powers);
+        run += own[j] + own[j + 1];
+        tie_run += (v.get(j) == cut) + (v.get(j + 1) == cut);
+      }
     }
-    const u64 own = run;
-    const uint32_t own_ties = tie_run;
+    const u64 mine_run = run;
+    const uint32_t mine_ties = tie_run;
     for (int o = 1; o < 32; o <<= 1) {
       const u64 r = __shfl_up_sync(0xFFFFFFFFu, run, o);
       const uint32_t n = __shfl_up_sync(0xFFFFFFFFu, tie_run, o);
       if (lane >= o) run += r, tie_run += n;
     }
-    uint32_t seen = tied_before + (tie_run - own_ties);
-    u64 at = before + (run - own) + tie_mass(tied_before, tie_run - own_ties);
+    if (lane == 31) sh.warp_sum[warp] = run, sh.warp_count[warp] = tie_run;
+    __syncthreads();
+    u64 at = before;
+    uint32_t at_ties = seen;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      const float l = v.get(j);
-      u64 w = 0;
-      if (l > cut) w = weight(l, sh.powers);
-      else if (l == cut && seen++ < ties) w = each;
-      if (at <= target && target < at + w) {
-        a.token[row] = rank * chunk + first + s * 32 * kVec + j;
-        if (a.prob) a.prob[row] = (float)((double)w / (double)total);
-      }
-      at += w;
+    for (int w = 0; w < kWarps; ++w) {
+      const u64 some = sh.warp_sum[w] + tie_mass(seen, sh.warp_count[w]);
+      before += some;
+      seen += sh.warp_count[w];
+      if (w < warp) at += some, at_ties = seen;
     }
-    run = __shfl_sync(0xFFFFFFFFu, run, 31);
-    tie_run = __shfl_sync(0xFFFFFFFFu, tie_run, 31);
-    before += run + tie_mass(tied_before, tie_run);
-    tied_before += tie_run;
+    if (s < steps) {
+      at += run - mine_run + tie_mass(at_ties, tie_run - mine_ties);
+      at_ties += tie_run - mine_ties;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const bool tie = v.get(j) == cut;
+        const u64 w = tie ? (at_ties < ties ? each : 0) : own[j];
+        at_ties += tie;
+        if (at <= target && target < at + w) {
+          a.token[row] = rank * chunk + (who * steps * 32 + s * 32 + lane) * kVec + j;
+          if (a.prob) a.prob[row] = (float)((double)w / (double)total);
+        }
+        at += w;
+      }
+    }
+    __syncthreads();
   }
 }
 
