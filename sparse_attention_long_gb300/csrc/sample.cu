@@ -194,6 +194,7 @@ struct __align__(16) Shared {
   u64 warp_sum[kWarps];
   uint32_t warp_count[kWarps];
   u64 sum[2][kMaxCluster], count[2][kMaxCluster];  // of every CTA of the cluster, two exchanges deep
+  u64 scan_sum[kWarps];
   u64 note[2];                                     // of CTA 0 to all
   float warp_mass[kWarps], z;
   int bin[3];
@@ -229,25 +230,6 @@ struct Team {
     exchange(sum, count);
     sum = 0, count = 0;
     for (int r = 0; r < size; ++r) sum += s.sum[turn][r], count += (uint32_t)s.count[turn][r];
-  }
-  // the sum of the threads before this one, and of all
-  __device__ __forceinline__ u64 before(u64 v, u64& all) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    u64 run = v;
-    for (int o = 1; o < 32; o <<= 1) {
-      const u64 r = __shfl_up_sync(0xFFFFFFFFu, run, o);
-      if (lane >= o) run += r;
-    }
-    __syncthreads();
-    if (lane == 31) s.warp_sum[warp] = run;
-    __syncthreads();
-    u64 at = run - v;
-    all = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) at += s.warp_sum[w];
-      all += s.warp_sum[w];
-    }
-    return at;
   }
 };
 
@@ -525,74 +507,167 @@ __device__ __forceinline__ void sort_down(u64* __restrict__ v, int m, u64 mask) 
 }
 
 // The end for n listed tokens, by one CTA: list[] in any order, other[] room for as many
-// (kList).  The first k are kept at most, p as in top-p.
-__device__ __forceinline__ void finish(const Args& a, Team& team, const Weight& weight, u64* __restrict__ list,
+// (kList).  The first k are kept at most, p as in top-p.  A scan's sums go by turns to
+// two places, so that one barrier is enough.
+__device__ __forceinline__ u64 scan(u64 v, u64* __restrict__ sums, u64& all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  u64 run = v;
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 r = __shfl_up_sync(0xFFFFFFFFu, run, o);
+    if (lane >= o) run += r;
+  }
+  if (lane == 31) sums[warp] = run;
+  __syncthreads();
+  u64 at = run - v;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const u64 x = sums[w];
+    if (w < warp) at += x;
+    all += x;
+  }
+  return at;
+}
+__device__ __forceinline__ void finish(const Args& a, Shared& s, const Weight& weight, u64* __restrict__ list,
                                        u64* __restrict__ other, int n, int k, float p, float u, int row) {
-  const Shared& s = team.s;
   const int tid = threadIdx.x, kk = min(n, k);
-  u64 *by_size = other, *by_index = list;
-  int m = kCounted;
-  while (m < n) m *= 2;
   if (n <= kCounted) {
-    // a key's place is the number of larger ones, by logit and index and by index alone
-    u64 key = 0;
-    int place = 0, at = 0;
+    // A token's place is the number of larger ones, by logit and index and by index alone.
+    u64 key = 0, w = 0;
+    int place = 0, at_index = 0;
     if (tid < n) {
       key = list[tid];
 #pragma unroll 4
       for (int j = 0; j < n; ++j) {
         const u64 o = list[j];
         place += o > key;
-        at += (uint32_t)o > (uint32_t)key;
+        at_index += (uint32_t)o > (uint32_t)key;
       }
+      w = weight(key_logit(key), s.powers);
+      other[place] = w;
+    }
+    int kept = kk;
+    if (p < 1.f) {
+      __syncthreads();
+      u64 all;
+      const u64 at = scan(tid < kk ? other[tid] : 0, s.warp_sum, all);
+      const u64 want = scaled(p, all, true);       // the mass before a kept token is below this
+      kept = __syncthreads_count(tid < kk && at < want);
+    } else {
+      __syncthreads();
+    }
+    if (tid < n) {
+      other[at_index] = place < kept ? w : 0;
+      list[at_index + kCounted] = key;
     }
     __syncthreads();
-    if (tid < n) by_size[place] = key, by_index[at] = key;
-    __syncthreads();
-  } else if (kk < n || p < 1.f) {
-    for (int i = tid; i < m; i += kThreads) by_size[i] = i < n ? list[i] : 0;
-    sort_down(by_size, m, ~0ull);
+    u64 total;
+    const u64 mine = tid < n ? other[tid] : 0, at = scan(mine, s.scan_sum, total), target = scaled(u, total, false);
+    if (at <= target && target < at + mine) {
+      a.token[row] = (int32_t)(0xFFFFFFFFu - (uint32_t)list[tid + kCounted]);
+      if (a.prob) a.prob[row] = (float)((double)mine / (double)total);
+    }
+    return;
   }
+  int m = kCounted;
+  while (m < n) m *= 2;
   const int each = (n + kThreads - 1) / kThreads, first = tid * each, behind = min(first + each, n);
   u64 least = 0;                                   // the last key that is kept
   if (kk < n || p < 1.f) {
+    for (int i = tid; i < m; i += kThreads) other[i] = i < n ? list[i] : 0;
+    sort_down(other, m, ~0ull);
     int kept = kk;
     if (p < 1.f) {
       u64 mine = 0, all;
-      for (int i = first; i < min(behind, kk); ++i) mine += weight(key_logit(by_size[i]), s.powers);
-      u64 at = team.before(mine, all);
-      const u64 want = scaled(p, all, true);       // the mass before a kept token is below this
-      int more = 0;
+      for (int i = first; i < min(behind, kk); ++i) mine += weight(key_logit(other[i]), s.powers);
+      u64 at = scan(mine, s.warp_sum, all);
+      const u64 want = scaled(p, all, true);
+      uint32_t more = 0;
       for (int i = first; i < min(behind, kk); ++i) {
         more += at < want;
-        if (each > 1) at += weight(key_logit(by_size[i]), s.powers);
+        at += weight(key_logit(other[i]), s.powers);
       }
-      u64 none = 0;
-      uint32_t count = more;
+      more = __reduce_add_sync(0xFFFFFFFFu, more);
+      if ((tid & 31) == 0) s.warp_count[tid >> 5] = more;
       __syncthreads();
-      team.add_cta(none, count);
-      kept = max(1, (int)count);
+      kept = 0;
+      for (int i = 0; i < kWarps; ++i) kept += (int)s.warp_count[i];
     }
-    least = by_size[kept - 1];
+    least = other[kept - 1];
   }
-  if (n > kCounted) {                              // (low words are the indices' complements)
-    for (int i = n + tid; i < m; i += kThreads) list[i] = 0;
-    sort_down(list, m, 0xFFFFFFFFull);
-  }
+  for (int i = n + tid; i < m; i += kThreads) list[i] = 0;
+  sort_down(list, m, 0xFFFFFFFFull);               // (low words are the indices' complements)
   u64 mine = 0, total;
   for (int i = first; i < behind; ++i)
-    if (by_index[i] >= least) mine += weight(key_logit(by_index[i]), s.powers);
-  u64 at = team.before(mine, total);
+    if (list[i] >= least) mine += weight(key_logit(list[i]), s.powers);
+  u64 at = scan(mine, s.scan_sum, total);
   const u64 target = scaled(u, total, false);
   if (at > target || at + mine <= target) return;
   for (int i = first; i < behind; ++i) {
-    const u64 w = each == 1 ? mine : by_index[i] >= least ? weight(key_logit(by_index[i]), s.powers) : 0;
+    const u64 w = list[i] >= least ? weight(key_logit(list[i]), s.powers) : 0;
     if (at <= target && target < at + w) {
-      a.token[row] = (int32_t)(0xFFFFFFFFu - (uint32_t)by_index[i]);
+      a.token[row] = (int32_t)(0xFFFFFFFFu - (uint32_t)list[i]);
       if (a.prob) a.prob[row] = (float)((double)w / (double)total);
     }
     at += w;
   }
+}
+
+// A request's settings, checked; what a greedy one does not use is left out.
+struct Settings {
+  float temp, p, least, u;
+  int k;
+  bool ok, greedy;
+  __device__ __forceinline__ Settings(const Args& a, int row) {
+    const int q = a.index ? a.index[row] : row;
+    ok = q >= 0 && q < a.requests;
+    temp = ok && a.temperature ? a.temperature[q] : 1.f;
+    p = ok && a.top_p ? a.top_p[q] : 1.f, least = ok && a.min_p ? a.min_p[q] : 0.f;
+    u = a.u[row], k = ok && a.top_k ? a.top_k[q] : 0;
+    ok = ok && temp >= 0.f && temp <= 0x1p100f;
+    greedy = temp == 0.f;
+    if (!ok || greedy) p = 1.f, least = 0.f, u = 0.f, k = 0;
+    ok = ok && k >= 0 && p > 0.f && p <= 1.f && least >= 0.f && least <= 1.f && u >= 0.f && u < 1.f;
+    if (k == 0 || k > a.vocab) k = a.vocab;
+    if (greedy) k = 1;
+  }
+  // how far below the largest logit min-p goes
+  __device__ __forceinline__ double far() const { return -log((double)least) * (double)temp; }
+  __device__ __forceinline__ Weight weight(float m, int bits) const {
+    Weight w{m, 0.f, 0.f, bits};
+    if (!greedy) {
+      // (no fp64: its units are few)
+      constexpr float kHi = 1.44269502162933349609375f, kLo = 1.9259629911e-8f;
+      w.hi = __fdiv_rn(kHi, temp);
+      w.lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-w.hi, temp, kHi), kLo), temp);
+      if (!(w.hi < 1e38f)) w.hi = 1e38f, w.lo = 0.f;
+    }
+    return w;
+  }
+};
+
+// A number that at least `need` threads' `best` reach: the search ends near the largest
+// such.  top: the largest best.
+__device__ __forceinline__ uint32_t reached_by(int need, uint32_t best, uint32_t top) {
+  if (need == 1) return top;
+  uint32_t lo = 0, hi = top + 1, step = 1u << 18;  // fewer than `need` threads reach hi, at least as many lo
+  while (hi - lo > 1) {
+    const uint32_t mid = lo == 0 && hi > step ? hi - step : lo + (hi - lo) / 2;
+    const int n = __syncthreads_count(best >= mid);
+    if (n >= need) lo = mid;
+    else hi = mid, step *= 2;
+    if (n >= need && n <= need + need / 4 + 1) break;
+    if (lo == 0 && step >= (1u << 30)) break;      // few logits: all reach it
+  }
+  return lo;
+}
+__device__ __forceinline__ uint32_t largest_of_cta(uint32_t best, uint32_t* __restrict__ of_warps) {
+  best = __reduce_max_sync(0xFFFFFFFFu, best);
+  if ((threadIdx.x & 31) == 0) of_warps[threadIdx.x >> 5] = best;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) best = max(best, of_warps[w]);
+  return best;
 }
 
 // chunk: logits of a CTA; steps: runs of eight per thread, so that the chunk fits the CTA
@@ -619,12 +694,8 @@ __global__ void __launch_bounds__(kThreads, 4)
   T* x = mine + first;
   float m = -INFINITY;
   constexpr int kAhead = sizeof(T) == 2 ? 8 : 4;   // runs in flight
-  int q = -1;
-  bool ok = false, greedy = false;
-  float temp = 1.f, p = 1.f, least = 0.f, u = 0.f;
-  int k = 0;
-  for (int s0 = 0; s0 < steps; s0 += kAhead) {
-    Run<T> run[kAhead];
+  Run<T> run[kAhead];
+  const auto load_runs = [&](int s0) {
 #pragma unroll
     for (int s = 0; s < kAhead; ++s) {
       const int i = first + (s0 + s) * 32 * kVec;
@@ -632,20 +703,15 @@ __global__ void __launch_bounds__(kThreads, 4)
       if (vec && i + kVec <= there) run[s].load(src + i);
       else run[s].load_some(src + i, there - i);
     }
-    if (s0 == 0) {                                 // meanwhile the request's settings
-      q = a.index ? a.index[row] : row;
-      ok = q >= 0 && q < a.requests;
-      temp = ok && a.temperature ? a.temperature[q] : 1.f;
-      p = ok && a.top_p ? a.top_p[q] : 1.f, least = ok && a.min_p ? a.min_p[q] : 0.f;
-      u = a.u[row], k = ok && a.top_k ? a.top_k[q] : 0;
-      ok = ok && temp >= 0.f && temp <= 0x1p100f;
-      greedy = temp == 0.f;
-      if (!ok || greedy) p = 1.f, least = 0.f, u = 0.f, k = 0;
-      ok = ok && k >= 0 && p > 0.f && p <= 1.f && least >= 0.f && least <= 1.f && u >= 0.f && u < 1.f;
-      if (k == 0 || k > a.vocab) k = a.vocab;
-      if (greedy) k = 1;
-      if (tid == 0 && least > 0.f) sh.far = -log((double)least) * (double)temp;
-    }
+  };
+  load_runs(0);
+  const Settings set(a, row);                      // (while they are on their way)
+  const bool ok = set.ok, greedy = set.greedy;
+  const float p = set.p, least = set.least, u = set.u;
+  const int k = set.k;
+  if (tid == 0 && least > 0.f) sh.far = set.far();
+  for (int s0 = 0; s0 < steps; s0 += kAhead) {
+    if (s0) load_runs(s0);
 #pragma unroll
     for (int s = 0; s < kAhead; ++s) {
       if (s0 + s >= steps) break;
@@ -666,30 +732,9 @@ __global__ void __launch_bounds__(kThreads, 4)
   // The CTA's largest logit; and with a small k a logit that at least k of the row reach:
   // ceil(k / size) threads of each CTA have one.
   const uint32_t best = ordered_key(m);
-  const uint32_t of_warp = __reduce_max_sync(0xFFFFFFFFu, best);
-  if (lane == 0) sh.warp_count[warp] = of_warp;
-  __syncthreads();
-  uint32_t top = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = max(top, sh.warp_count[w]);
-  uint32_t bound = 0;
+  uint32_t top = largest_of_cta(best, sh.warp_count);
   const bool small_k = k <= kSmallK && k < a.vocab;
-  if (small_k) {
-    const int need = (k + size - 1) / size;
-    bound = top;
-    if (need > 1) {
-      uint32_t lo = 0, hi = top + 1, step = 1u << 18;  // fewer than `need` threads reach hi, at least as many lo
-      while (hi - lo > 1) {
-        const uint32_t mid = lo == 0 && hi > step ? hi - step : lo + (hi - lo) / 2;
-        const int n = __syncthreads_count(best >= mid);
-        if (n >= need) lo = mid;
-        else hi = mid, step *= 2;
-        if (n >= need && n <= need + need / 4 + 1) break;
-        if (lo == 0 && step >= (1u << 30)) break;  // a CTA with few logits: all are candidates
-      }
-      bound = lo;
-    }
-  }
+  uint32_t bound = small_k ? reached_by((k + size - 1) / size, best, top) : 0;
   cluster_wait();
   team.exchange(top, bound);
   for (int r = 0; r < size; ++r) {
@@ -706,14 +751,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     return;
   }
   // kept: logits above `cut`, and of those equal to it the first `ties`; first what min-p keeps
-  Weight weight{m, 0.f, 0.f, a.bits};
-  if (!greedy) {
-    // (no fp64: its units are few)
-    constexpr float kHi = 1.44269502162933349609375f, kLo = 1.9259629911e-8f;
-    weight.hi = __fdiv_rn(kHi, temp);
-    weight.lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-weight.hi, temp, kHi), kLo), temp);
-    if (!(weight.hi < 1e38f)) weight.hi = 1e38f, weight.lo = 0.f;
-  }
+  const Weight weight = set.weight(m, a.bits);
   float cut = greedy ? m : -FLT_MAX;
   if (least > 0.f) cut = fmaxf(__double2float_ru((double)m - sh.far), -FLT_MAX);
   if (small_k || least > 0.f) {
@@ -743,22 +781,14 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
     if (all) {
       if (rank != 0) return;
-      // together; each CTA's part moves towards the front
-      if (size > 1) {
-        u64 keep[kList / kThreads];
-#pragma unroll
-        for (int i = 0; i < kList / kThreads; ++i) keep[i] = list[tid + i * kThreads];
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kList / kThreads; ++i) {
-          const int from = tid + i * kThreads, r = from / (int)room, o = from - r * (int)room;
-          int to = o;
-          for (int b = 0; b < r; ++b) to += (int)sh.count[team.turn][b];
-          if (o < (int)sh.count[team.turn][r]) list[to] = keep[i];
-        }
-        __syncthreads();
+      u64* packed = (u64*)mine;                    // (this CTA's logits are not looked at again)
+      int r = 0, begin = 0;
+      for (int i = tid; i < total; i += kThreads) {
+        while (i - begin >= (int)sh.count[team.turn][r]) begin += (int)sh.count[team.turn][r++];
+        packed[i] = list[r * room + i - begin];
       }
-      finish(a, team, weight, list, (u64*)mine, total, k, p, u, row);
+      __syncthreads();
+      finish(a, sh, weight, packed, list, total, k, p, u, row);
       return;
     }
   }
