@@ -16,6 +16,8 @@
 #include <float.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "dsa_common.cuh"
 
 namespace dsa {
@@ -201,6 +203,11 @@ struct __align__(16) Shared {
   uint32_t rank_in, listed;
 };
 
+__device__ __forceinline__ void load_powers(Shared& s) {
+  static_assert(kThreads == 256, "four powers per thread");
+  reinterpret_cast<uint4*>(s.powers)[threadIdx.x] = reinterpret_cast<const uint4*>(kPowers.at)[threadIdx.x];
+}
+
 // What a CTA sums, and what the cluster does.  An exchange's numbers stay readable until
 // the next but one.
 struct Team {
@@ -233,7 +240,8 @@ struct Team {
   }
 };
 
-// eight consecutive logits as they lie in memory
+// Eight consecutive logits as they lie in memory.  A NaN among them is never the largest,
+// reaches no bound and weighs nothing, as comparisons with it fail; +inf is taken out.
 template <typename T>
 struct Run;
 template <>
@@ -254,21 +262,21 @@ struct Run<float> {
   }
   __device__ __forceinline__ float get(int j) const { return __uint_as_float(w[j]); }
   __device__ __forceinline__ void get_negative(int j, float& a, float& b) const { a = -get(j), b = -get(j + 1); }
-  // infinities and NaN become -inf; returns the largest
-  __device__ __forceinline__ float clean() {
-    float m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float v = fabsf(get(j)) <= FLT_MAX ? get(j) : -INFINITY;
-      w[j] = __float_as_uint(v);
-      m = fmaxf(m, v);
-    }
-    return m;
-  }
   __device__ __forceinline__ float largest() const {
     float m = get(0);
 #pragma unroll
     for (int j = 1; j < 8; ++j) m = fmaxf(m, get(j));
+    return m;
+  }
+  // +inf becomes -inf; returns the largest
+  __device__ __forceinline__ float clean() {
+    float m = largest();
+    if (!(m < INFINITY)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!(get(j) < INFINITY)) w[j] = kNone;
+      m = largest();
+    }
     return m;
   }
 };
@@ -306,27 +314,18 @@ struct Run<__nv_bfloat16> {
     return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
   }
   __device__ __forceinline__ float clean() {
-    uint32_t bad = 0;                              // an exponent of all ones carries into the sign
-#pragma unroll
-    for (int j = 0; j < 4; ++j) bad |= (w[j] & 0x7F807F80u) + 0x00800080u;
-    if (bad & 0x80008000u)
+    float m = largest();
+    if (!(m < INFINITY)) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if ((w[j] & 0x7F80u) == 0x7F80u) w[j] = (w[j] & 0xFFFF0000u) | kNone;
-        if ((w[j] & 0x7F800000u) == 0x7F800000u) w[j] = (w[j] & 0xFFFFu) | kNone << 16;
+        if (!(__uint_as_float(w[j] << 16) < INFINITY)) w[j] = (w[j] & 0xFFFF0000u) | kNone;
+        if (!(__uint_as_float(w[j] & 0xFFFF0000u) < INFINITY)) w[j] = (w[j] & 0xFFFFu) | kNone << 16;
       }
-    return largest();
+      m = largest();
+    }
+    return m;
   }
 };
-
-__device__ __forceinline__ uint4 load_remote(const uint32_t* local, uint32_t rank) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(mapa_shared(smem_u32(local), rank))
-               : "memory");
-  return v;
-}
 
 // The largest grid value that `want` of what f counts (or weighs) reach: grid numbers lo
 // (reached) and hi (not); above: f at the grid number behind it.  f(v, w): of the logits
@@ -647,17 +646,32 @@ struct Settings {
 };
 
 // A number that at least `need` threads' `best` reach: the search ends near the largest
-// such.  top: the largest best.
-__device__ __forceinline__ uint32_t reached_by(int need, uint32_t best, uint32_t top) {
+// such.  top: the largest best; lo: 0, or a number known to be reached by so many.
+__device__ __forceinline__ uint32_t reached_by(int need, uint32_t best, uint32_t top, uint32_t lo) {
   if (need == 1) return top;
-  uint32_t lo = 0, hi = top + 1, step = 1u << 18;  // fewer than `need` threads reach hi, at least as many lo
-  while (hi - lo > 1) {
-    const uint32_t mid = lo == 0 && hi > step ? hi - step : lo + (hi - lo) / 2;
+  uint32_t hi = top + 1, step = 1u << 18;          // fewer than `need` threads reach hi
+  uint32_t mid = lo ? lo : hi > step ? hi - step : hi / 2;
+  bool open = lo == 0;
+  while (hi - lo > 1 || mid == lo) {
     const int n = __syncthreads_count(best >= mid);
-    if (n >= need) lo = mid;
-    else hi = mid, step *= 2;
-    if (n >= need && n <= need + need / 4 + 1) break;
-    if (lo == 0 && step >= (1u << 30)) break;      // few logits: all reach it
+    if (n >= need) {
+      lo = mid, open = false;
+      if (n <= need + need / 4 + 1) break;
+      if (hi == top + 1 && hi - lo > 2 * step) {   // up from below
+        mid = lo + step, step *= 2;
+        continue;
+      }
+    } else {
+      hi = mid;
+      if (open) {                                  // down from above
+        step *= 2;
+        if (step >= (1u << 30)) break;             // few logits: all reach it
+        mid = hi > step ? hi - step : hi / 2;
+        continue;
+      }
+    }
+    if (hi - lo <= 1) break;
+    mid = lo + (hi - lo) / 2;
   }
   return lo;
 }
@@ -670,22 +684,116 @@ __device__ __forceinline__ uint32_t largest_of_cta(uint32_t best, uint32_t* __re
   return best;
 }
 
-// chunk: logits of a CTA; steps: runs of eight per thread, so that the chunk fits the CTA
+// Many rows: one CTA per row, which reads it once and lists what a top_k up to kStreamK or a
+// min-p can keep.  The first 8,192 (fp32: 4,096) logits give a bound that top_k of them reach,
+// more logits a better one.  Rows that need anything else, or have too many candidates, are
+// left to sample_kernel.
+constexpr int kStreamK = 192, kLater = -2;
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4)
-    sample_kernel(const __grid_constant__ Args a, const T* __restrict__ logits, int chunk, int steps, int vec, DevCtx c) {
-  extern __shared__ __align__(16) uint8_t dyn[];
+    stream_kernel(const __grid_constant__ Args a, const T* __restrict__ logits, int vec, DevCtx c) {
   __shared__ Shared sh;
+  __shared__ u64 list[kList], other[kList];
+  constexpr int kRunList = 2 * kList;
+  int* runs = (int*)other;                         // runs with a logit that reached the bound when they were read
+  constexpr int kRuns = sizeof(T) == 2 ? 4 : 2, kGroup = kRuns * kThreads * kVec;
+  let_next_launch();
+  const int tid = threadIdx.x, row = blockIdx.x;
+  load_powers(sh);
+  if (tid == 0) sh.listed = sh.rank_in = 0;
+  wait_for_earlier();
+  const T* src = logits + row * a.ld;
+  Run<T> run[kRuns], next[kRuns];
+  const auto load = [&](Run<T>(&r)[kRuns], int at) {
+#pragma unroll
+    for (int s = 0; s < kRuns; ++s) {
+      const int i = at + (s * kThreads + tid) * kVec;
+      if (vec && i + kVec <= a.vocab) r[s].load(src + i);
+      else r[s].load_some(src + i, a.vocab - i);
+    }
+  };
+  load(run, 0);
+  const Settings set(a, row);
+  const bool by_k = set.k < a.vocab;
+  if (!set.ok || !(by_k ? set.k <= kStreamK : set.least > 0.f)) {
+    if (tid == 0) {
+      a.token[row] = set.ok ? kLater : -1;
+      if (a.prob) a.prob[row] = 0.f;
+      if (!set.ok) set_status(c, DSA_ERR_INDEX);
+    }
+    return;
+  }
+  const double far = set.least > 0.f ? set.far() : 0.;
+  const auto cut_at = [&](float m) {
+    return set.greedy ? m : set.least > 0.f ? fmaxf(__double2float_ru((double)m - far), -FLT_MAX) : -FLT_MAX;
+  };
+  float m = -INFINITY, low = -FLT_MAX;
+  uint32_t top = 0, bound = 0;
+  for (int at = 0, group = 1; at < a.vocab; at += kGroup, ++group) {
+    if (at + kGroup < a.vocab) load(next, at + kGroup);
+    float of_run[kRuns];
+#pragma unroll
+    for (int s = 0; s < kRuns; ++s) m = fmaxf(m, of_run[s] = run[s].clean());
+    if ((group & (group - 1)) == 0 || at + kGroup >= a.vocab) {
+      const uint32_t best = ordered_key(m);
+      top = largest_of_cta(best, sh.warp_count);
+      if (by_k) bound = reached_by(set.k, best, top, bound);
+      low = fmaxf(cut_at(ordered_value(top)), fmaxf(ordered_value(bound), -FLT_MAX));
+      __syncthreads();
+    }
+#pragma unroll
+    for (int s = 0; s < kRuns; ++s)
+      if (of_run[s] >= low) {
+        const uint32_t to = atomicAdd(&sh.listed, 1u);
+        if (to < kRunList) runs[to] = at + (s * kThreads + tid) * kVec;
+      }
+#pragma unroll
+    for (int s = 0; s < kRuns; ++s) run[s] = next[s];
+  }
+  __syncthreads();
+  m = ordered_value(top);
+  const int n = (int)sh.listed;
+  if (m == -INFINITY || n > kRunList) {
+    if (tid == 0) {
+      a.token[row] = m == -INFINITY ? -1 : kLater;
+      if (a.prob) a.prob[row] = 0.f;
+    }
+    return;
+  }
+  for (int i = tid; i < n; i += kThreads) {        // the logits that reach the last bound
+    const int at = runs[i];
+    if (vec && at + kVec <= a.vocab) run[0].load(src + at);
+    else run[0].load_some(src + at, a.vocab - at);
+    run[0].clean();
+    uint32_t hits = 0;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) hits |= (uint32_t)(run[0].get(j) >= low) << j;
+    uint32_t to = hits ? atomicAdd(&sh.rank_in, __popc(hits)) : 0;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+      if (hits >> j & 1) {
+        if (to < kList) list[to] = make_key(run[0].get(j), (uint32_t)(at + j));
+        ++to;
+      }
+  }
+  __syncthreads();
+  if (sh.rank_in > kList) {
+    if (tid == 0) a.token[row] = kLater;
+    return;
+  }
+  finish(a, sh, set.weight(m, a.bits), list, other, (int)sh.rank_in, set.k, set.p, set.u, row);
+}
+
+// A row by a cluster; called between an arrive at the cluster's barrier and the next.
+// chunk: logits of a CTA; steps: runs of eight per thread, so that the chunk fits the CTA.
+template <typename T>
+__device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ logits, int chunk, int steps, int vec,
+                                           const DevCtx& c, Shared& sh, uint8_t* dyn, int row) {
   u64* list = (u64*)dyn;
   T* mine = (T*)(dyn + kList * sizeof(u64));
-  let_next_launch();
-  cluster_arrive();                                // no CTA writes to one that has not begun
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int size = (int)cluster_nctarank(), rank = (int)cluster_ctarank(), row = blockIdx.x / size;
-  static_assert(kThreads == 256, "four powers per thread");
-  reinterpret_cast<uint4*>(sh.powers)[tid] = reinterpret_cast<const uint4*>(kPowers.at)[tid];
+  const int size = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
   if (tid == 0) sh.listed = 0;
-  wait_for_earlier();
   // The row's logits of this CTA to shared memory: a warp's together in index order, a
   // thread's in runs of eight.
   const int first = (warp * steps * 32 + lane) * kVec;
@@ -734,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   const uint32_t best = ordered_key(m);
   uint32_t top = largest_of_cta(best, sh.warp_count);
   const bool small_k = k <= kSmallK && k < a.vocab;
-  uint32_t bound = small_k ? reached_by((k + size - 1) / size, best, top) : 0;
+  uint32_t bound = small_k ? reached_by((k + size - 1) / size, best, top, 0) : 0;
   cluster_wait();
   team.exchange(top, bound);
   for (int r = 0; r < size; ++r) {
@@ -1098,6 +1206,46 @@ __global__ void __launch_bounds__(kThreads, 4)
   }
 }
 
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4)
+    sample_kernel(const __grid_constant__ Args a, const T* __restrict__ logits, int chunk, int steps, int vec, DevCtx c) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ Shared sh;
+  let_next_launch();
+  cluster_arrive();                                // no CTA writes to one that has not begun
+  load_powers(sh);
+  wait_for_earlier();
+  sample_row<T>(a, logits, chunk, steps, vec, c, sh, dyn, blockIdx.x / cluster_nctarank());
+}
+
+// the rows that stream_kernel left, each cluster every `clusters`-th (three CTAs per SM: the
+// loop's variables would spill with four)
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 3)
+    left_rows_kernel(const __grid_constant__ Args a, const T* __restrict__ logits, int chunk, int steps, int vec, DevCtx c) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ Shared sh;
+  let_next_launch();
+  cluster_arrive();                                // no CTA writes to one that has not begun, or not come to this row
+  load_powers(sh);
+  wait_for_earlier();
+  const int size = (int)cluster_nctarank(), clusters = gridDim.x / size, lane = threadIdx.x & 31;
+  bool first = true;
+  for (int row0 = blockIdx.x / size; row0 < a.rows; row0 += 32 * clusters) {
+    const int mine = row0 + lane * clusters;       // (a row's token is written after a barrier behind this read)
+    uint32_t left = __ballot_sync(0xFFFFFFFFu, mine < a.rows && a.token[min(mine, a.rows - 1)] == kLater);
+    for (; left; left &= left - 1) {
+      if (!first) {
+        __syncthreads();
+        cluster_arrive();
+      }
+      first = false;
+      sample_row<T>(a, logits, chunk, steps, vec, c, sh, dyn, row0 + (__ffs(left) - 1) * clusters);
+    }
+  }
+  if (first) cluster_wait();
+}
+
 static int check(const dsa_sampler* p) {
   if (!p) return DSA_ERR_INVALID_ARG;
   if (p->dtype != DSA_BF16 && p->dtype != DSA_FP32) return DSA_ERR_UNSUPPORTED;
@@ -1124,8 +1272,14 @@ static bool launch(const Args& a, const void* logits, DevCtx c, cudaStream_t st)
   const int steps = (chunk + step - 1) / step;
   const size_t room = (size_t)steps * step * sizeof(T), smem = kList * 8 + (room > kList * 8 ? room : kList * 8);
   const int vec = (((uintptr_t)logits | (uintptr_t)(a.ld * sizeof(T))) & 15u) == 0;
-  return cuda_ok(cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) &&
-         launch_programmatic(sample_kernel<T>, dim3((unsigned)(a.rows * size)), dim3(kThreads), smem, st, size, a,
+  const bool stream = a.rows >= sms && (a.top_k || a.min_p);
+  auto kernel = stream ? left_rows_kernel<T> : sample_kernel<T>;
+  if (!cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))) return false;
+  if (stream && !launch_programmatic(stream_kernel<T>, dim3((unsigned)a.rows), dim3(kThreads), 0, st, 1, a,
+                                     (const T*)logits, vec, c))
+    return false;
+  const int clusters = stream ? std::min(a.rows, 3 * sms / size) : a.rows;
+  return launch_programmatic(kernel, dim3((unsigned)(clusters * size)), dim3(kThreads), smem, st, size, a,
                              (const T*)logits, chunk, steps, vec, c);
 }
 
