@@ -65,8 +65,16 @@ __device__ __align__(16) const Powers kPowers{};
 __device__ __forceinline__ void store_remote(u64* local, uint32_t rank, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_u32(local), rank)), "l"(v) : "memory");
 }
+__device__ __forceinline__ void store_remote(uint32_t* local, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(local), rank)), "r"(v) : "memory");
+}
 __device__ __forceinline__ void store_remote(float* local, uint32_t rank, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(local), rank)), "f"(v) : "memory");
+}
+__device__ __forceinline__ float load_remote(const float* local, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(local), rank)) : "memory");
+  return v;
 }
 __device__ __forceinline__ float ordered_value(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
@@ -195,9 +203,10 @@ struct __align__(16) Shared {
   double far;                                      // how far below the largest logit min-p goes
   u64 warp_sum[kWarps];
   uint32_t warp_count[kWarps];
-  u64 sum[2][kMaxCluster], count[2][kMaxCluster];  // of every CTA of the cluster, two exchanges deep
+  u64 sum[2][kMaxCluster], more[2][kMaxCluster];   // of every CTA of the cluster, two exchanges deep
+  uint32_t count[2][kMaxCluster];
   u64 scan_sum[kWarps];
-  u64 note[2];                                     // of CTA 0 to all
+  u64 note;                                        // of CTA 0 to all
   float warp_mass[kWarps], z;
   int bin[3];
   uint32_t rank_in, listed;
@@ -213,13 +222,17 @@ __device__ __forceinline__ void load_powers(Shared& s) {
 struct Team {
   Shared& s;
   int rank, size, turn;
-  __device__ __forceinline__ void exchange(u64 sum, u64 count) {
+  __device__ __forceinline__ void exchange(u64 sum, uint32_t count) {
     turn ^= 1;
     if ((int)threadIdx.x < size) {
       store_remote(&s.sum[turn][rank], threadIdx.x, sum);
       store_remote(&s.count[turn][rank], threadIdx.x, count);
     }
     cluster_sync_all();
+  }
+  __device__ __forceinline__ void exchange(u64 sum, u64 more, uint32_t count) {
+    if ((int)threadIdx.x < size) store_remote(&s.more[turn ^ 1][rank], threadIdx.x, more);
+    exchange(sum, count);
   }
   // this CTA's totals; the same of all threads that come between two barriers
   __device__ __forceinline__ void add_cta(u64& sum, uint32_t& count) {
@@ -231,12 +244,20 @@ struct Team {
     sum = 0, count = 0;
     for (int w = 0; w < kWarps; ++w) sum += s.warp_sum[w], count += s.warp_count[w];
   }
+  __device__ __forceinline__ void add_cta(u64& a, u64& b) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o), b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    if (lane == 0) s.warp_sum[warp] = a, s.scan_sum[warp] = b;
+    __syncthreads();
+    a = b = 0;
+    for (int w = 0; w < kWarps; ++w) a += s.warp_sum[w], b += s.scan_sum[w];
+  }
   // totals over the cluster
   __device__ __forceinline__ void add(u64& sum, uint32_t& count) {
     add_cta(sum, count);                           // (read again before the exchange's barrier only)
     exchange(sum, count);
     sum = 0, count = 0;
-    for (int r = 0; r < size; ++r) sum += s.sum[turn][r], count += (uint32_t)s.count[turn][r];
+    for (int r = 0; r < size; ++r) sum += s.sum[turn][r], count += s.count[turn][r];
   }
 };
 
@@ -351,8 +372,8 @@ __device__ __forceinline__ int bin_at(uint32_t y) {  // (y's bits fall with the 
   return (int)min((__float_as_uint(Weight::kY) - y) >> 3, (uint32_t)(kBins - 1));
 }
 
-// The cluster's histograms summed in CTA 0's: each CTA sums a part of the bins.  Between
-// two barriers of the cluster.
+// The cluster's histograms summed in every CTA's: each CTA sums a part of the bins for all.
+// Between two barriers of the cluster.
 __device__ __forceinline__ void sum_histograms(uint32_t* __restrict__ hist, int rank, int size) {
   const int part = kBins / size, first = rank * part;
   for (int i = first + 2 * (int)threadIdx.x; i < first + part; i += 2 * kThreads) {
@@ -367,12 +388,15 @@ __device__ __forceinline__ void sum_histograms(uint32_t* __restrict__ hist, int 
     }
 #pragma unroll
     for (int r = 1; r < kMaxCluster; ++r) x[0] += x[r], y[0] += y[r];
-    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(mapa_shared(smem_u32(hist + i), 0)), "r"(x[0]), "r"(y[0])
-                 : "memory");
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < size)
+        asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(mapa_shared(smem_u32(hist + i), r)), "r"(x[0]), "r"(y[0])
+                     : "memory");
   }
 }
 
-// CTA 0's choice of bins.  bin[2]: where the k-th logit lies (kBins: none does), rank_in of
+// The choice of bins.  bin[2]: where the k-th logit lies (kBins: none does), rank_in of
 // its bin's tokens are kept; bin[0] to bin[1]: where top-p's border lies, by the counts and
 // the weights of the bins' middles, with a part `margin` of the mass to either side.  Who
 // has the exact sums looks whether the border lies there.
@@ -451,19 +475,16 @@ __device__ __forceinline__ void choose_bins(Shared& s, const uint32_t* __restric
 }
 
 // The masses of a thread's logits from the cut on: of those in bins before b1 and of those
-// between b2 and bk; and the number of the others up to bk.
-struct Masses {
-  u64 above, between;
-  uint32_t listed;
-};
-template <typename T>
-__device__ __forceinline__ Masses mass_around(const T* x, int steps, float cut, const Weight& weight,
-                                              const uint32_t* __restrict__ powers, int b1, int b2, int bk) {
-  Masses a{0, 0, 0};
+// between b2 and bk; list(logit, step) for the others up to bk.
+template <typename T, typename F>
+__device__ __forceinline__ void mass_around(const T* x, int steps, float cut, const Weight& weight,
+                                            const uint32_t* __restrict__ powers, int b1, int b2, int bk, u64& above,
+                                            u64& between, F list) {
   const uint32_t span = (uint32_t)(b2 - b1);
   for (int s = 0; s < steps; ++s) {
     Run<T> run;
     run.load(x + s * 32 * kVec);
+    uint32_t hits = 0;
 #pragma unroll
     for (int j = 0; j < kVec; j += 2) {
       float l[2];
@@ -476,13 +497,13 @@ __device__ __forceinline__ Masses mass_around(const T* x, int steps, float cut, 
       for (int i = 0; i < 2; ++i) {
         const int b = bin_at(y[i]);
         const bool listed = (uint32_t)(b - b1) <= span || b == bk;
-        a.listed += listed && in[i];
-        if (b < b1) a.above += w[i];
-        else if (!listed && b < bk) a.between += w[i];
+        hits |= (uint32_t)(listed && in[i]) << (j + i);
+        if (b < b1) above += w[i];
+        else if (!listed && b < bk) between += w[i];
       }
     }
+    if (hits) list(s, hits);
   }
-  return a;
 }
 
 // larger logit first, then lower index
@@ -610,6 +631,116 @@ __device__ __forceinline__ void finish(const Args& a, Shared& s, const Weight& w
     }
     at += w;
   }
+}
+
+// The cut by n listed logits (values), with the masses above and between their bins: the
+// logit at the cut and how many equal to it are kept.  bin bk, where there is one, keeps
+// its first rank_in; then p as in top-p, among the bins up to b2 (or in bk at its cut).
+// below: less than all of them.  False: top-p's border is not among them.
+template <typename B>
+__device__ __forceinline__ bool cut_of_few(Shared& s, const Weight& weight, B bin_of, float* __restrict__ values, int n,
+                                           float below, int b2, int bk, uint32_t rank_in, float p, u64 above, u64 between,
+                                           float& cut, uint32_t& ties) {
+  float* sorted = values + 1024;
+  u64* masses = (u64*)(values + 2048);
+  const int tid = threadIdx.x;
+  const float l = tid < n ? values[tid] : 0.f;
+  const int bin = tid < n ? bin_of(l) : kBins + 1;
+  int place = 0;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) place += values[j] > l || (values[j] == l && j < tid);
+  if (tid < n) {
+    sorted[place] = l;
+    masses[place] = weight(l, s.powers);
+  }
+  const int before_k = __syncthreads_count(bin < bk), in_p = __syncthreads_count(bin <= b2);
+  const int limit = bk < kBins ? before_k + (int)rank_in : n;
+  int kept = limit;
+  if (p < 1.f) {
+    u64 all;
+    const u64 mine = tid < limit ? masses[tid] : 0, at = above + scan(mine, s.warp_sum, all);
+    // (`all` and the masses between: what lies behind the border)
+    const u64 want = scaled(p, above + between + all, true);
+    const int last = min(in_p, limit);
+    kept = __syncthreads_count(tid < last && at < want);
+    // the border is among them if the last one that may be kept reaches it, or is the last of all
+    const int reached = __syncthreads_count(tid < last && at + mine >= want);
+    if (above >= want || kept == 0 || !reached) return false;
+  }
+  cut = kept ? sorted[kept - 1] : below;
+  ties = (uint32_t)__syncthreads_count(tid < kept && sorted[tid] == cut);
+  return true;
+}
+template <typename T, typename B>
+__device__ __forceinline__ bool cut_of_many(Team& team, const Weight& weight, B bin_of, const float* __restrict__ values,
+                                            int n, float below, int b2, int bk, uint32_t rank_in, float p, u64 above,
+                                            u64 between, float& cut, uint32_t& ties) {
+  Shared& s = team.s;
+  const auto each_listed = [&](auto f) {
+    for (int i = threadIdx.x; i < n; i += kThreads) f(values[i]);
+  };
+  const auto block_min = [&](uint32_t v) {
+    v = __reduce_min_sync(0xFFFFFFFFu, v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s.warp_count[threadIdx.x >> 5] = v;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v = min(v, s.warp_count[w]);
+    return v;
+  };
+  const auto mass_of = [&](float v, float w, int to_bin) {
+    u64 some = 0;
+    uint32_t none = 0;
+    each_listed([&](float l) {
+      if (l >= v && l < w && bin_of(l) <= to_bin) some += weight(l, s.powers);
+    });
+    __syncthreads();
+    team.add_cta(some, none);
+    return some;
+  };
+  uint32_t least = 0xFFFFFFFFu, most = 0, k_least = 0xFFFFFFFFu, k_most = 0;
+  each_listed([&](float l) {
+    const int b = bin_of(l);
+    const uint32_t g = Grid<T>::up(l);
+    if (b <= b2) least = min(least, g), most = max(most, g);
+    if (b == bk) k_least = min(k_least, g), k_most = max(k_most, g);
+  });
+  cut = below, ties = 0;
+  if (bk < kBins) {                                // the rank_in-th of its bin
+    uint32_t over = 0;
+    k_least = block_min(k_least), k_most = ~block_min(~k_most);
+    cut = bisect<T>(k_least, k_most + 1, rank_in, over, [&](float v, float w) {
+      uint32_t in = 0;
+      u64 none = 0;
+      each_listed([&](float l) { in += l >= v && l < w && bin_of(l) == bk; });
+      __syncthreads();
+      team.add_cta(none, in);
+      return in;
+    });
+    ties = rank_in - over;
+  }
+  if (p >= 1.f) return true;
+  u64 some = 0;
+  uint32_t none = 0;
+  each_listed([&](float l) {
+    if (l > cut) some += weight(l, s.powers);
+  });
+  __syncthreads();
+  team.add_cta(some, none);
+  some += above + between;                         // mass above the cut so far
+  const u64 each = weight(cut, s.powers), want = scaled(p, some + ties * each, true);
+  if (above >= want) return false;
+  if (some < want) {                               // tokens at the cut are among the kept
+    ties = (uint32_t)((want - some + each - 1) / each);
+    return true;
+  }
+  if (above + mass_of(-FLT_MAX, INFINITY, b2) < want) return false;
+  u64 over = above;
+  least = block_min(least), most = ~block_min(~most);
+  cut = bisect<T>(least, most + 1, want, over, [&](float v, float w) { return mass_of(v, w, b2); });
+  const u64 one = weight(cut, s.powers);
+  ties = (uint32_t)((want - over + one - 1) / one);
+  return true;
 }
 
 // A request's settings, checked; what a greedy one does not use is left out.
@@ -847,7 +978,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
   team.exchange(top, bound);
   for (int r = 0; r < size; ++r) {
     top = max(top, (uint32_t)sh.sum[team.turn][r]);
-    bound = min(bound, (uint32_t)sh.count[team.turn][r]);
+    bound = min(bound, sh.count[team.turn][r]);
   }
   m = ordered_value(top);
   if (!ok || m == -INFINITY) {                     // the same for the whole cluster
@@ -946,131 +1077,60 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
     sum_histograms(hist, rank, size);
     cluster_sync_all();
     uint32_t rank_in = 0;
-    if (rank == 0) {
-      choose_bins(sh, hist, k, cuts, p, margin, rank_in);
-      if (tid < size)
-        store_remote(&sh.note[0], tid, (u64)sh.bin[0] | (u64)sh.bin[1] << 16 | (u64)sh.bin[2] << 32);
-    }
-    cluster_sync_all();
-    const int b1 = (int)(sh.note[0] & 0xFFFF), b2 = (int)(sh.note[0] >> 16 & 0xFFFF), bk = (int)(sh.note[0] >> 32);
+    choose_bins(sh, hist, k, cuts, p, margin, rank_in);
+    const int b1 = sh.bin[0], b2 = sh.bin[1], bk = sh.bin[2];
     const auto is_listed = [&](int b) { return (uint32_t)(b - b1) <= (uint32_t)(b2 - b1) || b == bk; };
-    // exact masses of what lies above and between the listed bins
-    const Masses masses = mass_around<T>(x, steps, cut, weight, sh.powers, b1, b2, bk);
-    float* values = (float*)list;
+    float* values = (float*)list;                  // in the histogram's place
     const uint32_t room = 2 * kList / size;
-    if (masses.listed) {
-      uint32_t to = atomicAdd(&sh.listed, masses.listed);
-      each_logit([&](float l) {
-        if (l >= cut && is_listed(bin_of(l)) && to < room) store_remote(&values[rank * room + to++], 0, l);
-      });
-    }
-    u64 above = masses.above, between = masses.between;
-    uint32_t none = 0;
-    __syncthreads();
-    team.add_cta(above, none);
-    __syncthreads();
-    team.add_cta(between, none);
-    team.exchange(above, sh.listed);
+    u64 above = 0, between = 0;                    // exact masses of what lies above and between the listed bins
+    uint32_t with = 0;                             // steps with listed logits
+    mass_around<T>(x, steps, cut, weight, sh.powers, b1, b2, bk, above, between, [&](int s, uint32_t hits) {
+      with |= 1u << s;
+      uint32_t to = atomicAdd(&sh.listed, __popc(hits));
+      for (; hits && to < room; hits &= hits - 1) values[to++] = to_f32(x[s * 32 * kVec + __ffs(hits) - 1]);
+    });
+    const u64 above_here = above, between_here = between;
+    team.add_cta(above, between);
+    team.exchange(above, between, sh.listed);
     bool all = true;
-    above = 0;
+    above = between = 0;
     for (int r = 0; r < size; ++r) {
       all = all && sh.count[team.turn][r] <= room;
-      above += sh.sum[team.turn][r];
+      above += sh.sum[team.turn][r], between += sh.more[team.turn][r];
     }
-    const int last = team.turn;                    // how many each CTA listed
-    team.exchange(between, 0);
-    between = 0;
-    for (int r = 0; r < size; ++r) between += sh.sum[team.turn][r];
     if (!all) break;
     if (rank == 0) {
-      int total = 0;
-      for (int r = 0; r < size; ++r) total += (int)sh.count[last][r];
-      // f(logit) over this thread's part of the listed ones
-      const auto each_listed = [&](auto f) {
-        int r = 0, begin = 0;
-        for (int i = tid; i < total; i += kThreads) {
-          while (i - begin >= (int)sh.count[last][r]) begin += (int)sh.count[last][r++];
-          f(values[r * room + i - begin]);
-        }
-      };
-      uint32_t least_key = 0xFFFFFFFFu, most_key = 0, k_least = 0xFFFFFFFFu, k_most = 0;
-      each_listed([&](float l) {
-        const int b = bin_of(l);
-        const uint32_t g = Grid<T>::up(l);
-        if (b >= b1 && b <= b2) least_key = min(least_key, g), most_key = max(most_key, g);
-        if (b == bk) k_least = min(k_least, g), k_most = max(k_most, g);
-      });
-      const auto block_min = [&](uint32_t v) {
-        v = __reduce_min_sync(0xFFFFFFFFu, v);
-        __syncthreads();
-        if (lane == 0) sh.warp_count[warp] = v;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) v = min(v, sh.warp_count[w]);
-        return v;
-      };
-      float at_cut = next_below<T>(cut);           // without a cut: below all of them
-      uint32_t tied = 0;
-      bool right = true;
-      if (bk < kBins) {                            // the rank_in-th of its bin
-        uint32_t over = 0;
-        k_least = block_min(k_least), k_most = ~block_min(~k_most);
-        at_cut = bisect<T>(k_least, k_most + 1, rank_in, over, [&](float v, float w) {
-          uint32_t n = 0;
-          u64 none = 0;
-          each_listed([&](float l) { n += l >= v && l < w && bin_of(l) == bk; });
-          __syncthreads();
-          team.add_cta(none, n);
-          return n;
-        });
-        tied = rank_in - over;
+      int n = (int)sh.count[team.turn][0];
+      for (int r = 1; r < size; ++r) {             // the others' behind its own
+        const int more = (int)sh.count[team.turn][r];
+        for (int i = tid; i < more; i += kThreads) values[n + i] = load_remote(&values[i], r);
+        n += more;
       }
-      if (p < 1.f) {
-        u64 some = 0;
-        uint32_t none = 0;
-        each_listed([&](float l) {
-          if (bk == kBins || l > at_cut) some += weight(l, sh.powers);
-        });
-        __syncthreads();
-        team.add_cta(some, none);
-        some += above + between;                   // mass above the cut so far
-        const u64 each = weight(at_cut, sh.powers), want = scaled(p, some + tied * each, true);
-        if (some < want) {
-          tied = (uint32_t)((want - some + each - 1) / each);
-        } else {
-          u64 over = above;
-          const auto mass_of = [&](float v, float w) {
-            u64 some = 0;
-            uint32_t none = 0;
-            each_listed([&](float l) {
-              if (l >= v && l < w && bin_of(l) <= b2) some += weight(l, sh.powers);
-            });
-            __syncthreads();
-            team.add_cta(some, none);
-            return some;
-          };
-          right = above < want && above + mass_of(-FLT_MAX, INFINITY) >= want;
-          if (right) {
-            least_key = block_min(least_key), most_key = ~block_min(~most_key);
-            at_cut = bisect<T>(least_key, most_key + 1, want, over, mass_of);
-            const u64 one = weight(at_cut, sh.powers);
-            tied = (uint32_t)((want - over + one - 1) / one);
-          }
-        }
-      }
-      if (tid < size) store_remote(&sh.note[1], tid, right ? (u64)__float_as_uint(at_cut) << 32 | tied : ~0ull);
+      __syncthreads();
+      float at_cut;
+      uint32_t tied;
+      const bool right = n <= kCounted ? cut_of_few(sh, weight, bin_of, values, n, next_below<T>(cut), b2, bk, rank_in, p,
+                                                    above, between, at_cut, tied)
+                                       : cut_of_many<T>(team, weight, bin_of, values, n, next_below<T>(cut), b2, bk,
+                                                        rank_in, p, above, between, at_cut, tied);
+      if (tid < size) store_remote(&sh.note, tid, right ? (u64)__float_as_uint(at_cut) << 32 | tied : ~0ull);
     }
     cluster_sync_all();
-    found = sh.note[1] != ~0ull;
+    found = sh.note != ~0ull;
     if (found) {
-      cut = __uint_as_float((uint32_t)(sh.note[1] >> 32));
-      ties = (uint32_t)sh.note[1];
-      sum = masses.above + (bin_of(cut) > b2 ? masses.between : 0);
-      if (masses.listed)
-        each_logit([&](float l) {
+      cut = __uint_as_float((uint32_t)(sh.note >> 32));
+      ties = (uint32_t)sh.note;
+      sum = above_here + (bin_of(cut) > b2 ? between_here : 0);
+      for (; with; with &= with - 1) {
+        Run<T> run;
+        run.load(x + (__ffs(with) - 1) * 32 * kVec);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          const float l = run.get(j);
           if (l > cut && is_listed(bin_of(l))) sum += weight(l, sh.powers);
           count += l == cut;
-        });
+        }
+      }
     }
   }
   if (!found) {
@@ -1132,7 +1192,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
   // mass of n tokens at the cut when `seen` of them came before
   const auto tie_mass = [&](uint32_t seen, uint32_t n) { return (u64)(min(ties, seen + n) - min(ties, seen)) * each; };
   for (int r = 0; r < size; ++r) {
-    const uint32_t n = (uint32_t)sh.count[team.turn][r];
+    const uint32_t n = sh.count[team.turn][r];
     const u64 some = sh.sum[team.turn][r] + (ties ? tie_mass(tied, n) : 0);
     if (r < rank) before += some, seen += n;
     if (r == rank) kept = some;
