@@ -1059,10 +1059,10 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
     if (!greedy) cut = next_below<T>(cut), ties = 0;
     kept_here();
   }
-  // A histogram tells near which logits the cuts lie; CTA 0 gets those listed.  fp32 logits
-  // are many different ones as a rule, and few lie near a cut; if they do not (bf16 ones
-  // are few different ones), a second time with more room.
-  for (float margin = sizeof(T) == 4 ? 0x1p-13f : 0x1p-9f; !found && margin <= 0x1p-9f; margin *= 16.f) {
+  // A histogram tells near which logits the cuts lie; CTA 0 gets those listed.  The bins'
+  // middles are off by a part in 370 at most, a sum over many bins by much less: 2^-13 of
+  // the mass to either side is enough as a rule, 2^-9 the second time.
+  for (float margin = 0x1p-13f; !found && margin <= 0x1p-9f; margin *= 16.f) {
     uint32_t* hist = (uint32_t*)list;
     static_assert(kBins * 4 <= kList * 8, "the histogram takes the list's place");
     const auto bin_of = [&](float l) { return bin_at(__float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(m, l), -weight.hi), Weight::kY))); };
