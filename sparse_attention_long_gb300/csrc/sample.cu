@@ -31,7 +31,8 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kVec = 8;                            // consecutive logits of a thread
 constexpr int kMaxVocab = 1 << 18;
 constexpr int kList = 2048;                        // tokens that one CTA can order, 2^n
-constexpr int kCounted = 256;                      // up to so many by counting
+constexpr int kCounted = 256;                      // up to so many by counting, or, of logits alone,
+constexpr int kListed = 512;                       // so many
 constexpr int kSmallK = 1024;                      // top_k up to which candidates are listed
 
 typedef unsigned long long u64;
@@ -644,31 +645,38 @@ __device__ __forceinline__ bool cut_of_few(Shared& s, const Weight& weight, B bi
   float* sorted = values + 1024;
   u64* masses = (u64*)(values + 2048);
   const int tid = threadIdx.x;
-  const float l = tid < n ? values[tid] : 0.f;
-  const int bin = tid < n ? bin_of(l) : kBins + 1;
-  int place = 0;
+  int before_k = 0, in_p = 0;
+  for (int i = tid; i < kListed; i += kThreads) {  // (as often for every thread: they count together)
+    if (i - tid >= n) break;
+    const float l = i < n ? values[i] : 0.f;
+    const int bin = i < n ? bin_of(l) : kBins + 1;
+    int place = 0;
 #pragma unroll 4
-  for (int j = 0; j < n; ++j) place += values[j] > l || (values[j] == l && j < tid);
-  if (tid < n) {
-    sorted[place] = l;
-    masses[place] = weight(l, s.powers);
+    for (int j = 0; j < n; ++j) place += values[j] > l || (values[j] == l && j < i);
+    if (i < n) {
+      sorted[place] = l;
+      masses[place] = weight(l, s.powers);
+    }
+    before_k += __syncthreads_count(bin < bk), in_p += __syncthreads_count(bin <= b2);
   }
-  const int before_k = __syncthreads_count(bin < bk), in_p = __syncthreads_count(bin <= b2);
   const int limit = bk < kBins ? before_k + (int)rank_in : n;
+  // two neighbours per thread
+  const int i0 = 2 * tid, i1 = i0 + 1;
   int kept = limit;
   if (p < 1.f) {
     u64 all;
-    const u64 mine = tid < limit ? masses[tid] : 0, at = above + scan(mine, s.warp_sum, all);
+    const u64 m0 = i0 < limit ? masses[i0] : 0, m1 = i1 < limit ? masses[i1] : 0;
+    const u64 at = above + scan(m0 + m1, s.warp_sum, all);
     // (`all` and the masses between: what lies behind the border)
     const u64 want = scaled(p, above + between + all, true);
     const int last = min(in_p, limit);
-    kept = __syncthreads_count(tid < last && at < want);
-    // the border is among them if the last one that may be kept reaches it, or is the last of all
-    const int reached = __syncthreads_count(tid < last && at + mine >= want);
+    kept = __syncthreads_count(i0 < last && at < want) + __syncthreads_count(i1 < last && at + m0 < want);
+    // the border is among them if one that may be kept reaches it
+    const int reached = __syncthreads_or((i0 < last && at + m0 >= want) || (i1 < last && at + m0 + m1 >= want));
     if (above >= want || kept == 0 || !reached) return false;
   }
   cut = kept ? sorted[kept - 1] : below;
-  ties = (uint32_t)__syncthreads_count(tid < kept && sorted[tid] == cut);
+  ties = (uint32_t)(__syncthreads_count(i0 < kept && sorted[i0] == cut) + __syncthreads_count(i1 < kept && sorted[i1] == cut));
   return true;
 }
 template <typename T, typename B>
@@ -1109,9 +1117,9 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
       __syncthreads();
       float at_cut;
       uint32_t tied;
-      const bool right = n <= kCounted ? cut_of_few(sh, weight, bin_of, values, n, next_below<T>(cut), b2, bk, rank_in, p,
+      const bool right = n <= kListed ? cut_of_few(sh, weight, bin_of, values, n, next_below<T>(cut), b2, bk, rank_in, p,
                                                     above, between, at_cut, tied)
-                                       : cut_of_many<T>(team, weight, bin_of, values, n, next_below<T>(cut), b2, bk,
+                                      : cut_of_many<T>(team, weight, bin_of, values, n, next_below<T>(cut), b2, bk,
                                                         rank_in, p, above, between, at_cut, tied);
       if (tid < size) store_remote(&sh.note, tid, right ? (u64)__float_as_uint(at_cut) << 32 | tied : ~0ull);
     }
