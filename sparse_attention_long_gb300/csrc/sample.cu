@@ -211,6 +211,9 @@ struct __align__(16) Shared {
   float warp_mass[kWarps], z;
   int bin[3];
   uint32_t rank_in, listed;
+  int who;                                         // where the token lies: warp, kept mass before it, ...
+  uint32_t seen;
+  u64 before, target, total;
 };
 
 __device__ __forceinline__ void load_powers(Shared& s) {
@@ -1184,41 +1187,61 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
       }
     }
   }
-  // what each warp keeps, in the order of the tokens
-  const u64 each = weight(cut, sh.powers);
+  // What each warp keeps, in the order of the tokens.
+  const u64 each = ties ? weight(cut, sh.powers) : 0;
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   count = __reduce_add_sync(0xFFFFFFFFu, count);
   if (lane == 0) sh.warp_sum[warp] = sum, sh.warp_count[warp] = count;
   __syncthreads();
-  u64 cta_sum = 0;
-  uint32_t cta_count = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) cta_sum += sh.warp_sum[w], cta_count += sh.warp_count[w];
-  team.exchange(cta_sum, cta_count);
-  u64 total = 0, before = 0, kept = 0;
-  uint32_t tied = 0, seen = 0;                     // of all CTAs, and before this one
+  if (warp == 0) {
+    u64 s = lane < kWarps ? sh.warp_sum[lane] : 0;
+    for (int o = kWarps / 2; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    const uint32_t n = __reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? sh.warp_count[lane] : 0u);
+    sum = s, count = n;
+  }
+  team.exchange(sum, count);                       // (its stores are the first warp's)
   // mass of n tokens at the cut when `seen` of them came before
   const auto tie_mass = [&](uint32_t seen, uint32_t n) { return (u64)(min(ties, seen + n) - min(ties, seen)) * each; };
-  for (int r = 0; r < size; ++r) {
-    const uint32_t n = sh.count[team.turn][r];
-    const u64 some = sh.sum[team.turn][r] + (ties ? tie_mass(tied, n) : 0);
-    if (r < rank) before += some, seen += n;
-    if (r == rank) kept = some;
-    total += some;
-    tied += n;
+  if (warp == 0) {
+    // a CTA's, then a warp's, per lane: the kept mass before it and its own
+    u64 before, kept;
+    uint32_t seen;
+    const auto in_order = [&](u64 s, uint32_t n, u64 base, uint32_t base_seen) {
+      static_assert(kWarps <= 8 && kMaxCluster <= 8, "three steps");
+      uint32_t n_run = n;
+      for (int o = 1; o < 8; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, n_run, o);
+        if (lane >= o) n_run += v;
+      }
+      seen = base_seen + n_run - n;
+      kept = s + (ties ? tie_mass(seen, n) : 0);
+      u64 run = kept;
+      for (int o = 1; o < 8; o <<= 1) {
+        const u64 v = __shfl_up_sync(0xFFFFFFFFu, run, o);
+        if (lane >= o) run += v;
+      }
+      before = base + run - kept;
+    };
+    in_order(lane < size ? sh.sum[team.turn][lane] : 0, lane < size ? sh.count[team.turn][lane] : 0u, 0, 0);
+    const u64 total = __shfl_sync(0xFFFFFFFFu, before + kept, 7), target = scaled(u, total, false);
+    const bool here = __shfl_sync(0xFFFFFFFFu, before <= target && target < before + kept, rank);
+    const u64 base = __shfl_sync(0xFFFFFFFFu, before, rank);
+    const uint32_t base_seen = __shfl_sync(0xFFFFFFFFu, seen, rank);
+    if (lane == 0) sh.who = -1;
+    __syncwarp();
+    if (here) {
+      in_order(lane < kWarps ? sh.warp_sum[lane] : 0, lane < kWarps ? sh.warp_count[lane] : 0u, base, base_seen);
+      if (lane < kWarps && before <= target && target < before + kept)
+        sh.who = lane, sh.before = before, sh.seen = seen, sh.target = target, sh.total = total;
+    }
   }
-  const u64 target = scaled(u, total, false);
-  if (before > target || before + kept <= target) return;
-  // The CTA that holds the token: the warp whose tokens reach it, one of its steps per warp,
-  // one of the step's lanes.
-  int who = 0;
-  for (;; ++who) {
-    const u64 some = sh.warp_sum[who] + tie_mass(seen, sh.warp_count[who]);
-    if (who == kWarps - 1 || target < before + some) break;
-    before += some;
-    seen += sh.warp_count[who];
-  }
-  __syncthreads();                                 // warp_sum is read
+  __syncthreads();
+  const int who = sh.who;
+  if (who < 0) return;
+  // The CTA that holds the token: one step of the warp that does per warp, one of its lanes.
+  u64 before = sh.before;
+  uint32_t seen = sh.seen;
+  const u64 target = sh.target, total = sh.total;
   const T* at_x = mine + (who * steps * 32 + lane) * kVec;
   for (int s0 = 0; s0 < steps; s0 += kWarps) {
     const int s = s0 + warp;
