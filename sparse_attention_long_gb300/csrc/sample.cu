@@ -269,6 +269,21 @@ struct Team {
 // reaches no bound and weighs nothing, as comparisons with it fail; +inf is taken out.
 template <typename T>
 struct Run;
+// A row as runs of sixteen-byte alignment: places `skew` to `behind` - 1 from `at` on hold
+// its logits, the token at place i is i - skew.  (A run's other places are -inf.)
+template <typename T>
+struct RowOf {
+  const T* at;
+  int skew, behind;
+  __device__ __forceinline__ RowOf(const T* row, int vocab) {
+    skew = (int)(((uintptr_t)row & 15) / sizeof(T));
+    at = row - skew, behind = vocab + skew;
+  }
+  __device__ __forceinline__ void load(Run<T>& run, int i) const {
+    if (i >= skew && i + 8 <= behind) run.load(at + i);
+    else run.load_some(at + i, skew - i, behind - i);
+  }
+};
 template <>
 struct Run<float> {
   uint32_t w[8];
@@ -281,9 +296,9 @@ struct Run<float> {
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     *reinterpret_cast<uint4*>(p + 4) = make_uint4(w[4], w[5], w[6], w[7]);
   }
-  __device__ __forceinline__ void load_some(const float* p, int n) {
+  __device__ __forceinline__ void load_some(const float* p, int lo, int hi) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = j < n ? __float_as_uint(p[j]) : kNone;
+    for (int j = 0; j < 8; ++j) w[j] = j >= lo && j < hi ? __float_as_uint(p[j]) : kNone;
   }
   __device__ __forceinline__ float get(int j) const { return __uint_as_float(w[j]); }
   __device__ __forceinline__ void get_negative(int j, float& a, float& b) const { a = -get(j), b = -get(j + 1); }
@@ -316,11 +331,11 @@ struct Run<__nv_bfloat16> {
   __device__ __forceinline__ void store(__nv_bfloat16* p) const {
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __device__ __forceinline__ void load_some(const __nv_bfloat16* p, int n) {
+  __device__ __forceinline__ void load_some(const __nv_bfloat16* p, int lo, int hi) {
     const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+    const auto at = [&](int j) { return j >= lo && j < hi ? q[j] : kNone; };
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = (2 * j < n ? q[2 * j] : kNone) | (2 * j + 1 < n ? q[2 * j + 1] : kNone) << 16;
+    for (int j = 0; j < 4; ++j) w[j] = at(2 * j) | at(2 * j + 1) << 16;
   }
   __device__ __forceinline__ float get(int j) const {
     return __uint_as_float((j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
@@ -419,9 +434,10 @@ __device__ __forceinline__ void choose_bins(Shared& s, const uint32_t* __restric
   if (tid == 0) s.bin[2] = kBins;
   uint32_t count = 0;
   float mass = 0;
+  const float first_weight = exp2f(-((float)(tid * kMine) + 0.5f) / kPerUnit);
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
-    w[i] = n[i] * exp2f(-((float)(tid * kMine + i) + 0.5f) / kPerUnit);
+    w[i] = n[i] * (first_weight * exp2f(-i / kPerUnit));
     count += n[i], mass += w[i];
   }
   uint32_t c_run = count;
@@ -462,11 +478,14 @@ __device__ __forceinline__ void choose_bins(Shared& s, const uint32_t* __restric
     const float from = p * z * (1.f - margin), upto = p * z * (1.f + margin);
     float a = m_run;
     int b1 = kBins - 1, b2 = kBins - 1;
+    // (sums of other threads may differ in the last bits: a little more of them look)
+    if (m_run <= upto * 1.001f && m_run + mass >= from * 0.999f) {
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      a += w[i];
-      if (a >= from) b1 = min(b1, tid * kMine + i);
-      if (a >= upto) b2 = min(b2, tid * kMine + i);
+      for (int i = 0; i < kMine; ++i) {
+        a += w[i];
+        if (a >= from) b1 = min(b1, tid * kMine + i);
+        if (a >= upto) b2 = min(b2, tid * kMine + i);
+      }
     }
     if (b1 < kBins - 1) atomicMin(&s.bin[0], b1);
     if (b2 < kBins - 1) atomicMin(&s.bin[1], b2);
@@ -833,7 +852,7 @@ __device__ __forceinline__ uint32_t largest_of_cta(uint32_t best, uint32_t* __re
 constexpr int kStreamK = 192, kLater = -2;
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4)
-    stream_kernel(const __grid_constant__ Args a, const T* __restrict__ logits, int vec, DevCtx c) {
+    stream_kernel(const __grid_constant__ Args a, const T* __restrict__ logits, DevCtx c) {
   __shared__ Shared sh;
   __shared__ u64 list[kList], other[kList];
   constexpr int kRunList = 2 * kList;
@@ -844,14 +863,13 @@ __global__ void __launch_bounds__(kThreads, 4)
   load_powers(sh);
   if (tid == 0) sh.listed = sh.rank_in = 0;
   wait_for_earlier();
-  const T* src = logits + row * a.ld;
+  const RowOf<T> src(logits + row * a.ld, a.vocab);
   Run<T> run[kRuns], next[kRuns];
   const auto load = [&](Run<T>(&r)[kRuns], int at) {
 #pragma unroll
     for (int s = 0; s < kRuns; ++s) {
       const int i = at + (s * kThreads + tid) * kVec;
-      if (vec && i + kVec <= a.vocab) r[s].load(src + i);
-      else r[s].load_some(src + i, a.vocab - i);
+      src.load(r[s], i);
     }
   };
   load(run, 0);
@@ -871,12 +889,12 @@ __global__ void __launch_bounds__(kThreads, 4)
   };
   float m = -INFINITY, low = -FLT_MAX;
   uint32_t top = 0, bound = 0;
-  for (int at = 0, group = 1; at < a.vocab; at += kGroup, ++group) {
-    if (at + kGroup < a.vocab) load(next, at + kGroup);
+  for (int at = 0, group = 1; at < src.behind; at += kGroup, ++group) {
+    if (at + kGroup < src.behind) load(next, at + kGroup);
     float of_run[kRuns];
 #pragma unroll
     for (int s = 0; s < kRuns; ++s) m = fmaxf(m, of_run[s] = run[s].clean());
-    if ((group & (group - 1)) == 0 || at + kGroup >= a.vocab) {
+    if ((group & (group - 1)) == 0 || at + kGroup >= src.behind) {
       const uint32_t best = ordered_key(m);
       top = largest_of_cta(best, sh.warp_count);
       if (by_k) bound = reached_by(set.k, best, top, bound);
@@ -904,8 +922,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   }
   for (int i = tid; i < n; i += kThreads) {        // the logits that reach the last bound
     const int at = runs[i];
-    if (vec && at + kVec <= a.vocab) run[0].load(src + at);
-    else run[0].load_some(src + at, a.vocab - at);
+    src.load(run[0], at);
     run[0].clean();
     uint32_t hits = 0;
 #pragma unroll
@@ -914,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 #pragma unroll
     for (int j = 0; j < kVec; ++j)
       if (hits >> j & 1) {
-        if (to < kList) list[to] = make_key(run[0].get(j), (uint32_t)(at + j));
+        if (to < kList) list[to] = make_key(run[0].get(j), (uint32_t)(at + j - src.skew));
         ++to;
       }
   }
@@ -929,8 +946,8 @@ __global__ void __launch_bounds__(kThreads, 4)
 // A row by a cluster; called between an arrive at the cluster's barrier and the next.
 // chunk: logits of a CTA; steps: runs of eight per thread, so that the chunk fits the CTA.
 template <typename T>
-__device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ logits, int chunk, int steps, int vec,
-                                           const DevCtx& c, Shared& sh, uint8_t* dyn, int row) {
+__device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ logits, int chunk, int steps, const DevCtx& c,
+                                           Shared& sh, uint8_t* dyn, int row) {
   u64* list = (u64*)dyn;
   T* mine = (T*)(dyn + kList * sizeof(u64));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -939,8 +956,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
   // The row's logits of this CTA to shared memory: a warp's together in index order, a
   // thread's in runs of eight.
   const int first = (warp * steps * 32 + lane) * kVec;
-  const int there = min(chunk, a.vocab - rank * chunk);
-  const T* src = logits + row * a.ld + rank * chunk;
+  const RowOf<T> src(logits + row * a.ld, a.vocab);
   T* x = mine + first;
   float m = -INFINITY;
   constexpr int kAhead = sizeof(T) == 2 ? 8 : 4;   // runs in flight
@@ -950,8 +966,8 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
     for (int s = 0; s < kAhead; ++s) {
       const int i = first + (s0 + s) * 32 * kVec;
       if (s0 + s >= steps) break;
-      if (vec && i + kVec <= there) run[s].load(src + i);
-      else run[s].load_some(src + i, there - i);
+      if (i < chunk) src.load(run[s], rank * chunk + i);  // (chunks are whole runs)
+      else run[s].load_some(src.at, 0, 0);
     }
   };
   load_runs(0);
@@ -1018,7 +1034,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
       uint32_t to = atomicAdd(&sh.listed, __popc(hits));
       for (; hits && to < room; hits &= hits - 1, ++to) {
         const int i = s * 32 * kVec + __ffs(hits) - 1;
-        store_remote(&list[rank * room + to], 0, make_key(to_f32(x[i]), (uint32_t)(rank * chunk + first + i)));
+        store_remote(&list[rank * room + to], 0, make_key(to_f32(x[i]), (uint32_t)(rank * chunk + first + i - src.skew)));
       }
     }
     __syncthreads();
@@ -1287,7 +1303,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
         const u64 w = tie ? (at_ties < ties ? each : 0) : own[j];
         at_ties += tie;
         if (at <= target && target < at + w) {
-          a.token[row] = rank * chunk + (who * steps * 32 + s * 32 + lane) * kVec + j;
+          a.token[row] = rank * chunk + (who * steps * 32 + s * 32 + lane) * kVec + j - src.skew;
           if (a.prob) a.prob[row] = (float)((double)w / (double)total);
         }
         at += w;
@@ -1297,44 +1313,27 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
   }
 }
 
-template <typename T>
+// kLeft: only the rows that stream_kernel left.  (A grid of all rows whose other CTAs end at
+// once: 3 us for 768 rows of 64,000; fewer clusters that look for rows take 60 % longer
+// where most are left.)
+template <typename T, bool kLeft>
 __global__ void __launch_bounds__(kThreads, 4)
-    sample_kernel(const __grid_constant__ Args a, const T* __restrict__ logits, int chunk, int steps, int vec, DevCtx c) {
+    sample_kernel(const __grid_constant__ Args a, const T* __restrict__ logits, int chunk, int steps, DevCtx c) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ Shared sh;
   let_next_launch();
   cluster_arrive();                                // no CTA writes to one that has not begun
-  load_powers(sh);
+  const int row = blockIdx.x / cluster_nctarank();
+  if (!kLeft) load_powers(sh);
   wait_for_earlier();
-  sample_row<T>(a, logits, chunk, steps, vec, c, sh, dyn, blockIdx.x / cluster_nctarank());
-}
-
-// the rows that stream_kernel left, each cluster every `clusters`-th (three CTAs per SM: the
-// loop's variables would spill with four)
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 3)
-    left_rows_kernel(const __grid_constant__ Args a, const T* __restrict__ logits, int chunk, int steps, int vec, DevCtx c) {
-  extern __shared__ __align__(16) uint8_t dyn[];
-  __shared__ Shared sh;
-  let_next_launch();
-  cluster_arrive();                                // no CTA writes to one that has not begun, or not come to this row
-  load_powers(sh);
-  wait_for_earlier();
-  const int size = (int)cluster_nctarank(), clusters = gridDim.x / size, lane = threadIdx.x & 31;
-  bool first = true;
-  for (int row0 = blockIdx.x / size; row0 < a.rows; row0 += 32 * clusters) {
-    const int mine = row0 + lane * clusters;       // (a row's token is written after a barrier behind this read)
-    uint32_t left = __ballot_sync(0xFFFFFFFFu, mine < a.rows && a.token[min(mine, a.rows - 1)] == kLater);
-    for (; left; left &= left - 1) {
-      if (!first) {
-        __syncthreads();
-        cluster_arrive();
-      }
-      first = false;
-      sample_row<T>(a, logits, chunk, steps, vec, c, sh, dyn, row0 + (__ffs(left) - 1) * clusters);
+  if (kLeft) {
+    if (a.token[row] != kLater) {                  // (written after barriers behind this read)
+      cluster_wait();
+      return;
     }
+    load_powers(sh);
   }
-  if (first) cluster_wait();
+  sample_row<T>(a, logits, chunk, steps, c, sh, dyn, row);
 }
 
 static int check(const dsa_sampler* p) {
@@ -1359,19 +1358,20 @@ static bool launch(const Args& a, const void* logits, DevCtx c, cudaStream_t st)
   while (size < kMaxCluster && (size * (32768ll / (int)sizeof(T)) < a.vocab ||
                                 ((long long)a.rows * size * 2 <= sms && size * 2048 < a.vocab)))
     size *= 2;
-  const int chunk = (a.vocab + size * kVec - 1) / (size * kVec) * kVec, step = kThreads * kVec;
+  // (rows that do not begin at sixteen bytes take up to a run's places more)
+  const bool whole = (((uintptr_t)logits | (uintptr_t)(a.ld * sizeof(T))) & 15u) == 0;
+  const int places = a.vocab + (whole ? 0 : kVec - 1);
+  const int chunk = (places + size * kVec - 1) / (size * kVec) * kVec, step = kThreads * kVec;
   const int steps = (chunk + step - 1) / step;
   const size_t room = (size_t)steps * step * sizeof(T), smem = kList * 8 + (room > kList * 8 ? room : kList * 8);
-  const int vec = (((uintptr_t)logits | (uintptr_t)(a.ld * sizeof(T))) & 15u) == 0;
   const bool stream = a.rows >= sms && (a.top_k || a.min_p);
-  auto kernel = stream ? left_rows_kernel<T> : sample_kernel<T>;
+  auto kernel = stream ? sample_kernel<T, true> : sample_kernel<T, false>;
   if (!cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))) return false;
   if (stream && !launch_programmatic(stream_kernel<T>, dim3((unsigned)a.rows), dim3(kThreads), 0, st, 1, a,
-                                     (const T*)logits, vec, c))
+                                     (const T*)logits, c))
     return false;
-  const int clusters = stream ? std::min(a.rows, 3 * sms / size) : a.rows;
-  return launch_programmatic(kernel, dim3((unsigned)(clusters * size)), dim3(kThreads), smem, st, size, a,
-                             (const T*)logits, chunk, steps, vec, c);
+  return launch_programmatic(kernel, dim3((unsigned)(a.rows * size)), dim3(kThreads), smem, st, size, a,
+                             (const T*)logits, chunk, steps, c);
 }
 
 }  // namespace sample
