@@ -189,6 +189,96 @@ def test_frequencies_follow_the_distribution():
         assert abs(int(count[t]) - n * part) <= 1 + n * 2.0 ** -23
 
 
+MANY = 170                                       # rows enough for a CTA each
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V,ld,offset", [(1, None, 0), (3, 5, 1), (100, None, 0), (257, 260, 3), (2049, None, 0), (4096, None, 0),
+                                         (8193, 8200, 0), (12007, None, 2), (40001, None, 0)])
+def test_many_rows_of_every_kind(V, ld, offset, dtype):
+    """Rows with a small top_k or min_p, and among them all others."""
+    dsa = lib()
+    rng = random.Random(V)
+    pick = lambda *v: [rng.choice(v) for _ in range(MANY)]
+    u = uniform(MANY, seed=V + 1)
+    kw = dict(temperature=pick(0.0, 0.7, 1.0, 1.3), top_k=pick(0, 1, 2, 7, 40, 100, 192, 193, 400, V),
+              top_p=pick(1.0, 1.0, 0.9, 0.51, 0.99), min_p=pick(0.0, 0.0, 0.05, 0.3, 1.0))
+    check(dsa, rand(MANY, V, seed=V), u, ld=ld, dtype=dtype, offset=offset, **kw)
+    check(dsa, rand(MANY, V, seed=V + 5, scale=0.3), u, ld=ld, dtype=dtype, offset=offset, top_k=[min(50, V)] * MANY)
+    check(dsa, rand(MANY, V, seed=V + 6), u, ld=ld, dtype=dtype, offset=offset, min_p=[0.02] * MANY)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_rows_with_ties_and_masks(dtype):
+    """More candidates than can be listed; logits in ascending and descending order; masked rows."""
+    dsa = lib()
+    V = 1 << 15
+    u = uniform(MANY, seed=3)
+    ks = [1 + (7 * i) % 192 for i in range(MANY)]
+    flat = torch.zeros(MANY, V, dtype=torch.float64)
+    exact_u = [float(i % 64) / 64 for i in range(MANY)]
+    check(dsa, flat, exact_u, dtype=dtype, top_k=[1 << (i % 8) for i in range(MANY)], exact=True)
+    check(dsa, flat, exact_u, dtype=dtype, min_p=[1.0] * MANY, exact=True)
+    check(dsa, flat, [0.5] * MANY, dtype=dtype, top_k=[64] * MANY, temperature=[0.0] * MANY, exact=True)
+    ramp = (torch.arange(V, dtype=torch.float64) / 512).expand(MANY, V)
+    for x in (ramp, -ramp, (rand(MANY, V, seed=8).round() * 0.5)):
+        check(dsa, x, u, dtype=dtype, top_k=ks, top_p=[0.97] * MANY)
+    x = rand(MANY, 9000, seed=4)
+    for r in range(MANY):
+        kind = r % 8
+        if kind == 0:
+            x[r, 5:] = -INF                      # fewer logits than top_k
+        elif kind == 1:
+            x[r] = -INF                          # none
+        elif kind == 2:
+            x[r, ::2] = math.nan
+        elif kind == 3:
+            x[r, 1000:8500] = INF
+        elif kind == 4:
+            x[r] = torch.finfo(dtype).min
+        elif kind == 5:
+            x[r, :8900] = -1e9
+    check(dsa, x, u, dtype=dtype, top_k=ks)
+    check(dsa, x, u, dtype=dtype, min_p=[0.1] * MANY)
+
+
+def test_many_rows_as_a_graph():
+    dsa = lib()
+    n, V = 400, 9001
+    s = dsa.make_sampler(rows=n, vocab=V, dtype="bf16", requests=3)
+    x, u = torch.zeros(n, V, dtype=BF16, device=DEV), torch.zeros(n, device=DEV)
+    k, p, i = dev([20, 0, 500], torch.int32), dev([0.9, 0.8, 1.0]), torch.zeros(n, dtype=torch.int32, device=DEV)
+    token, prob = torch.zeros(n, dtype=torch.int32, device=DEV), torch.zeros(n, device=DEV)
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=side):
+        dsa.sample(s, x, u, None, k, p, None, i, token, prob)
+    f = lambda v: float(torch.tensor(v, dtype=F32))
+    for seed in range(2):
+        y, r, q = rand(n, V, seed=seed).to(BF16), uniform(n, seed), [(j + seed) % 3 for j in range(n)]
+        for t, v in ((x, y), (u, torch.tensor(r)), (i, torch.tensor(q))):
+            t.copy_(v)
+        g.replay()
+        torch.cuda.synchronize()
+        want = [sample(y[j].double().numpy(), f(r[j]), 1.0, [20, 0, 500][q[j]], f([0.9, 0.8, 1.0][q[j]])) for j in range(n)]
+        assert token.tolist() == [w[0] for w in want]
+        assert all(abs(a - w[1]) <= w[1] * 2.0 ** -23 for a, w in zip(prob.tolist(), want))
+
+
+@pytest.mark.parametrize("V,spread,T", [(131071, 1.0, 1.0), (131071, 2.5, 0.7), (100003, 0.05, 1.0), (60000, 3.0, 100.0),
+                                        (60000, 3.0, 1e6), (200000, 1.0, 1.0), (30011, 6.0, 1.0)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_large_nuclei(V, spread, T, dtype):
+    """Cuts among many logits: many different ones, few different ones (bf16 values in either type), and more
+    near the cut than can be listed."""
+    dsa = lib()
+    x = rand(3, V, seed=V, scale=spread)
+    x[1] = x[1].to(BF16).double()
+    u = uniform(3, seed=V + 1)
+    for kw in (dict(top_p=[0.9, 0.8, 0.99]), dict(top_p=[0.3, 0.6, 0.95], top_k=[V // 2, V // 3, 5000]),
+               dict(top_k=[V // 2, 1025, V - 1]), dict(top_p=[0.9703] * 3, min_p=[0.01, 0.001, 0.0])):
+        check(dsa, x, u, dtype=dtype, temperature=[T] * 3, **kw)
+
+
 def test_settings_out_of_range():
     dsa = lib()
     x = rand(8, 100, seed=1)
