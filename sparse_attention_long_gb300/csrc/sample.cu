@@ -394,8 +394,8 @@ __device__ __forceinline__ int bin_at(uint32_t y) {  // (y's bits fall with the 
 // The cluster's histograms summed in every CTA's: each CTA sums a part of the bins for all.
 // Between two barriers of the cluster.
 __device__ __forceinline__ void sum_histograms(uint32_t* __restrict__ hist, int rank, int size) {
-  const int part = kBins / size, first = rank * part;
-  for (int i = first + 2 * (int)threadIdx.x; i < first + part; i += 2 * kThreads) {
+  const int part = (kBins / 2 + size - 1) / size * 2, first = rank * part, behind = min(first + part, kBins);
+  for (int i = first + 2 * (int)threadIdx.x; i < behind; i += 2 * kThreads) {
     uint32_t x[kMaxCluster] = {}, y[kMaxCluster] = {};
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r) {
@@ -1355,9 +1355,9 @@ static bool launch(const Args& a, const void* logits, DevCtx c, cudaStream_t st)
   int dev = 0, sms = 0, size = 1;
   if (!cuda_ok(cudaGetDevice(&dev)) || !cuda_ok(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)))
     return false;
-  while (size < kMaxCluster && (size * (32768ll / (int)sizeof(T)) < a.vocab ||
-                                ((long long)a.rows * size * 2 <= sms && size * 2048 < a.vocab)))
-    size *= 2;
+  const int full = 32768 / (int)sizeof(T);
+  size = std::min(kMaxCluster, (a.vocab + full - 1) / full);
+  while (size < kMaxCluster && (long long)a.rows * size * 2 <= sms && size * 2048 < a.vocab) ++size;
   // (rows that do not begin at sixteen bytes take up to a run's places more)
   const bool whole = (((uintptr_t)logits | (uintptr_t)(a.ld * sizeof(T))) & 15u) == 0;
   const int places = a.vocab + (whole ? 0 : kVec - 1);
