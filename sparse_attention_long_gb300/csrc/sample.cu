@@ -535,20 +535,6 @@ __device__ __forceinline__ u64 make_key(float l, uint32_t idx) {
 }
 __device__ __forceinline__ float key_logit(u64 k) { return ordered_value((uint32_t)(k >> 32)); }
 
-// the m (2^n) keys at v in descending order of key & mask
-__device__ __forceinline__ void sort_down(u64* __restrict__ v, int m, u64 mask) {
-  for (int size = 2; size <= m; size *= 2)
-    for (int step = size / 2; step; step /= 2) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < m / 2; i += kThreads) {
-        const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
-        const u64 x = v[lo], y = v[hi];
-        if (((x & mask) < (y & mask)) == ((lo & size) == 0)) v[lo] = y, v[hi] = x;
-      }
-    }
-  __syncthreads();
-}
-
 // The end for n listed tokens, by one CTA: list[] in any order, other[] room for as many
 // (kList).  The first k are kept at most, p as in top-p.  A scan's sums go by turns to
 // two places, so that one barrier is enough.
@@ -570,6 +556,60 @@ __device__ __forceinline__ u64 scan(u64 v, u64* __restrict__ sums, u64& all) {
     all += x;
   }
   return at;
+}
+// The largest number c such that the keys from c on weigh `want` or more, eight bits at a
+// time, until one key is left (or, with `some`, until what is left is needed whole: c is
+// then less than the reaching key, but more than the next).  in(key): which ones count;
+// of(key): a weight.  sums: 768 numbers; a weight goes to limbs of 21 bits, which 2,048 of
+// them do not overflow, the upper bits of the third (of 2,048 weights it has 20 bits at
+// most) count the keys.
+template <typename I, typename W>
+__device__ __forceinline__ u64 reaching_key(Shared& s, uint32_t* __restrict__ sums, const u64* __restrict__ list, int n,
+                                            bool some, u64 want, I in, W of) {
+  const int tid = threadIdx.x, warp = tid >> 5;
+  // from the first bit that not all share
+  u64 any = 0, every = ~0ull;
+  for (int i = tid; i < n; i += kThreads)
+    if (in(list[i])) any |= list[i], every &= list[i];
+  any = (u64)__reduce_or_sync(0xFFFFFFFFu, (uint32_t)(any >> 32)) << 32 | __reduce_or_sync(0xFFFFFFFFu, (uint32_t)any);
+  every = (u64)__reduce_and_sync(0xFFFFFFFFu, (uint32_t)(every >> 32)) << 32 | __reduce_and_sync(0xFFFFFFFFu, (uint32_t)every);
+  if ((tid & 31) == 0) s.scan_sum[warp] = any, s.warp_sum[warp] = every;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) any |= s.scan_sum[w], every &= s.warp_sum[w];
+  int shift = max(56 - __clzll((long long)(any & ~every)), 0);
+  u64 fixed = shift > 55 ? 0 : ~0ull << (shift + 8), prefix = every & fixed, base = 0;  // fixed: bits that are known
+  for (;;) {
+    sums[tid] = sums[tid + 256] = sums[tid + 512] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+      const u64 key = list[i];
+      if (!in(key) || ((key ^ prefix) & fixed)) continue;
+      const u64 w = of(key);
+      uint32_t* at = sums + (key >> shift & 255);
+      atomicAdd(at, (uint32_t)w & 0x1FFFFFu);
+      if (w >> 21) atomicAdd(at + 256, (uint32_t)(w >> 21) & 0x1FFFFFu);
+      atomicAdd(at + 512, (uint32_t)(w >> 42) + (1u << 21));
+    }
+    __syncthreads();
+    const int bin = 255 - tid;                     // from the largest down
+    const u64 mine = sums[bin] + ((u64)sums[bin + 256] << 21) + ((u64)(sums[bin + 512] & 0x1FFFFFu) << 42);
+    u64 all;
+    const u64 before = base + scan(mine, s.warp_sum, all);
+    if (before < want && want <= before + mine) {
+      s.before = before, s.who = bin;
+      s.seen = sums[bin + 512] >> 21 == 1 || (some && before + mine == want);
+    }
+    __syncthreads();
+    prefix |= (u64)s.who << shift;
+    base = s.before;
+    if (shift == 0 || s.seen) break;
+    fixed = ~0ull << shift;
+    shift = max(shift - 8, 0);
+    __syncthreads();
+  }
+  __syncthreads();
+  return prefix;
 }
 __device__ __forceinline__ void finish(const Args& a, Shared& s, const Weight& weight, u64* __restrict__ list,
                                        u64* __restrict__ other, int n, int k, float p, float u, int row) {
@@ -612,47 +652,45 @@ __device__ __forceinline__ void finish(const Args& a, Shared& s, const Weight& w
     }
     return;
   }
-  int m = kCounted;
-  while (m < n) m *= 2;
-  const int each = (n + kThreads - 1) / kThreads, first = tid * each, behind = min(first + each, n);
-  u64 least = 0;                                   // the last key that is kept
-  if (kk < n || p < 1.f) {
-    for (int i = tid; i < m; i += kThreads) other[i] = i < n ? list[i] : 0;
-    sort_down(other, m, ~0ull);
-    int kept = kk;
-    if (p < 1.f) {
-      u64 mine = 0, all;
-      for (int i = first; i < min(behind, kk); ++i) mine += weight(key_logit(other[i]), s.powers);
-      u64 at = scan(mine, s.warp_sum, all);
-      const u64 want = scaled(p, all, true);
-      uint32_t more = 0;
-      for (int i = first; i < min(behind, kk); ++i) {
-        more += at < want;
-        at += weight(key_logit(other[i]), s.powers);
-      }
-      more = __reduce_add_sync(0xFFFFFFFFu, more);
-      if ((tid & 31) == 0) s.warp_count[tid >> 5] = more;
-      __syncthreads();
-      kept = 0;
-      for (int i = 0; i < kWarps; ++i) kept += (int)s.warp_count[i];
-    }
-    least = other[kept - 1];
+  // More tokens: the last key that is kept, by number, then by mass; then the token, which is
+  // the reaching one in the order of the indices.
+  uint32_t* sums = (uint32_t*)other;
+  const auto of = [&](u64 key) { return weight(key_logit(key), s.powers); };
+  u64 least = 0;
+  if (kk < n)
+    least = reaching_key(s, sums, list, n, true, (u64)kk, [](u64) { return true; }, [](u64) { return (u64)1; });
+  const auto kept = [&](u64 key) { return key >= least; };
+  const auto mass = [&] {
+    u64 mine = 0, all;
+    for (int i = tid; i < n; i += kThreads)
+      if (kept(list[i])) mine += of(list[i]);
+    scan(mine, s.scan_sum, all);
+    __syncthreads();
+    return all;
+  };
+  u64 total = mass();
+  if (p < 1.f) {
+    // (the mass before a kept token is below the wanted one)
+    least = max(least, reaching_key(s, sums, list, n, true, scaled(p, total, true), kept, of));
+    total = mass();
   }
-  for (int i = n + tid; i < m; i += kThreads) list[i] = 0;
-  sort_down(list, m, 0xFFFFFFFFull);               // (low words are the indices' complements)
-  u64 mine = 0, total;
-  for (int i = first; i < behind; ++i)
-    if (list[i] >= least) mine += weight(key_logit(list[i]), s.powers);
-  u64 at = scan(mine, s.scan_sum, total);
   const u64 target = scaled(u, total, false);
-  if (at > target || at + mine <= target) return;
-  for (int i = first; i < behind; ++i) {
-    const u64 w = list[i] >= least ? weight(key_logit(list[i]), s.powers) : 0;
-    if (at <= target && target < at + w) {
-      a.token[row] = (int32_t)(0xFFFFFFFFu - (uint32_t)list[i]);
-      if (a.prob) a.prob[row] = (float)((double)w / (double)total);
-    }
-    at += w;
+  // by index alone: the logits change places with it, what is not kept becomes 0
+  for (int i = tid; i < n; i += kThreads) list[i] = kept(list[i]) ? list[i] << 32 | list[i] >> 32 : 0;
+  __syncthreads();
+  const auto of_turned = [&](u64 key) { return weight(ordered_value((uint32_t)key), s.powers); };
+  const u64 found = reaching_key(s, sums, list, n, false, target + 1, [](u64 key) { return key != 0; }, of_turned);
+  // (one key is left: the smallest from there on)
+  u64 best = ~0ull;
+  for (int i = tid; i < n; i += kThreads)
+    if (list[i] >= found) best = min(best, list[i]);
+  for (int o = 16; o; o >>= 1) best = min(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
+  if ((tid & 31) == 0) s.scan_sum[tid >> 5] = best;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kWarps; ++w) best = min(best, s.scan_sum[w]);
+    a.token[row] = (int32_t)(0xFFFFFFFFu - (uint32_t)(best >> 32));
+    if (a.prob) a.prob[row] = (float)((double)of_turned(best) / (double)total);
   }
 }
 
@@ -1020,8 +1058,8 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
   const Weight weight = set.weight(m, a.bits);
   float cut = greedy ? m : -FLT_MAX;
   if (least > 0.f) cut = fmaxf(__double2float_ru((double)m - sh.far), -FLT_MAX);
-  if (small_k || least > 0.f) {
-    // Few tokens can be kept as a rule: CTA 0 gets them listed.
+  if (small_k || least > 0.f || (p < 1.f && a.vocab <= kList)) {
+    // Few tokens can be kept as a rule, or are there: CTA 0 gets them listed.
     const float low = small_k ? fmaxf(cut, fmaxf(ordered_value(bound), -FLT_MAX)) : cut;
     const uint32_t room = kList / size;
     for (int s = 0; s < steps; ++s) {
