@@ -137,9 +137,9 @@ struct Weight {
   float max, hi, lo;                               // log2(e) / temperature in two floats
   int shift;                                       // the largest weight is 2^(62 - shift) units
 
-  __device__ __forceinline__ u64 of(bool counts, float nx, uint32_t y, float z, const uint32_t* __restrict__ powers) const {
+  __device__ __forceinline__ u64 of(bool counts, uint32_t y, float z, const uint32_t* __restrict__ powers) const {
     // (what is further down, the exponent of 2 out of reach, weighs nothing)
-    const uint32_t p = counts && nx > (float)shift - 62.5f ? powers[y & 1023u] : 0u;
+    const uint32_t p = counts && __uint_as_float(y) > kY - 62.5f + (float)shift ? powers[y & 1023u] : 0u;
     const int s = (int)(__float_as_uint(z) - __float_as_uint(kZ) + 1u);
     uint32_t w;
     asm("mad.hi.s32 %0, %1, %2, %1;" : "=r"(w) : "r"(p), "r"(s));
@@ -160,9 +160,9 @@ struct Weight {
     const u64 y = add2(nx, pair(kY, kY)), q = add2(y, pair(-kY, -kY));
     const u64 r = fma2(f, one, fma2(q, one, nx));
     const u64 z = fma2(r, fma2(r, pair(kHalfLn2Sq, kHalfLn2Sq), pair(kLn2, kLn2)), pair(kZ, kZ));
-    float n0, n1, a0, a1, z0, z1;
-    halves(nx, n0, n1), halves(y, a0, a1), halves(z, z0, z1);
-    w0 = of(counts0, n0, __float_as_uint(a0), z0, powers), w1 = of(counts1, n1, __float_as_uint(a1), z1, powers);
+    float a0, a1, z0, z1;
+    halves(y, a0, a1), halves(z, z0, z1);
+    w0 = of(counts0, __float_as_uint(a0), z0, powers), w1 = of(counts1, __float_as_uint(a1), z1, powers);
     y0 = __float_as_uint(a0), y1 = __float_as_uint(a1);
   }
   __device__ __forceinline__ u64 operator()(float l, const uint32_t* __restrict__ powers) const {
@@ -170,6 +170,37 @@ struct Weight {
     uint32_t y;
     two(-l, -l, true, false, a, b, y, y, powers);
     return a;
+  }
+};
+
+// The same for bf16 logits that are not too large, with fewer steps: a logit's eight bits
+// times sixteen of the scale is exact, so l * scale - max * scale needs no exact
+// difference first.  (20 instead of 25 instructions per logit: 256 rows of 131,071 52 us instead of 59.)
+// A row's weights are all of one kind.
+struct DirectWeight {
+  float high, low, from, left;                     // scale in 16 bits and the rest; kY - max * scale in two parts
+  int shift;
+  bool fits;
+  __device__ __forceinline__ explicit DirectWeight(const Weight& w) {
+    high = __uint_as_float(__float_as_uint(w.hi) & 0xFFFFFF00u);
+    low = __fadd_rn(__fsub_rn(w.hi, high), w.lo);
+    const float t = __fmul_rn(w.max, high), y = __fadd_rn(t, Weight::kY), q = __fsub_rn(y, Weight::kY);
+    from = __fsub_rn(Weight::kY, q);               // both multiples of 2^-10 below 2^14: exact
+    left = __fmaf_rn(-w.max, low, __fsub_rn(q, t));
+    shift = w.shift;
+    fits = fabsf(w.max) * w.hi < 2000.f;
+  }
+  __device__ __forceinline__ void two(float l0, float l1, bool counts0, bool counts1, u64& w0, u64& w1,
+                                      const uint32_t* __restrict__ powers) const {
+    const u64 l = pair(l0, l1), t = mul2(l, pair(high, high));
+    const u64 y = add2(t, pair(from, from)), q = add2(y, pair(-from, -from));
+    const u64 r = add2(fma2(q, pair(-1.f, -1.f), t), fma2(l, pair(low, low), pair(left, left)));
+    const u64 z = fma2(r, fma2(r, pair(Weight::kHalfLn2Sq, Weight::kHalfLn2Sq), pair(Weight::kLn2, Weight::kLn2)),
+                       pair(Weight::kZ, Weight::kZ));
+    float y0, y1, z0, z1;
+    halves(y, y0, y1), halves(z, z0, z1);
+    const Weight g{0.f, 0.f, 0.f, shift};
+    w0 = g.of(counts0, __float_as_uint(y0), z0, powers), w1 = g.of(counts1, __float_as_uint(y1), z1, powers);
   }
 };
 
@@ -983,11 +1014,12 @@ __global__ void __launch_bounds__(kThreads, 4)
 
 // A row by a cluster; called between an arrive at the cluster's barrier and the next.
 // chunk: logits of a CTA; steps: runs of eight per thread, so that the chunk fits the CTA.
-template <typename T>
+// kCuts: there may be a top-k, top-p or min-p (and dyn begins with room for a list).
+template <typename T, bool kCuts>
 __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ logits, int chunk, int steps, const DevCtx& c,
                                            Shared& sh, uint8_t* dyn, int row) {
   u64* list = (u64*)dyn;
-  T* mine = (T*)(dyn + kList * sizeof(u64));
+  T* mine = (T*)(dyn + (kCuts ? kList * sizeof(u64) : 0));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int size = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
   if (tid == 0) sh.listed = 0;
@@ -1011,9 +1043,9 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
   load_runs(0);
   const Settings set(a, row);                      // (while they are on their way)
   const bool ok = set.ok, greedy = set.greedy;
-  const float p = set.p, least = set.least, u = set.u;
-  const int k = set.k;
-  if (tid == 0 && least > 0.f) sh.far = set.far();
+  const float p = kCuts ? set.p : 1.f, least = kCuts ? set.least : 0.f, u = set.u;
+  const int k = kCuts || greedy ? set.k : a.vocab;
+  if (kCuts && tid == 0 && least > 0.f) sh.far = set.far();
   for (int s0 = 0; s0 < steps; s0 += kAhead) {
     if (s0) load_runs(s0);
 #pragma unroll
@@ -1037,7 +1069,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
   // ceil(k / size) threads of each CTA have one.
   const uint32_t best = ordered_key(m);
   uint32_t top = largest_of_cta(best, sh.warp_count);
-  const bool small_k = k <= kSmallK && k < a.vocab;
+  const bool small_k = kCuts && k <= kSmallK && k < a.vocab;
   uint32_t bound = small_k ? reached_by((k + size - 1) / size, best, top, 0) : 0;
   cluster_wait();
   team.exchange(top, bound);
@@ -1058,7 +1090,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
   const Weight weight = set.weight(m, a.bits);
   float cut = greedy ? m : -FLT_MAX;
   if (least > 0.f) cut = fmaxf(__double2float_ru((double)m - sh.far), -FLT_MAX);
-  if (small_k || least > 0.f || (p < 1.f && a.vocab <= kList)) {
+  if (kCuts && (small_k || least > 0.f || (p < 1.f && a.vocab <= kList))) {
     // Few tokens can be kept as a rule, or are there: CTA 0 gets them listed.
     const float low = small_k ? fmaxf(cut, fmaxf(ordered_value(bound), -FLT_MAX)) : cut;
     const uint32_t room = kList / size;
@@ -1117,17 +1149,31 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
     if (ties)
       each_logit([&](float l) { count += l == cut; });
   };
-  const bool cuts = k < a.vocab && !greedy;
+  const bool cuts = kCuts && k < a.vocab && !greedy;
   bool found = !cuts && p >= 1.f;
   if (!greedy) cut = Grid<T>::value(Grid<T>::up(cut));
-  if (found) {                                     // nothing to cut, or the first of the largest
+  const DirectWeight direct(weight);
+  const bool directly = sizeof(T) == 2 && found && !greedy && direct.fits;
+  if (directly) {                                  // nothing to cut
+    cut = next_below<T>(cut), ties = 0;
+    for (int s = 0; s < steps; ++s) {
+      Run<T> run;
+      run.load(x + s * 32 * kVec);
+#pragma unroll
+      for (int j = 0; j < kVec; j += 2) {
+        u64 w0, w1;
+        direct.two(run.get(j), run.get(j + 1), run.get(j) > cut, run.get(j + 1) > cut, w0, w1, sh.powers);
+        sum += w0 + w1;
+      }
+    }
+  } else if (found) {                              // or the first of the largest
     if (!greedy) cut = next_below<T>(cut), ties = 0;
     kept_here();
   }
   // A histogram tells near which logits the cuts lie; CTA 0 gets those listed.  The bins'
   // middles are off by a part in 370 at most, a sum over many bins by much less: 2^-13 of
   // the mass to either side is enough as a rule, 2^-9 the second time.
-  for (float margin = 0x1p-13f; !found && margin <= 0x1p-9f; margin *= 16.f) {
+  for (float margin = 0x1p-13f; kCuts && !found && margin <= 0x1p-9f; margin *= 16.f) {
     uint32_t* hist = (uint32_t*)list;
     static_assert(kBins * 4 <= kList * 8, "the histogram takes the list's place");
     const auto bin_of = [&](float l) { return bin_at(__float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(m, l), -weight.hi), Weight::kY))); };
@@ -1198,7 +1244,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
       }
     }
   }
-  if (!found) {
+  if (kCuts && !found) {
     // Too many near a cut (equal logits, say): bisection over all of them.
     const auto count_of = [&](float v, float w) {
       uint32_t n = 0;
@@ -1309,7 +1355,8 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
         float l0, l1;
         uint32_t y;
         v.get_negative(j, l0, l1);
-        weight.two(l0, l1, l0 < -cut, l1 < -cut, own[j], own[j + 1], y, y, sh.powers);
+        if (directly) direct.two(-l0, -l1, l0 < -cut, l1 < -cut, own[j], own[j + 1], sh.powers);
+        else weight.two(l0, l1, l0 < -cut, l1 < -cut, own[j], own[j + 1], y, y, sh.powers);
         run += own[j] + own[j + 1];
         tie_run += (v.get(j) == cut) + (v.get(j + 1) == cut);
       }
@@ -1354,7 +1401,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
 // kLeft: only the rows that stream_kernel left.  (A grid of all rows whose other CTAs end at
 // once: 3 us for 768 rows of 64,000; fewer clusters that look for rows take 60 % longer
 // where most are left.)
-template <typename T, bool kLeft>
+template <typename T, bool kCuts, bool kLeft>
 __global__ void __launch_bounds__(kThreads, 4)
     sample_kernel(const __grid_constant__ Args a, const T* __restrict__ logits, int chunk, int steps, DevCtx c) {
   extern __shared__ __align__(16) uint8_t dyn[];
@@ -1371,7 +1418,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
     load_powers(sh);
   }
-  sample_row<T>(a, logits, chunk, steps, c, sh, dyn, row);
+  sample_row<T, kCuts>(a, logits, chunk, steps, c, sh, dyn, row);
 }
 
 static int check(const dsa_sampler* p) {
@@ -1401,9 +1448,11 @@ static bool launch(const Args& a, const void* logits, DevCtx c, cudaStream_t st)
   const int places = a.vocab + (whole ? 0 : kVec - 1);
   const int chunk = (places + size * kVec - 1) / (size * kVec) * kVec, step = kThreads * kVec;
   const int steps = (chunk + step - 1) / step;
-  const size_t room = (size_t)steps * step * sizeof(T), smem = kList * 8 + (room > kList * 8 ? room : kList * 8);
+  const bool cuts = a.top_k || a.top_p || a.min_p;
+  const size_t room = (size_t)steps * step * sizeof(T);
+  const size_t smem = cuts ? kList * 8 + std::max(room, (size_t)kList * 8) : room;
   const bool stream = a.rows >= sms && (a.top_k || a.min_p);
-  auto kernel = stream ? sample_kernel<T, true> : sample_kernel<T, false>;
+  auto kernel = stream ? sample_kernel<T, true, true> : cuts ? sample_kernel<T, true, false> : sample_kernel<T, false, false>;
   if (!cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))) return false;
   if (stream && !launch_programmatic(stream_kernel<T>, dim3((unsigned)a.rows), dim3(kThreads), 0, st, 1, a,
                                      (const T*)logits, c))
