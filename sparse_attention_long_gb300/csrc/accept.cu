@@ -1,6 +1,10 @@
 // Acceptance of drafted tokens (dsa_tree_accept): one warp walks a sequence's tree from
 // token 0 along the sampled tokens; when the counts of the sequences before it are known,
-// it writes the kept rows.
+// it writes the kept rows.  Up to 64 tokens are read at once, two per lane, and walked by
+// votes (a load per step took 11.8 us where this takes 5.1).
+//
+// Bound: latency.  One chain of 5 tokens 3.1 us, 256 trees of 17 to 64 tokens 5.1 us: launch, two
+// dependent loads, the walk, and with more than 32 sequences the cluster's barrier.
 #include <algorithm>
 
 #include "dsa_common.cuh"

@@ -1,18 +1,39 @@
 // Sampling of one token per row of logits (dsa_sample): temperature, min-p, top-k,
 // top-p, and a draw by a given uniform number.
 //
-// One thread-block cluster per row; the row stays in shared memory.
 // All three cuts keep a run of the tokens in the order (logit descending, index
 // ascending), so a cut is a logit and a number of tokens that have exactly this logit,
-// lowest index first.  min-p gives its logit outright, from the maximum.  top-k's and
-// top-p's are found by bisection over the logits' order-preserving bits: a step counts
-// (or weighs) the logits above a middle one.
+// lowest index first.  min-p gives its logit outright, from the maximum.
 //
 // Borders between tokens lie dense in a large vocabulary, so fp32 sums would draw
-// neighbours of the right token now and then.  Weights are computed to some 2^-31 of themselves
-// (the exponent in two floats, a table of 2^(j/256) and a short series) and summed as
-// integers, in units of 2^-44 of the largest one or finer: sums are exact, whatever
-// their order.
+// neighbours of the right token now and then (131,072 borders, sums off by 1e-7: one row in
+// fifty).  Weights are computed to 2^-29 of themselves and summed as integers, in units of 2^-44
+// of the largest one or finer: sums are exact, whatever their order, and so is what follows
+// from them.
+//
+// A thread-block cluster per row, as many CTAs as hold it in shared memory, 32 KB each
+// (more for a few rows).  Then one of
+//  - a list, where few tokens can be kept: ceil(k / CTAs) of a CTA's threads have a logit that
+//    reaches a number, so k of the row do, and few more than k reach the smallest such
+//    number; or those that min-p keeps.  CTA 0 gets them and does the rest;
+//  - nothing to cut: one pass of weights;
+//  - a histogram of distances to the maximum in 1/128 powers of two: it tells the bin of the
+//    k-th logit, and by the bins' middles about where top-p's border lies.  One pass of
+//    weights sums exactly what lies above and below; the few logits at the border go to CTA 0,
+//    which finds the cuts;
+//  - bisection over all logits, where too many lie at a cut (equal ones, say);
+// and a draw: the CTA, warp, step, thread and token at which the mass passes its part.
+// With a row for each SM or more, a row that needs but a list is read by one CTA
+// (stream_kernel), which keeps nothing of it but the candidates.
+//
+// Measured (us, calls back to back; in brackets the logits' bytes at 6.8 TB/s): one row of
+// 32,001 fp32, top-k and top-p 6.7 (0.02); 768 rows of 64,000 bf16, top-k and top-p 38 (14.5), of
+// which stream_kernel 33; 256 rows of 131,071 bf16 at a temperature 52 (9.9); 48 rows of 64,000 fp32,
+// top-p alone and large nuclei 46 (1.8); 64 rows of 131,071 bf16, a mixture 31 to 45 (2.5).
+// Bound: the first by the latency of loads and two cluster barriers; stream_kernel by 1.3
+// waves of rows, each 16 us, half of them without loads (settings, bounds, the end); a pass of
+// weights by instructions (20 per bf16 logit, 25 else; 2.4 per cycle and SM); the histogram's
+// path by its seven cluster barriers, 1 us each with what they wait for.
 #include <float.h>
 #include <math.h>
 
@@ -33,7 +54,7 @@ constexpr int kMaxVocab = 1 << 18;
 constexpr int kList = 2048;                        // tokens that one CTA can order, 2^n
 constexpr int kCounted = 256;                      // up to so many by counting, or, of logits alone,
 constexpr int kListed = 512;                       // so many
-constexpr int kSmallK = 1024;                      // top_k up to which candidates are listed
+constexpr int kSmallK = 1024;                      // top_k up to which candidates are listed at first
 
 typedef unsigned long long u64;
 
@@ -148,7 +169,7 @@ struct Weight {
   static constexpr float kY = 12288.f;             // 1.5 * 2^13: steps of 2^-10
   static constexpr float kZ = 0.0029296875f;       // 1.5 * 2^-9: steps of 2^-32
   static constexpr float kLn2 = 0.693147181f, kHalfLn2Sq = 0.240226507f;
-  // -l0, -l1 and whether they count; y0, y1: bits of the step numbers, see Bins
+  // l0, l1: the negated logits, and whether they count; y0, y1: bits of the step numbers, see bin_at
   __device__ __forceinline__ void two(float l0, float l1, bool counts0, bool counts1, u64& w0, u64& w1, uint32_t& y0,
                                       uint32_t& y1, const uint32_t* __restrict__ powers) const {
     const u64 m = pair(max, max), nm = pair(-max, -max), h = pair(hi, hi), nh = pair(-hi, -hi), one = pair(-1.f, -1.f);
@@ -952,9 +973,9 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
     return;
   }
-  const double far = set.least > 0.f ? set.far() : 0.;
+  if (tid == 0 && set.least > 0.f) sh.far = set.far();  // (read behind a barrier)
   const auto cut_at = [&](float m) {
-    return set.greedy ? m : set.least > 0.f ? fmaxf(__double2float_ru((double)m - far), -FLT_MAX) : -FLT_MAX;
+    return set.greedy ? m : set.least > 0.f ? fmaxf(__double2float_ru((double)m - sh.far), -FLT_MAX) : -FLT_MAX;
   };
   float m = -INFINITY, low = -FLT_MAX;
   uint32_t top = 0, bound = 0;

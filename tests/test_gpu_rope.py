@@ -164,6 +164,37 @@ def test_the_gradient_is_the_transposed_call(layout):
         assert abs(quotient - float(inner.sum())) <= (scale + float(inner.abs().sum())) * 2.0 ** -18
 
 
+def test_parts_of_one_buffer_in_place():
+    """Queries and keys as columns of one projection, rotated where they lie; its other columns stay."""
+    dsa = lib()
+    n, H, Hk, D = 37, 8, 2, 64
+    for dtype in ("bf16", "fp32"):
+        both = rand(n, (H + 2 * Hk) * D, seed=5, dtype=dtype)
+        before = both.clone()
+        q, k = both[:, :H * D].view(n, H, D), both[:, H * D:(H + Hk) * D].view(n, Hk, D)
+        r = dsa.make_rope(rot_dim=D, parts=[dsa.rope_part(heads=h, dim=D, layout="half", dtype=dtype) for h in (H, Hk)])
+        pos = list(range(100, 100 + n))
+        dsa.rope_apply(r, torch.tensor(pos, dtype=torch.int32, device=DEV), (q, k))
+        f = R.frequencies(D)
+        check(q, before[:, :H * D].view(n, H, D), pos, f, 0, "half", dtype)
+        check(k, before[:, H * D:(H + Hk) * D].view(n, Hk, D), pos, f, 0, "half", dtype)
+        assert torch.equal(both[:, (H + Hk) * D:], before[:, (H + Hk) * D:])
+
+
+def test_many_passes_and_short_tables():
+    """Enough rows for sixteen passes of a CTA, with one head (a table of few tokens) and with many."""
+    dsa = lib()
+    for n, H, rot in ((70001, 1, 256), (3001, 96, 64), (20011, 3, 32)):
+        r = dsa.make_rope(rot_dim=rot, parts=[dsa.rope_part(heads=H, dim=rot)])
+        x = rand(n, H, rot, seed=n, dtype="bf16")
+        pos = torch.arange(n, dtype=torch.int32, device=DEV) * 17
+        out = torch.empty_like(x)
+        dsa.rope_apply(r, pos, (x,), (out,))
+        i = torch.cat([torch.arange(40), torch.randint(0, n, (60,), generator=torch.Generator().manual_seed(1)),
+                       torch.arange(n - 40, n)])
+        check(out[i.to(DEV)], x[i.to(DEV)], pos.cpu()[i].tolist(), R.frequencies(rot), 0, "interleaved", "bf16")
+
+
 def test_rows_past_four_gigabytes():
     dsa = lib()
     n, D, rot = 3, 64, 64

@@ -279,6 +279,44 @@ def test_large_nuclei(V, spread, T, dtype):
         check(dsa, x, u, dtype=dtype, temperature=[T] * 3, **kw)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_more_wanted_than_there_are(dtype):
+    """A large top_k over a row with few usable logits, in every form of the call."""
+    dsa = lib()
+    x = rand(3, 20000, seed=9)
+    x[0, 1500:] = -INF
+    x[1, ::3], x[1, 1::3] = math.nan, INF
+    x[2, 7:] = -INF
+    u = uniform(3, seed=4)
+    for kw in (dict(top_k=[1501, 19999, 8]), dict(top_k=[1500, 6666, 7]), dict(top_k=[5000, 6000, 2000], top_p=[0.9] * 3),
+               dict(top_p=[0.95] * 3), dict(top_p=[0.95] * 3, min_p=[1e-3] * 3), dict(top_k=[1499, 6665, 6])):
+        check(dsa, x, u, dtype=dtype, **kw)
+    many = x.repeat(60, 1)
+    check(dsa, many, uniform(180, seed=5), dtype=dtype, top_k=[150, 190, 8] * 60)
+
+
+def test_two_calls_at_once():
+    """Nothing is shared between calls: two streams, many rows each."""
+    dsa = lib()
+    n, V = 300, 5001
+    s = dsa.make_sampler(rows=n, vocab=V, dtype="fp32")
+    xs = [rand(n, V, seed=40 + i).float().to(DEV) for i in range(2)]
+    us, k, p = [dev(uniform(n, seed=50 + i)) for i in range(2)], dev([30, 0, 300] * 100, torch.int32), dev([0.9, 0.95, 1.0] * 100)
+    want = []
+    for x, u in zip(xs, us):
+        t = torch.zeros(n, dtype=torch.int32, device=DEV)
+        dsa.sample(s, x, u, None, k, p, None, None, t)
+        want.append(t)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [torch.zeros(n, dtype=torch.int32, device=DEV) for _ in range(2)]
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                dsa.sample(s, xs[i], us[i], None, k, p, None, None, got[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and dsa.get_status() == 0
+
+
 def test_settings_out_of_range():
     dsa = lib()
     x = rand(8, 100, seed=1)
