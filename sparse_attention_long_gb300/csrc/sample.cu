@@ -27,12 +27,11 @@
 // (stream_kernel), which keeps nothing of it but the candidates.
 //
 // Measured (us, calls back to back; in brackets the logits' bytes at 6.8 TB/s): one row of
-// 32,001 fp32, top-k and top-p 6.7 (0.02); 768 rows of 64,000 bf16, top-k and top-p 38 (14.5), of
-// which stream_kernel 33; 256 rows of 131,071 bf16 at a temperature 52 (9.9); 48 rows of 64,000 fp32,
+// 32,001 fp32, top-k and top-p 6.7 (0.02); 768 rows of 64,000 bf16, top-k and top-p 37 (14.5), of
+// which stream_kernel 31; 256 rows of 131,071 bf16 at a temperature 52 (9.9); 48 rows of 64,000 fp32,
 // top-p alone and large nuclei 46 (1.8); 64 rows of 131,071 bf16, a mixture 31 to 45 (2.5).
-// Bound: the first by the latency of loads and two cluster barriers; stream_kernel by 1.3
-// waves of rows, each 16 us, half of them without loads (settings, bounds, the end); a pass of
-// weights by instructions (20 per bf16 logit, 25 else; 2.4 per cycle and SM); the histogram's
+// Bound: the first by the latency of loads and two cluster barriers; stream_kernel by
+// instructions and the phases without loads (settings, bounds, the end); a pass of weights by instructions (20 per bf16 logit, 25 else; 2.4 per cycle and SM); the histogram's
 // path by its seven cluster barriers, 1 us each with what they wait for.
 #include <float.h>
 #include <math.h>
@@ -936,33 +935,49 @@ __device__ __forceinline__ uint32_t largest_of_cta(uint32_t best, uint32_t* __re
 }
 
 // Many rows: one CTA per row, which reads it once and lists what a top_k up to kStreamK or a
-// min-p can keep.  The first 8,192 (fp32: 4,096) logits give a bound that top_k of them reach,
+// min-p can keep.  The first 4,096 (fp32: 2,048) logits give a bound that top_k of them reach,
 // more logits a better one.  Rows that need anything else, or have too many candidates, are
-// left to sample_kernel.
+// left to sample_kernel.  Logits on their way lie in shared memory, so that six CTAs fit an
+// SM's registers.  768 rows of 64,000 bf16: 31 us, 3.1 TB/s; 3,000 instructions per warp, a
+// third of them for settings, bounds and the end, at 2 per cycle and SM.
 constexpr int kStreamK = 192, kLater = -2;
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 6)
     stream_kernel(const __grid_constant__ Args a, const T* __restrict__ logits, DevCtx c) {
   __shared__ Shared sh;
-  __shared__ u64 list[kList], other[kList];
-  constexpr int kRunList = 2 * kList;
+  __shared__ __align__(16) u64 list[kList], other[kList / 2];
+  constexpr int kRunList = kList;
   int* runs = (int*)other;                         // runs with a logit that reached the bound when they were read
-  constexpr int kRuns = sizeof(T) == 2 ? 4 : 2, kGroup = kRuns * kThreads * kVec;
+  // Logits on their way, in the list's place: 64 bytes per thread, in two groups.
+  constexpr int kRuns = 32 / (int)sizeof(Run<T>), kGroup = kRuns * kThreads * kVec;
+  T* ring = (T*)list + threadIdx.x * kVec;
   let_next_launch();
   const int tid = threadIdx.x, row = blockIdx.x;
   load_powers(sh);
   if (tid == 0) sh.listed = sh.rank_in = 0;
   wait_for_earlier();
   const RowOf<T> src(logits + row * a.ld, a.vocab);
-  Run<T> run[kRuns], next[kRuns];
-  const auto load = [&](Run<T>(&r)[kRuns], int at) {
+  const T* mine = src.at + tid * kVec;
+  const uint32_t slot = smem_u32(ring);
+  constexpr int kStep = kThreads * kVec, kPieces = (int)sizeof(Run<T>) / 16;
+  const auto fetch = [&](int at, int half) {       // (each thread looks at what it fetched itself)
+    if (at >= src.skew && at + kGroup <= src.behind) {
 #pragma unroll
-    for (int s = 0; s < kRuns; ++s) {
-      const int i = at + (s * kThreads + tid) * kVec;
-      src.load(r[s], i);
+      for (int s = 0; s < kRuns * kPieces; ++s)
+        cp_async16_cg(slot + (half * kRuns + s / kPieces) * kStep * sizeof(T) + s % kPieces * 16,
+                      (const uint8_t*)(mine + at + s / kPieces * kStep) + s % kPieces * 16);
+    } else if (at < src.behind) {
+#pragma unroll 1
+      for (int s = 0; s < kRuns; ++s) {
+        Run<T> run;
+        src.load(run, at + s * kStep + tid * kVec);
+        run.store(ring + (half * kRuns + s) * kStep);
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  load(run, 0);
+  fetch(0, 0);
+  fetch(kGroup, 1);
   const Settings set(a, row);
   const bool by_k = set.k < a.vocab;
   if (!set.ok || !(by_k ? set.k <= kStreamK : set.least > 0.f)) {
@@ -971,6 +986,7 @@ __global__ void __launch_bounds__(kThreads, 4)
       if (a.prob) a.prob[row] = 0.f;
       if (!set.ok) set_status(c, DSA_ERR_INDEX);
     }
+    cp_async_wait_all();
     return;
   }
   if (tid == 0 && set.least > 0.f) sh.far = set.far();  // (read behind a barrier)
@@ -979,16 +995,27 @@ __global__ void __launch_bounds__(kThreads, 4)
   };
   float m = -INFINITY, low = -FLT_MAX;
   uint32_t top = 0, bound = 0;
-  for (int at = 0, group = 1; at < src.behind; at += kGroup, ++group) {
-    if (at + kGroup < src.behind) load(next, at + kGroup);
+  for (int at = 0, group = 1, bound_at = 1; at < src.behind; at += kGroup, ++group) {
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const int half = (group - 1) & 1;
     float of_run[kRuns];
 #pragma unroll
-    for (int s = 0; s < kRuns; ++s) m = fmaxf(m, of_run[s] = run[s].clean());
-    if ((group & (group - 1)) == 0 || at + kGroup >= src.behind) {
+    for (int s = 0; s < kRuns; ++s) {
+      Run<T> run;
+      run.load(ring + (half * kRuns + s) * kThreads * kVec);
+      m = fmaxf(m, of_run[s] = run.clean());
+    }
+    // (m, which is never +inf, is known when the logits have been read: only then new ones may come)
+    if (m < INFINITY) fetch(at + 2 * kGroup, half);
+    const bool last = at + kGroup >= src.behind;
+    if (group == bound_at || last) {               // after 1, 3, 9, ... groups and the last
+      bound_at *= 3;
       const uint32_t best = ordered_key(m);
-      top = largest_of_cta(best, sh.warp_count);
-      if (by_k) bound = reached_by(set.k, best, top, bound);
-      low = fmaxf(cut_at(ordered_value(top)), fmaxf(ordered_value(bound), -FLT_MAX));
+      const bool by_top = group == 1 || last || !by_k || set.k == 1;
+      if (by_top) top = largest_of_cta(best, sh.warp_count);
+      if (by_k) bound = reached_by(set.k, best, by_top ? top : 0xFFFFFFF0u, bound);
+      low = fmaxf(low, ordered_value(bound));      // (a bound once found holds)
+      if (by_top) low = fmaxf(low, cut_at(ordered_value(top)));
       __syncthreads();
     }
 #pragma unroll
@@ -997,9 +1024,8 @@ __global__ void __launch_bounds__(kThreads, 4)
         const uint32_t to = atomicAdd(&sh.listed, 1u);
         if (to < kRunList) runs[to] = at + (s * kThreads + tid) * kVec;
       }
-#pragma unroll
-    for (int s = 0; s < kRuns; ++s) run[s] = next[s];
   }
+  cp_async_wait_all();
   __syncthreads();
   m = ordered_value(top);
   const int n = (int)sh.listed;
@@ -1012,16 +1038,17 @@ __global__ void __launch_bounds__(kThreads, 4)
   }
   for (int i = tid; i < n; i += kThreads) {        // the logits that reach the last bound
     const int at = runs[i];
-    src.load(run[0], at);
-    run[0].clean();
+    Run<T> run;
+    src.load(run, at);
+    run.clean();
     uint32_t hits = 0;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) hits |= (uint32_t)(run[0].get(j) >= low) << j;
+    for (int j = 0; j < kVec; ++j) hits |= (uint32_t)(run.get(j) >= low) << j;
     uint32_t to = hits ? atomicAdd(&sh.rank_in, __popc(hits)) : 0;
 #pragma unroll
     for (int j = 0; j < kVec; ++j)
       if (hits >> j & 1) {
-        if (to < kList) list[to] = make_key(run[0].get(j), (uint32_t)(at + j - src.skew));
+        if (to < kList) list[to] = make_key(run.get(j), (uint32_t)(at + j - src.skew));
         ++to;
       }
   }
