@@ -15,7 +15,8 @@
 // (more for a few rows).  Then one of
 //  - a list, where few tokens can be kept: ceil(k / CTAs) of a CTA's threads have a logit that
 //    reaches a number, so k of the row do, and few more than k reach the smallest such
-//    number; or those that min-p keeps.  CTA 0 gets them and does the rest;
+//    number; or those that min-p keeps; or, of logits in the thousands for their temperature,
+//    those that weigh anything.  CTA 0 gets them and does the rest;
 //  - nothing to cut: one pass of weights;
 //  - a histogram of distances to the maximum in 1/128 powers of two: it tells the bin of the
 //    k-th logit, and by the bins' middles about where top-p's border lies.  One pass of
@@ -28,15 +29,18 @@
 //
 // Measured (us, calls back to back; in brackets the logits' bytes at 6.8 TB/s): one row of
 // 32,001 fp32, top-k and top-p 6.7 (0.02); 768 rows of 64,000 bf16, top-k and top-p 37 (14.5), of
-// which stream_kernel 31; 256 rows of 131,071 bf16 at a temperature 52 (9.9); 48 rows of 64,000 fp32,
-// top-p alone and large nuclei 46 (1.8); 64 rows of 131,071 bf16, a mixture 31 to 45 (2.5).
+// which stream_kernel 31; 256 rows of 131,071 bf16 at a temperature 51 (9.9); 48 rows of 64,000 fp32,
+// top-p alone and large nuclei 47 (1.8); 64 rows of 131,071 bf16, top-p alone 52, a mixture 31 to
+// 43 (2.5), all at a temperature of 0.01 13.
 // Bound: the first by the latency of loads and two cluster barriers; stream_kernel by
-// instructions and the phases without loads (settings, bounds, the end); a pass of weights by instructions (20 per bf16 logit, 25 else; 2.4 per cycle and SM); the histogram's
-// path by its seven cluster barriers, 1 us each with what they wait for.
+// instructions and the phases without loads (settings, bounds, the end); a pass of weights by instructions (20 per
+// bf16 logit, 25 else; 2.4 per cycle and SM); the histogram's path by such a pass and its seven
+// cluster barriers, 1 us each with what they wait for.
 #include <float.h>
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "dsa_common.cuh"
 
@@ -168,11 +172,11 @@ struct Weight {
   static constexpr float kY = 12288.f;             // 1.5 * 2^13: steps of 2^-10
   static constexpr float kZ = 0.0029296875f;       // 1.5 * 2^-9: steps of 2^-32
   static constexpr float kLn2 = 0.693147181f, kHalfLn2Sq = 0.240226507f;
-  // l0, l1: the negated logits, and whether they count; y0, y1: bits of the step numbers, see bin_at
+  // whether l0 and l1 count; y0, y1: bits of the step numbers, see bin_at
   __device__ __forceinline__ void two(float l0, float l1, bool counts0, bool counts1, u64& w0, u64& w1, uint32_t& y0,
                                       uint32_t& y1, const uint32_t* __restrict__ powers) const {
     const u64 m = pair(max, max), nm = pair(-max, -max), h = pair(hi, hi), nh = pair(-hi, -hi), one = pair(-1.f, -1.f);
-    const u64 nl = pair(l0, l1);
+    const u64 nl = pair(-l0, -l1);
     const u64 d = add2(m, nl), t = add2(d, nm);
     const u64 e = add2(fma2(fma2(t, one, d), one, m), fma2(t, one, nl));
     const u64 nx = mul2(d, nh);
@@ -188,19 +192,24 @@ struct Weight {
   __device__ __forceinline__ u64 operator()(float l, const uint32_t* __restrict__ powers) const {
     u64 a, b;
     uint32_t y;
-    two(-l, -l, true, false, a, b, y, y, powers);
+    two(l, l, true, false, a, b, y, y, powers);
     return a;
   }
+  __device__ __forceinline__ uint32_t step(float l) const {
+    return __float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(max, l), -hi), kY));
+  }
+  __device__ __forceinline__ bool fits() const { return true; }
 };
 
 // The same for bf16 logits that are not too large, with fewer steps: a logit's eight bits
 // times sixteen of the scale is exact, so l * scale - max * scale needs no exact
-// difference first.  (20 instead of 25 instructions per logit: 256 rows of 131,071 52 us instead of 59.)
+// difference first.  (20 instead of 25 instructions per logit: 256 rows of 131,071 52 us
+// instead of 59, with top-p alone 150 instead of 169.)
 // A row's weights are all of one kind.
 struct DirectWeight {
   float high, low, from, left;                     // scale in 16 bits and the rest; kY - max * scale in two parts
   int shift;
-  bool fits;
+  bool small;
   __device__ __forceinline__ explicit DirectWeight(const Weight& w) {
     high = __uint_as_float(__float_as_uint(w.hi) & 0xFFFFFF00u);
     low = __fadd_rn(__fsub_rn(w.hi, high), w.lo);
@@ -208,10 +217,11 @@ struct DirectWeight {
     from = __fsub_rn(Weight::kY, q);               // both multiples of 2^-10 below 2^14: exact
     left = __fmaf_rn(-w.max, low, __fsub_rn(q, t));
     shift = w.shift;
-    fits = fabsf(w.max) * w.hi < 2000.f;
+    small = fabsf(w.max) * w.hi < 2000.f;
   }
-  __device__ __forceinline__ void two(float l0, float l1, bool counts0, bool counts1, u64& w0, u64& w1,
-                                      const uint32_t* __restrict__ powers) const {
+  __device__ __forceinline__ bool fits() const { return small; }
+  __device__ __forceinline__ void two(float l0, float l1, bool counts0, bool counts1, u64& w0, u64& w1, uint32_t& s0,
+                                      uint32_t& s1, const uint32_t* __restrict__ powers) const {
     const u64 l = pair(l0, l1), t = mul2(l, pair(high, high));
     const u64 y = add2(t, pair(from, from)), q = add2(y, pair(-from, -from));
     const u64 r = add2(fma2(q, pair(-1.f, -1.f), t), fma2(l, pair(low, low), pair(left, left)));
@@ -221,7 +231,15 @@ struct DirectWeight {
     halves(y, y0, y1), halves(z, z0, z1);
     const Weight g{0.f, 0.f, 0.f, shift};
     w0 = g.of(counts0, __float_as_uint(y0), z0, powers), w1 = g.of(counts1, __float_as_uint(y1), z1, powers);
+    s0 = __float_as_uint(y0), s1 = __float_as_uint(y1);
   }
+  __device__ __forceinline__ u64 operator()(float l, const uint32_t* __restrict__ powers) const {
+    u64 a, b;
+    uint32_t y;
+    two(l, l, true, false, a, b, y, y, powers);
+    return a;
+  }
+  __device__ __forceinline__ uint32_t step(float l) const { return __float_as_uint(__fadd_rn(__fmul_rn(l, high), from)); }
 };
 
 // p * z rounded up or down to an integer, for a float 0 <= p <= 1
@@ -352,7 +370,6 @@ struct Run<float> {
     for (int j = 0; j < 8; ++j) w[j] = j >= lo && j < hi ? __float_as_uint(p[j]) : kNone;
   }
   __device__ __forceinline__ float get(int j) const { return __uint_as_float(w[j]); }
-  __device__ __forceinline__ void get_negative(int j, float& a, float& b) const { a = -get(j), b = -get(j + 1); }
   __device__ __forceinline__ float largest() const {
     float m = get(0);
 #pragma unroll
@@ -390,10 +407,6 @@ struct Run<__nv_bfloat16> {
   }
   __device__ __forceinline__ float get(int j) const {
     return __uint_as_float((j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
-  }
-  __device__ __forceinline__ void get_negative(int j, float& a, float& b) const {
-    const uint32_t v = w[j >> 1] ^ 0x80008000u;
-    a = __uint_as_float(v << 16), b = __uint_as_float(v & 0xFFFF0000u);
   }
   static __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
     uint32_t r;
@@ -550,30 +563,32 @@ __device__ __forceinline__ void choose_bins(Shared& s, const uint32_t* __restric
 
 // The masses of a thread's logits from the cut on: of those in bins before b1 and of those
 // between b2 and bk; list(logit, step) for the others up to bk.
-template <typename T, typename F>
-__device__ __forceinline__ void mass_around(const T* x, int steps, float cut, const Weight& weight,
+template <typename T, typename W, typename F>
+__device__ __forceinline__ void mass_around(const T* x, int steps, float cut, const W& weight,
                                             const uint32_t* __restrict__ powers, int b1, int b2, int bk, u64& above,
                                             u64& between, F list) {
-  const uint32_t span = (uint32_t)(b2 - b1);
+  // (bins as ranges of steps: bin b begins 8 b steps below kY, the last one ends nowhere)
+  const auto begin = [](int b) { return __uint_as_float(__float_as_uint(Weight::kY) - 8 * (uint32_t)b); };
+  const auto end = [&](int b) { return b < kBins - 1 ? __uint_as_float(__float_as_uint(begin(b)) - 7) : -INFINITY; };
+  const float begin1 = begin(b1), end2 = end(b2), begin_k = bk < kBins ? begin(bk) : -INFINITY,
+              end_k = bk < kBins ? end(bk) : INFINITY;
   for (int s = 0; s < steps; ++s) {
     Run<T> run;
     run.load(x + s * 32 * kVec);
     uint32_t hits = 0;
 #pragma unroll
     for (int j = 0; j < kVec; j += 2) {
-      float l[2];
       u64 w[2];
       uint32_t y[2];
-      run.get_negative(j, l[0], l[1]);
-      const bool in[2] = {l[0] <= -cut, l[1] <= -cut};
+      const float l[2] = {run.get(j), run.get(j + 1)};
+      const bool in[2] = {l[0] >= cut, l[1] >= cut};
       weight.two(l[0], l[1], in[0], in[1], w[0], w[1], y[0], y[1], powers);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int b = bin_at(y[i]);
-        const bool listed = (uint32_t)(b - b1) <= span || b == bk;
-        hits |= (uint32_t)(listed && in[i]) << (j + i);
-        if (b < b1) above += w[i];
-        else if (!listed && b < bk) between += w[i];
+        const float at = __uint_as_float(y[i]);
+        if (at > begin1) above += w[i];
+        else if (at < end2 && at > begin_k) between += w[i];
+        else if (at >= end2 || at >= end_k) hits |= (uint32_t)in[i] << (j + i);
       }
     }
     if (hits) list(s, hits);
@@ -749,8 +764,8 @@ __device__ __forceinline__ void finish(const Args& a, Shared& s, const Weight& w
 // logit at the cut and how many equal to it are kept.  bin bk, where there is one, keeps
 // its first rank_in; then p as in top-p, among the bins up to b2 (or in bk at its cut).
 // below: less than all of them.  False: top-p's border is not among them.
-template <typename B>
-__device__ __forceinline__ bool cut_of_few(Shared& s, const Weight& weight, B bin_of, float* __restrict__ values, int n,
+template <typename W, typename B>
+__device__ __forceinline__ bool cut_of_few(Shared& s, const W& weight, B bin_of, float* __restrict__ values, int n,
                                            float below, int b2, int bk, uint32_t rank_in, float p, u64 above, u64 between,
                                            float& cut, uint32_t& ties) {
   float* sorted = values + 1024;
@@ -790,8 +805,8 @@ __device__ __forceinline__ bool cut_of_few(Shared& s, const Weight& weight, B bi
   ties = (uint32_t)(__syncthreads_count(i0 < kept && sorted[i0] == cut) + __syncthreads_count(i1 < kept && sorted[i1] == cut));
   return true;
 }
-template <typename T, typename B>
-__device__ __forceinline__ bool cut_of_many(Team& team, const Weight& weight, B bin_of, const float* __restrict__ values,
+template <typename T, typename W, typename B>
+__device__ __forceinline__ bool cut_of_many(Team& team, const W& weight, B bin_of, const float* __restrict__ values,
                                             int n, float below, int b2, int bk, uint32_t rank_in, float p, u64 above,
                                             u64 between, float& cut, uint32_t& ties) {
   Shared& s = team.s;
@@ -1138,7 +1153,13 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
   const Weight weight = set.weight(m, a.bits);
   float cut = greedy ? m : -FLT_MAX;
   if (least > 0.f) cut = fmaxf(__double2float_ru((double)m - sh.far), -FLT_MAX);
-  if (kCuts && (small_k || least > 0.f || (p < 1.f && a.vocab <= kList))) {
+  using Fine = typename std::conditional<sizeof(T) == 2, DirectWeight, Weight>::type;
+  const Fine fine(weight);
+  // Logits too large for it at their temperature are far apart: what is 64 powers of two
+  // below the largest weighs nothing, and few are not.
+  const bool cold = kCuts && !greedy && !fine.fits();
+  if (cold) cut = fmaxf(cut, m - 64.f / weight.hi);
+  if (kCuts && (small_k || cold || least > 0.f || (p < 1.f && a.vocab <= kList))) {
     // Few tokens can be kept as a rule, or are there: CTA 0 gets them listed.
     const float low = small_k ? fmaxf(cut, fmaxf(ordered_value(bound), -FLT_MAX)) : cut;
     const uint32_t room = kList / size;
@@ -1179,52 +1200,39 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
   // Any number of tokens.
   u64 sum = 0;                                     // this thread's part of what is kept: logits above the cut,
   uint32_t count = 0, ties = greedy ? 1u : 0x7FFFFFFFu;  // and those equal to it
-  const auto kept_here = [&] {
+  const auto keep = [&](const auto& weight) {
     sum = 0, count = 0;
     for (int s = 0; s < steps; ++s) {
       Run<T> run;
       run.load(x + s * 32 * kVec);
 #pragma unroll
       for (int j = 0; j < kVec; j += 2) {
-        float l0, l1;
         u64 w0, w1;
         uint32_t y;
-        run.get_negative(j, l0, l1);
-        weight.two(l0, l1, l0 < -cut, l1 < -cut, w0, w1, y, y, sh.powers);
+        weight.two(run.get(j), run.get(j + 1), run.get(j) > cut, run.get(j + 1) > cut, w0, w1, y, y, sh.powers);
         sum += w0 + w1;
       }
     }
     if (ties)
       each_logit([&](float l) { count += l == cut; });
   };
+  // a row's weights are of one kind, from here on to its end
+  bool finely = !greedy && fine.fits();
   const bool cuts = kCuts && k < a.vocab && !greedy;
   bool found = !cuts && p >= 1.f;
   if (!greedy) cut = Grid<T>::value(Grid<T>::up(cut));
-  const DirectWeight direct(weight);
-  const bool directly = sizeof(T) == 2 && found && !greedy && direct.fits;
-  if (directly) {                                  // nothing to cut
-    cut = next_below<T>(cut), ties = 0;
-    for (int s = 0; s < steps; ++s) {
-      Run<T> run;
-      run.load(x + s * 32 * kVec);
-#pragma unroll
-      for (int j = 0; j < kVec; j += 2) {
-        u64 w0, w1;
-        direct.two(run.get(j), run.get(j + 1), run.get(j) > cut, run.get(j + 1) > cut, w0, w1, sh.powers);
-        sum += w0 + w1;
-      }
-    }
-  } else if (found) {                              // or the first of the largest
+  if (found) {                                     // nothing to cut, or the first of the largest
     if (!greedy) cut = next_below<T>(cut), ties = 0;
-    kept_here();
+    if (finely) keep(fine);
+    else keep(weight);
   }
   // A histogram tells near which logits the cuts lie; CTA 0 gets those listed.  The bins'
   // middles are off by a part in 370 at most, a sum over many bins by much less: 2^-13 of
   // the mass to either side is enough as a rule, 2^-9 the second time.
-  for (float margin = 0x1p-13f; kCuts && !found && margin <= 0x1p-9f; margin *= 16.f) {
+  for (float margin = 0x1p-13f; kCuts && finely && !found && margin <= 0x1p-9f; margin *= 16.f) {
     uint32_t* hist = (uint32_t*)list;
     static_assert(kBins * 4 <= kList * 8, "the histogram takes the list's place");
-    const auto bin_of = [&](float l) { return bin_at(__float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(m, l), -weight.hi), Weight::kY))); };
+    const auto bin_of = [&](float l) { return bin_at(fine.step(l)); };
     __syncthreads();
     if (tid == 0) sh.listed = 0;
     for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
@@ -1243,7 +1251,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
     const uint32_t room = 2 * kList / size;
     u64 above = 0, between = 0;                    // exact masses of what lies above and between the listed bins
     uint32_t with = 0;                             // steps with listed logits
-    mass_around<T>(x, steps, cut, weight, sh.powers, b1, b2, bk, above, between, [&](int s, uint32_t hits) {
+    mass_around<T>(x, steps, cut, fine, sh.powers, b1, b2, bk, above, between, [&](int s, uint32_t hits) {
       with |= 1u << s;
       uint32_t to = atomicAdd(&sh.listed, __popc(hits));
       for (; hits && to < room; hits &= hits - 1) values[to++] = to_f32(x[s * 32 * kVec + __ffs(hits) - 1]);
@@ -1268,9 +1276,9 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
       __syncthreads();
       float at_cut;
       uint32_t tied;
-      const bool right = n <= kListed ? cut_of_few(sh, weight, bin_of, values, n, next_below<T>(cut), b2, bk, rank_in, p,
+      const bool right = n <= kListed ? cut_of_few(sh, fine, bin_of, values, n, next_below<T>(cut), b2, bk, rank_in, p,
                                                     above, between, at_cut, tied)
-                                      : cut_of_many<T>(team, weight, bin_of, values, n, next_below<T>(cut), b2, bk,
+                                      : cut_of_many<T>(team, fine, bin_of, values, n, next_below<T>(cut), b2, bk,
                                                         rank_in, p, above, between, at_cut, tied);
       if (tid < size) store_remote(&sh.note, tid, right ? (u64)__float_as_uint(at_cut) << 32 | tied : ~0ull);
     }
@@ -1286,7 +1294,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
           const float l = run.get(j);
-          if (l > cut && is_listed(bin_of(l))) sum += weight(l, sh.powers);
+          if (l > cut && is_listed(bin_of(l))) sum += fine(l, sh.powers);
           count += l == cut;
         }
       }
@@ -1294,6 +1302,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
   }
   if (kCuts && !found) {
     // Too many near a cut (equal logits, say): bisection over all of them.
+    finely = false;
     const auto count_of = [&](float v, float w) {
       uint32_t n = 0;
       u64 none = 0;
@@ -1308,7 +1317,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
       cut = bisect<T>(Grid<T>::up(cut), end, (uint32_t)k, over, count_of);
       ties = k - over;
     }
-    kept_here();
+    keep(weight);
     if (p < 1.f) {
       u64 mass = sum;
       uint32_t tied = count;
@@ -1331,12 +1340,12 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
         });
         const u64 one = weight(cut, sh.powers);
         ties = (uint32_t)((want - over + one - 1) / one);
-        kept_here();
+        keep(weight);
       }
     }
   }
   // What each warp keeps, in the order of the tokens.
-  const u64 each = ties ? weight(cut, sh.powers) : 0;
+  const u64 each = !ties ? 0 : finely ? fine(cut, sh.powers) : weight(cut, sh.powers);
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   count = __reduce_add_sync(0xFFFFFFFFu, count);
   if (lane == 0) sh.warp_sum[warp] = sum, sh.warp_count[warp] = count;
@@ -1400,11 +1409,10 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
       v.load(at_x + s * 32 * kVec);
 #pragma unroll
       for (int j = 0; j < kVec; j += 2) {
-        float l0, l1;
+        const float l0 = v.get(j), l1 = v.get(j + 1);
         uint32_t y;
-        v.get_negative(j, l0, l1);
-        if (directly) direct.two(-l0, -l1, l0 < -cut, l1 < -cut, own[j], own[j + 1], sh.powers);
-        else weight.two(l0, l1, l0 < -cut, l1 < -cut, own[j], own[j + 1], y, y, sh.powers);
+        if (finely) fine.two(l0, l1, l0 > cut, l1 > cut, own[j], own[j + 1], y, y, sh.powers);
+        else weight.two(l0, l1, l0 > cut, l1 > cut, own[j], own[j + 1], y, y, sh.powers);
         run += own[j] + own[j + 1];
         tie_run += (v.get(j) == cut) + (v.get(j + 1) == cut);
       }

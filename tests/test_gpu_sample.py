@@ -280,6 +280,24 @@ def test_large_nuclei(V, spread, T, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [900, 20011, 131071])
+def test_cold_rows(V, dtype):
+    """Logits / temperature in the thousands: few tokens weigh anything, or many equal ones do."""
+    dsa = lib()
+    x = rand(12, V, seed=V + 1, scale=4.0)
+    x[6:9] += 1000.0
+    x[9:] = (x[9:] * 0.25).round() * 4.0
+    x[11] = 40.0
+    T = [0.01, 0.003, 0.0005, 0.01, 0.02, 0.003, 1.0, 0.7, 0.05, 0.01, 0.001, 0.02]
+    u = [0.5 + 2.0 ** -12] * 3 + uniform(8, seed=V + 5) + [0.75]
+    for p in (0.91, 0.23):
+        check(dsa, x[:11], u[:11], temperature=T[:11], top_p=[p] * 11, dtype=dtype)
+    check(dsa, x[:11], u[:11], temperature=T[:11], top_k=[300] * 11, top_p=[0.95] * 11, dtype=dtype)
+    check(dsa, x[:11], u[:11], temperature=T[:11], top_k=[V // 2] * 11, dtype=dtype)
+    check(dsa, x[11:], u[11:], temperature=T[11:], top_p=[0.5], dtype=dtype, exact=True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_more_wanted_than_there_are(dtype):
     """A large top_k over a row with few usable logits, in every form of the call."""
     dsa = lib()
