@@ -30,7 +30,7 @@
 // Measured (us, calls back to back; in brackets the logits' bytes at 6.8 TB/s): one row of
 // 32,001 fp32, top-k and top-p 6.7 (0.02); 768 rows of 64,000 bf16, top-k and top-p 37 (14.5), of
 // which stream_kernel 31; 256 rows of 131,071 bf16 at a temperature 51 (9.9); 48 rows of 64,000 fp32,
-// top-p alone and large nuclei 47 (1.8); 64 rows of 131,071 bf16, top-p alone 52, a mixture 31 to
+// top-p alone and large nuclei 47 (1.8); 64 rows of 131,071 bf16, top-p alone 49, a mixture 31 to
 // 43 (2.5), all at a temperature of 0.01 13.
 // Bound: the first by the latency of loads and two cluster barriers; stream_kernel by
 // instructions and the phases without loads (settings, bounds, the end); a pass of weights by instructions (20 per
@@ -768,23 +768,41 @@ template <typename W, typename B>
 __device__ __forceinline__ bool cut_of_few(Shared& s, const W& weight, B bin_of, float* __restrict__ values, int n,
                                            float below, int b2, int bk, uint32_t rank_in, float p, u64 above, u64 between,
                                            float& cut, uint32_t& ties) {
+  // A logit's place is the number of larger ones, and of equal ones in any order.
+  static_assert(kListed == 2 * kThreads, "two per thread");
   float* sorted = values + 1024;
+  uint32_t* equal = (uint32_t*)sorted + kListed;
   u64* masses = (u64*)(values + 2048);
-  const int tid = threadIdx.x;
-  int before_k = 0, in_p = 0;
-  for (int i = tid; i < kListed; i += kThreads) {  // (as often for every thread: they count together)
-    if (i - tid >= n) break;
-    const float l = i < n ? values[i] : 0.f;
-    const int bin = i < n ? bin_of(l) : kBins + 1;
-    int place = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) place += values[j] > l || (values[j] == l && j < i);
-    if (i < n) {
-      sorted[place] = l;
-      masses[place] = weight(l, s.powers);
+  const int tid = threadIdx.x, second = tid + kThreads;
+  const bool in0 = tid < n, in1 = second < n;
+  const float l0 = in0 ? values[tid] : 0.f, l1 = in1 ? values[second] : 0.f;
+  if (tid < 4) values[n + tid] = -INFINITY;
+  equal[tid] = equal[second] = 0;
+  __syncthreads();
+  int place0 = 0, place1 = 0;
+  if (n <= kThreads) {
+    if (in0)
+      for (int j = 0; j < n; j += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(values + j);
+        place0 += (v.x > l0) + (v.y > l0) + (v.z > l0) + (v.w > l0);
+      }
+  } else {
+    for (int j = 0; j < n; j += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(values + j);
+      place0 += (v.x > l0) + (v.y > l0) + (v.z > l0) + (v.w > l0);
+      place1 += (v.x > l1) + (v.y > l1) + (v.z > l1) + (v.w > l1);
     }
-    before_k += __syncthreads_count(bin < bk), in_p += __syncthreads_count(bin <= b2);
   }
+  const auto put = [&](float l, int place) {
+    place += (int)atomicAdd(&equal[place], 1u);
+    sorted[place] = l;
+    masses[place] = weight(l, s.powers);
+  };
+  if (in0) put(l0, place0);
+  if (in1) put(l1, place1);
+  const int bin0 = in0 ? bin_of(l0) : kBins + 1, bin1 = in1 ? bin_of(l1) : kBins + 1;
+  const int before_k = __syncthreads_count(bin0 < bk) + __syncthreads_count(bin1 < bk);
+  const int in_p = __syncthreads_count(bin0 <= b2) + __syncthreads_count(bin1 <= b2);
   const int limit = bk < kBins ? before_k + (int)rank_in : n;
   // two neighbours per thread
   const int i0 = 2 * tid, i1 = i0 + 1;
