@@ -30,12 +30,12 @@
 // Measured (us, calls back to back; in brackets the logits' bytes at 6.8 TB/s): one row of
 // 32,001 fp32, top-k and top-p 6.7 (0.02); 768 rows of 64,000 bf16, top-k and top-p 37 (14.5), of
 // which stream_kernel 31; 256 rows of 131,071 bf16 at a temperature 51 (9.9); 48 rows of 64,000 fp32,
-// top-p alone and large nuclei 47 (1.8); 64 rows of 131,071 bf16, top-p alone 49, a mixture 31 to
+// top-p alone and large nuclei 37 (1.8); 64 rows of 131,071 bf16, top-p alone 46, a mixture 31 to
 // 43 (2.5), all at a temperature of 0.01 13.
 // Bound: the first by the latency of loads and two cluster barriers; stream_kernel by
-// instructions and the phases without loads (settings, bounds, the end); a pass of weights by instructions (20 per
-// bf16 logit, 25 else; 2.4 per cycle and SM); the histogram's path by such a pass and its seven
-// cluster barriers, 1 us each with what they wait for.
+// instructions and the phases without loads (settings, bounds, the end); a pass of weights by
+// instructions (20 per bf16 logit, 25 else; 2.4 per cycle and SM); the histogram's path by
+// such a pass and its seven cluster barriers, 1 us each with what they wait for.
 #include <float.h>
 #include <math.h>
 
@@ -204,7 +204,7 @@ struct Weight {
 // The same for bf16 logits that are not too large, with fewer steps: a logit's eight bits
 // times sixteen of the scale is exact, so l * scale - max * scale needs no exact
 // difference first.  (20 instead of 25 instructions per logit: 256 rows of 131,071 52 us
-// instead of 59, with top-p alone 150 instead of 169.)
+// instead of 59, with top-p alone 148 instead of 169.)
 // A row's weights are all of one kind.
 struct DirectWeight {
   float high, low, from, left;                     // scale in 16 bits and the rest; kY - max * scale in two parts
@@ -481,10 +481,11 @@ __device__ __forceinline__ void sum_histograms(uint32_t* __restrict__ hist, int 
 
 // The choice of bins.  bin[2]: where the k-th logit lies (kBins: none does), rank_in of
 // its bin's tokens are kept; bin[0] to bin[1]: where top-p's border lies, by the counts and
-// the weights of the bins' middles, with a part `margin` of the mass to either side.  Who
-// has the exact sums looks whether the border lies there.
+// the weights of the bins' middles, with a part `margin` of the mass to either side, or, if
+// more than `limit` tokens lie there, less of it, down to 2^-13.  Who has the exact sums
+// looks whether the border lies there.
 __device__ __forceinline__ void choose_bins(Shared& s, const uint32_t* __restrict__ hist, int k, bool cuts, float p,
-                                            float margin, uint32_t& rank_in) {
+                                            float margin, uint32_t limit, uint32_t& rank_in) {
   constexpr int kMine = kBins / kThreads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t n[kMine];
@@ -539,22 +540,38 @@ __device__ __forceinline__ void choose_bins(Shared& s, const uint32_t* __restric
   rank_in = 0;
   if (s.bin[2] < kBins) rank_in = s.rank_in, z = s.z;
   if (p < 1.f) {
-    const float from = p * z * (1.f - margin), upto = p * z * (1.f + margin);
-    float a = m_run;
-    int b1 = kBins - 1, b2 = kBins - 1;
-    // (sums of other threads may differ in the last bits: a little more of them look)
-    if (m_run <= upto * 1.001f && m_run + mass >= from * 0.999f) {
+    for (;; margin *= margin > 0x1p-12f ? 0.25f : 0.5f) {
+      const float from = p * z * (1.f - margin), upto = p * z * (1.f + margin);
+      float a = m_run;
+      int b1 = kBins - 1, b2 = kBins - 1;
+      // (sums of other threads may differ in the last bits: a little more of them look)
+      if (m_run <= upto * 1.001f && m_run + mass >= from * 0.999f) {
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        a += w[i];
-        if (a >= from) b1 = min(b1, tid * kMine + i);
-        if (a >= upto) b2 = min(b2, tid * kMine + i);
+        for (int i = 0; i < kMine; ++i) {
+          a += w[i];
+          if (a >= from) b1 = min(b1, tid * kMine + i);
+          if (a >= upto) b2 = min(b2, tid * kMine + i);
+        }
       }
+      if (b1 < kBins - 1) atomicMin(&s.bin[0], b1);
+      if (b2 < kBins - 1) atomicMin(&s.bin[1], b2);
+      __syncthreads();
+      b1 = min(s.bin[0], s.bin[2]), b2 = max(b1, min(s.bin[1], s.bin[2]));
+      uint32_t in = 0;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i)
+        if (b1 <= tid * kMine + i && tid * kMine + i <= b2) in += n[i];
+      in = __reduce_add_sync(0xFFFFFFFFu, in);
+      if (lane == 0) s.warp_count[warp] = in;
+      __syncthreads();
+      in = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) in += s.warp_count[i];
+      const bool enough = in <= limit || margin <= 0x1p-13f;
+      if (tid < 2) s.bin[tid] = !enough ? kBins - 1 : tid ? b2 : b1;
+      if (enough) break;
+      __syncthreads();
     }
-    if (b1 < kBins - 1) atomicMin(&s.bin[0], b1);
-    if (b2 < kBins - 1) atomicMin(&s.bin[1], b2);
-    __syncthreads();
-    if (tid == 0) s.bin[0] = min(s.bin[0], s.bin[2]), s.bin[1] = max(s.bin[0], min(s.bin[1], s.bin[2]));
   } else if (tid == 0) {
     s.bin[0] = s.bin[1] = s.bin[2];
   }
@@ -1245,9 +1262,10 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
     else keep(weight);
   }
   // A histogram tells near which logits the cuts lie; CTA 0 gets those listed.  The bins'
-  // middles are off by a part in 370 at most, a sum over many bins by much less: 2^-13 of
-  // the mass to either side is enough as a rule, 2^-9 the second time.
-  for (float margin = 0x1p-13f; kCuts && finely && !found && margin <= 0x1p-9f; margin *= 16.f) {
+  // middles are off by a part in 370 at most, a sum over many bins by much less: 2^-11 of
+  // the mass to either side is enough as a rule, 2^-8 the second time.  (48 rows of 64,000 37
+  // us; from 2^-13 on 46, as 3 rows need a second time; from 2^-8 on 45, as lists get longer.)
+  for (int time = 0; kCuts && finely && !found && time < 2; ++time) {
     uint32_t* hist = (uint32_t*)list;
     static_assert(kBins * 4 <= kList * 8, "the histogram takes the list's place");
     const auto bin_of = [&](float l) { return bin_at(fine.step(l)); };
@@ -1262,7 +1280,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
     sum_histograms(hist, rank, size);
     cluster_sync_all();
     uint32_t rank_in = 0;
-    choose_bins(sh, hist, k, cuts, p, margin, rank_in);
+    choose_bins(sh, hist, k, cuts, p, time ? 0x1p-8f : 0x1p-11f, time ? 2 * kList : kCounted, rank_in);
     const int b1 = sh.bin[0], b2 = sh.bin[1], bk = sh.bin[2];
     const auto is_listed = [&](int b) { return (uint32_t)(b - b1) <= (uint32_t)(b2 - b1) || b == bk; };
     float* values = (float*)list;                  // in the histogram's place
