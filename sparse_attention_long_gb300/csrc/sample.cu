@@ -198,18 +198,15 @@ struct Weight {
   __device__ __forceinline__ uint32_t step(float l) const {
     return __float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(max, l), -hi), kY));
   }
-  __device__ __forceinline__ bool fits() const { return true; }
 };
 
 // The same for bf16 logits that are not too large, with fewer steps: a logit's eight bits
 // times sixteen of the scale is exact, so l * scale - max * scale needs no exact
 // difference first.  (20 instead of 25 instructions per logit: 256 rows of 131,071 52 us
 // instead of 59, with top-p alone 148 instead of 169.)
-// A row's weights are all of one kind.
 struct DirectWeight {
   float high, low, from, left;                     // scale in 16 bits and the rest; kY - max * scale in two parts
   int shift;
-  bool small;
   __device__ __forceinline__ explicit DirectWeight(const Weight& w) {
     high = __uint_as_float(__float_as_uint(w.hi) & 0xFFFFFF00u);
     low = __fadd_rn(__fsub_rn(w.hi, high), w.lo);
@@ -217,9 +214,7 @@ struct DirectWeight {
     from = __fsub_rn(Weight::kY, q);               // both multiples of 2^-10 below 2^14: exact
     left = __fmaf_rn(-w.max, low, __fsub_rn(q, t));
     shift = w.shift;
-    small = fabsf(w.max) * w.hi < 2000.f;
   }
-  __device__ __forceinline__ bool fits() const { return small; }
   __device__ __forceinline__ void two(float l0, float l1, bool counts0, bool counts1, u64& w0, u64& w1, uint32_t& s0,
                                       uint32_t& s1, const uint32_t* __restrict__ powers) const {
     const u64 l = pair(l0, l1), t = mul2(l, pair(high, high));
@@ -240,6 +235,20 @@ struct DirectWeight {
     return a;
   }
   __device__ __forceinline__ uint32_t step(float l) const { return __float_as_uint(__fadd_rn(__fmul_rn(l, high), from)); }
+};
+
+// A row's weights: all of one kind, whatever else is done for the row.
+template <typename T>
+struct RowWeight {
+  static constexpr bool kDirect = sizeof(T) == 2;
+  Weight plain;
+  typename std::conditional<kDirect, DirectWeight, Weight>::type fine;
+  bool fits;                                       // (false: plain)
+  __device__ __forceinline__ explicit RowWeight(const Weight& w)
+      : plain(w), fine(w), fits(!kDirect || fabsf(w.max) * w.hi < 2000.f) {}
+  __device__ __forceinline__ u64 operator()(float l, const uint32_t* __restrict__ powers) const {
+    return fits ? fine(l, powers) : plain(l, powers);
+  }
 };
 
 // p * z rounded up or down to an integer, for a float 0 <= p <= 1
@@ -694,7 +703,8 @@ __device__ __forceinline__ u64 reaching_key(Shared& s, uint32_t* __restrict__ su
   __syncthreads();
   return prefix;
 }
-__device__ __forceinline__ void finish(const Args& a, Shared& s, const Weight& weight, u64* __restrict__ list,
+template <typename W>
+__device__ __forceinline__ void finish(const Args& a, Shared& s, const W& weight, u64* __restrict__ list,
                                        u64* __restrict__ other, int n, int k, float p, float u, int row) {
   const int tid = threadIdx.x, kk = min(n, k);
   if (n <= kCounted) {
@@ -1107,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 6)
     if (tid == 0) a.token[row] = kLater;
     return;
   }
-  finish(a, sh, set.weight(m, a.bits), list, other, (int)sh.rank_in, set.k, set.p, set.u, row);
+  finish(a, sh, RowWeight<T>(set.weight(m, a.bits)), list, other, (int)sh.rank_in, set.k, set.p, set.u, row);
 }
 
 // A row by a cluster; called between an arrive at the cluster's barrier and the next.
@@ -1185,15 +1195,13 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
     return;
   }
   // kept: logits above `cut`, and of those equal to it the first `ties`; first what min-p keeps
-  const Weight weight = set.weight(m, a.bits);
+  const RowWeight<T> weight(set.weight(m, a.bits));
   float cut = greedy ? m : -FLT_MAX;
   if (least > 0.f) cut = fmaxf(__double2float_ru((double)m - sh.far), -FLT_MAX);
-  using Fine = typename std::conditional<sizeof(T) == 2, DirectWeight, Weight>::type;
-  const Fine fine(weight);
-  // Logits too large for it at their temperature are far apart: what is 64 powers of two
+  // Logits in the thousands for their temperature are far apart: what is 64 powers of two
   // below the largest weighs nothing, and few are not.
-  const bool cold = kCuts && !greedy && !fine.fits();
-  if (cold) cut = fmaxf(cut, m - 64.f / weight.hi);
+  const bool cold = kCuts && !greedy && !weight.fits;
+  if (cold) cut = fmaxf(cut, m - 64.f / weight.plain.hi);
   if (kCuts && (small_k || cold || least > 0.f || (p < 1.f && a.vocab <= kList))) {
     // Few tokens can be kept as a rule, or are there: CTA 0 gets them listed.
     const float low = small_k ? fmaxf(cut, fmaxf(ordered_value(bound), -FLT_MAX)) : cut;
@@ -1235,8 +1243,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
   // Any number of tokens.
   u64 sum = 0;                                     // this thread's part of what is kept: logits above the cut,
   uint32_t count = 0, ties = greedy ? 1u : 0x7FFFFFFFu;  // and those equal to it
-  const auto keep = [&](const auto& weight) {
-    sum = 0, count = 0;
+  const auto masses = [&](const auto& weight) {
     for (int s = 0; s < steps; ++s) {
       Run<T> run;
       run.load(x + s * 32 * kVec);
@@ -1248,27 +1255,29 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
         sum += w0 + w1;
       }
     }
+  };
+  const auto keep = [&] {
+    sum = 0, count = 0;
+    if (weight.fits) masses(weight.fine);
+    else masses(weight.plain);
     if (ties)
       each_logit([&](float l) { count += l == cut; });
   };
-  // a row's weights are of one kind, from here on to its end
-  bool finely = !greedy && fine.fits();
   const bool cuts = kCuts && k < a.vocab && !greedy;
   bool found = !cuts && p >= 1.f;
   if (!greedy) cut = Grid<T>::value(Grid<T>::up(cut));
   if (found) {                                     // nothing to cut, or the first of the largest
     if (!greedy) cut = next_below<T>(cut), ties = 0;
-    if (finely) keep(fine);
-    else keep(weight);
+    keep();
   }
   // A histogram tells near which logits the cuts lie; CTA 0 gets those listed.  The bins'
   // middles are off by a part in 370 at most, a sum over many bins by much less: 2^-11 of
   // the mass to either side is enough as a rule, 2^-8 the second time.  (48 rows of 64,000 37
   // us; from 2^-13 on 46, as 3 rows need a second time; from 2^-8 on 45, as lists get longer.)
-  for (int time = 0; kCuts && finely && !found && time < 2; ++time) {
+  for (int time = 0; kCuts && weight.fits && !found && time < 2; ++time) {
     uint32_t* hist = (uint32_t*)list;
     static_assert(kBins * 4 <= kList * 8, "the histogram takes the list's place");
-    const auto bin_of = [&](float l) { return bin_at(fine.step(l)); };
+    const auto bin_of = [&](float l) { return bin_at(weight.fine.step(l)); };
     __syncthreads();
     if (tid == 0) sh.listed = 0;
     for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
@@ -1287,7 +1296,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
     const uint32_t room = 2 * kList / size;
     u64 above = 0, between = 0;                    // exact masses of what lies above and between the listed bins
     uint32_t with = 0;                             // steps with listed logits
-    mass_around<T>(x, steps, cut, fine, sh.powers, b1, b2, bk, above, between, [&](int s, uint32_t hits) {
+    mass_around<T>(x, steps, cut, weight.fine, sh.powers, b1, b2, bk, above, between, [&](int s, uint32_t hits) {
       with |= 1u << s;
       uint32_t to = atomicAdd(&sh.listed, __popc(hits));
       for (; hits && to < room; hits &= hits - 1) values[to++] = to_f32(x[s * 32 * kVec + __ffs(hits) - 1]);
@@ -1312,9 +1321,9 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
       __syncthreads();
       float at_cut;
       uint32_t tied;
-      const bool right = n <= kListed ? cut_of_few(sh, fine, bin_of, values, n, next_below<T>(cut), b2, bk, rank_in, p,
+      const bool right = n <= kListed ? cut_of_few(sh, weight.fine, bin_of, values, n, next_below<T>(cut), b2, bk, rank_in, p,
                                                     above, between, at_cut, tied)
-                                      : cut_of_many<T>(team, fine, bin_of, values, n, next_below<T>(cut), b2, bk,
+                                      : cut_of_many<T>(team, weight.fine, bin_of, values, n, next_below<T>(cut), b2, bk,
                                                         rank_in, p, above, between, at_cut, tied);
       if (tid < size) store_remote(&sh.note, tid, right ? (u64)__float_as_uint(at_cut) << 32 | tied : ~0ull);
     }
@@ -1330,7 +1339,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
           const float l = run.get(j);
-          if (l > cut && is_listed(bin_of(l))) sum += fine(l, sh.powers);
+          if (l > cut && is_listed(bin_of(l))) sum += weight.fine(l, sh.powers);
           count += l == cut;
         }
       }
@@ -1338,7 +1347,6 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
   }
   if (kCuts && !found) {
     // Too many near a cut (equal logits, say): bisection over all of them.
-    finely = false;
     const auto count_of = [&](float v, float w) {
       uint32_t n = 0;
       u64 none = 0;
@@ -1353,7 +1361,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
       cut = bisect<T>(Grid<T>::up(cut), end, (uint32_t)k, over, count_of);
       ties = k - over;
     }
-    keep(weight);
+    keep();
     if (p < 1.f) {
       u64 mass = sum;
       uint32_t tied = count;
@@ -1376,12 +1384,12 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
         });
         const u64 one = weight(cut, sh.powers);
         ties = (uint32_t)((want - over + one - 1) / one);
-        keep(weight);
+        keep();
       }
     }
   }
   // What each warp keeps, in the order of the tokens.
-  const u64 each = !ties ? 0 : finely ? fine(cut, sh.powers) : weight(cut, sh.powers);
+  const u64 each = ties ? weight(cut, sh.powers) : 0;
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   count = __reduce_add_sync(0xFFFFFFFFu, count);
   if (lane == 0) sh.warp_sum[warp] = sum, sh.warp_count[warp] = count;
@@ -1447,8 +1455,8 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
       for (int j = 0; j < kVec; j += 2) {
         const float l0 = v.get(j), l1 = v.get(j + 1);
         uint32_t y;
-        if (finely) fine.two(l0, l1, l0 > cut, l1 > cut, own[j], own[j + 1], y, y, sh.powers);
-        else weight.two(l0, l1, l0 > cut, l1 > cut, own[j], own[j + 1], y, y, sh.powers);
+        if (weight.fits) weight.fine.two(l0, l1, l0 > cut, l1 > cut, own[j], own[j + 1], y, y, sh.powers);
+        else weight.plain.two(l0, l1, l0 > cut, l1 > cut, own[j], own[j + 1], y, y, sh.powers);
         run += own[j] + own[j + 1];
         tie_run += (v.get(j) == cut) + (v.get(j + 1) == cut);
       }
@@ -1545,7 +1553,9 @@ static bool launch(const Args& a, const void* logits, DevCtx c, cudaStream_t st)
   const size_t smem = cuts ? kList * 8 + std::max(room, (size_t)kList * 8) : room;
   const bool stream = a.rows >= sms && (a.top_k || a.min_p);
   auto kernel = stream ? sample_kernel<T, true, true> : cuts ? sample_kernel<T, true, false> : sample_kernel<T, false, false>;
-  if (!cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))) return false;
+  // (the most that any call takes: another thread's call may come between this one and the launch)
+  constexpr int kMost = kList * 8 + (kMaxVocab / kMaxCluster + kThreads * kVec) * (int)sizeof(T);
+  if (smem > kMost || !cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost))) return false;
   if (stream && !launch_programmatic(stream_kernel<T>, dim3((unsigned)a.rows), dim3(kThreads), 0, st, 1, a,
                                      (const T*)logits, c))
     return false;

@@ -7,6 +7,7 @@ that from a sum of weights (checked), or make all of them whole numbers of units
 """
 import math
 import random
+import threading
 
 import pytest
 import torch
@@ -365,6 +366,53 @@ def test_a_row_gives_the_same_bits_wherever_it_lies():
                        dtype=dtype)
             seen |= set(zip(t, p))
         assert len(seen) == 1
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cuts", [dict(min_p=0.0045), dict(top_k=200, top_p=0.97), dict(top_p=0.8), dict()])
+def test_a_row_gives_the_same_bits_in_any_batch(cuts, dtype):
+    """One row is spread over eight CTAs, 200 take one each; what is kept lies all in the first CTA's part."""
+    dsa = lib()
+    n, V = 200, 40000
+    x, u = rand(n, V, seed=77).sort(descending=True).values, uniform(n, seed=78)
+    of = lambda m: {k: [v] * m for k, v in dict(cuts, temperature=0.93).items()}
+    want = list(zip(*run(dsa, x, u, dtype=dtype, **of(n))))
+    assert list(zip(*run(dsa, x[:40], u[:40], dtype=dtype, **of(40)))) == want[:40]
+    for r in range(40):
+        assert list(zip(*run(dsa, x[r:r + 1], u[r:r + 1], dtype=dtype, **of(1)))) == want[r:r + 1]
+    assert dsa.get_status() == 0
+
+
+def test_host_threads_with_different_sizes():
+    dsa = lib()
+    sizes = [(2, 200001), (3, 901), (1, 131071), (5, 30011)]
+    calls = []
+    for i, (n, V) in enumerate(sizes):
+        calls.append((dsa.make_sampler(rows=n, vocab=V), rand(n, V, seed=90 + i).to(BF16).to(DEV), dev(uniform(n, seed=95 + i)),
+                      dev([0.8] * n), torch.zeros(n, dtype=torch.int32, device=DEV)))
+    sample = lambda c, token, stream: dsa.sample(c[0], c[1], c[2], None, None, c[3], None, None, token, stream=stream)
+    for c in calls:
+        sample(c, c[4], None)
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(c):
+        try:
+            stream, token = torch.cuda.Stream(), torch.zeros_like(c[4])
+            for _ in range(200):
+                sample(c, token, stream.cuda_stream)
+            stream.synchronize()
+            assert torch.equal(token, c[4])
+        except Exception as e:
+            errors.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors and dsa.get_status() == 0
 
 
 def test_graph_replay_on_new_logits_and_other_stream():
