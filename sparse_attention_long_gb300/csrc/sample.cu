@@ -31,7 +31,8 @@
 // 32,001 fp32, top-k and top-p 6.7 (0.02); 768 rows of 64,000 bf16, top-k and top-p 37 (14.5), of
 // which stream_kernel 31; 256 rows of 131,071 bf16 at a temperature 51 (9.9); 48 rows of 64,000 fp32,
 // top-p alone and large nuclei 37 (1.8); 64 rows of 131,071 bf16, top-p alone 46, a mixture 31 to
-// 43 (2.5), all at a temperature of 0.01 13.
+// 43 (2.5), all at a temperature of 0.01 13,
+// at 0 9.
 // Bound: the first by the latency of loads and two cluster barriers; stream_kernel by
 // instructions and the phases without loads (settings, bounds, the end); a pass of weights by
 // instructions (20 per bf16 logit, 25 else; 2.4 per cycle and SM); the histogram's path by
@@ -1258,8 +1259,12 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
   };
   const auto keep = [&] {
     sum = 0, count = 0;
-    if (weight.fits) masses(weight.fine);
-    else masses(weight.plain);
+    if (greedy) {                                  // (nothing above the largest)
+    } else if (weight.fits) {
+      masses(weight.fine);
+    } else {
+      masses(weight.plain);
+    }
     if (ties)
       each_logit([&](float l) { count += l == cut; });
   };
