@@ -10,13 +10,13 @@
 // A CTA takes consecutive rows (a row: one head of one token), its threads the same pairs
 // of several of them; sines and cosines of its tokens are computed once, into shared
 // memory, while the first rows are on their way.  (Each thread its own instead: 122
-// registers, a quarter of the SM's warps, 520 us where this takes 171.)
+// registers, a quarter of the SM's warps, 520 us where this takes 172.)
 //
 // Bound: HBM for many tokens.  16,384 tokens of the latent shapes (128 heads of 64 of 576
-// columns, 64 index heads of 128; 1.09 GB) 171 us, 6.4 TB/s, 94 % of the copy's measured rate; the gradients of
-// 8,192 90 us (90 %); 768 tokens 13 us (51 MB, 3.9 TB/s: launch and latency); one token 3 us.
-// With few heads the sines take longer than the rows: 13,897 tokens x 4 heads of 256
-// columns 38 us (57 MB).
+// columns, 64 index heads of 128; 1.09 GB) 172 us, 6.3 TB/s, 93 % of the copy's measured rate; the gradients of
+// 8,192 91 us (89 %); 768 tokens 13 us (51 MB, 3.9 TB/s: launch and latency); one token 3 us.
+// With few heads the sines take longer than the rows: 13,897 tokens x 8 heads of 256 bf16
+// columns 44 us (114 MB).
 #include <math.h>
 
 #include "dsa_common.cuh"
