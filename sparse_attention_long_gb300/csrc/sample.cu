@@ -968,7 +968,7 @@ __device__ __forceinline__ uint32_t reached_by(int need, uint32_t best, uint32_t
     if (n >= need) {
       lo = mid, open = false;
       if (n <= need + need / 4 + 1) break;
-      if (hi == top + 1 && hi - lo > 2 * step) {   // up from below
+      if (hi == top + 1 && (hi - lo) / 2 > step) {  // up from below (step stays below 2^31)
         mid = lo + step, step *= 2;
         continue;
       }

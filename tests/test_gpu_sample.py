@@ -243,6 +243,25 @@ def test_many_rows_with_ties_and_masks(dtype):
     check(dsa, x, u, dtype=dtype, min_p=[0.1] * MANY)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("begin", ["ascending", "lowest", "-1e4", "-3", "-inf"])
+def test_many_rows_whose_bound_rises(begin, dtype):
+    """The first logits of a row say little about the k-th largest: the bound rises by up to all of the type's range."""
+    dsa = lib()
+    n, V = 160, 30000
+    x = rand(n, V, seed=31)
+    if begin == "ascending":
+        x = x.sort().values
+    else:
+        x[:, :20000] = float(torch.finfo(dtype).min) if begin == "lowest" else float(begin)
+        x[:, :20000:3000] -= 0.5
+    index = [r % 4 for r in range(n)]
+    check(dsa, x, uniform(n, seed=32), index=index, dtype=dtype, top_k=[2, 40, 190, 1], top_p=[0.9, 0.95, 1.0, 1.0],
+          temperature=[1.0, 0.8, 1.3, 1.0])
+    check(dsa, -x.abs() if begin == "ascending" else x, uniform(n, seed=33), index=index, dtype=dtype,
+          min_p=[0.05, 0.3, 0.01, 1.0])
+
+
 def test_many_rows_as_a_graph():
     dsa = lib()
     n, V = 400, 9001
