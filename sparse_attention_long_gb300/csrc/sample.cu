@@ -71,7 +71,7 @@ struct Args {
   float* prob;
 };
 
-// 2^30 * 2^(j / 1024)
+// 2^31 * 2^(j / 1024)
 struct Powers {
   uint32_t at[1024];
   constexpr Powers() : at() {
@@ -82,7 +82,7 @@ struct Powers {
         term *= x / k;
         sum += term;
       }
-      at[j] = (uint32_t)(sum * 1073741824.0 + 0.5);
+      at[j] = (uint32_t)(sum * 2147483648.0 + 0.5);
     }
   }
 };
@@ -157,7 +157,8 @@ __device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
 // w = 2^-x as a whole number of units, x = (max - l) * log2(e) / temperature.  Two logits
 // at once: max - l = d + e and d * scale = x + f without error, -x = q + r with q a
 // multiple of 2^-10, 2^q from the table and 2^r by a series.  Off by 2^-29 of itself
-// (the table by half a step of 2^-30, the product below by one) and the last unit.
+// (the table by half a step of 2^-31, r by as much, the series without the cube of |r| < 2^-9 by 0.4
+// 2^-30, the product below by one step of 2^-30 at most) and the last unit.
 struct Weight {
   float max, hi, lo;                               // log2(e) / temperature in two floats
   int shift;                                       // the largest weight is 2^(62 - shift) units
@@ -165,13 +166,11 @@ struct Weight {
   __device__ __forceinline__ u64 of(bool counts, uint32_t y, float z, const uint32_t* __restrict__ powers) const {
     // (what is further down, the exponent of 2 out of reach, weighs nothing)
     const uint32_t p = counts && __uint_as_float(y) > kY - 62.5f + (float)shift ? powers[y & 1023u] : 0u;
-    const int s = (int)(__float_as_uint(z) - __float_as_uint(kZ) + 1u);
-    uint32_t w;
-    asm("mad.hi.s32 %0, %1, %2, %1;" : "=r"(w) : "r"(p), "r"(s));
+    const uint32_t w = __umulhi(p, __float_as_uint(z) - __float_as_uint(kZ) + (1u << 31));  // 2^30 * 2^(q's fraction + r)
     return ((u64)w << 32) >> (((shift << 10) + 1023 + __float_as_uint(kY) - y) >> 10 & 63u);
   }
   static constexpr float kY = 12288.f;             // 1.5 * 2^13: steps of 2^-10
-  static constexpr float kZ = 0.0029296875f;       // 1.5 * 2^-9: steps of 2^-32
+  static constexpr float kZ = 0.005859375f;        // 1.5 * 2^-8: steps of 2^-31, for |r| below 2^-9
   static constexpr float kLn2 = 0.693147181f, kHalfLn2Sq = 0.240226507f;
   // whether l0 and l1 count; y0, y1: bits of the step numbers, see bin_at
   __device__ __forceinline__ void two(float l0, float l1, bool counts0, bool counts1, u64& w0, u64& w1, uint32_t& y0,
@@ -209,7 +208,7 @@ struct DirectWeight {
   float high, low, from, left;                     // scale in 16 bits and the rest; kY - max * scale in two parts
   int shift;
   __device__ __forceinline__ explicit DirectWeight(const Weight& w) {
-    high = __uint_as_float(__float_as_uint(w.hi) & 0xFFFFFF00u);
+    high = __uint_as_float((__float_as_uint(w.hi) + 0x80u) & 0xFFFFFF00u);
     low = __fadd_rn(__fsub_rn(w.hi, high), w.lo);
     const float t = __fmul_rn(w.max, high), y = __fadd_rn(t, Weight::kY), q = __fsub_rn(y, Weight::kY);
     from = __fsub_rn(Weight::kY, q);               // both multiples of 2^-10 below 2^14: exact

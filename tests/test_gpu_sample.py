@@ -163,6 +163,23 @@ def test_a_large_spread_of_small_differences():
     check(dsa, x, [0.1, 0.6, 0.95], top_p=[0.5] * 3, temperature=[0.7] * 3)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n", [3, 600])
+def test_probabilities_of_light_tokens(n, dtype):
+    """u = 0 draws token 0, 2^-10 to 2^-30 of the largest weight (units of 2^-58 of that: 2^-28 of it at most)."""
+    dsa = lib()
+    g = torch.Generator().manual_seed(n)
+    T = (0.02 * 100 ** torch.rand(n, generator=g)).tolist()
+    x = torch.rand(n, 9, generator=g, dtype=torch.float64) * -4.0
+    t = torch.tensor(T, dtype=torch.float64)[:, None]
+    top = torch.rand(n, 1, generator=g, dtype=torch.float64) * 26.0 - 13.0
+    x = top + x * t
+    x[:, 4:5] = top
+    x[:, 0:1] = top - (10 + 19 * torch.rand(n, 1, generator=g, dtype=torch.float64)) * math.log(2) * t
+    for cuts in (dict(), dict(top_k=[9] * n), dict(min_p=[2.0 ** -40] * n)):
+        check(dsa, x, [0.0] * n, temperature=T, dtype=dtype, exact=True, **cuts)
+
+
 def test_every_cdf_step_of_a_small_row():
     """u in the middle of each token's part of the mass, and a hair below its end."""
     dsa = lib()
