@@ -30,7 +30,7 @@
 // Measured (us, calls back to back; in brackets the logits' bytes at 6.8 TB/s): one row of
 // 32,001 fp32, top-k and top-p 6.7 (0.02); 768 rows of 64,000 bf16, top-k and top-p 37 (14.5), of
 // which stream_kernel 31; 256 rows of 131,071 bf16 at a temperature 51 (9.9); 48 rows of 64,000 fp32,
-// top-p alone and large nuclei 37 (1.8); 64 rows of 131,071 bf16, top-p alone 46, a mixture 31 to
+// top-p alone and large nuclei 37 (1.8); 64 rows of 131,071 bf16, top-p alone 45, a mixture 31 to
 // 43 (2.5), all at a temperature of 0.01 13,
 // at 0 9.
 // Bound: the first by the latency of loads and two cluster barriers; stream_kernel by
@@ -202,8 +202,8 @@ struct Weight {
 
 // The same for bf16 logits that are not too large, with fewer steps: a logit's eight bits
 // times sixteen of the scale is exact, so l * scale - max * scale needs no exact
-// difference first.  (20 instead of 25 instructions per logit: 256 rows of 131,071 52 us
-// instead of 59, with top-p alone 148 instead of 169.)
+// difference first.  (20 instead of 25 instructions per logit: 256 rows of 131,071 51 us
+// instead of 59, with top-p alone 143 instead of 169.)
 struct DirectWeight {
   float high, low, from, left;                     // scale in 16 bits and the rest; kY - max * scale in two parts
   int shift;
