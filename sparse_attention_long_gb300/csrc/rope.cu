@@ -217,13 +217,13 @@ __device__ __forceinline__ void rotate_rows(const Args& g, const Part& p, const 
       }
       row += kUnroll * rows_step;
       if (row < end) load(row, t, h);
+      else let_next_launch();                      // (not earlier: 300 tokens 7.9 us instead of 9.0)
     }
   }
 }
 
 __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant__ Args g, const int32_t* __restrict__ pos) {
   __shared__ __align__(16) float cosines[kTable], sines[kTable];
-  let_next_launch();
   wait_for_earlier();
   int i = 0;
   while (i + 1 < g.n_parts && blockIdx.x >= g.part[i + 1].first_cta) ++i;

@@ -28,10 +28,10 @@
 // (stream_kernel), which keeps nothing of it but the candidates.
 //
 // Measured (us, calls back to back; in brackets the logits' bytes at 6.8 TB/s): one row of
-// 32,001 fp32, top-k and top-p 6.7 (0.02); 768 rows of 64,000 bf16, top-k and top-p 37 (14.5), of
-// which stream_kernel 31; 256 rows of 131,071 bf16 at a temperature 51 (9.9); 48 rows of 64,000 fp32,
-// top-p alone and large nuclei 37 (1.8); 64 rows of 131,071 bf16, top-p alone 45, a mixture 31 to
-// 43 (2.5), all at a temperature of 0.01 13,
+// 32,001 fp32, top-k and top-p 6.7 (0.02); 768 rows of 64,000 bf16, top-k and top-p 35 (14.5), of
+// which stream_kernel 31; 256 rows of 131,071 bf16 at a temperature 50 (9.9); 48 rows of 64,000 fp32,
+// top-p alone and large nuclei 31 (1.8); 64 rows of 131,071 bf16, top-p alone 45, a mixture 29 to
+// 40 (2.5), all at a temperature of 0.01 13,
 // at 0 9.
 // Bound: the first by the latency of loads and two cluster barriers; stream_kernel by
 // instructions and the phases without loads (settings, bounds, the end); a pass of weights by
@@ -1011,7 +1011,6 @@ __global__ void __launch_bounds__(kThreads, 6)
   // Logits on their way, in the list's place: 64 bytes per thread, in two groups.
   constexpr int kRuns = 32 / (int)sizeof(Run<T>), kGroup = kRuns * kThreads * kVec;
   T* ring = (T*)list + threadIdx.x * kVec;
-  let_next_launch();
   const int tid = threadIdx.x, row = blockIdx.x;
   load_powers(sh);
   if (tid == 0) sh.listed = sh.rank_in = 0;
@@ -1085,6 +1084,10 @@ __global__ void __launch_bounds__(kThreads, 6)
         if (to < kRunList) runs[to] = at + (s * kThreads + tid) * kVec;
       }
   }
+  // The next launch comes here and not at the beginning: CTAs that come while others hold
+  // an SM's places fill what is left, and some SMs get twice as many as others.  (300 rows of
+  // 16,000 12 us instead of 20; 48 rows of 64,000 by top-p 31 instead of 36.)
+  let_next_launch();
   cp_async_wait_all();
   __syncthreads();
   m = ordered_value(top);
@@ -1228,6 +1231,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
       total += (int)sh.count[team.turn][r];
     }
     if (all) {
+      let_next_launch();
       if (rank != 0) return;
       u64* packed = (u64*)mine;                    // (this CTA's logits are not looked at again)
       int r = 0, begin = 0;
@@ -1276,8 +1280,8 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
   }
   // A histogram tells near which logits the cuts lie; CTA 0 gets those listed.  The bins'
   // middles are off by a part in 370 at most, a sum over many bins by much less: 2^-11 of
-  // the mass to either side is enough as a rule, 2^-8 the second time.  (48 rows of 64,000 37
-  // us; from 2^-13 on 46, as 3 rows need a second time; from 2^-8 on 45, as lists get longer.)
+  // the mass to either side is enough as a rule, 2^-8 the second time.  (48 rows of 64,000: 9
+  // us more from 2^-13 on, as 3 rows need a second time, 8 more from 2^-8 on, as lists get longer.)
   for (int time = 0; kCuts && weight.fits && !found && time < 2; ++time) {
     uint32_t* hist = (uint32_t*)list;
     static_assert(kBins * 4 <= kList * 8, "the histogram takes the list's place");
@@ -1442,6 +1446,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
   }
   __syncthreads();
   const int who = sh.who;
+  let_next_launch();                               // (late, as in stream_kernel)
   if (who < 0) return;
   // The CTA that holds the token: one step of the warp that does per warp, one of its lanes.
   u64 before = sh.before;
@@ -1510,7 +1515,6 @@ __global__ void __launch_bounds__(kThreads, 4)
     sample_kernel(const __grid_constant__ Args a, const T* __restrict__ logits, int chunk, int steps, DevCtx c) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ Shared sh;
-  let_next_launch();
   cluster_arrive();                                // no CTA writes to one that has not begun
   const int row = blockIdx.x / cluster_nctarank();
   if (!kLeft) load_powers(sh);
