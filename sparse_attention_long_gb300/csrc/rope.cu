@@ -14,7 +14,7 @@
 //
 // Bound: HBM for many tokens.  16,384 tokens of the latent shapes (128 heads of 64 of 576
 // columns, 64 index heads of 128; 1.09 GB) 172 us, 6.3 TB/s, 93 % of the copy's measured rate; the gradients of
-// 8,192 91 us (89 %); 768 tokens 13 us (51 MB, 3.9 TB/s: launch and latency); one token 3 us.
+// 8,192 90 us (90 %); 768 tokens 13 us (51 MB, 4.0 TB/s: launch and latency); one token 3 us.
 // With few heads the sines take longer than the rows: 13,897 tokens x 8 heads of 256 bf16
 // columns 44 us (114 MB).
 #include <math.h>
