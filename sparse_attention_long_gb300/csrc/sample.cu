@@ -489,7 +489,7 @@ __device__ __forceinline__ void sum_histograms(uint32_t* __restrict__ hist, int 
 }
 
 // The choice of bins.  bin[2]: where the k-th logit lies (kBins: none does), rank_in of
-// its bin's tokens are kept; bin[0] to bin[1]: where top-p's border lies, by the counts and
+// its bin's tokens are kept; bin[0] to bin[1], with p < 1: where top-p's border lies, by the counts and
 // the weights of the bins' middles, with a part `margin` of the mass to either side, or, if
 // more than `limit` tokens lie there, less of it, down to 2^-13.  Who has the exact sums
 // looks whether the border lies there.
@@ -1299,6 +1299,12 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
     uint32_t rank_in = 0;
     choose_bins(sh, hist, k, cuts, p, time ? 0x1p-8f : 0x1p-11f, time ? 2 * kList : kCounted, rank_in);
     const int b1 = sh.bin[0], b2 = sh.bin[1], bk = sh.bin[2];
+    if (bk == kBins && p >= 1.f) {                 // fewer than k reach the cut: nothing more to cut
+      cut = next_below<T>(cut), ties = 0;
+      keep();
+      found = true;
+      break;
+    }
     const auto is_listed = [&](int b) { return (uint32_t)(b - b1) <= (uint32_t)(b2 - b1) || b == bk; };
     float* values = (float*)list;                  // in the histogram's place
     const uint32_t room = 2 * kList / size;

@@ -516,3 +516,50 @@ def test_refused_tensors():
             dsa.sample(s, **dict(ok, **kw))
         assert e.value.code == dsa.DSA_ERR_INVALID_ARG
     assert dsa.get_status() == 0
+
+
+LIGHT = 2.0 ** -32                               # of the largest weight
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("light,front,k,min_p", [(2800, False, 5000, 0.0), (2800, True, 5000, 0.0), (500, False, 2000, 0.0),
+                                                 (500, True, 1000, 0.0), (900, True, 1000, 0.0), (2000, False, 3000, 2.0 ** -34),
+                                                 (5000, False, 19999, 0.0)])
+def test_light_tokens_of_a_row_with_fewer_than_top_k(light, front, k, min_p, dtype):
+    """One token, and others below 2^-32 of it, all kept: they count in the mass and are drawn.
+
+    A weight is off by 2^-29 of itself and a unit of 2^-44 of the largest, so the mass before a token by a part of
+    light * 2^-32 * 2^-29 + light * 2^-44 < 2^-30 at most: the drawn token's part of the mass must hold u to that.  A
+    probability is off by as much of itself, a unit, and its rounding.
+    """
+    dsa = lib()
+    n, V = 5, 20000
+    g = torch.Generator().manual_seed(light + k)
+    x = torch.full((n, V), -INF, dtype=torch.float64)
+    for r in range(n):
+        at = 1 + (torch.arange(light) if front else torch.randperm(V - 1, generator=g)[:light].sort().values)
+        x[r, at] = -22.2 - 1.2 * torch.rand(light, generator=g, dtype=torch.float64) * (0.1 if light < 600 else 1.0)
+        x[r, at[0]] = -22.2
+        x[r, 0 if r < 3 else at[-1]] = 0.0       # in front of the light ones (u near 1 draws them) or behind (u = 0)
+    u = [0.5, 1 - 2.0 ** -24, 1 - 2.0 ** -23, 0.0, 0.5]
+    x = x.to(dtype).double()
+    keep = dict(top_k=[k] * n, min_p=[min_p] * n)
+    got = run(dsa, x, u, dtype=dtype, **keep)
+    assert dsa.get_status() == 0
+    drawn = 0
+    for r in range(n):
+        token, prob = got[0][r], got[1][r]
+        kept, w, _ = kept_tokens(x[r].numpy(), 1.0, k, 1.0, min_p)
+        part = dict(zip(kept.tolist(), (w / w.sum()).tolist()))
+        before = math.fsum(part[t] for t in kept.tolist() if t < token)
+        assert token in part and before - 2.0 ** -30 <= u[r] <= before + part[token] + 2.0 ** -30, (r, token)
+        assert abs(prob - part[token]) <= part[token] * (2.0 ** -24 + 2.0 ** -30) + 2.0 ** -44, (r, prob, part[token])
+        drawn += part[token] < LIGHT
+    assert drawn >= 1
+    # the same bits, whatever share of a row a CTA has and whatever kernel takes it
+    for m in (20, 40):
+        many = run(dsa, x.repeat(m, 1), u * m, dtype=dtype, top_k=[k] * n * m, min_p=[min_p] * n * m)
+        assert many[0] == got[0] * m and many[1] == got[1] * m
+    for r in range(n):
+        one = run(dsa, x[r:r + 1], u[r:r + 1], dtype=dtype, top_k=[k], min_p=[min_p])
+        assert one == (got[0][r:r + 1], got[1][r:r + 1])
