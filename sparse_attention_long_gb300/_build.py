@@ -38,7 +38,7 @@ def _nvcc() -> str:
 def _stale(obj: str, src: str) -> bool:
     if not os.path.exists(obj):
         return True
-    deps = [src, os.path.join(CSRC, "dsa_common.cuh"), os.path.join(CSRC, "tree_attn.cuh"),
+    deps = [src, os.path.join(CSRC, "dsa_common.cuh"), os.path.join(CSRC, "tree_attn.cuh"), os.path.join(CSRC, "bound.h"),
             os.path.join(ROOT, "include", "dsa.h"), __file__]
     return any(os.path.getmtime(d) > os.path.getmtime(obj) for d in deps)
 

@@ -43,6 +43,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "bound.h"
 #include "dsa_common.cuh"
 
 namespace dsa {
@@ -955,35 +956,9 @@ struct Settings {
   }
 };
 
-// A number that at least `need` threads' `best` reach: the search ends near the largest
-// such.  top: the largest best; lo: 0, or a number known to be reached by so many.
-__device__ __forceinline__ uint32_t reached_by(int need, uint32_t best, uint32_t top, uint32_t lo) {
-  if (need == 1) return top;
-  uint32_t hi = top + 1, step = 1u << 18;          // fewer than `need` threads reach hi
-  uint32_t mid = lo ? lo : hi > step ? hi - step : hi / 2;
-  bool open = lo == 0;
-  while (hi - lo > 1 || mid == lo) {
-    const int n = __syncthreads_count(best >= mid);
-    if (n >= need) {
-      lo = mid, open = false;
-      if (n <= need + need / 4 + 1) break;
-      if (hi == top + 1 && (hi - lo) / 2 > step) {  // up from below (step stays below 2^31)
-        mid = lo + step, step *= 2;
-        continue;
-      }
-    } else {
-      hi = mid;
-      if (open) {                                  // down from above
-        step *= 2;
-        if (step >= (1u << 30)) break;             // few logits: all reach it
-        mid = hi > step ? hi - step : hi / 2;
-        continue;
-      }
-    }
-    if (hi - lo <= 1) break;
-    mid = lo + (hi - lo) / 2;
-  }
-  return lo;
+// reached_by over a CTA's threads
+__device__ __forceinline__ uint32_t reached_by_threads(int need, uint32_t best, uint32_t top, uint32_t lo) {
+  return reached_by(need, top, lo, [&](uint32_t key) { return __syncthreads_count(best >= key); });
 }
 __device__ __forceinline__ uint32_t largest_of_cta(uint32_t best, uint32_t* __restrict__ of_warps) {
   best = __reduce_max_sync(0xFFFFFFFFu, best);
@@ -1070,9 +1045,9 @@ __global__ void __launch_bounds__(kThreads, 6)
     if (group == bound_at || last) {               // after 1, 3, 9, ... groups and the last
       bound_at *= 3;
       const uint32_t best = ordered_key(m);
-      const bool by_top = group == 1 || last || !by_k || set.k == 1;
+      const bool by_top = group == 1 || last || !by_k || set.k == 1 || !bound;
       if (by_top) top = largest_of_cta(best, sh.warp_count);
-      if (by_k) bound = reached_by(set.k, best, by_top ? top : 0xFFFFFFF0u, bound);
+      if (by_k) bound = reached_by_threads(set.k, best, by_top ? top : 0xFFFFFFF0u, bound);
       low = fmaxf(low, ordered_value(bound));      // (a bound once found holds)
       if (by_top) low = fmaxf(low, cut_at(ordered_value(top)));
       __syncthreads();
@@ -1181,7 +1156,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
   const uint32_t best = ordered_key(m);
   uint32_t top = largest_of_cta(best, sh.warp_count);
   const bool small_k = kCuts && k <= kSmallK && k < a.vocab;
-  uint32_t bound = small_k ? reached_by((k + size - 1) / size, best, top, 0) : 0;
+  uint32_t bound = small_k ? reached_by_threads((k + size - 1) / size, best, top, 0) : 0;
   cluster_wait();
   team.exchange(top, bound);
   for (int r = 0; r < size; ++r) {

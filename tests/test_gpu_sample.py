@@ -563,3 +563,31 @@ def test_light_tokens_of_a_row_with_fewer_than_top_k(light, front, k, min_p, dty
     for r in range(n):
         one = run(dsa, x[r:r + 1], u[r:r + 1], dtype=dtype, top_k=[k], min_p=[min_p])
         assert one == (got[0][r:r + 1], got[1][r:r + 1])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n", [2, 12, 200])
+def test_a_number_added_to_all_logits_changes_nothing(n, dtype):
+    """Logits on a grid that the type holds with every shift: the same tokens; in fp32 the same bits, as the
+    difference to the largest comes first."""
+    dsa = lib()
+    V = 20011
+    x = (rand(n, V, seed=61, scale=2.0) * 8).round().clamp(-56, 63) / 8   # -7 to 7.9 by eighths
+    x += torch.where(torch.arange(V) % 1999 == 5, 7.0, 0.0)
+    x.clamp_(max=12.0)
+    u = uniform(n, seed=62)
+    for kw in (dict(), dict(top_k=[40] * n), dict(top_k=[64] * n, top_p=[0.9013] * n), dict(min_p=[0.0137] * n),
+               dict(top_p=[0.8021] * n), dict(top_k=[3000] * n), dict(temperature=[0.0] * n)):
+        if n == 200:                             # (a row's result is compared with the definition's in the small batches)
+            base = run(dsa, x, u, dtype=dtype, **kw)
+        else:
+            check(dsa, x, u, dtype=dtype, **kw)
+            base = run(dsa, x, u, dtype=dtype, **kw)
+        for shift in (-4.0, -8.0, -13.0, 8.0):
+            tokens, probs = run(dsa, x + shift, u, dtype=dtype, **kw)
+            assert tokens == base[0]
+            if dtype == F32:
+                assert probs == base[1]
+            else:
+                assert all(abs(a - b) <= b * 2.0 ** -23 for a, b in zip(probs, base[1]))
+    assert dsa.get_status() == 0
