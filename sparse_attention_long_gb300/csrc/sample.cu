@@ -1246,7 +1246,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
     if (ties)
       each_logit([&](float l) { count += l == cut; });
   };
-  const bool cuts = kCuts && k < a.vocab && !greedy;
+  bool cuts = kCuts && k < a.vocab && !greedy;
   bool found = !cuts && p >= 1.f;
   if (!greedy) cut = Grid<T>::value(Grid<T>::up(cut));
   if (found) {                                     // nothing to cut, or the first of the largest
@@ -1275,9 +1275,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
     choose_bins(sh, hist, k, cuts, p, time ? 0x1p-8f : 0x1p-11f, time ? 2 * kList : kCounted, rank_in);
     const int b1 = sh.bin[0], b2 = sh.bin[1], bk = sh.bin[2];
     if (bk == kBins && p >= 1.f) {                 // fewer than k reach the cut: nothing more to cut
-      cut = next_below<T>(cut), ties = 0;
-      keep();
-      found = true;
+      cuts = false;
       break;
     }
     const auto is_listed = [&](int b) { return (uint32_t)(b - b1) <= (uint32_t)(b2 - b1) || b == bk; };
@@ -1335,7 +1333,7 @@ __device__ __forceinline__ void sample_row(const Args& a, const T* __restrict__ 
     }
   }
   if (kCuts && !found) {
-    // Too many near a cut (equal logits, say): bisection over all of them.
+    // Nothing more to cut, or too many near a cut (equal logits, say): bisection over all of them.
     const auto count_of = [&](float v, float w) {
       uint32_t n = 0;
       u64 none = 0;
