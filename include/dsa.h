@@ -520,9 +520,11 @@ int dsa_beam_select(const dsa_beam *p, const void *logits, const float *scores, 
  * columns i, i + rot_dim/2 of the rotated part, which begins at `offset`.
  *
  * step[i] is the angle per position in units of 2^-64 turns; an angle is
- * pos * step modulo one turn, exact whatever the position (steps by dsa_rope_steps
- * are rounded to 53 bits: at position 2^31 an angle is off by 2^-22 at most).
- * Arithmetic is fp32, each result rounded once.
+ * pos * step modulo one turn, which loses nothing whatever the position (steps by
+ * dsa_rope_steps are computed in 53 bits: at position 2^31 an angle is off by 2^-20
+ * radians at most, at 2^20 by 2^-31).  What is left of a turn is rounded to 24 bits (an
+ * angle by pi 2^-25 radians at most); arithmetic is fp32, each result then rounded to
+ * its type once.
  */
 enum { DSA_ROPE_INTERLEAVED = 0, DSA_ROPE_HALF = 1 };
 enum { DSA_ROPE_PLAIN = 0, DSA_ROPE_LINEAR = 1, DSA_ROPE_NTK = 2, DSA_ROPE_YARN = 3 };

@@ -3,9 +3,10 @@
 //
 // The angle of a pair is pos * f.  In fp32 that product has no bits of the turn's
 // fraction left at far positions, and a table of sines is one more thing to read.
-// Here f is a 64-bit fraction of a turn, and the product is taken modulo 2^64, that is
-// modulo a turn: exact at every position.  Its upper 32 bits (1.5e-9 radians) go through
-// sincospif.
+// Here f is a 64-bit fraction of a turn (good to some 2^-51 of itself, from fp64 on the host),
+// and the product is taken modulo 2^64, that is modulo a turn: nothing is lost of it at any
+// position.  Its upper 32 bits become a float, which keeps 24 of them (an angle is rounded
+// by pi 2^-25 = 9e-8 radians at most, near half a turn), and go through sincospif.
 //
 // A CTA takes consecutive rows (a row: one head of one token), its threads the same pairs
 // of several of them; sines and cosines of its tokens are computed once, into shared

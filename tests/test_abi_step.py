@@ -1,10 +1,12 @@
 """Refusals of rotary positions, sampling and acceptance: on the host, before any CUDA call."""
 import ctypes
 import math
+from decimal import Decimal
 
 import pytest
 import torch
 
+from oracle.rope import PI, frequencies
 from test_abi import _lib
 
 ref = ctypes.byref
@@ -39,6 +41,20 @@ def test_rope_steps_refuse(dsa):
     for n in (0, 5):
         with pytest.raises(ValueError):
             dsa.make_rope(rot_dim=64, parts=[dsa.rope_part(heads=1, dim=64)] * n)
+
+
+@pytest.mark.parametrize("base", [2.0, 12345.678, 10000.0, 500000.0, 1e6])
+def test_rope_steps_are_good_to_what_the_header_states(dsa, base):
+    """2^-20 radians at position 2^31.  Of a frequency f <= 1 in fp64: the power, the quotient by 2 pi and 2 pi itself are off
+    by 2^-53 of it or less each, the exponent's rounding by 2^-53 / e at most; a scaling's steps fall on f / factor or
+    on a mixture well below 1.  Together less than 2^-51."""
+    for rot in (2, 26, 64, 128, 256):
+        for kw in (dict(), dict(scaling="linear", factor=2.7), dict(scaling="ntk", factor=1.7),
+                   dict(scaling="yarn", factor=40.0, original=4096), dict(scaling="yarn", factor=3.3, original=8192)):
+            r = dsa.make_rope(rot_dim=rot, base=base, parts=[dsa.rope_part(heads=1, dim=256)], **kw)
+            for i, f in enumerate(frequencies(rot, base=base, **kw)):
+                angle = Decimal(int(r.step[i])) / Decimal(2) ** 64 * 2 * PI
+                assert abs(angle - f) * 2 ** 31 <= Decimal(2) ** -20
 
 
 def test_rope_apply_refuses(dsa):
