@@ -16,8 +16,10 @@
 // Bound: HBM for many tokens.  16,384 tokens of the latent shapes (128 heads of 64 of 576
 // columns, 64 index heads of 128; 1.09 GB) 172 us, 6.3 TB/s, 93 % of the copy's measured rate; the gradients of
 // 8,192 90 us (90 %); 768 tokens 13 us (51 MB, 4.0 TB/s: launch and latency); one token 3 us.
-// With few heads the sines take longer than the rows: 13,897 tokens x 8 heads of 256 bf16
-// columns 44 us (114 MB).
+// With few heads the table takes longer than the rows, and most of that is the steps: they are the
+// kernel's parameters, read with another index by each lane, which goes one address after the
+// other.  13,897 tokens of 8 + 1 heads of 256 bf16 columns 45 us (128 MB: 19 at the copy's rate), of 4 + 1 heads
+// 38; with the steps in shared memory 30 and 23.
 #include <math.h>
 
 #include "dsa_common.cuh"
