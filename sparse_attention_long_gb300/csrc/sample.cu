@@ -28,11 +28,10 @@
 // (stream_kernel), which keeps nothing of it but the candidates.
 //
 // Measured (us, calls back to back; in brackets the logits' bytes at 6.8 TB/s): one row of
-// 32,001 fp32, top-k and top-p 6.7 (0.02); 768 rows of 64,000 bf16, top-k and top-p 35 (14.5), of
-// which stream_kernel 31; 256 rows of 131,071 bf16 at a temperature 50 (9.9); 48 rows of 64,000 fp32,
-// top-p alone and large nuclei 31 (1.8); 64 rows of 131,071 bf16, top-p alone 45, a mixture 29 to
-// 40 (2.5), all at a temperature of 0.01 13,
-// at 0 9.
+// 32,001 fp32, top-k and top-p 7 (0.02); 768 rows of 64,000 bf16, top-k and top-p 33 (14.5), of
+// which stream_kernel 30; 256 rows of 131,071 bf16 at a temperature 50 (9.9), fp32 69 (19.7); 48 rows of
+// 64,000 fp32, top-p alone and large nuclei 30 (1.8); 64 rows of 131,071 bf16, top-p alone 46, a
+// mixture 29 to 34 (2.5), top-k 2,000 51, all at a temperature of 0.01 13, at 0 10.
 // Bound: the first by the latency of loads and two cluster barriers; stream_kernel by
 // instructions and the phases without loads (settings, bounds, the end); a pass of weights by
 // instructions (20 per bf16 logit, 25 else; 2.4 per cycle and SM); the histogram's path by
@@ -973,8 +972,8 @@ __device__ __forceinline__ uint32_t largest_of_cta(uint32_t best, uint32_t* __re
 // min-p can keep.  The first 4,096 (fp32: 2,048) logits give a bound that top_k of them reach,
 // more logits a better one.  Rows that need anything else, or have too many candidates, are
 // left to sample_kernel.  Logits on their way lie in shared memory, so that six CTAs fit an
-// SM's registers.  768 rows of 64,000 bf16: 31 us, 3.1 TB/s; 3,000 instructions per warp, a
-// third of them for settings, bounds and the end, at 2 per cycle and SM.
+// SM's registers.  768 rows of 64,000 bf16: 30 us, 3.3 TB/s; 2,700 instructions per warp, a
+// third of them for settings, bounds and the end, at 2.2 per cycle and SM.
 constexpr int kStreamK = 192, kLater = -2;
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 6)
